@@ -387,6 +387,144 @@ LA_API la_status la_orthogonal_features(const double* gauss_blocks, const double
  */
 LA_API int la_selected_path(int causal, int map, int dtype, int d_k, int d_v, int r);
 
+/*
+ * Operators around the attention call
+ * -----------------------------------
+ * The source pages have no counterpart of the three operators below; they are
+ * what a linear-attention layer runs next to the calls above, on the same
+ * packed [T, H, d] rows.  Beyond the conventions shared by every call: an
+ * output must not overlap an input or another output unless its declaration
+ * says so (checked on the host, LA_ERR_INVALID_ARG), and every call may be
+ * captured into a CUDA graph.
+ *
+ * Gated linear recurrence: every channel c of [T, H, d] carries one fp32 state,
+ *
+ *     h_t = a_t h_{t-1} + b_t        (element-wise, t over one packed sequence),
+ *
+ *   the causal recurrence of la_forward with r = 1 and phi(k) = 1 ("The Kernel
+ *   Zoo" §1.3) whose state is scaled by a gate before each token is added.
+ */
+#define LA_MAX_CHANNELS (1 << 20)   /* H * d of the gated recurrence              */
+#define LA_MAX_NORM_D 16384         /* row width of the layer norm                */
+#define LA_MAX_ROTARY_D 1024        /* head size of the rotary positions          */
+#define LA_MAX_AXES 4               /* position axes of the rotary positions      */
+
+/*
+ * la_gated_scan - h_t for every token of every packed sequence.
+ *   a: [T, H, d] of a_dtype (LA_F32 or LA_BF16, chosen apart from dtype: gates
+ *   close to one lose most of their distance from it in bf16).
+ *   b, h: [T, H, d] of dtype.  H * d <= LA_MAX_CHANNELS.
+ *   state_in:  NULL (every sequence starts from 0) or fp32 [nseq, H, d].
+ *   state_out: NULL or fp32 [nseq, H, d], the state after each sequence's last
+ *              token, not rounded to dtype; an empty sequence's state_in (or 0)
+ *              is copied.  May be the same array as state_in.
+ *   The state is fp32 throughout and h is rounded once from it.  Tokens are
+ *   combined in an order that depends on T, H and d alone, so results are
+ *   deterministic.  A state that crosses tiles of tokens is scaled by the
+ *   product of their gates: gates of magnitude above one are computed as given
+ *   as long as those products stay finite in fp32.  A sequence's values,
+ *   infinities and NaN among them, never reach another sequence.
+ *   cu_seqlens, nseq: as for la_forward.  workspace: device scratch of at least
+ *   la_gated_scan_workspace_bytes(...) bytes, 256-byte aligned, contents on
+ *   entry do not matter; calls that may overlap need workspaces of their own.
+ *   Malformed cu_seqlens are recorded in its error word (la_workspace_error)
+ *   and nothing else is written.
+ */
+LA_API la_status la_gated_scan(const void* a, const void* b, int a_dtype, int dtype, const int32_t* cu_seqlens,
+                               int nseq, int64_t T, int H, int d, const float* state_in, float* state_out, void* h,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * la_gated_scan_backward - gradients of L = sum(dh * h) + sum(dstate_out *
+ *   state_out) for la_gated_scan.  With g_t the gradient that reaches h_t,
+ *     g_t = dh_t + a_{t+1} g_{t+1}   (at a last token: dh_t + dstate_out),
+ *     db_t = g_t,  da_t = g_t h_{t-1}  (at a first token: g_t state_in),
+ *     dstate_in = a_t g_t at each first token.
+ *   h: [T, H, d] as la_gated_scan wrote it (its rounding to dtype enters da);
+ *   dh: [T, H, d] of dtype; da: of a_dtype; db: of dtype.
+ *   state_in, dstate_out: as NULL they are 0.  dstate_in: NULL or fp32
+ *   [nseq, H, d]; may be the same array as dstate_out; an empty sequence's
+ *   dstate_out (or 0) is copied.  g is fp32 throughout; db and da are rounded
+ *   once.  Other arguments, order and errors as for la_gated_scan.
+ */
+LA_API la_status la_gated_scan_backward(const void* a, const void* h, const void* dh, int a_dtype, int dtype,
+                                        const int32_t* cu_seqlens, int nseq, int64_t T, int H, int d,
+                                        const float* state_in, const float* dstate_out, void* da, void* db,
+                                        float* dstate_in, void* workspace, size_t workspace_bytes, void* stream);
+
+/* la_gated_scan_workspace_bytes - scratch size for la_gated_scan and
+ *   la_gated_scan_backward (0 for arguments they reject). */
+LA_API size_t la_gated_scan_workspace_bytes(int has_cu_seqlens, int nseq, int64_t T, int H, int d);
+
+/*
+ * la_gated_step - one new token for each of B sequences: state_out = a state_in
+ *   + b, h = state_out rounded to dtype.  a: [B, H, d] of a_dtype; b, h:
+ *   [B, H, d] of dtype; state_in, state_out: fp32 [B, H, d], the same array for
+ *   an update in place.  The arithmetic is la_gated_scan's for one token.
+ *   B = 0 enqueues nothing.  Needs no workspace.
+ */
+LA_API la_status la_gated_step(const void* a, const void* b, int a_dtype, int dtype, int B, int H, int d,
+                               const float* state_in, float* state_out, void* h, void* stream);
+
+/*
+ * la_layer_norm - y = (x - mean) rstd w + bias for every row of d values, with
+ *   mean the row's mean and rstd = 1 / sqrt(variance + eps), the variance over
+ *   d values about that mean (not d - 1).  Follows an unnormalised output
+ *   (LA_NORM_NONE), whose rows grow with the number of keys they sum.
+ *   x, y: [rows, d] of dtype; weight, bias: fp32 [groups, d], row i using row
+ *   i mod groups: groups = H gives every head of [T, H, d] its own, groups = 1
+ *   shares one.  groups must divide rows.  NULL weight is 1, NULL bias 0.
+ *   mean, rstd: NULL or fp32 [rows], what la_layer_norm_backward reads.
+ *   Statistics are fp32, the variance from deviations (no cancellation of
+ *   large means); y is rounded once.  d <= LA_MAX_NORM_D.  eps >= 0.
+ */
+LA_API la_status la_layer_norm(const void* x, const float* weight, const float* bias, int dtype, int64_t rows,
+                               int groups, int d, float eps, void* y, float* mean, float* rstd, void* stream);
+
+/*
+ * la_layer_norm_backward - gradients of L = sum(dy * y) for la_layer_norm.
+ *   With xh = (x - mean) rstd and u = dy w:
+ *     dx = rstd (u - mean_d(u) - xh mean_d(u xh)),
+ *     dweight = sum of dy xh and dbias = sum of dy over the rows of each group.
+ *   x, dy, dx: [rows, d] of dtype; mean, rstd: fp32 [rows] from la_layer_norm;
+ *   dweight, dbias: NULL or fp32 [groups, d] (written, not added to; 0 for no
+ *   rows).  Sums over rows are fp32 per block and fp64 across blocks, in a
+ *   fixed order (deterministic for a given device).  workspace:
+ *   la_layer_norm_backward_workspace_bytes(...) bytes, 256-byte aligned.
+ */
+LA_API la_status la_layer_norm_backward(const void* x, const void* dy, const float* weight, const float* mean,
+                                        const float* rstd, int dtype, int64_t rows, int groups, int d, void* dx,
+                                        float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
+                                        void* stream);
+
+/* la_layer_norm_backward_workspace_bytes - scratch size for la_layer_norm_backward
+ *   on the current device (0 for arguments it rejects). */
+LA_API size_t la_layer_norm_backward_workspace_bytes(int dtype, int64_t rows, int groups, int d);
+
+/*
+ * la_rotary - rotary positions with one to LA_MAX_AXES axes (a token's place in
+ *   its sequence; or time, height and width) on the rows of q and k.
+ *   Pair p of a head is turned by the angle positions[t, axis(p)] * freq[p]:
+ *     (x0, x1) -> (x0 cos - x1 sin, x1 cos + x0 sin).
+ *   q, k:      [T, H, d] of dtype; k (and k_out) may be NULL.
+ *   freq:      fp32 [P] radians per position (device), P = sum of pairs.
+ *   positions: int32 [T, naxes] (device), any value.
+ *   pairs:     HOST int [naxes]: how many pairs each axis turns, in the order
+ *              of p; zeros allowed, P >= 1, 2 P <= d.
+ *   interleaved: 0: pair p is channels p and p + P; 1: channels 2p and 2p + 1.
+ *              Channels from 2 P on are copied.
+ *   inverse:   1 turns by the negated angle: the inverse, and the gradient (the
+ *              rotation is orthogonal, so dq = inverse rotation of dq_out).
+ *   q_out, k_out: as q, k; q_out may be q itself and k_out k itself.
+ *   Angles are reduced modulo a whole turn in 64-bit fixed point, so far
+ *   positions are as accurate as an fp64 product; cos and sin are fp32 and
+ *   outputs are rounded once.  A non-finite frequency gives NaN in its pair.
+ *   d <= LA_MAX_ROTARY_D.  T = 0 enqueues nothing.
+ */
+LA_API la_status la_rotary(const void* q, const void* k, const float* freq, const int32_t* positions, int dtype,
+                           int64_t T, int H, int d, const int* pairs, int naxes, int interleaved, int inverse,
+                           void* q_out, void* k_out, void* stream);
+
 /* la_status_string - static description of a status code. */
 LA_API const char* la_status_string(la_status status);
 

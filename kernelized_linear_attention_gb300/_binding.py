@@ -64,6 +64,18 @@ def load_library():
         "la_workspace_error": ([_vp, ctypes.POINTER(_c_int), _vp], _c_int),
         "la_orthogonal_features": ([_vp, _vp, _c_int, _c_int, _vp, _vp], _c_int),
         "la_selected_path": ([_c_int, _c_int, _c_int, _c_int, _c_int, _c_int], _c_int),
+        "la_gated_scan": ([_vp, _vp, _c_int, _c_int, _vp, _c_int, _c_i64, _c_int, _c_int, _vp, _vp, _vp, _vp, _c_size,
+                           _vp], _c_int),
+        "la_gated_scan_backward": ([_vp, _vp, _vp, _c_int, _c_int, _vp, _c_int, _c_i64, _c_int, _c_int, _vp, _vp, _vp,
+                                    _vp, _vp, _vp, _c_size, _vp], _c_int),
+        "la_gated_scan_workspace_bytes": ([_c_int, _c_int, _c_i64, _c_int, _c_int], _c_size),
+        "la_gated_step": ([_vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp], _c_int),
+        "la_layer_norm": ([_vp, _vp, _vp, _c_int, _c_i64, _c_int, _c_int, _c_float, _vp, _vp, _vp, _vp], _c_int),
+        "la_layer_norm_backward": ([_vp, _vp, _vp, _vp, _vp, _c_int, _c_i64, _c_int, _c_int, _vp, _vp, _vp, _vp,
+                                    _c_size, _vp], _c_int),
+        "la_layer_norm_backward_workspace_bytes": ([_c_int, _c_i64, _c_int, _c_int], _c_size),
+        "la_rotary": ([_vp, _vp, _vp, _vp, _c_int, _c_i64, _c_int, _c_int, ctypes.POINTER(_c_int), _c_int, _c_int,
+                       _c_int, _vp, _vp, _vp], _c_int),
         "la_status_string": ([_c_int], ctypes.c_char_p),
         "la_version": ([], _c_int),
     }
@@ -420,3 +432,252 @@ def la_orthogonal_features(gauss_blocks: torch.Tensor, gauss_lengths: torch.Tens
     _check("la_orthogonal_features", load_library().la_orthogonal_features(
         _ptr(gauss_blocks), _ptr(gauss_lengths), r, d, _ptr(omega), _stream(stream)))
     return omega
+
+
+# --------------------------------------------------------------------------- operators around the attention call
+
+def _operands(*named):
+    """Checks (tensor, name, dtype or None, shape or None) operands: CUDA tensors on one device,
+    contiguous, of the given dtype (None: float32 or bfloat16) and shape; None tensors are
+    skipped.  Returns the device."""
+    dev = None
+    for t, name, dtype, shape in named:
+        if t is None:
+            continue
+        _need(t, name, dtype)
+        if dtype is None and t.dtype not in DTYPE_IDS:
+            raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, other operands on {dev}")
+    return dev
+
+
+class _On:
+    """Makes an operand's device current for a call and, where a stream is given, lets
+    what the call allocates belong to that stream."""
+
+    def __init__(self, dev, stream):
+        self.guards = []
+        if dev.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(dev))
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = (torch.cuda.ExternalStream(int(stream), device=dev) if int(stream)
+                          else torch.cuda.default_stream(dev))
+            elif stream.device != dev:
+                raise ValueError(f"the stream is on {stream.device}, the operands on {dev}")
+            self.guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def _sequences(T: int, cu_seqlens, nseq) -> int:
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be a vector of at least two entries")
+        if nseq is not None and nseq != cu_seqlens.numel() - 1:
+            raise ValueError(f"nseq is {nseq}, cu_seqlens has {cu_seqlens.numel() - 1} sequences")
+        return cu_seqlens.numel() - 1
+    return 1 if nseq is None else int(nseq)
+
+
+def _rows3(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [T, H, d], got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def la_gated_scan_workspace_bytes(has_cu_seqlens: bool, nseq: int, T: int, H: int, d: int) -> int:
+    return load_library().la_gated_scan_workspace_bytes(int(has_cu_seqlens), nseq, T, H, d)
+
+
+def la_gated_scan(a, b, cu_seqlens=None, nseq=None, state_in=None, state_out=None, return_state=False, h=None,
+                  workspace=None, stream=None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + b_t of packed rows a, b [T, H, d] (fp32 or
+    bf16 each); returns h [T, H, d] (dtype of b).  state_in / state_out: fp32 [nseq, H, d],
+    state_out may be state_in.  With return_state=True a state_out is allocated when none is
+    given and (h, state_out) is returned."""
+    lib = load_library()
+    T, H, d = shape = _rows3(b, "b")
+    nseq = _sequences(T, cu_seqlens, nseq)
+    states = torch.Size((nseq, H, d))
+    dev = _operands((b, "b", None, None), (a, "a", None, shape), (cu_seqlens, "cu_seqlens", torch.int32, None),
+                    (state_in, "state_in", torch.float32, states), (state_out, "state_out", torch.float32, states),
+                    (h, "h", b.dtype, shape), (workspace, "workspace", None if workspace is None else workspace.dtype,
+                                               None))
+    with _On(dev, stream) as s:
+        if h is None:
+            h = torch.empty_like(b)
+        if return_state and state_out is None:
+            state_out = torch.empty(states, dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = torch.empty(max(256, lib.la_gated_scan_workspace_bytes(cu_seqlens is not None, nseq, T, H, d)),
+                                    dtype=torch.uint8, device=dev)
+        _check("la_gated_scan", lib.la_gated_scan(
+            a.data_ptr(), b.data_ptr(), DTYPE_IDS[a.dtype], DTYPE_IDS[b.dtype], _ptr(cu_seqlens), nseq, T, H, d,
+            _ptr(state_in), _ptr(state_out), h.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), s))
+    return (h, state_out) if return_state else h
+
+
+def la_gated_scan_backward(a, h, dh, cu_seqlens=None, nseq=None, state_in=None, dstate_out=None, return_dstate=False,
+                           da=None, db=None, dstate_in=None, workspace=None, stream=None):
+    """Gradients (da, db) of sum(dh * h) + sum(dstate_out * state_out) for la_gated_scan, whose
+    output h is read; with return_dstate=True (da, db, dstate_in)."""
+    lib = load_library()
+    T, H, d = shape = _rows3(h, "h")
+    nseq = _sequences(T, cu_seqlens, nseq)
+    states = torch.Size((nseq, H, d))
+    dev = _operands((h, "h", None, None), (a, "a", None, shape), (dh, "dh", h.dtype, shape),
+                    (cu_seqlens, "cu_seqlens", torch.int32, None), (state_in, "state_in", torch.float32, states),
+                    (dstate_out, "dstate_out", torch.float32, states), (dstate_in, "dstate_in", torch.float32, states),
+                    (da, "da", a.dtype, shape), (db, "db", h.dtype, shape),
+                    (workspace, "workspace", None if workspace is None else workspace.dtype, None))
+    with _On(dev, stream) as s:
+        if da is None:
+            da = torch.empty_like(a)
+        if db is None:
+            db = torch.empty_like(h)
+        if return_dstate and dstate_in is None:
+            dstate_in = torch.empty(states, dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = torch.empty(max(256, lib.la_gated_scan_workspace_bytes(cu_seqlens is not None, nseq, T, H, d)),
+                                    dtype=torch.uint8, device=dev)
+        _check("la_gated_scan_backward", lib.la_gated_scan_backward(
+            a.data_ptr(), h.data_ptr(), dh.data_ptr(), DTYPE_IDS[a.dtype], DTYPE_IDS[h.dtype], _ptr(cu_seqlens), nseq,
+            T, H, d, _ptr(state_in), _ptr(dstate_out), da.data_ptr(), db.data_ptr(), _ptr(dstate_in),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), s))
+    return (da, db, dstate_in) if return_dstate else (da, db)
+
+
+def la_gated_step(a, b, state, state_out=None, h=None, stream=None):
+    """One token for each of B sequences of the gated recurrence: a, b [B, H, d]; state fp32
+    [B, H, d] is updated in place, or written to state_out when given; returns h [B, H, d]."""
+    lib = load_library()
+    B, H, d = shape = _rows3(b, "b")
+    dev = _operands((b, "b", None, None), (a, "a", None, shape), (state, "state", torch.float32, shape),
+                    (state_out, "state_out", torch.float32, shape), (h, "h", b.dtype, shape))
+    with _On(dev, stream) as s:
+        if h is None:
+            h = torch.empty_like(b)
+        _check("la_gated_step", lib.la_gated_step(
+            a.data_ptr(), b.data_ptr(), DTYPE_IDS[a.dtype], DTYPE_IDS[b.dtype], B, H, d, state.data_ptr(),
+            (state if state_out is None else state_out).data_ptr(), h.data_ptr(), s))
+    return h
+
+
+def _norm_shape(x, weight, bias):
+    """(rows, groups, d) of x [..., d] with weight and bias [d] (shared) or [G, d] (G: x's
+    second dimension from the right, each index with its own)."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError(f"x must be [..., d], got shape {tuple(x.shape)}")
+    d, groups = x.shape[-1], 1
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is None:
+            continue
+        if t.dim() == 2 and x.dim() >= 2 and tuple(t.shape) == (x.shape[-2], d):
+            groups = x.shape[-2]
+        elif tuple(t.shape) != (d,):
+            raise ValueError(f"{name} must have shape {(d,)} or x's last two dimensions, got {tuple(t.shape)}")
+    if weight is not None and bias is not None and weight.shape != bias.shape:
+        raise ValueError("weight and bias must have the same shape")
+    return x.numel() // d, groups, d
+
+
+def la_layer_norm(x, weight=None, bias=None, eps=1e-5, return_stats=False, y=None, mean=None, rstd=None, stream=None):
+    """Layer norm over the last dimension of x [..., d] (fp32 or bf16): (x - mean) rstd weight +
+    bias.  weight, bias: fp32 [d], or [H, d] for x [..., H, d].  Returns y, or with
+    return_stats=True (y, mean, rstd), the statistics fp32 of x's shape without its last
+    dimension, as la_layer_norm_backward reads them."""
+    lib = load_library()
+    rows, groups, d = _norm_shape(x, weight, bias)
+    stats = x.shape[:-1]
+    dev = _operands((x, "x", None, None), (weight, "weight", torch.float32, None), (bias, "bias", torch.float32, None),
+                    (y, "y", x.dtype, x.shape), (mean, "mean", torch.float32, stats),
+                    (rstd, "rstd", torch.float32, stats))
+    with _On(dev, stream) as s:
+        if y is None:
+            y = torch.empty_like(x)
+        if return_stats:
+            mean = torch.empty(stats, dtype=torch.float32, device=dev) if mean is None else mean
+            rstd = torch.empty(stats, dtype=torch.float32, device=dev) if rstd is None else rstd
+        _check("la_layer_norm", lib.la_layer_norm(x.data_ptr(), _ptr(weight), _ptr(bias), DTYPE_IDS[x.dtype], rows,
+                                                  groups, d, eps, y.data_ptr(), _ptr(mean), _ptr(rstd), s))
+    return (y, mean, rstd) if return_stats else y
+
+
+def la_layer_norm_backward_workspace_bytes(dtype, rows: int, groups: int, d: int) -> int:
+    dt = DTYPE_IDS[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    return load_library().la_layer_norm_backward_workspace_bytes(dt, rows, groups, d)
+
+
+def la_layer_norm_backward(x, dy, mean, rstd, weight, dx=None, dweight=None, dbias=None, workspace=None, stream=None):
+    """Gradients (dx, dweight, dbias) of sum(dy * y) for la_layer_norm; weight [d] or [H, d] gives
+    the shape of dweight and dbias (fp32)."""
+    lib = load_library()
+    if not isinstance(weight, torch.Tensor):
+        raise TypeError("weight must be a torch.Tensor")
+    rows, groups, d = _norm_shape(x, weight, None)
+    stats = x.shape[:-1]
+    dev = _operands((x, "x", None, None), (dy, "dy", x.dtype, x.shape), (mean, "mean", torch.float32, stats),
+                    (rstd, "rstd", torch.float32, stats), (weight, "weight", torch.float32, None),
+                    (dx, "dx", x.dtype, x.shape), (dweight, "dweight", torch.float32, weight.shape),
+                    (dbias, "dbias", torch.float32, weight.shape),
+                    (workspace, "workspace", None if workspace is None else workspace.dtype, None))
+    with _On(dev, stream) as s:
+        dx = torch.empty_like(x) if dx is None else dx
+        dweight = torch.empty_like(weight) if dweight is None else dweight
+        dbias = torch.empty_like(weight) if dbias is None else dbias
+        if workspace is None:
+            workspace = torch.empty(
+                max(256, lib.la_layer_norm_backward_workspace_bytes(DTYPE_IDS[x.dtype], rows, groups, d)),
+                dtype=torch.uint8, device=dev)
+        _check("la_layer_norm_backward", lib.la_layer_norm_backward(
+            x.data_ptr(), dy.data_ptr(), weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(), DTYPE_IDS[x.dtype], rows,
+            groups, d, dx.data_ptr(), dweight.data_ptr(), dbias.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), s))
+    return dx, dweight, dbias
+
+
+def la_rotary(q, k, freq, positions, pairs, interleaved=False, inverse=False, q_out=None, k_out=None, stream=None):
+    """Rotary positions on q and k [T, H, d] (k may be None): pair p turns by positions[t, axis(p)]
+    freq[p].  freq: fp32 [P]; positions: int32 [T, naxes] (or [T] for one axis); pairs: how many
+    pairs each axis turns, sum(pairs) = P.  interleaved: channels (2p, 2p + 1) instead of (p, p + P).
+    inverse=True turns back (the gradient).  q_out may be q, k_out k.  Returns (q_out, k_out), or
+    q_out alone when k is None."""
+    lib = load_library()
+    T, H, d = shape = _rows3(q, "q")
+    pairs = [int(n) for n in pairs]
+    if not isinstance(positions, torch.Tensor):
+        raise TypeError("positions must be a torch.Tensor")
+    dev = _operands((q, "q", None, None), (k, "k", q.dtype, shape), (freq, "freq", torch.float32, (sum(pairs),)),
+                    (positions, "positions", torch.int32,
+                     (T,) if len(pairs) == 1 and positions.dim() == 1 else (T, len(pairs))),
+                    (q_out, "q_out", q.dtype, shape), (k_out, "k_out", q.dtype, shape))
+    if k is None and k_out is not None:
+        raise ValueError("k_out is given without k")
+    with _On(dev, stream) as s:
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        if k is not None and k_out is None:
+            k_out = torch.empty_like(k)
+        _check("la_rotary", lib.la_rotary(
+            q.data_ptr(), _ptr(k), freq.data_ptr(), positions.data_ptr(), DTYPE_IDS[q.dtype], T, H, d,
+            (_c_int * len(pairs))(*pairs), len(pairs), int(interleaved), int(inverse), q_out.data_ptr(), _ptr(k_out),
+            s))
+    return q_out if k is None else (q_out, k_out)

@@ -67,6 +67,55 @@ cudaError_t decode_step(const void* q, const void* k, const void* v, const float
                         int norm, int B, int H, int dk, int dv, int r, float eps, float* state, void* out,
                         cudaStream_t s);
 
+// Gated linear recurrence (gated.cu), forward (reverse = 0) and its adjoint (reverse = 1).
+struct GatedParams {
+    const void* a;             // [T][C] gates
+    const void* x;             // [T][C] b (forward) or dh (adjoint)
+    const void* h;             // adjoint: [T][C] forward output
+    void* y;                   // [T][C] h (forward) or db (adjoint)
+    void* da;                  // adjoint: [T][C]
+    const float* state_in;     // [nseq][C] or NULL: state before each first token
+    const float* edge_in;      // [nseq][C] or NULL: what enters each sequence: state_in / dstate_out
+    float* edge_out;           // [nseq][C] or NULL: what leaves it: state_out / dstate_in
+    const int32_t* cu_seqlens;
+    int nseq;
+    int64_t T;
+    int C;                     // H d
+    // workspace
+    WsHeader* hdr;
+    int* tile_seq;             // [tiles]: the sequence that holds each tile's first token
+    float2* agg;               // [tiles][C]: product of the gates, state from 0
+    float* carry;              // [tiles][C]: state that enters the tile
+    float* head;               // [tiles][C]: first state of the tile's last sequence
+};
+size_t gated_workspace_bytes(int64_t T, int C);
+cudaError_t gated_scan(GatedParams p, int a_dtype, int dtype, int reverse, void* workspace, cudaStream_t s);
+cudaError_t gated_step(const void* a, const void* b, int a_dtype, int dtype, int64_t n, const float* state_in,
+                       float* state_out, void* h, cudaStream_t s);
+
+// Layer norm (layer_norm.cu).
+cudaError_t layer_norm(const void* x, const float* weight, const float* bias, int dtype, int64_t rows, int groups,
+                       int d, float eps, void* y, float* mean, float* rstd, cudaStream_t s);
+size_t layer_norm_backward_workspace_bytes(int dtype, int64_t rows, int groups, int d);
+cudaError_t layer_norm_backward(const void* x, const void* dy, const float* weight, const float* mean,
+                                const float* rstd, int dtype, int64_t rows, int groups, int d, void* dx,
+                                float* dweight, float* dbias, void* workspace, cudaStream_t s);
+
+// Rotary positions (rotary.cu).
+struct RotaryParams {
+    const void* q;
+    const void* k;             // may be NULL
+    void* q_out;
+    void* k_out;
+    const float* freq;         // [P]
+    const int32_t* positions;  // [T][naxes]
+    int64_t T;
+    int H, d, P, naxes;
+    int first[LA_MAX_AXES + 1];   // first pair of each axis, and P
+    int interleaved, inverse;
+};
+cudaError_t rotary(const RotaryParams& p, int dtype, cudaStream_t s);
+
 // Orthogonal random features (orf.cu).
 cudaError_t orf_build(const double* blocks, const double* lengths, int r, int d, float* omega,
                       cudaStream_t s);
