@@ -318,7 +318,10 @@ LA_API la_status la_noalloc_error(int* code, void* stream);
  *   out, the kernel records LA_DEVERR_WAIT_TIMEOUT in the workspace error word,
  *   every role gives up on its own bounded waits (2 s each), drains the copies
  *   and MMAs it started, frees its tensor memory and returns: the outputs of that
- *   call are incomplete and the context stays usable.  enable = 0 restores normal
+ *   call are incomplete and the context stays usable.  Later la_gated_scan and
+ *   la_gated_scan_backward launches over more than one tile of tokens likewise wait
+ *   1 ms in each tile for a state that nothing publishes, record
+ *   LA_DEVERR_WAIT_TIMEOUT and go on from zero.  enable = 0 restores normal
  *   operation.  Device-wide; not for concurrent use with other calls.  Returns
  *   LA_OK, or LA_ERR_CUDA when the device flag cannot be written.
  */

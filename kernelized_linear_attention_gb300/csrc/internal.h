@@ -83,12 +83,16 @@ struct GatedParams {
     int C;                     // H d
     // workspace
     WsHeader* hdr;
-    int* tile_seq;             // [tiles]: the sequence that holds each tile's first token
-    float2* agg;               // [tiles][C]: product of the gates, state from 0
-    float* carry;              // [tiles][C]: state that enters the tile
-    float* head;               // [tiles][C]: first state of the tile's last sequence
+    int* ticket;
+    int* flags;                // [slices][tiles]: 1 once the tile's run is there, 2 once its state is
+    int* tile_seq;             // [tiles]: 4 x the sequence of its first token, and what boundaries it holds
+    float2* run;               // [tiles][Cpad]: product of the gates and state from 0, two channels each as
+                               // (A, A, B, B); tiles in scan order
+    float* state;              // [tiles][Cpad]: state that leaves the tile
+    int Cpad;                  // C rounded up to whole slices
 };
 size_t gated_workspace_bytes(int64_t T, int C);
+cudaError_t gated_force_wait_timeout(int enable);   // test hook behind la_test_force_wait_timeout
 cudaError_t gated_scan(GatedParams p, int a_dtype, int dtype, int reverse, void* workspace, cudaStream_t s);
 cudaError_t gated_step(const void* a, const void* b, int a_dtype, int dtype, int64_t n, const float* state_in,
                        float* state_out, void* h, cudaStream_t s);

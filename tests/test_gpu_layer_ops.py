@@ -624,3 +624,24 @@ def test_one_token_at_a_time_equals_the_whole_sequence(la):
         yt = la.la_layer_norm(la.la_decode_step(qt, kt, vt, memory, "elu1"), w)
         # the attention output within 1e-4 of its row's size on both sides, which the norm scales to one
         assert (yt[0] - y[t]).abs().max().item() <= 4e-4 * max(1.0, y[t].abs().max().item())
+
+
+def test_gated_scan_wait_that_runs_out_is_reported(la):
+    """The hook makes every tile's look back wait 1 ms for a state that nothing publishes: the call
+    ends, reports it, and the next one is whole again."""
+    c = _scan_case([700], 1, 64, "f32", "f32", 19)
+    nb = la.la_gated_scan_workspace_bytes(False, 1, 700, 1, 64)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    la.la_test_force_wait_timeout(True)
+    try:
+        la.la_gated_scan(c["a"], c["b"], workspace=ws)
+        code = la.la_workspace_error(ws)
+        la.la_gated_scan_backward(c["a"], c["b"], c["dh"], workspace=ws)
+        code_b = la.la_workspace_error(ws)
+    finally:
+        la.la_test_force_wait_timeout(False)
+    assert (code, code_b) == (2, 2)
+    h, _ = _check_scan(la, c, "f32", "f32", True)
+    _check_scan_backward(la, c, h, "f32", "f32", True)
+    la.la_gated_scan(c["a"], c["b"], workspace=ws)
+    assert la.la_workspace_error(ws) == 0
