@@ -4,55 +4,82 @@
 //
 // The work is two (adjoint: three) flops per element, so the floor is one read
 // of every input and one write of every output.  One pass does that: a tile of
-// tokens x 64 channels is read into registers once; composing tokens
+// tokens x 64 channels is read once; composing tokens
 //     (A, B) o (a, b) = (a A, a B + b)
 // gives each warp's and then the tile's product of gates A and state from zero
 // B, and once the state that enters the tile is known the recurrence itself
-// runs over the registers and the outputs are written.
+// runs over the tile and the outputs are written.
 //
 // The entering state comes from the tiles before it.  Every tile publishes its
-// (A, B) as soon as it has them and its leaving state once it knows the
-// entering one; a tile walks back over at most 32 tiles to the nearest
-// published state and applies the (A, B) in between in token order, which are
-// the same fused multiply-adds as those of the tiles themselves: the result
-// does not depend on which tile was how far.  Tiles are handed out by a ticket in token order, so the
-// tiles that a block waits for are held by blocks already running.
+// (A, B) as soon as it has them, which waits for nothing.  Tiles form groups of
+// 16 in scan order, and the last of a group also publishes the state that
+// leaves it: a tile applies the (A, B) of the tiles before it in its group to
+// the state that left the group before, always in token order (the result does
+// not depend on timing), and the only serial chain is one trip to L2 per 16
+// tiles.  (With a state per tile and a walk back over up to 32 tiles to the
+// nearest one, the chain took 0.17 us per tile: 190 us for 65536 tokens.)  A
+// published word says itself that it is there (it is no longer kUnset), so a
+// publication needs no fence.  Tiles are handed out by a ticket in token order:
+// the tiles that a block waits for are held by blocks already running, and the
+// earliest unfinished tile never waits.
 //
-// A tile that holds a sequence boundary publishes its leaving state at once
-// and nothing from before the boundary enters what follows it: no value
-// crosses from one sequence to another.  For the adjoint, token order is
+// A tile that holds a sequence boundary publishes kCutTag for A: B is the state
+// that leaves it whatever entered, so no value crosses from one sequence to
+// another.  For the adjoint, token order is
 // reversed and a boundary is a last token.
 #include "internal.h"
+#include "tc_ptx.cuh"
 
 namespace la {
 
 namespace {
 
 constexpr int kPrepThreads = 256;
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr int kSlice = 64;           // channels per tile: two per lane
-constexpr int kMinTile = kWarps * 8;
+constexpr int kMinTile = 32;         // fewest tokens per tile: what the workspace is sized for
+constexpr int kGroup = 16;           // tiles per published state
 constexpr int kMarked = 1, kCut = 2;   // tile_seq: the tile holds a first or last row; one that cuts the recurrence
+constexpr uint32_t kUnset = 0xffffffffu;   // not published yet: a NaN that no arithmetic gives
+constexpr uint32_t kCutTag = 0xfffffffeu;  // as A: a boundary lies in the tile; another such NaN
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kForcedLimitNs = 1000000ull;
 
 // Set by the test hook: look backs then wait for a state that nothing publishes, for 1 ms.
 __device__ int g_force_timeout;
 
-__device__ __forceinline__ uint64_t now_ns() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
+using tc::globaltimer_ns;
+
+// Published words are written and read as they are (relaxed, past L1); a value with one of the two
+// reserved patterns, a NaN from the inputs, goes out as another NaN.
+__device__ __forceinline__ float settable(float x) {
+    return __float_as_uint(x) >= kCutTag ? __uint_as_float(0x7fffffffu) : x;
 }
-__device__ __forceinline__ int load_acquire(const int* p) {
-    int v;
-    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+__device__ __forceinline__ bool is_set(float x) { return __float_as_uint(x) != kUnset; }
+struct Run {
+    float2 A, B;
+};
+__device__ __forceinline__ void publish_run(float2* p, const Run& r, bool cut) {
+    const float tag = __uint_as_float(kCutTag);
+    asm volatile("st.relaxed.gpu.global.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(cut ? tag : settable(r.A.x)),
+                 "f"(cut ? tag : settable(r.A.y)), "f"(settable(r.B.x)), "f"(settable(r.B.y))
+                 : "memory");
+}
+__device__ __forceinline__ void publish2(float* p, float2 v) {
+    asm volatile("st.relaxed.gpu.global.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(settable(v.x)), "f"(settable(v.y)) : "memory");
+}
+__device__ __forceinline__ float4 peek4(const float2* p) {
+    float4 v;
+    asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
     return v;
 }
-__device__ __forceinline__ void store_release(int* p, int v) {
-    asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+__device__ __forceinline__ float2 peek2(const float* p) {
+    float2 v;
+    asm volatile("ld.relaxed.gpu.global.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
+    return v;
 }
+__device__ __forceinline__ bool is_set(float2 v) { return is_set(v.x) && is_set(v.y); }
+__device__ __forceinline__ bool is_set(float4 v) { return is_set(v.x) && is_set(v.y) && is_set(v.z) && is_set(v.w); }
 
 __device__ __forceinline__ int64_t seq_begin(const GatedParams& p, int s) {
     return p.cu_seqlens ? (int64_t)p.cu_seqlens[s] : (int64_t)s * (p.T / p.nseq);
@@ -79,11 +106,10 @@ __device__ int seq_of(const GatedParams& p, int64_t t) {
     return lo;
 }
 
-// Clears the header, the ticket and the flags, checks the packing rules and
+// Clears the header, the ticket and what tiles publish, checks the packing rules and
 // notes for each tile the sequence of its first token and whether a boundary
 // lies in it.
-__global__ void __launch_bounds__(kPrepThreads) gated_prep_kernel(GatedParams p, int tile_tokens, int tiles, int nflags,
-                                                                  int reverse) {
+__global__ void __launch_bounds__(kPrepThreads) gated_prep_kernel(GatedParams p, int tile_tokens, int tiles, int reverse) {
     asm volatile("griddepcontrol.launch_dependents;");
     if (blockIdx.x == 0) {
         const bool bad = malformed(p);
@@ -95,7 +121,10 @@ __global__ void __launch_bounds__(kPrepThreads) gated_prep_kernel(GatedParams p,
         }
     }
     const int step = gridDim.x * kPrepThreads, at = blockIdx.x * kPrepThreads + threadIdx.x;
-    for (int i = at; i < nflags; i += step) p.flags[i] = 0;
+    const uint4 unset = make_uint4(kUnset, kUnset, kUnset, kUnset);
+    const int64_t states = (int64_t)(tiles / kGroup) * (p.Cpad / 4), runs = (int64_t)tiles * (p.Cpad / 2);
+    for (int64_t i = at; i < states; i += step) reinterpret_cast<uint4*>(p.state)[i] = unset;
+    for (int64_t i = at; i < runs; i += step) reinterpret_cast<uint4*>(p.run)[i] = unset;
     for (int i = at; i < tiles; i += step) {
         const int64_t t0 = (int64_t)i * tile_tokens, t1 = min64(t0 + tile_tokens, p.T);
         const int s = seq_of(p, t0);
@@ -154,59 +183,103 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return make_float2(a.x * b.x, a.y * b.y); }
 
-// (A, B) of a run of tokens for a lane's two channels; a boundary inside it
-// makes B the leaving state whatever entered.
-struct Run {
-    float2 A, B;
-};
-
-template <int K>
+template <int W, int K>
 struct Shared {
-    float4 run[kWarps][32];          // (A.x, A.y, B.x, B.y) of each warp's tokens
-    int cut[kWarps];                 // a boundary among them
+    float4 run[W][32];               // (A.x, A.y, B.x, B.y) of each warp's tokens
+    int cut[W];                      // a boundary among them
     float2 carry[32];                // state that enters the tile
-    int first[kWarps * K], last[kWarps * K];   // the sequence that begins / ends at a row, else -1
+    int first[W * K], last[W * K];   // the sequence that begins / ends at a row, else -1
     int ticket, next;
 };
 
-// Waits (bounded) until a state is published within the 32 tiles before `tile` and every tile after it has its (A, B), and returns the state that
-// enters `tile` for the lane's two channels.  One warp.
-__device__ float2 look_back(const GatedParams& p, int tile, int slice, int tiles, int lane, bool forced) {
-    const int* flags = p.flags + (int64_t)slice * tiles;
-    const int mine = tile - 1 - lane;                        // lane 0: the tile just before
-    const uint64_t start = now_ns(), limit = forced ? kForcedLimitNs : kWaitLimitNs;
-    int back;                                                // tiles between the state found and this one
-    for (;;) {
-        const int f = forced ? 0 : mine >= 0 ? load_acquire(flags + mine) : 2;
-        const unsigned have = __ballot_sync(0xffffffffu, f >= 1), state = __ballot_sync(0xffffffffu, f == 2);
-        if (state) {
-            back = __ffs(state) - 1;
-            const unsigned between = (1u << back) - 1;       // back <= 31
-            if ((have & between) == between) break;
-        }
-        if (__any_sync(0xffffffffu, now_ns() - start > limit)) {
-            if (lane == 0) record_error(p.hdr, LA_DEVERR_WAIT_TIMEOUT);
+// The state that enters tile `order`, for the lane's two channels from c on.  Every wait is bounded;
+// a lane whose wait runs out records it and takes zero.
+__device__ __forceinline__ float2 look_back(const GatedParams& p, int order, int c, bool forced) {
+    const int q = order % kGroup, group = order / kGroup;
+    const uint64_t start = globaltimer_ns(), limit = forced ? kForcedLimitNs : kWaitLimitNs;
+    const float2* run = p.run + (int64_t)(order - q) * p.Cpad + c;
+    const float* state = p.state + (int64_t)(group - 1) * p.Cpad + c;
+    const float unset = __uint_as_float(kUnset);
+    float4 r[kGroup - 1];
+    float2 s = make_float2(unset, unset);
+    if (group > 0) s = peek2(state);
+#pragma unroll
+    for (int j = 0; j < kGroup - 1; ++j)
+        if (j < q) r[j] = peek4(run + (int64_t)j * p.Cpad);
+    for (unsigned polls = 1;; ++polls) {
+        // the state is needed unless a boundary lies in the group; the runs come without waiting for anything
+        bool missing = forced, cut = false;
+#pragma unroll
+        for (int j = 0; j < kGroup - 1; ++j)
+            if (j < q) {
+                if (!is_set(r[j])) missing = true;
+                cut |= __float_as_uint(r[j].x) == kCutTag;
+            }
+        if (!missing && (cut || is_set(s))) break;
+        if ((polls & 15) == 0 && (globaltimer_ns() - start > limit ||
+                                  *(volatile int*)&p.hdr->error == LA_DEVERR_WAIT_TIMEOUT)) {
+            record_error(p.hdr, LA_DEVERR_WAIT_TIMEOUT);
             return make_float2(0.f, 0.f);
         }
+        if (group > 0 && !is_set(s)) s = peek2(state);
+#pragma unroll
+        for (int j = 0; j < kGroup - 1; ++j)
+            if (j < q && !is_set(r[j])) r[j] = peek4(run + (int64_t)j * p.Cpad);
     }
-    __syncwarp();
-    const int c = slice * kSlice + 2 * lane;
-    float2 s = make_float2(0.f, 0.f);
-    const int from = tile - 1 - back;
-    const int Cp = p.Cpad;
-    if (from >= 0) s = __ldcg(reinterpret_cast<const float2*>(p.state + (int64_t)from * Cp + c));
-#pragma unroll 8
-    for (int i = from + 1; i < tile; ++i) {
-        const float4 r = __ldcg(reinterpret_cast<const float4*>(p.run + (int64_t)i * Cp + c));
-        s = fma2(make_float2(r.x, r.y), s, make_float2(r.z, r.w));
-    }
+#pragma unroll
+    for (int j = 0; j < kGroup - 1; ++j)
+        if (j < q) {
+            const float2 B = make_float2(r[j].z, r[j].w);
+            s = __float_as_uint(r[j].x) == kCutTag ? B : fma2(make_float2(r[j].x, r[j].y), s, B);
+        }
     return s;
 }
+__device__ __forceinline__ void publish_state(const GatedParams& p, int order, int c, const Run& whole, bool cut, float2 s) {
+    if (order % kGroup == kGroup - 1)
+        publish2(p.state + (int64_t)(order / kGroup) * p.Cpad + c, cut ? whole.B : fma2(whole.A, s, whole.B));
+}
 
-template <typename TA, typename TX, bool Rev, bool Vec, int K>
-__global__ void __launch_bounds__(kThreads, 2) gated_scan_kernel(GatedParams p, int tiles, int slices, int solo) {
-    __shared__ Shared<K> sh;
-    constexpr int kTile = kWarps * K;
+// first[i] / last[i]: the sequence whose first / last token is row t0 + i, else -1; n rows, and
+// the marks of `rows` rows are reset.  Called by `threads` threads that then synchronise.
+__device__ __forceinline__ void clear_marks(int rows, int* first, int* last, int thread, int threads) {
+    for (int i = thread; i < rows; i += threads) first[i] = last[i] = -1;
+}
+__device__ __forceinline__ void set_marks(const GatedParams& p, int seq, int64_t t0, int n, int* first, int* last, int thread,
+                                          int threads) {
+    for (int base = seq; base < p.nseq && seq_begin(p, base) < t0 + n; base += threads) {
+        const int s = base + thread;
+        if (s < p.nseq) {
+            const int64_t lo = seq_begin(p, s), hi = seq_begin(p, s + 1);
+            if (hi > lo) {
+                if (lo >= t0 && lo < t0 + n) first[lo - t0] = s;
+                if (hi - 1 >= t0 && hi - 1 < t0 + n) last[hi - 1 - t0] = s;
+            }
+        }
+    }
+}
+
+// An empty sequence passes its state on.
+__device__ void pass_empty(const GatedParams& p) {
+    if (!p.edge_out || !(p.cu_seqlens || p.T == 0)) return;
+    const int lane = threadIdx.x & 31;
+    for (int s0 = blockIdx.x * 32; s0 < p.nseq; s0 += gridDim.x * 32) {
+        const int s = s0 + lane;
+        unsigned empty = __ballot_sync(0xffffffffu, s < p.nseq && seq_begin(p, s) == seq_begin(p, s + 1));
+        for (; empty; empty &= empty - 1) {
+            const int64_t at = (int64_t)(s0 + __ffs(empty) - 1) * p.C;
+            for (int c = threadIdx.x; c < p.C; c += blockDim.x) p.edge_out[at + c] = p.edge_in ? p.edge_in[at + c] : 0.f;
+        }
+    }
+}
+
+// Tiles held in registers, one at a time per block: single tiles, and rows whose alignment rules
+// out tile copies.
+// The same warps, tokens and order of operations as the ring's: the same results.
+template <typename TA, typename TX, bool Rev, bool Vec, int W, int K, int PerSm>
+__global__ void __launch_bounds__((W + 1) * 32, PerSm) gated_scan_kernel(GatedParams p, int tiles, int slices, int solo) {
+    __shared__ Shared<W, K> sh;
+    constexpr int kTile = W * K, kThreads = (W + 1) * 32;   // the last warp looks back
+    static_assert(kTile >= kMinTile, "the workspace holds ceil(T / kMinTile) tiles");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const TA* a = static_cast<const TA*>(p.a);
     const TX* x = static_cast<const TX*>(p.x);
@@ -228,17 +301,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_kernel(GatedParams p, 
     }
     const bool forced = !solo && *(volatile int*)&g_force_timeout != 0;
 
-    // an empty sequence passes its state on
-    if (p.edge_out && (p.cu_seqlens || p.T == 0)) {
-        for (int s0 = blockIdx.x * 32; s0 < p.nseq; s0 += gridDim.x * 32) {
-            const int s = s0 + lane;
-            unsigned empty = __ballot_sync(0xffffffffu, s < p.nseq && seq_begin(p, s) == seq_begin(p, s + 1));
-            for (; empty; empty &= empty - 1) {
-                const int64_t at = (int64_t)(s0 + __ffs(empty) - 1) * C;
-                for (int c = threadIdx.x; c < p.C; c += kThreads) p.edge_out[at + c] = p.edge_in ? p.edge_in[at + c] : 0.f;
-            }
-        }
-    }
+    pass_empty(p);
 
     const int total = tiles * slices;
     int ticket = solo ? blockIdx.x : 0;
@@ -254,12 +317,13 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_kernel(GatedParams p, 
         const int n = (int)min64(kTile, p.T - t0);
         const int c = slice * kSlice + 2 * lane, left = p.C - c;
         // the warp's tokens: j = row within the tile, descending for the adjoint
-        const int j0 = (Rev ? kWarps - 1 - warp : warp) * K;
+        const bool work = warp < W;
+        const int j0 = work ? (Rev ? W - 1 - warp : warp) * K : kTile;
 
         // --- every load of the tile in flight
         Two<TA> ra[K];
         Two<TX> rx[K];
-        {
+        if (work) {
             const int64_t row = (t0 + j0) * C + c;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
@@ -277,24 +341,15 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_kernel(GatedParams p, 
         const int ts = solo ? kMarked | kCut : p.tile_seq[tile];
         const bool cut_tile = ts & kCut, marked = ts & kMarked;
         if (marked) {
-            for (int i = threadIdx.x; i < kTile; i += kThreads) sh.first[i] = sh.last[i] = -1;
+            clear_marks(kTile, sh.first, sh.last, threadIdx.x, kThreads);
             __syncthreads();
-            for (int base = ts >> 2; base < p.nseq && seq_begin(p, base) < t0 + n; base += kThreads) {
-                const int s = base + threadIdx.x;
-                if (s < p.nseq) {
-                    const int64_t lo = seq_begin(p, s), hi = seq_begin(p, s + 1);
-                    if (hi > lo) {
-                        if (lo >= t0 && lo < t0 + n) sh.first[lo - t0] = s;
-                        if (hi - 1 >= t0 && hi - 1 < t0 + n) sh.last[hi - 1 - t0] = s;
-                    }
-                }
-            }
+            set_marks(p, ts >> 2, t0, n, sh.first, sh.last, threadIdx.x, kThreads);
             __syncthreads();
         }
         // bit k: a boundary that cuts the recurrence at row j0 + k; and the rows whose state leaves
         unsigned cuts = 0, ends = 0;
         if (marked) {
-            const bool f = lane < K && sh.first[j0 + lane] >= 0, l = lane < K && sh.last[j0 + lane] >= 0;
+            const bool f = work && lane < K && sh.first[j0 + lane] >= 0, l = work && lane < K && sh.last[j0 + lane] >= 0;
             const unsigned fm = __ballot_sync(0xffffffffu, f), lm = __ballot_sync(0xffffffffu, l);
             cuts = Rev ? lm : fm;
             ends = Rev ? fm : lm;
@@ -306,6 +361,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_kernel(GatedParams p, 
         // it.  Sequences of earlier boundaries are closed by this warp itself, after its reads.
         Run r{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
         float2 open = make_float2(0.f, 0.f);
+        if (work) {
 #pragma unroll
         for (int i = 0; i < K; ++i) {
             const int k = Rev ? K - 1 - i : i;
@@ -325,55 +381,30 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_kernel(GatedParams p, 
         }
         sh.run[warp][lane] = make_float4(r.A.x, r.A.y, r.B.x, r.B.y);
         if (lane == 0) sh.cut[warp] = cuts != 0;
+        }
         if (threadIdx.x == 0) sh.next = next;
         __syncthreads();
 
-        // --- what stands before the warp within the tile
-        Run before{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
-        bool cut_before = false;
-        for (int w = 0; w < warp; ++w) {
-            const float4 q = sh.run[w][lane];
-            if (sh.cut[w]) {
-                before.B = make_float2(q.z, q.w);
-                cut_before = true;
-            } else {
-                before.A = mul2(before.A, make_float2(q.x, q.y));
-                before.B = fma2(make_float2(q.x, q.y), before.B, make_float2(q.z, q.w));
-            }
-        }
-
-        // --- the last warp publishes the tile's (A, B), or its leaving state where a boundary cuts it
-        Run whole = before;
-        if (!solo && warp == kWarps - 1) {
-            if (cuts) {
-                whole.B = r.B;
-            } else {
-                whole.A = mul2(whole.A, r.A);
-                whole.B = fma2(r.A, whole.B, r.B);
-            }
-            const int64_t at = (int64_t)order * p.Cpad + c;
-            const bool final = cut_tile || order == 0;
-            if (final) __stcg(reinterpret_cast<float2*>(p.state + at), whole.B);
-            else __stcg(reinterpret_cast<float4*>(p.run + at), make_float4(whole.A.x, whole.A.y, whole.B.x, whole.B.y));
-            __threadfence();
-            __syncwarp();
-            int* flag = p.flags + (int64_t)slice * tiles + order;
-            if (lane == 0) store_release(flag, final ? 2 : 1);
-            // --- and finds the state that enters it
+        // --- the tile's run goes out, and the state that enters it is found
+        if (!work) {
             float2 s = make_float2(0.f, 0.f);
-            const bool fresh = marked && (Rev ? sh.last[n - 1] : sh.first[0]) >= 0;   // nothing enters
-            if (!fresh) s = look_back(p, order, slice, tiles, lane, forced);
-            sh.carry[lane] = s;
-            if (!final) {
-                __stcg(reinterpret_cast<float2*>(p.state + at), fma2(whole.A, s, whole.B));
-                __threadfence();
-                __syncwarp();
-                if (lane == 0) store_release(flag, 2);
+            if (!solo) {
+                Run whole{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    const float4 q = sh.run[w][lane];
+                    whole.B = sh.cut[w] ? make_float2(q.z, q.w) : fma2(make_float2(q.x, q.y), whole.B, make_float2(q.z, q.w));
+                    whole.A = mul2(whole.A, make_float2(q.x, q.y));
+                }
+                publish_run(p.run + (int64_t)order * p.Cpad + c, whole, cut_tile);
+                const bool fresh = marked && (Rev ? sh.last[n - 1] : sh.first[0]) >= 0;   // nothing enters
+                if (!fresh) s = look_back(p, order, c, forced);
+                publish_state(p, order, c, whole, cut_tile, s);
             }
+            sh.carry[lane] = s;
         }
-        if (solo && threadIdx.x < 32) sh.carry[lane] = make_float2(0.f, 0.f);
         Two<TX> rh[Rev ? K : 1];
-        if (Rev) {
+        if (Rev && work) {
             const int64_t row = (t0 + j0) * C + c;
 #pragma unroll
             for (int k = 0; k < K; ++k)
@@ -382,7 +413,12 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_kernel(GatedParams p, 
         __syncthreads();
 
         // --- the recurrence from the state that enters the warp
-        float2 s = cut_before ? before.B : fma2(before.A, sh.carry[lane], before.B);
+        if (work) {
+        float2 s = sh.carry[lane];
+        for (int w = 0; w < warp; ++w) {
+            const float4 q = sh.run[w][lane];
+            s = sh.cut[w] ? make_float2(q.z, q.w) : fma2(make_float2(q.x, q.y), s, make_float2(q.z, q.w));
+        }
         const int64_t row = (t0 + j0) * C + c;
         const unsigned open_at = cuts ? (Rev ? __ffs(cuts) - 1 : 31 - __clz(cuts)) : 32;
 #pragma unroll
@@ -415,9 +451,302 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_kernel(GatedParams p, 
             if (((ends >> k) & 1) && p.edge_out)
                 store_edge(p.edge_out + (int64_t)(Rev ? sh.first : sh.last)[j0 + k] * C + c, left, leaving);
         }
+        }
         if (solo) return;
         ticket = sh.next;
         __syncthreads();      // the next tile overwrites the shared runs and marks
+    }
+}
+
+// --------------------------------------------------------------------------
+// Tiles that TMA brings into a ring in shared memory.  A producer warp takes tickets and starts the
+// copies, compute warps form the tile's runs, look-back warps publish them and find the entering
+// state, and the compute warps come back to the tile a few tiles later (all of the ring but the
+// stage being filled) to run the recurrence: the trip to L2 of one tile is hidden behind the tiles
+// after it.
+// --------------------------------------------------------------------------
+
+template <typename TA, typename TX, bool Rev, int W, int K, int S>
+struct Ring {
+    static constexpr int kCompute = W;                  // compute warps: K tokens each
+    static constexpr int kRows = kCompute * K;
+    static constexpr int kLag = S - 2;                  // tiles between a tile's run and its recurrence
+    static constexpr int kLookers = S < 4 ? S : 4;      // look-back warps, taking tiles in turn
+    static constexpr int kThreads = (kCompute + kLookers + 1) * 32;
+    static constexpr int kA = kRows * kSlice * (int)sizeof(TA), kX = kRows * kSlice * (int)sizeof(TX);
+    static constexpr int kStage = kA + kX + (Rev ? kX : 0);
+    struct Small {
+        float4 run[S][kCompute][32];
+        float2 carry[S][32];
+        int first[S][kRows], last[S][kRows];
+        int cut[S][kCompute];
+        int order[S], slice[S], seq[S];    // order < 0: no more tiles
+        uint64_t full[S], runs[S], carried[S], empty[S];
+        int gave_up;
+    };
+    static constexpr size_t kBytes = (size_t)S * kStage + sizeof(Small) + 128;
+};
+
+template <typename TA, typename TX, bool Rev, int W, int K, int S, int PerSm>
+__global__ void __launch_bounds__(Ring<TA, TX, Rev, W, K, S>::kThreads, PerSm) gated_ring_kernel(GatedParams p, int tiles, int slices,
+                                                                  const __grid_constant__ CUtensorMap map_a,
+                                                                  const __grid_constant__ CUtensorMap map_x,
+                                                                  const __grid_constant__ CUtensorMap map_h) {
+    using R = Ring<TA, TX, Rev, W, K, S>;
+    static_assert(R::kRows >= kMinTile, "the workspace holds ceil(T / kMinTile) tiles");
+    constexpr int kLag = R::kLag, kLookers = R::kLookers, kCompute = R::kCompute;
+    static_assert(S > kLag && kLag >= 1, "a tile stays in the ring until the compute warps come back to it");
+    static_assert(S >= kLookers, "the marks of the end need a stage for every look-back warp");
+    extern __shared__ uint8_t raw[];
+    uint8_t* data = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~(uintptr_t)127);
+    typename R::Small& sh = *reinterpret_cast<typename R::Small*>(data + (size_t)S * R::kStage);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            tc::mbar_init(&sh.full[i], 2);             // the copies, and the tile's marks
+            tc::mbar_init(&sh.runs[i], kCompute);
+            tc::mbar_init(&sh.carried[i], 1);
+            tc::mbar_init(&sh.empty[i], kCompute);
+        }
+        sh.gave_up = 0;
+        tc::fence_mbar_init();
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (p.hdr->error == LA_DEVERR_CU_SEQLENS) return;
+    __syncthreads();
+    const bool forced = *(volatile int*)&g_force_timeout != 0;
+    pass_empty(p);
+
+    // A wait that runs out (which takes a fault elsewhere) is recorded, and every role leaves.
+    auto wait = [&](uint64_t* bar, int i) {
+        if (tc::mbar_wait(bar, (i / S) & 1, 4 * kWaitLimitNs) && !*(volatile int*)&sh.gave_up) return true;
+        record_error(p.hdr, LA_DEVERR_WAIT_TIMEOUT);
+        *(volatile int*)&sh.gave_up = 1;
+        return false;
+    };
+
+    if (warp == kCompute + kLookers) {
+        // ---------------- producer
+        const int total = tiles * slices;
+        int ticket = lane == 0 ? atomicAdd(p.ticket, 1) : 0;
+        ticket = __shfl_sync(0xffffffffu, ticket, 0);
+        int i = 0, over = 0;
+        bool ok = true;
+        for (;; ++i) {
+            const int st = i % S;
+            int next = total;
+            if (lane == 0 && ticket < total) next = atomicAdd(p.ticket, 1);
+            if (i >= S) ok = wait(&sh.empty[st], i - S);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (ticket >= total) {
+                if (lane == 0) {
+                    sh.order[st] = -1;
+                    tc::mbar_arrive(&sh.full[st]);
+                    tc::mbar_arrive(&sh.full[st]);
+                }
+                if (++over == kLookers) break;      // every look-back warp meets one
+                continue;
+            }
+            const int order = ticket / slices, slice = ticket - order * slices;
+            const int tile = Rev ? tiles - 1 - order : order;
+            const int64_t t0 = (int64_t)tile * R::kRows;
+            if (lane == 0) {
+                uint8_t* at = data + (size_t)st * R::kStage;
+                tc::mbar_arrive_expect_tx(&sh.full[st], R::kStage);
+                // rows before the first and behind the last one come as zeros
+                tc::tma_load_2d(at, &map_a, slice * kSlice, (int)t0 + (Rev ? 1 : 0), &sh.full[st]);
+                tc::tma_load_2d(at + R::kA, &map_x, slice * kSlice, (int)t0, &sh.full[st]);
+                if (Rev) tc::tma_load_2d(at + R::kA + R::kX, &map_h, slice * kSlice, (int)t0 - 1, &sh.full[st]);
+            }
+            const int seq = p.tile_seq[tile];
+            if (seq & kMarked) {
+                clear_marks(R::kRows, sh.first[st], sh.last[st], lane, 32);
+                __syncwarp();
+                set_marks(p, seq >> 2, t0, (int)min64(R::kRows, p.T - t0), sh.first[st], sh.last[st], lane, 32);
+            }
+            __syncwarp();
+            if (lane == 0) {
+                sh.order[st] = order;
+                sh.slice[st] = slice;
+                sh.seq[st] = seq;
+                tc::mbar_arrive(&sh.full[st]);
+            }
+            ticket = __shfl_sync(0xffffffffu, next, 0);
+        }
+        // no copy is in flight when the block ends
+        if (!ok && lane == 0)
+            for (int j = i > S ? i - S : 0; j < i; ++j) tc::mbar_wait(&sh.full[j % S], (j / S) & 1, kWaitLimitNs);
+        return;
+    }
+
+    if (warp >= kCompute) {
+        // ---------------- look back: publishes the tile's run and finds the state that enters it
+        for (int i = warp - kCompute;; i += kLookers) {
+            const int st = i % S;
+            if (!wait(&sh.full[st], i) || sh.order[st] < 0) return;
+            if (!wait(&sh.runs[st], i)) return;
+            const int order = sh.order[st], c = sh.slice[st] * kSlice + 2 * lane;
+            const bool cut_tile = sh.seq[st] & kCut;
+            Run whole{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int w = 0; w < kCompute; ++w) {
+                const float4 q = sh.run[st][w][lane];
+                const bool cut = cut_tile && sh.cut[st][w];
+                whole.B = cut ? make_float2(q.z, q.w) : fma2(make_float2(q.x, q.y), whole.B, make_float2(q.z, q.w));
+                whole.A = mul2(whole.A, make_float2(q.x, q.y));
+            }
+            publish_run(p.run + (int64_t)order * p.Cpad + c, whole, cut_tile);
+            // a boundary at the tile's first row (adjoint: its last): nothing enters
+            const int64_t t0 = (int64_t)(Rev ? tiles - 1 - order : order) * R::kRows;
+            const int edge = Rev ? (int)min64(R::kRows, p.T - t0) - 1 : 0;
+            const bool fresh = cut_tile && (Rev ? sh.last[st] : sh.first[st])[edge] >= 0;
+            const float2 s = fresh ? make_float2(0.f, 0.f) : look_back(p, order, c, forced);
+            sh.carry[st][lane] = s;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sh.carried[st]);
+            publish_state(p, order, c, whole, cut_tile, s);
+        }
+    }
+
+    // ---------------- compute
+    const int j0 = (Rev ? kCompute - 1 - warp : warp) * K;    // the warp's rows; descending for the adjoint
+    // The state after the warp's last boundary is kept until it comes back to the tile: edge_out may
+    // be edge_in, and the sequence that begins there may be closed by another warp before.  Sequences
+    // of earlier boundaries are closed by this warp itself, after its reads.
+    float2 open[kLag + 1];
+    int end = -1;                                             // tiles of this block, once known
+    for (int i = 0;; ++i) {
+        if (end < 0) {
+            const int st = i % S;
+            if (!wait(&sh.full[st], i)) return;
+            const int order = sh.order[st];
+            if (order < 0) {
+                end = i;
+            } else {
+                const uint8_t* at = data + (size_t)st * R::kStage;
+                const Two<TA>* sa = reinterpret_cast<const Two<TA>*>(at) + j0 * (kSlice / 2) + lane;
+                const Two<TX>* sx = reinterpret_cast<const Two<TX>*>(at + R::kA) + j0 * (kSlice / 2) + lane;
+                const int64_t t0 = (int64_t)(Rev ? tiles - 1 - order : order) * R::kRows;
+                const int n = (int)min64(R::kRows, p.T - t0), c = sh.slice[st] * kSlice + 2 * lane, left = p.C - c;
+                unsigned cuts = 0;
+                if (sh.seq[st] & kCut) {
+                    const int* m = Rev ? sh.last[st] : sh.first[st];
+                    cuts = __ballot_sync(0xffffffffu, lane < K && m[j0 + lane] >= 0);
+                }
+                Run r{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
+                float2 o = make_float2(0.f, 0.f);
+                if (cuts == 0 && n == R::kRows) {
+#pragma unroll
+                    for (int q = 0; q < K; ++q) {
+                        const int k = Rev ? K - 1 - q : q;
+                        const float2 g = sa[k * (kSlice / 2)].get(), in = sx[k * (kSlice / 2)].get();
+                        r.A = mul2(r.A, g);
+                        r.B = fma2(g, r.B, in);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int q = 0; q < K; ++q) {
+                        const int k = Rev ? K - 1 - q : q;
+                        const float2 g = sa[k * (kSlice / 2)].get(), in = sx[k * (kSlice / 2)].get();
+                        if ((cuts >> k) & 1) {
+                            float2 s = in;
+                            if (p.edge_in) {
+                                const int sq = (Rev ? sh.last[st] : sh.first[st])[j0 + k];
+                                const float2 e = edge_two(p.edge_in + (int64_t)sq * p.C + c, left);
+                                s = Rev ? make_float2(in.x + e.x, in.y + e.y) : fma2(g, e, in);
+                            }
+                            r.A = make_float2(0.f, 0.f);
+                            r.B = o = s;
+                        } else if (j0 + k < n) {
+                            r.A = mul2(r.A, g);
+                            r.B = fma2(g, r.B, in);
+                        }
+                    }
+                }
+                open[0] = o;
+                sh.run[st][warp][lane] = make_float4(r.A.x, r.A.y, r.B.x, r.B.y);
+                if (lane == 0) sh.cut[st][warp] = cuts != 0;
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&sh.runs[st]);
+            }
+        }
+        const int b = i - kLag;                               // the tile to come back to
+        if (end >= 0 && b >= end) return;
+        if (b >= 0) {
+            const int st = b % S;
+            if (!wait(&sh.carried[st], b)) return;
+            const int order = sh.order[st], seq = sh.seq[st];
+            const uint8_t* at = data + (size_t)st * R::kStage;
+            const Two<TA>* sa = reinterpret_cast<const Two<TA>*>(at) + j0 * (kSlice / 2) + lane;
+            const Two<TX>* sx = reinterpret_cast<const Two<TX>*>(at + R::kA) + j0 * (kSlice / 2) + lane;
+            const Two<TX>* sh_h = reinterpret_cast<const Two<TX>*>(at + R::kA + R::kX) + j0 * (kSlice / 2) + lane;
+            const int64_t t0 = (int64_t)(Rev ? tiles - 1 - order : order) * R::kRows;
+            const int n = (int)min64(R::kRows, p.T - t0), c = sh.slice[st] * kSlice + 2 * lane, left = p.C - c;
+            const int64_t row = (t0 + j0) * p.C + c;
+            unsigned cuts = 0, ends = 0;
+            if (seq & kMarked) {
+                const unsigned fm = __ballot_sync(0xffffffffu, lane < K && sh.first[st][j0 + lane] >= 0);
+                const unsigned lm = __ballot_sync(0xffffffffu, lane < K && sh.last[st][j0 + lane] >= 0);
+                cuts = Rev ? lm : fm;
+                ends = Rev ? fm : lm;
+            }
+            float2 s = sh.carry[st][lane];
+            for (int w = 0; w < warp; ++w) {
+                const float4 q = sh.run[st][w][lane];
+                s = (seq & kCut) && sh.cut[st][w] ? make_float2(q.z, q.w)
+                                                  : fma2(make_float2(q.x, q.y), s, make_float2(q.z, q.w));
+            }
+            TX* y = static_cast<TX*>(p.y) + row;
+            TA* da = Rev ? static_cast<TA*>(p.da) + row : nullptr;
+            if ((cuts | ends) == 0 && n == R::kRows) {
+#pragma unroll
+                for (int q = 0; q < K; ++q) {
+                    const int k = Rev ? K - 1 - q : q;
+                    s = fma2(sa[k * (kSlice / 2)].get(), s, sx[k * (kSlice / 2)].get());
+                    store_two<true>(y + k * (int64_t)p.C, left, s);
+                    if (Rev) store_two<true>(da + k * (int64_t)p.C, left, mul2(s, sh_h[k * (kSlice / 2)].get()));
+                }
+            } else {
+                const int open_at = cuts ? (Rev ? __ffs(cuts) - 1 : 31 - __clz(cuts)) : 32;
+#pragma unroll 1
+                for (int q = 0; q < K; ++q) {
+                    const int k = Rev ? K - 1 - q : q;
+                    if (j0 + k >= n) continue;
+                    const float2 g = sa[k * (kSlice / 2)].get(), in = sx[k * (kSlice / 2)].get();
+                    if ((cuts >> k) & 1) {
+                        s = in;
+                        if (k == open_at) {
+                            s = open[kLag];
+                        } else if (p.edge_in) {
+                            const int sq = (Rev ? sh.last[st] : sh.first[st])[j0 + k];
+                            const float2 e = edge_two(p.edge_in + (int64_t)sq * p.C + c, left);
+                            s = Rev ? make_float2(in.x + e.x, in.y + e.y) : fma2(g, e, in);
+                        }
+                    } else {
+                        s = fma2(g, s, in);
+                    }
+                    store_two<true>(y + k * (int64_t)p.C, left, s);
+                    float2 leaving = s;
+                    if (Rev) {
+                        float2 prev = sh_h[k * (kSlice / 2)].get();
+                        if ((ends >> k) & 1) {
+                            const int sq = sh.first[st][j0 + k];
+                            prev = p.state_in ? edge_two(p.state_in + (int64_t)sq * p.C + c, left) : make_float2(0.f, 0.f);
+                            if (p.edge_out)
+                                leaving = mul2(load_two<true>(static_cast<const TA*>(p.a) + row + k * (int64_t)p.C, left).get(), s);
+                        }
+                        store_two<true>(da + k * (int64_t)p.C, left, mul2(s, prev));
+                    }
+                    if (((ends >> k) & 1) && p.edge_out)
+                        store_edge(p.edge_out + (int64_t)(Rev ? sh.first[st] : sh.last[st])[j0 + k] * p.C + c, left, leaving);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sh.empty[st]);
+        }
+#pragma unroll
+        for (int q = kLag; q > 0; --q) open[q] = open[q - 1];
     }
 }
 
@@ -432,7 +761,7 @@ __global__ void __launch_bounds__(kPrepThreads) gated_step_kernel(const TA* a, c
 }
 
 struct GatedLayout {
-    size_t ticket, flags, tile_seq, run, state, total;
+    size_t ticket, tile_seq, run, state, total;
     int slices, Cpad;
 };
 
@@ -440,13 +769,12 @@ GatedLayout gated_layout(int64_t T, int C) {
     GatedLayout lo{};
     lo.slices = (int)ceil_div(C, kSlice);
     lo.Cpad = lo.slices * kSlice;
-    const size_t tiles = T <= kMinTile ? 0 : (size_t)ceil_div(T, kMinTile);
+    const size_t tiles = T <= kMinTile ? 0 : (size_t)ceil_div(T, kMinTile), groups = tiles / kGroup;
     size_t o = align_up(sizeof(WsHeader), kAlign);
     lo.ticket = o;   o = align_up(o + sizeof(int), kAlign);
-    lo.flags = o;    o = align_up(o + sizeof(int) * tiles * lo.slices, kAlign);
     lo.tile_seq = o; o = align_up(o + sizeof(int) * tiles, kAlign);
     lo.run = o;      o = align_up(o + sizeof(float2) * tiles * lo.Cpad, kAlign);
-    lo.state = o;    o = align_up(o + sizeof(float) * tiles * lo.Cpad, kAlign);
+    lo.state = o;    o = align_up(o + sizeof(float) * groups * lo.Cpad, kAlign);
     lo.total = o;
     return lo;
 }
@@ -458,43 +786,84 @@ int sm_count() {
     return n;
 }
 
-template <typename TA, typename TX, bool Rev, bool Vec, int K>
-cudaError_t run_scan(const GatedParams& p, int slices, cudaStream_t s) {
-    constexpr int kTile = kWarps * K;
-    const int tiles = (int)ceil_div(p.T, kTile);
-    const bool solo = tiles <= 1;
+// More than one tile: the preparation, then a persistent kernel that may start while it ends.
+template <typename F, typename... Args>
+cudaError_t launch_tiles(F kernel, const GatedParams& p, int reverse, int tile_tokens, int tiles, int slices, int per_sm,
+                         int threads, size_t smem, cudaStream_t s, Args... args) {
+    const int nsm = sm_count();
+    if (nsm <= 0) return cudaErrorInvalidDevice;
+    const int64_t work = (int64_t)tiles * slices;
+    if (work > INT32_MAX / 2) return cudaErrorInvalidValue;
+    const int prep = (int)min64(ceil_div((int64_t)tiles * p.Cpad, 16 * kPrepThreads), 4 * nsm);
+    gated_prep_kernel<<<prep, kPrepThreads, 0, s>>>(p, tile_tokens, tiles, reverse);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
-    cfg.blockDim = dim3(kThreads);
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3((unsigned)min64(work, (int64_t)nsm * per_sm));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    if (solo) {
-        cfg.gridDim = dim3((unsigned)slices);
-    } else {
-        const int nsm = sm_count();
-        if (nsm <= 0) return cudaErrorInvalidDevice;
-        const int64_t nflags = (int64_t)tiles * slices;
-        if (nflags > INT32_MAX / 2) return cudaErrorInvalidValue;
-        const int prep = (int)min64(ceil_div(nflags > tiles ? nflags : tiles, kPrepThreads), nsm);
-        gated_prep_kernel<<<prep, kPrepThreads, 0, s>>>(p, kTile, tiles, (int)nflags, Rev ? 1 : 0);
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-        cfg.gridDim = dim3((unsigned)min64(nflags, (int64_t)nsm * 4));
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p, tiles, slices, args...);
+}
+
+template <typename TA, typename TX, bool Rev, bool Vec, int W, int K, int PerSm>
+cudaError_t run_registers(const GatedParams& p, int slices, cudaStream_t s) {
+    constexpr int kTile = W * K, kThreads = (W + 1) * 32;
+    const int tiles = (int)ceil_div(p.T, kTile);
+    auto kernel = gated_scan_kernel<TA, TX, Rev, Vec, W, K, PerSm>;
+    if (tiles <= 1) {
+        kernel<<<slices, kThreads, 0, s>>>(p, tiles, slices, 1);
+        return cudaGetLastError();
     }
-    return cudaLaunchKernelEx(&cfg, gated_scan_kernel<TA, TX, Rev, Vec, K>, p, tiles, slices, solo ? 1 : 0);
+    return launch_tiles(kernel, p, Rev ? 1 : 0, kTile, tiles, slices, PerSm, kThreads, 0, s, 0);
+}
+
+// [T][C] rows -> boxes of `rows` tokens x kSlice channels.
+template <typename T>
+bool row_map(CUtensorMap* m, const void* base, int64_t tokens, int C, int rows) {
+    const uint64_t dims[2] = {(uint64_t)C, (uint64_t)tokens};
+    const uint64_t strides[1] = {(uint64_t)C * sizeof(T)};
+    const uint32_t box[2] = {kSlice, (uint32_t)rows}, es[2] = {1, 1};
+    return tc_encode_tiled(m, sizeof(T) == 4, base, 2, dims, strides, box, es);
+}
+
+template <typename TA, typename TX, bool Rev, int W, int K, int S, int PerSm>
+cudaError_t run_ring(const GatedParams& p, int slices, cudaStream_t s) {
+    using R = Ring<TA, TX, Rev, W, K, S>;
+    static_assert(PerSm * (R::kBytes + 1024) <= 228 * 1024, "blocks per SM and their shared memory");
+    CUtensorMap ma, mx, mh;
+    if (!row_map<TA>(&ma, p.a, p.T, p.C, R::kRows) || !row_map<TX>(&mx, p.x, p.T, p.C, R::kRows) ||
+        !row_map<TX>(&mh, Rev ? p.h : p.x, p.T, p.C, R::kRows))
+        return cudaErrorInvalidValue;
+    auto kernel = gated_ring_kernel<TA, TX, Rev, W, K, S, PerSm>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)R::kBytes);
+    if (e != cudaSuccess) return e;
+    return launch_tiles(kernel, p, Rev ? 1 : 0, R::kRows, (int)ceil_div(p.T, R::kRows), slices, PerSm, R::kThreads, R::kBytes,
+                        s, ma, mx, mh);
 }
 
 bool two_aligned(const void* p, size_t esize) { return reinterpret_cast<uintptr_t>(p) % (2 * esize) == 0; }
+
+bool tile_aligned(const void* p, int C, size_t esize) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (size_t)C * esize % 16 == 0;
+}
 
 template <typename TA, typename TX, bool Rev>
 cudaError_t dispatch(const GatedParams& p, int slices, cudaStream_t s) {
     const bool vec = p.C % 2 == 0 && two_aligned(p.a, sizeof(TA)) && two_aligned(p.da, sizeof(TA)) &&
                      two_aligned(p.x, sizeof(TX)) && two_aligned(p.h, sizeof(TX)) && two_aligned(p.y, sizeof(TX));
-    constexpr int K = 16;
-    return vec ? run_scan<TA, TX, Rev, true, K>(p, slices, s) : run_scan<TA, TX, Rev, false, K>(p, slices, s);
+    const bool tma = vec && tile_aligned(p.a, p.C, sizeof(TA)) && tile_aligned(p.x, p.C, sizeof(TX)) &&
+                     tile_aligned(p.h, p.C, sizeof(TX));
+    // stages that fill shared memory
+    constexpr int kBytes = (int)(sizeof(TA) + (Rev ? 2 : 1) * sizeof(TX));   // of a token and channel
+    constexpr int W = 8, K = kBytes <= 8 ? 16 : 8, S = kBytes <= 4 ? 6 : kBytes <= 6 ? 4 : kBytes <= 8 ? 3 : 4;
+    if (tma && p.T > W * K) return run_ring<TA, TX, Rev, W, K, S, 1>(p, slices, s);
+    return vec ? run_registers<TA, TX, Rev, true, W, K, 1>(p, slices, s) : run_registers<TA, TX, Rev, false, W, K, 1>(p, slices, s);
 }
 
 template <typename TA, typename TX>
@@ -516,7 +885,6 @@ cudaError_t gated_scan(GatedParams p, int a_dtype, int dtype, int reverse, void*
     char* ws = static_cast<char*>(workspace);
     p.hdr = reinterpret_cast<WsHeader*>(ws);
     p.ticket = reinterpret_cast<int*>(ws + lo.ticket);
-    p.flags = reinterpret_cast<int*>(ws + lo.flags);
     p.tile_seq = reinterpret_cast<int*>(ws + lo.tile_seq);
     p.run = reinterpret_cast<float2*>(ws + lo.run);
     p.state = reinterpret_cast<float*>(ws + lo.state);

@@ -38,6 +38,9 @@ bool tc_supported(int map, int dk, int dv, int r, int causal);
 // Test hook behind la_test_force_wait_timeout: sets the causal output kernel's flag on the
 // current device.
 cudaError_t tc_force_wait_timeout(int enable);
+// An unswizzled tile map of `rank` dimensions over fp32 or bf16 elements; false where it cannot be made.
+bool tc_encode_tiled(void* map, bool f32, const void* base, int rank, const uint64_t* dims,
+                     const uint64_t* strides, const uint32_t* box, const uint32_t* steps);
 cudaError_t tc_state(const FwdParams& p, cudaStream_t s);
 cudaError_t tc_out(const FwdParams& p, int prefix_is_zero, cudaStream_t s);
 cudaError_t tc_feature_map(const void* x, const float* omega, int64_t T, int H, int r, float* phi, int* err,
@@ -84,7 +87,6 @@ struct GatedParams {
     // workspace
     WsHeader* hdr;
     int* ticket;
-    int* flags;                // [slices][tiles]: 1 once the tile's run is there, 2 once its state is
     int* tile_seq;             // [tiles]: 4 x the sequence of its first token, and what boundaries it holds
     float2* run;               // [tiles][Cpad]: product of the gates and state from 0, two channels each as
                                // (A, A, B, B); tiles in scan order
