@@ -11,16 +11,18 @@
 // runs over the tile and the outputs are written.
 //
 // The entering state comes from the tiles before it.  Every tile publishes its
-// (A, B) as soon as it has them, which waits for nothing.  Tiles form groups of
-// 16 in scan order, and the last of a group also publishes the state that
-// leaves it: a tile applies the (A, B) of the tiles before it in its group to
-// the state that left the group before, always in token order (the result does
-// not depend on timing), and the only serial chain is one trip to L2 per 16
-// tiles.  (With a state per tile and a walk back over up to 32 tiles to the
-// nearest one, the chain took 0.17 us per tile: 190 us for 65536 tokens.)  A
-// published word says itself that it is there (it is no longer kUnset), so a
-// publication needs no fence.  Tiles are handed out by a ticket in token order:
-// the tiles that a block waits for are held by blocks already running, and the
+// (A, B) as soon as it has them, which waits for nothing.  Eight tiles in scan
+// order form a group, whose last tile publishes the group's joint (A, B) as
+// soon as it sees the others', and eight groups a block of 64 tiles, whose last
+// tile publishes the state that leaves it.  A tile applies the groups before it
+// in its block and the tiles before it in its group to the state that left the
+// block before, always in token order, so the result does not depend on timing;
+// the only serial chain is one trip to L2 per 64 tiles.  (With a state per tile
+// and a walk back to the nearest one the chain took 0.17 us a tile, 190 us for
+// 65536 tokens; with a state per 16 tiles 107 us.)  A published word says
+// itself that it is there (it is no longer kUnset), so a publication needs no
+// fence.  Tiles are handed out by a ticket in token order: the tiles that a
+// thread block waits for are held by thread blocks already running, and the
 // earliest unfinished tile never waits.
 //
 // A tile that holds a sequence boundary publishes kCutTag for A: B is the state
@@ -37,17 +39,17 @@ namespace {
 constexpr int kPrepThreads = 256;
 constexpr int kSlice = 64;           // channels per tile: two per lane
 constexpr int kMinTile = 32;         // fewest tokens per tile: what the workspace is sized for
-constexpr int kGroup = 16;           // tiles per published state
+constexpr int kGroup = 8;            // tiles per group, and groups per published state
+constexpr int kSuper = kGroup * kGroup;
 constexpr int kMarked = 1, kCut = 2;   // tile_seq: the tile holds a first or last row; one that cuts the recurrence
 constexpr uint32_t kUnset = 0xffffffffu;   // not published yet: a NaN that no arithmetic gives
 constexpr uint32_t kCutTag = 0xfffffffeu;  // as A: a boundary lies in the tile; another such NaN
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
-constexpr uint64_t kForcedLimitNs = 1000000ull;
+// Limits of the waits in SM clocks: 2 s and 1 ms at 2 GHz.
+constexpr long long kWaitClocks = 4000000000ll;
+constexpr long long kForcedClocks = 2000000ll;
 
 // Set by the test hook: look backs then wait for a state that nothing publishes, for 1 ms.
 __device__ int g_force_timeout;
-
-using tc::globaltimer_ns;
 
 // Published words are written and read as they are (relaxed, past L1); a value with one of the two
 // reserved patterns, a NaN from the inputs, goes out as another NaN.
@@ -55,31 +57,23 @@ __device__ __forceinline__ float settable(float x) {
     return __float_as_uint(x) >= kCutTag ? __uint_as_float(0x7fffffffu) : x;
 }
 __device__ __forceinline__ bool is_set(float x) { return __float_as_uint(x) != kUnset; }
-struct Run {
-    float2 A, B;
-};
-__device__ __forceinline__ void publish_run(float2* p, const Run& r, bool cut) {
-    const float tag = __uint_as_float(kCutTag);
-    asm volatile("st.relaxed.gpu.global.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(cut ? tag : settable(r.A.x)),
-                 "f"(cut ? tag : settable(r.A.y)), "f"(settable(r.B.x)), "f"(settable(r.B.y))
-                 : "memory");
+__device__ __forceinline__ void publish(float2* p, float2 v) {
+    asm volatile("st.relaxed.gpu.global.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(v.x), "f"(v.y) : "memory");
 }
-__device__ __forceinline__ void publish2(float* p, float2 v) {
-    asm volatile("st.relaxed.gpu.global.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(settable(v.x)), "f"(settable(v.y)) : "memory");
+__device__ __forceinline__ void publish(float* p, float v) {
+    asm volatile("st.relaxed.gpu.global.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory");
 }
-__device__ __forceinline__ float4 peek4(const float2* p) {
-    float4 v;
-    asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
-    return v;
-}
-__device__ __forceinline__ float2 peek2(const float* p) {
+__device__ __forceinline__ float2 peek(const float2* p) {
     float2 v;
     asm volatile("ld.relaxed.gpu.global.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
     return v;
 }
+__device__ __forceinline__ float peek(const float* p) {
+    float v;
+    asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    return v;
+}
 __device__ __forceinline__ bool is_set(float2 v) { return is_set(v.x) && is_set(v.y); }
-__device__ __forceinline__ bool is_set(float4 v) { return is_set(v.x) && is_set(v.y) && is_set(v.z) && is_set(v.w); }
 
 __device__ __forceinline__ int64_t seq_begin(const GatedParams& p, int s) {
     return p.cu_seqlens ? (int64_t)p.cu_seqlens[s] : (int64_t)s * (p.T / p.nseq);
@@ -122,8 +116,10 @@ __global__ void __launch_bounds__(kPrepThreads) gated_prep_kernel(GatedParams p,
     }
     const int step = gridDim.x * kPrepThreads, at = blockIdx.x * kPrepThreads + threadIdx.x;
     const uint4 unset = make_uint4(kUnset, kUnset, kUnset, kUnset);
-    const int64_t states = (int64_t)(tiles / kGroup) * (p.Cpad / 4), runs = (int64_t)tiles * (p.Cpad / 2);
+    const int64_t states = (int64_t)(tiles / kSuper) * (p.Cpad / 4), joints = (int64_t)(tiles / kGroup) * (p.Cpad / 2),
+                  runs = (int64_t)tiles * (p.Cpad / 2);
     for (int64_t i = at; i < states; i += step) reinterpret_cast<uint4*>(p.state)[i] = unset;
+    for (int64_t i = at; i < joints; i += step) reinterpret_cast<uint4*>(p.joint)[i] = unset;
     for (int64_t i = at; i < runs; i += step) reinterpret_cast<uint4*>(p.run)[i] = unset;
     for (int i = at; i < tiles; i += step) {
         const int64_t t0 = (int64_t)i * tile_tokens, t1 = min64(t0 + tile_tokens, p.T);
@@ -183,60 +179,139 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return make_float2(a.x * b.x, a.y * b.y); }
 
+// (A, B) of a run of tokens, for a lane's two channels.
+struct Run {
+    float2 A, B;
+};
+
 template <int W, int K>
 struct Shared {
-    float4 run[W][32];               // (A.x, A.y, B.x, B.y) of each warp's tokens
+    float4 run[W][32];               // (A.x, A.y, B.x, B.y) of each warp's tokens; then the state that enters them
     int cut[W];                      // a boundary among them
-    float2 carry[32];                // state that enters the tile
     int first[W * K], last[W * K];   // the sequence that begins / ends at a row, else -1
     int ticket, next;
 };
 
-// The state that enters tile `order`, for the lane's two channels from c on.  Every wait is bounded;
-// a lane whose wait runs out records it and takes zero.
-__device__ __forceinline__ float2 look_back(const GatedParams& p, int order, int c, bool forced) {
-    const int q = order % kGroup, group = order / kGroup;
-    const uint64_t start = globaltimer_ns(), limit = forced ? kForcedLimitNs : kWaitLimitNs;
-    const float2* run = p.run + (int64_t)(order - q) * p.Cpad + c;
-    const float* state = p.state + (int64_t)(group - 1) * p.Cpad + c;
-    const float unset = __uint_as_float(kUnset);
-    float4 r[kGroup - 1];
-    float2 s = make_float2(unset, unset);
-    if (group > 0) s = peek2(state);
-#pragma unroll
-    for (int j = 0; j < kGroup - 1; ++j)
-        if (j < q) r[j] = peek4(run + (int64_t)j * p.Cpad);
-    for (unsigned polls = 1;; ++polls) {
-        // the state is needed unless a boundary lies in the group; the runs come without waiting for anything
-        bool missing = forced, cut = false;
-#pragma unroll
-        for (int j = 0; j < kGroup - 1; ++j)
-            if (j < q) {
-                if (!is_set(r[j])) missing = true;
-                cut |= __float_as_uint(r[j].x) == kCutTag;
-            }
-        if (!missing && (cut || is_set(s))) break;
-        if ((polls & 15) == 0 && (globaltimer_ns() - start > limit ||
-                                  *(volatile int*)&p.hdr->error == LA_DEVERR_WAIT_TIMEOUT)) {
-            record_error(p.hdr, LA_DEVERR_WAIT_TIMEOUT);
-            return make_float2(0.f, 0.f);
-        }
-        if (group > 0 && !is_set(s)) s = peek2(state);
-#pragma unroll
-        for (int j = 0; j < kGroup - 1; ++j)
-            if (j < q && !is_set(r[j])) r[j] = peek4(run + (int64_t)j * p.Cpad);
-    }
-#pragma unroll
-    for (int j = 0; j < kGroup - 1; ++j)
-        if (j < q) {
-            const float2 B = make_float2(r[j].z, r[j].w);
-            s = __float_as_uint(r[j].x) == kCutTag ? B : fma2(make_float2(r[j].x, r[j].y), s, B);
-        }
-    return s;
+// A published run cuts when a boundary lies in it: what enters does not reach what leaves.
+__device__ __forceinline__ bool cuts_off(float2 run) { return __float_as_uint(run.x) == kCutTag; }
+__device__ __forceinline__ float through(float2 run, float s) { return cuts_off(run) ? run.y : fmaf(run.x, s, run.y); }
+
+// The word of warp w's run (two channels each) that holds A of channel ch; B is two words on.
+__device__ __forceinline__ float* run_word(float4 (*run)[32], int w, int ch) {
+    return reinterpret_cast<float*>(&run[w][ch >> 1]) + (ch & 1);
 }
-__device__ __forceinline__ void publish_state(const GatedParams& p, int order, int c, const Run& whole, bool cut, float2 s) {
-    if (order % kGroup == kGroup - 1)
-        publish2(p.state + (int64_t)(order / kGroup) * p.Cpad + c, cut ? whole.B : fma2(whole.A, s, whole.B));
+
+// The tile's run in channel ch as it is published, from those of its warps.
+template <int W>
+__device__ __forceinline__ float2 tile_run(float4 (*run)[32], const int* warp_cut, bool cut_tile, int ch) {
+    float2 own = make_float2(1.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        const float a = run_word(run, w, ch)[0], b = run_word(run, w, ch)[2];
+        own.y = cut_tile && warp_cut[w] ? b : fmaf(a, own.y, b);
+        own.x *= a;
+    }
+    return make_float2(cut_tile ? __uint_as_float(kCutTag) : settable(own.x), settable(own.y));
+}
+
+// What a look-back lane does for its channel ch of a tile whose run `own` is published: finds the
+// state that enters the tile and leaves in the place of each warp's A the state that enters that
+// warp.  `fresh`: nothing enters.  Every wait is bounded; a lane whose wait runs out records it and
+// takes zero.
+template <int W>
+__device__ __forceinline__ void look_back(const GatedParams& p, float4 (*run)[32], const int* warp_cut, bool cut_tile,
+                                          bool fresh, float2 own, int order, int slice, int ch, bool forced) {
+    const int c = slice * kSlice + ch;
+    const int q = order % kGroup, group = order / kGroup, g = group % kGroup, super = group / kGroup;
+    const bool joins = q == kGroup - 1, leaves = order % kSuper == kSuper - 1;
+    float s = 0.f;
+    if (!fresh || joins) {
+        const long long start = clock64(), limit = forced ? kForcedClocks : kWaitClocks;
+        const float2* tile_runs = p.run + (int64_t)(order - q) * p.Cpad + c;
+        const float2* group_run = p.joint + (int64_t)(group - g) * p.Cpad + c;
+        const float* state = p.state + (int64_t)(super - 1) * p.Cpad + c;
+        float2 r[kGroup - 1], j[kGroup - 1];
+        float sup = __uint_as_float(kUnset);
+        unsigned polls = 0;
+        bool late = false;
+        auto run_out = [&]() {
+            if ((++polls & 15) == 0 && (clock64() - start > limit ||
+                                        *(volatile int*)&p.hdr->error == LA_DEVERR_WAIT_TIMEOUT)) {
+                record_error(p.hdr, LA_DEVERR_WAIT_TIMEOUT);
+                late = true;
+            }
+            return late;
+        };
+        // one trip for everything that may be there already
+        if (super > 0) sup = peek(state);
+#pragma unroll
+        for (int i = 0; i < kGroup - 1; ++i) {
+            r[i] = i < q ? peek(tile_runs + (int64_t)i * p.Cpad) : make_float2(0.f, 0.f);
+            j[i] = i < g ? peek(group_run + (int64_t)i * p.Cpad) : make_float2(0.f, 0.f);
+        }
+        // the tiles of the group: their runs come without waiting for anything
+        bool cut = false;
+        for (;;) {
+            bool missing = forced;
+            cut = false;
+#pragma unroll
+            for (int i = 0; i < kGroup - 1; ++i)
+                if (i < q) {
+                    missing |= !is_set(r[i]);
+                    cut |= cuts_off(r[i]);
+                }
+            if (!missing || run_out()) break;
+#pragma unroll
+            for (int i = 0; i < kGroup - 1; ++i)
+                if (i < q && !is_set(r[i])) r[i] = peek(tile_runs + (int64_t)i * p.Cpad);
+        }
+        if (joins) {
+            float A = 1.f, B = 0.f;
+#pragma unroll
+            for (int i = 0; i < kGroup - 1; ++i) {
+                B = through(r[i], B);
+                A *= r[i].x;
+            }
+            B = through(own, B);
+            A = cut || cut_tile ? __uint_as_float(kCutTag) : settable(A * own.x);
+            publish(p.joint + (int64_t)group * p.Cpad + c, make_float2(A, settable(B)));
+        }
+        // the groups of the block, needed unless a boundary lies in the group
+        if (!fresh && !cut) {
+            for (;;) {
+                bool missing = forced, far = super > 0;
+#pragma unroll
+                for (int i = 0; i < kGroup - 1; ++i)
+                    if (i < g) {
+                        missing |= !is_set(j[i]);
+                        far &= !cuts_off(j[i]);
+                    }
+                if (!(missing || (far && !is_set(sup))) || run_out()) break;
+                if (far && !is_set(sup)) sup = peek(state);
+#pragma unroll
+                for (int i = 0; i < kGroup - 1; ++i)
+                    if (i < g && !is_set(j[i])) j[i] = peek(group_run + (int64_t)i * p.Cpad);
+            }
+            s = super > 0 ? sup : 0.f;
+#pragma unroll
+            for (int i = 0; i < kGroup - 1; ++i)
+                if (i < g) s = through(j[i], s);
+        }
+        if (!fresh) {
+#pragma unroll
+            for (int i = 0; i < kGroup - 1; ++i)
+                if (i < q) s = through(r[i], s);
+        }
+        if (late) s = 0.f;
+    }
+    if (leaves) publish(p.state + (int64_t)super * p.Cpad + c, settable(through(own, s)));
+    float e = s;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        const float a = run_word(run, w, ch)[0], b = run_word(run, w, ch)[2];
+        run_word(run, w, ch)[0] = e;
+        e = cut_tile && warp_cut[w] ? b : fmaf(a, e, b);
+    }
 }
 
 // first[i] / last[i]: the sequence whose first / last token is row t0 + i, else -1; n rows, and
@@ -276,9 +351,9 @@ __device__ void pass_empty(const GatedParams& p) {
 // out tile copies.
 // The same warps, tokens and order of operations as the ring's: the same results.
 template <typename TA, typename TX, bool Rev, bool Vec, int W, int K, int PerSm>
-__global__ void __launch_bounds__((W + 1) * 32, PerSm) gated_scan_kernel(GatedParams p, int tiles, int slices, int solo) {
+__global__ void __launch_bounds__((W + 2) * 32, PerSm) gated_scan_kernel(GatedParams p, int tiles, int slices, int solo) {
     __shared__ Shared<W, K> sh;
-    constexpr int kTile = W * K, kThreads = (W + 1) * 32;   // the last warp looks back
+    constexpr int kTile = W * K, kThreads = (W + 2) * 32;   // the last two warps look back
     static_assert(kTile >= kMinTile, "the workspace holds ceil(T / kMinTile) tiles");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const TA* a = static_cast<const TA*>(p.a);
@@ -386,22 +461,19 @@ __global__ void __launch_bounds__((W + 1) * 32, PerSm) gated_scan_kernel(GatedPa
         __syncthreads();
 
         // --- the tile's run goes out, and the state that enters it is found
-        if (!work) {
+        if (!work && !solo) {
+            const bool fresh = marked && (Rev ? sh.last[n - 1] : sh.first[0]) >= 0;   // nothing enters
+            const int ch = threadIdx.x - W * 32;
+            const float2 own = tile_run<W>(sh.run, sh.cut, cut_tile, ch);
+            publish(p.run + (int64_t)order * p.Cpad + slice * kSlice + ch, own);
+            look_back<W>(p, sh.run, sh.cut, cut_tile, fresh, own, order, slice, ch, forced);
+        } else if (!work && warp == W) {
             float2 s = make_float2(0.f, 0.f);
-            if (!solo) {
-                Run whole{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    const float4 q = sh.run[w][lane];
-                    whole.B = sh.cut[w] ? make_float2(q.z, q.w) : fma2(make_float2(q.x, q.y), whole.B, make_float2(q.z, q.w));
-                    whole.A = mul2(whole.A, make_float2(q.x, q.y));
-                }
-                publish_run(p.run + (int64_t)order * p.Cpad + c, whole, cut_tile);
-                const bool fresh = marked && (Rev ? sh.last[n - 1] : sh.first[0]) >= 0;   // nothing enters
-                if (!fresh) s = look_back(p, order, c, forced);
-                publish_state(p, order, c, whole, cut_tile, s);
+            for (int w = 0; w < W; ++w) {
+                const float4 q = sh.run[w][lane];
+                *reinterpret_cast<float2*>(&sh.run[w][lane]) = s;
+                s = sh.cut[w] ? make_float2(q.z, q.w) : fma2(make_float2(q.x, q.y), s, make_float2(q.z, q.w));
             }
-            sh.carry[lane] = s;
         }
         Two<TX> rh[Rev ? K : 1];
         if (Rev && work) {
@@ -414,11 +486,7 @@ __global__ void __launch_bounds__((W + 1) * 32, PerSm) gated_scan_kernel(GatedPa
 
         // --- the recurrence from the state that enters the warp
         if (work) {
-        float2 s = sh.carry[lane];
-        for (int w = 0; w < warp; ++w) {
-            const float4 q = sh.run[w][lane];
-            s = sh.cut[w] ? make_float2(q.z, q.w) : fma2(make_float2(q.x, q.y), s, make_float2(q.z, q.w));
-        }
+        float2 s = *reinterpret_cast<const float2*>(&sh.run[warp][lane]);
         const int64_t row = (t0 + j0) * C + c;
         const unsigned open_at = cuts ? (Rev ? __ffs(cuts) - 1 : 31 - __clz(cuts)) : 32;
 #pragma unroll
@@ -458,30 +526,41 @@ __global__ void __launch_bounds__((W + 1) * 32, PerSm) gated_scan_kernel(GatedPa
     }
 }
 
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, long long limit) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    const long long start = clock64();
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 256; ++i)
+            if (tc::mbar_try_wait(bar, parity)) return true;
+        if (clock64() - start > limit) return false;
+    }
+}
+
 // --------------------------------------------------------------------------
 // Tiles that TMA brings into a ring in shared memory.  A producer warp takes tickets and starts the
-// copies, compute warps form the tile's runs, look-back warps publish them and find the entering
-// state, and the compute warps come back to the tile a few tiles later (all of the ring but the
-// stage being filled) to run the recurrence: the trip to L2 of one tile is hidden behind the tiles
-// after it.
+// copies, compute warps form the tile's runs, a publishing pair of warps sends them out without
+// waiting for other tiles, look-back warps find the entering state, and the compute warps come back to the tile when it is there to run the recurrence.  A
+// compute warp takes whichever of the two it can do next, so stages are neither held for a fixed
+// number of tiles nor idle: the trips to L2 are hidden behind the tiles that follow.
 // --------------------------------------------------------------------------
 
 template <typename TA, typename TX, bool Rev, int W, int K, int S>
 struct Ring {
-    static constexpr int kCompute = W;                  // compute warps: K tokens each
-    static constexpr int kRows = kCompute * K;
-    static constexpr int kLag = S - 2;                  // tiles between a tile's run and its recurrence
-    static constexpr int kLookers = S < 4 ? S : 4;      // look-back warps, taking tiles in turn
-    static constexpr int kThreads = (kCompute + kLookers + 1) * 32;
+    static constexpr int kTeams = 2;                    // compute teams, taking tiles in turn: W warps of K tokens
+    static constexpr int kRows = W * K;
+    static constexpr int kLookers = S < 4 ? S : 4;      // pairs of look-back warps, taking tiles in turn
+    static constexpr int kThreads = (kTeams * W + 2 * kLookers + 2 + 1) * 32;
     static constexpr int kA = kRows * kSlice * (int)sizeof(TA), kX = kRows * kSlice * (int)sizeof(TX);
     static constexpr int kStage = kA + kX + (Rev ? kX : 0);
     struct Small {
-        float4 run[S][kCompute][32];
-        float2 carry[S][32];
+        float4 run[S][W][32];              // each warp's run; then, in its first half, the state that enters it
+        float2 own[S][kSlice];             // the tile's run as it is published
+        float2 open[S][W][32];             // the state after the last boundary among the warp's tokens
         int first[S][kRows], last[S][kRows];
-        int cut[S][kCompute];
+        int cut[S][W];
         int order[S], slice[S], seq[S];    // order < 0: no more tiles
-        uint64_t full[S], runs[S], carried[S], empty[S];
+        uint64_t full[S], runs[S], sent[S], carried[S], empty[S];
         int gave_up;
     };
     static constexpr size_t kBytes = (size_t)S * kStage + sizeof(Small) + 128;
@@ -489,24 +568,27 @@ struct Ring {
 
 template <typename TA, typename TX, bool Rev, int W, int K, int S, int PerSm>
 __global__ void __launch_bounds__(Ring<TA, TX, Rev, W, K, S>::kThreads, PerSm) gated_ring_kernel(GatedParams p, int tiles, int slices,
+                                                                  unsigned long long over_slices,   // 2^64 / slices, rounded up; 0 for one
                                                                   const __grid_constant__ CUtensorMap map_a,
                                                                   const __grid_constant__ CUtensorMap map_x,
                                                                   const __grid_constant__ CUtensorMap map_h) {
     using R = Ring<TA, TX, Rev, W, K, S>;
     static_assert(R::kRows >= kMinTile, "the workspace holds ceil(T / kMinTile) tiles");
-    constexpr int kLag = R::kLag, kLookers = R::kLookers, kCompute = R::kCompute;
-    static_assert(S > kLag && kLag >= 1, "a tile stays in the ring until the compute warps come back to it");
+    constexpr int kLookers = R::kLookers, kTeams = R::kTeams;
     static_assert(S >= kLookers, "the marks of the end need a stage for every look-back warp");
-    extern __shared__ uint8_t raw[];
-    uint8_t* data = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~(uintptr_t)127);
+    // aligned by an offset: through an integer the compiler would lose that it is shared memory, and
+    // every access would be a generic one (twice the time per tile)
+    extern __shared__ __align__(128) uint8_t raw[];
+    uint8_t* data = raw + (-tc::smem_u32(raw) & 127u);
     typename R::Small& sh = *reinterpret_cast<typename R::Small*>(data + (size_t)S * R::kStage);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
             tc::mbar_init(&sh.full[i], 2);             // the copies, and the tile's marks
-            tc::mbar_init(&sh.runs[i], kCompute);
-            tc::mbar_init(&sh.carried[i], 1);
-            tc::mbar_init(&sh.empty[i], kCompute);
+            tc::mbar_init(&sh.runs[i], W);
+            tc::mbar_init(&sh.sent[i], 2);
+            tc::mbar_init(&sh.carried[i], 2);
+            tc::mbar_init(&sh.empty[i], W);
         }
         sh.gave_up = 0;
         tc::fence_mbar_init();
@@ -519,106 +601,140 @@ __global__ void __launch_bounds__(Ring<TA, TX, Rev, W, K, S>::kThreads, PerSm) g
 
     // A wait that runs out (which takes a fault elsewhere) is recorded, and every role leaves.
     auto wait = [&](uint64_t* bar, int i) {
-        if (tc::mbar_wait(bar, (i / S) & 1, 4 * kWaitLimitNs) && !*(volatile int*)&sh.gave_up) return true;
+        if (wait_phase(bar, (i / S) & 1, 4 * kWaitClocks) && !*(volatile int*)&sh.gave_up) return true;
         record_error(p.hdr, LA_DEVERR_WAIT_TIMEOUT);
         *(volatile int*)&sh.gave_up = 1;
         return false;
     };
 
-    if (warp == kCompute + kLookers) {
+    if (warp == kTeams * W + 2 * kLookers + 2) {
         // ---------------- producer
         const int total = tiles * slices;
-        int ticket = lane == 0 ? atomicAdd(p.ticket, 1) : 0;
-        ticket = __shfl_sync(0xffffffffu, ticket, 0);
+        // A ticket is asked for four tiles ahead and its sequence two tiles ahead: neither trip to L2
+        // stands between two copies (with one tile ahead every tile took 0.9 us).
+        constexpr int kAhead = 4;
+        auto order_of = [&](int t) { return over_slices ? (int)__umul64hi((unsigned long long)t, over_slices) : t; };
+        auto seq_of_ticket = [&](int t) {
+            const int order = order_of(t);
+            return t < total ? p.tile_seq[Rev ? tiles - 1 - order : order] : 0;
+        };
+        int asked[kAhead], ticket[kAhead], seq[kAhead];
+        const int first = lane == 0 ? atomicAdd(p.ticket, 1) : 0;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) asked[u] = u == 0 ? first : lane == 0 ? atomicAdd(p.ticket, 1) : 0;
+#pragma unroll
+        for (int u = 0; u < kAhead / 2; ++u) {
+            ticket[u] = __shfl_sync(0xffffffffu, asked[u], 0);
+            seq[u] = seq_of_ticket(ticket[u]);
+        }
         int i = 0, over = 0;
-        bool ok = true;
-        for (;; ++i) {
-            const int st = i % S;
-            int next = total;
-            if (lane == 0 && ticket < total) next = atomicAdd(p.ticket, 1);
-            if (i >= S) ok = wait(&sh.empty[st], i - S);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (ticket >= total) {
-                if (lane == 0) {
-                    sh.order[st] = -1;
-                    tc::mbar_arrive(&sh.full[st]);
-                    tc::mbar_arrive(&sh.full[st]);
+        bool ok = true, done = false;
+        while (!done) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (done) continue;
+                constexpr int kHalf = kAhead / 2;
+                const int v = (u + kHalf) % kAhead, st = i % S;
+                ticket[v] = __shfl_sync(0xffffffffu, asked[v], 0);
+                seq[v] = seq_of_ticket(ticket[v]);
+                asked[u] = lane == 0 && ticket[v] < total ? atomicAdd(p.ticket, 1) : total;
+                if (i >= S) ok = __all_sync(0xffffffffu, wait(&sh.empty[st], i - S));
+                if (!ok) {
+                    done = true;
+                } else if (ticket[u] >= total) {
+                    if (lane == 0) {
+                        sh.order[st] = -1;
+                        tc::mbar_arrive(&sh.full[st]);
+                        tc::mbar_arrive(&sh.full[st]);
+                    }
+                    if (++over == kLookers) done = true;      // every look-back warp and team meets one
+                    ++i;
+                } else {
+                    const int order = order_of(ticket[u]), slice = ticket[u] - order * slices;
+                    const int tile = Rev ? tiles - 1 - order : order;
+                    const int64_t t0 = (int64_t)tile * R::kRows;
+                    if (lane == 0) {
+                        uint8_t* at = data + (size_t)st * R::kStage;
+                        tc::mbar_arrive_expect_tx(&sh.full[st], R::kStage);
+                        // rows before the first and behind the last one come as zeros
+                        tc::tma_load_2d(at, &map_a, slice * kSlice, (int)t0 + (Rev ? 1 : 0), &sh.full[st]);
+                        tc::tma_load_2d(at + R::kA, &map_x, slice * kSlice, (int)t0, &sh.full[st]);
+                        if (Rev) tc::tma_load_2d(at + R::kA + R::kX, &map_h, slice * kSlice, (int)t0 - 1, &sh.full[st]);
+                    }
+                    if (seq[u] & kMarked) {
+                        clear_marks(R::kRows, sh.first[st], sh.last[st], lane, 32);
+                        __syncwarp();
+                        set_marks(p, seq[u] >> 2, t0, (int)min64(R::kRows, p.T - t0), sh.first[st], sh.last[st], lane, 32);
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        sh.order[st] = order;
+                        sh.slice[st] = slice;
+                        sh.seq[st] = seq[u];
+                        tc::mbar_arrive(&sh.full[st]);
+                    }
+                    ++i;
                 }
-                if (++over == kLookers) break;      // every look-back warp meets one
-                continue;
             }
-            const int order = ticket / slices, slice = ticket - order * slices;
-            const int tile = Rev ? tiles - 1 - order : order;
-            const int64_t t0 = (int64_t)tile * R::kRows;
-            if (lane == 0) {
-                uint8_t* at = data + (size_t)st * R::kStage;
-                tc::mbar_arrive_expect_tx(&sh.full[st], R::kStage);
-                // rows before the first and behind the last one come as zeros
-                tc::tma_load_2d(at, &map_a, slice * kSlice, (int)t0 + (Rev ? 1 : 0), &sh.full[st]);
-                tc::tma_load_2d(at + R::kA, &map_x, slice * kSlice, (int)t0, &sh.full[st]);
-                if (Rev) tc::tma_load_2d(at + R::kA + R::kX, &map_h, slice * kSlice, (int)t0 - 1, &sh.full[st]);
-            }
-            const int seq = p.tile_seq[tile];
-            if (seq & kMarked) {
-                clear_marks(R::kRows, sh.first[st], sh.last[st], lane, 32);
-                __syncwarp();
-                set_marks(p, seq >> 2, t0, (int)min64(R::kRows, p.T - t0), sh.first[st], sh.last[st], lane, 32);
-            }
-            __syncwarp();
-            if (lane == 0) {
-                sh.order[st] = order;
-                sh.slice[st] = slice;
-                sh.seq[st] = seq;
-                tc::mbar_arrive(&sh.full[st]);
-            }
-            ticket = __shfl_sync(0xffffffffu, next, 0);
         }
         // no copy is in flight when the block ends
         if (!ok && lane == 0)
-            for (int j = i > S ? i - S : 0; j < i; ++j) tc::mbar_wait(&sh.full[j % S], (j / S) & 1, kWaitLimitNs);
+            for (int j = i > S ? i - S : 0; j < i; ++j) wait_phase(&sh.full[j % S], (j / S) & 1, kWaitClocks);
         return;
     }
 
-    if (warp >= kCompute) {
-        // ---------------- look back: publishes the tile's run and finds the state that enters it
-        for (int i = warp - kCompute;; i += kLookers) {
+    if (warp >= kTeams * W) {
+        // ---------------- two warps publish every tile's run; pairs look back for the tiles in turn
+        const int pair = (warp - kTeams * W) / 2, ch = (warp - kTeams * W) % 2 * 32 + lane;
+        const bool publisher = pair == kLookers;
+        for (int i = publisher ? 0 : pair;; i += publisher ? 1 : kLookers) {
             const int st = i % S;
             if (!wait(&sh.full[st], i) || sh.order[st] < 0) return;
-            if (!wait(&sh.runs[st], i)) return;
-            const int order = sh.order[st], c = sh.slice[st] * kSlice + 2 * lane;
+            if (!wait(publisher ? &sh.runs[st] : &sh.sent[st], i)) return;
+            const int order = sh.order[st], slice = sh.slice[st];
             const bool cut_tile = sh.seq[st] & kCut;
-            Run whole{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
-#pragma unroll
-            for (int w = 0; w < kCompute; ++w) {
-                const float4 q = sh.run[st][w][lane];
-                const bool cut = cut_tile && sh.cut[st][w];
-                whole.B = cut ? make_float2(q.z, q.w) : fma2(make_float2(q.x, q.y), whole.B, make_float2(q.z, q.w));
-                whole.A = mul2(whole.A, make_float2(q.x, q.y));
+            if (publisher) {
+                const float2 own = tile_run<W>(sh.run[st], sh.cut[st], cut_tile, ch);
+                publish(p.run + (int64_t)order * p.Cpad + slice * kSlice + ch, own);
+                sh.own[st][ch] = own;
+            } else {
+                // a boundary at the tile's first row (adjoint: its last): nothing enters
+                const int64_t t0 = (int64_t)(Rev ? tiles - 1 - order : order) * R::kRows;
+                const int edge = Rev ? (int)min64(R::kRows, p.T - t0) - 1 : 0;
+                const bool fresh = cut_tile && (Rev ? sh.last[st] : sh.first[st])[edge] >= 0;
+                look_back<W>(p, sh.run[st], sh.cut[st], cut_tile, fresh, sh.own[st][ch], order, slice, ch, forced);
             }
-            publish_run(p.run + (int64_t)order * p.Cpad + c, whole, cut_tile);
-            // a boundary at the tile's first row (adjoint: its last): nothing enters
-            const int64_t t0 = (int64_t)(Rev ? tiles - 1 - order : order) * R::kRows;
-            const int edge = Rev ? (int)min64(R::kRows, p.T - t0) - 1 : 0;
-            const bool fresh = cut_tile && (Rev ? sh.last[st] : sh.first[st])[edge] >= 0;
-            const float2 s = fresh ? make_float2(0.f, 0.f) : look_back(p, order, c, forced);
-            sh.carry[st][lane] = s;
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&sh.carried[st]);
-            publish_state(p, order, c, whole, cut_tile, s);
+            if (lane == 0) tc::mbar_arrive(publisher ? &sh.sent[st] : &sh.carried[st]);
         }
     }
 
     // ---------------- compute
-    const int j0 = (Rev ? kCompute - 1 - warp : warp) * K;    // the warp's rows; descending for the adjoint
+    const int team = warp / W, member = warp % W;
+    const int j0 = (Rev ? W - 1 - member : member) * K;       // the warp's rows; descending for the adjoint
     // The state after the warp's last boundary is kept until it comes back to the tile: edge_out may
     // be edge_in, and the sequence that begins there may be closed by another warp before.  Sequences
     // of earlier boundaries are closed by this warp itself, after its reads.
-    float2 open[kLag + 1];
-    int end = -1;                                             // tiles of this block, once known
-    for (int i = 0;; ++i) {
-        if (end < 0) {
-            const int st = i % S;
+    int ahead = team, b = team;           // the next tile to form the run of; the next to come back to
+    int end = INT32_MAX;                  // the team's first tile that is none, once known
+    for (;;) {
+        if (b >= end) return;
+        bool form = false;
+        const long long start = clock64();
+        for (unsigned spins = 1;; ++spins) {
+            if (b < ahead && __any_sync(0xffffffffu, tc::mbar_test_wait(&sh.carried[b % S], (b / S) & 1))) break;
+            form = ahead < end && __any_sync(0xffffffffu, tc::mbar_test_wait(&sh.full[ahead % S], (ahead / S) & 1));
+            if (form) break;
+            if ((spins & 255) == 0 &&
+                __any_sync(0xffffffffu, *(volatile int*)&sh.gave_up || clock64() - start > 4 * kWaitClocks)) {
+                record_error(p.hdr, LA_DEVERR_WAIT_TIMEOUT);
+                *(volatile int*)&sh.gave_up = 1;
+                return;
+            }
+        }
+        if (form) {
+            const int i = ahead, st = i % S;
+            ahead += kTeams;
             if (!wait(&sh.full[st], i)) return;
             const int order = sh.order[st];
             if (order < 0) {
@@ -664,18 +780,17 @@ __global__ void __launch_bounds__(Ring<TA, TX, Rev, W, K, S>::kThreads, PerSm) g
                         }
                     }
                 }
-                open[0] = o;
-                sh.run[st][warp][lane] = make_float4(r.A.x, r.A.y, r.B.x, r.B.y);
-                if (lane == 0) sh.cut[st][warp] = cuts != 0;
+                if (cuts) sh.open[st][member][lane] = o;
+                sh.run[st][member][lane] = make_float4(r.A.x, r.A.y, r.B.x, r.B.y);
+                if (lane == 0) sh.cut[st][member] = cuts != 0;
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&sh.runs[st]);
             }
         }
-        const int b = i - kLag;                               // the tile to come back to
-        if (end >= 0 && b >= end) return;
-        if (b >= 0) {
+        if (!form) {
             const int st = b % S;
             if (!wait(&sh.carried[st], b)) return;
+            b += kTeams;
             const int order = sh.order[st], seq = sh.seq[st];
             const uint8_t* at = data + (size_t)st * R::kStage;
             const Two<TA>* sa = reinterpret_cast<const Two<TA>*>(at) + j0 * (kSlice / 2) + lane;
@@ -691,12 +806,7 @@ __global__ void __launch_bounds__(Ring<TA, TX, Rev, W, K, S>::kThreads, PerSm) g
                 cuts = Rev ? lm : fm;
                 ends = Rev ? fm : lm;
             }
-            float2 s = sh.carry[st][lane];
-            for (int w = 0; w < warp; ++w) {
-                const float4 q = sh.run[st][w][lane];
-                s = (seq & kCut) && sh.cut[st][w] ? make_float2(q.z, q.w)
-                                                  : fma2(make_float2(q.x, q.y), s, make_float2(q.z, q.w));
-            }
+            float2 s = *reinterpret_cast<const float2*>(&sh.run[st][member][lane]);
             TX* y = static_cast<TX*>(p.y) + row;
             TA* da = Rev ? static_cast<TA*>(p.da) + row : nullptr;
             if ((cuts | ends) == 0 && n == R::kRows) {
@@ -717,7 +827,7 @@ __global__ void __launch_bounds__(Ring<TA, TX, Rev, W, K, S>::kThreads, PerSm) g
                     if ((cuts >> k) & 1) {
                         s = in;
                         if (k == open_at) {
-                            s = open[kLag];
+                            s = sh.open[st][member][lane];
                         } else if (p.edge_in) {
                             const int sq = (Rev ? sh.last[st] : sh.first[st])[j0 + k];
                             const float2 e = edge_two(p.edge_in + (int64_t)sq * p.C + c, left);
@@ -745,8 +855,6 @@ __global__ void __launch_bounds__(Ring<TA, TX, Rev, W, K, S>::kThreads, PerSm) g
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&sh.empty[st]);
         }
-#pragma unroll
-        for (int q = kLag; q > 0; --q) open[q] = open[q - 1];
     }
 }
 
@@ -761,7 +869,7 @@ __global__ void __launch_bounds__(kPrepThreads) gated_step_kernel(const TA* a, c
 }
 
 struct GatedLayout {
-    size_t ticket, tile_seq, run, state, total;
+    size_t ticket, tile_seq, run, joint, state, total;
     int slices, Cpad;
 };
 
@@ -769,12 +877,13 @@ GatedLayout gated_layout(int64_t T, int C) {
     GatedLayout lo{};
     lo.slices = (int)ceil_div(C, kSlice);
     lo.Cpad = lo.slices * kSlice;
-    const size_t tiles = T <= kMinTile ? 0 : (size_t)ceil_div(T, kMinTile), groups = tiles / kGroup;
+    const size_t tiles = T <= kMinTile ? 0 : (size_t)ceil_div(T, kMinTile);
     size_t o = align_up(sizeof(WsHeader), kAlign);
     lo.ticket = o;   o = align_up(o + sizeof(int), kAlign);
     lo.tile_seq = o; o = align_up(o + sizeof(int) * tiles, kAlign);
     lo.run = o;      o = align_up(o + sizeof(float2) * tiles * lo.Cpad, kAlign);
-    lo.state = o;    o = align_up(o + sizeof(float) * groups * lo.Cpad, kAlign);
+    lo.joint = o;    o = align_up(o + sizeof(float2) * (tiles / kGroup) * lo.Cpad, kAlign);
+    lo.state = o;    o = align_up(o + sizeof(float) * (tiles / kSuper) * lo.Cpad, kAlign);
     lo.total = o;
     return lo;
 }
@@ -813,7 +922,7 @@ cudaError_t launch_tiles(F kernel, const GatedParams& p, int reverse, int tile_t
 
 template <typename TA, typename TX, bool Rev, bool Vec, int W, int K, int PerSm>
 cudaError_t run_registers(const GatedParams& p, int slices, cudaStream_t s) {
-    constexpr int kTile = W * K, kThreads = (W + 1) * 32;
+    constexpr int kTile = W * K, kThreads = (W + 2) * 32;
     const int tiles = (int)ceil_div(p.T, kTile);
     auto kernel = gated_scan_kernel<TA, TX, Rev, Vec, W, K, PerSm>;
     if (tiles <= 1) {
@@ -844,7 +953,7 @@ cudaError_t run_ring(const GatedParams& p, int slices, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)R::kBytes);
     if (e != cudaSuccess) return e;
     return launch_tiles(kernel, p, Rev ? 1 : 0, R::kRows, (int)ceil_div(p.T, R::kRows), slices, PerSm, R::kThreads, R::kBytes,
-                        s, ma, mx, mh);
+                        s, slices > 1 ? ~0ull / (unsigned)slices + 1 : 0ull, ma, mx, mh);
 }
 
 bool two_aligned(const void* p, size_t esize) { return reinterpret_cast<uintptr_t>(p) % (2 * esize) == 0; }
@@ -861,7 +970,7 @@ cudaError_t dispatch(const GatedParams& p, int slices, cudaStream_t s) {
                      tile_aligned(p.h, p.C, sizeof(TX));
     // stages that fill shared memory
     constexpr int kBytes = (int)(sizeof(TA) + (Rev ? 2 : 1) * sizeof(TX));   // of a token and channel
-    constexpr int W = 8, K = kBytes <= 8 ? 16 : 8, S = kBytes <= 4 ? 6 : kBytes <= 6 ? 4 : kBytes <= 8 ? 3 : 4;
+    constexpr int W = 4, K = kBytes <= 10 ? 16 : 8, S = kBytes <= 4 ? 11 : kBytes <= 6 ? 8 : kBytes <= 8 ? 6 : kBytes <= 10 ? 5 : 8;
     if (tma && p.T > W * K) return run_ring<TA, TX, Rev, W, K, S, 1>(p, slices, s);
     return vec ? run_registers<TA, TX, Rev, true, W, K, 1>(p, slices, s) : run_registers<TA, TX, Rev, false, W, K, 1>(p, slices, s);
 }
@@ -887,6 +996,7 @@ cudaError_t gated_scan(GatedParams p, int a_dtype, int dtype, int reverse, void*
     p.ticket = reinterpret_cast<int*>(ws + lo.ticket);
     p.tile_seq = reinterpret_cast<int*>(ws + lo.tile_seq);
     p.run = reinterpret_cast<float2*>(ws + lo.run);
+    p.joint = reinterpret_cast<float2*>(ws + lo.joint);
     p.state = reinterpret_cast<float*>(ws + lo.state);
     p.Cpad = lo.Cpad;
     auto go = [&](auto ta, auto tx) -> cudaError_t {

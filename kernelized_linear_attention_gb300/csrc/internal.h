@@ -88,9 +88,9 @@ struct GatedParams {
     WsHeader* hdr;
     int* ticket;
     int* tile_seq;             // [tiles]: 4 x the sequence of its first token, and what boundaries it holds
-    float2* run;               // [tiles][Cpad]: product of the gates and state from 0, two channels each as
-                               // (A, A, B, B); tiles in scan order
-    float* state;              // [tiles][Cpad]: state that leaves the tile
+    float2* run;               // [tiles][Cpad]: product of the gates and state from 0; tiles in scan order
+    float2* joint;             // [tiles / 8][Cpad]: the same of each group of 8 tiles
+    float* state;              // [tiles / 64][Cpad]: state that leaves each block of 64 tiles
     int Cpad;                  // C rounded up to whole slices
 };
 size_t gated_workspace_bytes(int64_t T, int C);
