@@ -538,8 +538,8 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, long 
 }
 
 // --------------------------------------------------------------------------
-// Tiles that TMA brings into a ring in shared memory.  A producer warp takes tickets and starts the
-// copies, compute warps form the tile's runs, a publishing pair of warps sends them out without
+// Tiles that TMA brings into a ring in shared memory.  One warp takes tickets, one starts the copies,
+// compute warps form the tile's runs, a publishing pair of warps sends them out without
 // waiting for other tiles, look-back warps find the entering state, and the compute warps come back to the tile when it is there to run the recurrence.  A
 // compute warp takes whichever of the two it can do next, so stages are neither held for a fixed
 // number of tiles nor idle: the trips to L2 are hidden behind the tiles that follow.
@@ -549,8 +549,8 @@ template <typename TA, typename TX, bool Rev, int W, int K, int S>
 struct Ring {
     static constexpr int kTeams = 2;                    // compute teams, taking tiles in turn: W warps of K tokens
     static constexpr int kRows = W * K;
-    static constexpr int kLookers = S < 4 ? S : 4;      // pairs of look-back warps, taking tiles in turn
-    static constexpr int kThreads = (kTeams * W + 2 * kLookers + 2 + 1) * 32;
+    static constexpr int kLookers = S % 4 == 0 ? 4 : S % 5 == 0 ? 5 : 3;   // pairs of look-back warps, in turn
+    static constexpr int kThreads = (kTeams * W + 2 * kLookers + 2 + 2) * 32;
     static constexpr int kA = kRows * kSlice * (int)sizeof(TA), kX = kRows * kSlice * (int)sizeof(TX);
     static constexpr int kStage = kA + kX + (Rev ? kX : 0);
     struct Small {
@@ -560,7 +560,7 @@ struct Ring {
         int first[S][kRows], last[S][kRows];
         int cut[S][W];
         int order[S], slice[S], seq[S];    // order < 0: no more tiles
-        uint64_t full[S], runs[S], sent[S], carried[S], empty[S];
+        uint64_t known[S], full[S], runs[S], sent[S], carried[S], empty[S];
         int gave_up;
     };
     static constexpr size_t kBytes = (size_t)S * kStage + sizeof(Small) + 128;
@@ -575,7 +575,10 @@ __global__ void __launch_bounds__(Ring<TA, TX, Rev, W, K, S>::kThreads, PerSm) g
     using R = Ring<TA, TX, Rev, W, K, S>;
     static_assert(R::kRows >= kMinTile, "the workspace holds ceil(T / kMinTile) tiles");
     constexpr int kLookers = R::kLookers, kTeams = R::kTeams;
-    static_assert(S >= kLookers, "the marks of the end need a stage for every look-back warp");
+    // Who takes every n-th tile waits for phases of its own tiles only, one after the other, when n
+    // divides S (another's tile may still be loading when its own later one is there, and a phase is
+    // told by its parity alone).  And the marks of the end need a stage for everyone.
+    static_assert(S % kLookers == 0 && S % kTeams == 0, "teams and look-back pairs stay with their stages");
     // aligned by an offset: through an integer the compiler would lose that it is shared memory, and
     // every access would be a generic one (twice the time per tile)
     extern __shared__ __align__(128) uint8_t raw[];
@@ -584,6 +587,7 @@ __global__ void __launch_bounds__(Ring<TA, TX, Rev, W, K, S>::kThreads, PerSm) g
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
+            tc::mbar_init(&sh.known[i], 1);
             tc::mbar_init(&sh.full[i], 2);             // the copies, and the tile's marks
             tc::mbar_init(&sh.runs[i], W);
             tc::mbar_init(&sh.sent[i], 2);
@@ -607,12 +611,40 @@ __global__ void __launch_bounds__(Ring<TA, TX, Rev, W, K, S>::kThreads, PerSm) g
         return false;
     };
 
+    if (warp == kTeams * W + 2 * kLookers + 3) {
+        // ---------------- copies of the tiles that the ticket warp names
+        if (lane == 0) {
+            int copied = 0;
+            for (int i = 0;; ++i) {
+                const int st = i % S;
+                if (!wait(&sh.known[st], i)) break;
+                const int order = sh.order[st];
+                if (order < 0) {
+                    tc::mbar_arrive(&sh.full[st]);
+                    if (sh.slice[st]) return;             // the last mark of the end
+                    continue;
+                }
+                const int x = sh.slice[st] * kSlice, t0 = (Rev ? tiles - 1 - order : order) * R::kRows;
+                uint8_t* at = data + (size_t)st * R::kStage;
+                tc::mbar_arrive_expect_tx(&sh.full[st], R::kStage);
+                // rows before the first and behind the last one come as zeros
+                tc::tma_load_2d(at, &map_a, x, t0 + (Rev ? 1 : 0), &sh.full[st]);
+                tc::tma_load_2d(at + R::kA, &map_x, x, t0, &sh.full[st]);
+                if (Rev) tc::tma_load_2d(at + R::kA + R::kX, &map_h, x, t0 - 1, &sh.full[st]);
+                copied = i + 1;
+            }
+            // no copy is in flight when the block ends
+            for (int j = copied > S ? copied - S : 0; j < copied; ++j) wait_phase(&sh.full[j % S], (j / S) & 1, kWaitClocks);
+        }
+        return;
+    }
+
     if (warp == kTeams * W + 2 * kLookers + 2) {
-        // ---------------- producer
+        // ---------------- tickets
         const int total = tiles * slices;
-        // A ticket is asked for four tiles ahead and its sequence two tiles ahead: neither trip to L2
-        // stands between two copies (with one tile ahead every tile took 0.9 us).
-        constexpr int kAhead = 4;
+        // A ticket is asked for two tiles ahead and its sequence one tile ahead: neither trip to L2
+        // stands between two copies.
+        constexpr int kAhead = 2;
         auto order_of = [&](int t) { return over_slices ? (int)__umul64hi((unsigned long long)t, over_slices) : t; };
         auto seq_of_ticket = [&](int t) {
             const int order = order_of(t);
@@ -642,44 +674,34 @@ __global__ void __launch_bounds__(Ring<TA, TX, Rev, W, K, S>::kThreads, PerSm) g
                 if (!ok) {
                     done = true;
                 } else if (ticket[u] >= total) {
+                    if (++over == kLookers) done = true;      // every look-back pair and team meets one
                     if (lane == 0) {
                         sh.order[st] = -1;
-                        tc::mbar_arrive(&sh.full[st]);
+                        sh.slice[st] = done;
+                        tc::mbar_arrive(&sh.known[st]);
                         tc::mbar_arrive(&sh.full[st]);
                     }
-                    if (++over == kLookers) done = true;      // every look-back warp and team meets one
                     ++i;
                 } else {
                     const int order = order_of(ticket[u]), slice = ticket[u] - order * slices;
-                    const int tile = Rev ? tiles - 1 - order : order;
-                    const int64_t t0 = (int64_t)tile * R::kRows;
                     if (lane == 0) {
-                        uint8_t* at = data + (size_t)st * R::kStage;
-                        tc::mbar_arrive_expect_tx(&sh.full[st], R::kStage);
-                        // rows before the first and behind the last one come as zeros
-                        tc::tma_load_2d(at, &map_a, slice * kSlice, (int)t0 + (Rev ? 1 : 0), &sh.full[st]);
-                        tc::tma_load_2d(at + R::kA, &map_x, slice * kSlice, (int)t0, &sh.full[st]);
-                        if (Rev) tc::tma_load_2d(at + R::kA + R::kX, &map_h, slice * kSlice, (int)t0 - 1, &sh.full[st]);
+                        sh.order[st] = order;
+                        sh.slice[st] = slice;
+                        sh.seq[st] = seq[u];
+                        tc::mbar_arrive(&sh.known[st]);
                     }
                     if (seq[u] & kMarked) {
+                        const int64_t t0 = (int64_t)(Rev ? tiles - 1 - order : order) * R::kRows;
                         clear_marks(R::kRows, sh.first[st], sh.last[st], lane, 32);
                         __syncwarp();
                         set_marks(p, seq[u] >> 2, t0, (int)min64(R::kRows, p.T - t0), sh.first[st], sh.last[st], lane, 32);
                     }
                     __syncwarp();
-                    if (lane == 0) {
-                        sh.order[st] = order;
-                        sh.slice[st] = slice;
-                        sh.seq[st] = seq[u];
-                        tc::mbar_arrive(&sh.full[st]);
-                    }
+                    if (lane == 0) tc::mbar_arrive(&sh.full[st]);
                     ++i;
                 }
             }
         }
-        // no copy is in flight when the block ends
-        if (!ok && lane == 0)
-            for (int j = i > S ? i - S : 0; j < i; ++j) wait_phase(&sh.full[j % S], (j / S) & 1, kWaitClocks);
         return;
     }
 
@@ -722,9 +744,10 @@ __global__ void __launch_bounds__(Ring<TA, TX, Rev, W, K, S>::kThreads, PerSm) g
         bool form = false;
         const long long start = clock64();
         for (unsigned spins = 1;; ++spins) {
-            if (b < ahead && __any_sync(0xffffffffu, tc::mbar_test_wait(&sh.carried[b % S], (b / S) & 1))) break;
+            // a run first: other tiles wait for it
             form = ahead < end && __any_sync(0xffffffffu, tc::mbar_test_wait(&sh.full[ahead % S], (ahead / S) & 1));
             if (form) break;
+            if (b < ahead && __any_sync(0xffffffffu, tc::mbar_test_wait(&sh.carried[b % S], (b / S) & 1))) break;
             if ((spins & 255) == 0 &&
                 __any_sync(0xffffffffu, *(volatile int*)&sh.gave_up || clock64() - start > 4 * kWaitClocks)) {
                 record_error(p.hdr, LA_DEVERR_WAIT_TIMEOUT);
@@ -970,7 +993,8 @@ cudaError_t dispatch(const GatedParams& p, int slices, cudaStream_t s) {
                      tile_aligned(p.h, p.C, sizeof(TX));
     // stages that fill shared memory
     constexpr int kBytes = (int)(sizeof(TA) + (Rev ? 2 : 1) * sizeof(TX));   // of a token and channel
-    constexpr int W = 4, K = kBytes <= 10 ? 16 : 8, S = kBytes <= 4 ? 11 : kBytes <= 6 ? 8 : kBytes <= 8 ? 6 : kBytes <= 10 ? 5 : 8;
+    constexpr int W = 4, K = kBytes <= 4 ? 32 : kBytes <= 10 ? 16 : 8;
+    constexpr int S = kBytes <= 4 ? 6 : kBytes <= 6 ? 8 : kBytes <= 8 ? 6 : kBytes <= 10 ? 4 : 8;
     if (tma && p.T > W * K) return run_ring<TA, TX, Rev, W, K, S, 1>(p, slices, s);
     return vec ? run_registers<TA, TX, Rev, true, W, K, 1>(p, slices, s) : run_registers<TA, TX, Rev, false, W, K, 1>(p, slices, s);
 }
