@@ -491,8 +491,8 @@ LA_API la_status la_layer_norm(const void* x, const float* weight, const float* 
  *     dweight = sum of dy xh and dbias = sum of dy over the rows of each group.
  *   x, dy, dx: [rows, d] of dtype; mean, rstd: fp32 [rows] from la_layer_norm;
  *   dweight, dbias: NULL or fp32 [groups, d] (written, not added to; 0 for no
- *   rows).  Sums over rows are fp32 per block and fp64 across blocks, in a
- *   fixed order (deterministic for a given device).  workspace:
+ *   rows).  Sums over rows are fp32 within a block and compensated fp32 across
+ *   blocks, in a fixed order (deterministic).  workspace:
  *   la_layer_norm_backward_workspace_bytes(...) bytes, 256-byte aligned.
  */
 LA_API la_status la_layer_norm_backward(const void* x, const void* dy, const float* weight, const float* mean,
@@ -501,7 +501,7 @@ LA_API la_status la_layer_norm_backward(const void* x, const void* dy, const flo
                                         void* stream);
 
 /* la_layer_norm_backward_workspace_bytes - scratch size for la_layer_norm_backward
- *   on the current device (0 for arguments it rejects). */
+ *   (0 for arguments it rejects). */
 LA_API size_t la_layer_norm_backward_workspace_bytes(int dtype, int64_t rows, int groups, int d);
 
 /*

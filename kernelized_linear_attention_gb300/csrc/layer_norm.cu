@@ -4,14 +4,16 @@
 // and dy and writes dx once.  A row stays in the registers of the L lanes that
 // share it (E vectors of N values each) between the sums over it and its
 // output; the variance comes from the deviations in registers, not from sums of
-// squares.  Rows of up to 64 vectors share a warp, which then holds U rows at
-// once so that their loads and sums overlap; longer rows take a block.
+// squares.  A group holds U rows at once so that their loads and sums overlap.
+// In the forward a row shares a warp as far as its lanes can hold it (16 vectors
+// each: sums without a barrier); in the backward, whose lanes also keep two fp32
+// sums per column, rows of more than a kilobyte take a block.
 //
 // A group of lanes keeps one weight row: it walks over rows a multiple of
 // `groups` apart.  Its weights are read once, and in the backward its columns'
 // weight gradients add up in registers over all its rows.  Blocks leave their
 // sums in the workspace as rows of a [M][groups * d] matrix that a second
-// kernel adds up by column in fp64, in a fixed order.
+// kernel adds up by column with compensated sums, in a fixed order.
 #include "internal.h"
 #include "vec.cuh"
 
@@ -54,111 +56,169 @@ __device__ __forceinline__ void row_sums(float (&x)[U], float* scratch) {
     }
 }
 
-// The lane's E vectors of a row: vector e starts at column (e L + lane) N.
+// The lane's E vectors of a row, which `row` points into at the lane's first column; vector e lies e L N
+// columns on and is there when that is below `left`, the columns from the lane's first on.
 template <typename S, typename T>
-__device__ __forceinline__ void load_row(Vec<T, S::N> (&x)[S::E], const T* row, int d, int lane, bool live) {
+__device__ __forceinline__ void load_row(Vec<T, S::N> (&x)[S::E], const T* row, int left) {
 #pragma unroll
     for (int e = 0; e < S::E; ++e) {
-        const int c = (e * S::L + lane) * S::N;
-        if (live && c < d) x[e] = *reinterpret_cast<const Vec<T, S::N>*>(row + c);
-        else
-#pragma unroll
-            for (int k = 0; k < S::N; ++k) x[e].v[k] = down<T>(0.f);
-    }
-}
-template <typename S>
-__device__ __forceinline__ void load_params(float (&w)[S::kValues], const float* p, int64_t at, int d, int lane, float missing) {
-#pragma unroll
-    for (int e = 0; e < S::E; ++e)
-#pragma unroll
-        for (int k = 0; k < S::N; ++k) {
-            const int c = (e * S::L + lane) * S::N + k;
-            w[e * S::N + k] = p && c < d ? p[at + c] : missing;
+        constexpr int kStep = S::L * S::N;
+        if (e * kStep < left) {
+            x[e] = *reinterpret_cast<const Vec<T, S::N>*>(row + e * kStep);
+        } else {
+            const float zero[S::N] = {};
+            pack(x[e], zero);
         }
+    }
 }
 
-template <typename T, typename S, int U>
-__global__ void __launch_bounds__(S::kThreads) layer_norm_kernel(const T* x, const float* weight, const float* bias,
-                                                                 int64_t rows, int groups, int d, float eps, T* y,
-                                                                 float* mean, float* rstd, int64_t stride) {
-    __shared__ float scratch[S::L > 32 ? U * S::L / 32 : 1];
-    const int lane = threadIdx.x % S::L;
-    const int64_t first = (int64_t)blockIdx.x * S::kRows + threadIdx.x / S::L;
-    const float fd = (float)d;
-    // one weight row for all rows of the group, held where the registers allow it
-    constexpr bool kHeld = S::kValues <= 8;
-    const bool one = stride % groups == 0;
-    float w[S::kValues], b[S::kValues];
-    if (kHeld && one) {
-        const int64_t at = first % groups * d;
-        load_params<S>(w, weight, at, d, lane, 1.f);
-        load_params<S>(b, bias, at, d, lane, 0.f);
-    }
-    // a row group that starts behind the last row still takes part in the block's sums
-    const int64_t turns = (rows - (int64_t)blockIdx.x * S::kRows + stride * U - 1) / (stride * U);
-    for (int64_t turn = 0; turn < turns; ++turn) {
-        Vec<T, S::N> v[U][S::E];
-        float s[U], q[U];
+// N weights or biases from column c < d on; `missing` where there are none.  Vectors of columns come with
+// 16-byte aligned parameters.
+template <int N>
+__device__ __forceinline__ void load_params(float* w, const float* p, int64_t at, float missing) {
+    if (!p) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t row = first + (turn * U + u) * stride;
-            load_row<S, T>(v[u], x + row * d, d, lane, row < rows);
+        for (int k = 0; k < N; ++k) w[k] = missing;
+    } else if constexpr (N >= 4) {
+#pragma unroll
+        for (int k = 0; k < N; k += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(p + at + k);
+            w[k] = v.x; w[k + 1] = v.y; w[k + 2] = v.z; w[k + 3] = v.w;
         }
+    } else {
+        w[0] = p[at];
+    }
+}
+// The lane's parameters of a whole row, `p` at its first column.
+template <typename S>
+__device__ __forceinline__ void load_row_params(float (&w)[S::kValues], const float* p, int left, float missing) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+    for (int e = 0; e < S::E; ++e) {
+        constexpr int kStep = S::L * S::N;
+        load_params<S::N>(w + e * S::N, e * kStep < left ? p : nullptr, e * kStep, missing);
+    }
+}
+__device__ __forceinline__ const float* row_of(const float* p, int64_t at) { return p ? p + at : nullptr; }
+
+template <int V>
+struct Count {
+    static constexpr int value = V;
+};
+
+// 1 / sqrt(v), within one step: the approximate root and one step of Newton's method (0 and infinity
+// keep the root's answer).
+__device__ __forceinline__ float inverse_root(float v) {
+    const float r = rsqrtf(v);
+    return v > 0.f && v < INFINITY ? fmaf(0.5f * r, fmaf(-v * r, r, 1.f), r) : r;
+}
+// s / d: the product with 1 / d and what it leaves (equal values have their value as mean).
+__device__ __forceinline__ float mean_of(float s, float d, float over_d) {
+    const float m = s * over_d;
+    return fmaf(fmaf(-m, d, s), over_d, m);
+}
+
+// The turns of a row group: rows first, first + stride, ..  `whole` turns of U rows that every group of
+// the block has; the rest one row at a time, which some groups may not have.
+struct Turns {
+    int whole, rest, mine;       // turns of U; further turns of one; the group's rows
+};
+template <typename S, int U>
+__device__ __forceinline__ Turns turns_of(int64_t rows, int64_t stride, int64_t first) {
+    const int64_t block = (int64_t)blockIdx.x * S::kRows, last = block + S::kRows - 1;
+    Turns t;
+    t.mine = first < rows ? (int)((rows - 1 - first) / stride) + 1 : 0;
+    const int most = block < rows ? (int)((rows - 1 - block) / stride) + 1 : 0;
+    t.whole = last < rows ? ((int)((rows - 1 - last) / stride) + 1) / U : 0;
+    t.rest = most - t.whole * U;
+    return t;
+}
+
+// stride is a multiple of groups: every row of a row group has the same weight row.
+template <typename T, typename S, int U>
+__global__ void __launch_bounds__(S::kThreads, S::E == 1 && S::L <= 32 ? 4 : 1)
+layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t rows, int groups, int d, float eps, T* y,
+                  float* mean, float* rstd, int64_t stride) {
+    __shared__ float scratch[S::L > 32 ? U * S::L / 32 : 1];
+    const int lane = threadIdx.x % S::L, col = lane * S::N, left = d - col;
+    const int64_t first = (int64_t)blockIdx.x * S::kRows + threadIdx.x / S::L, step = stride * d;
+    const float fd = (float)d, over_d = 1.f / fd;
+    // the group's weights stay where the registers allow it
+    constexpr bool kHeld = S::kValues <= 8;
+    float w[S::kValues], b[S::kValues];
+    const int64_t at = first % groups * d + col;
+    if (kHeld) {
+        load_row_params<S>(w, row_of(weight, at), left, 1.f);
+        load_row_params<S>(b, row_of(bias, at), left, 0.f);
+    }
+    const Turns turns = turns_of<S, U>(rows, stride, first);
+
+    // V rows from `row` on, stride apart; `live`: there are any
+    auto some_rows = [&](auto count, int64_t row, bool live) {
+        constexpr int V = decltype(count)::value;
+        Vec<T, S::N> v[V][S::E];
+        float s[V], q[V];
+        const T* at_x = x + row * d + col;
+        T* at_y = y + row * d + col;
+#pragma unroll
+        for (int u = 0; u < V; ++u) load_row<S, T>(v[u], at_x + u * step, live ? left : 0);
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
             s[u] = 0.f;
 #pragma unroll
-            for (int e = 0; e < S::E; ++e)
+            for (int e = 0; e < S::E; ++e) {
+                float f[S::N];
+                unpack(f, v[u][e]);
 #pragma unroll
-                for (int k = 0; k < S::N; ++k) s[u] += up(v[u][e].v[k]);
+                for (int k = 0; k < S::N; ++k) s[u] += f[k];
+            }
         }
-        row_sums<S, U>(s, scratch);
+        row_sums<S, V>(s, scratch);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            s[u] /= fd;         // (a product with 1 / d would miss the mean of equal values)
+        for (int u = 0; u < V; ++u) {
+            s[u] = mean_of(s[u], fd, over_d);
             q[u] = 0.f;
 #pragma unroll
             for (int e = 0; e < S::E; ++e)
-                if ((e * S::L + lane) * S::N < d)
+                if (e * S::L * S::N < left) {
+                    float f[S::N];
+                    unpack(f, v[u][e]);
 #pragma unroll
-                    for (int k = 0; k < S::N; ++k) {
-                        const float c = up(v[u][e].v[k]) - s[u];
-                        q[u] = fmaf(c, c, q[u]);
-                    }
+                    for (int k = 0; k < S::N; ++k) q[u] = fmaf(f[k] - s[u], f[k] - s[u], q[u]);
+                }
         }
-        row_sums<S, U>(q, scratch);
+        row_sums<S, V>(q, scratch);
+        if (!live) return;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t row = first + (turn * U + u) * stride;
-            if (row >= rows) continue;
-            const float mu = s[u], rs = 1.f / sqrtf(q[u] / fd + eps);
-            const int64_t at = kHeld && one ? 0 : row % groups * d;
+        for (int u = 0; u < V; ++u) {
+            const float mu = s[u], rs = inverse_root(fmaf(q[u], over_d, eps));
 #pragma unroll
             for (int e = 0; e < S::E; ++e) {
-                const int c = (e * S::L + lane) * S::N;
-                if (c >= d) continue;
-                Vec<T, S::N> o;
-#pragma unroll
-                for (int k = 0; k < S::N; ++k) {
-                    const float xh = (up(v[u][e].v[k]) - mu) * rs;
-                    float we, be;
-                    if (kHeld && one) {
-                        we = w[e * S::N + k];
-                        be = b[e * S::N + k];
-                    } else {
-                        we = weight ? weight[at + c + k] : 1.f;
-                        be = bias ? bias[at + c + k] : 0.f;
-                    }
-                    o.v[k] = down<T>(fmaf(xh, we, be));
+                constexpr int kStep = S::L * S::N;
+                if (e * kStep >= left) continue;
+                float f[S::N], we[S::N], be[S::N];
+                unpack(f, v[u][e]);
+                if (!kHeld) {
+                    load_params<S::N>(we, weight, at + e * kStep, 1.f);
+                    load_params<S::N>(be, bias, at + e * kStep, 0.f);
                 }
-                *reinterpret_cast<Vec<T, S::N>*>(y + row * d + c) = o;
+#pragma unroll
+                for (int k = 0; k < S::N; ++k)
+                    f[k] = kHeld ? fmaf((f[k] - mu) * rs, w[e * S::N + k], b[e * S::N + k])
+                                 : fmaf((f[k] - mu) * rs, we[k], be[k]);
+                Vec<T, S::N> o;
+                pack(o, f);
+                *reinterpret_cast<Vec<T, S::N>*>(at_y + u * step + e * kStep) = o;
             }
             if (lane == 0) {
-                if (mean) mean[row] = mu;
-                if (rstd) rstd[row] = rs;
+                if (mean) mean[row + u * stride] = mu;
+                if (rstd) rstd[row + u * stride] = rs;
             }
         }
-    }
+    };
+    int64_t row = first;
+    for (int turn = 0; turn < turns.whole; ++turn, row += U * stride) some_rows(Count<U>{}, row, true);
+    for (int turn = 0; turn < turns.rest; ++turn, row += stride)
+        some_rows(Count<1>{}, row, turns.whole * U + turn < turns.mine);
 }
 
 // part[slot][d]: the weight and bias gradients of one weight row over some rows, slot i of weight row
@@ -169,68 +229,81 @@ __global__ void __launch_bounds__(S::kThreads) layer_norm_backward_kernel(const 
                                                                           const float* mean, const float* rstd,
                                                                           int64_t rows, int groups, int d, T* dx,
                                                                           float2* part, int64_t stride) {
-    __shared__ float scratch[S::L > 32 ? U * S::L / 32 : 1];
+    __shared__ float scratch[S::L > 32 ? 2 * U * S::L / 32 : 1];
     extern __shared__ float2 sums[];                        // [kRows][d], L <= 32
-    const int lane = threadIdx.x % S::L, group = threadIdx.x / S::L;
-    const int64_t first = (int64_t)blockIdx.x * S::kRows + group;
+    const int lane = threadIdx.x % S::L, group = threadIdx.x / S::L, col = lane * S::N, left = d - col;
+    const int64_t first = (int64_t)blockIdx.x * S::kRows + group, step = stride * d;
     const float over_d = 1.f / d;
     constexpr bool kHeld = S::kValues <= 8;
-    const int64_t at = first % groups * d;                  // stride is a multiple of groups
+    const int64_t at = first % groups * d + col;            // stride is a multiple of groups
     float w[S::kValues], dw[S::kValues], db[S::kValues];
-    if (kHeld) load_params<S>(w, weight, at, d, lane, 1.f);
+    if (kHeld) load_row_params<S>(w, row_of(weight, at), left, 1.f);
 #pragma unroll
     for (int k = 0; k < S::kValues; ++k) dw[k] = db[k] = 0.f;
-    const int64_t turns = (rows - (int64_t)blockIdx.x * S::kRows + stride * U - 1) / (stride * U);
-    for (int64_t turn = 0; turn < turns; ++turn) {
-        Vec<T, S::N> v[U][S::E], g[U][S::E];
-        float mu[U], rs[U], s1[U], s2[U];
+    const Turns turns = turns_of<S, U>(rows, stride, first);
+
+    auto some_rows = [&](auto count, int64_t row, bool live) {
+        constexpr int V = decltype(count)::value;
+        Vec<T, S::N> v[V][S::E], g[V][S::E];
+        float mu[V], rs[V], sums_of[2 * V];                 // of w dy, and of w dy xh
+        const int64_t at_row = row * d + col;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t row = first + (turn * U + u) * stride;
-            load_row<S, T>(v[u], x + row * d, d, lane, row < rows);
-            load_row<S, T>(g[u], dy + row * d, d, lane, row < rows);
-            mu[u] = row < rows ? mean[row] : 0.f;
-            rs[u] = row < rows ? rstd[row] : 0.f;
+        for (int u = 0; u < V; ++u) {
+            load_row<S, T>(v[u], x + at_row + u * step, live ? left : 0);
+            load_row<S, T>(g[u], dy + at_row + u * step, live ? left : 0);
+            mu[u] = live ? mean[row + u * stride] : 0.f;
+            rs[u] = live ? rstd[row + u * stride] : 0.f;
         }
-        if (!kHeld) load_params<S>(w, weight, at, d, lane, 1.f);
+        if (!kHeld) load_row_params<S>(w, row_of(weight, at), left, 1.f);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            s1[u] = s2[u] = 0.f;
-            const bool live = first + (turn * U + u) * stride < rows;
+        for (int u = 0; u < V; ++u) {
+            float s1 = 0.f, s2 = 0.f;
 #pragma unroll
             for (int e = 0; e < S::E; ++e)
-                if (live && (e * S::L + lane) * S::N < d)
+                if (live && e * S::L * S::N < left) {
+                    float fx[S::N], fg[S::N];
+                    unpack(fx, v[u][e]);
+                    unpack(fg, g[u][e]);
 #pragma unroll
                     for (int k = 0; k < S::N; ++k) {
                         const int i = e * S::N + k;
-                        const float gy = up(g[u][e].v[k]), xh = (up(v[u][e].v[k]) - mu[u]) * rs[u], t = gy * w[i];
-                        s1[u] += t;
-                        s2[u] = fmaf(t, xh, s2[u]);
-                        dw[i] = fmaf(gy, xh, dw[i]);
-                        db[i] += gy;
+                        const float xh = (fx[k] - mu[u]) * rs[u], t = fg[k] * w[i];
+                        s1 += t;
+                        s2 = fmaf(t, xh, s2);
+                        dw[i] = fmaf(fg[k], xh, dw[i]);
+                        db[i] += fg[k];
                     }
+                }
+            sums_of[u] = s1;
+            sums_of[V + u] = s2;
         }
-        row_sums<S, U>(s1, scratch);
-        row_sums<S, U>(s2, scratch);
+        row_sums<S, 2 * V>(sums_of, scratch);
+        if (!live) return;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t row = first + (turn * U + u) * stride;
-            if (row >= rows) continue;
-            const float m1 = s1[u] * over_d, m2 = s2[u] * over_d;
+        for (int u = 0; u < V; ++u) {
+            const float m1 = sums_of[u] * over_d, m2 = sums_of[V + u] * over_d;
 #pragma unroll
             for (int e = 0; e < S::E; ++e) {
-                const int c = (e * S::L + lane) * S::N;
-                if (c >= d) continue;
-                Vec<T, S::N> o;
+                constexpr int kStep = S::L * S::N;
+                if (e * kStep >= left) continue;
+                float fx[S::N], fg[S::N];
+                unpack(fx, v[u][e]);
+                unpack(fg, g[u][e]);
 #pragma unroll
                 for (int k = 0; k < S::N; ++k) {
-                    const float t = up(g[u][e].v[k]) * w[e * S::N + k], xh = (up(v[u][e].v[k]) - mu[u]) * rs[u];
-                    o.v[k] = down<T>(rs[u] * (t - m1 - xh * m2));
+                    const float xh = (fx[k] - mu[u]) * rs[u];
+                    fx[k] = rs[u] * (fmaf(fg[k], w[e * S::N + k], -m1) - xh * m2);
                 }
-                *reinterpret_cast<Vec<T, S::N>*>(dx + row * d + c) = o;
+                Vec<T, S::N> o;
+                pack(o, fx);
+                *reinterpret_cast<Vec<T, S::N>*>(dx + at_row + u * step + e * kStep) = o;
             }
         }
-    }
+    };
+    int64_t row = first;
+    for (int turn = 0; turn < turns.whole; ++turn, row += U * stride) some_rows(Count<U>{}, row, true);
+    for (int turn = 0; turn < turns.rest; ++turn, row += stride)
+        some_rows(Count<1>{}, row, turns.whole * U + turn < turns.mine);
     asm volatile("griddepcontrol.launch_dependents;");
     if (!part) return;
     if (S::kRows > 1 && S::kRows % groups == 0) {
@@ -262,33 +335,51 @@ __global__ void __launch_bounds__(S::kThreads) layer_norm_backward_kernel(const 
     }
 }
 
+// A sum and what its additions have rounded away (the exact error of each, by two-sum): as good as fp64,
+// whose two additions a clock per SM made the join take 40 us.
+struct Sum {
+    float s = 0.f, c = 0.f;
+    __device__ __forceinline__ void add(float x) {
+        const float t = s + x, b = t - s;
+        c += (s - (t - b)) + (x - b);
+        s = t;
+    }
+    __device__ __forceinline__ float value() const {
+        const float t = s + c;
+        return isfinite(s) ? t : s;     // infinities leave no error term
+    }
+};
+
 // Column sums of part[M][n]: 32 columns a block, 32 threads a column.
 __global__ void __launch_bounds__(kJoinCols * kJoinRows) layer_norm_join_kernel(const float2* part, int64_t M, int64_t n,
                                                                                 float* dweight, float* dbias) {
-    __shared__ double sw[kJoinRows][kJoinCols], sb[kJoinRows][kJoinCols];
+    __shared__ float4 sums[kJoinRows][kJoinCols];
     const int col = threadIdx.x % kJoinCols, r = threadIdx.x / kJoinCols;
     const int64_t j = (int64_t)blockIdx.x * kJoinCols + col;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    double dw = 0., db = 0.;
+    Sum dw, db;
     if (j < n)
-#pragma unroll 4
+#pragma unroll 8
         for (int64_t m = r; m < M; m += kJoinRows) {
             const float2 v = part[m * n + j];
-            dw += v.x;
-            db += v.y;
+            dw.add(v.x);
+            db.add(v.y);
         }
-    sw[r][col] = dw;
-    sb[r][col] = db;
     for (int o = kJoinRows / 2; o > 0; o >>= 1) {
+        if (r < 2 * o) sums[r][col] = make_float4(dw.s, dw.c, db.s, db.c);
         __syncthreads();
         if (r < o) {
-            sw[r][col] += sw[r + o][col];
-            sb[r][col] += sb[r + o][col];
+            const float4 q = sums[r + o][col];
+            dw.add(q.x);
+            dw.c += q.y;
+            db.add(q.z);
+            db.c += q.w;
         }
+        __syncthreads();
     }
     if (r == 0 && j < n) {
-        if (dweight) dweight[j] = (float)sw[0][col];
-        if (dbias) dbias[j] = (float)sb[0][col];
+        if (dweight) dweight[j] = dw.value();
+        if (dbias) dbias[j] = db.value();
     }
 }
 
@@ -322,9 +413,10 @@ int64_t backward_slots(int64_t rows, int groups) {
 }
 
 struct Forward {
+    static constexpr bool kWide = true;      // rows of up to 16 vectors a lane share a warp
     template <typename T, typename S>
     static int64_t run(const Args& a) {
-        constexpr int U = S::kValues <= 8 && S::L <= 32 ? 4 : S::kValues <= 16 ? 2 : 1;
+        constexpr int U = S::E == 1 && S::L <= 32 ? 4 : S::E <= 2 ? 2 : 1;
         // as many blocks as fill the SMs several times, more only where the grid limit asks for it
         int64_t blocks = ceil_div(a.rows, (int64_t)S::kRows * U);
         const int64_t most = 152 * 16 * 256 / S::kThreads, unit = a.groups / gcd(a.groups, S::kRows);
@@ -337,9 +429,10 @@ struct Forward {
     }
 };
 struct Backward {
+    static constexpr bool kWide = false;
     template <typename T, typename S>
     static int64_t run(const Args& a) {
-        constexpr int U = S::kValues <= 8 && S::L <= 32 ? 2 : 1;
+        constexpr int U = S::kValues <= 8 ? 4 : S::kValues <= 16 && S::L <= 32 ? 2 : 1;
         const int64_t blocks = backward_blocks<S>(a.rows, a.groups);
         const bool reduce = a.part && S::kRows > 1 && S::kRows % a.groups == 0;
         const size_t smem = reduce ? sizeof(float2) * S::kRows * (size_t)a.d : 0;
@@ -350,12 +443,13 @@ struct Backward {
     }
 };
 struct Slots {
+    static constexpr bool kWide = false;
     template <typename T, typename S>
     static int64_t run(const Args& a) { return backward_slots<S>(a.rows, a.groups); }
 };
 
-// The lanes and vectors of a row: the fewest lanes that hold it in one vector each up to a warp, two
-// vectors a lane up to 64, then a block of 128 to 512 lanes.
+// The lanes and vectors of a row: the fewest lanes that hold it in one vector each up to a warp, then
+// more vectors a lane or a block of 128 to 512 lanes.
 template <typename Op, typename T>
 int64_t by_shape(const Args& a, bool aligned) {
     constexpr int N = 16 / sizeof(T);
@@ -367,6 +461,12 @@ int64_t by_shape(const Args& a, bool aligned) {
         if (n <= 16) return Op::template run<T, Shape<16, 1, N>>(a);
         if (n <= 32) return Op::template run<T, Shape<32, 1, N>>(a);
         if (n <= 64) return Op::template run<T, Shape<32, 2, N>>(a);
+        if constexpr (Op::kWide) {
+            if (n <= 128) return Op::template run<T, Shape<32, 4, N>>(a);
+            if (n <= 192) return Op::template run<T, Shape<32, 6, N>>(a);
+            if (n <= 256) return Op::template run<T, Shape<32, 8, N>>(a);
+            if (n <= 512) return Op::template run<T, Shape<32, 16, N>>(a);
+        }
         if (n <= 128) return Op::template run<T, Shape<128, 1, N>>(a);
         if (n <= 256) return Op::template run<T, Shape<256, 1, N>>(a);
         if (n <= 512) return Op::template run<T, Shape<512, 1, N>>(a);
@@ -377,6 +477,10 @@ int64_t by_shape(const Args& a, bool aligned) {
     }
     if (d <= 32) return Op::template run<T, Shape<32, 1, 1>>(a);
     if (d <= 128) return Op::template run<T, Shape<32, 4, 1>>(a);
+    if constexpr (Op::kWide) {
+        if (d <= 512) return Op::template run<T, Shape<32, 16, 1>>(a);
+        if (d <= 1024) return Op::template run<T, Shape<32, 32, 1>>(a);
+    }
     if (d <= 512) return Op::template run<T, Shape<128, 4, 1>>(a);
     if (d <= 1024) return Op::template run<T, Shape<256, 4, 1>>(a);
     if (d <= 4096) return Op::template run<T, Shape<512, 8, 1>>(a);
@@ -405,7 +509,7 @@ cudaError_t layer_norm(const void* x, const float* weight, const float* bias, in
     a.x = x; a.weight = weight; a.bias = bias;
     a.rows = rows; a.groups = groups; a.d = d; a.eps = eps;
     a.out = y; a.mean = mean; a.rstd = rstd; a.stream = s;
-    return (cudaError_t)by_type<Forward>(a, dtype, on_16(x) && on_16(y));
+    return (cudaError_t)by_type<Forward>(a, dtype, on_16(x) && on_16(y) && on_16(weight) && on_16(bias));
 }
 
 // Covers both layouts of the rows: the choice between them goes by the call's pointers.
@@ -417,7 +521,7 @@ size_t layer_norm_backward_workspace_bytes(int dtype, int64_t rows, int groups, 
 cudaError_t layer_norm_backward(const void* x, const void* dy, const float* weight, const float* mean,
                                 const float* rstd, int dtype, int64_t rows, int groups, int d, void* dx,
                                 float* dweight, float* dbias, void* workspace, cudaStream_t s) {
-    const bool aligned = on_16(x) && on_16(dy) && on_16(dx);
+    const bool aligned = on_16(x) && on_16(dy) && on_16(dx) && on_16(weight);
     Args a{};
     a.x = x; a.dy = dy; a.weight = weight; a.mean_in = mean; a.rstd_in = rstd;
     a.rows = rows; a.groups = groups; a.d = d;

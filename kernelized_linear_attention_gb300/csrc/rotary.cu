@@ -29,47 +29,54 @@ __device__ __forceinline__ unsigned long long turn_fraction(float freq) {
     return (unsigned long long)(long long)((frac < 0.5 ? frac : frac - 1.0) * 18446744073709551616.0);
 }
 
-// Units of a block: token x (q's heads, then k's) x unit within the head.  Units 0 .. pair_units - 1
-// turn pairs, the rest copy channels that are not rotated.
+// A block's units: token x head (of q's heads, then k's, the block's share of them) x unit of the head.
+// Units 0 .. pair_units - 1 of a head turn pairs, the rest copy channels that are not rotated.
 struct RotaryPlan {
-    int tokens;          // tokens per block
-    int heads;           // heads of q and k together
+    int tokens;              // tokens per block
+    int heads, share;        // heads of q and k together; per block
     int pair_units, units;   // per head
+    uint32_t over_units, over_share;   // 2^32 / units and 2^32 / (share units), rounded up
 };
+constexpr int kMostUnits = 8192;     // of a block: products of a unit and a divisor stay below 2^32
+
+// i / n for i, n <= kMostUnits, from m = 2^32 / n rounded up (0 for n = 1).
+__device__ __forceinline__ int over(int i, uint32_t m) { return m ? (int)__umulhi((uint32_t)i, m) : i; }
 
 template <typename T, int N, bool Interleaved>
 __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_constant__ RotaryParams p,
-                                                               const __grid_constant__ RotaryPlan plan) {
+                                                                const __grid_constant__ RotaryPlan plan) {
     extern __shared__ float2 cs[];       // [tokens][P]
     using V = Vec<T, N>;
+    constexpr bool kOne = Interleaved && N > 1;   // whole pairs in one vector
+    constexpr int kPairs = kOne ? N / 2 : N;
     const int64_t t0 = (int64_t)blockIdx.x * plan.tokens;
-    const int tokens = (int)min64(plan.tokens, p.T - t0);
-    const int per_token = plan.heads * plan.units, total = tokens * per_token;
+    const int h0 = blockIdx.y * plan.share;
+    const int tokens = (int)min64(plan.tokens, p.T - t0), per_token = plan.share * plan.units;
+    const int total = tokens * per_token, second = Interleaved ? 1 : p.P;
 
-    auto turn_units = [&](int first, bool table) {
+    for (int first = threadIdx.x; first - (int)threadIdx.x < total; first += kUnits * kRotaryThreads) {
         V a[kUnits], b[kUnits];
         T* out[kUnits];
         int pair[kUnits];                // token * P + first pair, or -1: copied; -2: nothing
-        constexpr bool kOne = Interleaved && N > 1;   // whole pairs in one vector
-        constexpr int kPairs = kOne ? N / 2 : N;
-        const int second = Interleaved ? 1 : p.P;
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
             const int i = first + u * kRotaryThreads;
             pair[u] = -2;
             if (i >= total) continue;
-            const int t = i / per_token, r = i - t * per_token, h = r / plan.units, e = r - h * plan.units;
-            const bool is_k = h >= p.H;
-            const int64_t row = ((t0 + t) * p.H + (is_k ? h - p.H : h)) * p.d;
-            const bool turned = e < plan.pair_units;
-            const int c = turned ? (Interleaved ? 2 : 1) * e * kPairs : 2 * p.P + (e - plan.pair_units) * N;
-            const T* x = static_cast<const T*>(is_k ? p.k : p.q) + row + c;
-            out[u] = static_cast<T*>(is_k ? p.k_out : p.q_out) + row + c;
+            const int t = over(i, plan.over_share), r = i - t * per_token, hh = over(r, plan.over_units);
+            const int e = r - hh * plan.units, h = h0 + hh;
+            if (h >= plan.heads) continue;
+            const bool is_k = h >= p.H, turned = e < plan.pair_units;
+            const int64_t at = ((t0 + t) * p.H + (is_k ? h - p.H : h)) * p.d +
+                               (turned ? (Interleaved ? 2 : 1) * e * kPairs : 2 * p.P + (e - plan.pair_units) * N);
+            const T* x = static_cast<const T*>(is_k ? p.k : p.q) + at;
+            out[u] = static_cast<T*>(is_k ? p.k_out : p.q_out) + at;
             a[u] = *reinterpret_cast<const V*>(x);
             if (turned && !kOne) b[u] = *reinterpret_cast<const V*>(x + second);
             pair[u] = turned ? t * p.P + e * kPairs : -1;
         }
-        if (table) {
+        if (first == (int)threadIdx.x) {
+            // the tokens' cos and sin, while the first loads are on their way
             for (int i = threadIdx.x; i < tokens * p.P; i += kRotaryThreads) {
                 const int t = i / p.P, j = i - t * p.P;
                 int axis = 0;
@@ -88,24 +95,31 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
         for (int u = 0; u < kUnits; ++u) {
             if (pair[u] == -2) continue;
             if (pair[u] >= 0) {
+                float fa[N], fb[N];
+                unpack(fa, a[u]);
+                if (!kOne) unpack(fb, b[u]);
 #pragma unroll
                 for (int k = 0; k < kPairs; ++k) {
                     const float2 w = cs[pair[u] + k];
-                    T& x0 = a[u].v[kOne ? 2 * k : k];
-                    T& x1 = kOne ? a[u].v[kOne ? 2 * k + 1 : 0] : b[u].v[k];
-                    const float f0 = up(x0), f1 = up(x1);
-                    x0 = down<T>(f0 * w.x - f1 * w.y);
-                    x1 = down<T>(f1 * w.x + f0 * w.y);
+                    float& x0 = fa[kOne ? 2 * k : k];
+                    float& x1 = kOne ? fa[kOne ? 2 * k + 1 : 0] : fb[k];
+                    const float f0 = x0, f1 = x1;
+                    // written out, so that every layout rounds alike
+                    x0 = fmaf(f0, w.x, -__fmul_rn(f1, w.y));
+                    x1 = fmaf(f1, w.x, __fmul_rn(f0, w.y));
                 }
-                if (!kOne) *reinterpret_cast<V*>(out[u] + second) = b[u];
+                pack(a[u], fa);
+                if (!kOne) {
+                    pack(b[u], fb);
+                    *reinterpret_cast<V*>(out[u] + second) = b[u];
+                }
             }
             *reinterpret_cast<V*>(out[u]) = a[u];
         }
-    };
-    turn_units(threadIdx.x, true);
-    for (int first = threadIdx.x + kUnits * kRotaryThreads; first < total; first += kUnits * kRotaryThreads)
-        turn_units(first, false);
+    }
 }
+
+uint32_t reciprocal(int n) { return n > 1 ? (uint32_t)(0xffffffffu / (uint32_t)n) + 1 : 0; }
 
 template <typename T, int N>
 cudaError_t run(const RotaryParams& p, cudaStream_t s) {
@@ -113,14 +127,20 @@ cudaError_t run(const RotaryParams& p, cudaStream_t s) {
     plan.heads = p.k ? 2 * p.H : p.H;
     plan.pair_units = p.interleaved && N > 1 ? 2 * p.P / N : p.P / N;
     plan.units = plan.pair_units + (p.d - 2 * p.P) / N;
-    // enough tokens that every thread has kUnits units, as far as the table fits 32 KB
-    const int64_t per_token = (int64_t)plan.heads * plan.units;
+    plan.share = (int)min64(plan.heads, kMostUnits / 2 / plan.units);
+    plan.share = (int)ceil_div(plan.heads, ceil_div(plan.heads, plan.share));
+    // enough tokens that every thread has kUnits units, but no fewer blocks than SMs for it, and no more
+    // than a table of 32 KB holds
+    const int64_t per_token = (int64_t)plan.share * plan.units, rest = ceil_div(plan.heads, plan.share);
     int64_t tokens = ceil_div((int64_t)kUnits * kRotaryThreads, per_token);
     tokens = min64(tokens, 32 * 1024 / ((int64_t)sizeof(float2) * p.P));
-    tokens = min64(tokens > 0 ? tokens : 1, p.T);
+    tokens = min64(tokens, p.T * rest / 152);
+    if (tokens < 1) tokens = 1;
     plan.tokens = (int)tokens;
+    plan.over_units = reciprocal(plan.units);
+    plan.over_share = reciprocal((int)per_token);
     const size_t smem = sizeof(float2) * (size_t)tokens * p.P;
-    const unsigned blocks = (unsigned)ceil_div(p.T, tokens);
+    const dim3 blocks((unsigned)ceil_div(p.T, tokens), (unsigned)rest);
     if (p.interleaved) rotary_kernel<T, N, true><<<blocks, kRotaryThreads, smem, s>>>(p, plan);
     else rotary_kernel<T, N, false><<<blocks, kRotaryThreads, smem, s>>>(p, plan);
     return cudaGetLastError();

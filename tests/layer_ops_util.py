@@ -84,7 +84,7 @@ def layer_norm_backward_bounds(x, dy, mean, rstd, weight, chain):
     """Bounds of dx, dweight, dbias for given statistics.  xh = (x - mean) rstd: two roundings;
     w dy: one; the two row means: K = norm_terms(d) more and a division; the rest five of the
     terms' magnitudes.  A weight gradient sums `chain` values one after the other in fp32 (two
-    roundings before each) and joins the sums in fp64."""
+    roundings before each) and joins the sums with compensation (two roundings)."""
     x, dy = np.asarray(x, np.float64), np.asarray(dy, np.float64)
     d = x.shape[-1]
     K = norm_terms(d)
@@ -96,7 +96,7 @@ def layer_norm_backward_bounds(x, dy, mean, rstd, weight, chain):
     m2 = (u * xh).mean(-1, keepdims=True)
     dx = r * U * (2 * u + (K + 3) * m1 + (K + 7) * xh * m2 + 5 * (u + m1 + xh * m2))
     lead = tuple(range(x.ndim - w.ndim))
-    return 1.01 * dx, (chain + 4) * U * (np.abs(dy) * xh).sum(lead), (chain + 1) * U * np.abs(dy).sum(lead)
+    return 1.01 * dx, (chain + 4) * U * (np.abs(dy) * xh).sum(lead), (chain + 2) * U * np.abs(dy).sum(lead)
 
 
 def rotary_bound(x, pairs, interleaved):
