@@ -4,10 +4,10 @@
 // and dy and writes dx once.  A row stays in the registers of the L lanes that
 // share it (E vectors of N values each) between the sums over it and its
 // output; the variance comes from the deviations in registers, not from sums of
-// squares.  A group holds U rows at once so that their loads and sums overlap.
-// In the forward a row shares a warp as far as its lanes can hold it (16 vectors
-// each: sums without a barrier); in the backward, whose lanes also keep two fp32
-// sums per column, rows of more than a kilobyte take a block.
+// squares.  Rows of up to 64 vectors share a warp, longer ones take a block.  A
+// group works on U rows at once so that their sums overlap, and each lane copies
+// its vectors of the next turns to shared memory ahead (asynchronous copies that
+// it alone waits for): what is in flight does not cost registers.
 //
 // A group of lanes keeps one weight row: it walks over rows a multiple of
 // `groups` apart.  Its weights are read once, and in the backward its columns'
@@ -30,7 +30,34 @@ struct Shape {
     static constexpr int kThreads = L > 32 ? L : 256;
     static constexpr int kRows = kThreads / L;              // row groups of a block
     static constexpr int kValues = E * N;                   // values a lane holds of a row
+    using P = typename Pairs<N>::P;                         // in pairs, n of them to a vector
+    static constexpr int n = Pairs<N>::n, kPairs = E * n;
 };
+
+constexpr int blocks_per_sm(int threads, int registers) {
+    const int n = 65536 / (threads * registers);
+    return n < 1 ? 1 : n * threads > 2048 ? 2048 / threads : n;
+}
+template <typename T, typename S>
+constexpr int row_registers() { return S::kValues * (int)sizeof(T) / 4 > 0 ? S::kValues * (int)sizeof(T) / 4 : 1; }
+
+// How far ahead rows are copied: `depth` turns of U rows (of x, or of x and dy) in up to 40 KB a block,
+// two turns where they are longer, one where two do not fit.
+// Rows of single elements are loaded when they are needed (a copy has at least four bytes).
+template <typename T, typename S, int U, int Arrays>
+struct Ahead {
+    static constexpr bool on = S::N > 1;
+    static constexpr int turn_bytes = U * Arrays * S::E * S::kThreads * 16;
+    static constexpr int most = 40 * 1024 / turn_bytes;
+    static constexpr int depth = most > 6 ? 6 : most >= 2 ? most : 2 * turn_bytes <= 200 * 1024 ? 2 : 1;
+    static constexpr size_t bytes = on ? (size_t)depth * turn_bytes : 0;
+};
+__device__ __forceinline__ void copy_16(void* to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // Sum over the L lanes of a row group, for each of U rows; every lane gets it.
 template <typename S, int U>
@@ -57,14 +84,24 @@ __device__ __forceinline__ void row_sums(float (&x)[U], float* scratch) {
 }
 
 // The lane's E vectors of a row, which `row` points into at the lane's first column; vector e lies e L N
-// columns on and is there when that is below `left`, the columns from the lane's first on.
+// columns on and is there when that is below `left`, the columns from the lane's first on.  In shared
+// memory vector e of a row has the place of this thread in a run of kThreads.
 template <typename S, typename T>
-__device__ __forceinline__ void load_row(Vec<T, S::N> (&x)[S::E], const T* row, int left) {
+__device__ __forceinline__ void copy_row(uint4* place, const T* row, int left) {
+#pragma unroll
+    for (int e = 0; e < S::E; ++e) {
+        constexpr int kStep = S::L * S::N;
+        if (e * kStep < left) copy_16(place + e * S::kThreads, row + e * kStep);
+    }
+}
+template <typename S, typename T>
+__device__ __forceinline__ void load_row(Vec<T, S::N> (&x)[S::E], const uint4* place, const T* row, int left) {
 #pragma unroll
     for (int e = 0; e < S::E; ++e) {
         constexpr int kStep = S::L * S::N;
         if (e * kStep < left) {
-            x[e] = *reinterpret_cast<const Vec<T, S::N>*>(row + e * kStep);
+            x[e] = place ? *reinterpret_cast<const Vec<T, S::N>*>(place + e * S::kThreads)
+                         : *reinterpret_cast<const Vec<T, S::N>*>(row + e * kStep);
         } else {
             const float zero[S::N] = {};
             pack(x[e], zero);
@@ -72,38 +109,40 @@ __device__ __forceinline__ void load_row(Vec<T, S::N> (&x)[S::E], const T* row, 
     }
 }
 
-// N weights or biases from column c < d on; `missing` where there are none.  Vectors of columns come with
-// 16-byte aligned parameters.
-template <int N>
-__device__ __forceinline__ void load_params(float* w, const float* p, int64_t at, float missing) {
-    if (!p) {
+// A vector of weights or biases; `missing` where there are none.  Vectors of columns come with 16-byte
+// aligned parameters.
+template <typename S>
+__device__ __forceinline__ void load_params(typename S::P* w, const float* p, float missing) {
+    Vec<float, S::N> v;
+    if (p) {
+        if constexpr (S::N >= 4) {
 #pragma unroll
-        for (int k = 0; k < N; ++k) w[k] = missing;
-    } else if constexpr (N >= 4) {
-#pragma unroll
-        for (int k = 0; k < N; k += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(p + at + k);
-            w[k] = v.x; w[k + 1] = v.y; w[k + 2] = v.z; w[k + 3] = v.w;
+            for (int k = 0; k < S::N; k += 4) {
+                const float4 q = *reinterpret_cast<const float4*>(p + k);
+                v.v[k] = q.x; v.v[k + 1] = q.y; v.v[k + 2] = q.z; v.v[k + 3] = q.w;
+            }
+        } else {
+            v.v[0] = p[0];
         }
     } else {
-        w[0] = p[at];
+#pragma unroll
+        for (int k = 0; k < S::N; ++k) v.v[k] = missing;
     }
+    typename S::P f[S::n];
+    unpack_pairs<S::N>(f, v);
+#pragma unroll
+    for (int k = 0; k < S::n; ++k) w[k] = f[k];
 }
 // The lane's parameters of a whole row, `p` at its first column.
 template <typename S>
-__device__ __forceinline__ void load_row_params(float (&w)[S::kValues], const float* p, int left, float missing) {
+__device__ __forceinline__ void load_row_params(typename S::P (&w)[S::kPairs], const float* p, int left, float missing) {
 #pragma unroll
     for (int e = 0; e < S::E; ++e) {
         constexpr int kStep = S::L * S::N;
-        load_params<S::N>(w + e * S::N, e * kStep < left ? p : nullptr, e * kStep, missing);
+        load_params<S>(w + e * S::n, p && e * kStep < left ? p + e * kStep : nullptr, missing);
     }
 }
 __device__ __forceinline__ const float* row_of(const float* p, int64_t at) { return p ? p + at : nullptr; }
-
-template <int V>
-struct Count {
-    static constexpr int value = V;
-};
 
 // 1 / sqrt(v), within one step: the approximate root and one step of Newton's method (0 and infinity
 // keep the root's answer).
@@ -117,25 +156,21 @@ __device__ __forceinline__ float mean_of(float s, float d, float over_d) {
     return fmaf(fmaf(-m, d, s), over_d, m);
 }
 
-// The turns of a row group: rows first, first + stride, ..  `whole` turns of U rows that every group of
-// the block has; the rest one row at a time, which some groups may not have.
-struct Turns {
-    int whole, rest, mine;       // turns of U; further turns of one; the group's rows
+// The rows of a row group: first, first + stride, ..; and the most that a group of the block has.
+struct Rows {
+    int mine, most;
 };
-template <typename S, int U>
-__device__ __forceinline__ Turns turns_of(int64_t rows, int64_t stride, int64_t first) {
-    const int64_t block = (int64_t)blockIdx.x * S::kRows, last = block + S::kRows - 1;
-    Turns t;
-    t.mine = first < rows ? (int)((rows - 1 - first) / stride) + 1 : 0;
-    const int most = block < rows ? (int)((rows - 1 - block) / stride) + 1 : 0;
-    t.whole = last < rows ? ((int)((rows - 1 - last) / stride) + 1) / U : 0;
-    t.rest = most - t.whole * U;
-    return t;
+template <typename S>
+__device__ __forceinline__ Rows rows_of(int64_t rows, int64_t stride, int64_t first) {
+    const int64_t block = (int64_t)blockIdx.x * S::kRows;
+    return {first < rows ? (int)((rows - 1 - first) / stride) + 1 : 0,
+            block < rows ? (int)((rows - 1 - block) / stride) + 1 : 0};
 }
 
 // stride is a multiple of groups: every row of a row group has the same weight row.
 template <typename T, typename S, int U>
-__global__ void __launch_bounds__(S::kThreads, S::E == 1 && S::L <= 32 ? 4 : 1)
+__global__ void __launch_bounds__(S::kThreads,
+                                  blocks_per_sm(S::kThreads, U * row_registers<T, S>() + (S::kValues <= 8 ? 2 * S::kValues : 0) + 38))
 layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t rows, int groups, int d, float eps, T* y,
                   float* mean, float* rstd, int64_t stride) {
     __shared__ float scratch[S::L > 32 ? U * S::L / 32 : 1];
@@ -144,175 +179,268 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
     const float fd = (float)d, over_d = 1.f / fd;
     // the group's weights stay where the registers allow it
     constexpr bool kHeld = S::kValues <= 8;
-    float w[S::kValues], b[S::kValues];
+    using P = typename S::P;
+    P w[S::kPairs], b[S::kPairs];
     const int64_t at = first % groups * d + col;
     if (kHeld) {
         load_row_params<S>(w, row_of(weight, at), left, 1.f);
         load_row_params<S>(b, row_of(bias, at), left, 0.f);
     }
-    const Turns turns = turns_of<S, U>(rows, stride, first);
-
-    // V rows from `row` on, stride apart; `live`: there are any
-    auto some_rows = [&](auto count, int64_t row, bool live) {
-        constexpr int V = decltype(count)::value;
+    using A = Ahead<T, S, U, 1>;
+    extern __shared__ uint4 ahead[];                         // [depth][U][E][kThreads]
+    uint4* mine = ahead + threadIdx.x;
+    const Rows have = rows_of<S>(rows, stride, first);
+    const T* lane_x = x + first * d + col;
+    auto copy_turn = [&](int turn) {
+        if (A::on) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = turn * U + u;
+                if (i < have.mine)
+                    copy_row<S, T>(mine + ((turn % A::depth) * U + u) * S::E * S::kThreads, lane_x + i * step, left);
+            }
+            copies_done();
+        }
+    };
+    if (A::on)
+        for (int t = 0; t < A::depth - 1; ++t) copy_turn(t);
+    for (int turn = 0; turn * U < have.most; ++turn) {
+        copy_turn(turn + A::depth - 1);
+        if (A::on) wait_copies<A::depth - 1>();
+        constexpr int V = U;
         Vec<T, S::N> v[V][S::E];
         float s[V], q[V];
-        const T* at_x = x + row * d + col;
-        T* at_y = y + row * d + col;
 #pragma unroll
-        for (int u = 0; u < V; ++u) load_row<S, T>(v[u], at_x + u * step, live ? left : 0);
+        for (int u = 0; u < U; ++u) {
+            const int i = turn * U + u;
+            load_row<S, T>(v[u], A::on ? mine + ((turn % A::depth) * U + u) * S::E * S::kThreads : nullptr, lane_x + i * step,
+                           i < have.mine ? left : 0);
+        }
 #pragma unroll
         for (int u = 0; u < V; ++u) {
-            s[u] = 0.f;
+            P t = psplat<P>(0.f);
 #pragma unroll
             for (int e = 0; e < S::E; ++e) {
-                float f[S::N];
-                unpack(f, v[u][e]);
+                P f[S::n];
+                unpack_pairs<S::N>(f, v[u][e]);
 #pragma unroll
-                for (int k = 0; k < S::N; ++k) s[u] += f[k];
+                for (int k = 0; k < S::n; ++k) t = padd(t, f[k]);
             }
+            s[u] = psum(t);
         }
         row_sums<S, V>(s, scratch);
 #pragma unroll
+        for (int u = 0; u < V; ++u)
+#pragma unroll
+            for (int e = 0; e < S::E; ++e) keep_packed(v[u][e]);
+#pragma unroll
         for (int u = 0; u < V; ++u) {
             s[u] = mean_of(s[u], fd, over_d);
-            q[u] = 0.f;
+            const P minus = psplat<P>(-s[u]);
+            P t = psplat<P>(0.f);
 #pragma unroll
             for (int e = 0; e < S::E; ++e)
                 if (e * S::L * S::N < left) {
-                    float f[S::N];
-                    unpack(f, v[u][e]);
+                    P f[S::n];
+                    unpack_pairs<S::N>(f, v[u][e]);
 #pragma unroll
-                    for (int k = 0; k < S::N; ++k) q[u] = fmaf(f[k] - s[u], f[k] - s[u], q[u]);
+                    for (int k = 0; k < S::n; ++k) {
+                        f[k] = padd(f[k], minus);
+                        t = pfma(f[k], f[k], t);
+                    }
                 }
+            q[u] = psum(t);
         }
         row_sums<S, V>(q, scratch);
-        if (!live) return;
+#pragma unroll
+        for (int u = 0; u < V; ++u)
+#pragma unroll
+            for (int e = 0; e < S::E; ++e) keep_packed(v[u][e]);
 #pragma unroll
         for (int u = 0; u < V; ++u) {
+            const int i = turn * U + u;
+            if (i >= have.mine) continue;
+            const int64_t row = first + i * stride;
+            T* at_y = y + row * d + col;
             const float mu = s[u], rs = inverse_root(fmaf(q[u], over_d, eps));
+            const P minus = psplat<P>(-mu), times = psplat<P>(rs);
 #pragma unroll
             for (int e = 0; e < S::E; ++e) {
                 constexpr int kStep = S::L * S::N;
                 if (e * kStep >= left) continue;
-                float f[S::N], we[S::N], be[S::N];
-                unpack(f, v[u][e]);
+                // parameters one vector at a time: loaded ahead they would push the row out of the registers
+                if (!kHeld) asm volatile("" ::: "memory");
+                P f[S::n], we[S::n], be[S::n];
+                unpack_pairs<S::N>(f, v[u][e]);
                 if (!kHeld) {
-                    load_params<S::N>(we, weight, at + e * kStep, 1.f);
-                    load_params<S::N>(be, bias, at + e * kStep, 0.f);
+                    load_params<S>(we, row_of(weight, at + e * kStep), 1.f);
+                    load_params<S>(be, row_of(bias, at + e * kStep), 0.f);
                 }
 #pragma unroll
-                for (int k = 0; k < S::N; ++k)
-                    f[k] = kHeld ? fmaf((f[k] - mu) * rs, w[e * S::N + k], b[e * S::N + k])
-                                 : fmaf((f[k] - mu) * rs, we[k], be[k]);
+                for (int k = 0; k < S::n; ++k)
+                    f[k] = pfma(pmul(padd(f[k], minus), times), kHeld ? w[e * S::n + k] : we[k], kHeld ? b[e * S::n + k] : be[k]);
                 Vec<T, S::N> o;
-                pack(o, f);
-                *reinterpret_cast<Vec<T, S::N>*>(at_y + u * step + e * kStep) = o;
+                pack_pairs<S::N>(o, f);
+                *reinterpret_cast<Vec<T, S::N>*>(at_y + e * kStep) = o;
             }
             if (lane == 0) {
-                if (mean) mean[row + u * stride] = mu;
-                if (rstd) rstd[row + u * stride] = rs;
+                if (mean) mean[row] = mu;
+                if (rstd) rstd[row] = rs;
             }
         }
-    };
-    int64_t row = first;
-    for (int turn = 0; turn < turns.whole; ++turn, row += U * stride) some_rows(Count<U>{}, row, true);
-    for (int turn = 0; turn < turns.rest; ++turn, row += stride)
-        some_rows(Count<1>{}, row, turns.whole * U + turn < turns.mine);
+    }
 }
 
 // part[slot][d]: the weight and bias gradients of one weight row over some rows, slot i of weight row
 // i mod groups.  Row groups of a block that share a weight row are added up first where every one of
 // its weight rows has equally many (kRows a multiple of groups).
 template <typename T, typename S, int U>
-__global__ void __launch_bounds__(S::kThreads) layer_norm_backward_kernel(const T* x, const T* dy, const float* weight,
-                                                                          const float* mean, const float* rstd,
-                                                                          int64_t rows, int groups, int d, T* dx,
-                                                                          float2* part, int64_t stride) {
+__global__ void __launch_bounds__(S::kThreads,
+                                  blocks_per_sm(S::kThreads, 2 * U * row_registers<T, S>() + 3 * S::kValues + 44))
+layer_norm_backward_kernel(const T* x, const T* dy, const float* weight, const float* mean, const float* rstd, int64_t rows,
+                           int groups, int d, T* dx, float2* part, int64_t stride) {
     __shared__ float scratch[S::L > 32 ? 2 * U * S::L / 32 : 1];
-    extern __shared__ float2 sums[];                        // [kRows][d], L <= 32
+    using A = Ahead<T, S, U, 2>;
+    extern __shared__ uint4 ahead[];                        // [depth][U][x, dy][E][kThreads]
+    float2* sums = reinterpret_cast<float2*>(ahead);        // afterwards [kRows][d], L <= 32
+    uint4* mine = ahead + threadIdx.x;
     const int lane = threadIdx.x % S::L, group = threadIdx.x / S::L, col = lane * S::N, left = d - col;
     const int64_t first = (int64_t)blockIdx.x * S::kRows + group, step = stride * d;
     const float over_d = 1.f / d;
     constexpr bool kHeld = S::kValues <= 8;
     const int64_t at = first % groups * d + col;            // stride is a multiple of groups
-    float w[S::kValues], dw[S::kValues], db[S::kValues];
+    using P = typename S::P;
+    P w[S::kPairs], dw[S::kPairs], db[S::kPairs];
     if (kHeld) load_row_params<S>(w, row_of(weight, at), left, 1.f);
 #pragma unroll
-    for (int k = 0; k < S::kValues; ++k) dw[k] = db[k] = 0.f;
-    const Turns turns = turns_of<S, U>(rows, stride, first);
-
-    auto some_rows = [&](auto count, int64_t row, bool live) {
-        constexpr int V = decltype(count)::value;
+    for (int k = 0; k < S::kPairs; ++k) dw[k] = db[k] = psplat<P>(0.f);
+    const Rows have = rows_of<S>(rows, stride, first);
+    const int64_t lane_at = first * d + col;
+    auto place = [&](int turn, int u, int array) {
+        return mine + (((turn % A::depth) * U + u) * 2 + array) * S::E * S::kThreads;
+    };
+    auto copy_turn = [&](int turn) {
+        if (A::on) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = turn * U + u;
+                if (i < have.mine) {
+                    copy_row<S, T>(place(turn, u, 0), x + lane_at + i * step, left);
+                    copy_row<S, T>(place(turn, u, 1), dy + lane_at + i * step, left);
+                }
+            }
+            copies_done();
+        }
+    };
+    float next_mu[U], next_rs[U];
+    auto load_stats = [&](int turn) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = turn * U + u;
+            next_mu[u] = i < have.mine ? mean[first + i * stride] : 0.f;
+            next_rs[u] = i < have.mine ? rstd[first + i * stride] : 0.f;
+        }
+    };
+    if (A::on)
+        for (int t = 0; t < A::depth - 1; ++t) copy_turn(t);
+    load_stats(0);
+    for (int turn = 0; turn * U < have.most; ++turn) {
+        constexpr int V = U;
+        copy_turn(turn + A::depth - 1);
+        if (A::on) wait_copies<A::depth - 1>();
         Vec<T, S::N> v[V][S::E], g[V][S::E];
         float mu[V], rs[V], sums_of[2 * V];                 // of w dy, and of w dy xh
-        const int64_t at_row = row * d + col;
 #pragma unroll
         for (int u = 0; u < V; ++u) {
-            load_row<S, T>(v[u], x + at_row + u * step, live ? left : 0);
-            load_row<S, T>(g[u], dy + at_row + u * step, live ? left : 0);
-            mu[u] = live ? mean[row + u * stride] : 0.f;
-            rs[u] = live ? rstd[row + u * stride] : 0.f;
+            const int i = turn * U + u;
+            load_row<S, T>(v[u], A::on ? place(turn, u, 0) : nullptr, x + lane_at + i * step, i < have.mine ? left : 0);
+            load_row<S, T>(g[u], A::on ? place(turn, u, 1) : nullptr, dy + lane_at + i * step, i < have.mine ? left : 0);
+            mu[u] = next_mu[u];
+            rs[u] = next_rs[u];
         }
+        load_stats(turn + 1);
         if (!kHeld) load_row_params<S>(w, row_of(weight, at), left, 1.f);
 #pragma unroll
         for (int u = 0; u < V; ++u) {
-            float s1 = 0.f, s2 = 0.f;
+            const P minus = psplat<P>(-mu[u]), times = psplat<P>(rs[u]);
+            P s1 = psplat<P>(0.f), s2 = s1;
 #pragma unroll
             for (int e = 0; e < S::E; ++e)
-                if (live && e * S::L * S::N < left) {
-                    float fx[S::N], fg[S::N];
-                    unpack(fx, v[u][e]);
-                    unpack(fg, g[u][e]);
+                if (turn * U + u < have.mine && e * S::L * S::N < left) {
+                    P fx[S::n], fg[S::n];
+                    unpack_pairs<S::N>(fx, v[u][e]);
+                    unpack_pairs<S::N>(fg, g[u][e]);
 #pragma unroll
-                    for (int k = 0; k < S::N; ++k) {
-                        const int i = e * S::N + k;
-                        const float xh = (fx[k] - mu[u]) * rs[u], t = fg[k] * w[i];
-                        s1 += t;
-                        s2 = fmaf(t, xh, s2);
-                        dw[i] = fmaf(fg[k], xh, dw[i]);
-                        db[i] += fg[k];
+                    for (int k = 0; k < S::n; ++k) {
+                        const int i = e * S::n + k;
+                        const P xh = pmul(padd(fx[k], minus), times), t = pmul(fg[k], w[i]);
+                        s1 = padd(s1, t);
+                        s2 = pfma(t, xh, s2);
+                        dw[i] = pfma(fg[k], xh, dw[i]);
+                        db[i] = padd(db[i], fg[k]);
                     }
                 }
-            sums_of[u] = s1;
-            sums_of[V + u] = s2;
+            sums_of[u] = psum(s1);
+            sums_of[V + u] = psum(s2);
         }
         row_sums<S, 2 * V>(sums_of, scratch);
-        if (!live) return;
+#pragma unroll
+        for (int u = 0; u < V; ++u)
+#pragma unroll
+            for (int e = 0; e < S::E; ++e) {
+                keep_packed(v[u][e]);
+                keep_packed(g[u][e]);
+            }
 #pragma unroll
         for (int u = 0; u < V; ++u) {
-            const float m1 = sums_of[u] * over_d, m2 = sums_of[V + u] * over_d;
+            const int i = turn * U + u;
+            if (i >= have.mine) continue;
+            const P m1 = psplat<P>(-sums_of[u] * over_d), m2 = psplat<P>(-sums_of[V + u] * over_d);
+            const P minus = psplat<P>(-mu[u]), times = psplat<P>(rs[u]);
 #pragma unroll
             for (int e = 0; e < S::E; ++e) {
                 constexpr int kStep = S::L * S::N;
                 if (e * kStep >= left) continue;
-                float fx[S::N], fg[S::N];
-                unpack(fx, v[u][e]);
-                unpack(fg, g[u][e]);
+                P fx[S::n], fg[S::n];
+                unpack_pairs<S::N>(fx, v[u][e]);
+                unpack_pairs<S::N>(fg, g[u][e]);
 #pragma unroll
-                for (int k = 0; k < S::N; ++k) {
-                    const float xh = (fx[k] - mu[u]) * rs[u];
-                    fx[k] = rs[u] * (fmaf(fg[k], w[e * S::N + k], -m1) - xh * m2);
+                for (int k = 0; k < S::n; ++k) {
+                    const P xh = pmul(padd(fx[k], minus), times);
+                    fx[k] = pmul(times, pfma(xh, m2, pfma(fg[k], w[e * S::n + k], m1)));
                 }
                 Vec<T, S::N> o;
-                pack(o, fx);
-                *reinterpret_cast<Vec<T, S::N>*>(dx + at_row + u * step + e * kStep) = o;
+                pack_pairs<S::N>(o, fx);
+                *reinterpret_cast<Vec<T, S::N>*>(dx + lane_at + i * step + e * kStep) = o;
             }
         }
-    };
-    int64_t row = first;
-    for (int turn = 0; turn < turns.whole; ++turn, row += U * stride) some_rows(Count<U>{}, row, true);
-    for (int turn = 0; turn < turns.rest; ++turn, row += stride)
-        some_rows(Count<1>{}, row, turns.whole * U + turn < turns.mine);
+    }
     asm volatile("griddepcontrol.launch_dependents;");
     if (!part) return;
+    float wv[S::kValues], bv[S::kValues];
+#pragma unroll
+    for (int e = 0; e < S::E; ++e) {
+        Vec<float, S::N> q;
+        P f[S::n];
+#pragma unroll
+        for (int k = 0; k < S::n; ++k) f[k] = dw[e * S::n + k];
+        pack_pairs<S::N>(q, f);
+#pragma unroll
+        for (int k = 0; k < S::N; ++k) wv[e * S::N + k] = q.v[k];
+#pragma unroll
+        for (int k = 0; k < S::n; ++k) f[k] = db[e * S::n + k];
+        pack_pairs<S::N>(q, f);
+#pragma unroll
+        for (int k = 0; k < S::N; ++k) bv[e * S::N + k] = q.v[k];
+    }
     if (S::kRows > 1 && S::kRows % groups == 0) {
+        __syncthreads();                                    // the copies' places are free
 #pragma unroll
         for (int e = 0; e < S::E; ++e)
 #pragma unroll
             for (int k = 0; k < S::N; ++k) {
                 const int c = (e * S::L + lane) * S::N + k;
-                if (c < d) sums[group * d + c] = make_float2(dw[e * S::N + k], db[e * S::N + k]);
+                if (c < d) sums[group * d + c] = make_float2(wv[e * S::N + k], bv[e * S::N + k]);
             }
         __syncthreads();
         for (int i = threadIdx.x; i < groups * d; i += S::kThreads) {
@@ -330,7 +458,7 @@ __global__ void __launch_bounds__(S::kThreads) layer_norm_backward_kernel(const 
 #pragma unroll
             for (int k = 0; k < S::N; ++k) {
                 const int c = (e * S::L + lane) * S::N + k;
-                if (c < d) part[first * d + c] = make_float2(dw[e * S::N + k], db[e * S::N + k]);
+                if (c < d) part[first * d + c] = make_float2(wv[e * S::N + k], bv[e * S::N + k]);
             }
     }
 }
@@ -413,29 +541,37 @@ int64_t backward_slots(int64_t rows, int groups) {
 }
 
 struct Forward {
-    static constexpr bool kWide = true;      // rows of up to 16 vectors a lane share a warp
     template <typename T, typename S>
     static int64_t run(const Args& a) {
-        constexpr int U = S::E == 1 && S::L <= 32 ? 4 : S::E <= 2 ? 2 : 1;
+        constexpr int U = S::E == 1 ? 2 : 1;
         // as many blocks as fill the SMs several times, more only where the grid limit asks for it
-        int64_t blocks = ceil_div(a.rows, (int64_t)S::kRows * U);
-        const int64_t most = 152 * 16 * 256 / S::kThreads, unit = a.groups / gcd(a.groups, S::kRows);
-        if (blocks > most) blocks = most;
+        const int64_t most = 152 * 8 * 256 / S::kThreads, unit = a.groups / gcd(a.groups, S::kRows);
+        const int64_t turns = ceil_div(a.rows, most * S::kRows * U);
+        int64_t blocks = ceil_div(a.rows, turns * S::kRows * U);
         blocks = ceil_div(blocks, unit) * unit;
-        layer_norm_kernel<T, S, U><<<(unsigned)blocks, S::kThreads, 0, a.stream>>>(
+        constexpr size_t smem = Ahead<T, S, U, 1>::bytes;
+        if (smem > 48 * 1024) {
+            const cudaError_t e = cudaFuncSetAttribute(layer_norm_kernel<T, S, U>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return (int64_t)e;
+        }
+        layer_norm_kernel<T, S, U><<<(unsigned)blocks, S::kThreads, smem, a.stream>>>(
             static_cast<const T*>(a.x), a.weight, a.bias, a.rows, a.groups, a.d, a.eps, static_cast<T*>(a.out), a.mean,
             a.rstd, blocks * S::kRows);
         return (int64_t)cudaGetLastError();
     }
 };
 struct Backward {
-    static constexpr bool kWide = false;
     template <typename T, typename S>
     static int64_t run(const Args& a) {
-        constexpr int U = S::kValues <= 8 ? 4 : S::kValues <= 16 && S::L <= 32 ? 2 : 1;
+        constexpr int U = S::kValues <= 8 ? 2 : 1;
         const int64_t blocks = backward_blocks<S>(a.rows, a.groups);
         const bool reduce = a.part && S::kRows > 1 && S::kRows % a.groups == 0;
-        const size_t smem = reduce ? sizeof(float2) * S::kRows * (size_t)a.d : 0;
+        const size_t join = reduce ? sizeof(float2) * S::kRows * (size_t)a.d : 0;
+        const size_t smem = join > Ahead<T, S, U, 2>::bytes ? join : Ahead<T, S, U, 2>::bytes;
+        if (smem > 48 * 1024) {
+            const cudaError_t e = cudaFuncSetAttribute(layer_norm_backward_kernel<T, S, U>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return (int64_t)e;
+        }
         layer_norm_backward_kernel<T, S, U><<<(unsigned)blocks, S::kThreads, smem, a.stream>>>(
             static_cast<const T*>(a.x), static_cast<const T*>(a.dy), a.weight, a.mean_in, a.rstd_in, a.rows, a.groups,
             a.d, static_cast<T*>(a.out), a.part, blocks * S::kRows);
@@ -443,13 +579,12 @@ struct Backward {
     }
 };
 struct Slots {
-    static constexpr bool kWide = false;
     template <typename T, typename S>
     static int64_t run(const Args& a) { return backward_slots<S>(a.rows, a.groups); }
 };
 
-// The lanes and vectors of a row: the fewest lanes that hold it in one vector each up to a warp, then
-// more vectors a lane or a block of 128 to 512 lanes.
+// The lanes and vectors of a row: the fewest lanes that hold it in one vector each up to a warp, two
+// vectors a lane up to 64, then a block of 128 to 512 lanes.
 template <typename Op, typename T>
 int64_t by_shape(const Args& a, bool aligned) {
     constexpr int N = 16 / sizeof(T);
@@ -461,12 +596,6 @@ int64_t by_shape(const Args& a, bool aligned) {
         if (n <= 16) return Op::template run<T, Shape<16, 1, N>>(a);
         if (n <= 32) return Op::template run<T, Shape<32, 1, N>>(a);
         if (n <= 64) return Op::template run<T, Shape<32, 2, N>>(a);
-        if constexpr (Op::kWide) {
-            if (n <= 128) return Op::template run<T, Shape<32, 4, N>>(a);
-            if (n <= 192) return Op::template run<T, Shape<32, 6, N>>(a);
-            if (n <= 256) return Op::template run<T, Shape<32, 8, N>>(a);
-            if (n <= 512) return Op::template run<T, Shape<32, 16, N>>(a);
-        }
         if (n <= 128) return Op::template run<T, Shape<128, 1, N>>(a);
         if (n <= 256) return Op::template run<T, Shape<256, 1, N>>(a);
         if (n <= 512) return Op::template run<T, Shape<512, 1, N>>(a);
@@ -477,10 +606,6 @@ int64_t by_shape(const Args& a, bool aligned) {
     }
     if (d <= 32) return Op::template run<T, Shape<32, 1, 1>>(a);
     if (d <= 128) return Op::template run<T, Shape<32, 4, 1>>(a);
-    if constexpr (Op::kWide) {
-        if (d <= 512) return Op::template run<T, Shape<32, 16, 1>>(a);
-        if (d <= 1024) return Op::template run<T, Shape<32, 32, 1>>(a);
-    }
     if (d <= 512) return Op::template run<T, Shape<128, 4, 1>>(a);
     if (d <= 1024) return Op::template run<T, Shape<256, 4, 1>>(a);
     if (d <= 4096) return Op::template run<T, Shape<512, 8, 1>>(a);

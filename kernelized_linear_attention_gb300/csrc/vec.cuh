@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include "tc_ptx.cuh"
+
 namespace la {
 
 template <typename T, int N>
@@ -53,6 +55,69 @@ __device__ __forceinline__ void pack(Vec<__nv_bfloat16, N>& x, const float (&f)[
             x.v[k] = *reinterpret_cast<const uint32_t*>(&p);
         }
     }
+}
+
+// Makes the compiler unpack a bf16 vector anew after this point, instead of keeping the twice as many
+// registers of its fp32 values.
+template <typename T, int N>
+__device__ __forceinline__ void keep_packed(Vec<T, N>& x) {
+    if constexpr (sizeof(T) == 2 && N > 1) {
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) asm volatile("" : "+r"(x.v[k]));
+    }
+}
+
+// A vector's values two to a register pair (f32x2 arithmetic: one instruction for both); a single value
+// alone.
+template <int N>
+struct Pairs {
+    using P = uint64_t;
+    static constexpr int n = N / 2;
+};
+template <>
+struct Pairs<1> {
+    using P = float;
+    static constexpr int n = 1;
+};
+__device__ __forceinline__ float padd(float a, float b) { return a + b; }
+__device__ __forceinline__ float pmul(float a, float b) { return a * b; }
+__device__ __forceinline__ float pfma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float psum(float a) { return a; }
+__device__ __forceinline__ uint64_t padd(uint64_t a, uint64_t b) { return tc::f32x2_add(a, b); }
+__device__ __forceinline__ uint64_t pmul(uint64_t a, uint64_t b) { return tc::f32x2_mul(a, b); }
+__device__ __forceinline__ uint64_t pfma(uint64_t a, uint64_t b, uint64_t c) { return tc::f32x2_fma(a, b, c); }
+__device__ __forceinline__ float psum(uint64_t a) { return tc::f32x2_lo(a) + tc::f32x2_hi(a); }
+template <typename P> __device__ __forceinline__ P psplat(float x);
+template <> __device__ __forceinline__ float psplat<float>(float x) { return x; }
+template <> __device__ __forceinline__ uint64_t psplat<uint64_t>(float x) { return tc::f32x2_splat(x); }
+
+template <int N, typename T>
+__device__ __forceinline__ void unpack_pairs(typename Pairs<N>::P (&f)[Pairs<N>::n], const Vec<T, N>& x) {
+    if constexpr (N == 1) {
+        float v[1];
+        unpack(v, x);
+        f[0] = v[0];
+    } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) f[k] = tc::f32x2_of(x.v[k] << 16, x.v[k] & 0xffff0000u);
+    } else {
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) f[k] = tc::f32x2_of(__float_as_uint(x.v[2 * k]), __float_as_uint(x.v[2 * k + 1]));
+    }
+}
+template <int N, typename T>
+__device__ __forceinline__ void pack_pairs(Vec<T, N>& x, const typename Pairs<N>::P (&f)[Pairs<N>::n]) {
+    float v[N];
+    if constexpr (N == 1) {
+        v[0] = f[0];
+    } else {
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) {
+            v[2 * k] = tc::f32x2_lo(f[k]);
+            v[2 * k + 1] = tc::f32x2_hi(f[k]);
+        }
+    }
+    pack(x, v);
 }
 
 }  // namespace la
