@@ -21,8 +21,9 @@ namespace la {
 
 namespace {
 
-constexpr int kMaxBlocks = 608;     // backward: four blocks of 256 threads on each of 152 SMs
-constexpr int kJoinCols = 32, kJoinRows = 32;
+constexpr int kSms = 152;
+constexpr int kCopyBytes = 40 * 1024;   // of rows copied ahead, per block
+constexpr int kJoinCols = 8, kJoinRows = 32;
 
 template <int L_, int E_, int N_>
 struct Shape {
@@ -41,17 +42,37 @@ constexpr int blocks_per_sm(int threads, int registers) {
 template <typename T, typename S>
 constexpr int row_registers() { return S::kValues * (int)sizeof(T) / 4 > 0 ? S::kValues * (int)sizeof(T) / 4 : 1; }
 
-// How far ahead rows are copied: `depth` turns of U rows (of x, or of x and dy) in up to 40 KB a block,
+// How far ahead rows are copied: `depth` turns of U rows (of x, or of x and dy) in kCopyBytes a block,
 // two turns where they are longer, one where two do not fit.
 // Rows of single elements are loaded when they are needed (a copy has at least four bytes).
 template <typename T, typename S, int U, int Arrays>
 struct Ahead {
     static constexpr bool on = S::N > 1;
     static constexpr int turn_bytes = U * Arrays * S::E * S::kThreads * 16;
-    static constexpr int most = 40 * 1024 / turn_bytes;
+    static constexpr int most = kCopyBytes / turn_bytes;
     static constexpr int depth = most > 6 ? 6 : most >= 2 ? most : 2 * turn_bytes <= 200 * 1024 ? 2 : 1;
     static constexpr size_t bytes = on ? (size_t)depth * turn_bytes : 0;
 };
+// The registers to compile for, and the blocks of an SM that this and the copies' memory allow.
+template <typename T, typename S>
+struct ForwardPlan {
+    static constexpr int U = S::E == 1 ? 2 : 1;
+    using A = Ahead<T, S, U, 1>;
+    static constexpr int registers = U * row_registers<T, S>() + (S::kValues <= 8 ? 2 * S::kValues : 0) + 38;
+    static constexpr int by_registers = blocks_per_sm(S::kThreads, registers);
+    static constexpr int by_memory = 227 * 1024 / ((int)A::bytes + 2048);
+    static constexpr int per_sm = by_registers < by_memory ? by_registers : by_memory;
+};
+template <typename T, typename S>
+struct BackwardPlan {
+    static constexpr int U = S::kValues <= 8 ? 2 : 1;
+    using A = Ahead<T, S, U, 2>;
+    static constexpr int registers = 2 * U * row_registers<T, S>() + 3 * S::kValues + 44;
+    static constexpr int by_registers = blocks_per_sm(S::kThreads, registers);
+    static constexpr int by_memory = 227 * 1024 / ((int)A::bytes + 2048);
+    static constexpr int per_sm = by_registers < by_memory ? by_registers : by_memory;
+};
+
 __device__ __forceinline__ void copy_16(void* to, const void* from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(to)), "l"(from) : "memory");
 }
@@ -168,11 +189,12 @@ __device__ __forceinline__ Rows rows_of(int64_t rows, int64_t stride, int64_t fi
 }
 
 // stride is a multiple of groups: every row of a row group has the same weight row.
-template <typename T, typename S, int U>
-__global__ void __launch_bounds__(S::kThreads,
-                                  blocks_per_sm(S::kThreads, U * row_registers<T, S>() + (S::kValues <= 8 ? 2 * S::kValues : 0) + 38))
+template <typename T, typename S>
+__global__ void __launch_bounds__(S::kThreads, ForwardPlan<T, S>::by_registers)
 layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t rows, int groups, int d, float eps, T* y,
                   float* mean, float* rstd, int64_t stride) {
+    constexpr int U = ForwardPlan<T, S>::U;
+    using A = typename ForwardPlan<T, S>::A;
     __shared__ float scratch[S::L > 32 ? U * S::L / 32 : 1];
     const int lane = threadIdx.x % S::L, col = lane * S::N, left = d - col;
     const int64_t first = (int64_t)blockIdx.x * S::kRows + threadIdx.x / S::L, step = stride * d;
@@ -186,7 +208,6 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
         load_row_params<S>(w, row_of(weight, at), left, 1.f);
         load_row_params<S>(b, row_of(bias, at), left, 0.f);
     }
-    using A = Ahead<T, S, U, 1>;
     extern __shared__ uint4 ahead[];                         // [depth][U][E][kThreads]
     uint4* mine = ahead + threadIdx.x;
     const Rows have = rows_of<S>(rows, stride, first);
@@ -294,13 +315,13 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
 // part[slot][d]: the weight and bias gradients of one weight row over some rows, slot i of weight row
 // i mod groups.  Row groups of a block that share a weight row are added up first where every one of
 // its weight rows has equally many (kRows a multiple of groups).
-template <typename T, typename S, int U>
-__global__ void __launch_bounds__(S::kThreads,
-                                  blocks_per_sm(S::kThreads, 2 * U * row_registers<T, S>() + 3 * S::kValues + 44))
+template <typename T, typename S>
+__global__ void __launch_bounds__(S::kThreads, BackwardPlan<T, S>::by_registers)
 layer_norm_backward_kernel(const T* x, const T* dy, const float* weight, const float* mean, const float* rstd, int64_t rows,
                            int groups, int d, T* dx, float2* part, int64_t stride) {
+    constexpr int U = BackwardPlan<T, S>::U;
+    using A = typename BackwardPlan<T, S>::A;
     __shared__ float scratch[S::L > 32 ? 2 * U * S::L / 32 : 1];
-    using A = Ahead<T, S, U, 2>;
     extern __shared__ uint4 ahead[];                        // [depth][U][x, dy][E][kThreads]
     float2* sums = reinterpret_cast<float2*>(ahead);        // afterwards [kRows][d], L <= 32
     uint4* mine = ahead + threadIdx.x;
@@ -472,43 +493,48 @@ struct Sum {
         c += (s - (t - b)) + (x - b);
         s = t;
     }
+    __device__ __forceinline__ void join(float s2, float c2) {
+        add(s2);
+        c += c2;
+    }
     __device__ __forceinline__ float value() const {
         const float t = s + c;
         return isfinite(s) ? t : s;     // infinities leave no error term
     }
 };
 
-// Column sums of part[M][n]: 32 columns a block, 32 threads a column.
+// Column sums of part[M][n]: 8 columns a block, 32 threads a column (few columns per block, so that a few
+// hundred columns still spread over the SMs: 32 a block took 9 us for 512 columns).
 __global__ void __launch_bounds__(kJoinCols * kJoinRows) layer_norm_join_kernel(const float2* part, int64_t M, int64_t n,
                                                                                 float* dweight, float* dbias) {
-    __shared__ float4 sums[kJoinRows][kJoinCols];
-    const int col = threadIdx.x % kJoinCols, r = threadIdx.x / kJoinCols;
+    constexpr int kWarps = kJoinCols * kJoinRows / 32;
+    __shared__ float4 sums[kWarps][kJoinCols];
+    const int col = threadIdx.x % kJoinCols, r = threadIdx.x / kJoinCols, warp = threadIdx.x >> 5;
     const int64_t j = (int64_t)blockIdx.x * kJoinCols + col;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     Sum dw, db;
     if (j < n)
-#pragma unroll 8
+#pragma unroll 4
         for (int64_t m = r; m < M; m += kJoinRows) {
             const float2 v = part[m * n + j];
             dw.add(v.x);
             db.add(v.y);
         }
-    for (int o = kJoinRows / 2; o > 0; o >>= 1) {
-        if (r < 2 * o) sums[r][col] = make_float4(dw.s, dw.c, db.s, db.c);
-        __syncthreads();
-        if (r < o) {
-            const float4 q = sums[r + o][col];
-            dw.add(q.x);
-            dw.c += q.y;
-            db.add(q.z);
-            db.c += q.w;
-        }
-        __syncthreads();
+#pragma unroll
+    for (int o = 16; o >= kJoinCols; o >>= 1) {
+        dw.join(__shfl_down_sync(0xffffffffu, dw.s, o), __shfl_down_sync(0xffffffffu, dw.c, o));
+        db.join(__shfl_down_sync(0xffffffffu, db.s, o), __shfl_down_sync(0xffffffffu, db.c, o));
     }
-    if (r == 0 && j < n) {
-        if (dweight) dweight[j] = dw.value();
-        if (dbias) dbias[j] = db.value();
+    if ((threadIdx.x & 31) < kJoinCols) sums[warp][col] = make_float4(dw.s, dw.c, db.s, db.c);
+    __syncthreads();
+    if (threadIdx.x >= kJoinCols || j >= n) return;
+    for (int w = 1; w < kWarps; ++w) {
+        const float4 q = sums[w][col];
+        dw.join(q.x, q.y);
+        db.join(q.z, q.w);
     }
+    if (dweight) dweight[j] = dw.value();
+    if (dbias) dbias[j] = db.value();
 }
 
 struct Args {
@@ -525,36 +551,35 @@ struct Args {
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
-// Blocks of the backward: as many as there are rows for, at most kMaxBlocks (half as many of 512
-// threads), rounded up so that a block's row groups meet the same weight rows on every turn.
-template <typename S>
-int64_t backward_blocks(int64_t rows, int groups) {
+// As many blocks as there are rows for, at most those that run at once, rounded up so that a block's
+// row groups meet the same weight rows on every turn.
+template <typename Plan, typename S>
+int64_t blocks_for(int64_t rows, int groups) {
     const int64_t unit = groups / gcd(groups, S::kRows);
-    int64_t blocks = min64(ceil_div(rows, S::kRows), S::kThreads > 256 ? kMaxBlocks / 2 : kMaxBlocks);
+    const int64_t blocks = min64(ceil_div(rows, S::kRows), (int64_t)kSms * Plan::per_sm);
     return ceil_div(blocks > 0 ? blocks : 1, unit) * unit;
 }
 // Rows of the matrix of partial sums.
-template <typename S>
-int64_t backward_slots(int64_t rows, int groups) {
+template <typename Plan, typename S>
+int64_t slots(int64_t rows, int groups) {
     const int64_t per_block = S::kRows > 1 && S::kRows % groups == 0 ? groups : S::kRows;
-    return rows > 0 ? backward_blocks<S>(rows, groups) * per_block / groups : 0;
+    return rows > 0 ? blocks_for<Plan, S>(rows, groups) * per_block / groups : 0;
+}
+
+template <typename K>
+cudaError_t allow_shared(K kernel, size_t bytes) {
+    if (bytes <= 48 * 1024) return cudaSuccess;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
 struct Forward {
     template <typename T, typename S>
     static int64_t run(const Args& a) {
-        constexpr int U = S::E == 1 ? 2 : 1;
-        // as many blocks as fill the SMs several times, more only where the grid limit asks for it
-        const int64_t most = 152 * 8 * 256 / S::kThreads, unit = a.groups / gcd(a.groups, S::kRows);
-        const int64_t turns = ceil_div(a.rows, most * S::kRows * U);
-        int64_t blocks = ceil_div(a.rows, turns * S::kRows * U);
-        blocks = ceil_div(blocks, unit) * unit;
-        constexpr size_t smem = Ahead<T, S, U, 1>::bytes;
-        if (smem > 48 * 1024) {
-            const cudaError_t e = cudaFuncSetAttribute(layer_norm_kernel<T, S, U>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            if (e != cudaSuccess) return (int64_t)e;
-        }
-        layer_norm_kernel<T, S, U><<<(unsigned)blocks, S::kThreads, smem, a.stream>>>(
+        using Plan = ForwardPlan<T, S>;
+        const int64_t blocks = blocks_for<Plan, S>(a.rows, a.groups);
+        const cudaError_t e = allow_shared(layer_norm_kernel<T, S>, Plan::A::bytes);
+        if (e != cudaSuccess) return (int64_t)e;
+        layer_norm_kernel<T, S><<<(unsigned)blocks, S::kThreads, Plan::A::bytes, a.stream>>>(
             static_cast<const T*>(a.x), a.weight, a.bias, a.rows, a.groups, a.d, a.eps, static_cast<T*>(a.out), a.mean,
             a.rstd, blocks * S::kRows);
         return (int64_t)cudaGetLastError();
@@ -563,16 +588,14 @@ struct Forward {
 struct Backward {
     template <typename T, typename S>
     static int64_t run(const Args& a) {
-        constexpr int U = S::kValues <= 8 ? 2 : 1;
-        const int64_t blocks = backward_blocks<S>(a.rows, a.groups);
+        using Plan = BackwardPlan<T, S>;
+        const int64_t blocks = blocks_for<Plan, S>(a.rows, a.groups);
         const bool reduce = a.part && S::kRows > 1 && S::kRows % a.groups == 0;
         const size_t join = reduce ? sizeof(float2) * S::kRows * (size_t)a.d : 0;
-        const size_t smem = join > Ahead<T, S, U, 2>::bytes ? join : Ahead<T, S, U, 2>::bytes;
-        if (smem > 48 * 1024) {
-            const cudaError_t e = cudaFuncSetAttribute(layer_norm_backward_kernel<T, S, U>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            if (e != cudaSuccess) return (int64_t)e;
-        }
-        layer_norm_backward_kernel<T, S, U><<<(unsigned)blocks, S::kThreads, smem, a.stream>>>(
+        const size_t smem = join > Plan::A::bytes ? join : Plan::A::bytes;
+        const cudaError_t e = allow_shared(layer_norm_backward_kernel<T, S>, smem);
+        if (e != cudaSuccess) return (int64_t)e;
+        layer_norm_backward_kernel<T, S><<<(unsigned)blocks, S::kThreads, smem, a.stream>>>(
             static_cast<const T*>(a.x), static_cast<const T*>(a.dy), a.weight, a.mean_in, a.rstd_in, a.rows, a.groups,
             a.d, static_cast<T*>(a.out), a.part, blocks * S::kRows);
         return (int64_t)cudaGetLastError();
@@ -580,7 +603,7 @@ struct Backward {
 };
 struct Slots {
     template <typename T, typename S>
-    static int64_t run(const Args& a) { return backward_slots<S>(a.rows, a.groups); }
+    static int64_t run(const Args& a) { return slots<BackwardPlan<T, S>, S>(a.rows, a.groups); }
 };
 
 // The lanes and vectors of a row: the fewest lanes that hold it in one vector each up to a warp, two
