@@ -435,34 +435,45 @@ def la_orthogonal_features(gauss_blocks: torch.Tensor, gauss_lengths: torch.Tens
 
 
 # --------------------------------------------------------------------------- operators around the attention call
+#
+# These calls are short enough that their checks count: an operand is tested as a whole and looked
+# at in detail only when something is wrong with it.
 
-def _operands(*named):
-    """Checks (tensor, name, dtype or None, shape or None) operands: CUDA tensors on one device,
-    contiguous, of the given dtype (None: float32 or bfloat16) and shape; None tensors are
-    skipped.  Returns the device."""
-    dev = None
-    for t, name, dtype, shape in named:
-        if t is None:
-            continue
+def _first(t, name) -> int:
+    """The device index of a call's first operand, a CUDA tensor of float32 or bfloat16."""
+    _need(t, name)
+    if t.dtype not in DTYPE_IDS:
+        raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    return t.get_device()
+
+
+def _addr(t, name, dtype, shape, index) -> int:
+    """Address of an operand: contiguous, on CUDA device `index`, of the given dtype (None: float32 or
+    bfloat16) and shape (None: any)."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == index and t.is_contiguous()
+            and (t.dtype is dtype if dtype is not None else t.dtype in DTYPE_IDS)
+            and (shape is None or t.shape == shape)):
         _need(t, name, dtype)
         if dtype is None and t.dtype not in DTYPE_IDS:
             raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
         if shape is not None and t.shape != shape:
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, other operands on {dev}")
-    return dev
+        raise ValueError(f"{name} is on {t.device}, other operands on cuda:{index}")
+    return t.data_ptr()
+
+
+def _addr_or_none(t, name, dtype, shape, index):
+    return None if t is None else _addr(t, name, dtype, shape, index)
 
 
 class _On:
-    """Makes an operand's device current for a call and, where a stream is given, lets
-    what the call allocates belong to that stream."""
+    """Makes an operand's device current for a call and, where a stream is given, that stream: what the
+    call allocates belongs to it."""
 
-    def __init__(self, dev, stream):
+    def __init__(self, index, stream):
+        dev = torch.device("cuda", index)
         self.guards = []
-        if dev.index != torch.cuda.current_device():
+        if index != torch.cuda.current_device():
             self.guards.append(torch.cuda.device(dev))
         if stream is not None:
             if not isinstance(stream, torch.cuda.Stream):
@@ -475,15 +486,34 @@ class _On:
     def __enter__(self):
         for g in self.guards:
             g.__enter__()
-        return torch.cuda.current_stream().cuda_stream
 
     def __exit__(self, *exc):
         for g in reversed(self.guards):
             g.__exit__(*exc)
 
 
-def _sequences(T: int, cu_seqlens, nseq) -> int:
+_current_stream = torch._C._cuda_getCurrentRawStream   # of a device index, as a handle
+
+
+def _elsewhere(index, stream) -> bool:
+    """Whether a call has to change the current device or stream first (it then calls itself under _On)."""
+    return stream is not None or index != torch._C._cuda_getDevice()
+
+
+def _workspace(workspace, nbytes, index):
+    """(workspace, its address, its bytes); allocates one of `nbytes` where none is given."""
+    if workspace is None:
+        # a size of 0 means the call will be rejected: let the library say why
+        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", index))
+        return workspace, workspace.data_ptr(), workspace.numel()
+    _addr(workspace, "workspace", workspace.dtype, None, index)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _sequences(cu_seqlens, nseq) -> int:
     if cu_seqlens is not None:
+        if not isinstance(cu_seqlens, torch.Tensor):
+            raise TypeError("cu_seqlens must be a torch.Tensor")
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
             raise ValueError("cu_seqlens must be a vector of at least two entries")
         if nseq is not None and nseq != cu_seqlens.numel() - 1:
@@ -512,24 +542,25 @@ def la_gated_scan(a, b, cu_seqlens=None, nseq=None, state_in=None, state_out=Non
     given and (h, state_out) is returned."""
     lib = load_library()
     T, H, d = shape = _rows3(b, "b")
-    nseq = _sequences(T, cu_seqlens, nseq)
-    states = torch.Size((nseq, H, d))
-    dev = _operands((b, "b", None, None), (a, "a", None, shape), (cu_seqlens, "cu_seqlens", torch.int32, None),
-                    (state_in, "state_in", torch.float32, states), (state_out, "state_out", torch.float32, states),
-                    (h, "h", b.dtype, shape), (workspace, "workspace", None if workspace is None else workspace.dtype,
-                                               None))
-    with _On(dev, stream) as s:
-        if h is None:
-            h = torch.empty_like(b)
-        if return_state and state_out is None:
-            state_out = torch.empty(states, dtype=torch.float32, device=dev)
-        if workspace is None:
-            workspace = torch.empty(max(256, lib.la_gated_scan_workspace_bytes(cu_seqlens is not None, nseq, T, H, d)),
-                                    dtype=torch.uint8, device=dev)
-        _check("la_gated_scan", lib.la_gated_scan(
-            a.data_ptr(), b.data_ptr(), DTYPE_IDS[a.dtype], DTYPE_IDS[b.dtype], _ptr(cu_seqlens), nseq, T, H, d,
-            _ptr(state_in), _ptr(state_out), h.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), s))
+    nseq = _sequences(cu_seqlens, nseq)
+    states, f32, dev = (nseq, H, d), torch.float32, _first(b, "b")
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return la_gated_scan(a, b, cu_seqlens, nseq, state_in, state_out, return_state, h, workspace)
+    pa = _addr(a, "a", None, shape, dev)
+    pc = _addr_or_none(cu_seqlens, "cu_seqlens", torch.int32, None, dev)
+    pi = _addr_or_none(state_in, "state_in", f32, states, dev)
+    if h is None:
+        h = torch.empty_like(b)
+    if return_state and state_out is None:
+        state_out = torch.empty(states, dtype=f32, device=b.device)
+    workspace, pw, nw = _workspace(
+        workspace, 0 if workspace is not None else
+        lib.la_gated_scan_workspace_bytes(cu_seqlens is not None, nseq, T, H, d), dev)
+    _check("la_gated_scan", lib.la_gated_scan(
+        pa, b.data_ptr(), DTYPE_IDS[a.dtype], DTYPE_IDS[b.dtype], pc, nseq, T, H, d, pi,
+        _addr_or_none(state_out, "state_out", f32, states, dev), _addr(h, "h", b.dtype, shape, dev), pw, nw,
+        _current_stream(dev)))
     return (h, state_out) if return_state else h
 
 
@@ -539,27 +570,29 @@ def la_gated_scan_backward(a, h, dh, cu_seqlens=None, nseq=None, state_in=None, 
     output h is read; with return_dstate=True (da, db, dstate_in)."""
     lib = load_library()
     T, H, d = shape = _rows3(h, "h")
-    nseq = _sequences(T, cu_seqlens, nseq)
-    states = torch.Size((nseq, H, d))
-    dev = _operands((h, "h", None, None), (a, "a", None, shape), (dh, "dh", h.dtype, shape),
-                    (cu_seqlens, "cu_seqlens", torch.int32, None), (state_in, "state_in", torch.float32, states),
-                    (dstate_out, "dstate_out", torch.float32, states), (dstate_in, "dstate_in", torch.float32, states),
-                    (da, "da", a.dtype, shape), (db, "db", h.dtype, shape),
-                    (workspace, "workspace", None if workspace is None else workspace.dtype, None))
-    with _On(dev, stream) as s:
-        if da is None:
-            da = torch.empty_like(a)
-        if db is None:
-            db = torch.empty_like(h)
-        if return_dstate and dstate_in is None:
-            dstate_in = torch.empty(states, dtype=torch.float32, device=dev)
-        if workspace is None:
-            workspace = torch.empty(max(256, lib.la_gated_scan_workspace_bytes(cu_seqlens is not None, nseq, T, H, d)),
-                                    dtype=torch.uint8, device=dev)
-        _check("la_gated_scan_backward", lib.la_gated_scan_backward(
-            a.data_ptr(), h.data_ptr(), dh.data_ptr(), DTYPE_IDS[a.dtype], DTYPE_IDS[h.dtype], _ptr(cu_seqlens), nseq,
-            T, H, d, _ptr(state_in), _ptr(dstate_out), da.data_ptr(), db.data_ptr(), _ptr(dstate_in),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), s))
+    nseq = _sequences(cu_seqlens, nseq)
+    states, f32, dev = (nseq, H, d), torch.float32, _first(h, "h")
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return la_gated_scan_backward(a, h, dh, cu_seqlens, nseq, state_in, dstate_out, return_dstate, da, db,
+                                          dstate_in, workspace)
+    pa, pd = _addr(a, "a", None, shape, dev), _addr(dh, "dh", h.dtype, shape, dev)
+    pc = _addr_or_none(cu_seqlens, "cu_seqlens", torch.int32, None, dev)
+    pi = _addr_or_none(state_in, "state_in", f32, states, dev)
+    po = _addr_or_none(dstate_out, "dstate_out", f32, states, dev)
+    if da is None:
+        da = torch.empty_like(a)
+    if db is None:
+        db = torch.empty_like(h)
+    if return_dstate and dstate_in is None:
+        dstate_in = torch.empty(states, dtype=f32, device=h.device)
+    workspace, pw, nw = _workspace(
+        workspace, 0 if workspace is not None else
+        lib.la_gated_scan_workspace_bytes(cu_seqlens is not None, nseq, T, H, d), dev)
+    _check("la_gated_scan_backward", lib.la_gated_scan_backward(
+        pa, h.data_ptr(), pd, DTYPE_IDS[a.dtype], DTYPE_IDS[h.dtype], pc, nseq, T, H, d, pi, po,
+        _addr(da, "da", a.dtype, shape, dev), _addr(db, "db", h.dtype, shape, dev),
+        _addr_or_none(dstate_in, "dstate_in", f32, states, dev), pw, nw, _current_stream(dev)))
     return (da, db, dstate_in) if return_dstate else (da, db)
 
 
@@ -568,14 +601,16 @@ def la_gated_step(a, b, state, state_out=None, h=None, stream=None):
     [B, H, d] is updated in place, or written to state_out when given; returns h [B, H, d]."""
     lib = load_library()
     B, H, d = shape = _rows3(b, "b")
-    dev = _operands((b, "b", None, None), (a, "a", None, shape), (state, "state", torch.float32, shape),
-                    (state_out, "state_out", torch.float32, shape), (h, "h", b.dtype, shape))
-    with _On(dev, stream) as s:
-        if h is None:
-            h = torch.empty_like(b)
-        _check("la_gated_step", lib.la_gated_step(
-            a.data_ptr(), b.data_ptr(), DTYPE_IDS[a.dtype], DTYPE_IDS[b.dtype], B, H, d, state.data_ptr(),
-            (state if state_out is None else state_out).data_ptr(), h.data_ptr(), s))
+    f32, dev = torch.float32, _first(b, "b")
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return la_gated_step(a, b, state, state_out, h)
+    pa, ps = _addr(a, "a", None, shape, dev), _addr(state, "state", f32, shape, dev)
+    po = ps if state_out is None else _addr(state_out, "state_out", f32, shape, dev)
+    if h is None:
+        h = torch.empty_like(b)
+    _check("la_gated_step", lib.la_gated_step(pa, b.data_ptr(), DTYPE_IDS[a.dtype], DTYPE_IDS[b.dtype], B, H, d, ps, po,
+                                              _addr(h, "h", b.dtype, shape, dev), _current_stream(dev)))
     return h
 
 
@@ -584,15 +619,18 @@ def _norm_shape(x, weight, bias):
     second dimension from the right, each index with its own)."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
-    if x.dim() < 1 or x.shape[-1] < 1:
-        raise ValueError(f"x must be [..., d], got shape {tuple(x.shape)}")
-    d, groups = x.shape[-1], 1
+    shape = x.shape
+    if len(shape) < 1 or shape[-1] < 1:
+        raise ValueError(f"x must be [..., d], got shape {tuple(shape)}")
+    d, groups = shape[-1], 1
     for t, name in ((weight, "weight"), (bias, "bias")):
         if t is None:
             continue
-        if t.dim() == 2 and x.dim() >= 2 and tuple(t.shape) == (x.shape[-2], d):
-            groups = x.shape[-2]
-        elif tuple(t.shape) != (d,):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if len(t.shape) == 2 and len(shape) >= 2 and t.shape == shape[-2:]:
+            groups = shape[-2]
+        elif t.shape != shape[-1:]:
             raise ValueError(f"{name} must have shape {(d,)} or x's last two dimensions, got {tuple(t.shape)}")
     if weight is not None and bias is not None and weight.shape != bias.shape:
         raise ValueError("weight and bias must have the same shape")
@@ -606,18 +644,21 @@ def la_layer_norm(x, weight=None, bias=None, eps=1e-5, return_stats=False, y=Non
     dimension, as la_layer_norm_backward reads them."""
     lib = load_library()
     rows, groups, d = _norm_shape(x, weight, bias)
-    stats = x.shape[:-1]
-    dev = _operands((x, "x", None, None), (weight, "weight", torch.float32, None), (bias, "bias", torch.float32, None),
-                    (y, "y", x.dtype, x.shape), (mean, "mean", torch.float32, stats),
-                    (rstd, "rstd", torch.float32, stats))
-    with _On(dev, stream) as s:
-        if y is None:
-            y = torch.empty_like(x)
-        if return_stats:
-            mean = torch.empty(stats, dtype=torch.float32, device=dev) if mean is None else mean
-            rstd = torch.empty(stats, dtype=torch.float32, device=dev) if rstd is None else rstd
-        _check("la_layer_norm", lib.la_layer_norm(x.data_ptr(), _ptr(weight), _ptr(bias), DTYPE_IDS[x.dtype], rows,
-                                                  groups, d, eps, y.data_ptr(), _ptr(mean), _ptr(rstd), s))
+    f32, dev, shape = torch.float32, _first(x, "x"), x.shape
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return la_layer_norm(x, weight, bias, eps, return_stats, y, mean, rstd)
+    stats = shape[:-1]
+    pw, pb = _addr_or_none(weight, "weight", f32, None, dev), _addr_or_none(bias, "bias", f32, None, dev)
+    if y is None:
+        y = torch.empty_like(x)
+    if return_stats:
+        mean = torch.empty(stats, dtype=f32, device=x.device) if mean is None else mean
+        rstd = torch.empty(stats, dtype=f32, device=x.device) if rstd is None else rstd
+    _check("la_layer_norm", lib.la_layer_norm(
+        x.data_ptr(), pw, pb, DTYPE_IDS[x.dtype], rows, groups, d, eps, _addr(y, "y", x.dtype, shape, dev),
+        _addr_or_none(mean, "mean", f32, stats, dev), _addr_or_none(rstd, "rstd", f32, stats, dev),
+        _current_stream(dev)))
     return (y, mean, rstd) if return_stats else y
 
 
@@ -633,24 +674,24 @@ def la_layer_norm_backward(x, dy, mean, rstd, weight, dx=None, dweight=None, dbi
     if not isinstance(weight, torch.Tensor):
         raise TypeError("weight must be a torch.Tensor")
     rows, groups, d = _norm_shape(x, weight, None)
-    stats = x.shape[:-1]
-    dev = _operands((x, "x", None, None), (dy, "dy", x.dtype, x.shape), (mean, "mean", torch.float32, stats),
-                    (rstd, "rstd", torch.float32, stats), (weight, "weight", torch.float32, None),
-                    (dx, "dx", x.dtype, x.shape), (dweight, "dweight", torch.float32, weight.shape),
-                    (dbias, "dbias", torch.float32, weight.shape),
-                    (workspace, "workspace", None if workspace is None else workspace.dtype, None))
-    with _On(dev, stream) as s:
-        dx = torch.empty_like(x) if dx is None else dx
-        dweight = torch.empty_like(weight) if dweight is None else dweight
-        dbias = torch.empty_like(weight) if dbias is None else dbias
-        if workspace is None:
-            workspace = torch.empty(
-                max(256, lib.la_layer_norm_backward_workspace_bytes(DTYPE_IDS[x.dtype], rows, groups, d)),
-                dtype=torch.uint8, device=dev)
-        _check("la_layer_norm_backward", lib.la_layer_norm_backward(
-            x.data_ptr(), dy.data_ptr(), weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(), DTYPE_IDS[x.dtype], rows,
-            groups, d, dx.data_ptr(), dweight.data_ptr(), dbias.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), s))
+    f32, dev, shape, wshape = torch.float32, _first(x, "x"), x.shape, weight.shape
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return la_layer_norm_backward(x, dy, mean, rstd, weight, dx, dweight, dbias, workspace)
+    stats = shape[:-1]
+    pd = _addr(dy, "dy", x.dtype, shape, dev)
+    pm, pr = _addr(mean, "mean", f32, stats, dev), _addr(rstd, "rstd", f32, stats, dev)
+    pw = _addr(weight, "weight", f32, None, dev)
+    dx = torch.empty_like(x) if dx is None else dx
+    dweight = torch.empty_like(weight) if dweight is None else dweight
+    dbias = torch.empty_like(weight) if dbias is None else dbias
+    workspace, pws, nws = _workspace(
+        workspace, 0 if workspace is not None else
+        lib.la_layer_norm_backward_workspace_bytes(DTYPE_IDS[x.dtype], rows, groups, d), dev)
+    _check("la_layer_norm_backward", lib.la_layer_norm_backward(
+        x.data_ptr(), pd, pw, pm, pr, DTYPE_IDS[x.dtype], rows, groups, d, _addr(dx, "dx", x.dtype, shape, dev),
+        _addr(dweight, "dweight", f32, wshape, dev), _addr(dbias, "dbias", f32, wshape, dev), pws, nws,
+        _current_stream(dev)))
     return dx, dweight, dbias
 
 
@@ -662,22 +703,23 @@ def la_rotary(q, k, freq, positions, pairs, interleaved=False, inverse=False, q_
     q_out alone when k is None."""
     lib = load_library()
     T, H, d = shape = _rows3(q, "q")
-    pairs = [int(n) for n in pairs]
+    dev, n = _first(q, "q"), len(pairs)
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return la_rotary(q, k, freq, positions, pairs, interleaved, inverse, q_out, k_out)
+    pk = _addr_or_none(k, "k", q.dtype, shape, dev)
+    pf = _addr(freq, "freq", torch.float32, (sum(pairs),), dev)
     if not isinstance(positions, torch.Tensor):
         raise TypeError("positions must be a torch.Tensor")
-    dev = _operands((q, "q", None, None), (k, "k", q.dtype, shape), (freq, "freq", torch.float32, (sum(pairs),)),
-                    (positions, "positions", torch.int32,
-                     (T,) if len(pairs) == 1 and positions.dim() == 1 else (T, len(pairs))),
-                    (q_out, "q_out", q.dtype, shape), (k_out, "k_out", q.dtype, shape))
+    pp = _addr(positions, "positions", torch.int32, (T,) if n == 1 and positions.dim() == 1 else (T, n), dev)
     if k is None and k_out is not None:
         raise ValueError("k_out is given without k")
-    with _On(dev, stream) as s:
-        if q_out is None:
-            q_out = torch.empty_like(q)
-        if k is not None and k_out is None:
-            k_out = torch.empty_like(k)
-        _check("la_rotary", lib.la_rotary(
-            q.data_ptr(), _ptr(k), freq.data_ptr(), positions.data_ptr(), DTYPE_IDS[q.dtype], T, H, d,
-            (_c_int * len(pairs))(*pairs), len(pairs), int(interleaved), int(inverse), q_out.data_ptr(), _ptr(k_out),
-            s))
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    if k is not None and k_out is None:
+        k_out = torch.empty_like(k)
+    _check("la_rotary", lib.la_rotary(
+        q.data_ptr(), pk, pf, pp, DTYPE_IDS[q.dtype], T, H, d, (_c_int * n)(*pairs), n, bool(interleaved),
+        bool(inverse), _addr(q_out, "q_out", q.dtype, shape, dev),
+        _addr_or_none(k_out, "k_out", q.dtype, shape, dev), _current_stream(dev)))
     return q_out if k is None else (q_out, k_out)

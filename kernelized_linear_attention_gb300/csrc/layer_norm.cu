@@ -7,7 +7,10 @@
 // squares.  Rows of up to 64 vectors share a warp, longer ones take a block.  A
 // group works on U rows at once so that their sums overlap, and each lane copies
 // its vectors of the next turns to shared memory ahead (asynchronous copies that
-// it alone waits for): what is in flight does not cost registers.
+// it alone waits for): what is in flight does not cost registers.  Where a row
+// takes a block, its warps meet at one barrier a turn: in the forward they
+// exchange their own sums and squared deviations from their own means, which
+// join exactly, in the backward their two sums.
 //
 // A group of lanes keeps one weight row: it walks over rows a multiple of
 // `groups` apart.  Its weights are read once, and in the backward its columns'
@@ -22,7 +25,7 @@ namespace la {
 namespace {
 
 constexpr int kSms = 152;
-constexpr int kCopyBytes = 40 * 1024;   // of rows copied ahead, per block
+constexpr int kCopyBytes = 64 * 1024;   // of rows copied ahead, per SM
 constexpr int kJoinCols = 8, kJoinRows = 32;
 
 template <int L_, int E_, int N_>
@@ -42,33 +45,36 @@ constexpr int blocks_per_sm(int threads, int registers) {
 template <typename T, typename S>
 constexpr int row_registers() { return S::kValues * (int)sizeof(T) / 4 > 0 ? S::kValues * (int)sizeof(T) / 4 : 1; }
 
-// How far ahead rows are copied: `depth` turns of U rows (of x, or of x and dy) in kCopyBytes a block,
-// two turns where they are longer, one where two do not fit.
-// Rows of single elements are loaded when they are needed (a copy has at least four bytes).
-template <typename T, typename S, int U, int Arrays>
+// How far ahead rows are copied: `depth` turns of U rows (of x, or of x and dy) in a block's share of
+// kCopyBytes, two turns where they are longer, one where two do not fit.  (96 KB per SM and more are no faster:
+// 51 us instead of 48 for 1048576 rows of 64.)  Rows of single elements are loaded when they are needed
+// (a copy has at least four bytes).
+template <typename T, typename S, int U, int Arrays, int Blocks>
 struct Ahead {
     static constexpr bool on = S::N > 1;
     static constexpr int turn_bytes = U * Arrays * S::E * S::kThreads * 16;
-    static constexpr int most = kCopyBytes / turn_bytes;
-    static constexpr int depth = most > 6 ? 6 : most >= 2 ? most : 2 * turn_bytes <= 200 * 1024 ? 2 : 1;
+    static constexpr int most = kCopyBytes / Blocks / turn_bytes;
+    static constexpr int depth = most > 8 ? 8 : most >= 2 ? most : 2 * turn_bytes <= 200 * 1024 ? 2 : 1;
     static constexpr size_t bytes = on ? (size_t)depth * turn_bytes : 0;
 };
 // The registers to compile for, and the blocks of an SM that this and the copies' memory allow.
 template <typename T, typename S>
 struct ForwardPlan {
     static constexpr int U = S::E == 1 ? 2 : 1;
-    using A = Ahead<T, S, U, 1>;
-    static constexpr int registers = U * row_registers<T, S>() + (S::kValues <= 8 ? 2 * S::kValues : 0) + 38;
+    static constexpr int registers = U * row_registers<T, S>() + (S::kValues <= 8 ? 2 * S::kValues + 38 : 52);
     static constexpr int by_registers = blocks_per_sm(S::kThreads, registers);
+    using A = Ahead<T, S, U, 1, by_registers>;
     static constexpr int by_memory = 227 * 1024 / ((int)A::bytes + 2048);
     static constexpr int per_sm = by_registers < by_memory ? by_registers : by_memory;
 };
 template <typename T, typename S>
 struct BackwardPlan {
-    static constexpr int U = S::kValues <= 8 ? 2 : 1;
-    using A = Ahead<T, S, U, 2>;
-    static constexpr int registers = 2 * U * row_registers<T, S>() + 3 * S::kValues + 44;
+    static constexpr bool held = S::kValues <= 8;           // xh and w dy of U rows stay in registers
+    static constexpr int U = held ? 2 : 1;
+    static constexpr int registers = held ? (2 * U + 3) * S::kValues + 40
+                                          : 2 * row_registers<T, S>() + 3 * S::kValues + 44;
     static constexpr int by_registers = blocks_per_sm(S::kThreads, registers);
+    using A = Ahead<T, S, U, 2, by_registers>;
     static constexpr int by_memory = 227 * 1024 / ((int)A::bytes + 2048);
     static constexpr int per_sm = by_registers < by_memory ? by_registers : by_memory;
 };
@@ -80,28 +86,41 @@ __device__ __forceinline__ void copies_done() { asm volatile("cp.async.commit_gr
 template <int N>
 __device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Sum over the L lanes of a row group, for each of U rows; every lane gets it.
+template <int Width>
+__device__ __forceinline__ float lane_sum(float x) {
+#pragma unroll
+    for (int o = Width / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+// Sum over the L lanes of a row group, for each of U rows; every lane gets it.  Where that is a block,
+// `scratch` holds two turns and `turn` chooses: one barrier keeps a turn's writers off the readers of
+// the turn before last.
 template <typename S, int U>
-__device__ __forceinline__ void row_sums(float (&x)[U], float* scratch) {
+__device__ __forceinline__ void row_sums(float (&x)[U], float* scratch, int turn) {
 #pragma unroll
-    for (int o = (S::L < 32 ? S::L : 32) / 2; o > 0; o >>= 1)
-#pragma unroll
-        for (int u = 0; u < U; ++u) x[u] += __shfl_xor_sync(0xffffffffu, x[u], o);
+    for (int u = 0; u < U; ++u) x[u] = lane_sum<S::L < 32 ? S::L : 32>(x[u]);
     if constexpr (S::L > 32) {
         constexpr int kWarps = S::L / 32;
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        __syncthreads();                                    // the scratch of the sums before is read
+        float* half = scratch + (turn & 1) * U * kWarps;
         if (lane == 0)
 #pragma unroll
-            for (int u = 0; u < U; ++u) scratch[u * kWarps + warp] = x[u];
+            for (int u = 0; u < U; ++u) half[u * kWarps + warp] = x[u];
         __syncthreads();
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            x[u] = lane < kWarps ? scratch[u * kWarps + lane] : 0.f;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) x[u] += __shfl_xor_sync(0xffffffffu, x[u], o);
-        }
+        for (int u = 0; u < U; ++u) x[u] = lane_sum<32>(lane < kWarps ? half[u * kWarps + lane] : 0.f);
     }
+}
+// Of the d columns of a row, those that warp w of a block holds.
+template <typename S>
+__device__ __forceinline__ int warp_columns(int w, int d) {
+    int n = 0;
+#pragma unroll
+    for (int e = 0; e < S::E; ++e) {
+        const int rest = d - (e * S::L + w * 32) * S::N;
+        n += rest < 0 ? 0 : rest > 32 * S::N ? 32 * S::N : rest;
+    }
+    return n;
 }
 
 // The lane's E vectors of a row, which `row` points into at the lane's first column; vector e lies e L N
@@ -195,7 +214,10 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
                   float* mean, float* rstd, int64_t stride) {
     constexpr int U = ForwardPlan<T, S>::U;
     using A = typename ForwardPlan<T, S>::A;
-    __shared__ float scratch[S::L > 32 ? U * S::L / 32 : 1];
+    constexpr bool kBlock = S::L > 32;                       // a row takes the block
+    constexpr int kWarps = S::L / 32;
+    __shared__ float2 scratch[kBlock ? 2 * U * kWarps : 1];
+    extern __shared__ uint4 ahead[];                         // [depth][U][E][kThreads]
     const int lane = threadIdx.x % S::L, col = lane * S::N, left = d - col;
     const int64_t first = (int64_t)blockIdx.x * S::kRows + threadIdx.x / S::L, step = stride * d;
     const float fd = (float)d, over_d = 1.f / fd;
@@ -208,19 +230,19 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
         load_row_params<S>(w, row_of(weight, at), left, 1.f);
         load_row_params<S>(b, row_of(bias, at), left, 0.f);
     }
-    extern __shared__ uint4 ahead[];                         // [depth][U][E][kThreads]
     uint4* mine = ahead + threadIdx.x;
     const Rows have = rows_of<S>(rows, stride, first);
-    const T* lane_x = x + first * d + col;
+    const T* next_x = x + first * d + col;                   // of the turn to copy, or to load
+    T* next_y = y + first * d + col;
+    int64_t row = first;
     auto copy_turn = [&](int turn) {
         if (A::on) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = turn * U + u;
-                if (i < have.mine)
-                    copy_row<S, T>(mine + ((turn % A::depth) * U + u) * S::E * S::kThreads, lane_x + i * step, left);
-            }
+            for (int u = 0; u < U; ++u)
+                if (turn * U + u < have.mine)
+                    copy_row<S, T>(mine + ((turn % A::depth) * U + u) * S::E * S::kThreads, next_x + u * step, left);
             copies_done();
+            next_x += U * step;
         }
     };
     if (A::on)
@@ -228,17 +250,14 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
     for (int turn = 0; turn * U < have.most; ++turn) {
         copy_turn(turn + A::depth - 1);
         if (A::on) wait_copies<A::depth - 1>();
-        constexpr int V = U;
-        Vec<T, S::N> v[V][S::E];
-        float s[V], q[V];
+        Vec<T, S::N> v[U][S::E];
+        float s[U], q[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            load_row<S, T>(v[u], A::on ? mine + ((turn % A::depth) * U + u) * S::E * S::kThreads : nullptr, next_x + u * step,
+                           turn * U + u < have.mine ? left : 0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = turn * U + u;
-            load_row<S, T>(v[u], A::on ? mine + ((turn % A::depth) * U + u) * S::E * S::kThreads : nullptr, lane_x + i * step,
-                           i < have.mine ? left : 0);
-        }
-#pragma unroll
-        for (int u = 0; u < V; ++u) {
             P t = psplat<P>(0.f);
 #pragma unroll
             for (int e = 0; e < S::E; ++e) {
@@ -247,17 +266,20 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
 #pragma unroll
                 for (int k = 0; k < S::n; ++k) t = padd(t, f[k]);
             }
-            s[u] = psum(t);
+            s[u] = lane_sum<kBlock ? 32 : S::L>(psum(t));
         }
-        row_sums<S, V>(s, scratch);
 #pragma unroll
-        for (int u = 0; u < V; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int e = 0; e < S::E; ++e) keep_packed(v[u][e]);
+        // deviations from the mean, of the warp's own columns where a row takes several warps
+        float mean_here[U];
+        const float columns = kBlock ? (float)warp_columns<S>(threadIdx.x >> 5, d) : fd;
+        const float over_columns = kBlock ? 1.f / fmaxf(columns, 1.f) : over_d;
 #pragma unroll
-        for (int u = 0; u < V; ++u) {
-            s[u] = mean_of(s[u], fd, over_d);
-            const P minus = psplat<P>(-s[u]);
+        for (int u = 0; u < U; ++u) {
+            mean_here[u] = mean_of(s[u], columns, over_columns);
+            const P minus = psplat<P>(-mean_here[u]);
             P t = psplat<P>(0.f);
 #pragma unroll
             for (int e = 0; e < S::E; ++e)
@@ -270,20 +292,33 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
                         t = pfma(f[k], f[k], t);
                     }
                 }
-            q[u] = psum(t);
+            q[u] = lane_sum<kBlock ? 32 : S::L>(psum(t));
         }
-        row_sums<S, V>(q, scratch);
+        if constexpr (kBlock) {
+            // sum over the warps of q_w + n_w (mean_w - mean)^2
+            const int wl = threadIdx.x & 31;
+            float2* half = scratch + (turn & 1) * U * kWarps;
+            if (wl == 0)
 #pragma unroll
-        for (int u = 0; u < V; ++u)
+                for (int u = 0; u < U; ++u) half[u * kWarps + (threadIdx.x >> 5)] = make_float2(s[u], q[u]);
+            __syncthreads();
+            const float n = wl < kWarps ? (float)warp_columns<S>(wl, d) : 0.f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float2 o = wl < kWarps ? half[u * kWarps + wl] : make_float2(0.f, 0.f);
+                mean_here[u] = mean_of(lane_sum<32>(o.x), fd, over_d);
+                const float off = n > 0.f ? o.x / n - mean_here[u] : 0.f;
+                q[u] = lane_sum<32>(fmaf(n * off, off, o.y));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int e = 0; e < S::E; ++e) keep_packed(v[u][e]);
 #pragma unroll
-        for (int u = 0; u < V; ++u) {
-            const int i = turn * U + u;
-            if (i >= have.mine) continue;
-            const int64_t row = first + i * stride;
-            T* at_y = y + row * d + col;
-            const float mu = s[u], rs = inverse_root(fmaf(q[u], over_d, eps));
+        for (int u = 0; u < U; ++u) {
+            if (turn * U + u >= have.mine) continue;
+            const float mu = mean_here[u], rs = inverse_root(fmaf(q[u], over_d, eps));
             const P minus = psplat<P>(-mu), times = psplat<P>(rs);
 #pragma unroll
             for (int e = 0; e < S::E; ++e) {
@@ -302,13 +337,16 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
                     f[k] = pfma(pmul(padd(f[k], minus), times), kHeld ? w[e * S::n + k] : we[k], kHeld ? b[e * S::n + k] : be[k]);
                 Vec<T, S::N> o;
                 pack_pairs<S::N>(o, f);
-                *reinterpret_cast<Vec<T, S::N>*>(at_y + e * kStep) = o;
+                *reinterpret_cast<Vec<T, S::N>*>(next_y + u * step + e * kStep) = o;
             }
             if (lane == 0) {
-                if (mean) mean[row] = mu;
-                if (rstd) rstd[row] = rs;
+                if (mean) mean[row + u * stride] = mu;
+                if (rstd) rstd[row + u * stride] = rs;
             }
         }
+        if (!A::on) next_x += U * step;
+        next_y += U * step;
+        row += U * stride;
     }
 }
 
@@ -321,7 +359,7 @@ layer_norm_backward_kernel(const T* x, const T* dy, const float* weight, const f
                            int groups, int d, T* dx, float2* part, int64_t stride) {
     constexpr int U = BackwardPlan<T, S>::U;
     using A = typename BackwardPlan<T, S>::A;
-    __shared__ float scratch[S::L > 32 ? 2 * U * S::L / 32 : 1];
+    __shared__ float scratch[S::L > 32 ? 4 * U * S::L / 32 : 1];
     extern __shared__ uint4 ahead[];                        // [depth][U][x, dy][E][kThreads]
     float2* sums = reinterpret_cast<float2*>(ahead);        // afterwards [kRows][d], L <= 32
     uint4* mine = ahead + threadIdx.x;
@@ -336,53 +374,56 @@ layer_norm_backward_kernel(const T* x, const T* dy, const float* weight, const f
 #pragma unroll
     for (int k = 0; k < S::kPairs; ++k) dw[k] = db[k] = psplat<P>(0.f);
     const Rows have = rows_of<S>(rows, stride, first);
-    const int64_t lane_at = first * d + col;
     auto place = [&](int turn, int u, int array) {
         return mine + (((turn % A::depth) * U + u) * 2 + array) * S::E * S::kThreads;
     };
+    const T *next_x = x + first * d + col, *next_dy = dy + first * d + col;   // of the turn to copy, or to load
+    T* next_dx = dx + first * d + col;
+    const float *next_mean = mean + first, *next_rstd = rstd + first;
     auto copy_turn = [&](int turn) {
         if (A::on) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = turn * U + u;
-                if (i < have.mine) {
-                    copy_row<S, T>(place(turn, u, 0), x + lane_at + i * step, left);
-                    copy_row<S, T>(place(turn, u, 1), dy + lane_at + i * step, left);
+            for (int u = 0; u < U; ++u)
+                if (turn * U + u < have.mine) {
+                    copy_row<S, T>(place(turn, u, 0), next_x + u * step, left);
+                    copy_row<S, T>(place(turn, u, 1), next_dy + u * step, left);
                 }
-            }
             copies_done();
+            next_x += U * step;
+            next_dy += U * step;
         }
     };
-    float next_mu[U], next_rs[U];
+    float ahead_mu[U], ahead_rs[U];
     auto load_stats = [&](int turn) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = turn * U + u;
-            next_mu[u] = i < have.mine ? mean[first + i * stride] : 0.f;
-            next_rs[u] = i < have.mine ? rstd[first + i * stride] : 0.f;
+            ahead_mu[u] = turn * U + u < have.mine ? next_mean[u * stride] : 0.f;
+            ahead_rs[u] = turn * U + u < have.mine ? next_rstd[u * stride] : 0.f;
         }
+        next_mean += U * stride;
+        next_rstd += U * stride;
     };
     if (A::on)
         for (int t = 0; t < A::depth - 1; ++t) copy_turn(t);
     load_stats(0);
     for (int turn = 0; turn * U < have.most; ++turn) {
-        constexpr int V = U;
         copy_turn(turn + A::depth - 1);
         if (A::on) wait_copies<A::depth - 1>();
-        Vec<T, S::N> v[V][S::E], g[V][S::E];
-        float mu[V], rs[V], sums_of[2 * V];                 // of w dy, and of w dy xh
+        Vec<T, S::N> v[U][S::E], g[U][S::E];
+        P xhs[U][kHeld ? S::kPairs : 1], ts[U][kHeld ? S::kPairs : 1];   // xh and w dy, kept where there is room
+        float mu[U], rs[U], sums_of[2 * U];                 // of w dy, and of w dy xh
 #pragma unroll
-        for (int u = 0; u < V; ++u) {
-            const int i = turn * U + u;
-            load_row<S, T>(v[u], A::on ? place(turn, u, 0) : nullptr, x + lane_at + i * step, i < have.mine ? left : 0);
-            load_row<S, T>(g[u], A::on ? place(turn, u, 1) : nullptr, dy + lane_at + i * step, i < have.mine ? left : 0);
-            mu[u] = next_mu[u];
-            rs[u] = next_rs[u];
+        for (int u = 0; u < U; ++u) {
+            const int there = turn * U + u < have.mine ? left : 0;
+            load_row<S, T>(v[u], A::on ? place(turn, u, 0) : nullptr, next_x + u * step, there);
+            load_row<S, T>(g[u], A::on ? place(turn, u, 1) : nullptr, next_dy + u * step, there);
+            mu[u] = ahead_mu[u];
+            rs[u] = ahead_rs[u];
         }
         load_stats(turn + 1);
         if (!kHeld) load_row_params<S>(w, row_of(weight, at), left, 1.f);
 #pragma unroll
-        for (int u = 0; u < V; ++u) {
+        for (int u = 0; u < U; ++u) {
             const P minus = psplat<P>(-mu[u]), times = psplat<P>(rs[u]);
             P s1 = psplat<P>(0.f), s2 = s1;
 #pragma unroll
@@ -399,42 +440,54 @@ layer_norm_backward_kernel(const T* x, const T* dy, const float* weight, const f
                         s2 = pfma(t, xh, s2);
                         dw[i] = pfma(fg[k], xh, dw[i]);
                         db[i] = padd(db[i], fg[k]);
+                        if (kHeld) {
+                            xhs[u][i] = xh;
+                            ts[u][i] = t;
+                        }
                     }
                 }
             sums_of[u] = psum(s1);
-            sums_of[V + u] = psum(s2);
+            sums_of[U + u] = psum(s2);
         }
-        row_sums<S, 2 * V>(sums_of, scratch);
+        row_sums<S, 2 * U>(sums_of, scratch, turn);
+        if (!kHeld)
 #pragma unroll
-        for (int u = 0; u < V; ++u)
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int e = 0; e < S::E; ++e) {
-                keep_packed(v[u][e]);
-                keep_packed(g[u][e]);
-            }
+                for (int e = 0; e < S::E; ++e) {
+                    keep_packed(v[u][e]);
+                    keep_packed(g[u][e]);
+                }
 #pragma unroll
-        for (int u = 0; u < V; ++u) {
-            const int i = turn * U + u;
-            if (i >= have.mine) continue;
-            const P m1 = psplat<P>(-sums_of[u] * over_d), m2 = psplat<P>(-sums_of[V + u] * over_d);
+        for (int u = 0; u < U; ++u) {
+            if (turn * U + u >= have.mine) continue;
+            const P m1 = psplat<P>(-sums_of[u] * over_d), m2 = psplat<P>(-sums_of[U + u] * over_d);
             const P minus = psplat<P>(-mu[u]), times = psplat<P>(rs[u]);
 #pragma unroll
             for (int e = 0; e < S::E; ++e) {
                 constexpr int kStep = S::L * S::N;
                 if (e * kStep >= left) continue;
-                P fx[S::n], fg[S::n];
-                unpack_pairs<S::N>(fx, v[u][e]);
-                unpack_pairs<S::N>(fg, g[u][e]);
+                P o[S::n], fg[S::n];
+                if (!kHeld) {
+                    unpack_pairs<S::N>(o, v[u][e]);
+                    unpack_pairs<S::N>(fg, g[u][e]);
+                }
 #pragma unroll
                 for (int k = 0; k < S::n; ++k) {
-                    const P xh = pmul(padd(fx[k], minus), times);
-                    fx[k] = pmul(times, pfma(xh, m2, pfma(fg[k], w[e * S::n + k], m1)));
+                    const int i = e * S::n + k;
+                    const P xh = kHeld ? xhs[u][i] : pmul(padd(o[k], minus), times), t = kHeld ? ts[u][i] : pmul(fg[k], w[i]);
+                    o[k] = pmul(times, pfma(xh, m2, padd(t, m1)));
                 }
-                Vec<T, S::N> o;
-                pack_pairs<S::N>(o, fx);
-                *reinterpret_cast<Vec<T, S::N>*>(dx + lane_at + i * step + e * kStep) = o;
+                Vec<T, S::N> out;
+                pack_pairs<S::N>(out, o);
+                *reinterpret_cast<Vec<T, S::N>*>(next_dx + u * step + e * kStep) = out;
             }
         }
+        if (!A::on) {
+            next_x += U * step;
+            next_dy += U * step;
+        }
+        next_dx += U * step;
     }
     asm volatile("griddepcontrol.launch_dependents;");
     if (!part) return;
@@ -568,7 +621,7 @@ int64_t slots(int64_t rows, int groups) {
 
 template <typename K>
 cudaError_t allow_shared(K kernel, size_t bytes) {
-    if (bytes <= 48 * 1024) return cudaSuccess;
+    if (bytes <= 40 * 1024) return cudaSuccess;      // 48 KB with the static part need no permission
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
@@ -620,7 +673,9 @@ int64_t by_shape(const Args& a, bool aligned) {
         if (n <= 32) return Op::template run<T, Shape<32, 1, N>>(a);
         if (n <= 64) return Op::template run<T, Shape<32, 2, N>>(a);
         if (n <= 128) return Op::template run<T, Shape<128, 1, N>>(a);
+        if (n <= 192) return Op::template run<T, Shape<192, 1, N>>(a);
         if (n <= 256) return Op::template run<T, Shape<256, 1, N>>(a);
+        if (n <= 384) return Op::template run<T, Shape<384, 1, N>>(a);
         if (n <= 512) return Op::template run<T, Shape<512, 1, N>>(a);
         if (n <= 1024) return Op::template run<T, Shape<512, 2, N>>(a);
         if (n <= 2048) return Op::template run<T, Shape<512, 4, N>>(a);
