@@ -25,6 +25,7 @@ namespace la {
 namespace {
 
 constexpr int kSms = 152;
+constexpr int kHeldValues = 16;         // forward: weights and biases of so many columns a lane stay in registers
 constexpr int kCopyBytes = 64 * 1024;   // of rows copied ahead, per SM
 constexpr int kJoinCols = 8, kJoinRows = 32;
 
@@ -61,7 +62,7 @@ struct Ahead {
 template <typename T, typename S>
 struct ForwardPlan {
     static constexpr int U = S::E == 1 ? 2 : 1;
-    static constexpr int registers = U * row_registers<T, S>() + (S::kValues <= 8 ? 2 * S::kValues + 38 : 52);
+    static constexpr int registers = U * row_registers<T, S>() + (S::kValues <= kHeldValues ? 2 * S::kValues + 38 : 52);
     static constexpr int by_registers = blocks_per_sm(S::kThreads, registers);
     using A = Ahead<T, S, U, 1, by_registers>;
     static constexpr int by_memory = 227 * 1024 / ((int)A::bytes + 2048);
@@ -92,6 +93,15 @@ __device__ __forceinline__ float lane_sum(float x) {
     for (int o = Width / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
+constexpr int power_of_two(int n) { return n <= 1 ? 1 : 2 * power_of_two((n + 1) / 2); }
+// Sum of value(w) over a block's warps, in every lane: as many lanes as there are warps take one each, again
+// and again across the warp.
+template <int Warps, typename F>
+__device__ __forceinline__ float warps_sum(int lane, F value) {
+    constexpr int kWidth = power_of_two(Warps);
+    const int w = lane % kWidth;
+    return lane_sum<kWidth>(w < Warps ? value(w) : 0.f);
+}
 // Sum over the L lanes of a row group, for each of U rows; every lane gets it.  Where that is a block,
 // `scratch` holds two turns and `turn` chooses: one barrier keeps a turn's writers off the readers of
 // the turn before last.
@@ -108,7 +118,7 @@ __device__ __forceinline__ void row_sums(float (&x)[U], float* scratch, int turn
             for (int u = 0; u < U; ++u) half[u * kWarps + warp] = x[u];
         __syncthreads();
 #pragma unroll
-        for (int u = 0; u < U; ++u) x[u] = lane_sum<32>(lane < kWarps ? half[u * kWarps + lane] : 0.f);
+        for (int u = 0; u < U; ++u) x[u] = warps_sum<kWarps>(lane, [&](int w) { return half[u * kWarps + w]; });
     }
 }
 // Of the d columns of a row, those that warp w of a block holds.
@@ -222,7 +232,7 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
     const int64_t first = (int64_t)blockIdx.x * S::kRows + threadIdx.x / S::L, step = stride * d;
     const float fd = (float)d, over_d = 1.f / fd;
     // the group's weights stay where the registers allow it
-    constexpr bool kHeld = S::kValues <= 8;
+    constexpr bool kHeld = S::kValues <= kHeldValues;
     using P = typename S::P;
     P w[S::kPairs], b[S::kPairs];
     const int64_t at = first % groups * d + col;
@@ -302,13 +312,14 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
 #pragma unroll
                 for (int u = 0; u < U; ++u) half[u * kWarps + (threadIdx.x >> 5)] = make_float2(s[u], q[u]);
             __syncthreads();
-            const float n = wl < kWarps ? (float)warp_columns<S>(wl, d) : 0.f;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const float2 o = wl < kWarps ? half[u * kWarps + wl] : make_float2(0.f, 0.f);
-                mean_here[u] = mean_of(lane_sum<32>(o.x), fd, over_d);
-                const float off = n > 0.f ? o.x / n - mean_here[u] : 0.f;
-                q[u] = lane_sum<32>(fmaf(n * off, off, o.y));
+                mean_here[u] = mean_of(warps_sum<kWarps>(wl, [&](int w) { return half[u * kWarps + w].x; }), fd, over_d);
+                q[u] = warps_sum<kWarps>(wl, [&](int w) {
+                    const float2 o = half[u * kWarps + w];
+                    const float n = (float)warp_columns<S>(w, d), off = n > 0.f ? o.x / n - mean_here[u] : 0.f;
+                    return fmaf(n * off, off, o.y);
+                });
             }
         }
 #pragma unroll
@@ -626,6 +637,7 @@ cudaError_t allow_shared(K kernel, size_t bytes) {
 }
 
 struct Forward {
+    static constexpr bool kForward = true;
     template <typename T, typename S>
     static int64_t run(const Args& a) {
         using Plan = ForwardPlan<T, S>;
@@ -639,6 +651,7 @@ struct Forward {
     }
 };
 struct Backward {
+    static constexpr bool kForward = false;
     template <typename T, typename S>
     static int64_t run(const Args& a) {
         using Plan = BackwardPlan<T, S>;
@@ -655,28 +668,31 @@ struct Backward {
     }
 };
 struct Slots {
+    static constexpr bool kForward = false;
     template <typename T, typename S>
     static int64_t run(const Args& a) { return slots<BackwardPlan<T, S>, S>(a.rows, a.groups); }
 };
 
-// The lanes and vectors of a row: the fewest lanes that hold it in one vector each up to a warp, two
-// vectors a lane up to 64, then a block of 128 to 512 lanes.
+// The lanes and vectors of a row.  One vector a lane, or two where the forward has bf16 rows (half the
+// lanes: the sums across lanes are most of its instructions; 27 us instead of 31 for 8192 x 4096.  The
+// backward's sums per column leave no room for two: 59 us instead of 48).  Up to 64 vectors share a
+// warp, two a lane from 32 on, longer rows take a block of up to 512 lanes.
 template <typename Op, typename T>
 int64_t by_shape(const Args& a, bool aligned) {
-    constexpr int N = 16 / sizeof(T);
+    constexpr int N = 16 / sizeof(T), E = Op::kForward && N == 8 ? 2 : 1;
     const int d = a.d;
     if (aligned && d % N == 0) {
         const int n = d / N;
         if (n <= 4) return Op::template run<T, Shape<4, 1, N>>(a);
-        if (n <= 8) return Op::template run<T, Shape<8, 1, N>>(a);
-        if (n <= 16) return Op::template run<T, Shape<16, 1, N>>(a);
-        if (n <= 32) return Op::template run<T, Shape<32, 1, N>>(a);
+        if (n <= 8) return Op::template run<T, Shape<8 / E, E, N>>(a);
+        if (n <= 16) return Op::template run<T, Shape<16 / E, E, N>>(a);
+        if (n <= 32) return Op::template run<T, Shape<32 / E, E, N>>(a);
         if (n <= 64) return Op::template run<T, Shape<32, 2, N>>(a);
-        if (n <= 128) return Op::template run<T, Shape<128, 1, N>>(a);
-        if (n <= 192) return Op::template run<T, Shape<192, 1, N>>(a);
-        if (n <= 256) return Op::template run<T, Shape<256, 1, N>>(a);
-        if (n <= 384) return Op::template run<T, Shape<384, 1, N>>(a);
-        if (n <= 512) return Op::template run<T, Shape<512, 1, N>>(a);
+        if (n <= 128) return Op::template run<T, Shape<128 / E, E, N>>(a);
+        if (n <= 192) return Op::template run<T, Shape<192 / E, E, N>>(a);
+        if (n <= 256) return Op::template run<T, Shape<256 / E, E, N>>(a);
+        if (n <= 384) return Op::template run<T, Shape<384 / E, E, N>>(a);
+        if (n <= 512) return Op::template run<T, Shape<512 / E, E, N>>(a);
         if (n <= 1024) return Op::template run<T, Shape<512, 2, N>>(a);
         if (n <= 2048) return Op::template run<T, Shape<512, 4, N>>(a);
         if constexpr (N == 4) return Op::template run<T, Shape<512, 8, N>>(a);
