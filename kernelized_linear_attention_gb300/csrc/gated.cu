@@ -333,8 +333,8 @@ __device__ __forceinline__ void set_marks(const GatedParams& p, int seq, int64_t
     }
 }
 
-// An empty sequence passes its state on.
-__device__ void pass_empty(const GatedParams& p) {
+// An empty sequence passes its state on.  The block's first `threads` threads call it.
+__device__ void pass_empty(const GatedParams& p, int threads) {
     if (!p.edge_out || !(p.cu_seqlens || p.T == 0)) return;
     const int lane = threadIdx.x & 31;
     for (int s0 = blockIdx.x * 32; s0 < p.nseq; s0 += gridDim.x * 32) {
@@ -342,7 +342,7 @@ __device__ void pass_empty(const GatedParams& p) {
         unsigned empty = __ballot_sync(0xffffffffu, s < p.nseq && seq_begin(p, s) == seq_begin(p, s + 1));
         for (; empty; empty &= empty - 1) {
             const int64_t at = (int64_t)(s0 + __ffs(empty) - 1) * p.C;
-            for (int c = threadIdx.x; c < p.C; c += blockDim.x) p.edge_out[at + c] = p.edge_in ? p.edge_in[at + c] : 0.f;
+            for (int c = threadIdx.x; c < p.C; c += threads) p.edge_out[at + c] = p.edge_in ? p.edge_in[at + c] : 0.f;
         }
     }
 }
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__((W + 2) * 32, PerSm) gated_scan_kernel(GatedPa
     }
     const bool forced = !solo && *(volatile int*)&g_force_timeout != 0;
 
-    pass_empty(p);
+    pass_empty(p, kThreads);
 
     const int total = tiles * slices;
     int ticket = solo ? blockIdx.x : 0;
@@ -597,11 +597,9 @@ __global__ void __launch_bounds__(Ring<TA, TX, Rev, W, K, S>::kThreads, PerSm) g
         sh.gave_up = 0;
         tc::fence_mbar_init();
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (p.hdr->error == LA_DEVERR_CU_SEQLENS) return;
     __syncthreads();
-    const bool forced = *(volatile int*)&g_force_timeout != 0;
-    pass_empty(p);
+    // up to here beside the preparation; what each warp then needs of it, it reads for itself
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // A wait that runs out (which takes a fault elsewhere) is recorded, and every role leaves.
     auto wait = [&](uint64_t* bar, int i) {
@@ -640,20 +638,21 @@ __global__ void __launch_bounds__(Ring<TA, TX, Rev, W, K, S>::kThreads, PerSm) g
     }
 
     if (warp == kTeams * W + 2 * kLookers + 2) {
-        // ---------------- tickets
-        const int total = tiles * slices;
+        // ---------------- tickets (none where the boundaries are malformed)
+        const int refused = *(volatile int*)&p.hdr->error;
         // A ticket is asked for two tiles ahead and its sequence one tile ahead: neither trip to L2
         // stands between two copies.
         constexpr int kAhead = 2;
         auto order_of = [&](int t) { return over_slices ? (int)__umul64hi((unsigned long long)t, over_slices) : t; };
         auto seq_of_ticket = [&](int t) {
             const int order = order_of(t);
-            return t < total ? p.tile_seq[Rev ? tiles - 1 - order : order] : 0;
+            return t < tiles * slices ? p.tile_seq[Rev ? tiles - 1 - order : order] : 0;
         };
         int asked[kAhead], ticket[kAhead], seq[kAhead];
-        const int first = lane == 0 ? atomicAdd(p.ticket, 1) : 0;
+        const int first = lane == 0 ? atomicAdd(p.ticket, kAhead) : 0;
+        const int total = refused == LA_DEVERR_CU_SEQLENS ? 0 : tiles * slices;
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) asked[u] = u == 0 ? first : lane == 0 ? atomicAdd(p.ticket, 1) : 0;
+        for (int u = 0; u < kAhead; ++u) asked[u] = first + u;
 #pragma unroll
         for (int u = 0; u < kAhead / 2; ++u) {
             ticket[u] = __shfl_sync(0xffffffffu, asked[u], 0);
@@ -707,6 +706,7 @@ __global__ void __launch_bounds__(Ring<TA, TX, Rev, W, K, S>::kThreads, PerSm) g
 
     if (warp >= kTeams * W) {
         // ---------------- two warps publish every tile's run; pairs look back for the tiles in turn
+        const bool forced = *(volatile int*)&g_force_timeout != 0;
         const int pair = (warp - kTeams * W) / 2, ch = (warp - kTeams * W) % 2 * 32 + lane;
         const bool publisher = pair == kLookers;
         for (int i = publisher ? 0 : pair;; i += publisher ? 1 : kLookers) {
@@ -732,6 +732,8 @@ __global__ void __launch_bounds__(Ring<TA, TX, Rev, W, K, S>::kThreads, PerSm) g
     }
 
     // ---------------- compute
+    if (p.edge_out && p.cu_seqlens && *(volatile int*)&p.hdr->error != LA_DEVERR_CU_SEQLENS)
+        pass_empty(p, kTeams * W * 32);
     const int team = warp / W, member = warp % W;
     const int j0 = (Rev ? W - 1 - member : member) * K;       // the warp's rows; descending for the adjoint
     // The state after the warp's last boundary is kept until it comes back to the tile: edge_out may
