@@ -27,8 +27,8 @@
 //
 // A tile that holds a sequence boundary publishes kCutTag for A: B is the state
 // that leaves it whatever entered, so no value crosses from one sequence to
-// another.  For the adjoint, token order is
-// reversed and a boundary is a last token.
+// another.  For the adjoint, token order is reversed and a boundary is a last
+// token.
 #include "internal.h"
 #include "tc_ptx.cuh"
 
@@ -438,24 +438,24 @@ __global__ void __launch_bounds__((W + 2) * 32, PerSm) gated_scan_kernel(GatedPa
         float2 open = make_float2(0.f, 0.f);
         if (work) {
 #pragma unroll
-        for (int i = 0; i < K; ++i) {
-            const int k = Rev ? K - 1 - i : i;
-            const float2 g = ra[k].get(), in = rx[k].get();
-            if ((cuts >> k) & 1) {
-                float2 s = in;
-                if (p.edge_in) {
-                    const float2 e = edge_two(p.edge_in + (int64_t)(Rev ? sh.last : sh.first)[j0 + k] * C + c, left);
-                    s = Rev ? make_float2(in.x + e.x, in.y + e.y) : fma2(g, e, in);
+            for (int i = 0; i < K; ++i) {
+                const int k = Rev ? K - 1 - i : i;
+                const float2 g = ra[k].get(), in = rx[k].get();
+                if ((cuts >> k) & 1) {
+                    float2 s = in;
+                    if (p.edge_in) {
+                        const float2 e = edge_two(p.edge_in + (int64_t)(Rev ? sh.last : sh.first)[j0 + k] * C + c, left);
+                        s = Rev ? make_float2(in.x + e.x, in.y + e.y) : fma2(g, e, in);
+                    }
+                    r.A = make_float2(0.f, 0.f);
+                    r.B = open = s;
+                } else if (j0 + k < n) {
+                    r.A = mul2(r.A, g);
+                    r.B = fma2(g, r.B, in);
                 }
-                r.A = make_float2(0.f, 0.f);
-                r.B = open = s;
-            } else if (j0 + k < n) {
-                r.A = mul2(r.A, g);
-                r.B = fma2(g, r.B, in);
             }
-        }
-        sh.run[warp][lane] = make_float4(r.A.x, r.A.y, r.B.x, r.B.y);
-        if (lane == 0) sh.cut[warp] = cuts != 0;
+            sh.run[warp][lane] = make_float4(r.A.x, r.A.y, r.B.x, r.B.y);
+            if (lane == 0) sh.cut[warp] = cuts != 0;
         }
         if (threadIdx.x == 0) sh.next = next;
         __syncthreads();
@@ -486,39 +486,39 @@ __global__ void __launch_bounds__((W + 2) * 32, PerSm) gated_scan_kernel(GatedPa
 
         // --- the recurrence from the state that enters the warp
         if (work) {
-        float2 s = *reinterpret_cast<const float2*>(&sh.run[warp][lane]);
-        const int64_t row = (t0 + j0) * C + c;
-        const unsigned open_at = cuts ? (Rev ? __ffs(cuts) - 1 : 31 - __clz(cuts)) : 32;
+            float2 s = *reinterpret_cast<const float2*>(&sh.run[warp][lane]);
+            const int64_t row = (t0 + j0) * C + c;
+            const unsigned open_at = cuts ? (Rev ? __ffs(cuts) - 1 : 31 - __clz(cuts)) : 32;
 #pragma unroll
-        for (int i = 0; i < K; ++i) {
-            const int k = Rev ? K - 1 - i : i;
-            if (j0 + k >= n) continue;
-            const float2 g = ra[k].get(), in = rx[k].get();
-            if ((cuts >> k) & 1) {
-                s = in;
-                if (k == open_at) {
-                    s = open;
-                } else if (p.edge_in) {
-                    const float2 e = edge_two(p.edge_in + (int64_t)(Rev ? sh.last : sh.first)[j0 + k] * C + c, left);
-                    s = Rev ? make_float2(in.x + e.x, in.y + e.y) : fma2(g, e, in);
+            for (int i = 0; i < K; ++i) {
+                const int k = Rev ? K - 1 - i : i;
+                if (j0 + k >= n) continue;
+                const float2 g = ra[k].get(), in = rx[k].get();
+                if ((cuts >> k) & 1) {
+                    s = in;
+                    if (k == open_at) {
+                        s = open;
+                    } else if (p.edge_in) {
+                        const float2 e = edge_two(p.edge_in + (int64_t)(Rev ? sh.last : sh.first)[j0 + k] * C + c, left);
+                        s = Rev ? make_float2(in.x + e.x, in.y + e.y) : fma2(g, e, in);
+                    }
+                } else {
+                    s = fma2(g, s, in);
                 }
-            } else {
-                s = fma2(g, s, in);
-            }
-            store_two<Vec>(static_cast<TX*>(p.y) + row + k * C, left, s);
-            float2 leaving = s;
-            if (Rev) {
-                float2 prev = rh[k].get();
-                if ((ends >> k) & 1) {
-                    const int q = sh.first[j0 + k];
-                    prev = p.state_in ? edge_two(p.state_in + (int64_t)q * C + c, left) : make_float2(0.f, 0.f);
-                    if (p.edge_out) leaving = mul2(load_two<Vec>(a + row + k * C, left).get(), s);
+                store_two<Vec>(static_cast<TX*>(p.y) + row + k * C, left, s);
+                float2 leaving = s;
+                if (Rev) {
+                    float2 prev = rh[k].get();
+                    if ((ends >> k) & 1) {
+                        const int q = sh.first[j0 + k];
+                        prev = p.state_in ? edge_two(p.state_in + (int64_t)q * C + c, left) : make_float2(0.f, 0.f);
+                        if (p.edge_out) leaving = mul2(load_two<Vec>(a + row + k * C, left).get(), s);
+                    }
+                    store_two<Vec>(static_cast<TA*>(p.da) + row + k * C, left, mul2(s, prev));
                 }
-                store_two<Vec>(static_cast<TA*>(p.da) + row + k * C, left, mul2(s, prev));
+                if (((ends >> k) & 1) && p.edge_out)
+                    store_edge(p.edge_out + (int64_t)(Rev ? sh.first : sh.last)[j0 + k] * C + c, left, leaving);
             }
-            if (((ends >> k) & 1) && p.edge_out)
-                store_edge(p.edge_out + (int64_t)(Rev ? sh.first : sh.last)[j0 + k] * C + c, left, leaving);
-        }
         }
         if (solo) return;
         ticket = sh.next;
@@ -998,7 +998,7 @@ cudaError_t dispatch(const GatedParams& p, int slices, cudaStream_t s) {
     constexpr int W = 4, K = kBytes <= 4 ? 32 : kBytes <= 10 ? 16 : 8;
     constexpr int S = kBytes <= 4 ? 6 : kBytes <= 6 ? 8 : kBytes <= 8 ? 6 : kBytes <= 10 ? 4 : 8;
     if (tma && p.T > W * K) return run_ring<TA, TX, Rev, W, K, S, 1>(p, slices, s);
-    return vec ? run_registers<TA, TX, Rev, true, W, K, 1>(p, slices, s) : run_registers<TA, TX, Rev, false, W, K, 1>(p, slices, s);
+    return vec ? run_registers<TA, TX, Rev, true, W, K, 2>(p, slices, s) : run_registers<TA, TX, Rev, false, W, K, 2>(p, slices, s);
 }
 
 template <typename TA, typename TX>
