@@ -347,8 +347,8 @@ __device__ void pass_empty(const GatedParams& p, int threads) {
     }
 }
 
-// Tiles held in registers, one at a time per block: single tiles, and rows whose alignment rules
-// out tile copies.
+// Tiles held in registers, one at a time per block: single tiles, and bf16 rows of odd length, whose
+// elements no asynchronous copy can fetch.
 // The same warps, tokens and order of operations as the ring's: the same results.
 template <typename TA, typename TX, bool Rev, bool Vec, int W, int K, int PerSm>
 __global__ void __launch_bounds__((W + 2) * 32, PerSm) gated_scan_kernel(GatedParams p, int tiles, int slices, int solo) {
@@ -540,17 +540,22 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, long 
 // --------------------------------------------------------------------------
 // Tiles that TMA brings into a ring in shared memory.  One warp takes tickets, one starts the copies,
 // compute warps form the tile's runs, a publishing pair of warps sends them out without
-// waiting for other tiles, look-back warps find the entering state, and the compute warps come back to the tile when it is there to run the recurrence.  A
-// compute warp takes whichever of the two it can do next, so stages are neither held for a fixed
-// number of tiles nor idle: the trips to L2 are hidden behind the tiles that follow.
+// waiting for other tiles, look-back warps find the entering state, and the compute warps come back to
+// the tile when it is there to run the recurrence.  A compute warp takes whichever of the two it can do
+// next, so stages are neither held for a fixed number of tiles nor idle: the trips to L2 are hidden
+// behind the tiles that follow.
+//
+// Tile copies (Tma) need rows that start on 16 bytes.  Other rows of four-byte steps are copied by four
+// warps, four bytes a lane, into the same places (32768 x 1023 in fp32: 182 us with tiles in registers).
 // --------------------------------------------------------------------------
 
-template <typename TA, typename TX, bool Rev, int W, int K, int S>
+template <typename TA, typename TX, bool Rev, bool Tma, int W, int K, int S>
 struct Ring {
     static constexpr int kTeams = 2;                    // compute teams, taking tiles in turn: W warps of K tokens
     static constexpr int kRows = W * K;
     static constexpr int kLookers = S % 4 == 0 ? 4 : S % 5 == 0 ? 5 : 3;   // pairs of look-back warps, in turn
-    static constexpr int kThreads = (kTeams * W + 2 * kLookers + 2 + 2) * 32;
+    static constexpr int kCopiers = Tma ? 1 : 4;
+    static constexpr int kThreads = (kTeams * W + 2 * kLookers + 2 + 1 + kCopiers) * 32;
     static constexpr int kA = kRows * kSlice * (int)sizeof(TA), kX = kRows * kSlice * (int)sizeof(TX);
     static constexpr int kStage = kA + kX + (Rev ? kX : 0);
     struct Small {
@@ -566,13 +571,34 @@ struct Ring {
     static constexpr size_t kBytes = (size_t)S * kStage + sizeof(Small) + 128;
 };
 
-template <typename TA, typename TX, bool Rev, int W, int K, int S, int PerSm>
-__global__ void __launch_bounds__(Ring<TA, TX, Rev, W, K, S>::kThreads, PerSm) gated_ring_kernel(GatedParams p, int tiles, int slices,
-                                                                  unsigned long long over_slices,   // 2^64 / slices, rounded up; 0 for one
-                                                                  const __grid_constant__ CUtensorMap map_a,
-                                                                  const __grid_constant__ CUtensorMap map_x,
-                                                                  const __grid_constant__ CUtensorMap map_h) {
-    using R = Ring<TA, TX, Rev, W, K, S>;
+// Copies `rows` rows x kSlice channels of [T][C] from row t0 and channel c0 on to `place`, rows and channels
+// outside as zeros: the share of one of kCopiers warps.
+template <typename T, int Rows>
+__device__ __forceinline__ void copy_rows(uint8_t* place, const void* from, int64_t t0, int c0, int64_t tokens, int C, int warp,
+                                          int warps, int lane) {
+    constexpr int kWords = kSlice * (int)sizeof(T) / 4, kEach = 4 / (int)sizeof(T);   // of a row; elements in a word
+    for (int r = warp; r < Rows; r += warps) {
+        const int64_t t = t0 + r;
+        const T* row = static_cast<const T*>(from) + (t < 0 ? 0 : t) * C + c0;
+#pragma unroll
+        for (int w = 0; w < kWords / 32; ++w) {
+            const int e = (w * 32 + lane) * kEach;
+            const int there = t >= 0 && t < tokens && c0 + e < C ? 4 : 0;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(place) + (r * kWords + w * 32 + lane) * 4),
+                         "l"(there ? row + e : static_cast<const T*>(from)), "r"(there)
+                         : "memory");
+        }
+    }
+}
+
+// over_slices: 2^64 / slices, rounded up; 0 for one slice.
+template <typename TA, typename TX, bool Rev, bool Tma, int W, int K, int S>
+__global__ void __launch_bounds__(Ring<TA, TX, Rev, Tma, W, K, S>::kThreads, 1)
+gated_ring_kernel(GatedParams p, int tiles, int slices, unsigned long long over_slices,
+                  const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_x,
+                  const __grid_constant__ CUtensorMap map_h) {
+    using R = Ring<TA, TX, Rev, Tma, W, K, S>;
+    constexpr bool Vec = Tma || sizeof(TA) == 2 || sizeof(TX) == 2;   // bf16 rows without tile copies: of even length
     static_assert(R::kRows >= kMinTile, "the workspace holds ceil(T / kMinTile) tiles");
     constexpr int kLookers = R::kLookers, kTeams = R::kTeams;
     // Who takes every n-th tile waits for phases of its own tiles only, one after the other, when n
@@ -588,7 +614,7 @@ __global__ void __launch_bounds__(Ring<TA, TX, Rev, W, K, S>::kThreads, PerSm) g
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
             tc::mbar_init(&sh.known[i], 1);
-            tc::mbar_init(&sh.full[i], 2);             // the copies, and the tile's marks
+            tc::mbar_init(&sh.full[i], 1 + (Tma ? 1 : 32 * R::kCopiers));   // the tile's marks, and the copies
             tc::mbar_init(&sh.runs[i], W);
             tc::mbar_init(&sh.sent[i], 2);
             tc::mbar_init(&sh.carried[i], 2);
@@ -609,30 +635,43 @@ __global__ void __launch_bounds__(Ring<TA, TX, Rev, W, K, S>::kThreads, PerSm) g
         return false;
     };
 
-    if (warp == kTeams * W + 2 * kLookers + 3) {
+    if (warp >= kTeams * W + 2 * kLookers + 3) {
         // ---------------- copies of the tiles that the ticket warp names
-        if (lane == 0) {
+        const int copier = warp - (kTeams * W + 2 * kLookers + 3);
+        if (!Tma || lane == 0) {
             int copied = 0;
             for (int i = 0;; ++i) {
                 const int st = i % S;
                 if (!wait(&sh.known[st], i)) break;
                 const int order = sh.order[st];
                 if (order < 0) {
+                    const bool last = sh.slice[st];       // the last mark of the end
                     tc::mbar_arrive(&sh.full[st]);
-                    if (sh.slice[st]) return;             // the last mark of the end
+                    if (last) return;
                     continue;
                 }
-                const int x = sh.slice[st] * kSlice, t0 = (Rev ? tiles - 1 - order : order) * R::kRows;
+                const int c0 = sh.slice[st] * kSlice, t0 = (Rev ? tiles - 1 - order : order) * R::kRows;
                 uint8_t* at = data + (size_t)st * R::kStage;
-                tc::mbar_arrive_expect_tx(&sh.full[st], R::kStage);
                 // rows before the first and behind the last one come as zeros
-                tc::tma_load_2d(at, &map_a, x, t0 + (Rev ? 1 : 0), &sh.full[st]);
-                tc::tma_load_2d(at + R::kA, &map_x, x, t0, &sh.full[st]);
-                if (Rev) tc::tma_load_2d(at + R::kA + R::kX, &map_h, x, t0 - 1, &sh.full[st]);
+                if (Tma) {
+                    tc::mbar_arrive_expect_tx(&sh.full[st], R::kStage);
+                    tc::tma_load_2d(at, &map_a, c0, t0 + (Rev ? 1 : 0), &sh.full[st]);
+                    tc::tma_load_2d(at + R::kA, &map_x, c0, t0, &sh.full[st]);
+                    if (Rev) tc::tma_load_2d(at + R::kA + R::kX, &map_h, c0, t0 - 1, &sh.full[st]);
+                } else {
+                    copy_rows<TA, R::kRows>(at, p.a, (int64_t)t0 + (Rev ? 1 : 0), c0, p.T, p.C, copier, R::kCopiers, lane);
+                    copy_rows<TX, R::kRows>(at + R::kA, p.x, t0, c0, p.T, p.C, copier, R::kCopiers, lane);
+                    if (Rev)
+                        copy_rows<TX, R::kRows>(at + R::kA + R::kX, p.h, (int64_t)t0 - 1, c0, p.T, p.C, copier, R::kCopiers, lane);
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(&sh.full[st])) : "memory");
+                }
                 copied = i + 1;
             }
             // no copy is in flight when the block ends
-            for (int j = copied > S ? copied - S : 0; j < copied; ++j) wait_phase(&sh.full[j % S], (j / S) & 1, kWaitClocks);
+            if (Tma)
+                for (int j = copied > S ? copied - S : 0; j < copied; ++j) wait_phase(&sh.full[j % S], (j / S) & 1, kWaitClocks);
+            else
+                asm volatile("cp.async.wait_all;" ::: "memory");
         }
         return;
     }
@@ -839,8 +878,8 @@ __global__ void __launch_bounds__(Ring<TA, TX, Rev, W, K, S>::kThreads, PerSm) g
                 for (int q = 0; q < K; ++q) {
                     const int k = Rev ? K - 1 - q : q;
                     s = fma2(sa[k * (kSlice / 2)].get(), s, sx[k * (kSlice / 2)].get());
-                    store_two<true>(y + k * (int64_t)p.C, left, s);
-                    if (Rev) store_two<true>(da + k * (int64_t)p.C, left, mul2(s, sh_h[k * (kSlice / 2)].get()));
+                    store_two<Vec>(y + k * (int64_t)p.C, left, s);
+                    if (Rev) store_two<Vec>(da + k * (int64_t)p.C, left, mul2(s, sh_h[k * (kSlice / 2)].get()));
                 }
             } else {
                 const int open_at = cuts ? (Rev ? __ffs(cuts) - 1 : 31 - __clz(cuts)) : 32;
@@ -861,7 +900,7 @@ __global__ void __launch_bounds__(Ring<TA, TX, Rev, W, K, S>::kThreads, PerSm) g
                     } else {
                         s = fma2(g, s, in);
                     }
-                    store_two<true>(y + k * (int64_t)p.C, left, s);
+                    store_two<Vec>(y + k * (int64_t)p.C, left, s);
                     float2 leaving = s;
                     if (Rev) {
                         float2 prev = sh_h[k * (kSlice / 2)].get();
@@ -869,9 +908,9 @@ __global__ void __launch_bounds__(Ring<TA, TX, Rev, W, K, S>::kThreads, PerSm) g
                             const int sq = sh.first[st][j0 + k];
                             prev = p.state_in ? edge_two(p.state_in + (int64_t)sq * p.C + c, left) : make_float2(0.f, 0.f);
                             if (p.edge_out)
-                                leaving = mul2(load_two<true>(static_cast<const TA*>(p.a) + row + k * (int64_t)p.C, left).get(), s);
+                                leaving = mul2(load_two<Vec>(static_cast<const TA*>(p.a) + row + k * (int64_t)p.C, left).get(), s);
                         }
-                        store_two<true>(da + k * (int64_t)p.C, left, mul2(s, prev));
+                        store_two<Vec>(da + k * (int64_t)p.C, left, mul2(s, prev));
                     }
                     if (((ends >> k) & 1) && p.edge_out)
                         store_edge(p.edge_out + (int64_t)(Rev ? sh.first[st] : sh.last[st])[j0 + k] * p.C + c, left, leaving);
@@ -966,19 +1005,19 @@ bool row_map(CUtensorMap* m, const void* base, int64_t tokens, int C, int rows) 
     return tc_encode_tiled(m, sizeof(T) == 4, base, 2, dims, strides, box, es);
 }
 
-template <typename TA, typename TX, bool Rev, int W, int K, int S, int PerSm>
+template <typename TA, typename TX, bool Rev, bool Tma, int W, int K, int S>
 cudaError_t run_ring(const GatedParams& p, int slices, cudaStream_t s) {
-    using R = Ring<TA, TX, Rev, W, K, S>;
-    static_assert(PerSm * (R::kBytes + 1024) <= 228 * 1024, "blocks per SM and their shared memory");
-    CUtensorMap ma, mx, mh;
-    if (!row_map<TA>(&ma, p.a, p.T, p.C, R::kRows) || !row_map<TX>(&mx, p.x, p.T, p.C, R::kRows) ||
-        !row_map<TX>(&mh, Rev ? p.h : p.x, p.T, p.C, R::kRows))
+    using R = Ring<TA, TX, Rev, Tma, W, K, S>;
+    static_assert(R::kBytes <= 227 * 1024, "a block's shared memory");
+    CUtensorMap ma{}, mx{}, mh{};
+    if (Tma && (!row_map<TA>(&ma, p.a, p.T, p.C, R::kRows) || !row_map<TX>(&mx, p.x, p.T, p.C, R::kRows) ||
+                !row_map<TX>(&mh, Rev ? p.h : p.x, p.T, p.C, R::kRows)))
         return cudaErrorInvalidValue;
-    auto kernel = gated_ring_kernel<TA, TX, Rev, W, K, S, PerSm>;
+    auto kernel = gated_ring_kernel<TA, TX, Rev, Tma, W, K, S>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)R::kBytes);
     if (e != cudaSuccess) return e;
-    return launch_tiles(kernel, p, Rev ? 1 : 0, R::kRows, (int)ceil_div(p.T, R::kRows), slices, PerSm, R::kThreads, R::kBytes,
-                        s, slices > 1 ? ~0ull / (unsigned)slices + 1 : 0ull, ma, mx, mh);
+    return launch_tiles(kernel, p, Rev ? 1 : 0, R::kRows, (int)ceil_div(p.T, R::kRows), slices, 1, R::kThreads, R::kBytes, s,
+                        slices > 1 ? ~0ull / (unsigned)slices + 1 : 0ull, ma, mx, mh);
 }
 
 bool two_aligned(const void* p, size_t esize) { return reinterpret_cast<uintptr_t>(p) % (2 * esize) == 0; }
@@ -997,7 +1036,10 @@ cudaError_t dispatch(const GatedParams& p, int slices, cudaStream_t s) {
     constexpr int kBytes = (int)(sizeof(TA) + (Rev ? 2 : 1) * sizeof(TX));   // of a token and channel
     constexpr int W = 4, K = kBytes <= 4 ? 32 : kBytes <= 10 ? 16 : 8;
     constexpr int S = kBytes <= 4 ? 6 : kBytes <= 6 ? 8 : kBytes <= 8 ? 6 : kBytes <= 10 ? 4 : 8;
-    if (tma && p.T > W * K) return run_ring<TA, TX, Rev, W, K, S, 1>(p, slices, s);
+    if (p.T > W * K) {
+        if (tma) return run_ring<TA, TX, Rev, true, W, K, S>(p, slices, s);
+        if (vec || (sizeof(TA) == 4 && sizeof(TX) == 4)) return run_ring<TA, TX, Rev, false, W, K, S>(p, slices, s);
+    }
     return vec ? run_registers<TA, TX, Rev, true, W, K, 2>(p, slices, s) : run_registers<TA, TX, Rev, false, W, K, 2>(p, slices, s);
 }
 
