@@ -45,19 +45,22 @@ __device__ __forceinline__ int over(int i, uint32_t m) { return m ? (int)__umulh
 template <typename T, int N, bool Interleaved>
 __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_constant__ RotaryParams p,
                                                                 const __grid_constant__ RotaryPlan plan) {
-    extern __shared__ float2 cs[];       // [tokens][P]
+    // [tokens][P]; where pairs are halves [tokens][N][P / N]: the k-th pairs of all units lie together, so
+    // that neighbouring lanes, which turn neighbouring units, read neighbouring words (82 us instead of 86
+    // for q and k of 65536 x 16 x 64 in bf16; interleaved pairs, half as many a unit, lose 5 us that way)
+    extern __shared__ float2 cs[];
     using V = Vec<T, N>;
     constexpr bool kOne = Interleaved && N > 1;   // whole pairs in one vector
     constexpr int kPairs = kOne ? N / 2 : N;
     const int64_t t0 = (int64_t)blockIdx.x * plan.tokens;
     const int h0 = blockIdx.y * plan.share;
     const int tokens = (int)min64(plan.tokens, p.T - t0), per_token = plan.share * plan.units;
-    const int total = tokens * per_token, second = Interleaved ? 1 : p.P;
+    const int total = tokens * per_token, second = Interleaved ? 1 : p.P, apart = kOne ? 1 : p.P / kPairs;
 
     for (int first = threadIdx.x; first - (int)threadIdx.x < total; first += kUnits * kRotaryThreads) {
         V a[kUnits], b[kUnits];
         T* out[kUnits];
-        int pair[kUnits];                // token * P + first pair, or -1: copied; -2: nothing
+        int pair[kUnits];                // the unit's first place in the table, or -1: copied; -2: nothing
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
             const int i = first + u * kRotaryThreads;
@@ -73,7 +76,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
             out[u] = static_cast<T*>(is_k ? p.k_out : p.q_out) + at;
             a[u] = *reinterpret_cast<const V*>(x);
             if (turned && !kOne) b[u] = *reinterpret_cast<const V*>(x + second);
-            pair[u] = turned ? t * p.P + e * kPairs : -1;
+            pair[u] = turned ? t * p.P + e * (kOne ? kPairs : 1) : -1;
         }
         if (first == (int)threadIdx.x) {
             // the tokens' cos and sin, while the first loads are on their way
@@ -87,7 +90,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
                 float s, c;
                 sincospif((float)(long long)turn * 0x1p-63f, &s, &c);
                 if (!isfinite(f)) s = c = __int_as_float(0x7fc00000);
-                cs[i] = make_float2(c, p.inverse ? -s : s);
+                cs[kOne ? i : t * p.P + j % kPairs * apart + j / kPairs] = make_float2(c, p.inverse ? -s : s);
             }
             __syncthreads();
         }
@@ -100,7 +103,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
                 if (!kOne) unpack(fb, b[u]);
 #pragma unroll
                 for (int k = 0; k < kPairs; ++k) {
-                    const float2 w = cs[pair[u] + k];
+                    const float2 w = cs[pair[u] + k * apart];
                     float& x0 = fa[kOne ? 2 * k : k];
                     float& x1 = kOne ? fa[kOne ? 2 * k + 1 : 0] : fb[k];
                     const float f0 = x0, f1 = x1;
