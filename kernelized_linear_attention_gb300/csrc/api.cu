@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "internal.h"
+#include "ops/ops.h"
 
 namespace la {
 

@@ -29,7 +29,8 @@
 // that leaves it whatever entered, so no value crosses from one sequence to
 // another.  For the adjoint, token order is reversed and a boundary is a last
 // token.
-#include "internal.h"
+#include "ops/ops.h"
+#include "ops/vec.cuh"
 #include "tc_ptx.cuh"
 
 namespace la {
@@ -922,14 +923,24 @@ gated_ring_kernel(GatedParams p, int tiles, int slices, unsigned long long over_
     }
 }
 
-template <typename TA, typename TX>
+// One token: N neighbouring elements a thread (four where the operands' alignment allows vectors).
+template <typename TA, typename TX, int N>
 __global__ void __launch_bounds__(kPrepThreads) gated_step_kernel(const TA* a, const TX* b, int64_t n,
                                                                   const float* state_in, float* state_out, TX* h) {
-    const int64_t i = (int64_t)blockIdx.x * kPrepThreads + threadIdx.x;
+    const int64_t i = ((int64_t)blockIdx.x * kPrepThreads + threadIdx.x) * N;
     if (i >= n) return;
-    const float s = fmaf(load_elem(a, i), state_in[i], load_elem(b, i));
-    state_out[i] = s;
-    store_elem(h, i, s);
+    float fa[N], fb[N], fs[N];
+    unpack(fa, *reinterpret_cast<const Vec<TA, N>*>(a + i));
+    unpack(fb, *reinterpret_cast<const Vec<TX, N>*>(b + i));
+    unpack(fs, *reinterpret_cast<const Vec<float, N>*>(state_in + i));
+#pragma unroll
+    for (int k = 0; k < N; ++k) fs[k] = fmaf(fa[k], fs[k], fb[k]);
+    Vec<float, N> s;
+    Vec<TX, N> o;
+    pack(s, fs);
+    pack(o, fs);
+    *reinterpret_cast<Vec<float, N>*>(state_out + i) = s;
+    *reinterpret_cast<Vec<TX, N>*>(h + i) = o;
 }
 
 struct GatedLayout {
@@ -996,13 +1007,28 @@ cudaError_t run_registers(const GatedParams& p, int slices, cudaStream_t s) {
     return launch_tiles(kernel, p, Rev ? 1 : 0, kTile, tiles, slices, PerSm, kThreads, 0, s, 0);
 }
 
-// [T][C] rows -> boxes of `rows` tokens x kSlice channels.
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+// The driver's encoder of tile maps, looked up once (the library is not linked with the driver's).
+EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+        return e == cudaSuccess && found == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeTiled>(f) : nullptr;
+    }();
+    return fn;
+}
+
+// [T][C] rows -> boxes of `rows` tokens x kSlice channels, unswizzled.
 template <typename T>
 bool row_map(CUtensorMap* m, const void* base, int64_t tokens, int C, int rows) {
-    const uint64_t dims[2] = {(uint64_t)C, (uint64_t)tokens};
-    const uint64_t strides[1] = {(uint64_t)C * sizeof(T)};
-    const uint32_t box[2] = {kSlice, (uint32_t)rows}, es[2] = {1, 1};
-    return tc_encode_tiled(m, sizeof(T) == 4, base, 2, dims, strides, box, es);
+    const cuuint64_t dims[2] = {(cuuint64_t)C, (cuuint64_t)tokens}, strides[1] = {(cuuint64_t)C * sizeof(T)};
+    const cuuint32_t box[2] = {kSlice, (cuuint32_t)rows}, steps[2] = {1, 1};
+    const EncodeTiled encode = encode_tiled();
+    return encode && encode(m, sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                            const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename TA, typename TX, bool Rev, bool Tma, int W, int K, int S>
@@ -1046,8 +1072,17 @@ cudaError_t dispatch(const GatedParams& p, int slices, cudaStream_t s) {
 template <typename TA, typename TX>
 cudaError_t step(const void* a, const void* b, int64_t n, const float* state_in, float* state_out, void* h,
                  cudaStream_t s) {
-    gated_step_kernel<TA, TX><<<(unsigned)ceil_div(n, kPrepThreads), kPrepThreads, 0, s>>>(
-        static_cast<const TA*>(a), static_cast<const TX*>(b), n, state_in, state_out, static_cast<TX*>(h));
+    auto aligned = [](const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; };
+    const TA* ta = static_cast<const TA*>(a);
+    const TX* tb = static_cast<const TX*>(b);
+    TX* th = static_cast<TX*>(h);
+    if (n % 4 == 0 && aligned(a, 4 * sizeof(TA)) && aligned(b, 4 * sizeof(TX)) && aligned(h, 4 * sizeof(TX)) &&
+        aligned(state_in, 16) && aligned(state_out, 16))
+        gated_step_kernel<TA, TX, 4><<<(unsigned)ceil_div(n / 4, kPrepThreads), kPrepThreads, 0, s>>>(ta, tb, n, state_in,
+                                                                                                    state_out, th);
+    else
+        gated_step_kernel<TA, TX, 1><<<(unsigned)ceil_div(n, kPrepThreads), kPrepThreads, 0, s>>>(ta, tb, n, state_in,
+                                                                                                state_out, th);
     return cudaGetLastError();
 }
 

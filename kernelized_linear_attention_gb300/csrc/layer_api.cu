@@ -2,7 +2,7 @@
 // recurrence, layer norm, rotary positions): argument checks and dispatch.
 #include <cmath>
 
-#include "internal.h"
+#include "ops/ops.h"
 
 namespace la {
 

@@ -17,8 +17,8 @@
 // weight gradients add up in registers over all its rows.  Blocks leave their
 // sums in the workspace as rows of a [M][groups * d] matrix that a second
 // kernel adds up by column with compensated sums, in a fixed order.
-#include "internal.h"
-#include "vec.cuh"
+#include "ops/ops.h"
+#include "ops/vec.cuh"
 
 namespace la {
 

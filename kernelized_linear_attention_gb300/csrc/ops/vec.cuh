@@ -5,7 +5,7 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
-#include "tc_ptx.cuh"
+#include "../tc_ptx.cuh"
 
 namespace la {
 

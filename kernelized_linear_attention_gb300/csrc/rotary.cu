@@ -12,8 +12,8 @@
 // turn and store.  A thread's unit of work is N neighbouring channels and, where
 // pairs are halves, their N partners; N channels are 16 bytes where every row
 // allows it, else one pair is the unit.
-#include "internal.h"
-#include "vec.cuh"
+#include "ops/ops.h"
+#include "ops/vec.cuh"
 
 namespace la {
 

@@ -2405,17 +2405,6 @@ cudaError_t set_smem(K kernel, size_t bytes) {
 
 }  // namespace
 
-bool tc_encode_tiled(void* map, bool f32, const void* base, int rank, const uint64_t* dims,
-                     const uint64_t* strides, const uint32_t* box, const uint32_t* steps) {
-    EncodeTiledFn fn = encode_fn();
-    static_assert(sizeof(cuuint64_t) == sizeof(uint64_t) && sizeof(cuuint32_t) == sizeof(uint32_t), "driver types");
-    return fn && fn(static_cast<CUtensorMap*>(map), f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                    (cuuint32_t)rank, const_cast<void*>(base), reinterpret_cast<const cuuint64_t*>(dims),
-                    reinterpret_cast<const cuuint64_t*>(strides), box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 cudaError_t tc_force_wait_timeout(int enable) {
     return cudaMemcpyToSymbol(g_force_wait_timeout, &enable, sizeof(int));
 }

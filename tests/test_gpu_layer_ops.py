@@ -137,6 +137,26 @@ def test_gated_scan_long_sequence_with_gates_near_one(la):
     _check_scan_backward(la, c, h, "f32", "f32", True)
 
 
+@pytest.mark.parametrize("d", [64, 62, 63, 72])
+@pytest.mark.parametrize("ta,tb", [("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16"), ("bf16", "f32")])
+def test_gated_scan_states_that_cross_many_tiles(la, d, ta, tb):
+    """Gates of 1 - 2^-7 and 1 - 2^-8 (exact in bf16) let a state reach over hundreds of tokens; the
+    long sequences span several blocks of 64 tiles in every type and every kind of copy."""
+    c = _scan_case([19000, 0, 5, 17003], 1, d, ta, tb, 20)
+    g = torch.Generator().manual_seed(20)
+    c["a"] = (1.0 - 2.0 ** -torch.randint(7, 9, c["a"].shape, generator=g).float()).to(TYPES[ta]).cuda()
+    h, _ = _check_scan(la, c, ta, tb, True)
+    _check_scan_backward(la, c, h, ta, tb, True)
+
+
+def test_gated_scan_thousands_of_short_sequences(la):
+    lengths = np.random.default_rng(21).integers(0, 4, 20000).tolist()
+    for d, ta, tb in ((48, "f32", "bf16"), (33, "f32", "f32")):
+        c = _scan_case(lengths, 1, d, ta, tb, 22)
+        h, _ = _check_scan(la, c, ta, tb, True)
+        _check_scan_backward(la, c, h, ta, tb, True)
+
+
 def test_gated_scan_split_over_calls_and_steps(la):
     c = _scan_case([700], 2, 24, "f32", "f32", 11)
     whole, end = la.la_gated_scan(c["a"], c["b"], state_in=c["s"], return_state=True)
@@ -645,3 +665,35 @@ def test_gated_scan_wait_that_runs_out_is_reported(la):
     _check_scan_backward(la, c, h, "f32", "f32", True)
     la.la_gated_scan(c["a"], c["b"], workspace=ws)
     assert la.la_workspace_error(ws) == 0
+
+
+def test_first_calls_of_a_process_can_be_captured(la):
+    """Nothing has to run once before a capture: a fresh process captures its very first calls."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import torch, kernelized_linear_attention_gb300 as la
+a = torch.rand(700, 2, 64, device="cuda"); b = torch.randn(700, 2, 64, device="cuda"); w = torch.ones(2, 64, device="cuda")
+f = torch.rand(32, device="cuda"); p = torch.arange(700, dtype=torch.int32, device="cuda"); big = torch.randn(3, 8192, device="cuda")
+w2 = torch.ones(8192, device="cuda")
+g = torch.cuda.CUDAGraph()
+def calls():
+    h = la.la_gated_scan(a, b)
+    da, db = la.la_gated_scan_backward(a, h, b)
+    y, m, r = la.la_layer_norm(h, w, return_stats=True)
+    n = la.la_layer_norm_backward(h, b, m, r, w)
+    y2, m2, r2 = la.la_layer_norm(big, w2, return_stats=True)
+    n2 = la.la_layer_norm_backward(big, b.new_ones(3, 8192), m2, r2, w2)
+    return (h, da, db, y, *n, y2, *n2, *la.la_rotary(a, b, f, p, [32]))
+with torch.cuda.graph(g):
+    outs = calls()
+g.replay()
+torch.cuda.synchronize()
+got = [o.clone() for o in outs]
+assert all(torch.equal(x, y) for x, y in zip(got, calls()))
+print("captured")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=root, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout + r.stderr
