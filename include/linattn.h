@@ -422,7 +422,7 @@ LA_API int la_selected_path(int causal, int map, int dtype, int d_k, int d_v, in
  *              token, not rounded to dtype; an empty sequence's state_in (or 0)
  *              is copied.  May be the same array as state_in.
  *   The state is fp32 throughout and h is rounded once from it.  Tokens are
- *   combined in an order that depends on T, H and d alone, so results are
+ *   combined in an order that depends on T and the types alone, so results are
  *   deterministic.  A state that crosses tiles of tokens is scaled by the
  *   product of their gates: gates of magnitude above one are computed as given
  *   as long as those products stay finite in fp32.  A sequence's values,
@@ -493,7 +493,8 @@ LA_API la_status la_layer_norm(const void* x, const float* weight, const float* 
  *   dweight, dbias: NULL or fp32 [groups, d] (written, not added to; 0 for no
  *   rows).  Sums over rows are fp32 within a block and compensated fp32 across
  *   blocks, in a fixed order (deterministic).  workspace:
- *   la_layer_norm_backward_workspace_bytes(...) bytes, 256-byte aligned.
+ *   la_layer_norm_backward_workspace_bytes(...) bytes, 256-byte aligned; calls
+ *   that may overlap need workspaces of their own.
  */
 LA_API la_status la_layer_norm_backward(const void* x, const void* dy, const float* weight, const float* mean,
                                         const float* rstd, int dtype, int64_t rows, int groups, int d, void* dx,

@@ -667,30 +667,32 @@ def la_layer_norm_backward_workspace_bytes(dtype, rows: int, groups: int, d: int
     return load_library().la_layer_norm_backward_workspace_bytes(dt, rows, groups, d)
 
 
-def la_layer_norm_backward(x, dy, mean, rstd, weight, dx=None, dweight=None, dbias=None, workspace=None, stream=None):
+def la_layer_norm_backward(x, dy, mean, rstd, weight=None, dx=None, dweight=None, dbias=None, workspace=None, stream=None):
     """Gradients (dx, dweight, dbias) of sum(dy * y) for la_layer_norm; weight [d] or [H, d] gives
-    the shape of dweight and dbias (fp32)."""
+    the shape of dweight and dbias (fp32).  weight None is 1, and without a dweight or dbias to tell
+    their shape these gradients are None."""
     lib = load_library()
-    if not isinstance(weight, torch.Tensor):
-        raise TypeError("weight must be a torch.Tensor")
-    rows, groups, d = _norm_shape(x, weight, None)
-    f32, dev, shape, wshape = torch.float32, _first(x, "x"), x.shape, weight.shape
+    like = weight if weight is not None else dweight if dweight is not None else dbias
+    rows, groups, d = _norm_shape(x, like, None)
+    f32, dev, shape = torch.float32, _first(x, "x"), x.shape
     if _elsewhere(dev, stream):
         with _On(dev, stream):
             return la_layer_norm_backward(x, dy, mean, rstd, weight, dx, dweight, dbias, workspace)
     stats = shape[:-1]
     pd = _addr(dy, "dy", x.dtype, shape, dev)
     pm, pr = _addr(mean, "mean", f32, stats, dev), _addr(rstd, "rstd", f32, stats, dev)
-    pw = _addr(weight, "weight", f32, None, dev)
+    pw = _addr_or_none(weight, "weight", f32, None, dev)
     dx = torch.empty_like(x) if dx is None else dx
-    dweight = torch.empty_like(weight) if dweight is None else dweight
-    dbias = torch.empty_like(weight) if dbias is None else dbias
+    wshape = None if like is None else like.shape
+    if like is not None:
+        dweight = torch.empty(wshape, dtype=f32, device=x.device) if dweight is None else dweight
+        dbias = torch.empty(wshape, dtype=f32, device=x.device) if dbias is None else dbias
     workspace, pws, nws = _workspace(
         workspace, 0 if workspace is not None else
         lib.la_layer_norm_backward_workspace_bytes(DTYPE_IDS[x.dtype], rows, groups, d), dev)
     _check("la_layer_norm_backward", lib.la_layer_norm_backward(
         x.data_ptr(), pd, pw, pm, pr, DTYPE_IDS[x.dtype], rows, groups, d, _addr(dx, "dx", x.dtype, shape, dev),
-        _addr(dweight, "dweight", f32, wshape, dev), _addr(dbias, "dbias", f32, wshape, dev), pws, nws,
+        _addr_or_none(dweight, "dweight", f32, wshape, dev), _addr_or_none(dbias, "dbias", f32, wshape, dev), pws, nws,
         _current_stream(dev)))
     return dx, dweight, dbias
 

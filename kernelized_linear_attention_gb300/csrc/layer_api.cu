@@ -45,7 +45,8 @@ la_status gated_dims(bool has_cu, int nseq, int64_t T, int H, int d) {
 
 la_status norm_dims(int dtype, int64_t rows, int groups, int d) {
     if (!dtype_ok(dtype) || rows < 0 || groups < 1 || d < 1 || rows % groups != 0) return LA_ERR_INVALID_ARG;
-    if (d > LA_MAX_NORM_D || (int64_t)groups * d > LA_MAX_CHANNELS || rows > (int64_t)1 << 40) return LA_ERR_UNSUPPORTED;
+    if (d > LA_MAX_NORM_D || (int64_t)groups * d > LA_MAX_CHANNELS || rows > (int64_t)1 << 40)
+        return LA_ERR_UNSUPPORTED;
     return LA_OK;
 }
 
@@ -105,7 +106,8 @@ la_status la_gated_scan_backward(const void* a, const void* h, const void* dh, i
         return LA_ERR_INVALID_ARG;
     const int C = H * d;
     if (workspace_bytes < gated_workspace_bytes(T, C)) return LA_ERR_WORKSPACE;
-    const size_t n = (size_t)T * C, na = n * esize(a_dtype), nx = n * esize(dtype), ns = sizeof(float) * (size_t)nseq * C;
+    const size_t n = (size_t)T * C, na = n * esize(a_dtype), nx = n * esize(dtype);
+    const size_t ns = sizeof(float) * (size_t)nseq * C;
     const Span out[] = {{da, na}, {db, nx}, {dstate_in, ns}, {workspace, gated_workspace_bytes(T, C)}};
     const Span in[] = {{a, na}, {h, nx}, {dh, nx}, {state_in, ns}, {dstate_out == dstate_in ? nullptr : dstate_out, ns},
                        {cu_seqlens, sizeof(int32_t) * ((size_t)nseq + 1)}};

@@ -12,6 +12,9 @@
 // turn and store.  A thread's unit of work is N neighbouring channels and, where
 // pairs are halves, their N partners; N channels are 16 bytes where every row
 // allows it, else one pair is the unit.
+//
+// Measured (GB300, 6.76 TB/s copies): q and k of 65536 x 16 x 64 in bf16 82 us, 6.6 TB/s (32768 x 16 x 64 in
+// fp32 80 us); 4099 x 7 x 83 in fp32, pair by pair, 15 us, 2.6 TB/s.
 #include "ops/ops.h"
 #include "ops/vec.cuh"
 

@@ -429,6 +429,20 @@ def test_layer_norm_no_rows_and_missing_gradients(la):
         assert torch.equal(db, full[2]) if keep[1] else bool((db == 3.0).all())
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_layer_norm_gradients_without_a_weight(la, dtype):
+    x, w, b, dy = _norm_inputs((30, 2), 64, dtype, 31, True)
+    _, mean, rstd = la.la_layer_norm(x, return_stats=True)
+    full = la.la_layer_norm_backward(x, dy, mean, rstd, torch.ones_like(w))    # a product with 1 is exact
+    dx, dw, db = la.la_layer_norm_backward(x, dy, mean, rstd)
+    # rows are given out by the groups of the weight, which change no row's own sums
+    assert dw is None and db is None and torch.equal(dx, full[0])
+    dx, dw, db = la.la_layer_norm_backward(x, dy, mean, rstd, dbias=torch.full_like(b, 9.0))
+    assert all(torch.equal(p, q) for p, q in zip((dx, dw, db), full))
+    with pytest.raises(ValueError):
+        la.la_layer_norm_backward(x, dy, mean, rstd, dweight=torch.empty(3, 64, device="cuda"))
+
+
 def test_layer_norm_refuses(la):
     x, w, b, dy = _norm_inputs((6, 2), 64, "bf16", 32, True)
     y, mean, rstd = la.la_layer_norm(x, w, b, return_stats=True)
