@@ -33,11 +33,16 @@ namespace {
 constexpr int kSms = 152;
 constexpr int kHeldValues = 16;         // forward: weights and biases of so many columns a lane stay in registers
 constexpr int kCopyBytes = 64 * 1024;   // of rows copied ahead, per SM
+constexpr int kShiftRegisters = 8;      // for where in its vectors a row starts and ends
 constexpr int kJoinCols = 8, kJoinRows = 32;
 
-template <int L_, int E_, int N_>
+// Shift: rows that do not start on 16 bytes (in arrays that do) are taken as the vectors that hold them.  A row
+// group's rows are a whole number of vectors apart, so its offset in the first vector, and with it the columns of
+// each lane, stay the same on every turn.
+template <int L_, int E_, int N_, bool Shift_ = false>
 struct Shape {
     static constexpr int L = L_, E = E_, N = N_;
+    static constexpr bool kShift = Shift_;
     static constexpr int kThreads = L > 32 ? L : 256;
     static constexpr int kRows = kThreads / L;              // row groups of a block
     static constexpr int kValues = E * N;                   // values a lane holds of a row
@@ -68,7 +73,8 @@ struct Ahead {
 template <typename T, typename S>
 struct ForwardPlan {
     static constexpr int U = S::E == 1 ? 2 : 1;
-    static constexpr int registers = U * row_registers<T, S>() + (S::kValues <= kHeldValues ? 2 * S::kValues + 38 : 52);
+    static constexpr int registers = U * row_registers<T, S>() + (S::kShift ? kShiftRegisters : 0) +
+                                     (S::kValues <= kHeldValues ? 2 * S::kValues + 38 : 52);
     static constexpr int by_registers = blocks_per_sm(S::kThreads, registers);
     using A = Ahead<T, S, U, 1, by_registers>;
     static constexpr int by_memory = 227 * 1024 / ((int)A::bytes + 2048);
@@ -78,8 +84,9 @@ template <typename T, typename S>
 struct BackwardPlan {
     static constexpr bool held = S::kValues <= 8;           // xh and w dy of U rows stay in registers
     static constexpr int U = held ? 2 : 1;
-    static constexpr int registers = held ? (2 * U + 3) * S::kValues + 40
-                                          : 2 * row_registers<T, S>() + 3 * S::kValues + 44;
+    static constexpr int registers = (held ? (2 * U + 3) * S::kValues + 40
+                                           : 2 * row_registers<T, S>() + 3 * S::kValues + 44) +
+                                     (S::kShift ? kShiftRegisters : 0);
     static constexpr int by_registers = blocks_per_sm(S::kThreads, registers);
     using A = Ahead<T, S, U, 2, by_registers>;
     static constexpr int by_memory = 227 * 1024 / ((int)A::bytes + 2048);
@@ -127,14 +134,16 @@ __device__ __forceinline__ void row_sums(float (&x)[U], float* scratch, int turn
         for (int u = 0; u < U; ++u) x[u] = warps_sum<kWarps>(lane, [&](int w) { return half[u * kWarps + w]; });
     }
 }
-// Of the d columns of a row, those that warp w of a block holds.
+// Of the d columns of a row, those that warp w of a block holds; the row starts at element `shift` of its
+// first vector.
 template <typename S>
-__device__ __forceinline__ int warp_columns(int w, int d) {
+__device__ __forceinline__ int warp_columns(int w, int d, int shift) {
     int n = 0;
 #pragma unroll
     for (int e = 0; e < S::E; ++e) {
-        const int rest = d - (e * S::L + w * 32) * S::N;
-        n += rest < 0 ? 0 : rest > 32 * S::N ? 32 * S::N : rest;
+        const int start = (e * S::L + w * 32) * S::N - shift, end = start + 32 * S::N;
+        const int a = S::kShift && start < 0 ? 0 : start, b = end < d ? end : d;
+        n += b > a ? b - a : 0;
     }
     return n;
 }
@@ -142,16 +151,27 @@ __device__ __forceinline__ int warp_columns(int w, int d) {
 // The lane's E vectors of a row, which `row` points into at the lane's first column; vector e lies e L N
 // columns on and is there when that is below `left`, the columns from the lane's first on.  In shared
 // memory vector e of a row has the place of this thread in a run of kThreads.
+// `end`: of the array; its last vector may be there in part.
 template <typename S, typename T>
-__device__ __forceinline__ void copy_row(uint4* place, const T* row, int left) {
+__device__ __forceinline__ void copy_row(uint4* place, const T* row, int left, const T* end) {
 #pragma unroll
     for (int e = 0; e < S::E; ++e) {
         constexpr int kStep = S::L * S::N;
-        if (e * kStep < left) copy_16(place + e * S::kThreads, row + e * kStep);
+        if (e * kStep >= left) continue;
+        if (!S::kShift || row + e * kStep + S::N <= end) {
+            copy_16(place + e * S::kThreads, row + e * kStep);
+        } else {
+#pragma unroll 1
+            for (int k = 0; k < S::N; ++k)
+                reinterpret_cast<T*>(place + e * S::kThreads)[k] =
+                    row + e * kStep + k < end ? row[e * kStep + k] : T(0.f);
+        }
     }
 }
+// Elements of a vector outside the row, `before` of the lane's first vector among them, count as zeros.
 template <typename S, typename T>
-__device__ __forceinline__ void load_row(Vec<T, S::N> (&x)[S::E], const uint4* place, const T* row, int left) {
+__device__ __forceinline__ void load_row(Vec<T, S::N> (&x)[S::E], const uint4* place, const T* row, int left,
+                                         int before) {
 #pragma unroll
     for (int e = 0; e < S::E; ++e) {
         constexpr int kStep = S::L * S::N;
@@ -163,6 +183,15 @@ __device__ __forceinline__ void load_row(Vec<T, S::N> (&x)[S::E], const uint4* p
             pack(x[e], zero);
         }
     }
+    if (S::kShift)
+#pragma unroll
+        for (int e = 0; e < S::E; ++e) {
+            const int there = left - e * S::L * S::N, skip = e == 0 ? before : 0;
+            if (skip <= 0 && there >= S::N) continue;
+#pragma unroll
+            for (int k = 0; k < S::N; ++k)
+                if (k < skip || k >= there) clear_element(x[e], k);
+        }
 }
 
 // A vector of weights or biases; `missing` where there are none.  Vectors of columns come with 16-byte
@@ -189,17 +218,68 @@ __device__ __forceinline__ void load_params(typename S::P* w, const float* p, fl
 #pragma unroll
     for (int k = 0; k < S::n; ++k) w[k] = f[k];
 }
-// The lane's parameters of a whole row, `p` at its first column.
+// The same one by one, of columns in [before, left) of the vector; zero in the others.
 template <typename S>
-__device__ __forceinline__ void load_row_params(typename S::P (&w)[S::kPairs], const float* p, int left,
+__device__ __forceinline__ void load_params_within(typename S::P* w, const float* p, float missing, int before,
+                                                   int left) {
+    Vec<float, S::N> v;
+#pragma unroll
+    for (int k = 0; k < S::N; ++k) v.v[k] = k >= before && k < left ? (p ? p[k] : missing) : 0.f;
+    typename S::P f[S::n];
+    unpack_pairs<S::N>(f, v);
+#pragma unroll
+    for (int k = 0; k < S::n; ++k) w[k] = f[k];
+}
+// Vector e of the lane's parameters, `p` at the lane's first column of the row.
+template <typename S>
+__device__ __forceinline__ void load_vector_params(typename S::P* w, const float* p, int e, int left, int before,
+                                                   float missing) {
+    const int at = e * S::L * S::N;
+    if constexpr (S::kShift) load_params_within<S>(w, p ? p + at : nullptr, missing, e == 0 ? before : 0, left - at);
+    else load_params<S>(w, p && at < left ? p + at : nullptr, missing);
+}
+// The lane's parameters of a whole row.
+template <typename S>
+__device__ __forceinline__ void load_row_params(typename S::P (&w)[S::kPairs], const float* p, int left, int before,
                                                 float missing) {
 #pragma unroll
-    for (int e = 0; e < S::E; ++e) {
-        constexpr int kStep = S::L * S::N;
-        load_params<S>(w + e * S::n, p && e * kStep < left ? p + e * kStep : nullptr, missing);
+    for (int e = 0; e < S::E; ++e) load_vector_params<S>(w + e * S::n, p, e, left, before, missing);
+}
+// f + minus for vector e of a row; outside the row zeros stay zeros.
+template <typename S>
+__device__ __forceinline__ void deviations(typename S::P (&f)[S::n], typename S::P minus, int e, int left, int before) {
+    const int there = left - e * S::L * S::N, skip = e == 0 ? before : 0;
+    if (S::kShift && (skip > 0 || there < S::N)) {
+        Vec<float, S::N> m;
+#pragma unroll
+        for (int k = 0; k < S::N; ++k) m.v[k] = k >= skip && k < there ? 1.f : 0.f;
+        typename S::P in[S::n];
+        unpack_pairs<S::N>(in, m);
+#pragma unroll
+        for (int k = 0; k < S::n; ++k) f[k] = pfma(minus, in[k], f[k]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < S::n; ++k) f[k] = padd(f[k], minus);
+    }
+}
+// Stores vector e of a row at `to`; of one that lies in the row in part, the elements that do.
+template <typename S, typename T>
+__device__ __forceinline__ void store_vector(T* to, const Vec<T, S::N>& v, int e, int left, int before) {
+    const int there = left - e * S::L * S::N, skip = e == 0 ? before : 0;
+    if (!S::kShift || (skip <= 0 && there >= S::N)) {
+        *reinterpret_cast<Vec<T, S::N>*>(to) = v;
+    } else {
+#pragma unroll
+        for (int k = 0; k < S::N; ++k)
+            if (k >= skip && k < there) to[k] = element(v, k);
     }
 }
 __device__ __forceinline__ const float* row_of(const float* p, int64_t at) { return p ? p + at : nullptr; }
+// The first element of row `row` within its 16 bytes.
+template <typename S>
+__device__ __forceinline__ int shift_of(int64_t row, int d) {
+    return S::kShift ? (int)((uint64_t)row * (uint64_t)d % S::N) : 0;
+}
 
 // 1 / sqrt(v), within one step: the approximate root and one step of Newton's method (0 and infinity
 // keep the root's answer).
@@ -217,9 +297,7 @@ __device__ __forceinline__ float mean_of(float s, float d, float over_d) {
 struct Rows {
     int mine, most;
 };
-template <typename S>
-__device__ __forceinline__ Rows rows_of(int64_t rows, int64_t stride, int64_t first) {
-    const int64_t block = (int64_t)blockIdx.x * S::kRows;
+__device__ __forceinline__ Rows rows_of(int64_t rows, int64_t stride, int64_t first, int64_t block) {
     return {first < rows ? (int)((rows - 1 - first) / stride) + 1 : 0,
             block < rows ? (int)((rows - 1 - block) / stride) + 1 : 0};
 }
@@ -235,8 +313,9 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
     constexpr int kWarps = S::L / 32;
     __shared__ float2 scratch[kBlock ? 2 * U * kWarps : 1];
     extern __shared__ uint4 ahead[];                         // [depth][U][E][kThreads]
-    const int lane = threadIdx.x % S::L, col = lane * S::N, left = d - col;
     const int64_t first = (int64_t)blockIdx.x * S::kRows + threadIdx.x / S::L, step = stride * d;
+    const int shift = shift_of<S>(first, d);
+    const int lane = threadIdx.x % S::L, col = lane * S::N - shift, left = d - col, before = -col;
     const float fd = (float)d, over_d = 1.f / fd;
     // the group's weights stay where the registers allow it
     constexpr bool kHeld = S::kValues <= kHeldValues;
@@ -244,11 +323,11 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
     P w[S::kPairs], b[S::kPairs];
     const int64_t at = first % groups * d + col;
     if (kHeld) {
-        load_row_params<S>(w, row_of(weight, at), left, 1.f);
-        load_row_params<S>(b, row_of(bias, at), left, 0.f);
+        load_row_params<S>(w, row_of(weight, at), left, before, 1.f);
+        load_row_params<S>(b, row_of(bias, at), left, before, 0.f);
     }
     uint4* mine = ahead + threadIdx.x;
-    const Rows have = rows_of<S>(rows, stride, first);
+    const Rows have = rows_of(rows, stride, first, (int64_t)blockIdx.x * S::kRows);
     const T* next_x = x + first * d + col;                   // of the turn to copy, or to load
     T* next_y = y + first * d + col;
     int64_t row = first;
@@ -257,7 +336,8 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (turn * U + u < have.mine)
-                    copy_row<S, T>(mine + ((turn % A::depth) * U + u) * S::E * S::kThreads, next_x + u * step, left);
+                    copy_row<S, T>(mine + ((turn % A::depth) * U + u) * S::E * S::kThreads, next_x + u * step, left,
+                                   x + rows * d);
             copies_done();
             next_x += U * step;
         }
@@ -272,7 +352,7 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
 #pragma unroll
         for (int u = 0; u < U; ++u)
             load_row<S, T>(v[u], A::on ? mine + ((turn % A::depth) * U + u) * S::E * S::kThreads : nullptr,
-                           next_x + u * step, turn * U + u < have.mine ? left : 0);
+                           next_x + u * step, turn * U + u < have.mine ? left : 0, before);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             P t = psplat<P>(0.f);
@@ -291,7 +371,7 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
             for (int e = 0; e < S::E; ++e) keep_packed(v[u][e]);
         // deviations from the mean, of the warp's own columns where a row takes several warps
         float mean_here[U];
-        const float columns = kBlock ? (float)warp_columns<S>(threadIdx.x >> 5, d) : fd;
+        const float columns = kBlock ? (float)warp_columns<S>(threadIdx.x >> 5, d, shift) : fd;
         const float over_columns = kBlock ? 1.f / fmaxf(columns, 1.f) : over_d;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -303,11 +383,9 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
                 if (e * S::L * S::N < left) {
                     P f[S::n];
                     unpack_pairs<S::N>(f, v[u][e]);
+                    deviations<S>(f, minus, e, left, before);
 #pragma unroll
-                    for (int k = 0; k < S::n; ++k) {
-                        f[k] = padd(f[k], minus);
-                        t = pfma(f[k], f[k], t);
-                    }
+                    for (int k = 0; k < S::n; ++k) t = pfma(f[k], f[k], t);
                 }
             q[u] = lane_sum<kBlock ? 32 : S::L>(psum(t));
         }
@@ -325,7 +403,7 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
                 mean_here[u] = mean_of(all, fd, over_d);
                 q[u] = warps_sum<kWarps>(wl, [&](int w) {
                     const float2 o = half[u * kWarps + w];
-                    const float n = (float)warp_columns<S>(w, d), off = n > 0.f ? o.x / n - mean_here[u] : 0.f;
+                    const float n = (float)warp_columns<S>(w, d, shift), off = n > 0.f ? o.x / n - mean_here[u] : 0.f;
                     return fmaf(n * off, off, o.y);
                 });
             }
@@ -348,8 +426,8 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
                 P f[S::n], we[S::n], be[S::n];
                 unpack_pairs<S::N>(f, v[u][e]);
                 if (!kHeld) {
-                    load_params<S>(we, row_of(weight, at + e * kStep), 1.f);
-                    load_params<S>(be, row_of(bias, at + e * kStep), 0.f);
+                    load_vector_params<S>(we, row_of(weight, at), e, left, before, 1.f);
+                    load_vector_params<S>(be, row_of(bias, at), e, left, before, 0.f);
                 }
 #pragma unroll
                 for (int k = 0; k < S::n; ++k)
@@ -357,7 +435,7 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
                                 kHeld ? b[e * S::n + k] : be[k]);
                 Vec<T, S::N> o;
                 pack_pairs<S::N>(o, f);
-                *reinterpret_cast<Vec<T, S::N>*>(next_y + u * step + e * kStep) = o;
+                store_vector<S>(next_y + u * step + e * kStep, o, e, left, before);
             }
             if (lane == 0) {
                 if (mean) mean[row + u * stride] = mu;
@@ -371,29 +449,33 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
 }
 
 // part[slot][d]: the weight and bias gradients of one weight row over some rows, slot i of weight row
-// i mod groups.  Row groups of a block that share a weight row are added up first where every one of
-// its weight rows has equally many (kRows a multiple of groups).
+// i mod groups.  A block has `weights` weight rows, and its row groups add up their sums of each first.  weights
+// is kRows (nothing to add up), groups, or 1: then the block's rows lie `groups` apart.
 template <typename T, typename S>
 __global__ void __launch_bounds__(S::kThreads, BackwardPlan<T, S>::by_registers)
 layer_norm_backward_kernel(const T* x, const T* dy, const float* weight, const float* mean, const float* rstd,
-                           int64_t rows, int groups, int d, T* dx, float2* part, int64_t stride) {
+                           int64_t rows, int groups, int d, T* dx, float2* part, int64_t stride, int weights) {
     constexpr int U = BackwardPlan<T, S>::U;
     using A = typename BackwardPlan<T, S>::A;
     __shared__ float scratch[S::L > 32 ? 4 * U * S::L / 32 : 1];
     extern __shared__ uint4 ahead[];                        // [depth][U][x, dy][E][kThreads]
     float2* sums = reinterpret_cast<float2*>(ahead);        // afterwards [kRows][d], L <= 32
     uint4* mine = ahead + threadIdx.x;
-    const int lane = threadIdx.x % S::L, group = threadIdx.x / S::L, col = lane * S::N, left = d - col;
-    const int64_t first = (int64_t)blockIdx.x * S::kRows + group, step = stride * d;
+    const int group = threadIdx.x / S::L, lane = threadIdx.x % S::L;
+    const bool apart = S::kRows > 1 && weights == 1;         // (and for one weight row either is the same)
+    const int64_t block = apart ? (int64_t)(blockIdx.x / groups) * groups * S::kRows + blockIdx.x % groups
+                                : (int64_t)blockIdx.x * S::kRows;
+    const int64_t first = block + (apart ? (int64_t)group * groups : group), step = stride * d;
+    const int shift = shift_of<S>(first, d), col = lane * S::N - shift, left = d - col, before = -col;
     const float over_d = 1.f / d;
     constexpr bool kHeld = S::kValues <= 8;
     const int64_t at = first % groups * d + col;            // stride is a multiple of groups
     using P = typename S::P;
     P w[S::kPairs], dw[S::kPairs], db[S::kPairs];
-    if (kHeld) load_row_params<S>(w, row_of(weight, at), left, 1.f);
+    if (kHeld) load_row_params<S>(w, row_of(weight, at), left, before, 1.f);
 #pragma unroll
     for (int k = 0; k < S::kPairs; ++k) dw[k] = db[k] = psplat<P>(0.f);
-    const Rows have = rows_of<S>(rows, stride, first);
+    const Rows have = rows_of(rows, stride, first, block);
     auto place = [&](int turn, int u, int array) {
         return mine + (((turn % A::depth) * U + u) * 2 + array) * S::E * S::kThreads;
     };
@@ -405,8 +487,8 @@ layer_norm_backward_kernel(const T* x, const T* dy, const float* weight, const f
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (turn * U + u < have.mine) {
-                    copy_row<S, T>(place(turn, u, 0), next_x + u * step, left);
-                    copy_row<S, T>(place(turn, u, 1), next_dy + u * step, left);
+                    copy_row<S, T>(place(turn, u, 0), next_x + u * step, left, x + rows * d);
+                    copy_row<S, T>(place(turn, u, 1), next_dy + u * step, left, dy + rows * d);
                 }
             copies_done();
             next_x += U * step;
@@ -435,13 +517,13 @@ layer_norm_backward_kernel(const T* x, const T* dy, const float* weight, const f
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int there = turn * U + u < have.mine ? left : 0;
-            load_row<S, T>(v[u], A::on ? place(turn, u, 0) : nullptr, next_x + u * step, there);
-            load_row<S, T>(g[u], A::on ? place(turn, u, 1) : nullptr, next_dy + u * step, there);
+            load_row<S, T>(v[u], A::on ? place(turn, u, 0) : nullptr, next_x + u * step, there, before);
+            load_row<S, T>(g[u], A::on ? place(turn, u, 1) : nullptr, next_dy + u * step, there, before);
             mu[u] = ahead_mu[u];
             rs[u] = ahead_rs[u];
         }
         load_stats(turn + 1);
-        if (!kHeld) load_row_params<S>(w, row_of(weight, at), left, 1.f);
+        if (!kHeld) load_row_params<S>(w, row_of(weight, at), left, before, 1.f);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const P minus = psplat<P>(-mu[u]), times = psplat<P>(rs[u]);
@@ -452,10 +534,11 @@ layer_norm_backward_kernel(const T* x, const T* dy, const float* weight, const f
                     P fx[S::n], fg[S::n];
                     unpack_pairs<S::N>(fx, v[u][e]);
                     unpack_pairs<S::N>(fg, g[u][e]);
+                    deviations<S>(fx, minus, e, left, before);
 #pragma unroll
                     for (int k = 0; k < S::n; ++k) {
                         const int i = e * S::n + k;
-                        const P xh = pmul(padd(fx[k], minus), times), t = pmul(fg[k], w[i]);
+                        const P xh = pmul(fx[k], times), t = pmul(fg[k], w[i]);
                         s1 = padd(s1, t);
                         s2 = pfma(t, xh, s2);
                         dw[i] = pfma(fg[k], xh, dw[i]);
@@ -501,7 +584,7 @@ layer_norm_backward_kernel(const T* x, const T* dy, const float* weight, const f
                 }
                 Vec<T, S::N> out;
                 pack_pairs<S::N>(out, o);
-                *reinterpret_cast<Vec<T, S::N>*>(next_dx + u * step + e * kStep) = out;
+                store_vector<S>(next_dx + u * step + e * kStep, out, e, left, before);
             }
         }
         if (!A::on) {
@@ -528,32 +611,34 @@ layer_norm_backward_kernel(const T* x, const T* dy, const float* weight, const f
 #pragma unroll
         for (int k = 0; k < S::N; ++k) bv[e * S::N + k] = q.v[k];
     }
-    if (S::kRows > 1 && S::kRows % groups == 0) {
+    if (weights < S::kRows) {
         __syncthreads();                                    // the copies' places are free
 #pragma unroll
         for (int e = 0; e < S::E; ++e)
 #pragma unroll
             for (int k = 0; k < S::N; ++k) {
-                const int c = (e * S::L + lane) * S::N + k;
-                if (c < d) sums[group * d + c] = make_float2(wv[e * S::N + k], bv[e * S::N + k]);
+                const int c = e * S::L * S::N + col + k;
+                if ((!S::kShift || c >= 0) && c < d)
+                    sums[group * d + c] = make_float2(wv[e * S::N + k], bv[e * S::N + k]);
             }
         __syncthreads();
-        for (int i = threadIdx.x; i < groups * d; i += S::kThreads) {
+        for (int i = threadIdx.x; i < weights * d; i += S::kThreads) {
             float2 t = sums[i];
-            for (int r = groups; r < S::kRows; r += groups) {
+            for (int r = weights; r < S::kRows; r += weights) {
                 const float2 q = sums[r * d + i];
                 t.x += q.x;
                 t.y += q.y;
             }
-            part[(int64_t)blockIdx.x * groups * d + i] = t;
+            part[(int64_t)blockIdx.x * weights * d + i] = t;
         }
     } else {
 #pragma unroll
         for (int e = 0; e < S::E; ++e)
 #pragma unroll
             for (int k = 0; k < S::N; ++k) {
-                const int c = (e * S::L + lane) * S::N + k;
-                if (c < d) part[first * d + c] = make_float2(wv[e * S::N + k], bv[e * S::N + k]);
+                const int c = e * S::L * S::N + col + k;
+                if ((!S::kShift || c >= 0) && c < d)
+                    part[first * d + c] = make_float2(wv[e * S::N + k], bv[e * S::N + k]);
             }
     }
 }
@@ -626,19 +711,36 @@ struct Args {
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
-// As many blocks as there are rows for, at most those that run at once, rounded up so that a block's
-// row groups meet the same weight rows on every turn.
+// As many blocks as there are rows for, at most those that run at once (a few more would take as long again), a
+// multiple of `unit`.
 template <typename Plan, typename S>
-int64_t blocks_for(int64_t rows, int groups) {
+int64_t blocks_for(int64_t rows, int64_t unit) {
+    const int64_t most = (int64_t)kSms * Plan::per_sm, wanted = rows > S::kRows ? ceil_div(rows, S::kRows) : 1;
+    const int64_t blocks = ceil_div(wanted, unit) * unit;
+    return blocks <= most ? blocks : most >= unit ? most / unit * unit : unit;
+}
+int64_t lcm(int64_t a, int b) { return a / gcd((int)(a % b), b) * b; }
+// A block's row groups meet the same weight rows on every turn, and rows with the same shift.
+template <typename S>
+int64_t whole_turns(int groups, int d) {
     const int64_t unit = groups / gcd(groups, S::kRows);
-    const int64_t blocks = min64(ceil_div(rows, S::kRows), (int64_t)kSms * Plan::per_sm);
-    return ceil_div(blocks > 0 ? blocks : 1, unit) * unit;
+    return S::kShift ? lcm(unit, S::N / gcd(S::N, S::kRows * (d % S::N))) : unit;
+}
+// Weight rows of a block of the backward (see the kernel).
+template <typename Plan, typename S>
+int weights_of_block(int groups) {
+    if (S::kRows % groups == 0) return groups;
+    return groups <= kSms * Plan::per_sm ? 1 : S::kRows;
+}
+template <typename Plan, typename S>
+int64_t backward_blocks(int64_t rows, int groups, int d) {
+    const int64_t unit = whole_turns<S>(groups, d);
+    return blocks_for<Plan, S>(rows, weights_of_block<Plan, S>(groups) == 1 ? lcm(unit, groups) : unit);
 }
 // Rows of the matrix of partial sums.
 template <typename Plan, typename S>
-int64_t slots(int64_t rows, int groups) {
-    const int64_t per_block = S::kRows > 1 && S::kRows % groups == 0 ? groups : S::kRows;
-    return rows > 0 ? blocks_for<Plan, S>(rows, groups) * per_block / groups : 0;
+int64_t slots(int64_t rows, int groups, int d) {
+    return rows > 0 ? backward_blocks<Plan, S>(rows, groups, d) * weights_of_block<Plan, S>(groups) / groups : 0;
 }
 
 template <typename K>
@@ -652,7 +754,7 @@ struct Forward {
     template <typename T, typename S>
     static int64_t run(const Args& a) {
         using Plan = ForwardPlan<T, S>;
-        const int64_t blocks = blocks_for<Plan, S>(a.rows, a.groups);
+        const int64_t blocks = blocks_for<Plan, S>(a.rows, whole_turns<S>(a.groups, a.d));
         const cudaError_t e = allow_shared(layer_norm_kernel<T, S>, Plan::A::bytes);
         if (e != cudaSuccess) return (int64_t)e;
         layer_norm_kernel<T, S><<<(unsigned)blocks, S::kThreads, Plan::A::bytes, a.stream>>>(
@@ -666,49 +768,56 @@ struct Backward {
     template <typename T, typename S>
     static int64_t run(const Args& a) {
         using Plan = BackwardPlan<T, S>;
-        const int64_t blocks = blocks_for<Plan, S>(a.rows, a.groups);
-        const bool reduce = a.part && S::kRows > 1 && S::kRows % a.groups == 0;
-        const size_t join = reduce ? sizeof(float2) * S::kRows * (size_t)a.d : 0;
+        const int64_t blocks = backward_blocks<Plan, S>(a.rows, a.groups, a.d);
+        const int weights = weights_of_block<Plan, S>(a.groups);
+        const size_t join = a.part && weights < S::kRows ? sizeof(float2) * S::kRows * (size_t)a.d : 0;
         const size_t smem = join > Plan::A::bytes ? join : Plan::A::bytes;
         const cudaError_t e = allow_shared(layer_norm_backward_kernel<T, S>, smem);
         if (e != cudaSuccess) return (int64_t)e;
         layer_norm_backward_kernel<T, S><<<(unsigned)blocks, S::kThreads, smem, a.stream>>>(
             static_cast<const T*>(a.x), static_cast<const T*>(a.dy), a.weight, a.mean_in, a.rstd_in, a.rows, a.groups,
-            a.d, static_cast<T*>(a.out), a.part, blocks * S::kRows);
+            a.d, static_cast<T*>(a.out), a.part, blocks * S::kRows, weights);
         return (int64_t)cudaGetLastError();
     }
 };
 struct Slots {
     static constexpr bool kForward = false;
     template <typename T, typename S>
-    static int64_t run(const Args& a) { return slots<BackwardPlan<T, S>, S>(a.rows, a.groups); }
+    static int64_t run(const Args& a) { return slots<BackwardPlan<T, S>, S>(a.rows, a.groups, a.d); }
 };
 
 // The lanes and vectors of a row.  One vector a lane, or two where the forward has bf16 rows (half the
 // lanes: the sums across lanes are most of its instructions; 27 us instead of 31 for 8192 x 4096.  The
 // backward's sums per column leave no room for two: 59 us instead of 48).  Up to 64 vectors share a
 // warp, two a lane from 32 on, longer rows take a block of up to 512 lanes.
-template <typename Op, typename T>
-int64_t by_shape(const Args& a, bool aligned) {
+// Rows that are not whole vectors: by the vectors that hold them (16384 x 1001 in bf16: 23 us, element by
+// element 33 us; 4096 x 5001 39 and 76 us, its gradients 68 and 171 us).  Element by element only where an array does not start on 16 bytes.
+enum RowLayout { kElements, kShifted, kVectors };
+
+template <typename Op, typename T, bool Shift>
+int64_t by_vectors(const Args& a, int n) {
     constexpr int N = 16 / sizeof(T), E = Op::kForward && N == 8 ? 2 : 1;
-    const int d = a.d;
-    if (aligned && d % N == 0) {
-        const int n = d / N;
-        if (n <= 4) return Op::template run<T, Shape<4, 1, N>>(a);
-        if (n <= 8) return Op::template run<T, Shape<8 / E, E, N>>(a);
-        if (n <= 16) return Op::template run<T, Shape<16 / E, E, N>>(a);
-        if (n <= 32) return Op::template run<T, Shape<32 / E, E, N>>(a);
-        if (n <= 64) return Op::template run<T, Shape<32, 2, N>>(a);
-        if (n <= 128) return Op::template run<T, Shape<128 / E, E, N>>(a);
-        if (n <= 192) return Op::template run<T, Shape<192 / E, E, N>>(a);
-        if (n <= 256) return Op::template run<T, Shape<256 / E, E, N>>(a);
-        if (n <= 384) return Op::template run<T, Shape<384 / E, E, N>>(a);
-        if (n <= 512) return Op::template run<T, Shape<512 / E, E, N>>(a);
-        if (n <= 1024) return Op::template run<T, Shape<512, 2, N>>(a);
-        if (n <= 2048) return Op::template run<T, Shape<512, 4, N>>(a);
-        if constexpr (N == 4) return Op::template run<T, Shape<512, 8, N>>(a);
-        return (int64_t)cudaErrorInvalidValue;      // d <= LA_MAX_NORM_D: not reached
-    }
+    if (n <= 4) return Op::template run<T, Shape<4, 1, N, Shift>>(a);
+    if (n <= 8) return Op::template run<T, Shape<8 / E, E, N, Shift>>(a);
+    if (n <= 16) return Op::template run<T, Shape<16 / E, E, N, Shift>>(a);
+    if (n <= 32) return Op::template run<T, Shape<32 / E, E, N, Shift>>(a);
+    if (n <= 64) return Op::template run<T, Shape<32, 2, N, Shift>>(a);
+    if (n <= 128) return Op::template run<T, Shape<128 / E, E, N, Shift>>(a);
+    if (n <= 192) return Op::template run<T, Shape<192 / E, E, N, Shift>>(a);
+    if (n <= 256) return Op::template run<T, Shape<256 / E, E, N, Shift>>(a);
+    if (n <= 384) return Op::template run<T, Shape<384 / E, E, N, Shift>>(a);
+    if (n <= 512) return Op::template run<T, Shape<512 / E, E, N, Shift>>(a);
+    if (n <= 1024) return Op::template run<T, Shape<512, 2, N, Shift>>(a);
+    if (n <= 2048) return Op::template run<T, Shape<512, 4, N, Shift>>(a);
+    if constexpr (N == 4) return Op::template run<T, Shape<512, 8, N, Shift>>(a);
+    return (int64_t)cudaErrorInvalidValue;      // d <= LA_MAX_NORM_D: not reached
+}
+template <typename Op, typename T>
+int64_t by_shape(const Args& a, RowLayout layout) {
+    constexpr int N = 16 / sizeof(T);
+    const int d = a.d, shifted = (d + 2 * N - 2) / N;      // vectors that hold a row, wherever it starts
+    if (layout == kVectors && d % N == 0) return by_vectors<Op, T, false>(a, d / N);
+    if (layout != kElements && shifted <= LA_MAX_NORM_D / N) return by_vectors<Op, T, true>(a, shifted);
     if (d <= 32) return Op::template run<T, Shape<32, 1, 1>>(a);
     if (d <= 128) return Op::template run<T, Shape<32, 4, 1>>(a);
     if (d <= 512) return Op::template run<T, Shape<128, 4, 1>>(a);
@@ -717,19 +826,21 @@ int64_t by_shape(const Args& a, bool aligned) {
     return Op::template run<T, Shape<512, 32, 1>>(a);
 }
 template <typename Op>
-int64_t by_type(const Args& a, int dtype, bool aligned) {
-    return dtype == LA_F32 ? by_shape<Op, float>(a, aligned) : by_shape<Op, __nv_bfloat16>(a, aligned);
+int64_t by_type(const Args& a, int dtype, RowLayout layout) {
+    return dtype == LA_F32 ? by_shape<Op, float>(a, layout) : by_shape<Op, __nv_bfloat16>(a, layout);
 }
 
 bool on_16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-int64_t slots_for(int dtype, int64_t rows, int groups, int d, bool aligned) {
+int64_t slots_for(int dtype, int64_t rows, int groups, int d, RowLayout layout) {
     Args a{};
     a.rows = rows;
     a.groups = groups;
     a.d = d;
-    return by_type<Slots>(a, dtype, aligned);
+    return by_type<Slots>(a, dtype, layout);
 }
+// rows: the arrays of rows start on 16 bytes; weights: the arrays of weights too.
+RowLayout layout_of(bool rows, bool weights) { return !rows ? kElements : weights ? kVectors : kShifted; }
 
 }  // namespace
 
@@ -739,30 +850,34 @@ cudaError_t layer_norm(const void* x, const float* weight, const float* bias, in
     a.x = x; a.weight = weight; a.bias = bias;
     a.rows = rows; a.groups = groups; a.d = d; a.eps = eps;
     a.out = y; a.mean = mean; a.rstd = rstd; a.stream = s;
-    return (cudaError_t)by_type<Forward>(a, dtype, on_16(x) && on_16(y) && on_16(weight) && on_16(bias));
+    return (cudaError_t)by_type<Forward>(a, dtype, layout_of(on_16(x) && on_16(y), on_16(weight) && on_16(bias)));
 }
 
-// Covers both layouts of the rows: the choice between them goes by the call's pointers.
+// Covers every layout of the rows: the choice between them goes by the call's pointers.
 size_t layer_norm_backward_workspace_bytes(int dtype, int64_t rows, int groups, int d) {
-    const int64_t v = slots_for(dtype, rows, groups, d, true), e = slots_for(dtype, rows, groups, d, false);
-    return align_up(sizeof(float2) * (size_t)(v > e ? v : e) * groups * d, kAlign) + kAlign;
+    int64_t most = 0;
+    for (RowLayout l : {kElements, kShifted, kVectors}) {
+        const int64_t n = slots_for(dtype, rows, groups, d, l);
+        if (n > most) most = n;
+    }
+    return align_up(sizeof(float2) * (size_t)most * groups * d, kAlign) + kAlign;
 }
 
 cudaError_t layer_norm_backward(const void* x, const void* dy, const float* weight, const float* mean,
                                 const float* rstd, int dtype, int64_t rows, int groups, int d, void* dx,
                                 float* dweight, float* dbias, void* workspace, cudaStream_t s) {
-    const bool aligned = on_16(x) && on_16(dy) && on_16(dx) && on_16(weight);
+    const RowLayout layout = layout_of(on_16(x) && on_16(dy) && on_16(dx), on_16(weight));
     Args a{};
     a.x = x; a.dy = dy; a.weight = weight; a.mean_in = mean; a.rstd_in = rstd;
     a.rows = rows; a.groups = groups; a.d = d;
     a.out = dx; a.stream = s;
     a.part = dweight || dbias ? static_cast<float2*>(workspace) : nullptr;
     if (rows > 0) {
-        const cudaError_t e = (cudaError_t)by_type<Backward>(a, dtype, aligned);
+        const cudaError_t e = (cudaError_t)by_type<Backward>(a, dtype, layout);
         if (e != cudaSuccess) return e;
     }
     if (!a.part) return cudaSuccess;
-    const int64_t n = (int64_t)groups * d, M = rows > 0 ? slots_for(dtype, rows, groups, d, aligned) : 0;
+    const int64_t n = (int64_t)groups * d, M = rows > 0 ? slots_for(dtype, rows, groups, d, layout) : 0;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

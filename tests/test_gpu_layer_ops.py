@@ -430,6 +430,42 @@ def test_layer_norm_no_rows_and_missing_gradients(la):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,H,d", [(9, 1, 1), (40, 3, 5), (37, 2, 7), (300, 7, 33), (77, 5, 129), (31, 1, 515), (19, 3, 1030),
+                                      (401, 1, 2051), (6, 2, 4097), (3, 1, 9001), (2, 1, 16383)])
+def test_layer_norm_rows_that_start_anywhere(la, rows, H, d, dtype):
+    # arrays on 16 bytes whose rows are not, among neighbours that keep their values
+    x, w, b, dy = _norm_inputs((rows, H), d, dtype, 33, True)
+    n, pad = x.numel(), 64
+    ref, rm, rr = ops.layer_norm(_np(x), _np(w), _np(b), 1e-5)
+
+    def among(t):
+        buf = torch.full((n + 2 * pad,), float("nan"), dtype=t.dtype, device="cuda")
+        buf[pad:pad + n] = t.reshape(-1)
+        return buf, buf[pad:pad + n].view(t.shape)
+
+    (_, xs), (_, dys), (yb, y), (gb, dx) = among(x), among(dy), among(x), among(x)
+    _, mean, rstd = la.la_layer_norm(xs, w, b, return_stats=True, y=y)
+    check(_np(y), ref, layer_norm_bounds(_np(x), _np(w), _np(b), rm, rr, 1e-5)[0], dtype, "y")
+    grads = la.la_layer_norm_backward(xs, dys, mean, rstd, w, dx=dx)
+    refs = ops.layer_norm_backward(_np(x), _np(dy), _np(mean), _np(rstd), _np(w))
+    bounds = layer_norm_backward_bounds(_np(x), _np(dy), _np(mean), _np(rstd), _np(w), min(rows, 256))
+    for g, r, bd, t in zip(grads, refs, bounds, (dtype, "f32", "f32")):
+        check(_np(g), r, bd, t, "gradient")
+    for buf in (yb, gb):
+        assert bool(torch.isnan(buf[:pad]).all()) and bool(torch.isnan(buf[pad + n:]).all())
+
+
+def test_layer_norm_large_constant_rows_of_odd_length(la):
+    # deviations are zero although the mean times rstd is beyond fp32
+    x = torch.full((24, 77), 1e36, device="cuda")
+    w, b = torch.ones(77, device="cuda"), torch.full((77,), 0.5, device="cuda")
+    y, mean, rstd = la.la_layer_norm(x, w, b, eps=1e-12, return_stats=True)
+    assert bool((y == 0.5).all()) and bool((mean == x[0, 0]).all())
+    dx, dw, db = la.la_layer_norm_backward(x, torch.ones_like(x), mean, rstd, w)
+    assert bool((dw == 0.0).all()) and bool((db == 24.0).all()) and bool(torch.isfinite(dx).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_layer_norm_gradients_without_a_weight(la, dtype):
     x, w, b, dy = _norm_inputs((30, 2), 64, dtype, 31, True)
     _, mean, rstd = la.la_layer_norm(x, return_stats=True)
