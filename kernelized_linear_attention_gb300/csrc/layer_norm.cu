@@ -23,6 +23,8 @@
 // per head 31 us, 3.3 TB/s; 8192 x 4096 48 us, 4.2 TB/s.  The backward issues about 24
 // instructions per element, the sums across lanes and the sums per column most of them: that bounds it, with the
 // second kernel's launch and its read of the blocks' sums.
+#include <float.h>
+
 #include "ops/ops.h"
 #include "ops/vec.cuh"
 
@@ -33,7 +35,7 @@ namespace {
 constexpr int kSms = 152;
 constexpr int kHeldValues = 16;         // forward: weights and biases of so many columns a lane stay in registers
 constexpr int kCopyBytes = 64 * 1024;   // of rows copied ahead, per SM
-constexpr int kShiftRegisters = 8;      // for where in its vectors a row starts and ends
+constexpr int kShiftRegisters = 16;      // for where in its vectors a row starts and ends
 constexpr int kJoinCols = 8, kJoinRows = 32;
 
 // Shift: rows that do not start on 16 bytes (in arrays that do) are taken as the vectors that hold them.  A row
@@ -67,7 +69,7 @@ struct Ahead {
     static constexpr int turn_bytes = U * Arrays * S::E * S::kThreads * 16;
     static constexpr int most = kCopyBytes / Blocks / turn_bytes;
     static constexpr int depth = most > 8 ? 8 : most >= 2 ? most : 2 * turn_bytes <= 200 * 1024 ? 2 : 1;
-    static constexpr size_t bytes = on ? (size_t)depth * turn_bytes : 0;
+    static constexpr size_t bytes = on ? (size_t)depth * turn_bytes : 0;   // a multiple of 16
 };
 // The registers to compile for, and the blocks of an SM that this and the copies' memory allow.
 template <typename T, typename S>
@@ -77,8 +79,12 @@ struct ForwardPlan {
                                      (S::kValues <= kHeldValues ? 2 * S::kValues + 38 : 52);
     static constexpr int by_registers = blocks_per_sm(S::kThreads, registers);
     using A = Ahead<T, S, U, 1, by_registers>;
-    static constexpr int by_memory = 227 * 1024 / ((int)A::bytes + 2048);
+    static constexpr size_t parameters = 2 * sizeof(float) * S::kValues * S::kThreads;
+    static constexpr bool staged = S::kShift && S::kValues > kHeldValues && A::bytes + parameters <= 200 * 1024;
+    static constexpr size_t bytes = A::bytes + (staged ? parameters : 0);
+    static constexpr int by_memory = 227 * 1024 / ((int)bytes + 2048);
     static constexpr int per_sm = by_registers < by_memory ? by_registers : by_memory;
+    static_assert(per_sm >= 1, "a block's shared memory");
 };
 template <typename T, typename S>
 struct BackwardPlan {
@@ -89,8 +95,11 @@ struct BackwardPlan {
                                      (S::kShift ? kShiftRegisters : 0);
     static constexpr int by_registers = blocks_per_sm(S::kThreads, registers);
     using A = Ahead<T, S, U, 2, by_registers>;
-    static constexpr int by_memory = 227 * 1024 / ((int)A::bytes + 2048);
+    static constexpr bool staged = S::kShift && !held;
+    static constexpr size_t bytes = A::bytes + (staged ? sizeof(float) * S::kValues * S::kThreads : 0);
+    static constexpr int by_memory = 227 * 1024 / ((int)bytes + 2048);
     static constexpr int per_sm = by_registers < by_memory ? by_registers : by_memory;
+    static_assert(per_sm >= 1, "a block's shared memory");
 };
 
 __device__ __forceinline__ void copy_16(void* to, const void* from) {
@@ -148,6 +157,44 @@ __device__ __forceinline__ int warp_columns(int w, int d, int shift) {
     return n;
 }
 
+// What of a lane's vectors lies in its rows: column `col` of a row is the lane's first (below zero where the
+// vector starts before the row), `left` columns of the row are there from it on.  Masks of the vectors' words (of an
+// fp32, or of two bf16) stay in registers where they are few.
+template <typename S, typename T>
+struct Edges {
+    static constexpr int kWords = S::N * (int)sizeof(T) >= 4 ? S::N * (int)sizeof(T) / 4 : 1, kEach = S::N / kWords;
+    static constexpr bool kKept = S::kShift && S::E <= 2;
+    int left, before;
+    uint32_t masks[kKept ? S::E : 1][kWords];
+
+    __device__ __forceinline__ Edges(int col, int d) : left(d - col), before(-col) {
+        if (kKept)
+#pragma unroll
+            for (int e = 0; e < S::E; ++e)
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) {
+                    masks[e][i] = made(e, i);
+                    asm volatile("" : "+r"(masks[e][i]));      // made once
+                }
+    }
+    __device__ __forceinline__ bool in(int e, int k) const {
+        return k >= (e == 0 ? before : 0) && k < left - e * S::L * S::N;
+    }
+    __device__ __forceinline__ bool partial(int e) const {
+        return S::kShift && ((e == 0 && before > 0) || left - e * S::L * S::N < S::N);
+    }
+    __device__ __forceinline__ uint32_t made(int e, int i) const {
+        if (kEach == 1) return in(e, i) ? 0xffffffffu : 0u;
+        return (in(e, 2 * i) ? 0xffffu : 0u) | (in(e, 2 * i + 1) ? 0xffff0000u : 0u);
+    }
+    __device__ __forceinline__ uint32_t mask(int e, int i) const { return kKept ? masks[e][i] : made(e, i); }
+    // all ones or zero, for element k
+    __device__ __forceinline__ uint32_t whole(int e, int k) const {
+        if (kEach == 1) return mask(e, k);
+        return __byte_perm(mask(e, k / 2), 0, k % 2 ? 0x3232 : 0x1010);
+    }
+};
+
 // The lane's E vectors of a row, which `row` points into at the lane's first column; vector e lies e L N
 // columns on and is there when that is below `left`, the columns from the lane's first on.  In shared
 // memory vector e of a row has the place of this thread in a run of kThreads.
@@ -168,10 +215,10 @@ __device__ __forceinline__ void copy_row(uint4* place, const T* row, int left, c
         }
     }
 }
-// Elements of a vector outside the row, `before` of the lane's first vector among them, count as zeros.
+// Elements of a vector outside the row count as zeros.
 template <typename S, typename T>
 __device__ __forceinline__ void load_row(Vec<T, S::N> (&x)[S::E], const uint4* place, const T* row, int left,
-                                         int before) {
+                                         const Edges<S, T>& edges) {
 #pragma unroll
     for (int e = 0; e < S::E; ++e) {
         constexpr int kStep = S::L * S::N;
@@ -183,15 +230,17 @@ __device__ __forceinline__ void load_row(Vec<T, S::N> (&x)[S::E], const uint4* p
             pack(x[e], zero);
         }
     }
-    if (S::kShift)
+    if constexpr (S::kShift) {
 #pragma unroll
-        for (int e = 0; e < S::E; ++e) {
-            const int there = left - e * S::L * S::N, skip = e == 0 ? before : 0;
-            if (skip <= 0 && there >= S::N) continue;
+        for (int e = 0; e < S::E; ++e)
+            if (Edges<S, T>::kKept || edges.partial(e)) {
 #pragma unroll
-            for (int k = 0; k < S::N; ++k)
-                if (k < skip || k >= there) clear_element(x[e], k);
-        }
+                for (int i = 0; i < Edges<S, T>::kWords; ++i) {
+                    uint32_t* word = reinterpret_cast<uint32_t*>(&x[e].v[i]);
+                    *word &= edges.mask(e, i);
+                }
+            }
+    }
 }
 
 // A vector of weights or biases; `missing` where there are none.  Vectors of columns come with 16-byte
@@ -246,33 +295,36 @@ __device__ __forceinline__ void load_row_params(typename S::P (&w)[S::kPairs], c
     for (int e = 0; e < S::E; ++e) load_vector_params<S>(w + e * S::n, p, e, left, before, missing);
 }
 // f + minus for vector e of a row; outside the row zeros stay zeros.
-template <typename S>
-__device__ __forceinline__ void deviations(typename S::P (&f)[S::n], typename S::P minus, int e, int left, int before) {
-    const int there = left - e * S::L * S::N, skip = e == 0 ? before : 0;
-    if (S::kShift && (skip > 0 || there < S::N)) {
-        Vec<float, S::N> m;
+template <typename S, typename T>
+__device__ __forceinline__ void deviations(typename S::P (&f)[S::n], typename S::P minus, int e,
+                                           const Edges<S, T>& edges) {
 #pragma unroll
-        for (int k = 0; k < S::N; ++k) m.v[k] = k >= skip && k < there ? 1.f : 0.f;
-        typename S::P in[S::n];
-        unpack_pairs<S::N>(in, m);
+    for (int k = 0; k < S::n; ++k) f[k] = padd(f[k], minus);
+    if constexpr (S::kShift) {
+        if (edges.partial(e))
 #pragma unroll
-        for (int k = 0; k < S::n; ++k) f[k] = pfma(minus, in[k], f[k]);
-    } else {
-#pragma unroll
-        for (int k = 0; k < S::n; ++k) f[k] = padd(f[k], minus);
+            for (int k = 0; k < S::n; ++k)
+                f[k] = tc::f32x2_of(__float_as_uint(tc::f32x2_lo(f[k])) & edges.whole(e, 2 * k),
+                                    __float_as_uint(tc::f32x2_hi(f[k])) & edges.whole(e, 2 * k + 1));
     }
 }
 // Stores vector e of a row at `to`; of one that lies in the row in part, the elements that do.
 template <typename S, typename T>
-__device__ __forceinline__ void store_vector(T* to, const Vec<T, S::N>& v, int e, int left, int before) {
-    const int there = left - e * S::L * S::N, skip = e == 0 ? before : 0;
-    if (!S::kShift || (skip <= 0 && there >= S::N)) {
+__device__ __forceinline__ void store_vector(T* to, const Vec<T, S::N>& v, int e, const Edges<S, T>& edges) {
+    if (!edges.partial(e)) {
         *reinterpret_cast<Vec<T, S::N>*>(to) = v;
     } else {
 #pragma unroll
         for (int k = 0; k < S::N; ++k)
-            if (k >= skip && k < there) to[k] = element(v, k);
+            if (edges.whole(e, k)) to[k] = element(v, k);
     }
+}
+// A lane's parameters in shared memory, for rows whose columns its registers cannot hold and whose vectors are
+// not the parameters': [kPairs][kThreads], each read by the thread that wrote it.
+template <typename S>
+__device__ __forceinline__ void staged_params(typename S::P* w, const typename S::P* place, int e) {
+#pragma unroll
+    for (int k = 0; k < S::n; ++k) w[k] = place[(e * S::n + k) * S::kThreads];
 }
 __device__ __forceinline__ const float* row_of(const float* p, int64_t at) { return p ? p + at : nullptr; }
 // The first element of row `row` within its 16 bytes.
@@ -315,16 +367,32 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
     extern __shared__ uint4 ahead[];                         // [depth][U][E][kThreads]
     const int64_t first = (int64_t)blockIdx.x * S::kRows + threadIdx.x / S::L, step = stride * d;
     const int shift = shift_of<S>(first, d);
-    const int lane = threadIdx.x % S::L, col = lane * S::N - shift, left = d - col, before = -col;
+    const int lane = threadIdx.x % S::L, col = lane * S::N - shift;
+    const Edges<S, T> edges(col, d);
+    const int left = edges.left, before = edges.before;
     const float fd = (float)d, over_d = 1.f / fd;
     // the group's weights stay where the registers allow it
     constexpr bool kHeld = S::kValues <= kHeldValues;
     using P = typename S::P;
     P w[S::kPairs], b[S::kPairs];
     const int64_t at = first % groups * d + col;
+    constexpr bool kStaged = ForwardPlan<T, S>::staged;
+    P* staged = reinterpret_cast<P*>(reinterpret_cast<char*>(ahead) + A::bytes) + threadIdx.x;
     if (kHeld) {
         load_row_params<S>(w, row_of(weight, at), left, before, 1.f);
         load_row_params<S>(b, row_of(bias, at), left, before, 0.f);
+    } else if (kStaged) {
+#pragma unroll 1
+        for (int e = 0; e < S::E; ++e) {
+            P we[S::n], be[S::n];
+            load_vector_params<S>(we, row_of(weight, at), e, left, before, 1.f);
+            load_vector_params<S>(be, row_of(bias, at), e, left, before, 0.f);
+#pragma unroll
+            for (int k = 0; k < S::n; ++k) {
+                staged[(e * S::n + k) * S::kThreads] = we[k];
+                staged[(S::kPairs + e * S::n + k) * S::kThreads] = be[k];
+            }
+        }
     }
     uint4* mine = ahead + threadIdx.x;
     const Rows have = rows_of(rows, stride, first, (int64_t)blockIdx.x * S::kRows);
@@ -352,7 +420,7 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
 #pragma unroll
         for (int u = 0; u < U; ++u)
             load_row<S, T>(v[u], A::on ? mine + ((turn % A::depth) * U + u) * S::E * S::kThreads : nullptr,
-                           next_x + u * step, turn * U + u < have.mine ? left : 0, before);
+                           next_x + u * step, turn * U + u < have.mine ? left : 0, edges);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             P t = psplat<P>(0.f);
@@ -383,7 +451,7 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
                 if (e * S::L * S::N < left) {
                     P f[S::n];
                     unpack_pairs<S::N>(f, v[u][e]);
-                    deviations<S>(f, minus, e, left, before);
+                    deviations(f, minus, e, edges);
 #pragma unroll
                     for (int k = 0; k < S::n; ++k) t = pfma(f[k], f[k], t);
                 }
@@ -425,7 +493,10 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
                 if (!kHeld) asm volatile("" ::: "memory");
                 P f[S::n], we[S::n], be[S::n];
                 unpack_pairs<S::N>(f, v[u][e]);
-                if (!kHeld) {
+                if (kStaged) {
+                    staged_params<S>(we, staged, e);
+                    staged_params<S>(be, staged + S::kPairs * S::kThreads, e);
+                } else if (!kHeld) {
                     load_vector_params<S>(we, row_of(weight, at), e, left, before, 1.f);
                     load_vector_params<S>(be, row_of(bias, at), e, left, before, 0.f);
                 }
@@ -435,7 +506,7 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
                                 kHeld ? b[e * S::n + k] : be[k]);
                 Vec<T, S::N> o;
                 pack_pairs<S::N>(o, f);
-                store_vector<S>(next_y + u * step + e * kStep, o, e, left, before);
+                store_vector<S>(next_y + u * step + e * kStep, o, e, edges);
             }
             if (lane == 0) {
                 if (mean) mean[row + u * stride] = mu;
@@ -466,13 +537,20 @@ layer_norm_backward_kernel(const T* x, const T* dy, const float* weight, const f
     const int64_t block = apart ? (int64_t)(blockIdx.x / groups) * groups * S::kRows + blockIdx.x % groups
                                 : (int64_t)blockIdx.x * S::kRows;
     const int64_t first = block + (apart ? (int64_t)group * groups : group), step = stride * d;
-    const int shift = shift_of<S>(first, d), col = lane * S::N - shift, left = d - col, before = -col;
+    const int shift = shift_of<S>(first, d), col = lane * S::N - shift;
+    const Edges<S, T> edges(col, d);
+    const int left = edges.left, before = edges.before;
     const float over_d = 1.f / d;
     constexpr bool kHeld = S::kValues <= 8;
     const int64_t at = first % groups * d + col;            // stride is a multiple of groups
     using P = typename S::P;
     P w[S::kPairs], dw[S::kPairs], db[S::kPairs];
-    if (kHeld) load_row_params<S>(w, row_of(weight, at), left, before, 1.f);
+    constexpr bool kStaged = BackwardPlan<T, S>::staged;
+    P* staged = reinterpret_cast<P*>(reinterpret_cast<char*>(ahead) + A::bytes) + threadIdx.x;
+    if (kHeld || kStaged) load_row_params<S>(w, row_of(weight, at), left, before, 1.f);
+    if (kStaged)
+#pragma unroll
+        for (int k = 0; k < S::kPairs; ++k) staged[k * S::kThreads] = w[k];
 #pragma unroll
     for (int k = 0; k < S::kPairs; ++k) dw[k] = db[k] = psplat<P>(0.f);
     const Rows have = rows_of(rows, stride, first, block);
@@ -517,13 +595,18 @@ layer_norm_backward_kernel(const T* x, const T* dy, const float* weight, const f
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int there = turn * U + u < have.mine ? left : 0;
-            load_row<S, T>(v[u], A::on ? place(turn, u, 0) : nullptr, next_x + u * step, there, before);
-            load_row<S, T>(g[u], A::on ? place(turn, u, 1) : nullptr, next_dy + u * step, there, before);
+            load_row<S, T>(v[u], A::on ? place(turn, u, 0) : nullptr, next_x + u * step, there, edges);
+            load_row<S, T>(g[u], A::on ? place(turn, u, 1) : nullptr, next_dy + u * step, there, edges);
             mu[u] = ahead_mu[u];
             rs[u] = ahead_rs[u];
         }
         load_stats(turn + 1);
-        if (!kHeld) load_row_params<S>(w, row_of(weight, at), left, before, 1.f);
+        if (kStaged) {
+#pragma unroll
+            for (int e = 0; e < S::E; ++e) staged_params<S>(w + e * S::n, staged, e);
+        } else if (!kHeld) {
+            load_row_params<S>(w, row_of(weight, at), left, before, 1.f);
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const P minus = psplat<P>(-mu[u]), times = psplat<P>(rs[u]);
@@ -534,7 +617,13 @@ layer_norm_backward_kernel(const T* x, const T* dy, const float* weight, const f
                     P fx[S::n], fg[S::n];
                     unpack_pairs<S::N>(fx, v[u][e]);
                     unpack_pairs<S::N>(fg, g[u][e]);
-                    deviations<S>(fx, minus, e, left, before);
+                    // what lies outside the row is zero in dy: its xh matters where it is not finite
+                    if (!S::kShift || fabsf(mu[u] * rs[u]) <= FLT_MAX) {
+#pragma unroll
+                        for (int k = 0; k < S::n; ++k) fx[k] = padd(fx[k], minus);
+                    } else {
+                        deviations(fx, minus, e, edges);
+                    }
 #pragma unroll
                     for (int k = 0; k < S::n; ++k) {
                         const int i = e * S::n + k;
@@ -584,7 +673,7 @@ layer_norm_backward_kernel(const T* x, const T* dy, const float* weight, const f
                 }
                 Vec<T, S::N> out;
                 pack_pairs<S::N>(out, o);
-                store_vector<S>(next_dx + u * step + e * kStep, out, e, left, before);
+                store_vector<S>(next_dx + u * step + e * kStep, out, e, edges);
             }
         }
         if (!A::on) {
@@ -755,9 +844,9 @@ struct Forward {
     static int64_t run(const Args& a) {
         using Plan = ForwardPlan<T, S>;
         const int64_t blocks = blocks_for<Plan, S>(a.rows, whole_turns<S>(a.groups, a.d));
-        const cudaError_t e = allow_shared(layer_norm_kernel<T, S>, Plan::A::bytes);
+        const cudaError_t e = allow_shared(layer_norm_kernel<T, S>, Plan::bytes);
         if (e != cudaSuccess) return (int64_t)e;
-        layer_norm_kernel<T, S><<<(unsigned)blocks, S::kThreads, Plan::A::bytes, a.stream>>>(
+        layer_norm_kernel<T, S><<<(unsigned)blocks, S::kThreads, Plan::bytes, a.stream>>>(
             static_cast<const T*>(a.x), a.weight, a.bias, a.rows, a.groups, a.d, a.eps, static_cast<T*>(a.out), a.mean,
             a.rstd, blocks * S::kRows);
         return (int64_t)cudaGetLastError();
@@ -771,7 +860,7 @@ struct Backward {
         const int64_t blocks = backward_blocks<Plan, S>(a.rows, a.groups, a.d);
         const int weights = weights_of_block<Plan, S>(a.groups);
         const size_t join = a.part && weights < S::kRows ? sizeof(float2) * S::kRows * (size_t)a.d : 0;
-        const size_t smem = join > Plan::A::bytes ? join : Plan::A::bytes;
+        const size_t smem = join > Plan::bytes ? join : Plan::bytes;
         const cudaError_t e = allow_shared(layer_norm_backward_kernel<T, S>, smem);
         if (e != cudaSuccess) return (int64_t)e;
         layer_norm_backward_kernel<T, S><<<(unsigned)blocks, S::kThreads, smem, a.stream>>>(
@@ -791,7 +880,10 @@ struct Slots {
 // backward's sums per column leave no room for two: 59 us instead of 48).  Up to 64 vectors share a
 // warp, two a lane from 32 on, longer rows take a block of up to 512 lanes.
 // Rows that are not whole vectors: by the vectors that hold them (16384 x 1001 in bf16: 23 us, element by
-// element 33 us; 4096 x 5001 39 and 76 us, its gradients 68 and 171 us).  Element by element only where an array does not start on 16 bytes.
+// element 33 us; 4096 x 5001 37 and 76 us, its gradients 59 and 171 us).  Element by element where an array does not
+// start on 16 bytes, and for the gradients of rows of a few warps (65536 x 300 in bf16: 66 us, as vectors 76 us;
+// 16384 x 1001 fp32 48 and 56 us; 4096 x 1023 bf16 19 and 24 us): the sums per column of lanes that hold
+// vectors fill the registers, and blocks as small as that leave more of them to join.
 enum RowLayout { kElements, kShifted, kVectors };
 
 template <typename Op, typename T, bool Shift>
@@ -801,10 +893,16 @@ int64_t by_vectors(const Args& a, int n) {
     if (n <= 8) return Op::template run<T, Shape<8 / E, E, N, Shift>>(a);
     if (n <= 16) return Op::template run<T, Shape<16 / E, E, N, Shift>>(a);
     if (n <= 32) return Op::template run<T, Shape<32 / E, E, N, Shift>>(a);
-    if (n <= 64) return Op::template run<T, Shape<32, 2, N, Shift>>(a);
+    // (shifted gradients in bf16: two vectors a lane leave no room to hold the weights)
+    if (n <= 64) {
+        if constexpr (Shift && !Op::kForward && N == 8) return Op::template run<T, Shape<64, 1, N, Shift>>(a);
+        else return Op::template run<T, Shape<32, 2, N, Shift>>(a);
+    }
     if (n <= 128) return Op::template run<T, Shape<128 / E, E, N, Shift>>(a);
     if (n <= 192) return Op::template run<T, Shape<192 / E, E, N, Shift>>(a);
     if (n <= 256) return Op::template run<T, Shape<256 / E, E, N, Shift>>(a);
+    if constexpr (Shift)
+        if (n <= 320) return Op::template run<T, Shape<320 / E, E, N, Shift>>(a);      // rows of a power of two of them
     if (n <= 384) return Op::template run<T, Shape<384 / E, E, N, Shift>>(a);
     if (n <= 512) return Op::template run<T, Shape<512 / E, E, N, Shift>>(a);
     if (n <= 1024) return Op::template run<T, Shape<512, 2, N, Shift>>(a);
@@ -817,7 +915,8 @@ int64_t by_shape(const Args& a, RowLayout layout) {
     constexpr int N = 16 / sizeof(T);
     const int d = a.d, shifted = (d + 2 * N - 2) / N;      // vectors that hold a row, wherever it starts
     if (layout == kVectors && d % N == 0) return by_vectors<Op, T, false>(a, d / N);
-    if (layout != kElements && shifted <= LA_MAX_NORM_D / N) return by_vectors<Op, T, true>(a, shifted);
+    const bool few_warps = !Op::kForward && d > 256 && d <= 1024;
+    if (layout != kElements && !few_warps && shifted <= LA_MAX_NORM_D / N) return by_vectors<Op, T, true>(a, shifted);
     if (d <= 32) return Op::template run<T, Shape<32, 1, 1>>(a);
     if (d <= 128) return Op::template run<T, Shape<32, 4, 1>>(a);
     if (d <= 512) return Op::template run<T, Shape<128, 4, 1>>(a);

@@ -57,16 +57,11 @@ __device__ __forceinline__ void pack(Vec<__nv_bfloat16, N>& x, const float (&f)[
     }
 }
 
-// Element k of a vector; and the vector with zero there.
+// Element k of a vector.
 template <typename T, int N>
 __device__ __forceinline__ T element(const Vec<T, N>& x, int k) {
     if constexpr (sizeof(T) == 2 && N > 1) return __ushort_as_bfloat16((unsigned short)(x.v[k / 2] >> (k % 2 * 16)));
     else return x.v[k];
-}
-template <typename T, int N>
-__device__ __forceinline__ void clear_element(Vec<T, N>& x, int k) {
-    if constexpr (sizeof(T) == 2 && N > 1) x.v[k / 2] &= k % 2 ? 0xffffu : 0xffff0000u;
-    else x.v[k] = T(0.f);
 }
 
 // Makes the compiler unpack a bf16 vector anew after this point, instead of keeping the twice as many
