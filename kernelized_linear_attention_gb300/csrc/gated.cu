@@ -356,8 +356,8 @@ __device__ void pass_empty(const GatedParams& p, int threads) {
     }
 }
 
-// Tiles held in registers, one at a time per block: single tiles, and bf16 rows of odd length, whose
-// elements no asynchronous copy can fetch (32768 x 1001: 245 us, bound by loads of two bytes).
+// Tiles held in registers, one at a time per block: single tiles, and bf16 arrays that do not start on four bytes,
+// whose elements no asynchronous copy can fetch (32768 x 1001: 243 us, bound by loads of two bytes).
 // The same warps, tokens and order of operations as the ring's: the same results.
 template <typename TA, typename TX, bool Rev, bool Vec, int W, int K, int PerSm>
 __global__ void __launch_bounds__((W + 2) * 32, PerSm) gated_scan_kernel(GatedParams p, int tiles, int slices,
@@ -558,18 +558,45 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, long 
 // next, so stages are neither held for a fixed number of tiles nor idle: the trips to L2 are hidden
 // behind the tiles that follow.
 //
-// Tile copies (Tma) need rows that start on 16 bytes.  Other rows of four-byte steps are copied by four
-// warps, four bytes a lane, into the same places (32768 x 1023 in fp32: 116 us; with tiles in registers 182 us).
+// Tile copies (kTiles) need rows that start on 16 bytes.  Other rows of four-byte steps are copied by four
+// warps, four bytes a lane, into the same places (kWords: 32768 x 1023 in fp32 116 us; with tiles in registers
+// 182 us).  bf16 rows of odd length, every other of which starts inside four bytes, are copied as the words that
+// hold them, one more a row than they fill, and put together by the lanes that read them (kHalves: 32768 x 1001
+// 113 us; in registers 243 us).
 // --------------------------------------------------------------------------
+enum Copies { kTiles, kWords, kHalves };
 
-template <typename TA, typename TX, bool Rev, bool Tma, int W, int K, int S>
+// A lane's two channels of the tile's rows from j0 on, row `token` of the array first (its parity tells where the
+// row starts where rows are of odd length).
+template <typename T, bool Halves>
+struct TileRows {
+    static constexpr bool kOdd = Halves && sizeof(T) == 2;
+    static constexpr int kPitch = kSlice * (int)sizeof(T) + (kOdd ? 4 : 0);     // bytes of a row
+    const uint8_t* at;
+    int parity;
+    __device__ __forceinline__ TileRows(const uint8_t* tile, int j0, int lane, int token)
+        : at(tile + j0 * kPitch + lane * 2 * (int)sizeof(T)), parity(token & 1) {}
+    __device__ __forceinline__ float2 operator[](int k) const {
+        if constexpr (kOdd) {
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(at + k * kPitch);
+            const uint32_t v = __byte_perm(w[0], w[1], (parity ^ k) & 1 ? 0x5432 : 0x3210);
+            return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+        } else {
+            return reinterpret_cast<const Two<T>*>(at + k * kPitch)->get();
+        }
+    }
+};
+
+template <typename TA, typename TX, bool Rev, Copies Copy, int W, int K, int S>
 struct Ring {
     static constexpr int kTeams = 2;                    // compute teams, taking tiles in turn: W warps of K tokens
     static constexpr int kRows = W * K;
     static constexpr int kLookers = S % 4 == 0 ? 4 : S % 5 == 0 ? 5 : 3;   // pairs of look-back warps, in turn
-    static constexpr int kCopiers = Tma ? 1 : 4;
+    static constexpr int kCopiers = Copy == kTiles ? 1 : 4;
     static constexpr int kThreads = (kTeams * W + 2 * kLookers + 2 + 1 + kCopiers) * 32;
-    static constexpr int kA = kRows * kSlice * (int)sizeof(TA), kX = kRows * kSlice * (int)sizeof(TX);
+    using A = TileRows<TA, Copy == kHalves>;
+    using X = TileRows<TX, Copy == kHalves>;
+    static constexpr int kA = kRows * A::kPitch, kX = kRows * X::kPitch;
     static constexpr int kStage = kA + kX + (Rev ? kX : 0);
     struct Small {
         float4 run[S][W][32];              // each warp's run; then, in its first half, the state that enters it
@@ -584,35 +611,43 @@ struct Ring {
     static constexpr size_t kBytes = (size_t)S * kStage + sizeof(Small) + 128;
 };
 
-// Copies `rows` rows x kSlice channels of [T][C] from row t0 and channel c0 on to `place`, rows and channels
-// outside as zeros: the share of one of kCopiers warps.
-template <typename T, int Rows>
+__device__ __forceinline__ void copy_word(uint32_t to, const void* from, int bytes) {   // the rest of the word as zero
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
+// Copies Rows rows x kSlice channels of [tokens][C] from row t0 and channel c0 on to `place`, rows and channels
+// outside as zeros: the share of one of `warps` warps.
+template <typename T, int Rows, bool Halves>
 __device__ __forceinline__ void copy_rows(uint8_t* place, const void* from, int64_t t0, int c0, int64_t tokens, int C,
                                           int warp, int warps, int lane) {
-    constexpr int kWords = kSlice * (int)sizeof(T) / 4, kEach = 4 / (int)sizeof(T);   // of a row; elements in a word
-    for (int r = warp; r < Rows; r += warps) {
-        const int64_t t = t0 + r;
-        const T* row = static_cast<const T*>(from) + (t < 0 ? 0 : t) * C + c0;
+    constexpr int kRowWords = kSlice * (int)sizeof(T) / 4, kEach = 4 / (int)sizeof(T);   // of a row; elements in a word
+    constexpr int kPitch = TileRows<T, Halves>::kPitch;
+    const uint32_t to = tc::smem_u32(place);
+    const T* base = static_cast<const T*>(from);
+    auto word = [&](int r, int w) {
+        const int64_t t = t0 + r, end = t * C + C;
+        int64_t e = t * C + c0 + w * kEach;
+        if constexpr (TileRows<T, Halves>::kOdd) e &= ~1ll;            // the word that holds it
+        int there = t >= 0 && t < tokens && e < end ? 4 : 0;
+        if constexpr (TileRows<T, Halves>::kOdd)
+            if (there && e + 1 == tokens * C) there = 2;               // the array's last element, alone in its word
+        copy_word(to + r * kPitch + w * 4, there ? base + e : base, there);
+    };
+    for (int r = warp; r < Rows; r += warps)
 #pragma unroll
-        for (int w = 0; w < kWords / 32; ++w) {
-            const int e = (w * 32 + lane) * kEach;
-            const int there = t >= 0 && t < tokens && c0 + e < C ? 4 : 0;
-            const uint32_t to = tc::smem_u32(place) + (r * kWords + w * 32 + lane) * 4;
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to),
-                         "l"(there ? row + e : static_cast<const T*>(from)), "r"(there)
-                         : "memory");
-        }
-    }
+        for (int w = 0; w < kRowWords / 32; ++w) word(r, w * 32 + lane);
+    if constexpr (TileRows<T, Halves>::kOdd)
+        for (int r = warp + lane * warps; r < Rows; r += 32 * warps) word(r, kRowWords);
 }
 
 // over_slices: 2^64 / slices, rounded up; 0 for one slice.
-template <typename TA, typename TX, bool Rev, bool Tma, int W, int K, int S>
-__global__ void __launch_bounds__(Ring<TA, TX, Rev, Tma, W, K, S>::kThreads, 1)
+template <typename TA, typename TX, bool Rev, Copies Copy, int W, int K, int S>
+__global__ void __launch_bounds__(Ring<TA, TX, Rev, Copy, W, K, S>::kThreads, 1)
 gated_ring_kernel(GatedParams p, int tiles, int slices, unsigned long long over_slices,
                   const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_x,
                   const __grid_constant__ CUtensorMap map_h) {
-    using R = Ring<TA, TX, Rev, Tma, W, K, S>;
-    constexpr bool Vec = Tma || sizeof(TA) == 2 || sizeof(TX) == 2;   // bf16 rows without tile copies: of even length
+    using R = Ring<TA, TX, Rev, Copy, W, K, S>;
+    constexpr bool Tma = Copy == kTiles, kOdd = Copy == kHalves;
+    constexpr bool Vec = Tma || (!kOdd && (sizeof(TA) == 2 || sizeof(TX) == 2));     // rows of even length
     static_assert(R::kRows >= kMinTile, "the workspace holds ceil(T / kMinTile) tiles");
     constexpr int kLookers = R::kLookers, kTeams = R::kTeams;
     // Who takes every n-th tile waits for phases of its own tiles only, one after the other, when n
@@ -673,12 +708,12 @@ gated_ring_kernel(GatedParams p, int tiles, int slices, unsigned long long over_
                     tc::tma_load_2d(at + R::kA, &map_x, c0, t0, &sh.full[st]);
                     if (Rev) tc::tma_load_2d(at + R::kA + R::kX, &map_h, c0, t0 - 1, &sh.full[st]);
                 } else {
-                    copy_rows<TA, R::kRows>(at, p.a, (int64_t)t0 + (Rev ? 1 : 0), c0, p.T, p.C, copier, R::kCopiers,
-                                            lane);
-                    copy_rows<TX, R::kRows>(at + R::kA, p.x, t0, c0, p.T, p.C, copier, R::kCopiers, lane);
+                    copy_rows<TA, R::kRows, kOdd>(at, p.a, (int64_t)t0 + (Rev ? 1 : 0), c0, p.T, p.C, copier,
+                                                  R::kCopiers, lane);
+                    copy_rows<TX, R::kRows, kOdd>(at + R::kA, p.x, t0, c0, p.T, p.C, copier, R::kCopiers, lane);
                     if (Rev)
-                        copy_rows<TX, R::kRows>(at + R::kA + R::kX, p.h, (int64_t)t0 - 1, c0, p.T, p.C, copier,
-                                                R::kCopiers, lane);
+                        copy_rows<TX, R::kRows, kOdd>(at + R::kA + R::kX, p.h, (int64_t)t0 - 1, c0, p.T, p.C, copier,
+                                                      R::kCopiers, lane);
                     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
                                      tc::smem_u32(&sh.full[st]))
                                  : "memory");
@@ -825,8 +860,8 @@ gated_ring_kernel(GatedParams p, int tiles, int slices, unsigned long long over_
                 end = i;
             } else {
                 const uint8_t* at = data + (size_t)st * R::kStage;
-                const Two<TA>* sa = reinterpret_cast<const Two<TA>*>(at) + j0 * (kSlice / 2) + lane;
-                const Two<TX>* sx = reinterpret_cast<const Two<TX>*>(at + R::kA) + j0 * (kSlice / 2) + lane;
+                const typename R::A sa(at, j0, lane, Rev ? 1 : 0);        // tiles and j0 are even
+                const typename R::X sx(at + R::kA, j0, lane, 0);
                 const int64_t t0 = (int64_t)(Rev ? tiles - 1 - order : order) * R::kRows;
                 const int n = (int)min64(R::kRows, p.T - t0), c = sh.slice[st] * kSlice + 2 * lane, left = p.C - c;
                 unsigned cuts = 0;
@@ -840,7 +875,7 @@ gated_ring_kernel(GatedParams p, int tiles, int slices, unsigned long long over_
 #pragma unroll
                     for (int q = 0; q < K; ++q) {
                         const int k = Rev ? K - 1 - q : q;
-                        const float2 g = sa[k * (kSlice / 2)].get(), in = sx[k * (kSlice / 2)].get();
+                        const float2 g = sa[k], in = sx[k];
                         r.A = mul2(r.A, g);
                         r.B = fma2(g, r.B, in);
                     }
@@ -848,7 +883,7 @@ gated_ring_kernel(GatedParams p, int tiles, int slices, unsigned long long over_
 #pragma unroll 1
                     for (int q = 0; q < K; ++q) {
                         const int k = Rev ? K - 1 - q : q;
-                        const float2 g = sa[k * (kSlice / 2)].get(), in = sx[k * (kSlice / 2)].get();
+                        const float2 g = sa[k], in = sx[k];
                         if ((cuts >> k) & 1) {
                             float2 s = in;
                             if (p.edge_in) {
@@ -877,9 +912,8 @@ gated_ring_kernel(GatedParams p, int tiles, int slices, unsigned long long over_
             b += kTeams;
             const int order = sh.order[st], seq = sh.seq[st];
             const uint8_t* at = data + (size_t)st * R::kStage;
-            const Two<TA>* sa = reinterpret_cast<const Two<TA>*>(at) + j0 * (kSlice / 2) + lane;
-            const Two<TX>* sx = reinterpret_cast<const Two<TX>*>(at + R::kA) + j0 * (kSlice / 2) + lane;
-            const Two<TX>* sh_h = reinterpret_cast<const Two<TX>*>(at + R::kA + R::kX) + j0 * (kSlice / 2) + lane;
+            const typename R::A sa(at, j0, lane, Rev ? 1 : 0);
+            const typename R::X sx(at + R::kA, j0, lane, 0), sh_h(at + R::kA + R::kX, j0, lane, 1);
             const int64_t t0 = (int64_t)(Rev ? tiles - 1 - order : order) * R::kRows;
             const int n = (int)min64(R::kRows, p.T - t0), c = sh.slice[st] * kSlice + 2 * lane, left = p.C - c;
             const int64_t row = (t0 + j0) * p.C + c;
@@ -897,9 +931,9 @@ gated_ring_kernel(GatedParams p, int tiles, int slices, unsigned long long over_
 #pragma unroll
                 for (int q = 0; q < K; ++q) {
                     const int k = Rev ? K - 1 - q : q;
-                    s = fma2(sa[k * (kSlice / 2)].get(), s, sx[k * (kSlice / 2)].get());
+                    s = fma2(sa[k], s, sx[k]);
                     store_two<Vec>(y + k * (int64_t)p.C, left, s);
-                    if (Rev) store_two<Vec>(da + k * (int64_t)p.C, left, mul2(s, sh_h[k * (kSlice / 2)].get()));
+                    if (Rev) store_two<Vec>(da + k * (int64_t)p.C, left, mul2(s, sh_h[k]));
                 }
             } else {
                 const int open_at = cuts ? (Rev ? __ffs(cuts) - 1 : 31 - __clz(cuts)) : 32;
@@ -907,7 +941,7 @@ gated_ring_kernel(GatedParams p, int tiles, int slices, unsigned long long over_
                 for (int q = 0; q < K; ++q) {
                     const int k = Rev ? K - 1 - q : q;
                     if (j0 + k >= n) continue;
-                    const float2 g = sa[k * (kSlice / 2)].get(), in = sx[k * (kSlice / 2)].get();
+                    const float2 g = sa[k], in = sx[k];
                     if ((cuts >> k) & 1) {
                         s = in;
                         if (k == open_at) {
@@ -923,7 +957,7 @@ gated_ring_kernel(GatedParams p, int tiles, int slices, unsigned long long over_
                     store_two<Vec>(y + k * (int64_t)p.C, left, s);
                     float2 leaving = s;
                     if (Rev) {
-                        float2 prev = sh_h[k * (kSlice / 2)].get();
+                        float2 prev = sh_h[k];
                         if ((ends >> k) & 1) {
                             const int sq = sh.first[st][j0 + k];
                             prev = p.state_in ? edge_two(p.state_in + (int64_t)sq * p.C + c, left)
@@ -1054,15 +1088,16 @@ bool row_map(CUtensorMap* m, const void* base, int64_t tokens, int C, int rows) 
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename TA, typename TX, bool Rev, bool Tma, int W, int K, int S>
+template <typename TA, typename TX, bool Rev, Copies Copy, int W, int K, int S>
 cudaError_t run_ring(const GatedParams& p, int slices, cudaStream_t s) {
-    using R = Ring<TA, TX, Rev, Tma, W, K, S>;
+    using R = Ring<TA, TX, Rev, Copy, W, K, S>;
+    static_assert(R::kRows % 2 == 0 && K % 2 == 0, "a row's parity is that of its place in the tile");
     static_assert(R::kBytes <= 227 * 1024, "a block's shared memory");
     CUtensorMap ma{}, mx{}, mh{};
-    if (Tma && (!row_map<TA>(&ma, p.a, p.T, p.C, R::kRows) || !row_map<TX>(&mx, p.x, p.T, p.C, R::kRows) ||
+    if (Copy == kTiles && (!row_map<TA>(&ma, p.a, p.T, p.C, R::kRows) || !row_map<TX>(&mx, p.x, p.T, p.C, R::kRows) ||
                 !row_map<TX>(&mh, Rev ? p.h : p.x, p.T, p.C, R::kRows)))
         return cudaErrorInvalidValue;
-    auto kernel = gated_ring_kernel<TA, TX, Rev, Tma, W, K, S>;
+    auto kernel = gated_ring_kernel<TA, TX, Rev, Copy, W, K, S>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)R::kBytes);
     if (e != cudaSuccess) return e;
     return launch_tiles(kernel, p, Rev ? 1 : 0, R::kRows, (int)ceil_div(p.T, R::kRows), slices, 1, R::kThreads,
@@ -1086,8 +1121,12 @@ cudaError_t dispatch(const GatedParams& p, int slices, cudaStream_t s) {
     constexpr int W = 4, K = kBytes <= 4 ? 32 : kBytes <= 10 ? 16 : 8;
     constexpr int S = kBytes <= 4 ? 6 : kBytes <= 6 ? 8 : kBytes <= 8 ? 6 : kBytes <= 10 ? 4 : 8;
     if (p.T > W * K) {
-        if (tma) return run_ring<TA, TX, Rev, true, W, K, S>(p, slices, s);
-        if (vec || (sizeof(TA) == 4 && sizeof(TX) == 4)) return run_ring<TA, TX, Rev, false, W, K, S>(p, slices, s);
+        if (tma) return run_ring<TA, TX, Rev, kTiles, W, K, S>(p, slices, s);
+        if (vec || (sizeof(TA) == 4 && sizeof(TX) == 4)) return run_ring<TA, TX, Rev, kWords, W, K, S>(p, slices, s);
+        auto on_4 = [](const void* q) { return reinterpret_cast<uintptr_t>(q) % 4 == 0; };
+        if constexpr (sizeof(TA) == 2 || sizeof(TX) == 2)
+            if (p.C % 2 == 1 && on_4(p.a) && on_4(p.x) && on_4(p.h))
+                return run_ring<TA, TX, Rev, kHalves, W, K, Rev && kBytes == 6 ? 6 : S>(p, slices, s);
     }
     return vec ? run_registers<TA, TX, Rev, true, W, K, 2>(p, slices, s)
                : run_registers<TA, TX, Rev, false, W, K, 2>(p, slices, s);

@@ -429,6 +429,33 @@ def test_layer_norm_no_rows_and_missing_gradients(la):
         assert torch.equal(db, full[2]) if keep[1] else bool((db == 3.0).all())
 
 
+@pytest.mark.parametrize("kinds", [("bf16", "bf16"), ("f32", "bf16"), ("bf16", "f32")], ids=str)
+@pytest.mark.parametrize("T,C", [(129, 1), (257, 63), (1000, 65), (2049, 191), (777, 1001)])
+def test_gated_scan_odd_rows_among_neighbours(la, T, C, kinds):
+    # rows that start inside four bytes, read by whole words, against the same rows read one by one
+    # (arrays that start inside four bytes): the same results, whatever lies before and after
+    g = torch.Generator().manual_seed(T + C)
+    ta, tb = (torch.float32 if k == "f32" else torch.bfloat16 for k in kinds)
+    vals = dict(a=torch.rand(T, 1, C, generator=g).to(ta), b=torch.randn(T, 1, C, generator=g).to(tb),
+                dh=torch.randn(T, 1, C, generator=g).to(tb))
+    cu = torch.tensor([0, T // 3, T // 3, T - 5, T], dtype=torch.int32, device="cuda")
+    state = torch.randn(4, 1, C, generator=g).cuda()
+
+    def at(t, by):
+        buf = torch.full((t.numel() + 64,), float("nan"), dtype=t.dtype, device="cuda")
+        buf[by:by + t.numel()] = t.reshape(-1).cuda()
+        return buf[by:by + t.numel()].view(t.shape)
+
+    got = []
+    for by in (32, 33):
+        a, b, dh = (at(vals[k], by) for k in ("a", "b", "dh"))
+        h, out = la.la_gated_scan(a, b, cu, state_in=state, return_state=True)
+        got.append((h, out) + la.la_gated_scan_backward(a, at(h, by), dh, cu, state_in=state, dstate_out=state,
+                                                       return_dstate=True))
+    for x, y in zip(*got):
+        assert bool(torch.isfinite(x).all()) and torch.equal(x, y)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,H,d", [(9, 1, 1), (40, 3, 5), (37, 2, 7), (300, 7, 33), (77, 5, 129), (31, 1, 515), (19, 3, 1030),
                                       (401, 1, 2051), (6, 2, 4097), (3, 1, 9001), (2, 1, 16383)])
