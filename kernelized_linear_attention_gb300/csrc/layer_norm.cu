@@ -102,13 +102,6 @@ struct BackwardPlan {
     static_assert(per_sm >= 1, "a block's shared memory");
 };
 
-__device__ __forceinline__ void copy_16(void* to, const void* from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(to)), "l"(from) : "memory");
-}
-__device__ __forceinline__ void copies_done() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 template <int Width>
 __device__ __forceinline__ float lane_sum(float x) {
 #pragma unroll

@@ -127,4 +127,13 @@ __device__ __forceinline__ void pack_pairs(Vec<T, N>& x, const typename Pairs<N>
     pack(x, v);
 }
 
+// Asynchronous copies of 16 bytes to shared memory; a group of them ends with copies_done(), and wait_copies<N>
+// waits until at most N groups of this thread are on their way.
+__device__ __forceinline__ void copy_16(void* to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 }  // namespace la

@@ -11,10 +11,12 @@
 // tokens' cos and sin into shared memory (once for all heads of q and k), then
 // turn and store.  A thread's unit of work is N neighbouring channels and, where
 // pairs are halves, their N partners; N channels are 16 bytes where every row
-// allows it, else one pair is the unit.
+// allows it.  Other rows are turned in shared memory, or pair by pair where
+// the arrays do not start on 16 bytes or a few tokens' rows do not fit there.
 //
 // Measured (GB300, 6.76 TB/s copies): q and k of 65536 x 16 x 64 in bf16 82 us, 6.6 TB/s (32768 x 16 x 64 in
-// fp32 80 us); 4099 x 7 x 83 in fp32, pair by pair, 15 us, 2.6 TB/s.
+// fp32 80 us); 32768 x 7 x 83 in fp32 52 us, 5.9 TB/s; 32768 x 9 x 77
+// in bf16, bound by instructions per pair, 46 us, 4.0 TB/s.
 #include "ops/ops.h"
 #include "ops/vec.cuh"
 
@@ -30,6 +32,19 @@ __device__ __forceinline__ unsigned long long turn_fraction(float freq) {
     const double turns = (double)freq * 0.15915494309189533577;   // 1 / (2 pi)
     const double frac = turns - floor(turns);                     // [0, 1]
     return (unsigned long long)(long long)((frac < 0.5 ? frac : frac - 1.0) * 18446744073709551616.0);
+}
+
+// (cos, sin) of token t's pair j; sin negated for the inverse.
+__device__ __forceinline__ float2 cos_sin(const RotaryParams& p, int64_t t, int j) {
+    int axis = 0;
+    while (axis + 1 < p.naxes && j >= p.first[axis + 1]) ++axis;
+    const float f = p.freq[j];
+    const unsigned long long turn =
+        turn_fraction(f) * (unsigned long long)(long long)p.positions[t * p.naxes + axis];
+    float s, c;
+    sincospif((float)(long long)turn * 0x1p-63f, &s, &c);
+    if (!isfinite(f)) s = c = __int_as_float(0x7fc00000);
+    return make_float2(c, p.inverse ? -s : s);
 }
 
 // A block's units: token x head (of q's heads, then k's, the block's share of them) x unit of the head.
@@ -85,15 +100,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
             // the tokens' cos and sin, while the first loads are on their way
             for (int i = threadIdx.x; i < tokens * p.P; i += kRotaryThreads) {
                 const int t = i / p.P, j = i - t * p.P;
-                int axis = 0;
-                while (axis + 1 < p.naxes && j >= p.first[axis + 1]) ++axis;
-                const float f = p.freq[j];
-                const unsigned long long turn =
-                    turn_fraction(f) * (unsigned long long)(long long)p.positions[(t0 + t) * p.naxes + axis];
-                float s, c;
-                sincospif((float)(long long)turn * 0x1p-63f, &s, &c);
-                if (!isfinite(f)) s = c = __int_as_float(0x7fc00000);
-                cs[kOne ? i : t * p.P + j % kPairs * apart + j / kPairs] = make_float2(c, p.inverse ? -s : s);
+                cs[kOne ? i : t * p.P + j % kPairs * apart + j / kPairs] = cos_sin(p, t0 + t, j);
             }
             __syncthreads();
         }
@@ -125,6 +132,66 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
     }
 }
 
+// Rows that units do not divide: a block copies its tokens' rows of q and k, which lie together and start on 16
+// bytes, to shared memory, turns the pairs there, wherever they lie, and writes the rows back as they came.
+struct StagedPlan {
+    int tokens;                        // per block: a whole number of vectors
+    uint32_t over_pairs, over_heads;   // 2^32 / P and 2^32 / H, rounded up
+};
+constexpr int kStagedBytes = 24 * 1024;   // of rows of q and k that a block aims at
+constexpr int kMostStaged = 40 * 1024;    // with the table
+
+template <typename T, bool Interleaved>
+__global__ void __launch_bounds__(kRotaryThreads) rotary_staged_kernel(const __grid_constant__ RotaryParams p,
+                                                                       const __grid_constant__ StagedPlan plan) {
+    extern __shared__ uint4 rows[];             // [q, k][tokens H d], then cos and sin [tokens][P]
+    constexpr int N = 16 / sizeof(T);
+    const int64_t t0 = (int64_t)blockIdx.x * plan.tokens, at = t0 * p.H * p.d;
+    const int tokens = (int)min64(plan.tokens, p.T - t0), row = p.H * p.d;
+    const int arrays = p.k ? 2 : 1, n = tokens * row, place = plan.tokens * row;
+    T* held = reinterpret_cast<T*>(rows);
+    float2* cs = reinterpret_cast<float2*>(held + arrays * place);
+    for (int a = 0; a < arrays; ++a) {
+        const T* x = static_cast<const T*>(a ? p.k : p.q) + at;
+        for (int i = threadIdx.x * N; i < n; i += kRotaryThreads * N) {
+            if (i + N <= n) {
+                copy_16(held + a * place + i, x + i);
+            } else {
+                for (int j = i; j < n; ++j) held[a * place + j] = x[j];
+            }
+        }
+    }
+    copies_done();
+    for (int i = threadIdx.x; i < tokens * p.P; i += kRotaryThreads) {
+        const int t = over(i, plan.over_pairs), j = i - t * p.P;
+        cs[i] = cos_sin(p, t0 + t, j);
+    }
+    wait_copies<0>();
+    __syncthreads();
+    const int heads = tokens * p.H;
+    for (int a = 0; a < arrays; ++a)
+        for (int i = threadIdx.x; i < heads * p.P; i += kRotaryThreads) {
+            const int r = over(i, plan.over_pairs), j = i - r * p.P;
+            T* x = held + a * place + r * p.d + (Interleaved ? 2 * j : j);
+            T* y = x + (Interleaved ? 1 : p.P);
+            const float2 w = cs[over(r, plan.over_heads) * p.P + j];
+            const float f0 = (float)*x, f1 = (float)*y;
+            *x = T(fmaf(f0, w.x, -__fmul_rn(f1, w.y)));
+            *y = T(fmaf(f1, w.x, __fmul_rn(f0, w.y)));
+        }
+    __syncthreads();
+    for (int a = 0; a < arrays; ++a) {
+        T* x = static_cast<T*>(a ? p.k_out : p.q_out) + at;
+        for (int i = threadIdx.x * N; i < n; i += kRotaryThreads * N) {
+            if (i + N <= n) {
+                *reinterpret_cast<uint4*>(x + i) = *reinterpret_cast<const uint4*>(held + a * place + i);
+            } else {
+                for (int j = i; j < n; ++j) x[j] = held[a * place + j];
+            }
+        }
+    }
+}
+
 uint32_t reciprocal(int n) { return n > 1 ? (uint32_t)(0xffffffffu / (uint32_t)n) + 1 : 0; }
 
 template <typename T, int N>
@@ -152,6 +219,30 @@ cudaError_t run(const RotaryParams& p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+// Tokens per block of the staged form: as many as kStagedBytes hold, but no fewer blocks than SMs for it; 0 where
+// not even the fewest whose rows are whole vectors fit.
+template <typename T>
+int64_t staged_tokens(const RotaryParams& p) {
+    constexpr int N = 16 / sizeof(T);
+    const int64_t row = (int64_t)p.H * p.d, arrays = p.k ? 2 : 1;
+    int64_t step = 1;
+    while (step * row % N) step *= 2;
+    const int64_t bytes = arrays * row * (int64_t)sizeof(T), table = (int64_t)sizeof(float2) * p.P;
+    if (step * (bytes + table) > kMostStaged) return 0;
+    int64_t tokens = min64(min64(kStagedBytes / bytes, kMostStaged / (bytes + table)), p.T / 152);
+    tokens = tokens / step * step;
+    return tokens > step ? tokens : step;
+}
+template <typename T>
+cudaError_t run_staged(const RotaryParams& p, int64_t tokens, cudaStream_t s) {
+    const StagedPlan plan{(int)tokens, reciprocal(p.P), reciprocal(p.H)};
+    const size_t smem = (size_t)tokens * ((p.k ? 2 : 1) * sizeof(T) * p.H * p.d + sizeof(float2) * p.P);
+    const unsigned blocks = (unsigned)ceil_div(p.T, tokens);
+    if (p.interleaved) rotary_staged_kernel<T, true><<<blocks, kRotaryThreads, smem, s>>>(p, plan);
+    else rotary_staged_kernel<T, false><<<blocks, kRotaryThreads, smem, s>>>(p, plan);
+    return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t dispatch(const RotaryParams& p, cudaStream_t s) {
     constexpr int N = 16 / sizeof(T);
@@ -159,7 +250,10 @@ cudaError_t dispatch(const RotaryParams& p, cudaStream_t s) {
     const uintptr_t at = reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.k) |
                          reinterpret_cast<uintptr_t>(p.q_out) | reinterpret_cast<uintptr_t>(p.k_out);
     if (at % 16 == 0 && p.d % N == 0 && (p.interleaved ? 2 : 1) * p.P % N == 0) return run<T, N>(p, s);
-    return run<T, 1>(p, s);
+    // (32768 x 9 x 77 in bf16: 46 us, pair by pair 84; 32768 x 8 x 128 with 43 pairs 53 and 152; 4099 x 7 x 83 in
+    // fp32 12.5 and 14.6)
+    const int64_t tokens = at % 16 == 0 ? staged_tokens<T>(p) : 0;
+    return tokens > 0 ? run_staged<T>(p, tokens, s) : run<T, 1>(p, s);
 }
 
 }  // namespace

@@ -548,6 +548,33 @@ def _check_rotary(la, q, k, freq, pos, pairs, interleaved, inverse, dtype, extra
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("T,H,d,pairs", [(1, 1, 3, (1,)), (2501, 9, 77, (20, 18)), (1003, 8, 128, (20, 23)), (333, 1, 255, (127,)),
+                                         (4099, 3, 7, (1, 0, 1)), (61, 25, 201, (50,)), (19, 301, 5, (2,))])
+def test_rotary_rows_of_any_length_among_neighbours(la, T, H, d, pairs, interleaved, dtype):
+    q, k, freq, pos = _rotary_inputs(T, H, d, pairs, dtype, 71)
+    n, pad = q.numel(), 64
+
+    def among(t, by):
+        buf = torch.full((n + 2 * pad,), float("nan"), dtype=t.dtype, device="cuda")
+        buf[by:by + n] = t.reshape(-1)
+        return buf, buf[by:by + n].view(t.shape)
+
+    (qb, q1), (kb, k1) = among(q, pad), among(k, pad)
+    ref_q, ref_k = (ops.rotary(_np(x), _np(freq), _np(pos), pairs, interleaved, False) for x in (q, k))
+    la.la_rotary(q1, k1, freq, pos, pairs, interleaved=interleaved, q_out=q1, k_out=k1)      # in place
+    check(_np(q1), ref_q, rotary_bound(_np(q), pairs, interleaved), dtype, "q")
+    check(_np(k1), ref_k, rotary_bound(_np(k), pairs, interleaved), dtype, "k")
+    for buf in (qb, kb):
+        assert bool(torch.isnan(buf[:pad]).all()) and bool(torch.isnan(buf[pad + n:]).all())
+    # arrays that do not start on 16 bytes, and q alone, turn alike
+    (_, q2), (_, k2) = among(q, pad + 1), among(k, pad + 1)
+    o2 = la.la_rotary(q2, k2, freq, pos, pairs, interleaved=interleaved)
+    assert torch.equal(o2[0], q1) and torch.equal(o2[1], k1)
+    assert torch.equal(la.la_rotary(q, None, freq, pos, pairs, interleaved=interleaved), q1)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("T,H,d,pairs", ROTARY, ids=str)
 def test_rotary(la, T, H, d, pairs, interleaved, dtype):
     q, k, freq, pos = _rotary_inputs(T, H, d, pairs, dtype, 41)
