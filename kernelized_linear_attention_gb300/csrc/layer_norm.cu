@@ -117,23 +117,42 @@ __device__ __forceinline__ float warps_sum(int lane, F value) {
     const int w = lane % kWidth;
     return lane_sum<kWidth>(w < Warps ? value(w) : 0.f);
 }
-// Sum over the L lanes of a row group, for each of U rows; every lane gets it.  Where that is a block,
-// `scratch` holds two turns and `turn` chooses: one barrier keeps a turn's writers off the readers of
-// the turn before last.
-template <typename S, int U>
-__device__ __forceinline__ void row_sums(float (&x)[U], float* scratch, int turn) {
+// The sums over a row group's L lanes of M values (two or four); every lane gets them.  Where a group is a block, a
+// step across lanes halves what each lane still sums as long as there are several values (M = 4: six exchanges
+// instead of 20), and the warps' sums are taken up the same way.  `scratch` holds two turns and `turn` chooses: one
+// barrier keeps a turn's writers off the readers of the turn before last.
+template <typename S, int M>
+__device__ __forceinline__ void row_sums(float (&x)[M], float* scratch, int turn) {
+    static_assert(M == 2 || M == 4, "halved once or twice");
+    if constexpr (S::L <= 32) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) x[u] = lane_sum<S::L < 32 ? S::L : 32>(x[u]);
-    if constexpr (S::L > 32) {
-        constexpr int kWarps = S::L / 32;
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        float* half = scratch + (turn & 1) * U * kWarps;
-        if (lane == 0)
+        for (int i = 0; i < M; ++i) x[i] = lane_sum<S::L>(x[i]);
+    } else {
+        constexpr int kWarps = S::L / 32, kLanes = 32 / M;         // lanes that end up with the same value
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mine = lane % kLanes, value = lane / kLanes;
+        float* half = scratch + (turn & 1) * M * kWarps;
+        const bool upper = lane & 16;
+        float part[M / 2];
 #pragma unroll
-            for (int u = 0; u < U; ++u) half[u * kWarps + warp] = x[u];
+        for (int i = 0; i < M / 2; ++i) {
+            const float keep = upper ? x[i + M / 2] : x[i], send = upper ? x[i] : x[i + M / 2];
+            part[i] = keep + __shfl_xor_sync(0xffffffffu, send, 16);
+        }
+        float t = part[0];
+        if constexpr (M == 4) {
+            const float send = lane & 8 ? part[0] : part[1];
+            t = (lane & 8 ? part[1] : part[0]) + __shfl_xor_sync(0xffffffffu, send, 8);
+        }
+        t = lane_sum<kLanes>(t);
+        if (mine == 0) half[value * kWarps + warp] = t;
         __syncthreads();
+        t = 0.f;
 #pragma unroll
-        for (int u = 0; u < U; ++u) x[u] = warps_sum<kWarps>(lane, [&](int w) { return half[u * kWarps + w]; });
+        for (int w = 0; w < kWarps; w += kLanes)
+            if (w + mine < kWarps) t += half[value * kWarps + w + mine];
+        t = lane_sum<kLanes>(t);
+#pragma unroll
+        for (int i = 0; i < M; ++i) x[i] = __shfl_sync(0xffffffffu, t, i * kLanes);
     }
 }
 // Of the d columns of a row, those that warp w of a block holds; the row starts at element `shift` of its
