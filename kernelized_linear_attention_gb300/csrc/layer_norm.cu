@@ -89,10 +89,11 @@ struct ForwardPlan {
 template <typename T, typename S>
 struct BackwardPlan {
     static constexpr bool held = S::kValues <= 8;           // xh and w dy of U rows stay in registers
-    static constexpr int U = held ? 2 : 1;
-    static constexpr int registers = (held ? (2 * U + 3) * S::kValues + 40
-                                           : 2 * row_registers<T, S>() + 3 * S::kValues + 44) +
-                                     (S::kShift ? kShiftRegisters : 0);
+    static constexpr int U = held ? 2 : 1, kForShift = S::kShift ? kShiftRegisters : 0;
+    // (bf16: unpacked values want another 30; with 96 registers and five blocks instead of four 32768 x 1024
+    // take 62 us instead of 48)
+    static constexpr int registers = held ? (2 * U + 3) * S::kValues + (S::N == 8 ? 70 : 40 + kForShift)
+                                          : 2 * row_registers<T, S>() + 3 * S::kValues + 44 + kForShift;
     static constexpr int by_registers = blocks_per_sm(S::kThreads, registers);
     using A = Ahead<T, S, U, 2, by_registers>;
     static constexpr bool staged = S::kShift && !held;
