@@ -19,10 +19,12 @@
 // kernel adds up by column with compensated sums, in a fixed order.
 //
 // Measured (GB300, 6.76 TB/s copies): bf16 rows with their statistics, 1048576 x 64 with weights per head 46 us,
-// 6.0 TB/s; 8192 x 4096 28 us, 4.9 TB/s; fp32 16384 x 768 23 us, 4.4 TB/s.  Gradients in bf16: 262144 x 64
-// per head 31 us, 3.3 TB/s; 8192 x 4096 48 us, 4.2 TB/s.  The backward issues about 24
-// instructions per element, the sums across lanes and the sums per column most of them: that bounds it, with the
-// second kernel's launch and its read of the blocks' sums.
+// 6.0 TB/s; 8192 x 4096 27 us, 4.9 TB/s; 16384 x 1001 23 us, 2.9 TB/s; fp32 16384 x 768 23 us, 4.4 TB/s.  Gradients
+// in bf16: 262144 x 64 per head 31 us, 3.3 TB/s; 8192 x 4096 46 us, 4.4 TB/s; 32768 x 1024 48 us, 4.2 TB/s;
+// 229376 x 128 with 7 heads 43 us, 4.1 TB/s.  The backward issues more than 20 instructions per element (unpacking,
+// the sums across lanes and per column): that bounds it, with the second kernel's launch and its read of the
+// blocks' sums.  More warps with fewer registers are slower (two blocks of 64 registers a thread for 8192 x 4096:
+// 62 us).
 #include <float.h>
 
 #include "ops/ops.h"
@@ -894,8 +896,8 @@ struct Slots {
 // warp, two a lane from 32 on, longer rows take a block of up to 512 lanes.
 // Rows that are not whole vectors: by the vectors that hold them (16384 x 1001 in bf16: 23 us, element by
 // element 33 us; 4096 x 5001 37 and 76 us, its gradients 59 and 171 us).  Element by element where an array does not
-// start on 16 bytes, and for the gradients of rows of a few warps (65536 x 300 in bf16: 66 us, as vectors 76 us;
-// 16384 x 1001 fp32 48 and 56 us; 4096 x 1023 bf16 19 and 24 us): the sums per column of lanes that hold
+// start on 16 bytes, and for the gradients of rows of a few warps (65536 x 300 in bf16: 64 us, as vectors 68 us;
+// 16384 x 1001 fp32 46 and 55 us; 4096 x 1023 bf16 17 and 19 us): the sums per column of lanes that hold
 // vectors fill the registers, and blocks as small as that leave more of them to join.
 enum RowLayout { kElements, kShifted, kVectors };
 
