@@ -647,6 +647,49 @@ def test_rotary_refuses(la):
 
 # --------------------------------------------------------------------------- graphs and streams
 
+@pytest.mark.parametrize("d", [1024, 1001])
+def test_layer_norm_offsets_beyond_32_bits(la, d):
+    # 64 rows over and over: rows that many apart start at the same place in their 16 bytes, so they give the same bits
+    n = (1 << 31) // (64 * d) + 200
+    x, w, b, dy = _norm_inputs((64,), d, "bf16", 81, False)
+    small, mean, rstd = la.la_layer_norm(x, w, b, return_stats=True)
+    dsmall = la.la_layer_norm_backward(x, dy, mean, rstd, w)[0]
+    big = x.repeat(n, 1)
+    y, mean, rstd = la.la_layer_norm(big, w, b, return_stats=True)
+    assert bool((y.view(n, 64, d) == small).all())
+    del y
+    assert bool((la.la_layer_norm_backward(big, dy.repeat(n, 1), mean, rstd, w)[0].view(n, 64, d) == dsmall).all())
+    del big
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("H,d,pairs", [(16, 64, (20, 12)), (8, 77, (38,)), (64, 877, (400,))])
+def test_rotary_offsets_beyond_32_bits(la, H, d, pairs):
+    n = (1 << 31) // (64 * H * d) + 20
+    q, _, freq, pos = _rotary_inputs(64, H, d, pairs, "bf16", 82)
+    small = la.la_rotary(q, None, freq, pos, pairs)
+    big = q.repeat(n, 1, 1)
+    la.la_rotary(big, None, freq, pos.repeat(n, 1), pairs, q_out=big)
+    assert bool((big.view(n, 64, H, d) == small).all())
+    del big
+    torch.cuda.empty_cache()
+
+
+def test_gated_scan_odd_rows_beyond_32_bits(la):
+    T, d = 64000, 33793                                   # 2.2 G elements per tensor
+    a = torch.full((T, 1, d), 0.5, dtype=torch.bfloat16, device="cuda")
+    b = torch.ones((T, 1, d), dtype=torch.bfloat16, device="cuda")
+    b[T - 3:] = 3.0
+    h, out = la.la_gated_scan(a, b, return_state=True)
+    assert bool((h[100:T - 3] == 2.0).all()) and bool((out == 5.5).all())
+    assert bool((h[T - 3:, 0] == torch.tensor([[4.0], [5.0], [5.5]], device="cuda")).all())
+    da, db = la.la_gated_scan_backward(a, h, b)
+    assert bool((db[T - 3:, 0] == torch.tensor([[5.25], [4.5], [3.0]], device="cuda")).all())
+    assert bool((db[:T - 100] == 2.0).all()) and bool((da[200:T - 100] == 4.0).all())
+    del a, b, h, da, db
+    torch.cuda.empty_cache()
+
+
 def test_captured_calls_replay_on_new_inputs(la):
     c = _scan_case([900, 0, 333], 2, 64, "f32", "bf16", 51)
     q, k, freq, pos = _rotary_inputs(200, 2, 64, (8, 12, 12), "bf16", 52)
