@@ -354,10 +354,10 @@ __device__ __forceinline__ float inverse_root(float v) {
     const float r = rsqrtf(v);
     return v > 0.f && v < INFINITY ? fmaf(0.5f * r, fmaf(-v * r, r, 1.f), r) : r;
 }
-// s / d: the product with 1 / d and what it leaves (equal values have their value as mean).
+// s / d: the product with 1 / d and what it leaves; an infinite sum stays one.
 __device__ __forceinline__ float mean_of(float s, float d, float over_d) {
     const float m = s * over_d;
-    return fmaf(fmaf(-m, d, s), over_d, m);
+    return fabsf(m) <= FLT_MAX ? fmaf(fmaf(-m, d, s), over_d, m) : m;
 }
 
 // The rows of a row group: first, first + stride, ..; and the most that a group of the block has.
