@@ -478,8 +478,11 @@ LA_API la_status la_gated_step(const void* a, const void* b, int a_dtype, int dt
  *   i mod groups: groups = H gives every head of [T, H, d] its own, groups = 1
  *   shares one.  groups must divide rows.  NULL weight is 1, NULL bias 0.
  *   mean, rstd: NULL or fp32 [rows], what la_layer_norm_backward reads.
- *   Statistics are fp32, the variance from deviations (no cancellation of
- *   large means); y is rounded once.  d <= LA_MAX_NORM_D.  eps >= 0.
+ *   Statistics are fp32: a mean that is large against the row's spread is within
+ *   its own rounding (equal values have their value as mean), and the variance
+ *   comes from deviations (no cancellation of large means).  A row whose fp32 sum
+ *   is infinite has that mean, and no finite y.  y is rounded once.
+ *   d <= LA_MAX_NORM_D.  eps >= 0.
  */
 LA_API la_status la_layer_norm(const void* x, const float* weight, const float* bias, int dtype, int64_t rows,
                                int groups, int d, float eps, void* y, float* mean, float* rstd, void* stream);

@@ -4,8 +4,9 @@
 // and dy and writes dx once.  A row stays in the registers of the L lanes that
 // share it (E vectors of N values each) between the sums over it and its
 // output; the variance comes from the deviations in registers, not from sums of
-// squares.  Rows of up to 64 vectors share a warp, longer ones take a block.  A
-// group works on U rows at once so that their sums overlap, and each lane copies
+// squares (and a row whose mean is large against them is done once more, with a
+// corrected mean).  Rows of up to 64 vectors share a warp, longer ones take a block.
+// A group works on U rows at once so that their sums overlap, and each lane copies
 // its vectors of the next turns to shared memory ahead (asynchronous copies that
 // it alone waits for): what is in flight does not cost registers.  Where a row
 // takes a block, its warps meet at one barrier a turn: in the forward they
@@ -112,14 +113,6 @@ __device__ __forceinline__ float lane_sum(float x) {
     return x;
 }
 constexpr int power_of_two(int n) { return n <= 1 ? 1 : 2 * power_of_two((n + 1) / 2); }
-// Sum of value(w) over a block's warps, in every lane: as many lanes as there are warps take one each, again
-// and again across the warp.
-template <int Warps, typename F>
-__device__ __forceinline__ float warps_sum(int lane, F value) {
-    constexpr int kWidth = power_of_two(Warps);
-    const int w = lane % kWidth;
-    return lane_sum<kWidth>(w < Warps ? value(w) : 0.f);
-}
 // The sums over a row group's L lanes of M values (two or four); every lane gets them.  Where a group is a block, a
 // step across lanes halves what each lane still sums as long as there are several values (M = 4: six exchanges
 // instead of 20), and the warps' sums are taken up the same way.  `scratch` holds two turns and `turn` chooses: one
@@ -341,7 +334,8 @@ __device__ __forceinline__ void staged_params(typename S::P* w, const typename S
 #pragma unroll
     for (int k = 0; k < S::n; ++k) w[k] = place[(e * S::n + k) * S::kThreads];
 }
-__device__ __forceinline__ const float* row_of(const float* p, int64_t at) { return p ? p + at : nullptr; }
+template <typename F>
+__device__ __forceinline__ F* row_of(F* p, int64_t at) { return p ? p + at : nullptr; }
 // The first element of row `row` within its 16 bytes.
 template <typename S>
 __device__ __forceinline__ int shift_of(int64_t row, int d) {
@@ -354,10 +348,61 @@ __device__ __forceinline__ float inverse_root(float v) {
     const float r = rsqrtf(v);
     return v > 0.f && v < INFINITY ? fmaf(0.5f * r, fmaf(-v * r, r, 1.f), r) : r;
 }
-// s / d: the product with 1 / d and what it leaves; an infinite sum stays one.
-__device__ __forceinline__ float mean_of(float s, float d, float over_d) {
-    const float m = s * over_d;
-    return fabsf(m) <= FLT_MAX ? fmaf(fmaf(-m, d, s), over_d, m) : m;
+// A mean more than 16 times as large as the spread (or a variance that is not finite): the rounding of the row's sum,
+// which is relative to the mean, shows in what is taken about it.
+__device__ __forceinline__ bool far_mean(float mean, float var) {
+    const float part = mean * 0.0625f, rest = fmaf(-part, part, var);
+    return !(rest >= 0.f && rest <= FLT_MAX);
+}
+// The sums over a row group's L lanes of two values; every lane gets them.  Its barriers keep what other lanes wrote
+// before and after apart.
+template <int L>
+__device__ __forceinline__ float2 group_sums(float a, float b, float2* scratch) {
+    a = lane_sum<(L < 32 ? L : 32)>(a);
+    b = lane_sum<(L < 32 ? L : 32)>(b);
+    if constexpr (L > 32) {
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = make_float2(a, b);
+        __syncthreads();
+        a = b = 0.f;
+        for (int w = 0; w < L / 32; ++w) {
+            a += scratch[w].x;
+            b += scratch[w].y;
+        }
+    } else {
+        __syncwarp();
+    }
+    return make_float2(a, b);
+}
+// Such a row once more (d = 0: nothing to do for this row group), its y, mean and rstd written anew: the first mean
+// corrected by that of the deviations from it (its error is then its own rounding, and equal values have their value
+// as mean), and the squares of the deviations from that.  A row without a finite mean keeps the first.
+template <int L, typename T>
+__device__ __forceinline__ void far_row(const T* x, const float* weight, const float* bias, int d, float over_d,
+                                        float eps, float mu, int lane, float2* scratch, T* y, float* mean,
+                                        float* rstd) {
+    float t = 0.f, q = 0.f;
+#pragma unroll 1
+    for (int c = lane; c < d; c += L) t += (float)x[c] - mu;
+    const float off = group_sums<L>(t, 0.f, scratch).x * over_d;
+    if (fabsf(off) <= FLT_MAX) mu += off;
+    t = 0.f;
+#pragma unroll 1
+    for (int c = lane; c < d; c += L) {
+        const float f = (float)x[c] - mu;
+        t += f;
+        q = fmaf(f, f, q);
+    }
+    const float2 s = group_sums<L>(t, q, scratch);
+    q = s.y <= FLT_MAX ? fmaxf(fmaf(-s.x, s.x * over_d, s.y), 0.f) : s.y;      // about the unrounded mean
+    const float rs = inverse_root(fmaf(q, over_d, eps));
+#pragma unroll 1
+    for (int c = lane; c < d; c += L)
+        y[c] = T(fmaf(((float)x[c] - mu) * rs, weight ? weight[c] : 1.f, bias ? bias[c] : 0.f));
+    if (lane == 0 && d > 0) {
+        if (mean) *mean = mu;
+        if (rstd) *rstd = rs;
+    }
 }
 
 // The rows of a row group: first, first + stride, ..; and the most that a group of the block has.
@@ -378,14 +423,20 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
     using A = typename ForwardPlan<T, S>::A;
     constexpr bool kBlock = S::L > 32;                       // a row takes the block
     constexpr int kWarps = S::L / 32;
-    __shared__ float2 scratch[kBlock ? 2 * U * kWarps : 1];
+    __shared__ float2 scratch[kBlock ? (2 * U + 1) * kWarps : 1];
     extern __shared__ uint4 ahead[];                         // [depth][U][E][kThreads]
     const int64_t first = (int64_t)blockIdx.x * S::kRows + threadIdx.x / S::L, step = stride * d;
     const int shift = shift_of<S>(first, d);
     const int lane = threadIdx.x % S::L, col = lane * S::N - shift;
     const Edges<S, T> edges(col, d);
     const int left = edges.left, before = edges.before;
-    const float fd = (float)d, over_d = 1.f / fd;
+    const float over_d = 1.f / (float)d;
+    // of a row's columns, those of this warp, and those of the warp that this lane takes up
+    constexpr int kWidth = power_of_two(kWarps);
+    const int takes = (threadIdx.x & 31) % kWidth;
+    const float over_columns = kBlock ? 1.f / fmaxf((float)warp_columns<S>(threadIdx.x >> 5, d, shift), 1.f) : over_d;
+    const float n = kBlock && takes < kWarps ? (float)warp_columns<S>(takes, d, shift) : 0.f;
+    const float over_n = 1.f / fmaxf(n, 1.f);
     // the group's weights stay where the registers allow it
     constexpr bool kHeld = S::kValues <= kHeldValues;
     using P = typename S::P;
@@ -432,6 +483,7 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
         if (A::on) wait_copies<A::depth - 1>();
         Vec<T, S::N> v[U][S::E];
         float s[U], q[U];
+        bool far = false;
 #pragma unroll
         for (int u = 0; u < U; ++u)
             load_row<S, T>(v[u], A::on ? mine + ((turn % A::depth) * U + u) * S::E * S::kThreads : nullptr,
@@ -454,11 +506,9 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
             for (int e = 0; e < S::E; ++e) keep_packed(v[u][e]);
         // deviations from the mean, of the warp's own columns where a row takes several warps
         float mean_here[U];
-        const float columns = kBlock ? (float)warp_columns<S>(threadIdx.x >> 5, d, shift) : fd;
-        const float over_columns = kBlock ? 1.f / fmaxf(columns, 1.f) : over_d;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            mean_here[u] = mean_of(s[u], columns, over_columns);
+            mean_here[u] = s[u] * over_columns;
             const P minus = psplat<P>(-mean_here[u]);
             P t = psplat<P>(0.f);
 #pragma unroll
@@ -482,13 +532,10 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
             __syncthreads();
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const float all = warps_sum<kWarps>(wl, [&](int w) { return half[u * kWarps + w].x; });
-                mean_here[u] = mean_of(all, fd, over_d);
-                q[u] = warps_sum<kWarps>(wl, [&](int w) {
-                    const float2 o = half[u * kWarps + w];
-                    const float n = (float)warp_columns<S>(w, d, shift), off = n > 0.f ? o.x / n - mean_here[u] : 0.f;
-                    return fmaf(n * off, off, o.y);
-                });
+                const float2 of = takes < kWarps ? half[u * kWarps + takes] : make_float2(0.f, 0.f);
+                mean_here[u] = lane_sum<kWidth>(of.x) * over_d;
+                const float off = fmaf(of.x, over_n, -mean_here[u]);
+                q[u] = lane_sum<kWidth>(fmaf(n * off, off, of.y));
             }
         }
 #pragma unroll
@@ -498,7 +545,8 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (turn * U + u >= have.mine) continue;
-            const float mu = mean_here[u], rs = inverse_root(fmaf(q[u], over_d, eps));
+            const float mu = mean_here[u], var = q[u] * over_d, rs = inverse_root(var + eps);
+            far |= far_mean(mu, var);
             const P minus = psplat<P>(-mu), times = psplat<P>(rs);
 #pragma unroll
             for (int e = 0; e < S::E; ++e) {
@@ -526,6 +574,18 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
             if (lane == 0) {
                 if (mean) mean[row + u * stride] = mu;
                 if (rstd) rstd[row + u * stride] = rs;
+            }
+        }
+        // (after the turn: in its middle the branch cost 8 percent more; rows of a block: the same in all of it)
+        if (__any_sync(0xffffffffu, far)) {
+            const int64_t first_col = first % groups * d;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const bool mine_far = turn * U + u < have.mine && far_mean(mean_here[u], q[u] * over_d);
+                const int64_t r = row + u * stride;
+                far_row<S::L>(x + r * d, row_of(weight, first_col), row_of(bias, first_col), mine_far ? d : 0, over_d,
+                              eps, mean_here[u], lane, scratch + (kBlock ? 2 * U * kWarps : 0), y + r * d,
+                              row_of(mean, r), row_of(rstd, r));
             }
         }
         if (!A::on) next_x += U * step;
