@@ -25,6 +25,11 @@
 // thread block waits for are held by thread blocks already running, and the
 // earliest unfinished tile never waits.
 //
+// A product of gates (up to one) below fp32's normal range is off by up to 2^-150 for each of at most 32 tokens of a
+// warp, 4 warps and 8 tiles, so by less than 2^-144, and what a state of up to 2^20 adds through it by less than
+// 2^-124.  A larger state (an infinite one stays infinite however often it is halved) goes through the tokens of such
+// a run one by one (Channel).  Looking out for these runs costs 1 to 2 percent, 6 with odd bf16 rows.
+//
 // A tile that holds a sequence boundary publishes kCutTag for A: B is the state
 // that leaves it whatever entered, so no value crosses from one sequence to
 // another.  For the adjoint, token order is reversed and a boundary is a last
@@ -36,6 +41,8 @@
 // the first copies and the last tiles.  Beyond that the stages are what bounds it: a tile keeps its
 // place in shared memory while its entering state is on the way (with states that are at once there the
 // first of these takes 91 us).
+#include <float.h>
+
 #include "ops/ops.h"
 #include "ops/vec.cuh"
 #include "tc_ptx.cuh"
@@ -204,36 +211,154 @@ struct Shared {
 // A published run cuts when a boundary lies in it: what enters does not reach what leaves.
 __device__ __forceinline__ bool cuts_off(float2 run) { return __float_as_uint(run.x) == kCutTag; }
 __device__ __forceinline__ float through(float2 run, float s) { return cuts_off(run) ? run.y : fmaf(run.x, s, run.y); }
+// Whether a product A of gates says too little about a state s that enters: below the normal range, with a large s.
+// (NaN stays NaN.)
+__device__ __forceinline__ bool inexact(float smallest_a, float largest_s) {
+    return smallest_a < FLT_MIN && !(largest_s <= 0x1p20f);
+}
+// The same for several runs at once: no run of them is inexact where this is not.
+struct Extremes {
+    float a = FLT_MAX, s = 0.f;
+    __device__ __forceinline__ void add(float2 run, float s_enters) {
+        a = fminf(a, fabsf(run.x));            // (kCutTag is a NaN, which neither takes)
+        s = fmaxf(s, fabsf(s_enters));
+    }
+    __device__ __forceinline__ bool inexact() const { return la::inexact(a, s); }
+};
+
+// A channel's rows in scan order, counted in places from the first tile's first (the adjoint: from the last tile's
+// end, which may lie behind the last row).
+template <typename TA, typename TX, bool Rev>
+struct Channel {
+    const TA* a;
+    const TX* x;
+    int64_t C, T, places;
+    int c;
+
+    // The recurrence from s over n places from `at` on, none of which cuts.
+    __device__ __forceinline__ float walk(float s, int64_t at, int n) const {
+        const int64_t lo = Rev ? places - at - n : at, end = min64(lo + n, T);
+        if (c >= C) return s;
+        constexpr int kAhead = 2;             // rows whose loads are under way together (eight take registers from the
+                                              // callers: the adjoint of 32768 x 512 in bf16 52 us instead of 48)
+        for (int64_t i = 0; lo + i < end; i += kAhead) {
+            float gate[kAhead], in[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int64_t t = Rev ? end - 1 - i - k : lo + i + k;
+                const bool there = t >= lo && t < end;
+                // (the array's last row cuts: the adjoint's gate of a row that does not, a_{t+1}, is there)
+                gate[k] = there ? (float)a[(t + (Rev ? 1 : 0)) * C + c] : 0.f;
+                in[k] = there ? (float)x[t * C + c] : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (lo + i + k < end) s = fmaf(gate[k], s, in[k]);
+        }
+        return s;
+    }
+    __device__ __forceinline__ float exactly(float2 run, float s, int64_t at, int n) const {
+        return !cuts_off(run) && !isnan(s) && inexact(fabsf(run.x), fabsf(s)) ? walk(s, at, n) : through(run, s);
+    }
+};
+template <typename TA, typename TX, bool Rev>
+__device__ __forceinline__ Channel<TA, TX, Rev> channel_of(const GatedParams& p, int c, int64_t places) {
+    return {static_cast<const TA*>(p.a), static_cast<const TX*>(p.x), p.C, p.T, places, c};
+}
 
 // The word of warp w's run (two channels each) that holds A of channel ch; B is two words on.
 __device__ __forceinline__ float* run_word(float4 (*run)[32], int w, int ch) {
     return reinterpret_cast<float*>(&run[w][ch >> 1]) + (ch & 1);
 }
 
+// s through the runs of a tile's W warps of K tokens each, the tile at place `at`, in channel ch; Leave: the state that
+// enters each warp is left in the place of its A.
+template <typename TA, typename TX, bool Rev, int W, int K, bool Leave>
+__device__ __noinline__ float exactly_warps(const GatedParams& p, float4 (*run)[32], const int* warp_cut, bool cut_tile,
+                                            int tiles, int slice, int ch, float s, int64_t at) {
+    const auto channel = channel_of<TA, TX, Rev>(p, slice * kSlice + ch, (int64_t)tiles * (W * K));
+#pragma unroll 1
+    for (int w = 0; w < W; ++w) {
+        const float a = run_word(run, w, ch)[0], b = run_word(run, w, ch)[2];
+        if (Leave) run_word(run, w, ch)[0] = s;
+        s = cut_tile && warp_cut[w] ? b : channel.exactly(make_float2(a, b), s, at + w * K, K);
+    }
+    return s;
+}
+
 // The tile's run in channel ch as it is published, from those of its warps.
-template <int W>
-__device__ __forceinline__ float2 tile_run(float4 (*run)[32], const int* warp_cut, bool cut_tile, int ch) {
+template <typename TA, typename TX, bool Rev, int W, int K>
+__device__ __forceinline__ float2 tile_run(const GatedParams& p, float4 (*run)[32], const int* warp_cut, bool cut_tile,
+                                           int tiles, int order, int slice, int ch) {
     float2 own = make_float2(1.f, 0.f);
+    Extremes of;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
         const float a = run_word(run, w, ch)[0], b = run_word(run, w, ch)[2];
+        if (w > 0) of.add(make_float2(a, b), own.y);      // (zero enters the first)
         own.y = cut_tile && warp_cut[w] ? b : fmaf(a, own.y, b);
         own.x *= a;
     }
+    if (__builtin_expect(of.inexact(), 0))
+        own.y = exactly_warps<TA, TX, Rev, W, K, false>(p, run, warp_cut, cut_tile, tiles, slice, ch, 0.f,
+                                                        (int64_t)order * (W * K));
     return make_float2(cut_tile ? __uint_as_float(kCutTag) : settable(own.x), settable(own.y));
+}
+
+// What look_back has found to be inexact, once more from what is published: all that its lane leaves and publishes.
+template <typename TA, typename TX, bool Rev, int W, int K>
+__device__ __noinline__ void look_back_exactly(const GatedParams& p, float4 (*run)[32], const int* warp_cut,
+                                               bool cut_tile, bool fresh, float2 own, int tiles, int order, int slice,
+                                               int ch) {
+    constexpr int kTile = W * K, kGroupTokens = kGroup * kTile;
+    const auto channel = channel_of<TA, TX, Rev>(p, slice * kSlice + ch, (int64_t)tiles * kTile);
+    const int q = order % kGroup, group = order / kGroup, g = group % kGroup, super = group / kGroup;
+    const int64_t at = (int64_t)order * kTile;
+    const float2* tile_runs = p.run + (int64_t)(order - q) * p.Cpad + channel.c;
+    float A = 1.f, B = 0.f, s = 0.f;
+    bool cut = false;
+#pragma unroll 1
+    for (int i = 0; i < q; ++i) {
+        const float2 r = peek(tile_runs + (int64_t)i * p.Cpad);
+        cut |= cuts_off(r);
+        B = channel.exactly(r, B, at + (i - q) * kTile, kTile);
+        A *= r.x;
+    }
+    if (q == kGroup - 1) {
+        B = channel.exactly(own, B, at, kTile);
+        A = cut || cut_tile ? __uint_as_float(kCutTag) : settable(A * own.x);
+        publish(p.joint + (int64_t)group * p.Cpad + channel.c, make_float2(A, settable(B)));
+    }
+    if (!fresh) {
+        if (!cut) {
+            if (super > 0) s = peek(p.state + (int64_t)(super - 1) * p.Cpad + channel.c);
+#pragma unroll 1
+            for (int i = 0; i < g; ++i)
+                s = channel.exactly(peek(p.joint + (int64_t)(group - g + i) * p.Cpad + channel.c), s,
+                                    (int64_t)(group - g + i) * kGroupTokens, kGroupTokens);
+        }
+#pragma unroll 1
+        for (int i = 0; i < q; ++i)
+            s = channel.exactly(peek(tile_runs + (int64_t)i * p.Cpad), s, at + (i - q) * kTile, kTile);
+    }
+    const float left = exactly_warps<TA, TX, Rev, W, K, true>(p, run, warp_cut, cut_tile, tiles, slice, ch, s, at);
+    if (order % kSuper == kSuper - 1) publish(p.state + (int64_t)super * p.Cpad + channel.c, settable(left));
 }
 
 // What a look-back lane does for its channel ch of a tile whose run `own` is published: finds the
 // state that enters the tile and leaves in the place of each warp's A the state that enters that
 // warp.  `fresh`: nothing enters.  Every wait is bounded; a lane whose wait runs out records it and
 // takes zero.
-template <int W>
+template <typename TA, typename TX, bool Rev, int W, int K>
 __device__ __forceinline__ void look_back(const GatedParams& p, float4 (*run)[32], const int* warp_cut, bool cut_tile,
-                                          bool fresh, float2 own, int order, int slice, int ch, bool forced) {
+                                          bool fresh, float2 own, int tiles, int order, int slice, int ch,
+                                          bool forced) {
     const int c = slice * kSlice + ch;
     const int q = order % kGroup, group = order / kGroup, g = group % kGroup, super = group / kGroup;
     const bool joins = q == kGroup - 1, leaves = order % kSuper == kSuper - 1;
     float s = 0.f;
+    Extremes of;                         // of all the runs below
+    bool late = false;                   // a wait has run out
     if (!fresh || joins) {
         const long long start = clock64(), limit = forced ? kForcedClocks : kWaitClocks;
         const float2* tile_runs = p.run + (int64_t)(order - q) * p.Cpad + c;
@@ -242,7 +367,6 @@ __device__ __forceinline__ void look_back(const GatedParams& p, float4 (*run)[32
         float2 r[kGroup - 1], j[kGroup - 1];
         float sup = __uint_as_float(kUnset);
         unsigned polls = 0;
-        bool late = false;
         auto run_out = [&]() {
             if ((++polls & 15) == 0 && (clock64() - start > limit ||
                                         *(volatile int*)&p.hdr->error == LA_DEVERR_WAIT_TIMEOUT)) {
@@ -278,12 +402,14 @@ __device__ __forceinline__ void look_back(const GatedParams& p, float4 (*run)[32
             float A = 1.f, B = 0.f;
 #pragma unroll
             for (int i = 0; i < kGroup - 1; ++i) {
+                if (i > 0) of.add(r[i], B);
                 B = through(r[i], B);
                 A *= r[i].x;
             }
+            of.add(own, B);
             B = through(own, B);
             A = cut || cut_tile ? __uint_as_float(kCutTag) : settable(A * own.x);
-            publish(p.joint + (int64_t)group * p.Cpad + c, make_float2(A, settable(B)));
+            if (!of.inexact() || late) publish(p.joint + (int64_t)group * p.Cpad + c, make_float2(A, settable(B)));
         }
         // the groups of the block, needed unless a boundary lies in the group
         if (!fresh && !cut) {
@@ -304,23 +430,37 @@ __device__ __forceinline__ void look_back(const GatedParams& p, float4 (*run)[32
             s = super > 0 ? sup : 0.f;
 #pragma unroll
             for (int i = 0; i < kGroup - 1; ++i)
-                if (i < g) s = through(j[i], s);
+                if (i < g) {
+                    of.add(j[i], s);
+                    s = through(j[i], s);
+                }
         }
         if (!fresh) {
 #pragma unroll
             for (int i = 0; i < kGroup - 1; ++i)
-                if (i < q) s = through(r[i], s);
+                if (i < q) {
+                    of.add(r[i], s);
+                    s = through(r[i], s);
+                }
         }
         if (late) s = 0.f;
     }
-    if (leaves) publish(p.state + (int64_t)super * p.Cpad + c, settable(through(own, s)));
-    float e = s;
+    float e[W + 1];                      // the states that enter the warps
+    e[0] = s;
+    if (leaves) of.add(own, s);
 #pragma unroll
     for (int w = 0; w < W; ++w) {
         const float a = run_word(run, w, ch)[0], b = run_word(run, w, ch)[2];
-        run_word(run, w, ch)[0] = e;
-        e = cut_tile && warp_cut[w] ? b : fmaf(a, e, b);
+        of.add(make_float2(a, b), e[w]);
+        e[w + 1] = cut_tile && warp_cut[w] ? b : fmaf(a, e[w], b);
     }
+    if (__builtin_expect(of.inexact() && !late, 0)) {
+        look_back_exactly<TA, TX, Rev, W, K>(p, run, warp_cut, cut_tile, fresh, own, tiles, order, slice, ch);
+        return;
+    }
+    if (leaves) publish(p.state + (int64_t)super * p.Cpad + c, settable(through(own, s)));
+#pragma unroll
+    for (int w = 0; w < W; ++w) run_word(run, w, ch)[0] = e[w];
 }
 
 // first[i] / last[i]: the sequence whose first / last token is row t0 + i, else -1; n rows, and
@@ -360,8 +500,8 @@ __device__ void pass_empty(const GatedParams& p, int threads) {
 // whose elements no asynchronous copy can fetch (32768 x 1001: 243 us, bound by loads of two bytes).
 // The same warps, tokens and order of operations as the ring's: the same results.
 template <typename TA, typename TX, bool Rev, bool Vec, int W, int K, int PerSm>
-__global__ void __launch_bounds__((W + 2) * 32, PerSm) gated_scan_kernel(GatedParams p, int tiles, int slices,
-                                                                         int solo) {
+__global__ void __launch_bounds__((W + 2) * 32, PerSm)
+gated_scan_kernel(const __grid_constant__ GatedParams p, int tiles, int slices, int solo) {
     __shared__ Shared<W, K> sh;
     constexpr int kTile = W * K, kThreads = (W + 2) * 32;   // the last two warps look back
     static_assert(kTile >= kMinTile, "the workspace holds ceil(T / kMinTile) tiles");
@@ -476,16 +616,12 @@ __global__ void __launch_bounds__((W + 2) * 32, PerSm) gated_scan_kernel(GatedPa
         if (!work && !solo) {
             const bool fresh = marked && (Rev ? sh.last[n - 1] : sh.first[0]) >= 0;   // nothing enters
             const int ch = threadIdx.x - W * 32;
-            const float2 own = tile_run<W>(sh.run, sh.cut, cut_tile, ch);
+            const float2 own = tile_run<TA, TX, Rev, W, K>(p, sh.run, sh.cut, cut_tile, tiles, order, slice, ch);
             publish(p.run + (int64_t)order * p.Cpad + slice * kSlice + ch, own);
-            look_back<W>(p, sh.run, sh.cut, cut_tile, fresh, own, order, slice, ch, forced);
-        } else if (!work && warp == W) {
-            float2 s = make_float2(0.f, 0.f);
-            for (int w = 0; w < W; ++w) {
-                const float4 q = sh.run[w][lane];
-                *reinterpret_cast<float2*>(&sh.run[w][lane]) = s;
-                s = sh.cut[w] ? make_float2(q.z, q.w) : fma2(make_float2(q.x, q.y), s, make_float2(q.z, q.w));
-            }
+            look_back<TA, TX, Rev, W, K>(p, sh.run, sh.cut, cut_tile, fresh, own, tiles, order, slice, ch, forced);
+        } else if (!work) {
+            const int ch = threadIdx.x - W * 32;
+            exactly_warps<TA, TX, Rev, W, K, true>(p, sh.run, sh.cut, true, tiles, slice, ch, 0.f, 0);
         }
         Two<TX> rh[Rev ? K : 1];
         if (Rev && work) {
@@ -642,7 +778,7 @@ __device__ __forceinline__ void copy_rows(uint8_t* place, const void* from, int6
 // over_slices: 2^64 / slices, rounded up; 0 for one slice.
 template <typename TA, typename TX, bool Rev, Copies Copy, int W, int K, int S>
 __global__ void __launch_bounds__(Ring<TA, TX, Rev, Copy, W, K, S>::kThreads, 1)
-gated_ring_kernel(GatedParams p, int tiles, int slices, unsigned long long over_slices,
+gated_ring_kernel(const __grid_constant__ GatedParams p, int tiles, int slices, unsigned long long over_slices,
                   const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_x,
                   const __grid_constant__ CUtensorMap map_h) {
     using R = Ring<TA, TX, Rev, Copy, W, K, S>;
@@ -810,7 +946,8 @@ gated_ring_kernel(GatedParams p, int tiles, int slices, unsigned long long over_
             const int order = sh.order[st], slice = sh.slice[st];
             const bool cut_tile = sh.seq[st] & kCut;
             if (publisher) {
-                const float2 own = tile_run<W>(sh.run[st], sh.cut[st], cut_tile, ch);
+                const float2 own =
+                    tile_run<TA, TX, Rev, W, K>(p, sh.run[st], sh.cut[st], cut_tile, tiles, order, slice, ch);
                 publish(p.run + (int64_t)order * p.Cpad + slice * kSlice + ch, own);
                 sh.own[st][ch] = own;
             } else {
@@ -818,7 +955,8 @@ gated_ring_kernel(GatedParams p, int tiles, int slices, unsigned long long over_
                 const int64_t t0 = (int64_t)(Rev ? tiles - 1 - order : order) * R::kRows;
                 const int edge = Rev ? (int)min64(R::kRows, p.T - t0) - 1 : 0;
                 const bool fresh = cut_tile && (Rev ? sh.last[st] : sh.first[st])[edge] >= 0;
-                look_back<W>(p, sh.run[st], sh.cut[st], cut_tile, fresh, sh.own[st][ch], order, slice, ch, forced);
+                look_back<TA, TX, Rev, W, K>(p, sh.run[st], sh.cut[st], cut_tile, fresh, sh.own[st][ch], tiles, order,
+                                             slice, ch, forced);
             }
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(publisher ? &sh.sent[st] : &sh.carried[st]);
