@@ -526,9 +526,9 @@ LA_API size_t la_layer_norm_backward_workspace_bytes(int dtype, int64_t rows, in
  *   inverse:   1 turns by the negated angle: the inverse, and the gradient (the
  *              rotation is orthogonal, so dq = inverse rotation of dq_out).
  *   q_out, k_out: as q, k; q_out may be q itself and k_out k itself.
- *   Angles are reduced modulo a whole turn in 64-bit fixed point, so far
- *   positions are as accurate as an fp64 product; cos and sin are fp32 and
- *   outputs are rounded once.  A non-finite frequency gives NaN in its pair.
+ *   Angles are reduced modulo a whole turn in 64-bit fixed point, within
+ *   |position| (2^-63 + 2^-106 |freq|) turns, so far positions and large
+ *   frequencies lose nothing; cos and sin are fp32 and outputs are rounded once.  A non-finite frequency gives NaN in its pair.
  *   d <= LA_MAX_ROTARY_D.  T = 0 enqueues nothing.
  */
 LA_API la_status la_rotary(const void* q, const void* k, const float* freq, const int32_t* positions, int dtype,
