@@ -508,7 +508,7 @@ LA_API la_status la_layer_norm_backward(const void* x, const void* dy, const flo
                                         void* stream);
 
 /* la_layer_norm_backward_workspace_bytes - scratch size for la_layer_norm_backward
- *   (0 for arguments it rejects). */
+ *   on the current device (0 for arguments it rejects, or without a device). */
 LA_API size_t la_layer_norm_backward_workspace_bytes(int dtype, int64_t rows, int groups, int d);
 
 /*

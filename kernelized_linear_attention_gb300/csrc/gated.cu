@@ -1157,13 +1157,6 @@ GatedLayout gated_layout(int64_t T, int C) {
     return lo;
 }
 
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    return n;
-}
-
 // More than one tile: the preparation, then a persistent kernel that may start while it ends.
 template <typename F, typename... Args>
 cudaError_t launch_tiles(F kernel, const GatedParams& p, int reverse, int tile_tokens, int tiles, int slices,

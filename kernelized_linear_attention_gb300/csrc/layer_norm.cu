@@ -35,7 +35,6 @@ namespace la {
 
 namespace {
 
-constexpr int kSms = 152;
 constexpr int kHeldValues = 16;         // forward: weights and biases of so many columns a lane stay in registers
 constexpr int kCopyBytes = 64 * 1024;   // of rows copied ahead, per SM
 constexpr int kShiftRegisters = 16;      // for where in its vectors a row starts and ends
@@ -865,7 +864,7 @@ struct Args {
     const void *x, *dy;
     const float *weight, *bias, *mean_in, *rstd_in;
     int64_t rows;
-    int groups, d;
+    int groups, d, sms;
     float eps;
     void* out;
     float *mean, *rstd;
@@ -878,8 +877,8 @@ int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 // As many blocks as there are rows for, at most those that run at once (a few more would take as long again), a
 // multiple of `unit`.
 template <typename Plan, typename S>
-int64_t blocks_for(int64_t rows, int64_t unit) {
-    const int64_t most = (int64_t)kSms * Plan::per_sm, wanted = rows > S::kRows ? ceil_div(rows, S::kRows) : 1;
+int64_t blocks_for(int64_t rows, int64_t unit, int sms) {
+    const int64_t most = (int64_t)sms * Plan::per_sm, wanted = rows > S::kRows ? ceil_div(rows, S::kRows) : 1;
     const int64_t blocks = ceil_div(wanted, unit) * unit;
     return blocks <= most ? blocks : most >= unit ? most / unit * unit : unit;
 }
@@ -892,19 +891,20 @@ int64_t whole_turns(int groups, int d) {
 }
 // Weight rows of a block of the backward (see the kernel).
 template <typename Plan, typename S>
-int weights_of_block(int groups) {
+int weights_of_block(int groups, int sms) {
     if (S::kRows % groups == 0) return groups;
-    return groups <= kSms * Plan::per_sm ? 1 : S::kRows;
+    return groups <= sms * Plan::per_sm ? 1 : S::kRows;
 }
 template <typename Plan, typename S>
-int64_t backward_blocks(int64_t rows, int groups, int d) {
+int64_t backward_blocks(int64_t rows, int groups, int d, int sms) {
     const int64_t unit = whole_turns<S>(groups, d);
-    return blocks_for<Plan, S>(rows, weights_of_block<Plan, S>(groups) == 1 ? lcm(unit, groups) : unit);
+    return blocks_for<Plan, S>(rows, weights_of_block<Plan, S>(groups, sms) == 1 ? lcm(unit, groups) : unit, sms);
 }
 // Rows of the matrix of partial sums.
 template <typename Plan, typename S>
-int64_t slots(int64_t rows, int groups, int d) {
-    return rows > 0 ? backward_blocks<Plan, S>(rows, groups, d) * weights_of_block<Plan, S>(groups) / groups : 0;
+int64_t slots(int64_t rows, int groups, int d, int sms) {
+    if (rows <= 0) return 0;
+    return backward_blocks<Plan, S>(rows, groups, d, sms) * weights_of_block<Plan, S>(groups, sms) / groups;
 }
 
 template <typename K>
@@ -918,7 +918,7 @@ struct Forward {
     template <typename T, typename S>
     static int64_t run(const Args& a) {
         using Plan = ForwardPlan<T, S>;
-        const int64_t blocks = blocks_for<Plan, S>(a.rows, whole_turns<S>(a.groups, a.d));
+        const int64_t blocks = blocks_for<Plan, S>(a.rows, whole_turns<S>(a.groups, a.d), a.sms);
         const cudaError_t e = allow_shared(layer_norm_kernel<T, S>, Plan::bytes);
         if (e != cudaSuccess) return (int64_t)e;
         layer_norm_kernel<T, S><<<(unsigned)blocks, S::kThreads, Plan::bytes, a.stream>>>(
@@ -932,8 +932,8 @@ struct Backward {
     template <typename T, typename S>
     static int64_t run(const Args& a) {
         using Plan = BackwardPlan<T, S>;
-        const int64_t blocks = backward_blocks<Plan, S>(a.rows, a.groups, a.d);
-        const int weights = weights_of_block<Plan, S>(a.groups);
+        const int64_t blocks = backward_blocks<Plan, S>(a.rows, a.groups, a.d, a.sms);
+        const int weights = weights_of_block<Plan, S>(a.groups, a.sms);
         const size_t join = a.part && weights < S::kRows ? sizeof(float2) * S::kRows * (size_t)a.d : 0;
         const size_t smem = join > Plan::bytes ? join : Plan::bytes;
         const cudaError_t e = allow_shared(layer_norm_backward_kernel<T, S>, smem);
@@ -947,7 +947,7 @@ struct Backward {
 struct Slots {
     static constexpr bool kForward = false;
     template <typename T, typename S>
-    static int64_t run(const Args& a) { return slots<BackwardPlan<T, S>, S>(a.rows, a.groups, a.d); }
+    static int64_t run(const Args& a) { return slots<BackwardPlan<T, S>, S>(a.rows, a.groups, a.d, a.sms); }
 };
 
 // The lanes and vectors of a row.  One vector a lane, or two where the forward has bf16 rows (half the
@@ -1006,11 +1006,12 @@ int64_t by_type(const Args& a, int dtype, RowLayout layout) {
 
 bool on_16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-int64_t slots_for(int dtype, int64_t rows, int groups, int d, RowLayout layout) {
+int64_t slots_for(int dtype, int64_t rows, int groups, int d, int sms, RowLayout layout) {
     Args a{};
     a.rows = rows;
     a.groups = groups;
     a.d = d;
+    a.sms = sms;
     return by_type<Slots>(a, dtype, layout);
 }
 // rows: the arrays of rows start on 16 bytes; weights: the arrays of weights too.
@@ -1022,16 +1023,19 @@ cudaError_t layer_norm(const void* x, const float* weight, const float* bias, in
                        int d, float eps, void* y, float* mean, float* rstd, cudaStream_t s) {
     Args a{};
     a.x = x; a.weight = weight; a.bias = bias;
-    a.rows = rows; a.groups = groups; a.d = d; a.eps = eps;
+    a.rows = rows; a.groups = groups; a.d = d; a.sms = sm_count(); a.eps = eps;
+    if (a.sms <= 0) return cudaErrorInvalidDevice;
     a.out = y; a.mean = mean; a.rstd = rstd; a.stream = s;
     return (cudaError_t)by_type<Forward>(a, dtype, layout_of(on_16(x) && on_16(y), on_16(weight) && on_16(bias)));
 }
 
 // Covers every layout of the rows: the choice between them goes by the call's pointers.
 size_t layer_norm_backward_workspace_bytes(int dtype, int64_t rows, int groups, int d) {
+    const int sms = sm_count();
+    if (sms <= 0) return 0;
     int64_t most = 0;
     for (RowLayout l : {kElements, kShifted, kVectors}) {
-        const int64_t n = slots_for(dtype, rows, groups, d, l);
+        const int64_t n = slots_for(dtype, rows, groups, d, sms, l);
         if (n > most) most = n;
     }
     return align_up(sizeof(float2) * (size_t)most * groups * d, kAlign) + kAlign;
@@ -1043,7 +1047,8 @@ cudaError_t layer_norm_backward(const void* x, const void* dy, const float* weig
     const RowLayout layout = layout_of(on_16(x) && on_16(dy) && on_16(dx), on_16(weight));
     Args a{};
     a.x = x; a.dy = dy; a.weight = weight; a.mean_in = mean; a.rstd_in = rstd;
-    a.rows = rows; a.groups = groups; a.d = d;
+    a.rows = rows; a.groups = groups; a.d = d; a.sms = sm_count();
+    if (a.sms <= 0) return cudaErrorInvalidDevice;
     a.out = dx; a.stream = s;
     a.part = dweight || dbias ? static_cast<float2*>(workspace) : nullptr;
     if (rows > 0) {
@@ -1051,7 +1056,7 @@ cudaError_t layer_norm_backward(const void* x, const void* dy, const float* weig
         if (e != cudaSuccess) return e;
     }
     if (!a.part) return cudaSuccess;
-    const int64_t n = (int64_t)groups * d, M = rows > 0 ? slots_for(dtype, rows, groups, d, layout) : 0;
+    const int64_t n = (int64_t)groups * d, M = rows > 0 ? slots_for(dtype, rows, groups, d, a.sms, layout) : 0;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -5,6 +5,14 @@
 
 namespace la {
 
+// SMs of the current device; 0 where it cannot be asked.
+inline int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return n;
+}
+
 // Gated linear recurrence (gated.cu), forward (reverse = 0) and its adjoint (reverse = 1).
 struct GatedParams {
     const void* a;             // [T][C] gates
@@ -37,7 +45,7 @@ cudaError_t gated_step(const void* a, const void* b, int a_dtype, int dtype, int
 // Layer norm (layer_norm.cu).
 cudaError_t layer_norm(const void* x, const float* weight, const float* bias, int dtype, int64_t rows, int groups,
                        int d, float eps, void* y, float* mean, float* rstd, cudaStream_t s);
-size_t layer_norm_backward_workspace_bytes(int dtype, int64_t rows, int groups, int d);
+size_t layer_norm_backward_workspace_bytes(int dtype, int64_t rows, int groups, int d);   // 0: no device
 cudaError_t layer_norm_backward(const void* x, const void* dy, const float* weight, const float* mean,
                                 const float* rstd, int dtype, int64_t rows, int groups, int d, void* dx,
                                 float* dweight, float* dbias, void* workspace, cudaStream_t s);

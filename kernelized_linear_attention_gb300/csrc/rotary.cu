@@ -3,9 +3,8 @@
 //
 // Angles.  A position is an integer, so freq / 2 pi as a 64-bit fixed-point
 // fraction of a turn times the position, modulo 2^64, is the angle modulo one
-// turn.  The fraction comes from the quotient in two doubles, the second what the
-// first has rounded away, so it is off by 2^-63 + 2^-106 |freq| turns at most, and
-// the angle by |position| times that.  Read as a signed number it is an angle in
+// turn.  The fraction is off by 2^-63 + 2^-106 |freq| turns at most, and the angle
+// by |position| times that.  Read as a signed number it is an angle in
 // [-pi, pi); rounded to fp32, by pi 2^-25 at most, it goes through fp32 cos and sin,
 // whose own error is of that size.
 //
@@ -230,7 +229,7 @@ int groups_of(int pairs) { return pairs < kRotaryThreads ? kRotaryThreads / pair
 uint32_t reciprocal(int n) { return n > 1 ? (uint32_t)(0xffffffffu / (uint32_t)n) + 1 : 0; }
 
 template <typename T, int N>
-cudaError_t run(const RotaryParams& p, cudaStream_t s) {
+cudaError_t run(const RotaryParams& p, int sms, cudaStream_t s) {
     RotaryPlan plan{};
     plan.heads = p.k ? 2 * p.H : p.H;
     plan.pair_units = p.interleaved && N > 1 ? 2 * p.P / N : p.P / N;
@@ -242,7 +241,7 @@ cudaError_t run(const RotaryParams& p, cudaStream_t s) {
     const int64_t per_token = (int64_t)plan.share * plan.units, rest = ceil_div(plan.heads, plan.share);
     int64_t tokens = ceil_div((int64_t)kUnits * kRotaryThreads, per_token);
     tokens = min64(tokens, 32 * 1024 / ((int64_t)sizeof(float2) * p.P));
-    tokens = min64(tokens, p.T * rest / 152);
+    tokens = min64(tokens, p.T * rest / sms);
     if (tokens < 1) tokens = 1;
     plan.tokens = (int)tokens;
     plan.groups = groups_of(p.P);
@@ -258,14 +257,14 @@ cudaError_t run(const RotaryParams& p, cudaStream_t s) {
 // Tokens per block of the staged form: as many as kStagedBytes hold, but no fewer blocks than SMs for it; 0 where
 // not even the fewest whose rows are whole vectors fit.
 template <typename T>
-int64_t staged_tokens(const RotaryParams& p) {
+int64_t staged_tokens(const RotaryParams& p, int sms) {
     constexpr int N = 16 / sizeof(T);
     const int64_t row = (int64_t)p.H * p.d, arrays = p.k ? 2 : 1;
     int64_t step = 1;
     while (step * row % N) step *= 2;
     const int64_t bytes = arrays * row * (int64_t)sizeof(T), table = (int64_t)sizeof(float2) * p.P;
     if (step * (bytes + table) > kMostStaged) return 0;
-    int64_t tokens = min64(min64(kStagedBytes / bytes, kMostStaged / (bytes + table)), p.T / 152);
+    int64_t tokens = min64(min64(kStagedBytes / bytes, kMostStaged / (bytes + table)), p.T / sms);
     tokens = tokens / step * step;
     return tokens > step ? tokens : step;
 }
@@ -282,14 +281,16 @@ cudaError_t run_staged(const RotaryParams& p, int64_t tokens, cudaStream_t s) {
 template <typename T>
 cudaError_t dispatch(const RotaryParams& p, cudaStream_t s) {
     constexpr int N = 16 / sizeof(T);
+    const int sms = sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
     // every unit starts on 16 bytes: the pointers, the rows, and where the second half and the tail begin
     const uintptr_t at = reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.k) |
                          reinterpret_cast<uintptr_t>(p.q_out) | reinterpret_cast<uintptr_t>(p.k_out);
-    if (at % 16 == 0 && p.d % N == 0 && (p.interleaved ? 2 : 1) * p.P % N == 0) return run<T, N>(p, s);
+    if (at % 16 == 0 && p.d % N == 0 && (p.interleaved ? 2 : 1) * p.P % N == 0) return run<T, N>(p, sms, s);
     // (32768 x 9 x 77 in bf16: 46 us, pair by pair 84; 32768 x 8 x 128 with 43 pairs 53 and 152; 4099 x 7 x 83 in
     // fp32 12.5 and 14.6)
-    const int64_t tokens = at % 16 == 0 ? staged_tokens<T>(p) : 0;
-    return tokens > 0 ? run_staged<T>(p, tokens, s) : run<T, 1>(p, s);
+    const int64_t tokens = at % 16 == 0 ? staged_tokens<T>(p, sms) : 0;
+    return tokens > 0 ? run_staged<T>(p, tokens, s) : run<T, 1>(p, sms, s);
 }
 
 }  // namespace
