@@ -496,12 +496,13 @@ __device__ void pass_empty(const GatedParams& p, int threads) {
     }
 }
 
-// Tiles held in registers, one at a time per block: single tiles, and bf16 arrays that do not start on four bytes,
-// whose elements no asynchronous copy can fetch (32768 x 1001: 243 us, bound by loads of two bytes).
+// Tiles held in registers, one at a time per block: a single tile of tokens (Solo), and bf16 arrays that do not start on
+// four bytes, whose elements no asynchronous copy can fetch (32768 x 1001: 243 us, bound by loads of two bytes).
 // The same warps, tokens and order of operations as the ring's: the same results.
-template <typename TA, typename TX, bool Rev, bool Vec, int W, int K, int PerSm>
-__global__ void __launch_bounds__((W + 2) * 32, PerSm)
-gated_scan_kernel(const __grid_constant__ GatedParams p, int tiles, int slices, int solo) {
+constexpr int kRegisterBlocks = 2;       // per SM
+template <typename TA, typename TX, bool Rev, bool Vec, bool Solo, int W, int K>
+__global__ void __launch_bounds__((W + 2) * 32, Solo ? 1 : kRegisterBlocks)
+gated_scan_kernel(const __grid_constant__ GatedParams p, int tiles, int slices) {
     __shared__ Shared<W, K> sh;
     constexpr int kTile = W * K, kThreads = (W + 2) * 32;   // the last two warps look back
     static_assert(kTile >= kMinTile, "the workspace holds ceil(T / kMinTile) tiles");
@@ -512,8 +513,8 @@ gated_scan_kernel(const __grid_constant__ GatedParams p, int tiles, int slices, 
     const int64_t C = p.C;
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (solo) {
-        // a single tile of tokens: no other kernel has looked at the arguments
+    if constexpr (Solo) {
+        // no other kernel has looked at the arguments
         const bool bad = malformed(p);
         if (blockIdx.x == 0 && threadIdx.x == 0) {
             p.hdr->error = bad ? LA_DEVERR_CU_SEQLENS : LA_DEVERR_NONE;
@@ -524,13 +525,13 @@ gated_scan_kernel(const __grid_constant__ GatedParams p, int tiles, int slices, 
     } else if (p.hdr->error == LA_DEVERR_CU_SEQLENS) {
         return;
     }
-    const bool forced = !solo && *(volatile int*)&g_force_timeout != 0;
+    const bool forced = !Solo && *(volatile int*)&g_force_timeout != 0;
 
     pass_empty(p, kThreads);
 
     const int total = tiles * slices;
-    int ticket = solo ? blockIdx.x : 0;
-    if (!solo) {
+    int ticket = blockIdx.x;
+    if constexpr (!Solo) {
         if (threadIdx.x == 0) sh.ticket = atomicAdd(p.ticket, 1);
         __syncthreads();
         ticket = sh.ticket;
@@ -560,10 +561,10 @@ gated_scan_kernel(const __grid_constant__ GatedParams p, int tiles, int slices, 
             }
         }
         int next = 0;
-        if (!solo && threadIdx.x == 0) next = atomicAdd(p.ticket, 1);
+        if (!Solo && threadIdx.x == 0) next = atomicAdd(p.ticket, 1);
 
         // --- boundaries
-        const int ts = solo ? kMarked | kCut : p.tile_seq[tile];
+        const int ts = Solo ? kMarked | kCut : p.tile_seq[tile];
         const bool cut_tile = ts & kCut, marked = ts & kMarked;
         if (marked) {
             clear_marks(kTile, sh.first, sh.last, threadIdx.x, kThreads);
@@ -613,7 +614,7 @@ gated_scan_kernel(const __grid_constant__ GatedParams p, int tiles, int slices, 
         __syncthreads();
 
         // --- the tile's run goes out, and the state that enters it is found
-        if (!work && !solo) {
+        if (!work && !Solo) {
             const bool fresh = marked && (Rev ? sh.last[n - 1] : sh.first[0]) >= 0;   // nothing enters
             const int ch = threadIdx.x - W * 32;
             const float2 own = tile_run<TA, TX, Rev, W, K>(p, sh.run, sh.cut, cut_tile, tiles, order, slice, ch);
@@ -669,7 +670,7 @@ gated_scan_kernel(const __grid_constant__ GatedParams p, int tiles, int slices, 
                     store_edge(p.edge_out + (int64_t)(Rev ? sh.first : sh.last)[j0 + k] * C + c, left, leaving);
             }
         }
-        if (solo) return;
+        if (Solo) return;
         ticket = sh.next;
         __syncthreads();      // the next tile overwrites the shared runs and marks
     }
@@ -776,14 +777,14 @@ __device__ __forceinline__ void copy_rows(uint8_t* place, const void* from, int6
 }
 
 // over_slices: 2^64 / slices, rounded up; 0 for one slice.
-template <typename TA, typename TX, bool Rev, Copies Copy, int W, int K, int S>
+// Vec: outputs that take two channels of every row in one store.
+template <typename TA, typename TX, bool Rev, Copies Copy, bool Vec, int W, int K, int S>
 __global__ void __launch_bounds__(Ring<TA, TX, Rev, Copy, W, K, S>::kThreads, 1)
 gated_ring_kernel(const __grid_constant__ GatedParams p, int tiles, int slices, unsigned long long over_slices,
                   const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_x,
                   const __grid_constant__ CUtensorMap map_h) {
     using R = Ring<TA, TX, Rev, Copy, W, K, S>;
     constexpr bool Tma = Copy == kTiles, kOdd = Copy == kHalves;
-    constexpr bool Vec = Tma || (!kOdd && (sizeof(TA) == 2 || sizeof(TX) == 2));     // rows of even length
     static_assert(R::kRows >= kMinTile, "the workspace holds ceil(T / kMinTile) tiles");
     constexpr int kLookers = R::kLookers, kTeams = R::kTeams;
     // Who takes every n-th tile waits for phases of its own tiles only, one after the other, when n
@@ -1101,7 +1102,7 @@ gated_ring_kernel(const __grid_constant__ GatedParams p, int tiles, int slices, 
                             prev = p.state_in ? edge_two(p.state_in + (int64_t)sq * p.C + c, left)
                                               : make_float2(0.f, 0.f);
                             const TA* gate = static_cast<const TA*>(p.a) + row + k * (int64_t)p.C;
-                            if (p.edge_out) leaving = mul2(load_two<Vec>(gate, left).get(), s);
+                            if (p.edge_out) leaving = mul2(load_two<false>(gate, left).get(), s);
                         }
                         store_two<Vec>(da + k * (int64_t)p.C, left, mul2(s, prev));
                     }
@@ -1182,16 +1183,17 @@ cudaError_t launch_tiles(F kernel, const GatedParams& p, int reverse, int tile_t
     return cudaLaunchKernelEx(&cfg, kernel, p, tiles, slices, args...);
 }
 
-template <typename TA, typename TX, bool Rev, bool Vec, int W, int K, int PerSm>
+template <typename TA, typename TX, bool Rev, bool Vec, bool Solo, int W, int K>
 cudaError_t run_registers(const GatedParams& p, int slices, cudaStream_t s) {
     constexpr int kTile = W * K, kThreads = (W + 2) * 32;
     const int tiles = (int)ceil_div(p.T, kTile);
-    auto kernel = gated_scan_kernel<TA, TX, Rev, Vec, W, K, PerSm>;
-    if (tiles <= 1) {
-        kernel<<<slices, kThreads, 0, s>>>(p, tiles, slices, 1);
+    auto kernel = gated_scan_kernel<TA, TX, Rev, Vec, Solo, W, K>;
+    if constexpr (Solo) {
+        kernel<<<slices, kThreads, 0, s>>>(p, tiles, slices);
         return cudaGetLastError();
+    } else {
+        return launch_tiles(kernel, p, Rev ? 1 : 0, kTile, tiles, slices, kRegisterBlocks, kThreads, 0, s);
     }
-    return launch_tiles(kernel, p, Rev ? 1 : 0, kTile, tiles, slices, PerSm, kThreads, 0, s, 0);
 }
 
 using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
@@ -1219,7 +1221,7 @@ bool row_map(CUtensorMap* m, const void* base, int64_t tokens, int C, int rows) 
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename TA, typename TX, bool Rev, Copies Copy, int W, int K, int S>
+template <typename TA, typename TX, bool Rev, Copies Copy, bool Vec, int W, int K, int S>
 cudaError_t run_ring(const GatedParams& p, int slices, cudaStream_t s) {
     using R = Ring<TA, TX, Rev, Copy, W, K, S>;
     static_assert(R::kRows % 2 == 0 && K % 2 == 0, "a row's parity is that of its place in the tile");
@@ -1228,7 +1230,7 @@ cudaError_t run_ring(const GatedParams& p, int slices, cudaStream_t s) {
     if (Copy == kTiles && (!row_map<TA>(&ma, p.a, p.T, p.C, R::kRows) || !row_map<TX>(&mx, p.x, p.T, p.C, R::kRows) ||
                 !row_map<TX>(&mh, Rev ? p.h : p.x, p.T, p.C, R::kRows)))
         return cudaErrorInvalidValue;
-    auto kernel = gated_ring_kernel<TA, TX, Rev, Copy, W, K, S>;
+    auto kernel = gated_ring_kernel<TA, TX, Rev, Copy, Vec, W, K, S>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)R::kBytes);
     if (e != cudaSuccess) return e;
     return launch_tiles(kernel, p, Rev ? 1 : 0, R::kRows, (int)ceil_div(p.T, R::kRows), slices, 1, R::kThreads,
@@ -1241,26 +1243,39 @@ bool tile_aligned(const void* p, int C, size_t esize) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (size_t)C * esize % 16 == 0;
 }
 
+// Every row in words of four bytes.
+bool word_aligned(const void* p, int C, size_t esize) {
+    return reinterpret_cast<uintptr_t>(p) % 4 == 0 && (size_t)C * esize % 4 == 0;
+}
+
+// The inputs' places choose how tiles come in, the outputs' how rows go out.
 template <typename TA, typename TX, bool Rev>
 cudaError_t dispatch(const GatedParams& p, int slices, cudaStream_t s) {
-    const bool vec = p.C % 2 == 0 && two_aligned(p.a, sizeof(TA)) && two_aligned(p.da, sizeof(TA)) &&
-                     two_aligned(p.x, sizeof(TX)) && two_aligned(p.h, sizeof(TX)) && two_aligned(p.y, sizeof(TX));
-    const bool tma = vec && tile_aligned(p.a, p.C, sizeof(TA)) && tile_aligned(p.x, p.C, sizeof(TX)) &&
-                     tile_aligned(p.h, p.C, sizeof(TX));
+    constexpr size_t ea = sizeof(TA), ex = sizeof(TX);
+    const bool out = p.C % 2 == 0 && two_aligned(p.y, ex) && two_aligned(p.da, ea);
     // stages that fill shared memory
-    constexpr int kBytes = (int)(sizeof(TA) + (Rev ? 2 : 1) * sizeof(TX));   // of a token and channel
+    constexpr int kBytes = (int)(ea + (Rev ? 2 : 1) * ex);   // of a token and channel
     constexpr int W = 4, K = kBytes <= 4 ? 32 : kBytes <= 10 ? 16 : 8;
     constexpr int S = kBytes <= 4 ? 6 : kBytes <= 6 ? 8 : kBytes <= 8 ? 6 : kBytes <= 10 ? 4 : 8;
-    if (p.T > W * K) {
-        if (tma) return run_ring<TA, TX, Rev, kTiles, W, K, S>(p, slices, s);
-        if (vec || (sizeof(TA) == 4 && sizeof(TX) == 4)) return run_ring<TA, TX, Rev, kWords, W, K, S>(p, slices, s);
-        auto on_4 = [](const void* q) { return reinterpret_cast<uintptr_t>(q) % 4 == 0; };
-        if constexpr (sizeof(TA) == 2 || sizeof(TX) == 2)
-            if (p.C % 2 == 1 && on_4(p.a) && on_4(p.x) && on_4(p.h))
-                return run_ring<TA, TX, Rev, kHalves, W, K, Rev && kBytes == 6 ? 6 : S>(p, slices, s);
+    if (p.T <= W * K) {
+        const bool vec = out && two_aligned(p.a, ea) && two_aligned(p.x, ex) && two_aligned(p.h, ex);
+        return vec ? run_registers<TA, TX, Rev, true, true, W, K>(p, slices, s)
+                   : run_registers<TA, TX, Rev, false, true, W, K>(p, slices, s);
     }
-    return vec ? run_registers<TA, TX, Rev, true, W, K, 2>(p, slices, s)
-               : run_registers<TA, TX, Rev, false, W, K, 2>(p, slices, s);
+    if (out && tile_aligned(p.a, p.C, ea) && tile_aligned(p.x, p.C, ex) && tile_aligned(p.h, p.C, ex))
+        return run_ring<TA, TX, Rev, kTiles, true, W, K, S>(p, slices, s);
+    if constexpr (ea == 4 && ex == 4) {
+        return run_ring<TA, TX, Rev, kWords, false, W, K, S>(p, slices, s);
+    } else {
+        if (word_aligned(p.a, p.C, ea) && word_aligned(p.x, p.C, ex) && word_aligned(p.h, p.C, ex))
+            return out ? run_ring<TA, TX, Rev, kWords, true, W, K, S>(p, slices, s)
+                       : run_ring<TA, TX, Rev, kWords, false, W, K, S>(p, slices, s);
+        // (rows of even length start on four bytes with their array)
+        const bool starts = word_aligned(p.a, 2, ea) && word_aligned(p.x, 2, ex) && word_aligned(p.h, 2, ex);
+        if (p.C % 2 == 1 && starts)
+            return run_ring<TA, TX, Rev, kHalves, false, W, K, Rev && kBytes == 6 ? 6 : S>(p, slices, s);
+        return run_registers<TA, TX, Rev, false, false, W, K>(p, slices, s);
+    }
 }
 
 template <typename TA, typename TX>
