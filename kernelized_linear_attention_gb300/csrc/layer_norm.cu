@@ -77,7 +77,9 @@ struct Ahead {
 template <typename T, typename S>
 struct ForwardPlan {
     static constexpr int U = S::E == 1 ? 2 : 1;
-    static constexpr int registers = U * row_registers<T, S>() + (S::kShift ? kShiftRegisters : 0) +
+    // (two vectors of bf16: with 16 registers for the shift as elsewhere 32768 x 1001 take 46 us instead of 41)
+    static constexpr int registers = U * row_registers<T, S>() +
+                                     (S::kShift ? (S::N == 8 ? 2 : 1) * kShiftRegisters : 0) +
                                      (S::kValues <= kHeldValues ? 2 * S::kValues + 38 : 52);
     static constexpr int by_registers = blocks_per_sm(S::kThreads, registers);
     using A = Ahead<T, S, U, 1, by_registers>;
@@ -373,32 +375,72 @@ __device__ __forceinline__ float2 group_sums(float a, float b, float2* scratch) 
     }
     return make_float2(a, b);
 }
-// Such a row once more (d = 0: nothing to do for this row group), its y, mean and rstd written anew: the first mean
-// corrected by that of the deviations from it (its error is then its own rounding, and equal values have their value
-// as mean), and the squares of the deviations from that.  A row without a finite mean keeps the first.
-template <int L, typename T>
-__device__ __forceinline__ void far_row(const T* x, const float* weight, const float* bias, int d, float over_d,
-                                        float eps, float mu, int lane, float2* scratch, T* y, float* mean,
-                                        float* rstd) {
-    float t = 0.f, q = 0.f;
+// Such a row once more (not `mine`: of another row group), its y, mean and rstd written anew: the first mean corrected
+// by that of the deviations from it (its error is then its own rounding, and equal values have their value as mean), and
+// the squares of the deviations from that.  A row without a finite mean keeps the first.  The lane's vectors come from
+// where load_row found them; loops that are not unrolled, as this is rare and must not crowd what is not.
+template <typename S, typename T>
+__device__ __forceinline__ void far_row(bool mine, const uint4* place, const T* x, const float* weight,
+                                        const float* bias, const Edges<S, T>& edges, float over_d, float eps, float mu,
+                                        float2* scratch, T* y, float* mean, float* rstd) {
+    constexpr int kStep = S::L * S::N;
+    const int left = mine ? edges.left : 0;
+    // each of the row's vectors that this lane holds: its number and its values
+    const auto vectors = [&](auto f) {
 #pragma unroll 1
-    for (int c = lane; c < d; c += L) t += (float)x[c] - mu;
-    const float off = group_sums<L>(t, 0.f, scratch).x * over_d;
+        for (int e = 0; e * kStep < left; ++e) {
+            Vec<T, S::N> v;
+            if constexpr (S::N > 1) v = *reinterpret_cast<const Vec<T, S::N>*>(place + e * S::kThreads);
+            else v = *reinterpret_cast<const Vec<T, S::N>*>(x + e * kStep);
+            float q[S::N];
+            unpack(q, v);
+            f(e, q);
+        }
+    };
+    float t = 0.f, t2 = 0.f;
+    vectors([&](int e, float (&q)[S::N]) {
+#pragma unroll
+        for (int k = 0; k < S::N; ++k)
+            if (!S::kShift || edges.in(e, k)) t += q[k] - mu;
+    });
+    const float off = group_sums<S::L>(t, 0.f, scratch).x * over_d;
     if (fabsf(off) <= FLT_MAX) mu += off;
     t = 0.f;
-#pragma unroll 1
-    for (int c = lane; c < d; c += L) {
-        const float f = (float)x[c] - mu;
-        t += f;
-        q = fmaf(f, f, q);
-    }
-    const float2 s = group_sums<L>(t, q, scratch);
-    q = s.y <= FLT_MAX ? fmaxf(fmaf(-s.x, s.x * over_d, s.y), 0.f) : s.y;      // about the unrounded mean
-    const float rs = inverse_root(fmaf(q, over_d, eps));
-#pragma unroll 1
-    for (int c = lane; c < d; c += L)
-        y[c] = T(fmaf(((float)x[c] - mu) * rs, weight ? weight[c] : 1.f, bias ? bias[c] : 0.f));
-    if (lane == 0 && d > 0) {
+    vectors([&](int e, float (&q)[S::N]) {
+#pragma unroll
+        for (int k = 0; k < S::N; ++k)
+            if (!S::kShift || edges.in(e, k)) {
+                const float c = q[k] - mu;
+                t += c;
+                t2 = fmaf(c, c, t2);
+            }
+    });
+    const float2 sums = group_sums<S::L>(t, t2, scratch);
+    // about the unrounded mean
+    const float squares = sums.y <= FLT_MAX ? fmaxf(fmaf(-sums.x, sums.x * over_d, sums.y), 0.f) : sums.y;
+    const float rs = inverse_root(fmaf(squares, over_d, eps));
+    vectors([&](int e, float (&q)[S::N]) {
+        const int at = e * kStep;
+        typename S::P we[S::n], be[S::n], c[S::n];
+        load_vector_params<S>(we, weight, e, left, edges.before, 1.f);
+        load_vector_params<S>(be, bias, e, left, edges.before, 0.f);
+        Vec<float, S::N> f;
+#pragma unroll
+        for (int k = 0; k < S::N; ++k) f.v[k] = !S::kShift || edges.in(e, k) ? (q[k] - mu) * rs : 0.f;
+        unpack_pairs<S::N>(c, f);
+#pragma unroll
+        for (int k = 0; k < S::n; ++k) c[k] = pfma(c[k], we[k], be[k]);
+        Vec<T, S::N> o;
+        pack_pairs<S::N>(o, c);
+        if (!edges.partial(e)) {
+            *reinterpret_cast<Vec<T, S::N>*>(y + at) = o;
+        } else {
+#pragma unroll
+            for (int k = 0; k < S::N; ++k)
+                if (edges.in(e, k)) y[at + k] = element(o, k);
+        }
+    });
+    if (mine && threadIdx.x % S::L == 0) {
         if (mean) *mean = mu;
         if (rstd) *rstd = rs;
     }
@@ -577,14 +619,13 @@ layer_norm_kernel(const T* x, const float* weight, const float* bias, int64_t ro
         }
         // (after the turn: in its middle the branch cost 8 percent more; rows of a block: the same in all of it)
         if (__any_sync(0xffffffffu, far)) {
-            const int64_t first_col = first % groups * d;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const bool mine_far = turn * U + u < have.mine && far_mean(mean_here[u], q[u] * over_d);
-                const int64_t r = row + u * stride;
-                far_row<S::L>(x + r * d, row_of(weight, first_col), row_of(bias, first_col), mine_far ? d : 0, over_d,
-                              eps, mean_here[u], lane, scratch + (kBlock ? 2 * U * kWarps : 0), y + r * d,
-                              row_of(mean, r), row_of(rstd, r));
+                far_row<S, T>(mine_far, mine + ((turn % A::depth) * U + u) * S::E * S::kThreads, next_x + u * step,
+                              row_of(weight, at), row_of(bias, at), edges, over_d, eps, mean_here[u],
+                              scratch + (kBlock ? 2 * U * kWarps : 0), next_y + u * step,
+                              row_of(mean, row + u * stride), row_of(rstd, row + u * stride));
             }
         }
         if (!A::on) next_x += U * step;
