@@ -4,9 +4,9 @@
 // Angles.  A position is an integer, so freq / 2 pi as a 64-bit fixed-point
 // fraction of a turn times the position, modulo 2^64, is the angle modulo one
 // turn.  The fraction is off by 2^-63 + 2^-106 |freq| turns at most, and the angle
-// by |position| times that.  Read as a signed number it is an angle in
-// [-pi, pi); rounded to fp32, by pi 2^-25 at most, it goes through fp32 cos and sin,
-// whose own error is of that size.
+// by |position| times that.  What is left of it beside whole quarters of a turn, pi / 4
+// at most, is rounded to 2^-32 turns and to fp32, by pi 2^-27 in all, and goes through
+// fp32 cos and sin.
 //
 // Bound by memory: each channel is read and written once.  A block turns a few
 // tokens: its threads first issue the loads of their channels, then compute the
@@ -70,8 +70,12 @@ __device__ __forceinline__ Turn turn_of(const RotaryParams& p, int j) {
 __device__ __forceinline__ float2 cos_sin(const RotaryParams& p, const Turn& turn, int64_t t) {
     const long long position = p.positions[t * p.naxes + turn.axis];
     const unsigned long long angle = turn.fraction * (unsigned long long)position;
-    float s, c;
-    sincospif((float)(long long)angle * 0x1p-63f, &s, &c);
+    // the nearest quarter of a turn apart, so that fp32 rounds what is left: an eighth at most, in units of 2^-32
+    const uint32_t turns = (uint32_t)(angle >> 32), quarter = (turns + (1u << 29)) >> 30;
+    float s0, c0;
+    sincospif((float)(int)(turns - (quarter << 30)) * 0x1p-31f, &s0, &c0);
+    float s = __uint_as_float(__float_as_uint(quarter & 1 ? c0 : s0) ^ (quarter & 2) << 30);
+    float c = __uint_as_float(__float_as_uint(quarter & 1 ? s0 : c0) ^ (quarter + 1 & 2) << 30);
     if (!turn.finite) s = c = __int_as_float(0x7fc00000);
     return make_float2(c, p.inverse ? -s : s);
 }

@@ -57,3 +57,21 @@ def test_angles_of_many_turns(la, scale, far):
     bound = ((math.pi / 2 + 4) * U + off) * (np.abs(x0) + np.abs(x1))
     got = la.la_rotary(x.cuda(), None, freq.cuda(), pos.cuda(), [P]).cpu().double().numpy()[:, 0]
     check(got, ref, np.concatenate([bound, bound], 1), "f32", "rotary")
+
+
+@pytest.mark.parametrize("far", [1000, 1 << 20])
+@pytest.mark.parametrize("inverse", [False, True])
+def test_what_fp32_rounds_of_an_angle(la, far, inverse):
+    """The pair (1, 0) turns into cos and sin themselves.  An angle is rounded beside whole quarters of a turn: by pi 2^-27,
+    (pi / 8) u; each value is within a step of it, 2 u of itself.  So where one of them is almost zero it is within
+    (pi / 8) u, not within the rounding of a whole turn.  (fp64 angles here are off by 2^20 2^-53 radians, 2^-9 u.)"""
+    g = torch.Generator().manual_seed(far)
+    T, P = 20000, 32
+    x = torch.cat([torch.ones(T, 1, P), torch.zeros(T, 1, P)], -1)
+    freq = (10000.0 ** (-torch.arange(P, dtype=torch.float64) / P)).float()
+    pos = torch.randint(-far, far, (T,), generator=g).to(torch.int32)
+    angle = pos.double()[:, None] * freq.double() * (-1 if inverse else 1)
+    ref = np.concatenate([angle.cos().numpy(), angle.sin().numpy()], 1)
+    bound = (math.pi / 8 + 2 ** -8) * U + 2 * U * np.abs(ref)
+    got = la.la_rotary(x.cuda(), None, freq.cuda(), pos.cuda(), [P], inverse=inverse).cpu().double().numpy()[:, 0]
+    check(got, ref, bound, "f32", "rotary")
