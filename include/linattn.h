@@ -407,7 +407,7 @@ LA_API int la_selected_path(int causal, int map, int dtype, int d_k, int d_v, in
  *   the causal recurrence of la_forward with r = 1 and phi(k) = 1 ("The Kernel
  *   Zoo" §1.3) whose state is scaled by a gate before each token is added.
  */
-#define LA_MAX_CHANNELS (1 << 20)   /* H * d of the gated recurrence              */
+#define LA_MAX_CHANNELS (1 << 20)   /* H * d of the gated recurrence, groups * d of the layer norm */
 #define LA_MAX_NORM_D 16384         /* row width of the layer norm                */
 #define LA_MAX_ROTARY_D 1024        /* head size of the rotary positions          */
 #define LA_MAX_AXES 4               /* position axes of the rotary positions      */
@@ -467,7 +467,7 @@ LA_API size_t la_gated_scan_workspace_bytes(int has_cu_seqlens, int nseq, int64_
  *   + b, h = state_out rounded to dtype.  a: [B, H, d] of a_dtype; b, h:
  *   [B, H, d] of dtype; state_in, state_out: fp32 [B, H, d], the same array for
  *   an update in place.  The arithmetic is la_gated_scan's for one token.
- *   B = 0 enqueues nothing.  Needs no workspace.
+ *   H * d <= LA_MAX_CHANNELS.  B = 0 enqueues nothing.  Needs no workspace.
  */
 LA_API la_status la_gated_step(const void* a, const void* b, int a_dtype, int dtype, int B, int H, int d,
                                const float* state_in, float* state_out, void* h, void* stream);
@@ -484,8 +484,9 @@ LA_API la_status la_gated_step(const void* a, const void* b, int a_dtype, int dt
  *   Statistics are fp32: a mean that is large against the row's spread is within
  *   its own rounding (equal values have their value as mean), and the variance
  *   comes from deviations (no cancellation of large means).  A row whose fp32 sum
- *   is infinite has that mean, and no finite y.  y is rounded once.
- *   d <= LA_MAX_NORM_D.  eps >= 0.
+ *   is infinite has that mean, and no finite y; one whose squared deviations
+ *   overflow in sum has rstd 0.  y is rounded once.  d <= LA_MAX_NORM_D,
+ *   groups * d <= LA_MAX_CHANNELS (LA_ERR_UNSUPPORTED beyond).  eps >= 0.
  */
 LA_API la_status la_layer_norm(const void* x, const float* weight, const float* bias, int dtype, int64_t rows,
                                int groups, int d, float eps, void* y, float* mean, float* rstd, void* stream);
