@@ -35,9 +35,9 @@
 // another.  For the adjoint, token order is reversed and a boundary is a last
 // token.
 //
-// Measured (GB300, 6.76 TB/s copies): 65536 x 1024 with fp32 gates and bf16 rows 109 us, 4.9 TB/s; all
-// bf16 96 us; 40009 x 512 fp32 in 64 sequences 61 us, 4.0 TB/s; the adjoint of 8 x 4096 x 512 bf16
-// 46 us, 3.7 TB/s, of 65536 x 512 with fp32 gates 92 us, 5.1 TB/s.  About 12 us of each are the preparation,
+// Measured (GB300, 6.76 TB/s copies): 65536 x 1024 with fp32 gates and bf16 rows 111 us, 4.8 TB/s; all
+// bf16 97 us; 40009 x 512 fp32 in 64 sequences 63 us, 3.9 TB/s; the adjoint of 8 x 4096 x 512 bf16
+// 47 us, 3.6 TB/s, of 65536 x 512 with fp32 gates 93 us, 5.0 TB/s.  About 12 us of each are the preparation,
 // the first copies and the last tiles.  Beyond that the stages are what bounds it: a tile keeps its
 // place in shared memory while its entering state is on the way (with states that are at once there the
 // first of these takes 91 us).
@@ -497,7 +497,7 @@ __device__ void pass_empty(const GatedParams& p, int threads) {
 }
 
 // Tiles held in registers, one at a time per block: a single tile of tokens (Solo), and bf16 arrays that do not start on
-// four bytes, whose elements no asynchronous copy can fetch (32768 x 1001: 243 us, bound by loads of two bytes).
+// four bytes, whose elements no asynchronous copy can fetch (32768 x 1002: 273 us, bound by loads of two bytes).
 // The same warps, tokens and order of operations as the ring's: the same results.
 constexpr int kRegisterBlocks = 2;       // per SM
 template <typename TA, typename TX, bool Rev, bool Vec, bool Solo, int W, int K>
@@ -696,10 +696,10 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, long 
 // behind the tiles that follow.
 //
 // Tile copies (kTiles) need rows that start on 16 bytes.  Other rows of four-byte steps are copied by four
-// warps, four bytes a lane, into the same places (kWords: 32768 x 1023 in fp32 116 us; with tiles in registers
+// warps, four bytes a lane, into the same places (kWords: 32768 x 1023 in fp32 119 us; with tiles in registers
 // 182 us).  bf16 rows of odd length, every other of which starts inside four bytes, are copied as the words that
 // hold them, one more a row than they fill, and put together by the lanes that read them (kHalves: 32768 x 1001
-// 113 us; in registers 243 us).
+// 121 us; in registers 243 us).
 // --------------------------------------------------------------------------
 enum Copies { kTiles, kWords, kHalves };
 

@@ -20,12 +20,13 @@
 // kernel adds up by column with compensated sums, in a fixed order.
 //
 // Measured (GB300, 6.76 TB/s copies): bf16 rows with their statistics, 1048576 x 64 with weights per head 46 us,
-// 6.0 TB/s; 8192 x 4096 27 us, 4.9 TB/s; 16384 x 1001 23 us, 2.9 TB/s; fp32 16384 x 768 23 us, 4.4 TB/s.  Gradients
+// 6.0 TB/s; 8192 x 4096 28 us, 4.8 TB/s; 16384 x 1001 25 us, 2.7 TB/s; fp32 16384 x 768 23 us, 4.4 TB/s.  Gradients
 // in bf16: 262144 x 64 per head 31 us, 3.3 TB/s; 8192 x 4096 46 us, 4.4 TB/s; 32768 x 1024 48 us, 4.2 TB/s;
-// 229376 x 128 with 7 heads 43 us, 4.1 TB/s.  The backward issues more than 20 instructions per element (unpacking,
-// the sums across lanes and per column): that bounds it, with the second kernel's launch and its read of the
-// blocks' sums.  More warps with fewer registers are slower (two blocks of 64 registers a thread for 8192 x 4096:
-// 62 us).
+// 229376 x 128 with 7 heads 43 us, 4.1 TB/s.  What bounds the backward is latency: for 8192 x 4096 it takes half of
+// the issue slots (22 M instructions, 18 us of them) and 56 percent of DRAM with a quarter of the warps, one block of
+// 512 threads per SM that meets at a barrier every turn, with one turn of rows on their way; the second kernel's
+// launch and its read of the blocks' sums come on top.  More warps with fewer registers are slower (two blocks of 64
+// registers a thread for 8192 x 4096: 62 us).
 #include <float.h>
 
 #include "ops/ops.h"
@@ -62,8 +63,8 @@ template <typename T, typename S>
 constexpr int row_registers() { return S::kValues * (int)sizeof(T) / 4 > 0 ? S::kValues * (int)sizeof(T) / 4 : 1; }
 
 // How far ahead rows are copied: `depth` turns of U rows (of x, or of x and dy) in a block's share of
-// kCopyBytes, two turns where they are longer, one where two do not fit.  (96 KB per SM and more are no faster:
-// 51 us instead of 48 for 1048576 rows of 64.)  Rows of single elements are loaded when they are needed
+// kCopyBytes, two turns where they are longer, one where two do not fit.  (96 KB per SM and more are no faster in the
+// forward: 51 us instead of 48 for 1048576 rows of 64; the backward was not measured with more.)  Rows of single elements are loaded when they are needed
 // (a copy has at least four bytes).
 template <typename T, typename S, int U, int Arrays, int Blocks>
 struct Ahead {
@@ -73,7 +74,9 @@ struct Ahead {
     static constexpr int depth = most > 8 ? 8 : most >= 2 ? most : 2 * turn_bytes <= 200 * 1024 ? 2 : 1;
     static constexpr size_t bytes = on ? (size_t)depth * turn_bytes : 0;   // a multiple of 16
 };
-// The registers to compile for, and the blocks of an SM that this and the copies' memory allow.
+// The registers to compile for, and the blocks of an SM that this and the copies' memory allow.  Some kernels want a few
+// more and spill them: fp32 gradients of up to 256 columns 4 to 96 bytes a thread, those of rows beyond 8192 columns
+// (beyond 4096 in arrays off 16 bytes) 470 to 800, a few forward ones 4 to 40.
 template <typename T, typename S>
 struct ForwardPlan {
     static constexpr int U = S::E == 1 ? 2 : 1;
@@ -995,8 +998,8 @@ struct Slots {
 // lanes: the sums across lanes are most of its instructions; 27 us instead of 31 for 8192 x 4096.  The
 // backward's sums per column leave no room for two: 59 us instead of 48).  Up to 64 vectors share a
 // warp, two a lane from 32 on, longer rows take a block of up to 512 lanes.
-// Rows that are not whole vectors: by the vectors that hold them (16384 x 1001 in bf16: 23 us, element by
-// element 33 us; 4096 x 5001 37 and 76 us, its gradients 59 and 171 us).  Element by element where an array does not
+// Rows that are not whole vectors: by the vectors that hold them (16384 x 1001 in bf16: 25 us, element by
+// element 33 us; 4096 x 5001 35 and 82 us, its gradients 59 and 171 us).  Element by element where an array does not
 // start on 16 bytes, and for the gradients of rows of a few warps (65536 x 300 in bf16: 64 us, as vectors 68 us;
 // 16384 x 1001 fp32 46 and 55 us; 4096 x 1023 bf16 17 and 19 us): the sums per column of lanes that hold
 // vectors fill the registers, and blocks as small as that leave more of them to join.

@@ -16,9 +16,9 @@
 // allows it.  Other rows are turned in shared memory, or pair by pair where
 // the arrays do not start on 16 bytes or a few tokens' rows do not fit there.
 //
-// Measured (GB300, 6.76 TB/s copies): q and k of 65536 x 16 x 64 in bf16 82 us, 6.6 TB/s (32768 x 16 x 64 in
-// fp32 80 us); 32768 x 7 x 83 in fp32 52 us, 5.9 TB/s; 32768 x 9 x 77
-// in bf16, bound by instructions per pair, 46 us, 4.0 TB/s.
+// Measured (GB300, 6.76 TB/s copies): q and k of 65536 x 16 x 64 in bf16 81 us, 6.6 TB/s (32768 x 16 x 64 in
+// fp32 80 us); 32768 x 7 x 83 in fp32 53 us, 5.7 TB/s; 32768 x 9 x 77
+// in bf16, bound by instructions per pair, 43 us, 4.2 TB/s.
 #include "ops/ops.h"
 #include "ops/vec.cuh"
 
@@ -53,8 +53,8 @@ __device__ __forceinline__ unsigned long long turn_fraction(float freq) {
     return freq < 0.f ? 0 - r : r;
 }
 
-// What pair j turns by per position: the fraction is fp64 work, which is slow here, and the same for all tokens
-// (30000 x 3 x 201 with 100 pairs: 43 us, 60 with a fraction for every token).
+// What pair j turns by per position: the fraction is the same for all tokens (when all of it was fp64 work, which is slow
+// here, 30000 x 3 x 201 with 100 pairs took 60 us with a fraction for every token; 42 now).
 struct Turn {
     unsigned long long fraction;
     int axis;
@@ -291,7 +291,7 @@ cudaError_t dispatch(const RotaryParams& p, cudaStream_t s) {
     const uintptr_t at = reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.k) |
                          reinterpret_cast<uintptr_t>(p.q_out) | reinterpret_cast<uintptr_t>(p.k_out);
     if (at % 16 == 0 && p.d % N == 0 && (p.interleaved ? 2 : 1) * p.P % N == 0) return run<T, N>(p, sms, s);
-    // (32768 x 9 x 77 in bf16: 46 us, pair by pair 84; 32768 x 8 x 128 with 43 pairs 53 and 152; 4099 x 7 x 83 in
+    // (32768 x 9 x 77 in bf16: 43 us, pair by pair 92; 32768 x 8 x 128 with 43 pairs 51 and 168; 4099 x 7 x 83 in
     // fp32 12.5 and 14.6)
     const int64_t tokens = at % 16 == 0 ? staged_tokens<T>(p, sms) : 0;
     return tokens > 0 ? run_staged<T>(p, tokens, s) : run<T, 1>(p, sms, s);
