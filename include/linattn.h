@@ -425,9 +425,10 @@ LA_API int la_selected_path(int causal, int map, int dtype, int d_k, int d_v, in
  *   combined in an order that depends on T and the types alone, so results are
  *   deterministic.  A state that crosses tiles of tokens is scaled by the
  *   product of their gates.  Gates of magnitude up to one: h is the recurrence's
- *   within fp32 rounding and 2^-124 (products below the normal range); a state
- *   beyond 2^20, an infinite one too, goes through such gates token by token, which
- *   is many times slower.  Gates above one are computed as given as long as the
+ *   within fp32 rounding and 2^-124 (products below the normal range); states
+ *   beyond 2^20 with such products take several times as long, and one that
+ *   outweighs what the tokens add by 2^100, an infinite one too, goes token by
+ *   token, which takes a hundred times as long.  Gates above one are computed as given as long as the
  *   products of consecutive gates stay in fp32's normal range.  A sequence's
  *   values, infinities and NaN among them, never reach another sequence.
  *   cu_seqlens, nseq: as for la_forward.  workspace: device scratch of at least

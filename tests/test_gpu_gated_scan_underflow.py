@@ -140,6 +140,16 @@ def test_states_of_ordinary_size_with_strong_forgetting(la, ta, tb):
 
 
 @pytest.mark.parametrize("ta,tb", KINDS)
+@pytest.mark.parametrize("added", [1e8, 1e30])
+def test_large_values_with_strong_forgetting(la, added, ta, tb):
+    # large states beside inputs of their size: the products are enough (their 2^-144 |s| is 2^-44 of such an input)
+    for d in (64, 63):
+        c = _case([1300, 0, 90, 700], d, ta, tb, (0.2, 0.05), added, (1e9, -1e31, 1.0), 5)
+        c["b"][200:205] = 0.0
+        _check(la, c, ta, tb)
+
+
+@pytest.mark.parametrize("ta,tb", KINDS)
 def test_infinite_states_over_many_tiles(la, ta, tb):
     # every tile goes token by token through all that lies before it in its block of 64 tiles: slow, but no wait runs out
     T, d = 30000, 512
