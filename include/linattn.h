@@ -537,6 +537,93 @@ LA_API la_status la_rotary(const void* q, const void* k, const float* freq, cons
                            int64_t T, int H, int d, const int* pairs, int naxes, int interleaved, int inverse,
                            void* q_out, void* k_out, void* stream);
 
+/*
+ * Linear attention with a decay for each head
+ * -------------------------------------------
+ * The causal recurrence of la_forward with the identity map and LA_NORM_NONE
+ * ("The Kernel Zoo" §1.2-1.3, the fast weight programmer) whose state is scaled
+ * before each token is added:
+ *
+ *     S_t = g S_{t-1} + k_t v_t^T,     out_t = scale q_t^T S_t,     g = exp(log_decay[h]).
+ *
+ *   The source pages have no counterpart of the decay.  Feature maps are applied
+ *   by the caller; a state is fp32 [d_k, d_v] (no z column: there is no
+ *   denominator).  The conventions of the operators around the attention call
+ *   hold (outputs apart from inputs, capture into graphs).
+ *   1 <= d_k <= LA_MAX_DK, 1 <= d_v <= LA_MAX_DV.
+ */
+
+/*
+ * la_decay_attention - out_t for every token of every packed sequence.
+ *   q, k: [T, H, d_k]; v, out: [T, H, d_v], all of dtype.
+ *   log_decay: fp32 [H] (device), natural logarithms, at most 0: 0 forgets
+ *              nothing, -inf everything but the token itself.  Positive ones
+ *              grow, and are computed as given as long as powers over a few
+ *              thousand tokens stay in fp32's range.
+ *   scale:     finite.
+ *   cu_seqlens, nseq: as for la_forward.
+ *   state_in:  NULL (every sequence starts from 0) or fp32 [nseq, H, d_k, d_v].
+ *   state_out: NULL or fp32 [nseq, H, d_k, d_v], the state after each
+ *              sequence's last token; an empty sequence's state_in (or 0) is
+ *              copied.  May be the same array as state_in.
+ *   States and sums are fp32 and decays are carried beyond fp32, so far tokens
+ *   lose nothing; out is rounded once.  Results are deterministic.  A value
+ *   that is not finite reaches its own token and later ones of its sequence
+ *   only.
+ *   workspace: la_decay_attention_workspace_bytes(...) bytes, 256-byte aligned,
+ *   contents on entry do not matter; calls that may overlap need workspaces of
+ *   their own.  Malformed cu_seqlens are recorded in its error word
+ *   (la_workspace_error) and nothing else is written.
+ */
+LA_API la_status la_decay_attention(const void* q, const void* k, const void* v, const float* log_decay, int dtype,
+                                    const int32_t* cu_seqlens, int nseq, int64_t T, int H, int d_k, int d_v,
+                                    float scale, const float* state_in, float* state_out, void* out, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* la_decay_attention_workspace_bytes - scratch size for la_decay_attention on the
+ *   current device (0 for arguments it rejects). */
+LA_API size_t la_decay_attention_workspace_bytes(int dtype, int has_cu_seqlens, int nseq, int64_t T, int H, int d_k,
+                                                 int d_v);
+
+/*
+ * la_decay_attention_backward - gradients of L = sum(dout * out) +
+ *   sum(dstate_out * state_out) for la_decay_attention.  With R_t the gradient
+ *   that reaches S_t,
+ *     R_t = g R_{t+1} + scale q_t dout_t^T     (at a last token: dstate_out + ..),
+ *     dq_t = scale S_t dout_t,  dk_t = R_t v_t,  dv_t = R_t^T k_t,
+ *     dstate_in = g R_t at each first token.
+ *   log_decay is treated as a constant.
+ *   dout: [T, H, d_v]; dq, dk: [T, H, d_k]; dv: [T, H, d_v], of dtype.
+ *   state_in, dstate_out: as NULL they are 0.  dstate_in: NULL or fp32 [nseq, H,
+ *   d_k, d_v]; may be the same array as dstate_out; an empty sequence's
+ *   dstate_out (or 0) is copied.  The states are recomputed.  Other arguments,
+ *   arithmetic and errors as for la_decay_attention, with
+ *   la_decay_attention_backward_workspace_bytes(...).  A value that is not
+ *   finite reaches, in dq, its own token and later ones, in dk and dv its own
+ *   and earlier ones.
+ */
+LA_API la_status la_decay_attention_backward(const void* q, const void* k, const void* v, const void* dout,
+                                             const float* log_decay, int dtype, const int32_t* cu_seqlens, int nseq,
+                                             int64_t T, int H, int d_k, int d_v, float scale, const float* state_in,
+                                             const float* dstate_out, void* dq, void* dk, void* dv, float* dstate_in,
+                                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* la_decay_attention_backward_workspace_bytes - scratch size for
+ *   la_decay_attention_backward on the current device (0 for arguments it rejects). */
+LA_API size_t la_decay_attention_backward_workspace_bytes(int dtype, int has_cu_seqlens, int nseq, int64_t T, int H,
+                                                          int d_k, int d_v);
+
+/*
+ * la_decay_step - one new token for each of B sequences: state_out = g state_in
+ *   + k v^T, out = scale q^T state_out.  q, k: [B, H, d_k]; v, out: [B, H, d_v]
+ *   of dtype; state_in, state_out: fp32 [B, H, d_k, d_v], the same array for an
+ *   update in place (the state_out of la_decay_attention over the prompt
+ *   continues directly).  B = 0 enqueues nothing.  Needs no workspace.
+ */
+LA_API la_status la_decay_step(const void* q, const void* k, const void* v, const float* log_decay, int dtype, int B,
+                               int H, int d_k, int d_v, float scale, const float* state_in, float* state_out,
+                               void* out, void* stream);
+
 /* la_status_string - static description of a status code. */
 LA_API const char* la_status_string(la_status status);
 

@@ -76,6 +76,15 @@ def load_library():
         "la_layer_norm_backward_workspace_bytes": ([_c_int, _c_i64, _c_int, _c_int], _c_size),
         "la_rotary": ([_vp, _vp, _vp, _vp, _c_int, _c_i64, _c_int, _c_int, ctypes.POINTER(_c_int), _c_int, _c_int,
                        _c_int, _vp, _vp, _vp], _c_int),
+        "la_decay_attention": ([_vp, _vp, _vp, _vp, _c_int, _vp, _c_int, _c_i64, _c_int, _c_int, _c_int, _c_float, _vp,
+                                _vp, _vp, _vp, _c_size, _vp], _c_int),
+        "la_decay_attention_workspace_bytes": ([_c_int, _c_int, _c_int, _c_i64, _c_int, _c_int, _c_int], _c_size),
+        "la_decay_attention_backward": ([_vp, _vp, _vp, _vp, _vp, _c_int, _vp, _c_int, _c_i64, _c_int, _c_int, _c_int,
+                                         _c_float, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_size, _vp], _c_int),
+        "la_decay_attention_backward_workspace_bytes": ([_c_int, _c_int, _c_int, _c_i64, _c_int, _c_int, _c_int],
+                                                        _c_size),
+        "la_decay_step": ([_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_float, _vp, _vp, _vp, _vp],
+                          _c_int),
         "la_status_string": ([_c_int], ctypes.c_char_p),
         "la_version": ([], _c_int),
     }
@@ -725,3 +734,106 @@ def la_rotary(q, k, freq, positions, pairs, interleaved=False, inverse=False, q_
         bool(inverse), _addr(q_out, "q_out", q.dtype, shape, dev),
         _addr_or_none(k_out, "k_out", q.dtype, shape, dev), _current_stream(dev)))
     return q_out if k is None else (q_out, k_out)
+
+
+# --------------------------------------------------------------------------- linear attention with a decay for each head
+
+def _decay_operands(q, k, v, log_decay):
+    """(T, H, d_k, d_v, shape of v, device index, addresses of q, k, v, log_decay)."""
+    T, H, dk = shape = _rows3(q, "q")
+    dv, dev = _rows3(v, "v")[2], _first(q, "q")
+    vshape = (T, H, dv)
+    return (T, H, dk, dv, vshape, dev, q.data_ptr(), _addr(k, "k", q.dtype, shape, dev),
+            _addr(v, "v", q.dtype, vshape, dev), _addr(log_decay, "log_decay", torch.float32, (H,), dev))
+
+
+def la_decay_attention_workspace_bytes(dtype, has_cu_seqlens: bool, nseq: int, T: int, H: int, d_k: int, d_v: int) -> int:
+    dt = DTYPE_IDS[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    return load_library().la_decay_attention_workspace_bytes(dt, int(has_cu_seqlens), nseq, T, H, d_k, d_v)
+
+
+def la_decay_attention(q, k, v, log_decay, scale=1.0, cu_seqlens=None, nseq=None, state_in=None, state_out=None,
+                       return_state=False, out=None, workspace=None, stream=None):
+    """Causal linear attention with a decay for each head: S_t = exp(log_decay) S_{t-1} + k_t v_t^T,
+    out_t = scale q_t^T S_t.  q, k [T, H, d_k], v [T, H, d_v] (fp32 or bf16); log_decay fp32 [H], at
+    most 0; returns out [T, H, d_v].  state_in / state_out: fp32 [nseq, H, d_k, d_v], state_out may be
+    state_in.  With return_state=True a state_out is allocated when none is given and (out, state_out)
+    is returned."""
+    lib = load_library()
+    nseq = _sequences(cu_seqlens, nseq)
+    if _elsewhere(_first(q, "q"), stream):
+        with _On(q.get_device(), stream):
+            return la_decay_attention(q, k, v, log_decay, scale, cu_seqlens, nseq, state_in, state_out, return_state,
+                                      out, workspace)
+    T, H, dk, dv, shape, dev, pq, pk, pv, pl = _decay_operands(q, k, v, log_decay)
+    states, f32, dt = (nseq, H, dk, dv), torch.float32, DTYPE_IDS[q.dtype]
+    pc = _addr_or_none(cu_seqlens, "cu_seqlens", torch.int32, None, dev)
+    pi = _addr_or_none(state_in, "state_in", f32, states, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+    if return_state and state_out is None:
+        state_out = torch.empty(states, dtype=f32, device=q.device)
+    workspace, pw, nw = _workspace(
+        workspace, 0 if workspace is not None else
+        lib.la_decay_attention_workspace_bytes(dt, cu_seqlens is not None, nseq, T, H, dk, dv), dev)
+    _check("la_decay_attention", lib.la_decay_attention(
+        pq, pk, pv, pl, dt, pc, nseq, T, H, dk, dv, scale, pi, _addr_or_none(state_out, "state_out", f32, states, dev),
+        _addr(out, "out", q.dtype, shape, dev), pw, nw, _current_stream(dev)))
+    return (out, state_out) if return_state else out
+
+
+def la_decay_attention_backward_workspace_bytes(dtype, has_cu_seqlens: bool, nseq: int, T: int, H: int, d_k: int,
+                                                d_v: int) -> int:
+    dt = DTYPE_IDS[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    return load_library().la_decay_attention_backward_workspace_bytes(dt, int(has_cu_seqlens), nseq, T, H, d_k, d_v)
+
+
+def la_decay_attention_backward(q, k, v, dout, log_decay, scale=1.0, cu_seqlens=None, nseq=None, state_in=None,
+                                dstate_out=None, return_dstate=False, dq=None, dk=None, dv=None, dstate_in=None,
+                                workspace=None, stream=None):
+    """Gradients (dq, dk, dv) of sum(dout * out) + sum(dstate_out * state_out) for la_decay_attention
+    with the same arguments (log_decay a constant); with return_dstate=True (dq, dk, dv, dstate_in)."""
+    lib = load_library()
+    nseq = _sequences(cu_seqlens, nseq)
+    if _elsewhere(_first(q, "q"), stream):
+        with _On(q.get_device(), stream):
+            return la_decay_attention_backward(q, k, v, dout, log_decay, scale, cu_seqlens, nseq, state_in, dstate_out,
+                                               return_dstate, dq, dk, dv, dstate_in, workspace)
+    T, H, d_k, d_v, shape, dev, pq, pk, pv, pl = _decay_operands(q, k, v, log_decay)
+    states, f32, dt = (nseq, H, d_k, d_v), torch.float32, DTYPE_IDS[q.dtype]
+    pd = _addr(dout, "dout", q.dtype, shape, dev)
+    pc = _addr_or_none(cu_seqlens, "cu_seqlens", torch.int32, None, dev)
+    pi = _addr_or_none(state_in, "state_in", f32, states, dev)
+    po = _addr_or_none(dstate_out, "dstate_out", f32, states, dev)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    if return_dstate and dstate_in is None:
+        dstate_in = torch.empty(states, dtype=f32, device=q.device)
+    workspace, pw, nw = _workspace(
+        workspace, 0 if workspace is not None else
+        lib.la_decay_attention_backward_workspace_bytes(dt, cu_seqlens is not None, nseq, T, H, d_k, d_v), dev)
+    _check("la_decay_attention_backward", lib.la_decay_attention_backward(
+        pq, pk, pv, pd, pl, dt, pc, nseq, T, H, d_k, d_v, scale, pi, po, _addr(dq, "dq", q.dtype, q.shape, dev),
+        _addr(dk, "dk", q.dtype, q.shape, dev), _addr(dv, "dv", q.dtype, shape, dev),
+        _addr_or_none(dstate_in, "dstate_in", f32, states, dev), pw, nw, _current_stream(dev)))
+    return (dq, dk, dv, dstate_in) if return_dstate else (dq, dk, dv)
+
+
+def la_decay_step(q, k, v, log_decay, state, scale=1.0, state_out=None, out=None, stream=None):
+    """One token for each of B sequences of la_decay_attention: q, k [B, H, d_k], v [B, H, d_v]; state
+    fp32 [B, H, d_k, d_v] is updated in place, or written to state_out when given; returns out
+    [B, H, d_v]."""
+    lib = load_library()
+    if _elsewhere(_first(q, "q"), stream):
+        with _On(q.get_device(), stream):
+            return la_decay_step(q, k, v, log_decay, state, scale, state_out, out)
+    B, H, dk, dv, shape, dev, pq, pk, pv, pl = _decay_operands(q, k, v, log_decay)
+    states, f32 = (B, H, dk, dv), torch.float32
+    ps = _addr(state, "state", f32, states, dev)
+    po = ps if state_out is None else _addr(state_out, "state_out", f32, states, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+    _check("la_decay_step", lib.la_decay_step(pq, pk, pv, pl, DTYPE_IDS[q.dtype], B, H, dk, dv, scale, ps, po,
+                                              _addr(out, "out", q.dtype, shape, dev), _current_stream(dev)))
+    return out

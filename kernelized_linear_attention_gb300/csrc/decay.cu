@@ -1,0 +1,610 @@
+// Linear attention with a decay for each head, S_t = g S_(t-1) + k_t v_t^T, out_t = scale q_t^T S_t: the work table,
+// the join of segment states, the one-token step, and the products on CUDA cores (any type and size).
+//
+// A sequence is cut into segments of L tokens that run at once.  State passes sum each segment's own k v^T; the join
+// walks the segments of a sequence and leaves what enters each; the product passes walk a segment in chunks with the
+// state on chip.  Decays are powers of g between two tokens, at most one, so no product of a large and a small
+// factor is formed.  The gradients are the same three products with other operands, two of them from the end.
+#include <initializer_list>
+
+#include "ops/decay.h"
+#include "ops/vec.cuh"
+
+namespace la {
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Work table of packed sequences
+// ---------------------------------------------------------------------------
+constexpr int kPlanThreads = 1024;
+
+__global__ void __launch_bounds__(kPlanThreads) decay_plan_kernel(const __grid_constant__ DecayCall c) {
+    __shared__ int2 sums[32];
+    __shared__ int bad;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        bad = c.cu_seqlens[0] != 0 || c.cu_seqlens[c.nseq] != c.T;
+        c.hdr->range = 0;
+    }
+    __syncthreads();
+    const int per = (c.nseq + kPlanThreads - 1) / kPlanThreads;
+    const int s0 = min(c.nseq, (int)threadIdx.x * per), s1 = min(c.nseq, s0 + per);
+    int2 n = make_int2(0, 0);            // segments and slots of this thread's sequences
+    bool wrong = false;
+    for (int s = s0; s < s1; ++s) {
+        const int lo = c.cu_seqlens[s], hi = c.cu_seqlens[s + 1];
+        // (a decrease makes another sequence's sum wrong, so every sequence has to be right)
+        if (lo < 0 || hi < lo || hi > c.T) {
+            wrong = true;
+            continue;
+        }
+        const int m = decay_segments(hi - lo, c.L);
+        n.x += m;
+        n.y += m > 0 ? m - 1 : 0;
+    }
+    if (wrong) bad = 1;
+    int2 before = n;
+    for (int o = 1; o < 32; o *= 2) {
+        const int x = __shfl_up_sync(0xffffffffu, before.x, o), y = __shfl_up_sync(0xffffffffu, before.y, o);
+        if (lane >= o) {
+            before.x += x;
+            before.y += y;
+        }
+    }
+    if (lane == 31) sums[warp] = before;
+    before.x -= n.x;
+    before.y -= n.y;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) {
+        before.x += sums[w].x;
+        before.y += sums[w].y;
+    }
+    int total = 0;
+    for (int w = 0; w < 32; ++w) total += sums[w].x;
+    if (bad) {
+        if (threadIdx.x == 0) {
+            c.hdr->error = LA_DEVERR_CU_SEQLENS;
+            c.hdr->n_units = 0;
+        }
+        return;
+    }
+    for (int s = s0; s < s1; ++s) {
+        c.segment_first[s] = before.x;
+        c.slot_first[s] = before.y;
+        const int m = decay_segments(c.cu_seqlens[s + 1] - c.cu_seqlens[s], c.L);
+        before.x += m;
+        before.y += m > 0 ? m - 1 : 0;
+    }
+    if (threadIdx.x == 0) {
+        c.segment_first[c.nseq] = total;
+        c.hdr->error = LA_DEVERR_NONE;
+        c.hdr->n_units = total;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < total; i += kPlanThreads) {
+        // the last sequence that begins at or before segment i: the one that has it (empty ones begin where the next does)
+        int lo = 0, hi = c.nseq;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (c.segment_first[mid] <= i) lo = mid;
+            else hi = mid;
+        }
+        const int k = i - c.segment_first[lo], end = c.cu_seqlens[lo + 1];
+        DecaySegment g;
+        g.seq = lo;
+        g.start = c.cu_seqlens[lo] + k * c.L;
+        g.end = (int)min64((int64_t)g.start + c.L, end);
+        g.place = (c.slot_first[lo] + k) * 4 + (k == 0) + 2 * (g.end == end);
+        c.table[i] = g;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Join: what enters each segment, from the segments' own sums
+// ---------------------------------------------------------------------------
+constexpr int kJoinThreads = 256;
+constexpr int kJoinAhead = 8;      // segments whose loads are on their way together
+
+template <int N>
+__global__ void __launch_bounds__(kJoinThreads) decay_join_kernel(const __grid_constant__ DecayCall c,
+                                                                  const __grid_constant__ DecayStates p) {
+    using V = Vec<float, N>;
+    if (c.cu_seqlens && c.hdr->error) return;
+    const int s = blockIdx.x, h = blockIdx.y, n = c.dk * c.dv;
+    const int e = (blockIdx.z * kJoinThreads + threadIdx.x) * N;
+    DecaySegment last, first;
+    if (!decay_edge_segment(c, s, false, last) || decay_first(last)) return;      // no boundary inside
+    decay_edge_segment(c, s, true, first);
+    if (e >= n) return;
+    const int m = decay_slot(last) - decay_slot(first);                           // boundaries
+    const DecayBase base = decay_base(c.log_decay[h]);
+    const float whole = decay_power(base, c.L);
+    float factor = p.reverse ? decay_power(base, last.end - last.start) : whole;
+    const int64_t step = (int64_t)c.H * n;
+    float* const own = c.states[p.reverse] + ((int64_t)decay_slot(first) * c.H + h) * n + e;
+    V acc;
+#pragma unroll
+    for (int k = 0; k < N; ++k) acc.v[k] = 0.f;
+    if (p.edge_in) acc = *reinterpret_cast<const V*>(p.edge_in + ((int64_t)s * c.H + h) * n + e);
+    for (int i0 = 0; i0 < m; i0 += kJoinAhead) {
+        V part[kJoinAhead];
+#pragma unroll
+        for (int k = 0; k < kJoinAhead; ++k)
+            if (i0 + k < m) part[k] = *reinterpret_cast<const V*>(own + (p.reverse ? m - 1 - i0 - k : i0 + k) * step);
+#pragma unroll
+        for (int k = 0; k < kJoinAhead; ++k) {
+            if (i0 + k >= m) break;
+#pragma unroll
+            for (int j = 0; j < N; ++j) acc.v[j] = fmaf(factor, acc.v[j], part[k].v[j]);
+            *reinterpret_cast<V*>(own + (p.reverse ? m - 1 - i0 - k : i0 + k) * step) = acc;
+            factor = whole;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// CUDA-core products: chunks of 32 tokens, 64 columns of z a block
+// ---------------------------------------------------------------------------
+constexpr int kSimtThreads = 256;
+constexpr int kRows = 32;          // tokens of a chunk
+constexpr int kCols = 64;          // columns of a block
+
+// Eight neighbouring values of a row, nothing from `valid` on; `vec`: the eight start on 16 bytes.
+template <typename T>
+__device__ __forceinline__ void load8(float (&f)[8], const T* p, int valid, bool vec) {
+    if (vec && valid >= 8) {
+        constexpr int N = 16 / sizeof(T);
+#pragma unroll
+        for (int k = 0; k < 8; k += N) {
+            float g[N];
+            unpack(g, *reinterpret_cast<const Vec<T, N>*>(p + k));
+#pragma unroll
+            for (int j = 0; j < N; ++j) f[k + j] = g[j];
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = k < valid ? (float)p[k] : 0.f;
+    }
+}
+__device__ __forceinline__ void store8(float* to, const float (&f)[8]) {
+    reinterpret_cast<float4*>(to)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(to)[1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+
+// Sums of one segment (or, final, what leaves each sequence): blocks of 64 x 64 of [dk][dv], 4 x 4 a thread.
+template <typename T>
+__global__ void __launch_bounds__(kSimtThreads) decay_states_kernel(const __grid_constant__ DecayCall c,
+                                                                    const __grid_constant__ DecayStates p, bool final,
+                                                                    bool vec) {
+    __shared__ __align__(16) float ys[kRows][kCols], zs[kRows][kCols];
+    const int h = blockIdx.y, nb = (c.dv + kCols - 1) / kCols;
+    const int a0 = blockIdx.z / nb * kCols, b0 = blockIdx.z % nb * kCols;
+    DecaySegment g;
+    bool any = true;
+    if (c.cu_seqlens && c.hdr->error) return;
+    if (final) any = decay_edge_segment(c, blockIdx.x, p.reverse, g);
+    else if (!decay_segment(c, blockIdx.x, g) || (p.reverse ? decay_first(g) : decay_last(g))) return;
+    const DecayBase base = decay_base(c.log_decay[h]);
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16, row = threadIdx.x / 8, col = threadIdx.x % 8 * 8;
+    float acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    float fy[8], fz[8];
+    auto load = [&](int t0) {
+        const int t = t0 + row, out = t < g.end ? 0 : 1 << 20;
+        const int64_t r = ((int64_t)(out ? g.start : t) * c.H + h);
+        load8(fy, static_cast<const T*>(p.y) + r * c.dk + a0 + col, c.dk - a0 - col - out, vec);
+        load8(fz, static_cast<const T*>(p.z) + r * c.dv + b0 + col, c.dv - b0 - col - out, vec);
+        if (out) return;
+        const float w = p.reverse ? c.scale * decay_power(base, t - g.start + 1) : decay_power(base, g.end - 1 - t);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) fy[k] *= w;
+    };
+    if (any) load(g.start);
+    for (int t0 = g.start; any && t0 < g.end; t0 += kRows) {
+        store8(&ys[row][col], fy);
+        store8(&zs[row][col], fz);
+        __syncthreads();
+        const int n = min(kRows, g.end - t0);
+        if (t0 + kRows < g.end) load(t0 + kRows);
+        for (int t = 0; t < n; ++t) {
+            const float4 y = *reinterpret_cast<const float4*>(&ys[t][ty * 4]);
+            const float4 z = *reinterpret_cast<const float4*>(&zs[t][tx * 4]);
+            const float yv[4] = {y.x, y.y, y.z, y.w}, zv[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(yv[i], zv[j], acc[i][j]);
+        }
+        __syncthreads();
+    }
+    const int64_t n = (int64_t)c.dk * c.dv;
+    const float* enter = nullptr;
+    float* to;
+    if (final) {
+        enter = any ? decay_entering(c, g, h, p.reverse, p.edge_in)
+                    : p.edge_in ? p.edge_in + ((int64_t)blockIdx.x * c.H + h) * n : nullptr;
+        to = p.edge_out + ((int64_t)blockIdx.x * c.H + h) * n;
+    } else {
+        to = c.states[p.reverse] + ((int64_t)(decay_slot(g) - (p.reverse ? 1 : 0)) * c.H + h) * n;
+    }
+    const float keep = any ? decay_power(base, g.end - g.start) : 1.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int a = a0 + ty * 4 + i, b = b0 + tx * 4 + j;
+            if (a >= c.dk || b >= c.dv) continue;
+            const int64_t at = (int64_t)a * c.dv + b;
+            to[at] = enter ? fmaf(keep, enter[at], acc[i][j]) : acc[i][j];
+        }
+}
+
+__host__ __device__ inline int simt_stride(int ds) { return (ds + 31) / 32 * 32 + 4; }   // of rows: no bank twice
+__host__ __device__ inline size_t simt_smem(int ds) {
+    return sizeof(float) * ((size_t)(ds + 3) / 4 * 4 * kCols + 2 * (size_t)kRows * simt_stride(ds) + kRows * kCols +
+                            kRows * (kRows + 4) + kRows + 1);
+}
+
+// One segment of a product pass.  A thread has two rows, 16 apart, and four columns (of the products with z and the
+// state) or two (of the scores).
+template <typename T>
+__global__ void __launch_bounds__(kSimtThreads) decay_pass_kernel(const __grid_constant__ DecayCall c,
+                                                                  const __grid_constant__ DecayPass p, bool vec) {
+    extern __shared__ __align__(16) float smem[];
+    const int ds = p.ds, ds4 = (ds + 3) / 4 * 4, ld = simt_stride(ds), h = blockIdx.y, c0 = blockIdx.z * kCols;
+    float* S = smem;                          // [ds4][64]
+    float* xs = S + ds4 * kCols;              // [32][ld]
+    float* ys = xs + kRows * ld;              // [32][ld]
+    float* zs = ys + kRows * ld;              // [32][64]
+    float* P = zs + kRows * kCols;            // [32][36]
+    float* pw = P + kRows * (kRows + 4);      // [33]: powers of the decay
+    DecaySegment g;
+    if (!decay_segment(c, blockIdx.x, g)) return;
+    const DecayBase base = decay_base(c.log_decay[h]);
+    if (threadIdx.x <= kRows) pw[threadIdx.x] = decay_power(base, threadIdx.x);
+    const float* enter = decay_entering(c, g, h, p.reverse, p.edge);
+    for (int i = threadIdx.x; i < ds4 * kCols; i += kSimtThreads) {
+        const int a = p.transposed ? i % ds4 : i / kCols, b = p.transposed ? i / ds4 : i % kCols;
+        float v = 0.f;
+        if (enter && a < ds && c0 + b < p.dz)
+            v = enter[p.transposed ? (int64_t)(c0 + b) * ds + a : (int64_t)a * p.dz + c0 + b];
+        S[a * kCols + b] = v;
+    }
+    const int r0 = threadIdx.x / 16, q0 = threadIdx.x % 16, row = threadIdx.x / 8, col = threadIdx.x % 8 * 8;
+    const int chunks = (g.end - g.start + kRows - 1) / kRows;
+    for (int k = 0; k < chunks; ++k) {
+        const int t0 = g.start + (p.reverse ? chunks - 1 - k : k) * kRows, n = min(kRows, g.end - t0);
+        {   // the chunk's rows, nothing behind its end
+            const int out = row < n ? 0 : 1 << 20;
+            const int64_t r = (int64_t)(out ? t0 : t0 + row) * c.H + h;
+            for (int a = col; a < ds4; a += 64) {
+                float f[8];
+                load8(f, static_cast<const T*>(p.x) + r * ds + a, ds - a - out, vec);
+                store8(xs + row * ld + a, f);
+                load8(f, static_cast<const T*>(p.y) + r * ds + a, ds - a - out, vec);
+                store8(ys + row * ld + a, f);
+            }
+            float f[8];
+            load8(f, static_cast<const T*>(p.z) + r * p.dz + c0 + col, p.dz - c0 - col - out, vec);
+            store8(zs + row * kCols + col, f);
+        }
+        __syncthreads();
+        {   // scores, decayed; only those of tokens that a row sees are read below
+            float acc[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+            for (int a = 0; a < ds4; a += 4) {
+                float4 x[2], y[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    x[i] = *reinterpret_cast<const float4*>(xs + (r0 + 16 * i) * ld + a);
+                    y[i] = *reinterpret_cast<const float4*>(ys + (q0 + 16 * i) * ld + a);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        acc[i][j] = fmaf(x[i].x, y[j].x, fmaf(x[i].y, y[j].y, fmaf(x[i].z, y[j].z, fmaf(x[i].w, y[j].w,
+                                                                                                    acc[i][j]))));
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int ri = r0 + 16 * i, rj = q0 + 16 * j, apart = p.reverse ? rj - ri : ri - rj;
+                    P[ri * (kRows + 4) + rj] = apart >= 0 ? c.scale * pw[apart] * acc[i][j] : 0.f;
+                }
+        }
+        __syncthreads();
+        {
+            float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            for (int a = 0; a < ds4; a += 4) {
+                float4 x[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) x[i] = *reinterpret_cast<const float4*>(xs + (r0 + 16 * i) * ld + a);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float4 s = *reinterpret_cast<const float4*>(S + (a + u) * kCols + q0 * 4);
+                    const float sv[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float xv = u == 0 ? x[i].x : u == 1 ? x[i].y : u == 2 ? x[i].z : x[i].w;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xv, sv[j], acc[i][j]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int ri = r0 + 16 * i;
+                const float f = p.reverse ? pw[max(0, n - 1 - ri)] : c.scale * pw[ri + 1];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] = enter || k ? f * acc[i][j] : 0.f;
+            }
+            for (int t = 0; t < n; ++t) {
+                const float4 z = *reinterpret_cast<const float4*>(zs + t * kCols + q0 * 4);
+                const float zv[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    // a token that the row does not see adds nothing, NaN neither
+                    const int ri = r0 + 16 * i;
+                    if (p.reverse ? t < ri : t > ri) continue;
+                    const float s = P[ri * (kRows + 4) + t];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(s, zv[j], acc[i][j]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int ri = r0 + 16 * i;
+                if (ri >= n) continue;
+                T* out = static_cast<T*>(p.out) + ((int64_t)(t0 + ri) * c.H + h) * p.dz + c0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (c0 + q0 * 4 + j < p.dz) store_elem(out, q0 * 4 + j, acc[i][j]);
+            }
+        }
+        __syncthreads();
+        if (k + 1 == chunks) break;
+        const float keep = pw[n];
+        for (int a = r0 * 4; a < ds4; a += 64) {
+            float acc[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 s = *reinterpret_cast<const float4*>(S + (a + i) * kCols + q0 * 4);
+                acc[i][0] = keep * s.x;
+                acc[i][1] = keep * s.y;
+                acc[i][2] = keep * s.z;
+                acc[i][3] = keep * s.w;
+            }
+            for (int t = 0; t < n; ++t) {
+                const float w = p.reverse ? c.scale * pw[t + 1] : pw[n - 1 - t];
+                const float4 y = *reinterpret_cast<const float4*>(ys + t * ld + a);
+                const float4 z = *reinterpret_cast<const float4*>(zs + t * kCols + q0 * 4);
+                const float yv[4] = {w * y.x, w * y.y, w * y.z, w * y.w}, zv[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(yv[i], zv[j], acc[i][j]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<float4*>(S + (a + i) * kCols + q0 * 4) =
+                    make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// One token for each of B sequences
+// ---------------------------------------------------------------------------
+constexpr int kStepThreads = 256;
+constexpr int kStepRows = 4;       // rows of the state that a thread has on their way together
+
+// A block has one (sequence, head); lanes along dv in vectors of N, thread groups along dk.
+template <typename T, int N>
+__global__ void __launch_bounds__(kStepThreads) decay_step_kernel(const T* __restrict__ q, const T* __restrict__ k,
+                                                                  const T* __restrict__ v,
+                                                                  const float* __restrict__ log_decay, int H, int dk,
+                                                                  int dv, int lanes, float scale, const float* state_in,
+                                                                  float* state_out, T* __restrict__ out) {
+    using V = Vec<float, N>;
+    __shared__ float qs[LA_MAX_DK], ks[LA_MAX_DK];
+    __shared__ float part[kStepThreads * N];
+    const int64_t pair = blockIdx.x;
+    const int h = (int)(pair % H), cols = dv / N, groups = kStepThreads / lanes;
+    const int lane = threadIdx.x % lanes, group = threadIdx.x / lanes;
+    const bool on = lane < cols;
+    const int64_t at = pair * dk * dv + lane * N, step = (int64_t)groups * dv;
+    V held[kStepRows];
+#pragma unroll
+    for (int r = 0; r < kStepRows; ++r)
+        if (on && group + r * groups < dk) held[r] = *reinterpret_cast<const V*>(state_in + at + group * dv + r * step);
+    const float g = decay_power(decay_base(log_decay[h]), 1);
+    for (int a = threadIdx.x; a < dk; a += kStepThreads) {
+        qs[a] = (float)q[pair * dk + a];
+        ks[a] = (float)k[pair * dk + a];
+    }
+    float fv[N], sum[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        fv[j] = on ? (float)v[pair * dv + lane * N + j] : 0.f;
+        sum[j] = 0.f;
+    }
+    __syncthreads();
+    for (int a0 = group; a0 < dk; a0 += kStepRows * groups) {
+        if (a0 != group) {
+#pragma unroll
+            for (int r = 0; r < kStepRows; ++r)
+                if (on && a0 + r * groups < dk) held[r] = *reinterpret_cast<const V*>(state_in + at + (int64_t)a0 * dv + r * step);
+        }
+#pragma unroll
+        for (int r = 0; r < kStepRows; ++r) {
+            const int a = a0 + r * groups;
+            if (!on || a >= dk) continue;
+            const float kv = ks[a], qv = qs[a];
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float s = fmaf(g, held[r].v[j], __fmul_rn(kv, fv[j]));
+                held[r].v[j] = s;
+                sum[j] = fmaf(qv, s, sum[j]);
+            }
+            *reinterpret_cast<V*>(state_out + at + (int64_t)a0 * dv + r * step) = held[r];
+        }
+    }
+    if (on) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) part[(group * cols + lane) * N + j] = sum[j];
+    }
+    __syncthreads();
+    for (int b = threadIdx.x; b < dv; b += kStepThreads) {
+        float o = 0.f;
+        for (int i = 0; i < groups; ++i) o += part[i * dv + b];
+        store_elem(out, pair * dv + b, scale * o);
+    }
+}
+
+template <typename T>
+cudaError_t step(const void* q, const void* k, const void* v, const float* log_decay, int B, int H, int dk, int dv,
+                 float scale, const float* state_in, float* state_out, void* out, cudaStream_t s) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(state_in) | reinterpret_cast<uintptr_t>(state_out);
+    const bool vec = dv % 4 == 0 && at % 16 == 0;
+    const int cols = vec ? dv / 4 : dv;
+    int lanes = 1;
+    while (lanes < cols) lanes *= 2;
+    const unsigned grid = (unsigned)B * H;
+    if (vec)
+        decay_step_kernel<T, 4><<<grid, kStepThreads, 0, s>>>(
+            static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), log_decay, H, dk, dv, lanes,
+            scale, state_in, state_out, static_cast<T*>(out));
+    else
+        decay_step_kernel<T, 1><<<grid, kStepThreads, 0, s>>>(
+            static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), log_decay, H, dk, dv, lanes,
+            scale, state_in, state_out, static_cast<T*>(out));
+    return cudaGetLastError();
+}
+
+bool vector_rows(const DecayCall& c, int dtype, std::initializer_list<const void*> arrays) {
+    const int n = dtype == LA_F32 ? 4 : 8;
+    uintptr_t at = 0;
+    for (const void* a : arrays) at |= reinterpret_cast<uintptr_t>(a);
+    return at % 16 == 0 && c.dk % n == 0 && c.dv % n == 0;
+}
+
+constexpr int64_t kLongest = 1 << 20;      // tokens of a segment: exact in fp32
+
+cudaError_t plan(const DecayCall& c, cudaStream_t s) {
+    if (!c.cu_seqlens) return cudaMemsetAsync(c.hdr, 0, sizeof(WsHeader), s);
+    decay_plan_kernel<<<1, kPlanThreads, 0, s>>>(c);
+    return cudaGetLastError();
+}
+
+cudaError_t join(const DecayCall& c, const DecayStates& p, cudaStream_t s) {
+    const int n = c.dk * c.dv;
+    const bool vec = n % 4 == 0 && reinterpret_cast<uintptr_t>(p.edge_in) % 16 == 0;
+    const dim3 grid(c.nseq, c.H, (unsigned)ceil_div(n, kJoinThreads * (vec ? 4 : 1)));
+    if (vec) decay_join_kernel<4><<<grid, kJoinThreads, 0, s>>>(c, p);
+    else decay_join_kernel<1><<<grid, kJoinThreads, 0, s>>>(c, p);
+    return cudaGetLastError();
+}
+
+cudaError_t states(const DecayCall& c, const DecayStates& p, int dtype, bool final, cudaStream_t s) {
+    const dim3 grid(final ? c.nseq : c.segments, c.H, (unsigned)(ceil_div(c.dk, kCols) * ceil_div(c.dv, kCols)));
+    const bool vec = vector_rows(c, dtype, {p.y, p.z});
+    if (dtype == LA_F32) decay_states_kernel<float><<<grid, kSimtThreads, 0, s>>>(c, p, final, vec);
+    else decay_states_kernel<__nv_bfloat16><<<grid, kSimtThreads, 0, s>>>(c, p, final, vec);
+    return cudaGetLastError();
+}
+
+// What enters every segment (nothing to do where every sequence is one segment).
+cudaError_t enter(const DecayCall& c, const DecayStates& p, int dtype, cudaStream_t s) {
+    if (c.slots == 0) return cudaSuccess;
+    const cudaError_t e = states(c, p, dtype, false, s);
+    return e != cudaSuccess ? e : join(c, p, s);
+}
+
+cudaError_t pass(const DecayCall& c, const DecayPass& p, int dtype, cudaStream_t s) {
+    if (c.segments == 0) return cudaSuccess;
+    const dim3 grid(c.segments, c.H, (unsigned)ceil_div(p.dz, kCols));
+    const size_t smem = simt_smem(p.ds);
+    const bool vec = vector_rows(c, dtype, {p.x, p.y, p.z});
+    auto kernel = dtype == LA_F32 ? decay_pass_kernel<float> : decay_pass_kernel<__nv_bfloat16>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kSimtThreads, smem, s>>>(c, p, vec);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t decay_layout(DecayCall& c, int dtype, bool backward, void* workspace) {
+    // segments: two for each SM, of whole 128-token chunks
+    int sms = sm_count();
+    if (sms <= 0) sms = 152;
+    const int64_t n = c.cu_seqlens ? c.T : c.T / c.nseq;
+    int64_t L = ceil_div(ceil_div(c.T * c.H, 2 * sms), 128) * 128;
+    L = min64(L < 128 ? 128 : L, ceil_div(n < 1 ? 1 : n, 128) * 128);
+    L = min64(L, kLongest);
+    c.L = (int)L;
+    const int64_t per = n > 0 ? ceil_div(n, L) : 0;
+    const int64_t segments = c.cu_seqlens ? c.T / L + c.nseq : per * c.nseq;
+    c.segments = (int)segments;
+    c.slots = c.cu_seqlens ? c.T / L : (per > 0 ? per - 1 : 0) * c.nseq;
+    unsigned char* w = static_cast<unsigned char*>(workspace);
+    size_t o = 0;
+    auto take = [&](size_t bytes) {
+        unsigned char* at = w ? w + o : nullptr;
+        o = align_up(o + bytes, kAlign);
+        return at;
+    };
+    c.hdr = reinterpret_cast<WsHeader*>(take(sizeof(WsHeader)));
+    if (c.cu_seqlens) {
+        c.slot_first = reinterpret_cast<int*>(take(sizeof(int) * ((size_t)c.nseq + 1)));
+        c.segment_first = reinterpret_cast<int*>(take(sizeof(int) * ((size_t)c.nseq + 1)));
+        c.table = reinterpret_cast<DecaySegment*>(take(sizeof(DecaySegment) * (size_t)segments));
+    }
+    for (int i = 0; i < (backward ? 2 : 1); ++i)
+        c.states[i] = reinterpret_cast<float*>(take(sizeof(float) * (size_t)c.slots * c.H * c.dk * c.dv));
+    return o;
+}
+
+cudaError_t decay_forward(const DecayCall& c, const void* q, const void* k, const void* v, int dtype,
+                          const float* state_in, float* state_out, void* out, cudaStream_t s) {
+    const DecayStates sums{k, v, 0, state_in, state_out};
+    const DecayPass p{q, k, v, out, c.dk, c.dv, 0, 0, state_in};
+    cudaError_t e = plan(c, s);
+    if (e == cudaSuccess) e = enter(c, sums, dtype, s);
+    if (e == cudaSuccess) e = pass(c, p, dtype, s);
+    // last: state_out may be state_in
+    if (e == cudaSuccess && state_out) e = states(c, sums, dtype, true, s);
+    return e;
+}
+
+cudaError_t decay_backward(const DecayCall& c, const void* q, const void* k, const void* v, const void* dout, int dtype,
+                           const float* state_in, const float* dstate_out, void* dq, void* dk, void* dv,
+                           float* dstate_in, cudaStream_t s) {
+    const DecayStates sums{k, v, 0, state_in, nullptr}, back{q, dout, 1, dstate_out, dstate_in};
+    const DecayPass pq{dout, v, k, dq, c.dv, c.dk, 0, 1, state_in}, pk{v, dout, q, dk, c.dv, c.dk, 1, 1, dstate_out},
+        pv{k, q, dout, dv, c.dk, c.dv, 1, 0, dstate_out};
+    cudaError_t e = plan(c, s);
+    if (e == cudaSuccess) e = enter(c, sums, dtype, s);
+    if (e == cudaSuccess) e = pass(c, pq, dtype, s);
+    if (e == cudaSuccess) e = enter(c, back, dtype, s);
+    if (e == cudaSuccess) e = pass(c, pk, dtype, s);
+    if (e == cudaSuccess) e = pass(c, pv, dtype, s);
+    // last: dstate_in may be dstate_out
+    if (e == cudaSuccess && dstate_in) e = states(c, back, dtype, true, s);
+    return e;
+}
+
+cudaError_t decay_step(const void* q, const void* k, const void* v, const float* log_decay, int dtype, int B, int H,
+                       int dk, int dv, float scale, const float* state_in, float* state_out, void* out,
+                       cudaStream_t s) {
+    return dtype == LA_F32 ? step<float>(q, k, v, log_decay, B, H, dk, dv, scale, state_in, state_out, out, s)
+                           : step<__nv_bfloat16>(q, k, v, log_decay, B, H, dk, dv, scale, state_in, state_out, out, s);
+}
+
+}  // namespace la

@@ -1,7 +1,9 @@
 // C entry points of the operators around the attention call (gated linear
-// recurrence, layer norm, rotary positions): argument checks and dispatch.
+// recurrence, layer norm, rotary positions) and of linear attention with a
+// decay for each head: argument checks and dispatch.
 #include <cmath>
 
+#include "ops/decay.h"
 #include "ops/ops.h"
 
 namespace la {
@@ -48,6 +50,36 @@ la_status norm_dims(int dtype, int64_t rows, int groups, int d) {
     if (d > LA_MAX_NORM_D || (int64_t)groups * d > LA_MAX_CHANNELS || rows > (int64_t)1 << 40)
         return LA_ERR_UNSUPPORTED;
     return LA_OK;
+}
+
+la_status decay_dims(int dtype, bool has_cu, int nseq, int64_t T, int H, int dk, int dv) {
+    if (!dtype_ok(dtype) || nseq < 1 || nseq > 65535 || H < 1 || H > 65535 || dk < 1 || dv < 1) return LA_ERR_INVALID_ARG;
+    if (T < 0 || T > (int64_t)INT32_MAX) return LA_ERR_INVALID_ARG;
+    if (!has_cu && T % nseq != 0) return LA_ERR_INVALID_ARG;
+    if (dk > LA_MAX_DK || dv > LA_MAX_DV) return LA_ERR_UNSUPPORTED;
+    return LA_OK;
+}
+
+DecayCall decay_call(const float* log_decay, const int32_t* cu_seqlens, int nseq, int64_t T, int H, int dk, int dv,
+                     float scale) {
+    DecayCall c{};
+    c.log_decay = log_decay;
+    c.cu_seqlens = cu_seqlens;
+    c.nseq = nseq;
+    c.T = T;
+    c.H = H;
+    c.dk = dk;
+    c.dv = dv;
+    c.scale = scale;
+    return c;
+}
+
+// Bytes of workspace; `some` stands for a cu_seqlens that is not read.
+size_t decay_bytes(int dtype, bool has_cu, int nseq, int64_t T, int H, int dk, int dv, bool backward) {
+    static const int32_t some = 0;
+    if (decay_dims(dtype, has_cu, nseq, T, H, dk, dv) != LA_OK) return 0;
+    DecayCall c = decay_call(nullptr, has_cu ? &some : nullptr, nseq, T, H, dk, dv, 1.f);
+    return decay_layout(c, dtype, backward, nullptr);
 }
 
 la_status result(cudaError_t e) { return e == cudaSuccess ? LA_OK : LA_ERR_CUDA; }
@@ -135,6 +167,92 @@ la_status la_gated_step(const void* a, const void* b, int a_dtype, int dtype, in
                        {state_in == state_out ? nullptr : state_in, (size_t)n * 4}};
     if (!disjoint(out, in)) return LA_ERR_INVALID_ARG;
     return result(gated_step(a, b, a_dtype, dtype, n, state_in, state_out, h, static_cast<cudaStream_t>(stream)));
+}
+
+size_t la_decay_attention_workspace_bytes(int dtype, int has_cu_seqlens, int nseq, int64_t T, int H, int d_k, int d_v) {
+    return decay_bytes(dtype, has_cu_seqlens != 0, nseq, T, H, d_k, d_v, false);
+}
+
+la_status la_decay_attention(const void* q, const void* k, const void* v, const float* log_decay, int dtype,
+                             const int32_t* cu_seqlens, int nseq, int64_t T, int H, int d_k, int d_v, float scale,
+                             const float* state_in, float* state_out, void* out, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+    la_status st = decay_dims(dtype, cu_seqlens != nullptr, nseq, T, H, d_k, d_v);
+    if (st != LA_OK) return st;
+    if (!std::isfinite(scale) || !log_decay || !aligned(log_decay, 4)) return LA_ERR_INVALID_ARG;
+    if (workspace == nullptr || !aligned(workspace, kAlign)) return LA_ERR_INVALID_ARG;
+    if (T > 0 && (!q || !k || !v || !out)) return LA_ERR_INVALID_ARG;
+    for (const void* x : {q, k, v, static_cast<const void*>(out)})
+        if (!aligned(x, esize(dtype))) return LA_ERR_INVALID_ARG;
+    if (!aligned(state_in, 4) || !aligned(state_out, 4) || !aligned(cu_seqlens, 4)) return LA_ERR_INVALID_ARG;
+    DecayCall c = decay_call(log_decay, cu_seqlens, nseq, T, H, d_k, d_v, scale);
+    const size_t need = decay_layout(c, dtype, false, workspace);
+    if (workspace_bytes < need) return LA_ERR_WORKSPACE;
+    const size_t nk = (size_t)T * H * d_k * esize(dtype), nv = (size_t)T * H * d_v * esize(dtype);
+    const size_t ns = sizeof(float) * (size_t)nseq * H * d_k * d_v;
+    const Span outs[] = {{out, nv}, {state_out, ns}, {workspace, need}};
+    const Span ins[] = {{q, nk}, {k, nk}, {v, nv}, {log_decay, (size_t)H * 4},
+                        {state_in == state_out ? nullptr : state_in, ns},
+                        {cu_seqlens, sizeof(int32_t) * ((size_t)nseq + 1)}};
+    if (!disjoint(outs, ins)) return LA_ERR_INVALID_ARG;
+    return result(decay_forward(c, q, k, v, dtype, state_in, state_out, out, static_cast<cudaStream_t>(stream)));
+}
+
+size_t la_decay_attention_backward_workspace_bytes(int dtype, int has_cu_seqlens, int nseq, int64_t T, int H, int d_k,
+                                                   int d_v) {
+    return decay_bytes(dtype, has_cu_seqlens != 0, nseq, T, H, d_k, d_v, true);
+}
+
+la_status la_decay_attention_backward(const void* q, const void* k, const void* v, const void* dout,
+                                      const float* log_decay, int dtype, const int32_t* cu_seqlens, int nseq, int64_t T,
+                                      int H, int d_k, int d_v, float scale, const float* state_in,
+                                      const float* dstate_out, void* dq, void* dk, void* dv, float* dstate_in,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+    la_status st = decay_dims(dtype, cu_seqlens != nullptr, nseq, T, H, d_k, d_v);
+    if (st != LA_OK) return st;
+    if (!std::isfinite(scale) || !log_decay || !aligned(log_decay, 4)) return LA_ERR_INVALID_ARG;
+    if (workspace == nullptr || !aligned(workspace, kAlign)) return LA_ERR_INVALID_ARG;
+    if (T > 0 && (!q || !k || !v || !dout || !dq || !dk || !dv)) return LA_ERR_INVALID_ARG;
+    for (const void* x : {q, k, v, dout, static_cast<const void*>(dq), static_cast<const void*>(dk),
+                          static_cast<const void*>(dv)})
+        if (!aligned(x, esize(dtype))) return LA_ERR_INVALID_ARG;
+    if (!aligned(state_in, 4) || !aligned(dstate_out, 4) || !aligned(dstate_in, 4) || !aligned(cu_seqlens, 4))
+        return LA_ERR_INVALID_ARG;
+    DecayCall c = decay_call(log_decay, cu_seqlens, nseq, T, H, d_k, d_v, scale);
+    const size_t need = decay_layout(c, dtype, true, workspace);
+    if (workspace_bytes < need) return LA_ERR_WORKSPACE;
+    const size_t nk = (size_t)T * H * d_k * esize(dtype), nv = (size_t)T * H * d_v * esize(dtype);
+    const size_t ns = sizeof(float) * (size_t)nseq * H * d_k * d_v;
+    const Span outs[] = {{dq, nk}, {dk, nk}, {dv, nv}, {dstate_in, ns}, {workspace, need}};
+    const Span ins[] = {{q, nk}, {k, nk}, {v, nv}, {dout, nv}, {log_decay, (size_t)H * 4}, {state_in, ns},
+                        {dstate_out == dstate_in ? nullptr : dstate_out, ns},
+                        {cu_seqlens, sizeof(int32_t) * ((size_t)nseq + 1)}};
+    if (!disjoint(outs, ins)) return LA_ERR_INVALID_ARG;
+    return result(decay_backward(c, q, k, v, dout, dtype, state_in, dstate_out, dq, dk, dv, dstate_in,
+                                 static_cast<cudaStream_t>(stream)));
+}
+
+la_status la_decay_step(const void* q, const void* k, const void* v, const float* log_decay, int dtype, int B, int H,
+                        int d_k, int d_v, float scale, const float* state_in, float* state_out, void* out,
+                        void* stream) {
+    if (B < 0) return LA_ERR_INVALID_ARG;
+    la_status st = decay_dims(dtype, true, 1, B, H, d_k, d_v);
+    if (st != LA_OK) return st;
+    if (!std::isfinite(scale)) return LA_ERR_INVALID_ARG;
+    if ((int64_t)B * H > (int64_t)INT32_MAX) return LA_ERR_UNSUPPORTED;
+    if (B == 0) return LA_OK;
+    if (!q || !k || !v || !log_decay || !state_in || !state_out || !out) return LA_ERR_INVALID_ARG;
+    for (const void* x : {q, k, v, static_cast<const void*>(out)})
+        if (!aligned(x, esize(dtype))) return LA_ERR_INVALID_ARG;
+    if (!aligned(log_decay, 4) || !aligned(state_in, 4) || !aligned(state_out, 4)) return LA_ERR_INVALID_ARG;
+    const size_t nk = (size_t)B * H * d_k * esize(dtype), nv = (size_t)B * H * d_v * esize(dtype);
+    const size_t ns = sizeof(float) * (size_t)B * H * d_k * d_v;
+    const Span outs[] = {{out, nv}, {state_out, ns}};
+    const Span ins[] = {{q, nk}, {k, nk}, {v, nv}, {log_decay, (size_t)H * 4},
+                        {state_in == state_out ? nullptr : state_in, ns}};
+    if (!disjoint(outs, ins)) return LA_ERR_INVALID_ARG;
+    return result(decay_step(q, k, v, log_decay, dtype, B, H, d_k, d_v, scale, state_in, state_out, out,
+                             static_cast<cudaStream_t>(stream)));
 }
 
 la_status la_layer_norm(const void* x, const float* weight, const float* bias, int dtype, int64_t rows, int groups,

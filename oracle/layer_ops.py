@@ -82,3 +82,50 @@ def rotary(x, freq, positions, pairs, interleaved=False, inverse=False):
     y = x.copy()
     y[i0], y[i1] = z.real, z.imag
     return y
+
+
+def decay_attention(q, k, v, log_decay, scale=1.0, cu_seqlens=None, nseq=1, state_in=None):
+    """(out, state_out) of S_t = exp(log_decay) S_{t-1} + k_t v_t^T, out_t = scale q_t^T S_t on q, k
+    [T, H, dk], v [T, H, dv]; states [nseq, H, dk, dv]."""
+    q, k, v = (np.asarray(x, np.float64) for x in (q, k, v))
+    g = np.exp(np.asarray(log_decay, np.float64))[:, None, None]
+    spans = _spans(q.shape[0], cu_seqlens, nseq)
+    out = np.empty_like(v)
+    states = np.zeros((len(spans), q.shape[1], q.shape[2], v.shape[2]))
+    if state_in is not None:
+        states[:] = state_in
+    for s, (lo, hi) in enumerate(spans):
+        S = states[s]
+        for t in range(lo, hi):
+            S = g * S + k[t][:, :, None] * v[t][:, None, :]
+            out[t] = scale * np.matmul(q[t][:, None, :], S)[:, 0]
+        states[s] = S
+    return out, states
+
+
+def decay_attention_backward(q, k, v, dout, log_decay, scale=1.0, cu_seqlens=None, nseq=1, state_in=None,
+                             dstate_out=None):
+    """(dq, dk, dv, dstate_in) of sum(dout * out) + sum(dstate_out * state_out) for decay_attention."""
+    q, k, v, dout = (np.asarray(x, np.float64) for x in (q, k, v, dout))
+    g = np.exp(np.asarray(log_decay, np.float64))[:, None, None]
+    spans = _spans(q.shape[0], cu_seqlens, nseq)
+    dq, dk, dv = np.empty_like(q), np.empty_like(k), np.empty_like(v)
+    shape = (len(spans), q.shape[1], q.shape[2], v.shape[2])
+    first, dstates = np.zeros(shape), np.zeros(shape)
+    if state_in is not None:
+        first[:] = state_in
+    if dstate_out is not None:
+        dstates[:] = dstate_out
+    for s, (lo, hi) in enumerate(spans):
+        S = first[s]
+        for t in range(lo, hi):
+            S = g * S + k[t][:, :, None] * v[t][:, None, :]
+            dq[t] = scale * np.matmul(S, dout[t][:, :, None])[:, :, 0]
+        R = dstates[s]
+        for t in range(hi - 1, lo - 1, -1):
+            R = R + scale * q[t][:, :, None] * dout[t][:, None, :]
+            dk[t] = np.matmul(R, v[t][:, :, None])[:, :, 0]
+            dv[t] = np.matmul(k[t][:, None, :], R)[:, 0]
+            R = g * R
+        dstates[s] = R
+    return dq, dk, dv, dstates

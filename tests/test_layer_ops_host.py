@@ -138,6 +138,88 @@ def test_rotary_rejects_a_missing_list_of_pairs(lib):
     assert lib.la_rotary(*a) == 1
 
 
+def _decay(lib, **kw):
+    a = dict(q=P[0], k=P[1], v=P[2], ld=P[3], dt=1, cu=None, nseq=1, T=128, H=2, dk=64, dv=32, scale=1.0, si=None, so=None,
+             out=P[4], ws=P[5], bytes=1 << 26, stream=None)
+    a.update(kw)
+    return lib.la_decay_attention(*a.values())
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(dt=2), 1), (dict(nseq=0), 1), (dict(nseq=65536), 1), (dict(T=-1), 1), (dict(T=1 << 31), 1), (dict(H=0), 1),
+    (dict(H=65536), 1), (dict(dk=0), 1), (dict(dv=0), 1), (dict(dk=257), 2), (dict(dv=257), 2), (dict(T=130, nseq=4), 1),
+    (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(q=None), 1), (dict(k=None), 1), (dict(v=None), 1),
+    (dict(ld=None), 1), (dict(out=None), 1), (dict(ws=None), 1), (dict(ws=P[5] + 16), 1), (dict(bytes=255), 3),
+    (dict(q=P[0] + 1), 1), (dict(v=P[2] + 1), 1), (dict(ld=P[3] + 2), 1), (dict(si=P[6] + 2), 1), (dict(so=P[6] + 2), 1),
+    (dict(cu=P[6] + 2), 1), (dict(out=P[0]), 1), (dict(out=P[2]), 1), (dict(so=P[1] + 4), 1), (dict(out=P[3] - 2), 1),
+    (dict(si=P[6], so=P[6] + 4), 1), (dict(out=P[5] + 64), 1), (dict(cu=P[4]), 1),
+])
+def test_decay_attention_rejects_bad_arguments(lib, bad, code):
+    assert _decay(lib, **bad) == code
+
+
+def _decay_bwd(lib, **kw):
+    a = dict(q=P[0], k=P[1], v=P[2], do=P[3], ld=P[4], dt=1, cu=None, nseq=1, T=128, H=2, dk=64, dv=32, scale=1.0, si=None,
+             dso=None, dq=P[5], dk_=P[6], dv_=P[7], dsi=None, ws=P[8], bytes=1 << 26, stream=None)
+    a.update(kw)
+    return lib.la_decay_attention_backward(*a.values())
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(dt=-1), 1), (dict(nseq=0), 1), (dict(T=1 << 31), 1), (dict(H=0), 1), (dict(dk=257), 2), (dict(dv=0), 1),
+    (dict(T=130, nseq=4), 1), (dict(scale=float("inf")), 1), (dict(q=None), 1), (dict(do=None), 1), (dict(ld=None), 1),
+    (dict(dq=None), 1), (dict(dk_=None), 1), (dict(dv_=None), 1), (dict(ws=None), 1), (dict(ws=P[8] + 8), 1),
+    (dict(bytes=255), 3), (dict(do=P[3] + 1), 1), (dict(dv_=P[7] + 1), 1), (dict(dso=P[9] + 2), 1), (dict(dsi=P[9] + 1), 1),
+    (dict(dq=P[0]), 1), (dict(dk_=P[5]), 1), (dict(dv_=P[3]), 1), (dict(dso=P[9], dsi=P[9] + 4), 1),
+    (dict(si=P[9], dsi=P[9]), 1), (dict(dq=P[8] + 64), 1),
+])
+def test_decay_attention_backward_rejects_bad_arguments(lib, bad, code):
+    assert _decay_bwd(lib, **bad) == code
+
+
+def _decay_step(lib, **kw):
+    a = dict(q=P[0], k=P[1], v=P[2], ld=P[3], dt=1, B=4, H=2, dk=64, dv=32, scale=1.0, si=P[4], so=P[4], out=P[5],
+             stream=None)
+    a.update(kw)
+    return lib.la_decay_step(*a.values())
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(dt=3), 1), (dict(B=-1), 1), (dict(H=0), 1), (dict(dk=0), 1), (dict(dk=257), 2), (dict(dv=257), 2),
+    (dict(B=1 << 20, H=1 << 12), 2), (dict(scale=float("nan")), 1), (dict(q=None), 1), (dict(ld=None), 1),
+    (dict(si=None), 1), (dict(so=None), 1), (dict(out=None), 1), (dict(si=P[4] + 2), 1), (dict(k=P[1] + 1), 1),
+    (dict(so=P[4] + 4), 1), (dict(out=P[0]), 1), (dict(so=P[0]), 1), (dict(B=0), 0), (dict(B=0, q=None), 0),
+])
+def test_decay_step_rejects_bad_arguments(lib, bad, code):
+    assert _decay_step(lib, **bad) == code
+
+
+def test_decay_workspace_queries(lib):
+    import kernelized_linear_attention_gb300 as la
+    for query in (la.la_decay_attention_workspace_bytes, la.la_decay_attention_backward_workspace_bytes):
+        assert query(torch.bfloat16, False, 3, 100, 2, 64, 64) == 0
+        assert query(torch.bfloat16, True, 3, 100, 2, 64, 64) > 0
+        assert query(torch.bfloat16, True, 1, 0, 1, 1, 1) > 0
+        assert query(torch.bfloat16, True, 1, 10, 2, 300, 64) == 0
+        # states are kept between segments only, not for each of many short sequences
+        assert query(torch.bfloat16, True, 60000, 60000, 16, 64, 64) < 1 << 30
+    assert (la.la_decay_attention_backward_workspace_bytes(torch.float32, True, 1, 100000, 2, 64, 64)
+            > la.la_decay_attention_workspace_bytes(torch.float32, True, 1, 100000, 2, 64, 64))
+
+
+def test_decay_binding_refuses_what_does_not_fit():
+    import kernelized_linear_attention_gb300 as la
+    x, ld = torch.zeros(4, 2, 8), torch.zeros(2)
+    for call in (lambda: la.la_decay_attention(x, x, x, ld), lambda: la.la_decay_attention_backward(x, x, x, x, ld),
+                 lambda: la.la_decay_step(x, x, x, ld, torch.zeros(4, 2, 8, 8)),
+                 lambda: la.la_decay_attention(x[0], x, x, ld),
+                 lambda: la.la_decay_attention(x, x, x, ld, cu_seqlens=torch.zeros(3, dtype=torch.int32), nseq=5)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        la.la_decay_attention(None, x, x, ld)
+
+
 def test_binding_refuses_cpu_tensors_and_wrong_ranks():
     import kernelized_linear_attention_gb300 as la
     x = torch.zeros(4, 2, 8)

@@ -97,3 +97,48 @@ def test_rotary_scores_depend_on_position_differences():
     q, k, freq = rng.standard_normal((1, 1, 8)), rng.standard_normal((1, 1, 8)), rng.standard_normal(4)
     dot = lambda p, r: (ops.rotary(q, freq, [[p, 2 * p]], [2, 2]) * ops.rotary(k, freq, [[r, 2 * r]], [2, 2])).sum()  # noqa: E731
     assert abs(dot(5, 2) - dot(105, 102)) < 1e-10
+
+
+def test_decay_attention_worked_values():
+    # one channel each: S = 1*2, then 2/2 + 3*1 = 4, then a new sequence from its state 8: 8/2 + 1*1
+    q, k, v = (np.array(x, float).reshape(3, 1, 1) for x in ([1, 2, 1], [1, 3, 1], [2, 1, 1]))
+    half = np.log([0.5])
+    out, st = ops.decay_attention(q, k, v, half, scale=0.5, cu_seqlens=[0, 2, 2, 3],
+                                  state_in=np.array([0.0, 5.0, 8.0]).reshape(3, 1, 1, 1))
+    assert np.allclose(out.ravel(), [1.0, 4.0, 2.5])
+    assert np.allclose(st.ravel(), [4.0, 5.0, 5.0])
+
+
+def test_decay_attention_is_the_sum_over_earlier_tokens():
+    g = np.random.default_rng(3)
+    q, k, v = g.normal(size=(9, 2, 4)), g.normal(size=(9, 2, 4)), g.normal(size=(9, 2, 3))
+    ld = np.array([-0.3, -np.inf])
+    out, _ = ops.decay_attention(q, k, v, ld, scale=0.7)
+    for h in range(2):
+        for i in range(9):
+            want = sum((np.exp(ld[h] * (i - j)) if i > j else 1.0) * (q[i, h] @ k[j, h]) * v[j, h] for j in range(i + 1))
+            assert np.allclose(out[i, h], 0.7 * want)
+
+
+def test_decay_attention_without_decay_is_the_unnormalised_output():
+    import oracle
+    g = np.random.default_rng(4)
+    q, k, v = g.normal(size=(12, 2, 4)), g.normal(size=(12, 2, 4)), g.normal(size=(12, 2, 4))
+    out, _ = ops.decay_attention(q, k, v, np.zeros(2), cu_seqlens=[0, 5, 12])
+    ref = oracle.forward(q, k, v, "identity", True, cu_seqlens=np.array([0, 5, 12]), norm="none")
+    assert np.allclose(out, ref)
+
+
+def test_decay_attention_gradients():
+    g = np.random.default_rng(5)
+    q, k, v, do = g.normal(size=(7, 2, 3)), g.normal(size=(7, 2, 3)), g.normal(size=(7, 2, 2)), g.normal(size=(7, 2, 2))
+    s, ds = g.normal(size=(3, 2, 3, 2)), g.normal(size=(3, 2, 3, 2))
+    ld, cu = np.array([-0.2, -1.5]), [0, 4, 4, 7]
+
+    def loss():
+        out, st = ops.decay_attention(q, k, v, ld, 0.6, cu, state_in=s)
+        return (out * do).sum() + (st * ds).sum()
+
+    got = ops.decay_attention_backward(q, k, v, do, ld, 0.6, cu, state_in=s, dstate_out=ds)
+    for x, y in zip((q, k, v, s), got):
+        assert np.allclose(_num_grad(loss, x), y, atol=1e-7)
