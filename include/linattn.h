@@ -393,7 +393,7 @@ LA_API int la_selected_path(int causal, int map, int dtype, int d_k, int d_v, in
 /*
  * Operators around the attention call
  * -----------------------------------
- * The source pages have no counterpart of the three operators below; they are
+ * The source pages have no counterpart of the four operators below; they are
  * what a linear-attention layer runs next to the calls above, on the same
  * packed [T, H, d] rows.  Beyond the conventions shared by every call: an
  * output must not overlap an input or another output unless its declaration
@@ -536,6 +536,56 @@ LA_API size_t la_layer_norm_backward_workspace_bytes(int dtype, int64_t rows, in
 LA_API la_status la_rotary(const void* q, const void* k, const float* freq, const int32_t* positions, int dtype,
                            int64_t T, int H, int d, const int* pairs, int naxes, int interleaved, int inverse,
                            void* q_out, void* k_out, void* stream);
+
+/*
+ * la_qk_norm_rotary - norm of every head's queries and keys and their rotation,
+ *   in one pass.  Each row x of d channels becomes u = x rstd w with rstd =
+ *   1 / sqrt(mean(x^2) + eps) (no mean is taken off), and its pairs are turned
+ *   as by la_rotary.
+ *   q: [T, Hq, d], k: [T, Hk, d] of dtype; a token's rows lie next to one
+ *   another, tokens q_stride and k_stride elements apart (Hq d and Hk d for
+ *   arrays of their own, more inside a fused projection's output).  Hk may be
+ *   less than Hq, or 0 with k, k_out and k_rstd NULL.  q_out: [T, Hq, d], k_out:
+ *   [T, Hk, d], contiguous; q_out may be q itself and k_out k itself where these
+ *   are contiguous too.
+ *   q_weight, k_weight: fp32 [d], or with per_head = 1 [Hq, d] and [Hk, d]; NULL
+ *   is 1.  q_rstd, k_rstd: NULL or fp32 [T, Hq] and [T, Hk], what
+ *   la_qk_norm_rotary_backward reads.
+ *   freq, positions, pairs, naxes, interleaved: as for la_rotary.  eps >= 0.
+ *   Arithmetic is fp32, outputs are rounded once.  A row whose squares
+ *   overflow in sum has rstd 0; a row of zeros with eps = 0 gives NaN.
+ *   d <= LA_MAX_ROTARY_D, (Hq + Hk) d <= LA_MAX_CHANNELS.  T = 0 enqueues nothing.
+ */
+LA_API la_status la_qk_norm_rotary(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                                   const float* freq, const int32_t* positions, int dtype, int64_t T, int Hq, int Hk,
+                                   int d, int64_t q_stride, int64_t k_stride, const int* pairs, int naxes,
+                                   int interleaved, int per_head, float eps, void* q_out, void* k_out, float* q_rstd,
+                                   float* k_rstd, void* stream);
+
+/*
+ * la_qk_norm_rotary_backward - gradients of L = sum(dq_out * q_out) +
+ *   sum(dk_out * k_out) for la_qk_norm_rotary.  With du the rows of dq_out (dk_out)
+ *   turned back, xh = x rstd and g = du w:
+ *     dx = rstd (g - xh mean_d(g xh)),  dw = sum of du xh over the rows that share w.
+ *   dq_out, dk_out, dq, dk: [T, Hq, d] and [T, Hk, d], contiguous; q_rstd, k_rstd from
+ *   la_qk_norm_rotary.  dq_weight, dk_weight: NULL or as the weights (written, not
+ *   added to; 0 for no rows).  Sums over rows are fp32 within a block and
+ *   compensated fp32 across blocks, in a fixed order (deterministic).
+ *   workspace: la_qk_norm_rotary_backward_workspace_bytes(...) bytes, 256-byte
+ *   aligned; calls that may overlap need workspaces of their own.
+ */
+LA_API la_status la_qk_norm_rotary_backward(const void* q, const void* k, const float* q_rstd, const float* k_rstd,
+                                            const void* dq_out, const void* dk_out, const float* q_weight,
+                                            const float* k_weight, const float* freq, const int32_t* positions,
+                                            int dtype, int64_t T, int Hq, int Hk, int d, int64_t q_stride,
+                                            int64_t k_stride, const int* pairs, int naxes, int interleaved,
+                                            int per_head, void* dq, void* dk, float* dq_weight, float* dk_weight,
+                                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* la_qk_norm_rotary_backward_workspace_bytes - scratch size for
+ *   la_qk_norm_rotary_backward on the current device (0 for arguments it rejects, or
+ *   without a device). */
+LA_API size_t la_qk_norm_rotary_backward_workspace_bytes(int dtype, int64_t T, int Hq, int Hk, int d);
 
 /*
  * Linear attention with a decay for each head

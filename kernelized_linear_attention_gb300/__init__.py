@@ -13,6 +13,7 @@ Entry points (same names as the C ABI in include/linattn.h):
 and the operators around the attention call:
   la_gated_scan, la_gated_scan_backward, la_gated_scan_workspace_bytes, la_gated_step (gated linear recurrence),
   la_layer_norm, la_layer_norm_backward, la_layer_norm_backward_workspace_bytes, la_rotary,
+  la_qk_norm_rotary, la_qk_norm_rotary_backward, la_qk_norm_rotary_backward_workspace_bytes,
 and linear attention with a decay for each head:
   la_decay_attention, la_decay_attention_workspace_bytes, la_decay_attention_backward,
   la_decay_attention_backward_workspace_bytes, la_decay_step,
@@ -26,6 +27,7 @@ from ._binding import (  # noqa: F401
     la_workspace_bytes, la_check_cu_seqlens, la_workspace_error, la_orthogonal_features, la_selected_path,
     la_gated_scan, la_gated_scan_backward, la_gated_scan_workspace_bytes, la_gated_step, la_layer_norm,
     la_layer_norm_backward, la_layer_norm_backward_workspace_bytes, la_rotary,
+    la_qk_norm_rotary, la_qk_norm_rotary_backward, la_qk_norm_rotary_backward_workspace_bytes,
     la_decay_attention, la_decay_attention_workspace_bytes, la_decay_attention_backward,
     la_decay_attention_backward_workspace_bytes, la_decay_step,
     la_status_string, la_version, attention, forward_ptrs, forward_general_ptrs,

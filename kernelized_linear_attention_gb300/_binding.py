@@ -76,6 +76,12 @@ def load_library():
         "la_layer_norm_backward_workspace_bytes": ([_c_int, _c_i64, _c_int, _c_int], _c_size),
         "la_rotary": ([_vp, _vp, _vp, _vp, _c_int, _c_i64, _c_int, _c_int, ctypes.POINTER(_c_int), _c_int, _c_int,
                        _c_int, _vp, _vp, _vp], _c_int),
+        "la_qk_norm_rotary": ([_vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_i64, _c_int, _c_int, _c_int, _c_i64, _c_i64,
+                               ctypes.POINTER(_c_int), _c_int, _c_int, _c_int, _c_float, _vp, _vp, _vp, _vp, _vp], _c_int),
+        "la_qk_norm_rotary_backward": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_i64, _c_int, _c_int,
+                                        _c_int, _c_i64, _c_i64, ctypes.POINTER(_c_int), _c_int, _c_int, _c_int, _vp, _vp,
+                                        _vp, _vp, _vp, _c_size, _vp], _c_int),
+        "la_qk_norm_rotary_backward_workspace_bytes": ([_c_int, _c_i64, _c_int, _c_int, _c_int], _c_size),
         "la_decay_attention": ([_vp, _vp, _vp, _vp, _c_int, _vp, _c_int, _c_i64, _c_int, _c_int, _c_int, _c_float, _vp,
                                 _vp, _vp, _vp, _c_size, _vp], _c_int),
         "la_decay_attention_workspace_bytes": ([_c_int, _c_int, _c_int, _c_i64, _c_int, _c_int, _c_int], _c_size),
@@ -734,6 +740,134 @@ def la_rotary(q, k, freq, positions, pairs, interleaved=False, inverse=False, q_
         bool(inverse), _addr(q_out, "q_out", q.dtype, shape, dev),
         _addr_or_none(k_out, "k_out", q.dtype, shape, dev), _current_stream(dev)))
     return q_out if k is None else (q_out, k_out)
+
+
+def _strided(t, name, dtype, index):
+    """(address, elements between tokens) of rows [T, H, d] whose tokens may be any distance apart, a token's
+    rows next to one another: a slice of a fused projection's output."""
+    T, H, d = _rows3(t, name)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, other operands on cuda:{index}")
+    if t.is_contiguous() or t.numel() == 0:
+        return t.data_ptr(), H * d
+    st, sh, sd = t.stride()
+    if sd != 1 or (H > 1 and sh != d) or (T > 1 and st < H * d):
+        raise ValueError(f"{name}: a token's rows must lie next to one another, got strides {(st, sh, sd)}")
+    return t.data_ptr(), st if T > 1 else H * d
+
+
+def _qk_operands(q, k, q_weight, k_weight, freq, positions, pairs):
+    """Device index, addresses and sizes that la_qk_norm_rotary and its gradients share."""
+    T, Hq, d = _rows3(q, "q")
+    if not q.is_cuda or q.dtype not in DTYPE_IDS:
+        raise ValueError(f"q must be a CUDA tensor of float32 or bfloat16, got {q.dtype} on {q.device}")
+    dev, n, Hk = q.get_device(), len(pairs), 0
+    pq, sq = _strided(q, "q", q.dtype, dev)
+    pk, sk = None, 0
+    if k is not None:
+        Tk, Hk, dk = _rows3(k, "k")
+        if Tk != T or dk != d:
+            raise ValueError(f"k must have shape {(T, 'Hk', d)}, got {tuple(k.shape)}")
+        pk, sk = _strided(k, "k", q.dtype, dev)
+    elif k_weight is not None:
+        raise ValueError("k_weight is given without k")
+    per_head, ws = False, []
+    for w, name, H in ((q_weight, "q_weight", Hq), (k_weight, "k_weight", Hk)):
+        if w is not None and isinstance(w, torch.Tensor) and w.dim() == 2:
+            per_head = True
+    for w, name, H in ((q_weight, "q_weight", Hq), (k_weight, "k_weight", Hk)):
+        ws.append(_addr_or_none(w, name, torch.float32, (H, d) if per_head else (d,), dev))
+    pf = _addr(freq, "freq", torch.float32, (sum(pairs),), dev)
+    if not isinstance(positions, torch.Tensor):
+        raise TypeError("positions must be a torch.Tensor")
+    pp = _addr(positions, "positions", torch.int32, (T,) if n == 1 and positions.dim() == 1 else (T, n), dev)
+    return dev, T, Hq, Hk, d, pq, sq, pk, sk, ws[0], ws[1], per_head, pf, pp, (_c_int * n)(*pairs), n
+
+
+def _device_of(t, name) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def la_qk_norm_rotary(q, k, q_weight, k_weight, freq, positions, pairs, eps=1e-6, interleaved=False, return_rstd=False,
+                      q_out=None, k_out=None, q_rstd=None, k_rstd=None, stream=None):
+    """Norm of every head's queries and keys (x / sqrt(mean(x^2) + eps) weight) and their rotation (as
+    la_rotary) in one pass.  q [T, Hq, d], k [T, Hk, d] (fp32 or bf16, k may be None), tokens any
+    distance apart: slices of a fused projection need no copy.  q_weight, k_weight: fp32 [d], or both
+    per head ([Hq, d], [Hk, d]), or None.  Returns (q_out, k_out), contiguous, or with return_rstd=True
+    (q_out, k_out, q_rstd, k_rstd), as la_qk_norm_rotary_backward reads them.  q_out may be q, k_out k."""
+    lib = load_library()
+    if _elsewhere(_device_of(q, "q"), stream):
+        with _On(q.get_device(), stream):
+            return la_qk_norm_rotary(q, k, q_weight, k_weight, freq, positions, pairs, eps, interleaved, return_rstd,
+                                     q_out, k_out, q_rstd, k_rstd)
+    dev, T, Hq, Hk, d, pq, sq, pk, sk, wq, wk, per_head, pf, pp, pa, n = _qk_operands(q, k, q_weight, k_weight, freq,
+                                                                                      positions, pairs)
+    if k is None and (k_out is not None or k_rstd is not None):
+        raise ValueError("k_out or k_rstd is given without k")
+    dt, f32 = q.dtype, torch.float32
+    q_out = torch.empty((T, Hq, d), dtype=dt, device=q.device) if q_out is None else q_out
+    k_out = torch.empty((T, Hk, d), dtype=dt, device=q.device) if k is not None and k_out is None else k_out
+    if return_rstd:
+        q_rstd = torch.empty((T, Hq), dtype=f32, device=q.device) if q_rstd is None else q_rstd
+        k_rstd = torch.empty((T, Hk), dtype=f32, device=q.device) if k is not None and k_rstd is None else k_rstd
+    _check("la_qk_norm_rotary", lib.la_qk_norm_rotary(
+        pq, pk, wq, wk, pf, pp, DTYPE_IDS[dt], T, Hq, Hk, d, sq, sk, pa, n, bool(interleaved), per_head, eps,
+        _addr(q_out, "q_out", dt, (T, Hq, d), dev), _addr_or_none(k_out, "k_out", dt, (T, Hk, d), dev),
+        _addr_or_none(q_rstd, "q_rstd", f32, (T, Hq), dev), _addr_or_none(k_rstd, "k_rstd", f32, (T, Hk), dev),
+        _current_stream(dev)))
+    return (q_out, k_out, q_rstd, k_rstd) if return_rstd else (q_out, k_out)
+
+
+def la_qk_norm_rotary_backward_workspace_bytes(dtype, T: int, Hq: int, Hk: int, d: int) -> int:
+    dt = DTYPE_IDS[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    return load_library().la_qk_norm_rotary_backward_workspace_bytes(dt, T, Hq, Hk, d)
+
+
+def la_qk_norm_rotary_backward(q, k, q_rstd, k_rstd, dq_out, dk_out, q_weight, k_weight, freq, positions, pairs,
+                               interleaved=False, dq=None, dk=None, dq_weight=None, dk_weight=None, workspace=None,
+                               stream=None):
+    """Gradients (dq, dk, dq_weight, dk_weight) of sum(dq_out * q_out) + sum(dk_out * k_out) for
+    la_qk_norm_rotary; dq, dk contiguous, those of the weights fp32 of the weights' shapes (None where a
+    weight is None)."""
+    lib = load_library()
+    if _elsewhere(_device_of(q, "q"), stream):
+        with _On(q.get_device(), stream):
+            return la_qk_norm_rotary_backward(q, k, q_rstd, k_rstd, dq_out, dk_out, q_weight, k_weight, freq, positions,
+                                              pairs, interleaved, dq, dk, dq_weight, dk_weight, workspace)
+    dev, T, Hq, Hk, d, pq, sq, pk, sk, wq, wk, per_head, pf, pp, pa, n = _qk_operands(q, k, q_weight, k_weight, freq,
+                                                                                      positions, pairs)
+    dt, f32 = q.dtype, torch.float32
+    for w, dw, name in ((q_weight, dq_weight, "dq_weight"), (k_weight, dk_weight, "dk_weight")):
+        if w is None and dw is not None:
+            raise ValueError(f"{name} is given without its weight")
+    if k is None and any(x is not None for x in (k_rstd, dk_out, dk)):
+        raise ValueError("k_rstd, dk_out or dk is given without k")
+    pqr, pdq = _addr(q_rstd, "q_rstd", f32, (T, Hq), dev), _addr(dq_out, "dq_out", dt, (T, Hq, d), dev)
+    pkr = pdk = None
+    if k is not None:
+        pkr, pdk = _addr(k_rstd, "k_rstd", f32, (T, Hk), dev), _addr(dk_out, "dk_out", dt, (T, Hk, d), dev)
+    dq = torch.empty((T, Hq, d), dtype=dt, device=q.device) if dq is None else dq
+    dk = torch.empty((T, Hk, d), dtype=dt, device=q.device) if k is not None and dk is None else dk
+    dq_weight = torch.empty_like(q_weight) if q_weight is not None and dq_weight is None else dq_weight
+    dk_weight = torch.empty_like(k_weight) if k_weight is not None and dk_weight is None else dk_weight
+    workspace, pw, nw = _workspace(
+        workspace, 0 if workspace is not None else
+        lib.la_qk_norm_rotary_backward_workspace_bytes(DTYPE_IDS[dt], T, Hq, Hk, d), dev)
+    _check("la_qk_norm_rotary_backward", lib.la_qk_norm_rotary_backward(
+        pq, pk, pqr, pkr, pdq, pdk, wq, wk, pf, pp, DTYPE_IDS[dt], T, Hq, Hk, d, sq, sk, pa, n, bool(interleaved),
+        per_head, _addr(dq, "dq", dt, (T, Hq, d), dev), _addr_or_none(dk, "dk", dt, (T, Hk, d), dev),
+        _addr_or_none(dq_weight, "dq_weight", f32, None if q_weight is None else q_weight.shape, dev),
+        _addr_or_none(dk_weight, "dk_weight", f32, None if k_weight is None else k_weight.shape, dev), pw, nw,
+        _current_stream(dev)))
+    return dq, dk, dq_weight, dk_weight
 
 
 # --------------------------------------------------------------------------- linear attention with a decay for each head

@@ -1,6 +1,6 @@
 // C entry points of the operators around the attention call (gated linear
-// recurrence, layer norm, rotary positions) and of linear attention with a
-// decay for each head: argument checks and dispatch.
+// recurrence, layer norm, rotary positions, norm of queries and keys) and of
+// linear attention with a decay for each head: argument checks and dispatch.
 #include <cmath>
 
 #include "ops/decay.h"
@@ -72,6 +72,41 @@ DecayCall decay_call(const float* log_decay, const int32_t* cu_seqlens, int nseq
     c.dv = dv;
     c.scale = scale;
     return c;
+}
+
+la_status turns(Turns& p, const float* freq, const int32_t* positions, int d, const int* pairs, int naxes,
+                int interleaved, int inverse) {
+    if (naxes < 1 || pairs == nullptr || (interleaved & ~1) || (inverse & ~1)) return LA_ERR_INVALID_ARG;
+    if (naxes > LA_MAX_AXES || d > LA_MAX_ROTARY_D) return LA_ERR_UNSUPPORTED;
+    int64_t P = 0;
+    for (int i = 0; i < naxes; ++i) {
+        if (pairs[i] < 0) return LA_ERR_INVALID_ARG;
+        p.first[i] = (int)P;
+        P += pairs[i];
+        if (2 * P > d) return LA_ERR_INVALID_ARG;
+    }
+    for (int i = naxes; i <= LA_MAX_AXES; ++i) p.first[i] = (int)P;
+    if (P < 1) return LA_ERR_INVALID_ARG;
+    p.freq = freq;
+    p.positions = positions;
+    p.P = (int)P;
+    p.naxes = naxes;
+    p.interleaved = interleaved;
+    p.inverse = inverse;
+    return LA_OK;
+}
+
+// Rows [T][H][d] whose tokens are `stride` elements apart: q and k of the norm with rotation.
+la_status qk_dims(int dtype, int64_t T, int Hq, int Hk, int d, int64_t q_stride, int64_t k_stride, int per_head) {
+    if (!dtype_ok(dtype) || T < 0 || T > (int64_t)INT32_MAX || Hq < 1 || Hq > 65535 || Hk < 0 || Hk > 65535 || d < 2 ||
+        (per_head & ~1))
+        return LA_ERR_INVALID_ARG;
+    if (q_stride < (int64_t)Hq * d || k_stride < (int64_t)Hk * d) return LA_ERR_INVALID_ARG;
+    if ((int64_t)(Hq + Hk) * d > LA_MAX_CHANNELS || q_stride > INT32_MAX || k_stride > INT32_MAX) return LA_ERR_UNSUPPORTED;
+    return LA_OK;
+}
+size_t strided_bytes(int64_t T, int H, int d, int64_t stride, int dtype) {
+    return T < 1 ? 0 : ((size_t)(T - 1) * stride + (size_t)H * d) * esize(dtype);
 }
 
 // Bytes of workspace; `some` stands for a cu_seqlens that is not read.
@@ -305,18 +340,9 @@ la_status la_rotary(const void* q, const void* k, const float* freq, const int32
                     int H, int d, const int* pairs, int naxes, int interleaved, int inverse, void* q_out, void* k_out,
                     void* stream) {
     if (!dtype_ok(dtype) || T < 0 || T > (int64_t)INT32_MAX || H < 1 || H > 65535 || d < 2) return LA_ERR_INVALID_ARG;
-    if (naxes < 1 || pairs == nullptr || (interleaved & ~1) || (inverse & ~1)) return LA_ERR_INVALID_ARG;
-    if (naxes > LA_MAX_AXES || d > LA_MAX_ROTARY_D) return LA_ERR_UNSUPPORTED;
     RotaryParams p{};
-    int64_t P = 0;
-    for (int i = 0; i < naxes; ++i) {
-        if (pairs[i] < 0) return LA_ERR_INVALID_ARG;
-        p.first[i] = (int)P;
-        P += pairs[i];
-        if (2 * P > d) return LA_ERR_INVALID_ARG;
-    }
-    for (int i = naxes; i <= LA_MAX_AXES; ++i) p.first[i] = (int)P;
-    if (P < 1) return LA_ERR_INVALID_ARG;
+    const la_status st = turns(p, freq, positions, d, pairs, naxes, interleaved, inverse);
+    if (st != LA_OK) return st;
     if ((k == nullptr) != (k_out == nullptr)) return LA_ERR_INVALID_ARG;
     if (T == 0) return LA_OK;
     if (!q || !q_out || !freq || !positions) return LA_ERR_INVALID_ARG;
@@ -325,14 +351,98 @@ la_status la_rotary(const void* q, const void* k, const float* freq, const int32
     if (!aligned(freq, 4) || !aligned(positions, 4)) return LA_ERR_INVALID_ARG;
     const size_t n = (size_t)T * H * d * esize(dtype);
     const Span out[] = {{q_out, n}, {k_out, n}};
-    const Span in[] = {{q == q_out ? nullptr : q, n}, {k == k_out ? nullptr : k, n}, {freq, (size_t)P * 4},
+    const Span in[] = {{q == q_out ? nullptr : q, n}, {k == k_out ? nullptr : k, n}, {freq, (size_t)p.P * 4},
                        {positions, (size_t)T * naxes * 4}};
     if (!disjoint(out, in)) return LA_ERR_INVALID_ARG;
     p.q = q; p.k = k; p.q_out = q_out; p.k_out = k_out;
-    p.freq = freq; p.positions = positions;
-    p.T = T; p.H = H; p.d = d; p.P = (int)P; p.naxes = naxes;
-    p.interleaved = interleaved; p.inverse = inverse;
+    p.T = T; p.H = H; p.d = d;
     return result(rotary(p, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+la_status la_qk_norm_rotary(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                            const float* freq, const int32_t* positions, int dtype, int64_t T, int Hq, int Hk, int d,
+                            int64_t q_stride, int64_t k_stride, const int* pairs, int naxes, int interleaved,
+                            int per_head, float eps, void* q_out, void* k_out, float* q_rstd, float* k_rstd,
+                            void* stream) {
+    la_status st = qk_dims(dtype, T, Hq, Hk, d, q_stride, k_stride, per_head);
+    if (st != LA_OK) return st;
+    QkNormParams p{};
+    st = turns(p, freq, positions, d, pairs, naxes, interleaved, 0);
+    if (st != LA_OK) return st;
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return LA_ERR_INVALID_ARG;
+    if (T == 0) return LA_OK;
+    if (!q || !q_out || !freq || !positions || (Hk > 0 && (!k || !k_out)) || (Hk == 0 && (k || k_out || k_rstd)))
+        return LA_ERR_INVALID_ARG;
+    for (const void* x : {q, k, static_cast<const void*>(q_out), static_cast<const void*>(k_out)})
+        if (!aligned(x, esize(dtype))) return LA_ERR_INVALID_ARG;
+    for (const float* x : {q_weight, k_weight, freq, static_cast<const float*>(q_rstd), static_cast<const float*>(k_rstd)})
+        if (!aligned(x, 4)) return LA_ERR_INVALID_ARG;
+    if (!aligned(positions, 4)) return LA_ERR_INVALID_ARG;
+    const size_t nq = (size_t)T * Hq * d * esize(dtype), nk = (size_t)T * Hk * d * esize(dtype);
+    const size_t wq = (size_t)(per_head ? Hq : 1) * d * 4, wk = (size_t)(per_head ? Hk : 1) * d * 4;
+    const bool q_place = q == q_out && q_stride == (int64_t)Hq * d, k_place = k == k_out && k_stride == (int64_t)Hk * d;
+    const Span out[] = {{q_out, nq}, {k_out, nk}, {q_rstd, (size_t)T * Hq * 4}, {k_rstd, (size_t)T * Hk * 4}};
+    const Span in[] = {{q_place ? nullptr : q, strided_bytes(T, Hq, d, q_stride, dtype)},
+                       {k_place ? nullptr : k, strided_bytes(T, Hk, d, k_stride, dtype)}, {q_weight, wq}, {k_weight, wk},
+                       {freq, (size_t)p.P * 4}, {positions, (size_t)T * naxes * 4}};
+    if (!disjoint(out, in)) return LA_ERR_INVALID_ARG;
+    p.x[0] = q; p.x[1] = k;
+    p.y[0] = q_out; p.y[1] = k_out;
+    p.w[0] = q_weight; p.w[1] = k_weight;
+    p.rstd[0] = q_rstd; p.rstd[1] = k_rstd;
+    p.stride[0] = q_stride; p.stride[1] = k_stride;
+    p.T = T; p.H[0] = Hq; p.H[1] = Hk; p.d = d; p.per_head = per_head; p.eps = eps;
+    return result(qk_norm_rotary(p, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+size_t la_qk_norm_rotary_backward_workspace_bytes(int dtype, int64_t T, int Hq, int Hk, int d) {
+    if (qk_dims(dtype, T, Hq, Hk, d, (int64_t)Hq * d, (int64_t)Hk * d, 0) != LA_OK || d > LA_MAX_ROTARY_D) return 0;
+    return qk_norm_rotary_backward_workspace_bytes(T, Hq + Hk, d);
+}
+
+la_status la_qk_norm_rotary_backward(const void* q, const void* k, const float* q_rstd, const float* k_rstd,
+                                     const void* dq_out, const void* dk_out, const float* q_weight,
+                                     const float* k_weight, const float* freq, const int32_t* positions, int dtype,
+                                     int64_t T, int Hq, int Hk, int d, int64_t q_stride, int64_t k_stride,
+                                     const int* pairs, int naxes, int interleaved, int per_head, void* dq, void* dk,
+                                     float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+    la_status st = qk_dims(dtype, T, Hq, Hk, d, q_stride, k_stride, per_head);
+    if (st != LA_OK) return st;
+    QkNormParams p{};
+    st = turns(p, freq, positions, d, pairs, naxes, interleaved, 1);
+    if (st != LA_OK) return st;
+    if (workspace == nullptr || !aligned(workspace, kAlign)) return LA_ERR_INVALID_ARG;
+    if (Hk == 0 && (k || dk_out || dk || k_rstd || k_weight || dk_weight)) return LA_ERR_INVALID_ARG;
+    if (T > 0 && (!q || !q_rstd || !dq_out || !dq || !freq || !positions ||
+                  (Hk > 0 && (!k || !k_rstd || !dk_out || !dk))))
+        return LA_ERR_INVALID_ARG;
+    for (const void* x : {q, k, dq_out, dk_out, static_cast<const void*>(dq), static_cast<const void*>(dk)})
+        if (!aligned(x, esize(dtype))) return LA_ERR_INVALID_ARG;
+    for (const float* x : {q_rstd, k_rstd, q_weight, k_weight, freq, static_cast<const float*>(dq_weight),
+                           static_cast<const float*>(dk_weight)})
+        if (!aligned(x, 4)) return LA_ERR_INVALID_ARG;
+    if (!aligned(positions, 4)) return LA_ERR_INVALID_ARG;
+    const size_t need = qk_norm_rotary_backward_workspace_bytes(T, Hq + Hk, d);
+    if (need == 0) return LA_ERR_CUDA;
+    if (workspace_bytes < need) return LA_ERR_WORKSPACE;
+    const size_t nq = (size_t)T * Hq * d * esize(dtype), nk = (size_t)T * Hk * d * esize(dtype);
+    const size_t wq = (size_t)(per_head ? Hq : 1) * d * 4, wk = (size_t)(per_head ? Hk : 1) * d * 4;
+    const Span out[] = {{dq, nq}, {dk, nk}, {dq_weight, wq}, {dk_weight, wk}, {workspace, need}};
+    const Span in[] = {{q, strided_bytes(T, Hq, d, q_stride, dtype)}, {k, strided_bytes(T, Hk, d, k_stride, dtype)},
+                       {q_rstd, (size_t)T * Hq * 4}, {k_rstd, (size_t)T * Hk * 4}, {dq_out, nq}, {dk_out, nk},
+                       {q_weight, wq}, {k_weight, wk}, {freq, (size_t)p.P * 4}, {positions, (size_t)T * naxes * 4}};
+    if (!disjoint(out, in)) return LA_ERR_INVALID_ARG;
+    p.x[0] = q; p.x[1] = k;
+    p.dy[0] = dq_out; p.dy[1] = dk_out;
+    p.y[0] = dq; p.y[1] = dk;
+    p.w[0] = q_weight; p.w[1] = k_weight;
+    p.rstd[0] = const_cast<float*>(q_rstd); p.rstd[1] = const_cast<float*>(k_rstd);
+    p.dw[0] = dq_weight; p.dw[1] = dk_weight;
+    p.partial = dq_weight || dk_weight ? static_cast<float*>(workspace) : nullptr;
+    p.stride[0] = q_stride; p.stride[1] = k_stride;
+    p.T = T; p.H[0] = Hq; p.H[1] = Hk; p.d = d; p.per_head = per_head;
+    return result(qk_norm_rotary_backward(p, dtype, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -50,19 +50,43 @@ cudaError_t layer_norm_backward(const void* x, const void* dy, const float* weig
                                 const float* rstd, int dtype, int64_t rows, int groups, int d, void* dx,
                                 float* dweight, float* dbias, void* workspace, cudaStream_t s);
 
+// What pairs turn by: pair p of token t by positions[t][axis(p)] freq[p].
+struct Turns {
+    const float* freq;         // [P]
+    const int32_t* positions;  // [T][naxes]
+    int P, naxes;
+    int first[LA_MAX_AXES + 1];   // first pair of each axis, and P
+    int interleaved, inverse;
+};
+
 // Rotary positions (rotary.cu).
-struct RotaryParams {
+struct RotaryParams : Turns {
     const void* q;
     const void* k;             // may be NULL
     void* q_out;
     void* k_out;
-    const float* freq;         // [P]
-    const int32_t* positions;  // [T][naxes]
     int64_t T;
-    int H, d, P, naxes;
-    int first[LA_MAX_AXES + 1];   // first pair of each axis, and P
-    int interleaved, inverse;
+    int H, d;
 };
 cudaError_t rotary(const RotaryParams& p, int dtype, cudaStream_t s);
+
+// Norm of queries and keys with their rotation (qk_norm_rotary.cu); [0] are the queries, [1] the keys or NULL.
+struct QkNormParams : Turns {
+    const void* x[2];          // [T][stride]: a token's rows [H][d] next to one another
+    const void* dy[2];         // backward: [T][H][d]
+    void* y[2];                // [T][H][d] outputs (forward) or dx (backward)
+    const float* w[2];         // [d], or [H][d] per head, or NULL
+    float* rstd[2];            // [T][H]: written if not NULL (forward), read (backward)
+    float* dw[2];              // backward: as w, or NULL
+    float* partial;            // backward: [blocks][H of both][d], or NULL: no gradients of weights
+    int64_t stride[2];         // of x's tokens, in elements
+    int64_t T;
+    int H[2];
+    int d, per_head;
+    float eps;
+};
+cudaError_t qk_norm_rotary(const QkNormParams& p, int dtype, cudaStream_t s);
+size_t qk_norm_rotary_backward_workspace_bytes(int64_t T, int H, int d);   // H of both; 0: no device
+cudaError_t qk_norm_rotary_backward(const QkNormParams& p, int dtype, cudaStream_t s);
 
 }  // namespace la

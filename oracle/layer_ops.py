@@ -129,3 +129,26 @@ def decay_attention_backward(q, k, v, dout, log_decay, scale=1.0, cu_seqlens=Non
             R = g * R
         dstates[s] = R
     return dq, dk, dv, dstates
+
+
+def qk_norm_rotary(x, weight, freq, positions, pairs, interleaved=False, eps=1e-6):
+    """(y, rstd) of rows x [T, H, d]: x rstd weight (weight [d], [H, d] or None), then turned as by rotary."""
+    x = np.asarray(x, np.float64)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        rstd = 1.0 / np.sqrt((x * x).mean(-1) + eps)
+        u = x * rstd[..., None]
+    if weight is not None:
+        u = u * weight
+    return rotary(u, freq, positions, pairs, interleaved), rstd
+
+
+def qk_norm_rotary_backward(x, rstd, dy, weight, freq, positions, pairs, interleaved=False):
+    """(dx, dweight) of sum(dy * y) for qk_norm_rotary, for given rstd."""
+    x = np.asarray(x, np.float64)
+    w = np.ones(x.shape[-1]) if weight is None else np.asarray(weight, np.float64)
+    r = np.asarray(rstd, np.float64)[..., None]
+    du = rotary(dy, freq, positions, pairs, interleaved, inverse=True)
+    xh = x * r
+    g = du * w
+    dx = r * (g - xh * (g * xh).mean(-1, keepdims=True))
+    return dx, (du * xh).sum(tuple(range(x.ndim - w.ndim)))

@@ -207,6 +207,48 @@ def test_decay_workspace_queries(lib):
             > la.la_decay_attention_workspace_bytes(torch.float32, True, 1, 100000, 2, 64, 64))
 
 
+def _qk(lib, pairs=(16, 16), **kw):
+    a = dict(q=P[0], k=P[1], qw=P[2], kw_=P[3], freq=P[4], pos=P[5], dt=1, T=128, Hq=4, Hk=2, d=64, qs=256, ks=128,
+             pairs=(ctypes.c_int * max(1, len(pairs)))(*pairs), naxes=len(pairs), il=0, per=0, eps=1e-6, qo=P[6], ko=P[7],
+             qr=P[8], kr=P[9], stream=None)
+    a.update(kw)
+    return lib.la_qk_norm_rotary(*a.values())
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(dt=2), 1), (dict(T=-1), 1), (dict(T=1 << 31), 1), (dict(Hq=0), 1), (dict(Hk=-1), 1), (dict(d=1), 1), (dict(per=2), 1),
+    (dict(qs=255), 1), (dict(ks=127), 1), (dict(qs=1 << 31), 2), (dict(naxes=0), 1), (dict(pairs=(0, 0)), 1),
+    (dict(pairs=(16, 17)), 1), (dict(pairs=(-1, 4)), 1), (dict(pairs=(1,) * 5), 2), (dict(d=1025, qs=4100, ks=2050), 2),
+    (dict(Hq=20000, d=64, qs=1280000), 2), (dict(il=2), 1), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1),
+    (dict(q=None), 1), (dict(k=None), 1), (dict(qo=None), 1), (dict(ko=None), 1), (dict(freq=None), 1), (dict(pos=None), 1),
+    (dict(Hk=0, ks=0), 1), (dict(q=P[0] + 1), 1), (dict(qw=P[2] + 2), 1), (dict(kr=P[9] + 2), 1), (dict(pos=P[5] + 2), 1),
+    (dict(qo=P[0] + 2), 1), (dict(qo=P[1]), 1), (dict(ko=P[6]), 1), (dict(qo=P[2]), 1), (dict(qr=P[6]), 1),
+    (dict(qo=P[0], qs=512), 1),                                  # in place only where rows are contiguous
+    (dict(q=P[6] - 100 * 512, qs=512), 1),                       # the output inside a strided input
+    (dict(T=0), 0), (dict(T=0, q=None, qo=None), 0),
+])
+def test_qk_norm_rotary_rejects_bad_arguments(lib, bad, code):
+    assert _qk(lib, **bad) == code
+
+
+def _qk_bwd(lib, pairs=(16, 16), **kw):
+    a = dict(q=P[0], k=P[1], qr=P[2], kr=P[3], dqo=P[4], dko=P[5], qw=P[6], kw_=P[7], freq=P[8], pos=P[9], dt=1, T=128, Hq=4,
+             Hk=2, d=64, qs=256, ks=128, pairs=(ctypes.c_int * max(1, len(pairs)))(*pairs), naxes=len(pairs), il=0, per=0,
+             dq=P[10], dk=P[11], dqw=P[12], dkw=P[13], ws=P[14], bytes=1 << 27, stream=None)
+    a.update(kw)
+    return lib.la_qk_norm_rotary_backward(*a.values())
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(dt=-1), 1), (dict(T=-1), 1), (dict(Hq=0), 1), (dict(d=1), 1), (dict(qs=200), 1), (dict(per=-1), 1),
+    (dict(pairs=(16, 17)), 1), (dict(il=3), 1), (dict(ws=None), 1), (dict(ws=P[14] + 8), 1), (dict(q=None), 1),
+    (dict(qr=None), 1), (dict(kr=None), 1), (dict(dqo=None), 1), (dict(dk=None), 1), (dict(Hk=0, ks=0), 1),
+    (dict(dq=P[10] + 1), 1), (dict(dqw=P[12] + 2), 1), (dict(d=1025, qs=4100, ks=2050), 2),
+])
+def test_qk_norm_rotary_backward_rejects_bad_arguments(lib, bad, code):
+    assert _qk_bwd(lib, **bad) == code
+
+
 def test_decay_binding_refuses_what_does_not_fit():
     import kernelized_linear_attention_gb300 as la
     x, ld = torch.zeros(4, 2, 8), torch.zeros(2)

@@ -142,3 +142,27 @@ def test_decay_attention_gradients():
     got = ops.decay_attention_backward(q, k, v, do, ld, 0.6, cu, state_in=s, dstate_out=ds)
     for x, y in zip((q, k, v, s), got):
         assert np.allclose(_num_grad(loss, x), y, atol=1e-7)
+
+
+def test_qk_norm_rotary_worked_values():
+    x = np.array([3.0, 4.0, 0.0]).reshape(1, 1, 3)
+    y, r = ops.qk_norm_rotary(x, np.array([1.0, 2.0, 5.0]), [np.pi / 2], [[1]], [1], eps=0.0)
+    assert np.allclose(r, np.sqrt(3.0) / 5)
+    assert np.allclose(y.ravel(), np.array([-8.0, 3.0, 0.0]) * np.sqrt(3.0) / 5)   # a quarter of a turn of (3, 8)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("per_head", [False, True])
+def test_qk_norm_rotary_gradients(per_head, interleaved):
+    g = np.random.default_rng(6)
+    x, dy = g.normal(size=(4, 2, 7)), g.normal(size=(4, 2, 7))
+    w = g.normal(size=(2, 7) if per_head else 7)
+    args = ([0.3, 1.0, 0.01], [[0, 5], [1, -3], [2, 9], [70, 0]], [1, 2], interleaved)
+
+    def loss():
+        return (ops.qk_norm_rotary(x, w, *args, eps=0.1)[0] * dy).sum()
+
+    _, r = ops.qk_norm_rotary(x, w, *args, eps=0.1)
+    dx, dw = ops.qk_norm_rotary_backward(x, r, dy, w, *args)
+    assert np.allclose(_num_grad(loss, x), dx, atol=1e-7)
+    assert np.allclose(_num_grad(loss, w), dw, atol=1e-7)
