@@ -321,7 +321,9 @@ LA_API la_status la_noalloc_error(int* code, void* stream);
  *   call are incomplete and the context stays usable.  Later la_gated_scan and
  *   la_gated_scan_backward launches over more than one tile of tokens likewise wait
  *   1 ms in each tile for a state that nothing publishes, record
- *   LA_DEVERR_WAIT_TIMEOUT and go on from zero.  enable = 0 restores normal
+ *   LA_DEVERR_WAIT_TIMEOUT and go on from zero.  The tensor-core kernels of
+ *   la_decay_attention and its gradients wait 1 ms likewise, record it, and end
+ *   as after any wait that ran out.  enable = 0 restores normal
  *   operation.  Device-wide; not for concurrent use with other calls.  Returns
  *   LA_OK, or LA_ERR_CUDA when the device flag cannot be written.
  */

@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "internal.h"
+#include "ops/decay.h"
 #include "ops/ops.h"
 
 namespace la {
@@ -522,6 +523,7 @@ la_status la_workspace_error(const void* workspace, int* code, void* stream) {
 
 la_status la_test_force_wait_timeout(int enable) {
     if (la::gated_force_wait_timeout(enable ? 1 : 0) != cudaSuccess) return LA_ERR_CUDA;
+    if (la::decay_force_wait_timeout(enable ? 1 : 0) != cudaSuccess) return LA_ERR_CUDA;
     return la::tc_force_wait_timeout(enable ? 1 : 0) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }
 

@@ -110,7 +110,7 @@ template <int N>
 __global__ void __launch_bounds__(kJoinThreads) decay_join_kernel(const __grid_constant__ DecayCall c,
                                                                   const __grid_constant__ DecayStates p) {
     using V = Vec<float, N>;
-    if (c.cu_seqlens && c.hdr->error) return;
+    if (decay_malformed(c)) return;
     const int s = blockIdx.x, h = blockIdx.y, n = c.dk * c.dv;
     const int e = (blockIdx.z * kJoinThreads + threadIdx.x) * N;
     DecaySegment last, first;
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kSimtThreads) decay_states_kernel(const __grid
     const int a0 = blockIdx.z / nb * kCols, b0 = blockIdx.z % nb * kCols;
     DecaySegment g;
     bool any = true;
-    if (c.cu_seqlens && c.hdr->error) return;
+    if (decay_malformed(c)) return;
     if (final) any = decay_edge_segment(c, blockIdx.x, p.reverse, g);
     else if (!decay_segment(c, blockIdx.x, g) || (p.reverse ? decay_first(g) : decay_last(g))) return;
     const DecayBase base = decay_base(c.log_decay[h]);
@@ -487,11 +487,14 @@ cudaError_t step(const void* q, const void* k, const void* v, const float* log_d
     return cudaGetLastError();
 }
 
-bool vector_rows(const DecayCall& c, int dtype, std::initializer_list<const void*> arrays) {
-    const int n = dtype == LA_F32 ? 4 : 8;
+bool on_16_bytes(std::initializer_list<const void*> arrays) {
     uintptr_t at = 0;
     for (const void* a : arrays) at |= reinterpret_cast<uintptr_t>(a);
-    return at % 16 == 0 && c.dk % n == 0 && c.dv % n == 0;
+    return at % 16 == 0;
+}
+bool vector_rows(const DecayCall& c, int dtype, std::initializer_list<const void*> arrays) {
+    const int n = dtype == LA_F32 ? 4 : 8;
+    return on_16_bytes(arrays) && c.dk % n == 0 && c.dv % n == 0;
 }
 
 constexpr int64_t kLongest = 1 << 20;      // tokens of a segment: exact in fp32
@@ -512,6 +515,7 @@ cudaError_t join(const DecayCall& c, const DecayStates& p, cudaStream_t s) {
 }
 
 cudaError_t states(const DecayCall& c, const DecayStates& p, int dtype, bool final, cudaStream_t s) {
+    if (decay_tc_fits(c, dtype) && on_16_bytes({p.y, p.z})) return decay_tc_states(c, p, final, s);
     const dim3 grid(final ? c.nseq : c.segments, c.H, (unsigned)(ceil_div(c.dk, kCols) * ceil_div(c.dv, kCols)));
     const bool vec = vector_rows(c, dtype, {p.y, p.z});
     if (dtype == LA_F32) decay_states_kernel<float><<<grid, kSimtThreads, 0, s>>>(c, p, final, vec);
@@ -527,7 +531,8 @@ cudaError_t enter(const DecayCall& c, const DecayStates& p, int dtype, cudaStrea
 }
 
 cudaError_t pass(const DecayCall& c, const DecayPass& p, int dtype, cudaStream_t s) {
-    if (c.segments == 0) return cudaSuccess;
+    if (c.T == 0) return cudaSuccess;
+    if (decay_tc_fits(c, dtype) && on_16_bytes({p.x, p.y, p.z, p.out})) return decay_tc_pass(c, p, s);
     const dim3 grid(c.segments, c.H, (unsigned)ceil_div(p.dz, kCols));
     const size_t smem = simt_smem(p.ds);
     const bool vec = vector_rows(c, dtype, {p.x, p.y, p.z});

@@ -73,6 +73,12 @@ cudaError_t decay_step(const void* q, const void* k, const void* v, const float*
                        int dk, int dv, float scale, const float* state_in, float* state_out, void* out,
                        cudaStream_t s);
 
+// Tensor cores: bf16 of up to 128 channels, a multiple of 8, in arrays that start on 16 bytes (decay_tc.cu).
+bool decay_tc_fits(const DecayCall& c, int dtype);
+cudaError_t decay_tc_states(const DecayCall& c, const DecayStates& p, bool final, cudaStream_t s);
+cudaError_t decay_tc_pass(const DecayCall& c, const DecayPass& p, cudaStream_t s);
+cudaError_t decay_force_wait_timeout(int enable);   // test hook behind la_test_force_wait_timeout
+
 // ---------------------------------------------------------------------------
 // Device helpers
 // ---------------------------------------------------------------------------
@@ -96,10 +102,16 @@ __device__ __forceinline__ float decay_power(const DecayBase& b, int n) {
     return fmaf(g, e * 0.693147182f, g);
 }
 
+// Whether cu_seqlens broke the packing rules: nothing is computed then.  (Another error that a block of this call has
+// recorded changes nothing for the others.)
+__device__ __forceinline__ bool decay_malformed(const DecayCall& c) {
+    return c.cu_seqlens && c.hdr->error == LA_DEVERR_CU_SEQLENS;
+}
+
 // The segment of block index i: from the table, or of an equal-length batch.
 __device__ __forceinline__ bool decay_segment(const DecayCall& c, int i, DecaySegment& g) {
     if (c.cu_seqlens) {
-        if (c.hdr->error || i >= c.hdr->n_units) return false;
+        if (decay_malformed(c) || i >= c.hdr->n_units) return false;
         g = c.table[i];
         return true;
     }

@@ -323,6 +323,26 @@ def test_two_streams_at_once(la):
             assert all(torch.equal(x, y) for x, y in zip(g, w))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_wait_that_runs_out_is_reported(la, d):
+    c = _case([500, 300], 2, d, d, "bf16", seed=22)
+    want = _forward(la, c, True) + _backward(la, c, True)
+    ws = torch.empty(la.la_decay_attention_backward_workspace_bytes(torch.bfloat16, True, 2, 800, 2, d, d), dtype=torch.uint8,
+                     device="cuda")
+    la.la_test_force_wait_timeout(True)
+    try:
+        _forward(la, c, True, cu_seqlens=c["cu_t"], return_state=True, workspace=ws)
+        assert la.la_workspace_error(ws) == 2
+        _backward(la, c, True, cu_seqlens=c["cu_t"], return_dstate=True, workspace=ws)
+        assert la.la_workspace_error(ws) == 2
+    finally:
+        la.la_test_force_wait_timeout(False)
+    got = (_forward(la, c, True, cu_seqlens=c["cu_t"], return_state=True, workspace=ws)
+           + _backward(la, c, True, cu_seqlens=c["cu_t"], return_dstate=True, workspace=ws))
+    assert la.la_workspace_error(ws) == 0
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
 def test_no_tokens(la):
     c = _case([0, 0], 2, 64, 64, "bf16", seed=19)
     out, new = _forward(la, c, True)
