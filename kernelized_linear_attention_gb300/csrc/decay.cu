@@ -499,6 +499,36 @@ bool vector_rows(const DecayCall& c, int dtype, std::initializer_list<const void
 
 constexpr int64_t kLongest = 1 << 20;      // tokens of a segment: exact in fp32
 
+// Tokens of a segment.  Tensor cores: whole chunks of 128, one block per SM.  Equal sequences are cut so that the waves
+// of blocks times a segment's chunks, and two for a block's beginning and end, are fewest; packed ones, whose lengths
+// are not known here, into three blocks' worth per SM.  CUDA cores: four blocks per SM, of chunks of 32.
+int64_t segment_length(const DecayCall& c, bool tensor, int sms) {
+    const int64_t n = c.cu_seqlens ? c.T : c.T / c.nseq;
+    if (n < 1) return 128;
+    if (!tensor) {
+        const int64_t L = ceil_div(ceil_div(c.T * c.H, 4 * sms), 64) * 64;
+        return min64(min64(L < 64 ? 64 : L, ceil_div(n, 64) * 64), kLongest);
+    }
+    const int64_t chunks = ceil_div(n, 128);
+    int64_t best = 1, least = INT64_MAX;
+    if (c.cu_seqlens) {
+        best = ceil_div(c.T, 128) * c.H / (3 * sms);
+        best = min64(best < 1 ? 1 : best, chunks);
+    } else {
+        // (more segments than a few per SM, or than chunks, never pay)
+        const int64_t pairs = (int64_t)c.nseq * c.H, most = min64(chunks, ceil_div(8 * sms, pairs));
+        for (int64_t per = 1; per <= most; ++per) {
+            const int64_t k = ceil_div(chunks, per);
+            const int64_t cost = ceil_div(ceil_div(chunks, k) * pairs, sms) * (k + 2);
+            if (cost < least) {
+                least = cost;
+                best = k;
+            }
+        }
+    }
+    return min64(best * 128, kLongest);
+}
+
 cudaError_t plan(const DecayCall& c, cudaStream_t s) {
     if (!c.cu_seqlens) return cudaMemsetAsync(c.hdr, 0, sizeof(WsHeader), s);
     decay_plan_kernel<<<1, kPlanThreads, 0, s>>>(c);
@@ -546,14 +576,10 @@ cudaError_t pass(const DecayCall& c, const DecayPass& p, int dtype, cudaStream_t
 }  // namespace
 
 size_t decay_layout(DecayCall& c, int dtype, bool backward, void* workspace) {
-    // segments: two for each SM, of whole 128-token chunks
     int sms = sm_count();
     if (sms <= 0) sms = 152;
-    const int64_t n = c.cu_seqlens ? c.T : c.T / c.nseq;
-    int64_t L = ceil_div(ceil_div(c.T * c.H, 2 * sms), 128) * 128;
-    L = min64(L < 128 ? 128 : L, ceil_div(n < 1 ? 1 : n, 128) * 128);
-    L = min64(L, kLongest);
-    c.L = (int)L;
+    c.L = (int)segment_length(c, decay_tc_fits(c, dtype), sms);
+    const int64_t n = c.cu_seqlens ? c.T : c.T / c.nseq, L = c.L;
     const int64_t per = n > 0 ? ceil_div(n, L) : 0;
     const int64_t segments = c.cu_seqlens ? c.T / L + c.nseq : per * c.nseq;
     c.segments = (int)segments;

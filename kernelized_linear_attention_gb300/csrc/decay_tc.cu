@@ -30,16 +30,13 @@ constexpr uint32_t kTile = kC * 128;          // [128][64] bf16
 constexpr uint64_t kDrainNs = 100000000ull;   // bound of the waits before an early exit
 __device__ int g_force_wait_timeout = 0;      // test hook: a wait that nothing ends
 
-template <int D> struct Shape {
-    static constexpr int blocks = D / 64;                  // of 64 channels
-    static constexpr int threads = D == 64 ? 256 : 512;
-    static constexpr int parts = threads / 128;            // column groups of 32 (of D) or 128 / parts (of the scores)
-    static constexpr int per_sm = D == 64 ? 2 : 1;
-};
-
 // ---------------------------------------------------------------------------
 // Pieces
 // ---------------------------------------------------------------------------
+// Bytes to the next multiple of 1024 (as an offset, so that what lies there is known to be shared memory: through a
+// pointer that went through an integer every access is a generic one).
+__device__ __forceinline__ uint32_t to_1024(const void* p) { return (0u - smem_u32(p)) & 1023u; }
+
 // A pair of fp32 as bf16 and the rest.
 __device__ __forceinline__ uint32_t split(uint64_t& v) {
     const uint32_t h = f32x2_to_bf16x2(v);
@@ -48,51 +45,110 @@ __device__ __forceinline__ uint32_t split(uint64_t& v) {
 }
 __device__ __forceinline__ uint64_t pair_of(uint32_t w) { return f32x2_of(w << 16, w & 0xffff0000u); }
 
+// The loops of all roles have to stay in the instruction caches together (unrolled and with every wait's retries in
+// place the products took 128 us for 65536 x 16 x 64, code of 78 KB): waits that are not over at once, and what only
+// values that are not finite need, are calls.
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity); }
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+    return mbar_try_wait(bar, parity) || wait_long(bar, parity);
+}
+// After a wait for tensor memory: values that were on their way are not used before it.
+template <int N>
+__device__ __forceinline__ void arrived(uint32_t (&v)[N]) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) asm volatile("" : "+r"(v[j]));
+}
+// A whole warp's wait: true for every lane or for none.
+__device__ __forceinline__ bool wait_w(uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait(bar, parity));
+}
+// A warp's arrival, behind what its lanes have written to shared memory for the async proxy.
+__device__ __forceinline__ void arrive_w(uint64_t* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+__device__ __forceinline__ void init_all(uint64_t* bars, int n, uint32_t count) {
+    for (int i = 0; i < n; ++i) mbar_init(bars + i, count);
+}
+
 // Powers 0 .. 128 of the decay.
 __device__ __forceinline__ void fill_powers(float* pw, const DecayBase& base) {
     for (int i = threadIdx.x; i <= kC; i += blockDim.x) pw[i] = decay_power(base, i);
 }
 
-// Whether a value of 32 channels of this thread's row of a tile is not finite; rows from n on are set to zero.
-template <int Blocks>
-__device__ __forceinline__ bool inspect(unsigned char* tile, int row, int part, int n) {
-    unsigned char* const block = tile + (part >> 1) * kTile;
-    const int c0 = (part & 1) * 4;
-    if (row >= n) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(block + sw128_chunk(row, c0 + c)) = make_uint4(0, 0, 0, 0);
-        return false;
+// A channel that is not finite at token `row` of the chunk.
+__device__ inline void move_edge(unsigned short* edge, int row, bool reverse) {
+    unsigned short held = *edge;
+    while (reverse ? row + 1 > held : row < held) {
+        const unsigned short seen = atomicCAS(edge, held, (unsigned short)(reverse ? row + 1 : row));
+        if (seen == held) break;
+        held = seen;
     }
-    uint32_t top = 0;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const uint4 w = *reinterpret_cast<const uint4*>(block + sw128_chunk(row, c0 + c));
-        top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
-                                     __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+}
+
+// Sets a row's values that are not finite to zero in four of its 16-byte chunks (row -1: nothing).
+__device__ __noinline__ void clear_strange(unsigned char* tile, unsigned short* edge, int* strange, int row, int c0, bool reverse) {
+    if (row < 0) return;
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i) {
+        uint16_t* const at = reinterpret_cast<uint16_t*>(tile + sw128_chunk(row, c0 + (i >> 3))) + (i & 7);
+        if ((*at & 0x7f80u) != 0x7f80u) continue;
+        *at = 0;
+        move_edge(edge + 8 * c0 + i, row, reverse);
+        *strange = 1;
     }
-    return (top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u;
+}
+// Channel i of a row's 32 (pairs in o) from the token on that made it strange is NaN.
+__device__ __noinline__ uint32_t mark_strange(uint32_t o, const unsigned short* edge, int row, bool reverse) {
+    if (reverse ? row < edge[0] : row >= edge[0]) o = (o & 0xffff0000u) | 0x7fc0u;
+    if (reverse ? row < edge[1] : row >= edge[1]) o = (o & 0xffffu) | 0x7fc00000u;
+    return o;
+}
+
+__device__ __forceinline__ void store_32(void* to, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 
 // ---------------------------------------------------------------------------
 // State sums of a segment
 // ---------------------------------------------------------------------------
+// Warp 0 loads, warp 1 issues the products, 16 warps weight y (D = 64: eight for the even chunks and eight for the odd
+// ones).  The tensor cores truncate when they accumulate: after kFlush chunks the sums go on in fp32 registers, rounded
+// to nearest.
+constexpr int kStatesThreads = 640;
+constexpr int kFlush = 8;
+template <int D> struct StatesShape {
+    static constexpr int blocks = D / 64;                 // of 64 channels
+    static constexpr int stages = D == 64 ? 4 : 2;        // of y and z
+    static constexpr int buffers = D == 64 ? 2 : 1;       // of weighted y
+    static constexpr int warps = D == 64 ? 8 : 16;        // that weight one chunk
+    static constexpr int sums = D == 64 ? 2 : 1;          // accumulators, of `columns` each
+    static constexpr int columns = D == 64 ? 128 : 384;
+    static constexpr int tmem = D == 64 ? 256 : 512;
+};
 template <int D> struct __align__(1024) StatesSmem {
-    unsigned char yw[3][Shape<D>::blocks][kTile];          // weighted y in three parts
-    unsigned char y[Shape<D>::blocks][kTile], z[2][Shape<D>::blocks][kTile];
+    using F = StatesShape<D>;
+    unsigned char yw[F::buffers][3][F::blocks][kTile];    // weighted y in three parts
+    unsigned char y[F::stages][F::blocks][kTile], z[F::stages][F::blocks][kTile];
     float pw[kC + 4];
-    uint64_t full_y, full_z[2], mma, drain, never;
+    uint64_t full[F::stages], empty[F::stages];           // TMA -> weighting, products;  both -> TMA
+    uint64_t yw_full[F::buffers], yw_empty[F::buffers];   // weighting -> products;  products -> weighting
+    uint64_t sum_full[2], sum_empty[2];                   // products -> registers;  registers -> products
+    uint64_t drain, never;
     uint32_t tmem;
 };
 
 template <int D>
-__global__ void __launch_bounds__(Shape<D>::threads, Shape<D>::per_sm)
+__global__ void __launch_bounds__(kStatesThreads, 1)
     decay_tc_states_kernel(const __grid_constant__ DecayCall c, const __grid_constant__ DecayStates p, bool final,
                            const __grid_constant__ CUtensorMap my, const __grid_constant__ CUtensorMap mz) {
-    using F = Shape<D>;
+    using F = StatesShape<D>;
     extern __shared__ __align__(1024) unsigned char raw[];
-    StatesSmem<D>& s = *reinterpret_cast<StatesSmem<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    StatesSmem<D>& s = *reinterpret_cast<StatesSmem<D>*>(raw + to_1024(raw));
     const int h = blockIdx.x, index = blockIdx.y + 65535 * blockIdx.z;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, part = warp >> 2, row = 32 * q + lane;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     DecaySegment g;
     if (index >= (final ? c.nseq : c.segments)) return;
     if (decay_malformed(c)) return;
@@ -104,7 +160,7 @@ __global__ void __launch_bounds__(Shape<D>::threads, Shape<D>::per_sm)
         if (!decay_edge_segment(c, index, p.reverse, g)) {
             // an empty sequence: what enters it leaves it
             const float* from = p.edge_in ? p.edge_in + ((int64_t)index * c.H + h) * size : nullptr;
-            for (int i = threadIdx.x; i < size; i += F::threads) to[i] = from ? from[i] : 0.f;
+            for (int i = threadIdx.x; i < size; i += kStatesThreads) to[i] = from ? from[i] : 0.f;
             return;
         }
         enter = decay_entering(c, g, h, p.reverse, p.edge_in);
@@ -113,25 +169,20 @@ __global__ void __launch_bounds__(Shape<D>::threads, Shape<D>::per_sm)
         to = c.states[p.reverse] + ((int64_t)(decay_slot(g) - (p.reverse ? 1 : 0)) * c.H + h) * size;
     }
     const DecayBase base = decay_base(c.log_decay[h]);
-    const int chunks = (g.end - g.start + kC - 1) / kC;
-    int y_loads = 0, z_loads = 0;             // of thread 0
-    auto load_y = [&]() {
-        mbar_arrive_expect_tx(&s.full_y, F::blocks * kTile);
-        for (int b = 0; b < F::blocks; ++b) tma_load_3d(s.y[b], &my, 64 * b, h, g.start + y_loads * kC, &s.full_y);
-        ++y_loads;
-    };
-    auto load_z = [&]() {
-        uint64_t* const full = &s.full_z[z_loads & 1];
-        mbar_arrive_expect_tx(full, F::blocks * kTile);
-        for (int b = 0; b < F::blocks; ++b) tma_load_3d(s.z[z_loads & 1][b], &mz, 64 * b, h, g.start + z_loads * kC, full);
-        ++z_loads;
-    };
+    const int chunks = (g.end - g.start + kC - 1) / kC, groups = (chunks + kFlush - 1) / kFlush;
     if (threadIdx.x == 0) {
-        for (uint64_t* b : {&s.full_y, &s.full_z[0], &s.full_z[1], &s.mma, &s.drain, &s.never}) mbar_init(b, 1);
+        init_all(s.full, F::stages, 1);
+        init_all(s.empty, F::stages, F::warps + 1);
+        init_all(s.yw_full, F::buffers, F::warps);
+        init_all(s.yw_empty, F::buffers, 1);
+        init_all(s.sum_full, 2, 1);
+        init_all(s.sum_empty, 2, F::warps);
+        init_all(&s.drain, 1, 1);
+        init_all(&s.never, 1, 1);
         fence_mbar_init();
     }
-    if (warp == 0) {
-        tmem_alloc(&s.tmem, 128);
+    if (warp == 1) {
+        tmem_alloc(&s.tmem, F::tmem);
         tmem_relinquish();
     }
     fill_powers(s.pw, base);
@@ -139,466 +190,626 @@ __global__ void __launch_bounds__(Shape<D>::threads, Shape<D>::per_sm)
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = s.tmem;
-    if (threadIdx.x == 0) {
-        load_y();
-        load_z();
-        if (chunks > 1) load_z();
-    }
     bool ok = true;
-    if (g_force_wait_timeout) ok = mbar_wait(&s.never, 0, 1000000ull);
+    int loads = 0;
+    float sum[32];                            // of the warps that weight: their 32 columns of their row
+    const int w = warp - 4, q = warp & 3, part = (D == 64 ? w & 7 : w) >> 2, row = 32 * q + lane, col = 32 * part;
 
-    for (int k = 0; k < chunks; ++k) {
-        const int st = k & 1, t0 = g.start + k * kC, n = min(kC, g.end - t0);
-        ok = ok && mbar_wait(&s.full_y, k & 1);
-        if (k > 0) {
-            // the products of the chunk before have read the weighted y and their z
-            ok = ok && mbar_wait(&s.mma, (k - 1) & 1);
-            if (ok && threadIdx.x == 0 && k + 1 < chunks) load_z();
-        }
-        ok = ok && mbar_wait(&s.full_z[st], (k >> 1) & 1);
-        {
-            const float far = p.reverse ? c.scale * decay_power(base, t0 - g.start) : decay_power(base, g.end - t0 - n);
-            const float w = row < n ? far * s.pw[p.reverse ? row + 1 : n - 1 - row] : 0.f;
-            const unsigned char* const from = s.y[part >> 1];
-            const int c0 = (part & 1) * 4;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t at = sw128_chunk(row, c0 + j);
-                const uint4 v = *reinterpret_cast<const uint4*>(from + at);
-                const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-                uint32_t o[3][4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint64_t f = f32x2_mul(pair_of(row < n ? in[i] : 0u), f32x2_splat(w));
-                    o[0][i] = split(f);
-                    o[1][i] = split(f);
-                    o[2][i] = f32x2_to_bf16x2(f);
+    if (warp == 0) {
+        if (lane == 0) {
+            for (; loads < chunks && ok; ++loads) {
+                const int st = loads % F::stages;
+                if (loads >= F::stages) ok = wait(&s.empty[st], (loads / F::stages - 1) & 1);
+                if (!ok) break;
+                mbar_arrive_expect_tx(&s.full[st], 2 * F::blocks * kTile);
+                for (int b = 0; b < F::blocks; ++b) {
+                    tma_load_3d(s.y[st][b], &my, 64 * b, h, g.start + loads * kC, &s.full[st]);
+                    tma_load_3d(s.z[st][b], &mz, 64 * b, h, g.start + loads * kC, &s.full[st]);
                 }
-#pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    *reinterpret_cast<uint4*>(s.yw[i][part >> 1] + at) = make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
-                // nothing from another sequence
-                if (row >= n) *reinterpret_cast<uint4*>(s.z[st][part >> 1] + at) = make_uint4(0, 0, 0, 0);
             }
         }
-        fence_async_smem();
-        if (__syncthreads_or(!ok)) break;
-        if (threadIdx.x == 0 && k + 1 < chunks) load_y();
         __syncwarp();
-        if (warp == 0) {
+    } else if (warp == 1) {
+        for (int k = 0; k < chunks && ok; ++k) {
+            const int st = k % F::stages, b = k % F::buffers, f = k / kFlush, a = f % F::sums;
+            ok = wait_w(&s.yw_full[b], (k / F::buffers) & 1);
+            if (ok && k % kFlush == 0 && f >= F::sums) ok = wait_w(&s.sum_empty[a], (f / F::sums - 1) & 1);
+            if (!ok) break;
             tc_fence_after();
             constexpr uint32_t id = idesc_bf16(128, D, true, true);
             const uint64_t dz = sdesc_sw128(smem_u32(s.z[st]), kTile, 1024);
             // D = 64: the first two parts of y are one product's 128 rows; the third's other rows are not used
 #pragma unroll
             for (int i = 0; i < (D == 64 ? 2 : 3); ++i) {
-                const uint64_t dy = sdesc_sw128(smem_u32(s.yw[D == 64 ? 2 * i : i]), kTile, 1024);
-                const uint32_t acc = tm + (D == 64 ? 64 * i : 0);
+                const uint64_t dy = sdesc_sw128(smem_u32(s.yw[b][D == 64 ? 2 * i : i]), kTile, 1024);
+                const uint32_t acc = tm + a * F::columns + D * i;
 #pragma unroll
                 for (int j = 0; j < kC / 16; ++j)
-                    mma_ss_w(acc, sdesc_add(dy, 2048 * j), sdesc_add(dz, 2048 * j), id,
-                             k > 0 || j > 0 || (D != 64 && i > 0) ? 1u : 0u);
+                    mma_ss_w(acc, sdesc_add(dy, 2048 * j), sdesc_add(dz, 2048 * j), id, k % kFlush > 0 || j > 0 ? 1u : 0u);
             }
-            mma_commit_w(&s.mma);
+            mma_commit_w(&s.yw_empty[b]);
+            mma_commit_w(&s.empty[st]);
+            if (k % kFlush == kFlush - 1 || k + 1 == chunks) mma_commit_w(&s.sum_full[a]);
         }
+    } else if (warp >= 4) {
+        const int mine = D == 64 ? w >> 3 : 0, block = part >> 1, c0 = (part & 1) * 4;
+        if (g_force_wait_timeout) ok = __all_sync(0xffffffffu, mbar_wait(&s.never, 0, 1000000ull));
+#pragma unroll
+        for (int j = 0; j < 32; ++j) sum[j] = 0.f;
+        int flushed = 0;
+        auto flush = [&]() {
+            const int a = flushed % F::sums;
+            ok = wait_w(&s.sum_full[a], (flushed / F::sums) & 1);
+            if (!ok) return;
+            tc_fence_after();
+            // D = 64: rows 64 .. 127 of the first columns are the second part's; the third part's rows are 0 .. 63
+#pragma unroll
+            for (int i = 0; i < (D == 64 ? 2 : 3); ++i) {
+                if (D == 64 && i == 1 && q >= 2) break;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t v[16];
+                    tmem_ld16(tmem_addr(tm, 32 * q, a * F::columns + D * i + col + 16 * u), v);
+                    tmem_ld_wait();
+                    arrived(v);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) sum[16 * u + j] += __uint_as_float(v[j]);
+                }
+            }
+            tc_fence_before();
+            arrive_w(&s.sum_empty[a]);
+            ++flushed;
+        };
+        for (int k = mine; k < chunks && ok; k += F::buffers) {
+            const int st = k % F::stages, b = k % F::buffers, t0 = g.start + k * kC, n = min(kC, g.end - t0);
+            ok = wait_w(&s.full[st], (k / F::stages) & 1);
+            if (ok && k >= F::buffers) ok = wait_w(&s.yw_empty[b], (k / F::buffers - 1) & 1);
+            if (!ok) break;
+            const float far = p.reverse ? c.scale * decay_power(base, t0 - g.start) : decay_power(base, g.end - t0 - n);
+            const float weight = row < n ? far * s.pw[p.reverse ? row + 1 : n - 1 - row] : 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t at = sw128_chunk(row, c0 + j);
+                const uint4 v = *reinterpret_cast<const uint4*>(s.y[st][block] + at);
+                const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                uint32_t o[3][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint64_t e = f32x2_mul(pair_of(row < n ? in[i] : 0u), f32x2_splat(weight));
+                    o[0][i] = split(e);
+                    o[1][i] = split(e);
+                    o[2][i] = f32x2_to_bf16x2(e);
+                }
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    *reinterpret_cast<uint4*>(s.yw[b][i][block] + at) = make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
+                // nothing from another sequence
+                if (row >= n) *reinterpret_cast<uint4*>(s.z[st][block] + at) = make_uint4(0, 0, 0, 0);
+            }
+            fence_async_smem();
+            arrive_w(&s.yw_full[b]);
+            arrive_w(&s.empty[st]);
+            if (mine == 0 && k >= kFlush * (flushed + 1)) flush();
+        }
+        while (mine == 0 && ok && flushed < groups) flush();
     }
-    ok = ok && mbar_wait(&s.mma, (chunks - 1) & 1);
     if (__syncthreads_or(!ok)) {
         // copies and products on their way end before the block does
         if (threadIdx.x == 0) {
             record_error(c.hdr, LA_DEVERR_WAIT_TIMEOUT);
-            mbar_wait(&s.full_y, (y_loads - 1) & 1, kDrainNs);
-            for (int i = max(0, z_loads - 2); i < z_loads; ++i) mbar_wait(&s.full_z[i & 1], (i >> 1) & 1, kDrainNs);
+            for (int i = max(0, loads - F::stages); i < loads; ++i)
+                mbar_wait(&s.full[i % F::stages], (i / F::stages) & 1, kDrainNs);
         }
-        __syncwarp();
-        if (warp == 0) {
+        if (warp == 1) {
             mma_commit_w(&s.drain);
             mbar_wait(&s.drain, 0, kDrainNs);
         }
     } else {
-        tc_fence_after();
+        const bool on = warp >= 4 && (D != 64 || w < 8);
         const float keep = decay_power(base, g.end - g.start);
-        const int col = 32 * part;
-        uint32_t v[32];
         if (D == 64) {
-            // rows 64 .. 127 hold the second part of rows 0 .. 63
             float (*ex)[65] = reinterpret_cast<float (*)[65]>(s.yw);
-            tmem_ld32(tmem_addr(tm, 32 * q, col), v);
-            tmem_ld_wait();
-            if (q >= 2) {
+            if (on && q >= 2) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) ex[row - 64][col + j] = __uint_as_float(v[j]);
+                for (int j = 0; j < 32; ++j) ex[row - 64][col + j] = sum[j];
             }
             __syncthreads();
-            if (q < 2) {
-                uint32_t lo[32];
-                tmem_ld32(tmem_addr(tm, 32 * q, 64 + col), lo);
-                tmem_ld_wait();
+            if (on && q < 2) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    v[j] = __float_as_uint(__uint_as_float(v[j]) + (ex[row][col + j] + __uint_as_float(lo[j])));
+                for (int j = 0; j < 32; ++j) sum[j] += ex[row][col + j];
             }
-        } else {
-            tmem_ld32(tmem_addr(tm, 32 * q, col), v);
-            tmem_ld_wait();
         }
-        if (row < c.dk) {
+        if (on && row < c.dk) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
                 if (col + j >= c.dv) break;
                 const int64_t at = (int64_t)row * c.dv + col + j;
-                const float f = __uint_as_float(v[j]);
-                to[at] = enter ? fmaf(keep, enter[at], f) : f;
+                to[at] = enter ? fmaf(keep, enter[at], sum[j]) : sum[j];
             }
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) tmem_dealloc(tm, 128);
+    if (warp == 1) tmem_dealloc(tm, F::tmem);
 }
 
 // ---------------------------------------------------------------------------
 // Products of a segment
 // ---------------------------------------------------------------------------
+// Warp 0 loads; warps 1, 2 and 3 issue products (scores and P z; the state's update; x S: one warp for all was what the
+// others waited for, a hundred cycles and more for each of its waits and commits); warps 4 .. 11 look z over and turn
+// scores into P; 12 .. 19 weight y (in its place, once the scores have read it) and make an operand of the state;
+// 20 .. 27 write the outputs.
+constexpr int kPassThreads = 896;
+template <int D> struct PassShape {
+    static constexpr int blocks = D / 64;
+    static constexpr int stages = D == 64 ? 4 : 2, z_stages = D == 64 ? 4 : 1;   // of x and y; of z
+    static constexpr int scores = D == 64 ? 2 : 1;        // buffers of scores and P
+    // operands of the state; D = 64: its two parts side by side, one product of twice the width
+    static constexpr int states = D == 64 ? 2 : 1, width = 128;
+    static constexpr int ring = 4;                        // chunks from the look at z to the outputs, at most
+    // tensor memory: the state, scores (then P: for each 16 tokens eight columns), x S, P z
+    static constexpr uint32_t state = 0, score = D, read = score + 128 * scores, out = read + width;
+};
 template <int D> struct __align__(1024) PassSmem {
-    unsigned char x[Shape<D>::blocks][kTile], y[Shape<D>::blocks][kTile], z[Shape<D>::blocks][kTile];
-    unsigned char yw[2][Shape<D>::blocks][kTile];                     // weighted y in two parts; outputs on their way
-    // the state [D][64] in blocks, in two parts; D = 64: and the second part's own sums (rows 64 .. 127 of tensor memory)
-    unsigned char state[D == 64 ? 3 : 2][Shape<D>::blocks][D * 128];
-    float pw[kC + 4];
-    __align__(16) float in_block[32];                                 // decay inside a block of 32 tokens
-    int edge[D];                                                      // first (last) token whose channel is not finite
-    uint64_t full_xy, full_z, mma_a, mma_o, mma_s, mma_f, drain, never;
+    using F = PassShape<D>;
+    unsigned char x[F::stages][F::blocks][kTile], y[F::stages][F::blocks][kTile], z[F::z_stages][F::blocks][kTile];
+    unsigned char state[F::states][2][F::blocks][D * 128];   // [D][64] in blocks, in two parts
+    float pw[kC + 4 + 32];                                // powers of the decay, then 0 .. 31 of them with the scale
+    __align__(16) float in_block[32];                     // decay inside a block of 32 tokens
+    // by chunk: the first token whose channel is not finite (or 128); reverse: one behind the last one (or 0)
+    unsigned short edge[F::ring][D];
+    int strange[F::ring];                                 // by chunk: whether there is one
+    uint64_t xy_full[F::stages], xy_empty[F::stages], z_full[F::z_stages], z_empty[F::z_stages];
+    uint64_t a_full[2], p_full[2];                        // scores;  P, and z looked over
+    uint64_t conv_full[2], state_full;                    // operands made;  state updated
+    uint64_t r_full[2], r_empty, o_full, o_empty;         // x S, P z;  taken by the outputs' warps
+    uint64_t drain, never;
     uint32_t tmem;
 };
 
-// Tensor memory: state, scores (then P: for each 32 tokens 16 columns of the first parts and 16 of the second), outputs.
-template <int D> struct PassColumns {
-    static constexpr uint32_t state = 0, score = D, out = D + 128, all = D == 64 ? 256 : 512;
-};
-
-template <int D>
-__global__ void __launch_bounds__(Shape<D>::threads, Shape<D>::per_sm)
-    decay_tc_pass_kernel(const __grid_constant__ DecayCall c, const __grid_constant__ DecayPass p,
+template <int D, bool Reverse>
+__global__ void __launch_bounds__(kPassThreads, 1)
+    decay_tc_pass_kernel(const __grid_constant__ DecayCall c, const __grid_constant__ DecayPass p, bool wide,
                          const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my,
                          const __grid_constant__ CUtensorMap mz) {
-    using F = Shape<D>;
-    using C = PassColumns<D>;
+    using F = PassShape<D>;
     extern __shared__ __align__(1024) unsigned char raw[];
-    PassSmem<D>& s = *reinterpret_cast<PassSmem<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    PassSmem<D>& s = *reinterpret_cast<PassSmem<D>*>(raw + to_1024(raw));
     const int h = blockIdx.x, index = blockIdx.y + 65535 * blockIdx.z;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, part = warp >> 2, row = 32 * q + lane;
-    const int block = part >> 1, c0 = (part & 1) * 4, col = 32 * part;      // this thread's 32 of D channels
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, row = 32 * q + lane;
     DecaySegment g;
     if (index >= c.segments || !decay_segment(c, index, g)) return;
     const DecayBase base = decay_base(c.log_decay[h]);
     const float* const enter = decay_entering(c, g, h, p.reverse, p.edge);
     const int chunks = (g.end - g.start + kC - 1) / kC;
-    const bool reverse = p.reverse;
+    constexpr bool reverse = Reverse;
     auto token = [&](int it) { return g.start + (reverse ? chunks - 1 - it : it) * kC; };
-    auto load_xy = [&](int it) {
-        mbar_arrive_expect_tx(&s.full_xy, 2 * F::blocks * kTile);
-        for (int b = 0; b < F::blocks; ++b) {
-            tma_load_3d(s.x[b], &mx, 64 * b, h, token(it), &s.full_xy);
-            tma_load_3d(s.y[b], &my, 64 * b, h, token(it), &s.full_xy);
-        }
-    };
-    auto load_z = [&](int it) {
-        mbar_arrive_expect_tx(&s.full_z, F::blocks * kTile);
-        for (int b = 0; b < F::blocks; ++b) tma_load_3d(s.z[b], &mz, 64 * b, h, token(it), &s.full_z);
-    };
     if (threadIdx.x == 0) {
-        for (uint64_t* b : {&s.full_xy, &s.full_z, &s.mma_a, &s.mma_o, &s.mma_s, &s.mma_f, &s.drain, &s.never}) mbar_init(b, 1);
+        init_all(s.xy_full, F::stages, 1);
+        init_all(s.xy_empty, F::stages, 2);
+        init_all(s.z_full, F::z_stages, 1);
+        init_all(s.z_empty, F::z_stages, 2);
+        init_all(s.a_full, 2, 1);
+        init_all(s.p_full, 2, 8);
+        init_all(s.conv_full, 2, 8);
+        init_all(&s.state_full, 1, 1);
+        init_all(s.r_full, 2, 1);
+        init_all(&s.r_empty, 1, 8);
+        init_all(&s.o_full, 1, 1);
+        init_all(&s.o_empty, 1, 8);
+        init_all(&s.drain, 1, 3);
+        init_all(&s.never, 1, 1);
         fence_mbar_init();
     }
-    if (warp == 0) {
-        tmem_alloc(&s.tmem, C::all);
+    if (warp == 1) {
+        tmem_alloc(&s.tmem, 512);
         tmem_relinquish();
     }
     fill_powers(s.pw, base);
     if (threadIdx.x < 32) s.in_block[threadIdx.x] = decay_power(base, reverse ? threadIdx.x : 31 - threadIdx.x);
+    if (threadIdx.x < 32) s.pw[kC + 4 + threadIdx.x] = c.scale * decay_power(base, threadIdx.x);
+    for (int i = threadIdx.x; i < F::ring * D; i += kPassThreads) s.edge[i / D][i % D] = reverse ? 0 : kC;
+    if (threadIdx.x < F::ring) s.strange[threadIdx.x] = 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = s.tmem, lanes = tmem_addr(tm, 32 * q, 0);
-    int xy_loads = 0, z_loads = 0;            // of thread 0
-    if (threadIdx.x == 0) {
-        load_xy(0);
-        load_z(0);
-        xy_loads = z_loads = 1;
-    }
-    if (enter) {
-        // lanes are the state's rows; D = 64: rows 64 .. 127 hold the sums of the weighted y's second part
-        uint32_t v[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            float f = 0.f;
-            if (row < p.ds && col + j < p.dz)
-                f = enter[p.transposed ? (int64_t)(col + j) * p.ds + row : (int64_t)row * p.dz + col + j];
-            v[j] = __float_as_uint(f);
-        }
-        tmem_st32(lanes + C::state + col, v);
-        tmem_st_wait();
-    }
-    bool has = enter != nullptr, ok = true;   // whether there is a state
-    if (g_force_wait_timeout) ok = mbar_wait(&s.never, 0, 1000000ull);
+    bool ok = true;
+    int xy_loads = 0, z_loads = 0;
 
-    for (int it = 0; it < chunks; ++it) {
-        const int t0 = token(it), n = min(kC, g.end - t0), par = it & 1;
-        const bool last = it + 1 == chunks;
-        ok = ok && mbar_wait(&s.full_xy, par);
-        const bool go = warp == 0 && __all_sync(0xffffffffu, ok);     // this warp issues the products
-        if (go) {
+    if (warp == 0) {
+        // ---- loads
+        if (lane == 0) {
+            for (int it = 0; it < chunks; ++it) {
+                const int st = it % F::stages, sz = it % F::z_stages;
+                if (it >= F::stages) ok = wait(&s.xy_empty[st], (it / F::stages - 1) & 1);
+                if (!ok) break;
+                mbar_arrive_expect_tx(&s.xy_full[st], 2 * F::blocks * kTile);
+                for (int b = 0; b < F::blocks; ++b) {
+                    tma_load_3d(s.x[st][b], &mx, 64 * b, h, token(it), &s.xy_full[st]);
+                    tma_load_3d(s.y[st][b], &my, 64 * b, h, token(it), &s.xy_full[st]);
+                }
+                ++xy_loads;
+                if (it >= F::z_stages) ok = wait(&s.z_empty[sz], (it / F::z_stages - 1) & 1);
+                if (!ok) break;
+                mbar_arrive_expect_tx(&s.z_full[sz], F::blocks * kTile);
+                for (int b = 0; b < F::blocks; ++b) tma_load_3d(s.z[sz][b], &mz, 64 * b, h, token(it), &s.z_full[sz]);
+                ++z_loads;
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---- scores (a buffer ahead or two) and P z
+        auto scores = [&](int it) {
+            const int st = it % F::stages, b = it % F::scores;
+            ok = wait_w(&s.xy_full[st], (it / F::stages) & 1);
+            if (!ok) return;
             tc_fence_after();
             constexpr uint32_t id = idesc_bf16(128, 128, false, false);
-            const uint64_t dx = sdesc_sw128(smem_u32(s.x), 16, 1024), dy = sdesc_sw128(smem_u32(s.y), 16, 1024);
-#pragma unroll
+            const uint64_t dx = sdesc_sw128(smem_u32(s.x[st]), 16, 1024), dy = sdesc_sw128(smem_u32(s.y[st]), 16, 1024);
+#pragma unroll 4
             for (int j = 0; j < D / 16; ++j) {
                 const uint32_t at = (j >> 2) * kTile + 32 * (j & 3);
-                mma_ss_w(tm + C::score, sdesc_add(dx, at), sdesc_add(dy, at), id, j > 0 ? 1u : 0u);
+                mma_ss_w(tm + F::score + 128 * b, sdesc_add(dx, at), sdesc_add(dy, at), id, j > 0 ? 1u : 0u);
             }
-            mma_commit_w(&s.mma_a);
-        }
-        if (has) {
-            // the state as an operand, and decayed over this chunk
-            if (it > 0) ok = ok && mbar_wait(&s.mma_s, (it - 1) & 1);
+            mma_commit_w(&s.a_full[b]);
+        };
+        for (int it = 0; it < min(F::scores, chunks) && ok; ++it) scores(it);
+        for (int it = 0; it < chunks && ok; ++it) {
+            const int b = it % F::scores, sz = it % F::z_stages;
+            ok = wait_w(&s.p_full[b], (it / F::scores) & 1) && wait_w(&s.z_full[sz], (it / F::z_stages) & 1) &&
+                 (it == 0 || wait_w(&s.o_empty, (it - 1) & 1));
+            if (!ok) break;
             tc_fence_after();
-            uint32_t v[32];
-            tmem_ld32(lanes + C::state + col, v);
-            tmem_ld_wait();
-            const bool rest = D == 64 && q >= 2;
-            const int a = rest ? row - 64 : row;
-            unsigned char* const hi = s.state[rest ? (D == 64 ? 2 : 0) : 0][block];
-            unsigned char* const lo = s.state[1][block];
-            const uint64_t keep = f32x2_splat(s.pw[n]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t oh[4], ol[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t& w0 = v[8 * j + 2 * i];
-                    uint32_t& w1 = v[8 * j + 2 * i + 1];
-                    uint64_t f = f32x2_of(w0, w1);
-                    const uint64_t kept = f32x2_mul(f, keep);
-                    w0 = (uint32_t)kept;
-                    w1 = (uint32_t)(kept >> 32);
-                    oh[i] = split(f);
-                    ol[i] = f32x2_to_bf16x2(f);
-                }
-                *reinterpret_cast<uint4*>(hi + sw128_chunk(a, c0 + j)) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
-                if (!rest) *reinterpret_cast<uint4*>(lo + sw128_chunk(a, c0 + j)) = make_uint4(ol[0], ol[1], ol[2], ol[3]);
-            }
-            if (!last) {
-                tmem_st32(lanes + C::state + col, v);
-                tmem_st_wait();
-            }
+            constexpr uint32_t id = idesc_bf16(128, D, false, true);
+            const uint64_t dz = sdesc_sw128(smem_u32(s.z[sz]), kTile, 1024);
+#pragma unroll 4
+            for (int j = 0; j < kC / 16; ++j)
+                mma_ts_w(tm + F::out, tm + F::score + 128 * b + 16 * j, sdesc_add(dz, 2048 * j), id, j > 0 ? 1u : 0u);
+            mma_commit_w(&s.o_full);
+            mma_commit_w(&s.z_empty[sz]);
+            // (the warps that weight y have seen this buffer's scores done, too)
+            if (it + F::scores < chunks) ok = wait_w(&s.conv_full[it & 1], (it >> 1) & 1);
+            if (ok && it + F::scores < chunks) scores(it + F::scores);
         }
-        if (!last) {
-            const float w = row < n ? (reverse ? c.scale * s.pw[row + 1] : s.pw[n - 1 - row]) : 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t at = sw128_chunk(row, c0 + j);
-                const uint4 v = *reinterpret_cast<const uint4*>(s.y[block] + at);
-                const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-                uint32_t oh[4], ol[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint64_t f = f32x2_mul(pair_of(row < n ? in[i] : 0u), f32x2_splat(w));
-                    oh[i] = split(f);
-                    ol[i] = f32x2_to_bf16x2(f);
-                }
-                *reinterpret_cast<uint4*>(s.yw[0][block] + at) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
-                *reinterpret_cast<uint4*>(s.yw[1][block] + at) = make_uint4(ol[0], ol[1], ol[2], ol[3]);
-            }
-        }
-        ok = ok && mbar_wait(&s.full_z, par);
-        const bool found = inspect<F::blocks>(s.z[0], row, part, n);
-        fence_async_smem();
-        tc_fence_before();
-        const bool strange = __syncthreads_or(found);
-        if (go) {
+    } else if (warp == 2) {
+        // ---- the state's update; D = 64: rows 64 .. 127 are whatever lies behind the weighted y, nothing reads them
+        for (int it = 0; it + 1 < chunks && ok; ++it) {
+            const int st = it % F::stages, sz = it % F::z_stages;
+            ok = wait_w(&s.conv_full[it & 1], (it >> 1) & 1) && wait_w(&s.z_full[sz], (it / F::z_stages) & 1);
+            if (!ok) break;
             tc_fence_after();
-            if (has) {
-                constexpr uint32_t id = idesc_bf16(128, D, false, true);
-                const uint64_t dx = sdesc_sw128(smem_u32(s.x), 16, 1024);
-#pragma unroll
-                for (int i = 0; i < (D == 64 ? 3 : 2); ++i) {
-                    const uint64_t dst = sdesc_sw128(smem_u32(s.state[i]), D * 128, 1024);
-#pragma unroll
+            constexpr uint32_t id = idesc_bf16(128, D, true, true);
+            const uint64_t dy = sdesc_sw128(smem_u32(s.y[st]), kTile, 1024), dz = sdesc_sw128(smem_u32(s.z[sz]), kTile, 1024);
+#pragma unroll 4
+            for (int j = 0; j < kC / 16; ++j)
+                mma_ss_w(tm + F::state, sdesc_add(dy, 2048 * j), sdesc_add(dz, 2048 * j), id, it > 0 || enter || j > 0 ? 1u : 0u);
+            mma_commit_w(&s.state_full);
+            mma_commit_w(&s.xy_empty[st]);
+            mma_commit_w(&s.z_empty[sz]);
+        }
+    } else if (warp == 3) {
+        // ---- x S
+        for (int it = 0; it < chunks && ok; ++it) {
+            const int st = it % F::stages;
+            ok = wait_w(&s.conv_full[it & 1], (it >> 1) & 1) && wait_w(&s.xy_full[st], (it / F::stages) & 1) &&
+                 (it == 0 || wait_w(&s.r_empty, (it - 1) & 1));
+            if (!ok) break;
+            if (it > 0 || enter) {
+                tc_fence_after();
+                constexpr uint32_t id = idesc_bf16(128, F::width, false, true);
+                const uint64_t dx = sdesc_sw128(smem_u32(s.x[st]), 16, 1024);
+#pragma unroll 1
+                for (int i = 0; i < (D == 64 ? 1 : 2); ++i) {
+                    const uint64_t ds = sdesc_sw128(smem_u32(s.state[it % F::states][i]), D * 128, 1024);
+#pragma unroll 4
                     for (int j = 0; j < D / 16; ++j)
-                        mma_ss_w(tm + C::out, sdesc_add(dx, (j >> 2) * kTile + 32 * (j & 3)), sdesc_add(dst, 2048 * j), id,
+                        mma_ss_w(tm + F::read, sdesc_add(dx, (j >> 2) * kTile + 32 * (j & 3)), sdesc_add(ds, 2048 * j), id,
                                  i > 0 || j > 0 ? 1u : 0u);
                 }
             }
-            mma_commit_w(&s.mma_o);
-            if (!last) {
-                constexpr uint32_t id = idesc_bf16(128, D, true, true);
-                const uint64_t dz = sdesc_sw128(smem_u32(s.z), kTile, 1024);
-#pragma unroll
-                for (int i = 0; i < (D == 64 ? 1 : 2); ++i) {
-                    const uint64_t dy = sdesc_sw128(smem_u32(s.yw[i]), kTile, 1024);
-#pragma unroll
-                    for (int j = 0; j < kC / 16; ++j)
-                        mma_ss_w(tm + C::state, sdesc_add(dy, 2048 * j), sdesc_add(dz, 2048 * j), id,
-                                 has || i > 0 || j > 0 ? 1u : 0u);
-                }
-                mma_commit_w(&s.mma_s);
-            }
+            mma_commit_w(&s.r_full[it & 1]);
+            mma_commit_w(&s.xy_empty[st]);
         }
-        ok = ok && mbar_wait(&s.mma_a, par);
-        tc_fence_after();
-        // scores to P, 32 tokens at a time
+    } else if (warp >= 4 && warp < 12) {
+        // ---- scores to P, 16 tokens at a time
+        const int half = (warp - 4) >> 2, c0 = half * 4;           // of z: this thread's 32 channels of every 64
+        const uint32_t place = sw128_chunk(row, c0);               // of their first 16 bytes; the j-th: place ^ 16 j
+        if (g_force_wait_timeout) ok = __all_sync(0xffffffffu, mbar_wait(&s.never, 0, 1000000ull));
+        for (int it = 0; it < chunks && ok; ++it) {
+            const int b = it % F::scores, n = min(kC, g.end - token(it)), sz = it % F::z_stages;
+            const uint32_t zpar = (it / F::z_stages) & 1;
+            const bool last = it + 1 == chunks;
+            // before the scores are there: is a value of z not finite?
+            ok = wait_w(&s.z_full[sz], zpar);
+            if (!ok) break;
+            uint32_t top = 0;
 #pragma unroll
-        for (int b = 0; b < 4 / F::parts; ++b) {
-            const int jb = part * (4 / F::parts) + b;
-            uint32_t v[32];
-            if (reverse ? jb < q : jb > q) {
+            for (int k = 0; k < F::blocks; ++k)
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = 0;
-            } else {
-                tmem_ld32(lanes + C::score + 32 * jb, v);
-                tmem_ld_wait();
-                if (jb != q) {
-                    // decay to the block's nearest token, times that inside the block
-                    const uint64_t f = f32x2_splat(c.scale * s.pw[reverse ? 32 * jb - row : row - 32 * jb - 31]);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float4 w = *reinterpret_cast<const float4*>(s.in_block + 4 * j);
-                        const uint64_t a = f32x2_mul(f32x2_mul(f32x2_of(v[4 * j], v[4 * j + 1]), f),
-                                                     f32x2_of(__float_as_uint(w.x), __float_as_uint(w.y)));
-                        const uint64_t d = f32x2_mul(f32x2_mul(f32x2_of(v[4 * j + 2], v[4 * j + 3]), f),
-                                                     f32x2_of(__float_as_uint(w.z), __float_as_uint(w.w)));
-                        v[4 * j] = (uint32_t)a;
-                        v[4 * j + 1] = (uint32_t)(a >> 32);
-                        v[4 * j + 2] = (uint32_t)d;
-                        v[4 * j + 3] = (uint32_t)(d >> 32);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const int apart = reverse ? j - lane : lane - j;
-                        v[j] = apart >= 0 ? __float_as_uint(c.scale * s.pw[max(apart, 0)] * __uint_as_float(v[j])) : 0u;
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(s.z[sz][k] + (place ^ (16 * j)));
+                    if (row < n) top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
+                                                 __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
                 }
-                if (reverse && 32 * jb + 32 > n) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (32 * jb + j >= n) v[j] = 0;
-                }
-                uint32_t o[32];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    uint64_t f = f32x2_of(v[2 * j], v[2 * j + 1]);
-                    o[j] = split(f);
-                    o[16 + j] = f32x2_to_bf16x2(f);
-                }
-#pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = o[j];
+            if (__any_sync(0xffffffffu, (top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u)) {
+                // once the state has taken them, they are set to zero
+                if (!last) ok = wait_w(&s.state_full, it & 1);
+                if (!ok) break;
+                for (int k = 0; k < F::blocks; ++k)
+                    clear_strange(s.z[sz][k], s.edge[it % F::ring] + 64 * k, &s.strange[it % F::ring], row < n ? row : -1, c0, reverse);
+                fence_async_smem();
             }
-            tmem_st32(lanes + C::score + 32 * jb, v);
-        }
-        ok = ok && mbar_wait(&s.mma_o, par);
-        if (has) {
+            ok = wait_w(&s.a_full[b], (it / F::scores) & 1);
+            if (!ok) break;
             tc_fence_after();
-            uint32_t v[32];
-            tmem_ld32(lanes + C::out + col, v);
-            tmem_ld_wait();
-            const float f = reverse ? s.pw[max(n - 1 - row, 0)] : c.scale * s.pw[row + 1];
+            const uint32_t at = lanes + F::score + 128 * b;
+#pragma unroll 1
+            for (int jb = 2 * half; jb < 2 * half + 2; ++jb) {
+                uint32_t o[16];
+                if (reverse ? jb < q : jb > q) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(f * __uint_as_float(v[j]));
-            tmem_st32(lanes + C::out + col, v);
-        }
-        if (threadIdx.x == 0 && ok && !last) {
-            load_xy(it + 1);                  // the scores and x S are done, and every thread is past its y
-            ++xy_loads;
-        }
-        __syncwarp();
-        if (strange) {
-            // the state has taken them (this wait is every thread's); now nothing else may meet them
-            if (!last) ok = ok && mbar_wait(&s.mma_s, par);
-            for (int i = threadIdx.x; i < D; i += F::threads) s.edge[i] = reverse ? -1 : kC;
-            __syncthreads();
+                    for (int j = 0; j < 16; ++j) o[j] = 0;
+                } else {
+                    uint32_t v[32];
+                    tmem_ld32(at + 32 * jb, v);
+                    tmem_ld_wait();
+                    arrived(v);
+                    if (jb != q) {
+                        // decay to the block's nearest token, times that inside the block
+                        const uint64_t f = f32x2_splat(c.scale * s.pw[reverse ? 32 * jb - row : row - 32 * jb - 31]);
+                        const float4* const in = reinterpret_cast<const float4*>(s.in_block);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint16_t* at = reinterpret_cast<uint16_t*>(s.z[block] + sw128_chunk(row, c0 + j));
-                for (int i = 0; i < 8; ++i) {
-                    if ((at[i] & 0x7f80u) != 0x7f80u) continue;
-                    at[i] = 0;
-                    if (reverse) atomicMax(&s.edge[col + 8 * j + i], row);
-                    else atomicMin(&s.edge[col + 8 * j + i], row);
+                        for (int j = 0; j < 8; ++j) {
+                            const float4 w = in[j];
+                            o[2 * j] = f32x2_to_bf16x2(f32x2_mul(f32x2_mul(f32x2_of(v[4 * j], v[4 * j + 1]), f),
+                                                                 f32x2_of(__float_as_uint(w.x), __float_as_uint(w.y))));
+                            o[2 * j + 1] = f32x2_to_bf16x2(f32x2_mul(f32x2_mul(f32x2_of(v[4 * j + 2], v[4 * j + 3]), f),
+                                                                     f32x2_of(__float_as_uint(w.z), __float_as_uint(w.w))));
+                        }
+                    } else {
+                        const float* const w = s.pw + kC + 4 + (reverse ? -lane : lane);   // (masked ones lie in front)
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            const float e0 = w[reverse ? j : -j] * __uint_as_float(v[j]);
+                            const float e1 = w[reverse ? j + 1 : -j - 1] * __uint_as_float(v[j + 1]);
+                            o[j / 2] = pack_bf16x2((reverse ? j >= lane : j <= lane) ? e0 : 0.f,
+                                                   (reverse ? j + 1 >= lane : j + 1 <= lane) ? e1 : 0.f);
+                        }
+                    }
+                    if (reverse && 32 * jb + 32 > n) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const int left = n - 32 * jb - 2 * j;       // of this pair and on, tokens that there are
+                            o[j] &= left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
+                        }
+                    }
                 }
+                const uint32_t (&lo)[8] = *reinterpret_cast<const uint32_t (*)[8]>(o);
+                const uint32_t (&hi)[8] = *reinterpret_cast<const uint32_t (*)[8]>(o + 8);
+                tmem_st8(at + 32 * jb, lo);
+                tmem_st8(at + 32 * jb + 16, hi);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            arrive_w(&s.p_full[b]);
+        }
+    } else if (warp >= 12 && warp < 20) {
+        // ---- weighted y, the state as an operand, a look at z
+        const int part = (warp - 12) >> 2;                         // this thread's 32 channels of every 64
+        const uint32_t place = sw128_chunk(row, 4 * part);         // of their first 16 bytes; the j-th: place ^ 16 j
+        const bool rows = D == 128 || q < 2;                       // tensor memory lanes that are rows of the state
+        if (enter && rows) {
+#pragma unroll 1
+            for (int k = 0; k < F::blocks; ++k) {
+                const int col = 64 * k + 32 * part;
+                uint32_t v[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    float f = 0.f;
+                    if (row < p.ds && col + j < p.dz)
+                        f = enter[p.transposed ? (int64_t)(col + j) * p.ds + row : (int64_t)row * p.dz + col + j];
+                    v[j] = __float_as_uint(f);
+                }
+                tmem_st32(lanes + F::state + col, v);
+            }
+            tmem_st_wait();
+        }
+        for (int it = 0; it < chunks && ok; ++it) {
+            const int st = it % F::stages, sz = it % F::z_stages, n = min(kC, g.end - token(it));
+            const uint32_t zpar = (it / F::z_stages) & 1;
+            const bool last = it + 1 == chunks, has = it > 0 || enter;
+            if (!last) {
+                // the scores have read y
+                ok = wait_w(&s.a_full[it % F::scores], (it / F::scores) & 1);
+                if (!ok) break;
+                const uint64_t w = f32x2_splat(row < n ? (reverse ? c.scale * s.pw[row + 1] : s.pw[n - 1 - row]) : 0.f);
+#pragma unroll
+                for (int k = 0; k < F::blocks; ++k) {
+                    uint32_t v[4][4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint4 in = *reinterpret_cast<const uint4*>(s.y[st][k] + (place ^ (16 * j)));
+                        v[j][0] = in.x; v[j][1] = in.y; v[j][2] = in.z; v[j][3] = in.w;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[j][i] = row < n ? f32x2_to_bf16x2(f32x2_mul(pair_of(v[j][i]), w)) : 0u;
+                        *reinterpret_cast<uint4*>(s.y[st][k] + (place ^ (16 * j))) =
+                            make_uint4(v[j][0], v[j][1], v[j][2], v[j][3]);
+                    }
+                }
+            }
+            if (n < kC) {
+                // nothing from another sequence
+                ok = wait_w(&s.z_full[sz], zpar);
+                if (!ok) break;
+                if (row >= n)
+                    for (int k = 0; k < F::blocks; ++k)
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<uint4*>(s.z[sz][k] + (place ^ (16 * j))) = make_uint4(0, 0, 0, 0);
+            }
+            // the state is there, and the operand that its buffer held has been read
+            if (it >= F::states) {
+                const int then = it - F::states;
+                ok = wait_w(&s.r_full[then & 1], (then >> 1) & 1);
+            }
+            if (ok && it > 0) ok = wait_w(&s.state_full, (it - 1) & 1);
+            if (!ok) break;
+            if (has && rows) {
+                tc_fence_after();
+                const uint64_t keep = f32x2_splat(s.pw[n]);
+#pragma unroll 1
+                for (int k = 0; k < F::blocks; ++k) {
+                    const uint32_t at = lanes + F::state + 64 * k + 32 * part;
+                    uint32_t v[32];
+                    tmem_ld32(at, v);
+                    tmem_ld_wait();
+                    arrived(v);
+                    unsigned char* const hi = s.state[it % F::states][0][k];
+                    unsigned char* const lo = s.state[it % F::states][1][k];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t oh[4], ol[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t& w0 = v[8 * j + 2 * i];
+                            uint32_t& w1 = v[8 * j + 2 * i + 1];
+                            uint64_t f = f32x2_of(w0, w1);
+                            const uint64_t kept = f32x2_mul(f, keep);
+                            w0 = (uint32_t)kept;
+                            w1 = (uint32_t)(kept >> 32);
+                            oh[i] = split(f);
+                            ol[i] = f32x2_to_bf16x2(f);
+                        }
+                        *reinterpret_cast<uint4*>(hi + (place ^ (16 * j))) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
+                        *reinterpret_cast<uint4*>(lo + (place ^ (16 * j))) = make_uint4(ol[0], ol[1], ol[2], ol[3]);
+                    }
+                    if (!last) tmem_st32(at, v);
+                }
+                tmem_st_wait();
             }
             fence_async_smem();
+            tc_fence_before();
+            arrive_w(&s.conv_full[it & 1]);
         }
-        tmem_st_wait();
-        tc_fence_before();
-        if (__syncthreads_or(!ok)) break;
-        __syncwarp();
-        if (warp == 0) {
+    } else if (warp >= 20) {
+        // ---- outputs: this thread's 32 channels of every 64
+        const int part = (warp - 20) >> 2;
+        for (int it = 0; it < chunks && ok; ++it) {
+            const int t0 = token(it), n = min(kC, g.end - t0);
+            const bool has = it > 0 || enter;
+            ok = wait_w(&s.r_full[it & 1], (it >> 1) & 1);
+            if (!ok) break;
+            const uint64_t f = f32x2_splat(reverse ? s.pw[max(n - 1 - row, 0)] : c.scale * s.pw[row + 1]);
+            __nv_bfloat16* const to = static_cast<__nv_bfloat16*>(p.out) + ((int64_t)(t0 + row) * c.H + h) * p.dz + 32 * part;
+            // what the state adds, while P z runs
+            uint64_t held[16];
+            auto take = [&](int k) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t r[16], t[16];
+                    tmem_ld16(lanes + F::read + 64 * k + 32 * part + 16 * u, r);
+                    if (D == 64) tmem_ld16(lanes + F::read + 64 + 32 * part + 16 * u, t);
+                    tmem_ld_wait();
+                    arrived(r);
+                    if (D == 64) arrived(t);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        uint64_t a = f32x2_of(r[2 * j], r[2 * j + 1]);
+                        if (D == 64) a = f32x2_add(a, f32x2_of(t[2 * j], t[2 * j + 1]));
+                        held[8 * u + j] = f32x2_mul(a, f);
+                    }
+                }
+            };
+            if (has) {
+                tc_fence_after();
+                take(0);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) held[j] = 0;
+            }
+            if (D == 64) {
+                tc_fence_before();
+                arrive_w(&s.r_empty);
+            }
+            ok = wait_w(&s.o_full, it & 1);
+            if (!ok) break;
             tc_fence_after();
-            constexpr uint32_t id = idesc_bf16(128, D, false, true);
-            const uint64_t dz = sdesc_sw128(smem_u32(s.z), kTile, 1024);
+            const bool strange = *reinterpret_cast<volatile int*>(&s.strange[it % F::ring]);
+#pragma unroll 1
+            for (int k = 0; k < F::blocks; ++k) {
+                if (k > 0 && has) take(k);
+                if (k > 0 && !has) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+                    for (int j = 0; j < 16; ++j) held[j] = 0;
+                }
+                uint32_t o[16];
 #pragma unroll
-                for (int j = 0; j < kC / 16; ++j)
-                    mma_ts_w(tm + C::out, tm + C::score + 32 * (j >> 1) + 16 * i + 8 * (j & 1), sdesc_add(dz, 2048 * j), id,
-                             has || i > 0 || j > 0 ? 1u : 0u);
-            mma_commit_w(&s.mma_f);
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t v[16];
+                    tmem_ld16(lanes + F::out + 64 * k + 32 * part + 16 * u, v);
+                    tmem_ld_wait();
+                    arrived(v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        o[8 * u + j] = f32x2_to_bf16x2(f32x2_add(held[8 * u + j], f32x2_of(v[2 * j], v[2 * j + 1])));
+                }
+                if (strange) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        o[j] = mark_strange(o[j], s.edge[it % F::ring] + 64 * k + 32 * part + 2 * j, row, reverse);
+                }
+                if (k + 1 == F::blocks) {
+                    tc_fence_before();
+                    if (strange) {
+                        named_sync(1, 256);
+                        for (int i = threadIdx.x - 640; i < D; i += 256) s.edge[it % F::ring][i] = reverse ? 0 : kC;
+                        if (threadIdx.x == 640) s.strange[it % F::ring] = 0;
+                        named_sync(1, 256);
+                    }
+                    if (D != 64) arrive_w(&s.r_empty);
+                    arrive_w(&s.o_empty);
+                }
+                if (row < n) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int at = 64 * k + 16 * u;
+                        if (wide) {
+                            const uint32_t (&w)[8] = *reinterpret_cast<const uint32_t (*)[8]>(o + 8 * u);
+                            if (at + 32 * part < p.dz) store_32(to + at, w);
+                        } else {
+                            if (at + 32 * part < p.dz)
+                                *reinterpret_cast<uint4*>(to + at) = make_uint4(o[8 * u], o[8 * u + 1], o[8 * u + 2], o[8 * u + 3]);
+                            if (at + 32 * part + 8 < p.dz)
+                                *reinterpret_cast<uint4*>(to + at + 8) =
+                                    make_uint4(o[8 * u + 4], o[8 * u + 5], o[8 * u + 6], o[8 * u + 7]);
+                        }
+                    }
+                }
+            }
         }
-        has = true;
-        ok = ok && mbar_wait(&s.mma_f, par);
-        tc_fence_after();
-        if (threadIdx.x == 0 && ok && !last) {
-            load_z(it + 1);
-            ++z_loads;
-        }
-        __syncwarp();
-        uint32_t v[32];
-        tmem_ld32(lanes + C::out + col, v);
-        tmem_ld_wait();
-        if (strange) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (reverse ? row <= s.edge[col + j] : row >= s.edge[col + j]) v[j] = 0x7fc00000u;
-        }
-        // a warp's 32 rows of 32 channels by way of shared memory (where it alone puts its weighted y), 64 bytes a row
-        unsigned char* const stage = s.yw[0][block];
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                o[i] = pack_bf16x2(__uint_as_float(v[8 * j + 2 * i]), __uint_as_float(v[8 * j + 2 * i + 1]));
-            *reinterpret_cast<uint4*>(stage + sw128_chunk(row, c0 + j)) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = 32 * q + 8 * j + (lane >> 2), at = col + 8 * (lane & 3);
-            const uint4 o = *reinterpret_cast<const uint4*>(stage + sw128_chunk(r, c0 + (lane & 3)));
-            if (r < n && at < p.dz && ok)
-                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + ((int64_t)(t0 + r) * c.H + h) * p.dz + at) = o;
-        }
-        __syncwarp();
     }
     if (__syncthreads_or(!ok)) {
         // copies and products on their way end before the block does
         if (threadIdx.x == 0) {
             record_error(c.hdr, LA_DEVERR_WAIT_TIMEOUT);
-            if (xy_loads) mbar_wait(&s.full_xy, (xy_loads - 1) & 1, kDrainNs);
-            if (z_loads) mbar_wait(&s.full_z, (z_loads - 1) & 1, kDrainNs);
+            for (int i = max(0, xy_loads - F::stages); i < xy_loads; ++i)
+                mbar_wait(&s.xy_full[i % F::stages], (i / F::stages) & 1, kDrainNs);
+            for (int i = max(0, z_loads - F::z_stages); i < z_loads; ++i)
+                mbar_wait(&s.z_full[i % F::z_stages], (i / F::z_stages) & 1, kDrainNs);
         }
-        __syncwarp();
-        if (warp == 0) {
+        if (warp >= 1 && warp <= 3) {
             mma_commit_w(&s.drain);
             mbar_wait(&s.drain, 0, kDrainNs);
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) tmem_dealloc(tm, C::all);
+    if (warp == 1) tmem_dealloc(tm, 512);
 }
 
 // ---------------------------------------------------------------------------
@@ -644,9 +855,10 @@ cudaError_t states(const DecayCall& c, const DecayStates& p, bool final, cudaStr
     CUtensorMap my{}, mz{};
     if (c.T > 0 && (!rows_map(&my, p.y, c, c.dk) || !rows_map(&mz, p.z, c, c.dv))) return cudaErrorInvalidValue;
     constexpr size_t smem = sizeof(StatesSmem<D>) + 1024;
+    static_assert(smem <= 227 * 1024, "shared memory");
     const cudaError_t e = opt_in(decay_tc_states_kernel<D>, smem);
     if (e != cudaSuccess) return e;
-    decay_tc_states_kernel<D><<<grid_of(c.H, final ? c.nseq : c.segments), Shape<D>::threads, smem, s>>>(c, p, final, my, mz);
+    decay_tc_states_kernel<D><<<grid_of(c.H, final ? c.nseq : c.segments), kStatesThreads, smem, s>>>(c, p, final, my, mz);
     return cudaGetLastError();
 }
 
@@ -656,9 +868,12 @@ cudaError_t pass(const DecayCall& c, const DecayPass& p, cudaStream_t s) {
     if (!rows_map(&mx, p.x, c, p.ds) || !rows_map(&my, p.y, c, p.ds) || !rows_map(&mz, p.z, c, p.dz)) return cudaErrorInvalidValue;
     constexpr size_t smem = sizeof(PassSmem<D>) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory");
-    const cudaError_t e = opt_in(decay_tc_pass_kernel<D>, smem);
+    auto kernel = p.reverse ? decay_tc_pass_kernel<D, true> : decay_tc_pass_kernel<D, false>;
+    const cudaError_t e = opt_in(kernel, smem);
     if (e != cudaSuccess) return e;
-    decay_tc_pass_kernel<D><<<grid_of(c.H, c.segments), Shape<D>::threads, smem, s>>>(c, p, mx, my, mz);
+    // 32-byte stores of 16 channels where every row allows them
+    const bool wide = p.dz % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
+    kernel<<<grid_of(c.H, c.segments), kPassThreads, smem, s>>>(c, p, wide, mx, my, mz);
     return cudaGetLastError();
 }
 

@@ -13,14 +13,16 @@ An output sums d_k products of q with the state (d_k + 4 roundings of scale |q|^
 The scores' form q.k first (d_k roundings), then weights (8 u) and sums over a chunk's tokens (at most 2 u
 a token: counted in E), is covered by the same.
 
-bf16 operands on the tensor cores: scores and states go in as a bf16 and the bf16 of what it leaves, off
-by (2^-9)^2 = 2^-18 together, weighted keys likewise: three such factors at most in one term, 2^-16 M.
+bf16 operands on the tensor cores: decayed scores, and weighted keys (queries) on their way into a state that
+stays in one call, are rounded to bf16, off by 2^-8; a state goes in as a bf16 and the bf16 of what it leaves,
+off by 2^-16: 2^-8 + 2^-16 + 2^-24 of M at most.  States that a call returns are sums of three such parts, 2^-24:
+counted above.
 """
 import numpy as np
 
 from layer_ops_util import HALF, U, check  # noqa: F401
 
-PARTS = {"f32": 0.0, "bf16": 2.0 ** -16}
+PARTS = {"f32": 0.0, "bf16": 2.0 ** -8 + 2.0 ** -15}
 
 
 def forward_bounds(q, k, v, log_decay, scale, spans, state, dtype):

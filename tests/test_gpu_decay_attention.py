@@ -105,12 +105,29 @@ def test_widths(la, dk, dv, dtype):
     _check_backward(la, c, True)
 
 
-@pytest.mark.parametrize("dtype,H,d", [("f32", 70, 24), ("bf16", 70, 24), ("bf16", 48, 64), ("bf16", 33, 128)])
-def test_segments_of_several_chunks(la, dtype, H, d):
+@pytest.mark.parametrize("dtype,H,dk,dv", [("f32", 70, 24, 24), ("bf16", 70, 24, 24), ("bf16", 48, 64, 64), ("bf16", 33, 128, 128),
+                                           ("bf16", 400, 16, 8), ("bf16", 300, 8, 72)])
+def test_segments_of_several_chunks(la, dtype, H, dk, dv):
     """Enough tokens that a segment has several chunks, in the sequences' middle and at their ends."""
-    c = _case([1500, 3, 901], H, d, d, dtype, seed=3)
+    c = _case([1500, 3, 901], H, dk, dv, dtype, seed=3)
     _check_forward(la, c, True)
     _check_backward(la, c, True)
+
+
+@pytest.mark.parametrize("dk,dv", [(16, 16), (8, 72)])
+def test_one_segment_of_many_chunks(la, dk, dv):
+    """Each of so many heads is one segment: no state between segments, 30 chunks after one another."""
+    c = _case([3800], 200, dk, dv, "bf16", seed=23)
+    q, k, v, do, ld = (_np(c[x]) for x in ("q", "k", "v", "do", "ld"))
+    out, new = _forward(la, c, False, nseq=1, return_state=True)
+    ref, ref_new = ops.decay_attention(q, k, v, ld, c["scale"], c["cu"])
+    b_out, b_new = forward_bounds(q, k, v, ld, c["scale"], c["spans"], None, "bf16")
+    check(_np(out), ref, b_out, "bf16", "out")
+    check(_np(new), ref_new, b_new, "f32", "state_out")
+    got = _backward(la, c, False, nseq=1)
+    refs = ops.decay_attention_backward(q, k, v, do, ld, c["scale"], c["cu"])
+    for x, y, b in zip(got, refs, backward_bounds(q, k, v, do, ld, c["scale"], c["spans"], None, None, "bf16")):
+        check(_np(x), y, b, "bf16")
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -325,22 +342,21 @@ def test_two_streams_at_once(la):
 
 @pytest.mark.parametrize("d", [64, 128])
 def test_a_wait_that_runs_out_is_reported(la, d):
-    c = _case([500, 300], 2, d, d, "bf16", seed=22)
-    want = _forward(la, c, True) + _backward(la, c, True)
-    ws = torch.empty(la.la_decay_attention_backward_workspace_bytes(torch.bfloat16, True, 2, 800, 2, d, d), dtype=torch.uint8,
+    """(The state sums' kernel and the products', one launch each: every role's own wait takes two seconds.)"""
+    c = _case([500, 100], 2, d, d, "bf16", seed=22)
+    kw = dict(cu_seqlens=c["cu_t"])
+    want = _forward(la, c, True, **kw)
+    ws = torch.empty(la.la_decay_attention_workspace_bytes(torch.bfloat16, True, 2, 600, 2, d, d), dtype=torch.uint8,
                      device="cuda")
     la.la_test_force_wait_timeout(True)
     try:
-        _forward(la, c, True, cu_seqlens=c["cu_t"], return_state=True, workspace=ws)
-        assert la.la_workspace_error(ws) == 2
-        _backward(la, c, True, cu_seqlens=c["cu_t"], return_dstate=True, workspace=ws)
+        _forward(la, c, True, workspace=ws, **kw)
         assert la.la_workspace_error(ws) == 2
     finally:
         la.la_test_force_wait_timeout(False)
-    got = (_forward(la, c, True, cu_seqlens=c["cu_t"], return_state=True, workspace=ws)
-           + _backward(la, c, True, cu_seqlens=c["cu_t"], return_dstate=True, workspace=ws))
+    got = _forward(la, c, True, workspace=ws, **kw)
     assert la.la_workspace_error(ws) == 0
-    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert torch.equal(got, want)
 
 
 def test_no_tokens(la):
