@@ -108,25 +108,31 @@ constexpr int kJoinAhead = 8;      // segments whose loads are on their way toge
 
 template <int N>
 __global__ void __launch_bounds__(kJoinThreads) decay_join_kernel(const __grid_constant__ DecayCall c,
-                                                                  const __grid_constant__ DecayStates p) {
+                                                                  const __grid_constant__ DecayStates p, bool ends) {
     using V = Vec<float, N>;
     if (decay_malformed(c)) return;
     const int s = blockIdx.x, h = blockIdx.y, n = c.dk * c.dv;
     const int e = (blockIdx.z * kJoinThreads + threadIdx.x) * N;
-    DecaySegment last, first;
-    if (!decay_edge_segment(c, s, false, last) || decay_first(last)) return;      // no boundary inside
-    decay_edge_segment(c, s, true, first);
     if (e >= n) return;
+    const int64_t edge = ((int64_t)s * c.H + h) * n + e;
+    V acc;
+#pragma unroll
+    for (int k = 0; k < N; ++k) acc.v[k] = 0.f;
+    if (p.edge_in) acc = *reinterpret_cast<const V*>(p.edge_in + edge);
+    DecaySegment last, first;
+    if (!decay_edge_segment(c, s, false, last)) {
+        // an empty sequence: what enters it leaves it
+        if (ends) *reinterpret_cast<V*>(p.edge_out + edge) = acc;
+        return;
+    }
+    if (decay_first(last) && !ends) return;                                       // no boundary inside
+    decay_edge_segment(c, s, true, first);
     const int m = decay_slot(last) - decay_slot(first);                           // boundaries
     const DecayBase base = decay_base(c.log_decay[h]);
     const float whole = decay_power(base, c.L);
     float factor = p.reverse ? decay_power(base, last.end - last.start) : whole;
     const int64_t step = (int64_t)c.H * n;
     float* const own = c.states[p.reverse] + ((int64_t)decay_slot(first) * c.H + h) * n + e;
-    V acc;
-#pragma unroll
-    for (int k = 0; k < N; ++k) acc.v[k] = 0.f;
-    if (p.edge_in) acc = *reinterpret_cast<const V*>(p.edge_in + ((int64_t)s * c.H + h) * n + e);
     for (int i0 = 0; i0 < m; i0 += kJoinAhead) {
         V part[kJoinAhead];
 #pragma unroll
@@ -141,6 +147,16 @@ __global__ void __launch_bounds__(kJoinThreads) decay_join_kernel(const __grid_c
             factor = whole;
         }
     }
+    if (!ends) return;
+    // the segment at the other end: its own sum, and what enters it where something does
+    const DecaySegment& end = p.reverse ? first : last;
+    const float keep = decay_power(base, end.end - end.start);
+    V own_sum = *reinterpret_cast<const V*>(p.edge_out + edge);
+    if (m > 0 || p.edge_in) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) own_sum.v[k] = fmaf(keep, acc.v[k], own_sum.v[k]);
+    }
+    *reinterpret_cast<V*>(p.edge_out + edge) = own_sum;
 }
 
 // ---------------------------------------------------------------------------
@@ -175,7 +191,7 @@ __device__ __forceinline__ void store8(float* to, const float (&f)[8]) {
 // Sums of one segment (or, final, what leaves each sequence): blocks of 64 x 64 of [dk][dv], 4 x 4 a thread.
 template <typename T>
 __global__ void __launch_bounds__(kSimtThreads) decay_states_kernel(const __grid_constant__ DecayCall c,
-                                                                    const __grid_constant__ DecayStates p, bool final,
+                                                                    const __grid_constant__ DecayStates p, DecayWhich which,
                                                                     bool vec) {
     __shared__ __align__(16) float ys[kRows][kCols], zs[kRows][kCols];
     const int h = blockIdx.y, nb = (c.dv + kCols - 1) / kCols;
@@ -183,8 +199,10 @@ __global__ void __launch_bounds__(kSimtThreads) decay_states_kernel(const __grid
     DecaySegment g;
     bool any = true;
     if (decay_malformed(c)) return;
-    if (final) any = decay_edge_segment(c, blockIdx.x, p.reverse, g);
-    else if (!decay_segment(c, blockIdx.x, g) || (p.reverse ? decay_first(g) : decay_last(g))) return;
+    if (which == kEnds) any = decay_edge_segment(c, blockIdx.x, p.reverse, g);
+    else if (!decay_segment(c, blockIdx.x, g)) return;
+    const bool end = which == kEnds || (p.reverse ? decay_first(g) : decay_last(g));
+    if (end && which == kInner) return;
     const DecayBase base = decay_base(c.log_decay[h]);
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16, row = threadIdx.x / 8, col = threadIdx.x % 8 * 8;
     float acc[4][4];
@@ -224,13 +242,10 @@ __global__ void __launch_bounds__(kSimtThreads) decay_states_kernel(const __grid
     const int64_t n = (int64_t)c.dk * c.dv;
     const float* enter = nullptr;
     float* to;
-    if (final) {
-        enter = any ? decay_entering(c, g, h, p.reverse, p.edge_in)
-                    : p.edge_in ? p.edge_in + ((int64_t)blockIdx.x * c.H + h) * n : nullptr;
-        to = p.edge_out + ((int64_t)blockIdx.x * c.H + h) * n;
-    } else {
-        to = c.states[p.reverse] + ((int64_t)(decay_slot(g) - (p.reverse ? 1 : 0)) * c.H + h) * n;
-    }
+    if (which == kEnds) enter = any ? decay_entering(c, g, h, p.reverse, p.edge_in)
+                                    : p.edge_in ? p.edge_in + ((int64_t)blockIdx.x * c.H + h) * n : nullptr;
+    if (end) to = p.edge_out + ((int64_t)(which == kEnds ? (int)blockIdx.x : g.seq) * c.H + h) * n;
+    else to = c.states[p.reverse] + ((int64_t)(decay_slot(g) - (p.reverse ? 1 : 0)) * c.H + h) * n;
     const float keep = any ? decay_power(base, g.end - g.start) : 1.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -535,29 +550,36 @@ cudaError_t plan(const DecayCall& c, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-cudaError_t join(const DecayCall& c, const DecayStates& p, cudaStream_t s) {
+cudaError_t join(const DecayCall& c, const DecayStates& p, bool ends, cudaStream_t s) {
     const int n = c.dk * c.dv;
-    const bool vec = n % 4 == 0 && reinterpret_cast<uintptr_t>(p.edge_in) % 16 == 0;
+    const bool vec = n % 4 == 0 && on_16_bytes({p.edge_in, ends ? p.edge_out : nullptr});
     const dim3 grid(c.nseq, c.H, (unsigned)ceil_div(n, kJoinThreads * (vec ? 4 : 1)));
-    if (vec) decay_join_kernel<4><<<grid, kJoinThreads, 0, s>>>(c, p);
-    else decay_join_kernel<1><<<grid, kJoinThreads, 0, s>>>(c, p);
+    if (vec) decay_join_kernel<4><<<grid, kJoinThreads, 0, s>>>(c, p, ends);
+    else decay_join_kernel<1><<<grid, kJoinThreads, 0, s>>>(c, p, ends);
     return cudaGetLastError();
 }
 
-cudaError_t states(const DecayCall& c, const DecayStates& p, int dtype, bool final, cudaStream_t s) {
-    if (decay_tc_fits(c, dtype) && on_16_bytes({p.y, p.z})) return decay_tc_states(c, p, final, s);
-    const dim3 grid(final ? c.nseq : c.segments, c.H, (unsigned)(ceil_div(c.dk, kCols) * ceil_div(c.dv, kCols)));
+cudaError_t states(const DecayCall& c, const DecayStates& p, int dtype, DecayWhich which, cudaStream_t s) {
+    if (decay_tc_fits(c, dtype) && on_16_bytes({p.y, p.z})) return decay_tc_states(c, p, which, s);
+    const dim3 grid(which == kEnds ? c.nseq : c.segments, c.H, (unsigned)(ceil_div(c.dk, kCols) * ceil_div(c.dv, kCols)));
     const bool vec = vector_rows(c, dtype, {p.y, p.z});
-    if (dtype == LA_F32) decay_states_kernel<float><<<grid, kSimtThreads, 0, s>>>(c, p, final, vec);
-    else decay_states_kernel<__nv_bfloat16><<<grid, kSimtThreads, 0, s>>>(c, p, final, vec);
+    if (dtype == LA_F32) decay_states_kernel<float><<<grid, kSimtThreads, 0, s>>>(c, p, which, vec);
+    else decay_states_kernel<__nv_bfloat16><<<grid, kSimtThreads, 0, s>>>(c, p, which, vec);
     return cudaGetLastError();
 }
 
-// What enters every segment (nothing to do where every sequence is one segment).
+// What enters every segment, and what leaves every sequence unless that overwrites what enters it (nothing to do where
+// every sequence is one segment and nothing is to leave).
 cudaError_t enter(const DecayCall& c, const DecayStates& p, int dtype, cudaStream_t s) {
-    if (c.slots == 0) return cudaSuccess;
-    const cudaError_t e = states(c, p, dtype, false, s);
-    return e != cudaSuccess ? e : join(c, p, s);
+    const bool ends = p.edge_out && p.edge_out != p.edge_in;
+    if (c.slots == 0 && !ends) return cudaSuccess;
+    cudaError_t e = cudaSuccess;
+    if (c.T > 0) e = states(c, p, dtype, ends ? kAll : kInner, s);
+    return e != cudaSuccess ? e : join(c, p, ends, s);
+}
+// What leaves every sequence, where that takes the place of what enters it: once nothing reads it any more.
+cudaError_t leave(const DecayCall& c, const DecayStates& p, int dtype, cudaStream_t s) {
+    return p.edge_out && p.edge_out == p.edge_in ? states(c, p, dtype, kEnds, s) : cudaSuccess;
 }
 
 cudaError_t pass(const DecayCall& c, const DecayPass& p, int dtype, cudaStream_t s) {
@@ -609,8 +631,7 @@ cudaError_t decay_forward(const DecayCall& c, const void* q, const void* k, cons
     cudaError_t e = plan(c, s);
     if (e == cudaSuccess) e = enter(c, sums, dtype, s);
     if (e == cudaSuccess) e = pass(c, p, dtype, s);
-    // last: state_out may be state_in
-    if (e == cudaSuccess && state_out) e = states(c, sums, dtype, true, s);
+    if (e == cudaSuccess) e = leave(c, sums, dtype, s);
     return e;
 }
 
@@ -626,8 +647,7 @@ cudaError_t decay_backward(const DecayCall& c, const void* q, const void* k, con
     if (e == cudaSuccess) e = enter(c, back, dtype, s);
     if (e == cudaSuccess) e = pass(c, pk, dtype, s);
     if (e == cudaSuccess) e = pass(c, pv, dtype, s);
-    // last: dstate_in may be dstate_out
-    if (e == cudaSuccess && dstate_in) e = states(c, back, dtype, true, s);
+    if (e == cudaSuccess) e = leave(c, back, dtype, s);
     return e;
 }
 

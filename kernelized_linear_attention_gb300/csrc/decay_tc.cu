@@ -86,6 +86,14 @@ __device__ inline void move_edge(unsigned short* edge, int row, bool reverse) {
     }
 }
 
+// Waits, like mbar_wait, until a count in shared memory has got to `least`.
+__device__ __noinline__ bool wait_count(const int* count, int least) {
+    const uint64_t began = globaltimer_ns();
+    while (*reinterpret_cast<const volatile int*>(count) < least)
+        if (globaltimer_ns() - began > 2000000000ull) return false;
+    __threadfence_block();
+    return true;
+}
 // Sets a row's values that are not finite to zero in four of its 16-byte chunks (row -1: nothing).
 __device__ __noinline__ void clear_strange(unsigned char* tile, unsigned short* edge, int* strange, int row, int c0, bool reverse) {
     if (row < 0) return;
@@ -114,27 +122,26 @@ __device__ __forceinline__ void store_32(void* to, const uint32_t (&v)[8]) {
 // ---------------------------------------------------------------------------
 // State sums of a segment
 // ---------------------------------------------------------------------------
-// Warp 0 loads, warp 1 issues the products, 16 warps weight y (D = 64: eight for the even chunks and eight for the odd
-// ones).  The tensor cores truncate when they accumulate: after kFlush chunks the sums go on in fp32 registers, rounded
-// to nearest.
+// Warp 0 loads, warp 1 issues the products, two groups of eight warps weight y, one the even tiles and one the odd ones.
+// The tensor cores truncate when they accumulate: after 64 steps (1024 tokens) the sums go on in fp32 registers, rounded
+// to nearest.  (Two parts of the weighted y instead of three, which outputs alone would not notice: 57 us instead of 60.)
 constexpr int kStatesThreads = 640;
-constexpr int kFlush = 8;
 template <int D> struct StatesShape {
     static constexpr int blocks = D / 64;                 // of 64 channels
-    static constexpr int stages = D == 64 ? 4 : 2;        // of y and z
-    static constexpr int buffers = D == 64 ? 2 : 1;       // of weighted y
-    static constexpr int warps = D == 64 ? 8 : 16;        // that weight one chunk
-    static constexpr int sums = D == 64 ? 2 : 1;          // accumulators, of `columns` each
-    static constexpr int columns = D == 64 ? 128 : 384;
-    static constexpr int tmem = D == 64 ? 256 : 512;
+    static constexpr int rows = D == 64 ? 128 : 64;       // tokens of a tile
+    static constexpr int flush = 1024 / rows;             // tiles
+    static constexpr int warps = D == 64 ? 8 : 16;        // that have the sums
+    static constexpr int columns = D == 64 ? 128 : 256;   // of tensor memory a set of sums, of two
+    static constexpr int stages = 4;                      // of y and z
+    static constexpr uint32_t tile = rows * 128;          // bytes of a block
 };
 template <int D> struct __align__(1024) StatesSmem {
     using F = StatesShape<D>;
-    unsigned char yw[F::buffers][3][F::blocks][kTile];    // weighted y in three parts
-    unsigned char y[F::stages][F::blocks][kTile], z[F::stages][F::blocks][kTile];
+    unsigned char yw[2][3][F::blocks][F::tile];           // weighted y in three parts, two tiles
+    unsigned char y[F::stages][F::blocks][F::tile], z[F::stages][F::blocks][F::tile];
     float pw[kC + 4];
     uint64_t full[F::stages], empty[F::stages];           // TMA -> weighting, products;  both -> TMA
-    uint64_t yw_full[F::buffers], yw_empty[F::buffers];   // weighting -> products;  products -> weighting
+    uint64_t yw_full[2], yw_empty[2];                     // weighting -> products;  products -> weighting
     uint64_t sum_full[2], sum_empty[2];                   // products -> registers;  registers -> products
     uint64_t drain, never;
     uint32_t tmem;
@@ -142,7 +149,7 @@ template <int D> struct __align__(1024) StatesSmem {
 
 template <int D>
 __global__ void __launch_bounds__(kStatesThreads, 1)
-    decay_tc_states_kernel(const __grid_constant__ DecayCall c, const __grid_constant__ DecayStates p, bool final,
+    decay_tc_states_kernel(const __grid_constant__ DecayCall c, const __grid_constant__ DecayStates p, DecayWhich which,
                            const __grid_constant__ CUtensorMap my, const __grid_constant__ CUtensorMap mz) {
     using F = StatesShape<D>;
     extern __shared__ __align__(1024) unsigned char raw[];
@@ -150,12 +157,12 @@ __global__ void __launch_bounds__(kStatesThreads, 1)
     const int h = blockIdx.x, index = blockIdx.y + 65535 * blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     DecaySegment g;
-    if (index >= (final ? c.nseq : c.segments)) return;
+    if (index >= (which == kEnds ? c.nseq : c.segments)) return;
     if (decay_malformed(c)) return;
     const int64_t size = (int64_t)c.dk * c.dv;
     float* to;
     const float* enter = nullptr;
-    if (final) {
+    if (which == kEnds) {
         to = p.edge_out + ((int64_t)index * c.H + h) * size;
         if (!decay_edge_segment(c, index, p.reverse, g)) {
             // an empty sequence: what enters it leaves it
@@ -165,16 +172,21 @@ __global__ void __launch_bounds__(kStatesThreads, 1)
         }
         enter = decay_entering(c, g, h, p.reverse, p.edge_in);
     } else {
-        if (!decay_segment(c, index, g) || (p.reverse ? decay_first(g) : decay_last(g))) return;
-        to = c.states[p.reverse] + ((int64_t)(decay_slot(g) - (p.reverse ? 1 : 0)) * c.H + h) * size;
+        if (!decay_segment(c, index, g)) return;
+        if (p.reverse ? decay_first(g) : decay_last(g)) {
+            if (which == kInner) return;
+            to = p.edge_out + ((int64_t)g.seq * c.H + h) * size;
+        } else {
+            to = c.states[p.reverse] + ((int64_t)(decay_slot(g) - (p.reverse ? 1 : 0)) * c.H + h) * size;
+        }
     }
     const DecayBase base = decay_base(c.log_decay[h]);
-    const int chunks = (g.end - g.start + kC - 1) / kC, groups = (chunks + kFlush - 1) / kFlush;
+    const int tiles = (g.end - g.start + F::rows - 1) / F::rows, groups = (tiles + F::flush - 1) / F::flush;
     if (threadIdx.x == 0) {
         init_all(s.full, F::stages, 1);
-        init_all(s.empty, F::stages, F::warps + 1);
-        init_all(s.yw_full, F::buffers, F::warps);
-        init_all(s.yw_empty, F::buffers, 1);
+        init_all(s.empty, F::stages, 8 + 1);
+        init_all(s.yw_full, 2, 8);
+        init_all(s.yw_empty, 2, 1);
         init_all(s.sum_full, 2, 1);
         init_all(s.sum_empty, 2, F::warps);
         init_all(&s.drain, 1, 1);
@@ -182,7 +194,7 @@ __global__ void __launch_bounds__(kStatesThreads, 1)
         fence_mbar_init();
     }
     if (warp == 1) {
-        tmem_alloc(&s.tmem, F::tmem);
+        tmem_alloc(&s.tmem, 2 * F::columns);
         tmem_relinquish();
     }
     fill_powers(s.pw, base);
@@ -192,60 +204,100 @@ __global__ void __launch_bounds__(kStatesThreads, 1)
     const uint32_t tm = s.tmem;
     bool ok = true;
     int loads = 0;
-    float sum[32];                            // of the warps that weight: their 32 columns of their row
-    const int w = warp - 4, q = warp & 3, part = (D == 64 ? w & 7 : w) >> 2, row = 32 * q + lane, col = 32 * part;
+    // of the warps that have sums: 32 columns of a row
+    const int w = warp - 4, q = w & 3, part = (D == 64 ? w & 7 : w) >> 2, row = 32 * q + lane, col = 32 * part;
+    float sum[32];
 
     if (warp == 0) {
         if (lane == 0) {
-            for (; loads < chunks && ok; ++loads) {
+            for (; loads < tiles; ++loads) {
                 const int st = loads % F::stages;
                 if (loads >= F::stages) ok = wait(&s.empty[st], (loads / F::stages - 1) & 1);
                 if (!ok) break;
-                mbar_arrive_expect_tx(&s.full[st], 2 * F::blocks * kTile);
+                mbar_arrive_expect_tx(&s.full[st], 2 * F::blocks * F::tile);
                 for (int b = 0; b < F::blocks; ++b) {
-                    tma_load_3d(s.y[st][b], &my, 64 * b, h, g.start + loads * kC, &s.full[st]);
-                    tma_load_3d(s.z[st][b], &mz, 64 * b, h, g.start + loads * kC, &s.full[st]);
+                    tma_load_3d(s.y[st][b], &my, 64 * b, h, g.start + loads * F::rows, &s.full[st]);
+                    tma_load_3d(s.z[st][b], &mz, 64 * b, h, g.start + loads * F::rows, &s.full[st]);
                 }
             }
         }
         __syncwarp();
     } else if (warp == 1) {
-        for (int k = 0; k < chunks && ok; ++k) {
-            const int st = k % F::stages, b = k % F::buffers, f = k / kFlush, a = f % F::sums;
-            ok = wait_w(&s.yw_full[b], (k / F::buffers) & 1);
-            if (ok && k % kFlush == 0 && f >= F::sums) ok = wait_w(&s.sum_empty[a], (f / F::sums - 1) & 1);
+        for (int k = 0; k < tiles; ++k) {
+            const int st = k % F::stages, b = k & 1, f = k / F::flush, a = f & 1;
+            ok = wait_w(&s.yw_full[b], (k >> 1) & 1);
+            if (ok && k % F::flush == 0 && f >= 2) ok = wait_w(&s.sum_empty[a], (f / 2 - 1) & 1);
             if (!ok) break;
             tc_fence_after();
             constexpr uint32_t id = idesc_bf16(128, D, true, true);
-            const uint64_t dz = sdesc_sw128(smem_u32(s.z[st]), kTile, 1024);
-            // D = 64: the first two parts of y are one product's 128 rows; the third's other rows are not used
-#pragma unroll
+            const uint64_t dz = sdesc_sw128(smem_u32(s.z[st]), F::tile, 1024);
+            // D = 64: the first two parts of y are one product's 128 rows; the third's other rows are whatever lies behind
+            // it, not used.  D = 128: the first part has sums of its own, the small ones share theirs.
+#pragma unroll 1
             for (int i = 0; i < (D == 64 ? 2 : 3); ++i) {
-                const uint64_t dy = sdesc_sw128(smem_u32(s.yw[b][D == 64 ? 2 * i : i]), kTile, 1024);
-                const uint32_t acc = tm + a * F::columns + D * i;
-#pragma unroll
-                for (int j = 0; j < kC / 16; ++j)
-                    mma_ss_w(acc, sdesc_add(dy, 2048 * j), sdesc_add(dz, 2048 * j), id, k % kFlush > 0 || j > 0 ? 1u : 0u);
+                const uint64_t dy = sdesc_sw128(smem_u32(s.yw[b][D == 64 ? 2 * i : i]), F::tile, 1024);
+                const uint32_t acc = tm + a * F::columns + D * (i < 2 ? i : 1);
+#pragma unroll 4
+                for (int j = 0; j < F::rows / 16; ++j)
+                    mma_ss_w(acc, sdesc_add(dy, 2048 * j), sdesc_add(dz, 2048 * j), id,
+                             k % F::flush > 0 || j > 0 || i == 2 ? 1u : 0u);
             }
             mma_commit_w(&s.yw_empty[b]);
             mma_commit_w(&s.empty[st]);
-            if (k % kFlush == kFlush - 1 || k + 1 == chunks) mma_commit_w(&s.sum_full[a]);
+            if (k % F::flush == F::flush - 1 || k + 1 == tiles) mma_commit_w(&s.sum_full[a]);
         }
     } else if (warp >= 4) {
-        const int mine = D == 64 ? w >> 3 : 0, block = part >> 1, c0 = (part & 1) * 4;
+        const int mine = w >> 3, w8 = w & 7;
+        // of a tile: this thread's row, and its 32 channels' first 16 bytes (the j-th: place ^ 16 j)
+        const int r = D == 64 ? 32 * (w8 & 3) + lane : 32 * (w8 & 1) + lane, p8 = D == 64 ? w8 >> 2 : w8 >> 1;
+        const uint32_t place = sw128_chunk(r, (p8 & 1) * 4);
+        const bool sums = D == 128 || mine == 0;
         if (g_force_wait_timeout) ok = __all_sync(0xffffffffu, mbar_wait(&s.never, 0, 1000000ull));
 #pragma unroll
         for (int j = 0; j < 32; ++j) sum[j] = 0.f;
         int flushed = 0;
-        auto flush = [&]() {
-            const int a = flushed % F::sums;
-            ok = wait_w(&s.sum_full[a], (flushed / F::sums) & 1);
-            if (!ok) return;
+        for (int k = mine; ok && (k < tiles || (sums && flushed < groups)); k += 2) {
+            if (k < tiles) {
+                const int st = k % F::stages, b = k & 1, t0 = g.start + k * F::rows, n = min(F::rows, g.end - t0);
+                ok = wait_w(&s.full[st], (k / F::stages) & 1);
+                if (ok && k >= 2) ok = wait_w(&s.yw_empty[b], (k / 2 - 1) & 1);
+                if (!ok) break;
+                const float far = p.reverse ? c.scale * decay_power(base, t0 - g.start) : decay_power(base, g.end - t0 - n);
+                const uint64_t weight = f32x2_splat(r < n ? far * s.pw[p.reverse ? r + 1 : n - 1 - r] : 0.f);
+                uint4 in[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) in[j] = *reinterpret_cast<const uint4*>(s.y[st][p8 >> 1] + (place ^ (16 * j)));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t v[4] = {in[j].x, in[j].y, in[j].z, in[j].w};
+                    uint32_t o[3][4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint64_t e = f32x2_mul(pair_of(r < n ? v[i] : 0u), weight);
+                        o[0][i] = split(e);
+                        o[1][i] = split(e);
+                        o[2][i] = f32x2_to_bf16x2(e);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 3; ++i)
+                        *reinterpret_cast<uint4*>(s.yw[b][i][p8 >> 1] + (place ^ (16 * j))) =
+                            make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
+                    // nothing from another sequence
+                    if (r >= n) *reinterpret_cast<uint4*>(s.z[st][p8 >> 1] + (place ^ (16 * j))) = make_uint4(0, 0, 0, 0);
+                }
+                fence_async_smem();
+                arrive_w(&s.yw_full[b]);
+                arrive_w(&s.empty[st]);
+            }
+            if (!sums || flushed == groups || (k < tiles && k < F::flush * (flushed + 1))) continue;
+            const int a = flushed & 1;
+            ok = wait_w(&s.sum_full[a], (flushed >> 1) & 1);
+            if (!ok) break;
             tc_fence_after();
             // D = 64: rows 64 .. 127 of the first columns are the second part's; the third part's rows are 0 .. 63
-#pragma unroll
-            for (int i = 0; i < (D == 64 ? 2 : 3); ++i) {
-                if (D == 64 && i == 1 && q >= 2) break;
+            const int sets = D == 64 && q >= 2 ? 1 : 2;
+#pragma unroll 1
+            for (int i = 0; i < sets; ++i)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     uint32_t v[16];
@@ -255,43 +307,10 @@ __global__ void __launch_bounds__(kStatesThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) sum[16 * u + j] += __uint_as_float(v[j]);
                 }
-            }
             tc_fence_before();
             arrive_w(&s.sum_empty[a]);
             ++flushed;
-        };
-        for (int k = mine; k < chunks && ok; k += F::buffers) {
-            const int st = k % F::stages, b = k % F::buffers, t0 = g.start + k * kC, n = min(kC, g.end - t0);
-            ok = wait_w(&s.full[st], (k / F::stages) & 1);
-            if (ok && k >= F::buffers) ok = wait_w(&s.yw_empty[b], (k / F::buffers - 1) & 1);
-            if (!ok) break;
-            const float far = p.reverse ? c.scale * decay_power(base, t0 - g.start) : decay_power(base, g.end - t0 - n);
-            const float weight = row < n ? far * s.pw[p.reverse ? row + 1 : n - 1 - row] : 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t at = sw128_chunk(row, c0 + j);
-                const uint4 v = *reinterpret_cast<const uint4*>(s.y[st][block] + at);
-                const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-                uint32_t o[3][4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint64_t e = f32x2_mul(pair_of(row < n ? in[i] : 0u), f32x2_splat(weight));
-                    o[0][i] = split(e);
-                    o[1][i] = split(e);
-                    o[2][i] = f32x2_to_bf16x2(e);
-                }
-#pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    *reinterpret_cast<uint4*>(s.yw[b][i][block] + at) = make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
-                // nothing from another sequence
-                if (row >= n) *reinterpret_cast<uint4*>(s.z[st][block] + at) = make_uint4(0, 0, 0, 0);
-            }
-            fence_async_smem();
-            arrive_w(&s.yw_full[b]);
-            arrive_w(&s.empty[st]);
-            if (mine == 0 && k >= kFlush * (flushed + 1)) flush();
         }
-        while (mine == 0 && ok && flushed < groups) flush();
     }
     if (__syncthreads_or(!ok)) {
         // copies and products on their way end before the block does
@@ -305,7 +324,7 @@ __global__ void __launch_bounds__(kStatesThreads, 1)
             mbar_wait(&s.drain, 0, kDrainNs);
         }
     } else {
-        const bool on = warp >= 4 && (D != 64 || w < 8);
+        const bool on = warp >= 4 && (D == 128 || w < 8);
         const float keep = decay_power(base, g.end - g.start);
         if (D == 64) {
             float (*ex)[65] = reinterpret_cast<float (*)[65]>(s.yw);
@@ -330,7 +349,7 @@ __global__ void __launch_bounds__(kStatesThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) tmem_dealloc(tm, F::tmem);
+    if (warp == 1) tmem_dealloc(tm, 2 * F::columns);
 }
 
 // ---------------------------------------------------------------------------
@@ -366,6 +385,7 @@ template <int D> struct __align__(1024) PassSmem {
     uint64_t r_full[2], r_empty, o_full, o_empty;         // x S, P z;  taken by the outputs' warps
     uint64_t drain, never;
     uint32_t tmem;
+    int updated;                                          // chunks that the state has taken
 };
 
 template <int D, bool Reverse>
@@ -411,6 +431,7 @@ __global__ void __launch_bounds__(kPassThreads, 1)
     if (threadIdx.x < 32) s.pw[kC + 4 + threadIdx.x] = c.scale * decay_power(base, threadIdx.x);
     for (int i = threadIdx.x; i < F::ring * D; i += kPassThreads) s.edge[i / D][i % D] = reverse ? 0 : kC;
     if (threadIdx.x < F::ring) s.strange[threadIdx.x] = 0;
+    if (threadIdx.x == 0) s.updated = 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -458,8 +479,10 @@ __global__ void __launch_bounds__(kPassThreads, 1)
         for (int it = 0; it < min(F::scores, chunks) && ok; ++it) scores(it);
         for (int it = 0; it < chunks && ok; ++it) {
             const int b = it % F::scores, sz = it % F::z_stages;
+            // (a chunk that is not whole: rows behind its end are zero once the operands are made)
             ok = wait_w(&s.p_full[b], (it / F::scores) & 1) && wait_w(&s.z_full[sz], (it / F::z_stages) & 1) &&
-                 (it == 0 || wait_w(&s.o_empty, (it - 1) & 1));
+                 (it == 0 || wait_w(&s.o_empty, (it - 1) & 1)) &&
+                 (g.end - token(it) >= kC || wait_w(&s.conv_full[it & 1], (it >> 1) & 1));
             if (!ok) break;
             tc_fence_after();
             constexpr uint32_t id = idesc_bf16(128, D, false, true);
@@ -488,6 +511,9 @@ __global__ void __launch_bounds__(kPassThreads, 1)
             mma_commit_w(&s.state_full);
             mma_commit_w(&s.xy_empty[st]);
             mma_commit_w(&s.z_empty[sz]);
+            ok = wait_w(&s.state_full, it & 1);
+            if (lane == 0) *reinterpret_cast<volatile int*>(&s.updated) = it + 1;
+            __syncwarp();
         }
     } else if (warp == 3) {
         // ---- x S
@@ -535,7 +561,7 @@ __global__ void __launch_bounds__(kPassThreads, 1)
                 }
             if (__any_sync(0xffffffffu, (top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u)) {
                 // once the state has taken them, they are set to zero
-                if (!last) ok = wait_w(&s.state_full, it & 1);
+                if (!last) ok = __all_sync(0xffffffffu, wait_count(&s.updated, it + 1));
                 if (!ok) break;
                 for (int k = 0; k < F::blocks; ++k)
                     clear_strange(s.z[sz][k], s.edge[it % F::ring] + 64 * k, &s.strange[it % F::ring], row < n ? row : -1, c0, reverse);
@@ -643,15 +669,6 @@ __global__ void __launch_bounds__(kPassThreads, 1)
                     }
                 }
             }
-            if (n < kC) {
-                // nothing from another sequence
-                ok = wait_w(&s.z_full[sz], zpar);
-                if (!ok) break;
-                if (row >= n)
-                    for (int k = 0; k < F::blocks; ++k)
-                        for (int j = 0; j < 4; ++j)
-                            *reinterpret_cast<uint4*>(s.z[sz][k] + (place ^ (16 * j))) = make_uint4(0, 0, 0, 0);
-            }
             // the state is there, and the operand that its buffer held has been read
             if (it >= F::states) {
                 const int then = it - F::states;
@@ -659,6 +676,16 @@ __global__ void __launch_bounds__(kPassThreads, 1)
             }
             if (ok && it > 0) ok = wait_w(&s.state_full, (it - 1) & 1);
             if (!ok) break;
+            if (n < kC) {
+                // nothing from another sequence (z of the chunk before has been there: the state has it; so this is not
+                // taken for the one that the barrier's parity last stood for)
+                ok = wait_w(&s.z_full[sz], zpar);
+                if (!ok) break;
+                if (row >= n)
+                    for (int k = 0; k < F::blocks; ++k)
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<uint4*>(s.z[sz][k] + (place ^ (16 * j))) = make_uint4(0, 0, 0, 0);
+            }
             if (has && rows) {
                 tc_fence_after();
                 const uint64_t keep = f32x2_splat(s.pw[n]);
@@ -831,13 +858,13 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// [T][H][d] bf16 -> boxes of 128 tokens x 64 channels of one head, zeros behind the last channel and token.
-bool rows_map(CUtensorMap* m, const void* base, const DecayCall& c, int d) {
+// [T][H][d] bf16 -> boxes of `rows` tokens x 64 channels of one head, zeros behind the last channel and token.
+bool rows_map(CUtensorMap* m, const void* base, const DecayCall& c, int d, int rows = kC) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)c.H, (cuuint64_t)c.T};
     const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)c.H * d * 2};
-    const cuuint32_t box[3] = {64, 1, (cuuint32_t)kC}, one[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows}, one[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -851,14 +878,15 @@ cudaError_t opt_in(K kernel, size_t bytes) {
 }
 
 template <int D>
-cudaError_t states(const DecayCall& c, const DecayStates& p, bool final, cudaStream_t s) {
+cudaError_t states(const DecayCall& c, const DecayStates& p, DecayWhich which, cudaStream_t s) {
     CUtensorMap my{}, mz{};
-    if (c.T > 0 && (!rows_map(&my, p.y, c, c.dk) || !rows_map(&mz, p.z, c, c.dv))) return cudaErrorInvalidValue;
+    constexpr int rows = StatesShape<D>::rows;
+    if (c.T > 0 && (!rows_map(&my, p.y, c, c.dk, rows) || !rows_map(&mz, p.z, c, c.dv, rows))) return cudaErrorInvalidValue;
     constexpr size_t smem = sizeof(StatesSmem<D>) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory");
     const cudaError_t e = opt_in(decay_tc_states_kernel<D>, smem);
     if (e != cudaSuccess) return e;
-    decay_tc_states_kernel<D><<<grid_of(c.H, final ? c.nseq : c.segments), kStatesThreads, smem, s>>>(c, p, final, my, mz);
+    decay_tc_states_kernel<D><<<grid_of(c.H, which == kEnds ? c.nseq : c.segments), kStatesThreads, smem, s>>>(c, p, which, my, mz);
     return cudaGetLastError();
 }
 
@@ -885,8 +913,8 @@ bool decay_tc_fits(const DecayCall& c, int dtype) {
     return dtype == LA_BF16 && c.dk <= 128 && c.dv <= 128 && c.dk % 8 == 0 && c.dv % 8 == 0;
 }
 
-cudaError_t decay_tc_states(const DecayCall& c, const DecayStates& p, bool final, cudaStream_t s) {
-    return c.dk <= 64 && c.dv <= 64 ? states<64>(c, p, final, s) : states<128>(c, p, final, s);
+cudaError_t decay_tc_states(const DecayCall& c, const DecayStates& p, DecayWhich which, cudaStream_t s) {
+    return c.dk <= 64 && c.dv <= 64 ? states<64>(c, p, which, s) : states<128>(c, p, which, s);
 }
 
 cudaError_t decay_tc_pass(const DecayCall& c, const DecayPass& p, cudaStream_t s) {

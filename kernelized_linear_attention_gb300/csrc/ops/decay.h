@@ -60,8 +60,13 @@ struct DecayStates {
     const void* z;               // [T][H][dv]
     int reverse;
     const float* edge_in;        // [nseq][H][dk][dv] or NULL: what enters each sequence
-    float* edge_out;             // [nseq][H][dk][dv]: what leaves it (final pass)
+    float* edge_out;             // [nseq][H][dk][dv] or NULL: what leaves it
 };
+
+// Which segments a state pass sums.  Inner: those that another one follows.  All: the ones at the sequences' ends too,
+// whose sums wait in edge_out for the join to add what enters them.  Ends: these alone, with what enters them (where
+// edge_out is edge_in, which the products still need, the ends come behind them).
+enum DecayWhich { kInner, kAll, kEnds };
 
 size_t decay_layout(DecayCall& c, int dtype, bool backward, void* workspace);   // bytes; sets the workspace members
 cudaError_t decay_forward(const DecayCall& c, const void* q, const void* k, const void* v, int dtype,
@@ -75,7 +80,7 @@ cudaError_t decay_step(const void* q, const void* k, const void* v, const float*
 
 // Tensor cores: bf16 of up to 128 channels, a multiple of 8, in arrays that start on 16 bytes (decay_tc.cu).
 bool decay_tc_fits(const DecayCall& c, int dtype);
-cudaError_t decay_tc_states(const DecayCall& c, const DecayStates& p, bool final, cudaStream_t s);
+cudaError_t decay_tc_states(const DecayCall& c, const DecayStates& p, DecayWhich which, cudaStream_t s);
 cudaError_t decay_tc_pass(const DecayCall& c, const DecayPass& p, cudaStream_t s);
 cudaError_t decay_force_wait_timeout(int enable);   // test hook behind la_test_force_wait_timeout
 

@@ -21,209 +21,322 @@ namespace la {
 namespace {
 
 constexpr int kQkThreads = 256;       // the most a block has
-constexpr int kJoinColumns = 32, kJoinRows = 16;
+constexpr int kJoinColumns = 32, kJoinRows = 32;
 
 struct QkPlan {
-    int G;                   // lanes of a row
+    int log_G;               // lanes of a row
     int heads, share;        // heads of q and k together; of a block
     int tokens;              // token places of a block: groups of its heads that run side by side
     int tile;                // tokens whose cos and sin are held together
-    int64_t span;            // tokens of a block
+    int blocks;              // along the tokens
     int pair_units, units;   // of a head
 };
 
-template <typename T, int N, bool Interleaved, int KU, bool Backward>
-__global__ void __launch_bounds__(kQkThreads) qk_norm_rotary_kernel(const __grid_constant__ QkNormParams p,
+// Forward, rows that a lane's vectors of 16 bytes hold are copied to shared memory ahead of their use, by the lane that
+// uses them: two blocks per SM of 114 registers a thread (65536 x 32 x 64 in bf16 97 us; four of 64, which take a quarter
+// more instructions, 106).  The backward pass has twice the rows on their way and more registers to keep, and is faster
+// with three blocks and loads to registers (32768 x 16 x 64: 48 us and 65).
+constexpr int kRing = 4;              // rows on their way, a power of two
+template <typename T, int N, int KU, bool Backward>
+constexpr bool copied = !Backward && N > 1 && KU == 1 && sizeof(T) * N == 16;
+
+// Where pair j's cos lies in a token's part of the table, in floats, and how far behind it its sin.  Halves in vectors:
+// [N / 2][P / N] of (cos, cos, sin, sin) of two neighbouring pairs, so that neighbouring lanes, which have neighbouring
+// units, read neighbouring 16 bytes, two pairs in each half of a register pair; otherwise [P] of (cos, sin).
+template <int N, bool Interleaved>
+__device__ __forceinline__ int table_place(int j, int apart) {
+    if constexpr (N > 1 && !Interleaved) return ((j % N / 2) * apart + j / N) * 4 + (j & 1);
+    else return 2 * j;
+}
+template <int N, bool Interleaved>
+constexpr int kSinBehind = N > 1 && !Interleaved ? 2 : 1;
+
+// Turns a unit's pairs, two to an instruction: a[0] and a[1] hold the first and second channels of N pairs, or, whole
+// pairs in one vector, a[0] N / 2 pairs.  `cs`: the unit's first place in its token's table.
+template <int N, bool Interleaved, int Sides>
+__device__ __forceinline__ void turn_unit(typename Pairs<N>::P (&a)[Sides][Pairs<N>::n], const float* cs, int apart) {
+    if constexpr (N == 1) {
+        const float c = cs[0], s = cs[1], f0 = a[0][0], f1 = a[1][0];
+        a[0][0] = fmaf(f0, c, -__fmul_rn(f1, s));
+        a[1][0] = fmaf(f1, c, __fmul_rn(f0, s));
+    } else if constexpr (Interleaved) {
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) {
+            const float2 w = *reinterpret_cast<const float2*>(cs + 2 * k);
+            const float f0 = tc::f32x2_lo(a[0][k]), f1 = tc::f32x2_hi(a[0][k]);
+            a[0][k] = tc::f32x2_of(__float_as_uint(fmaf(f0, w.x, -__fmul_rn(f1, w.y))),
+                                   __float_as_uint(fmaf(f1, w.x, __fmul_rn(f0, w.y))));
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) {
+            const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(cs + 4 * k * apart);
+            const uint64_t f0 = a[0][k], f1 = a[1][k];
+            a[0][k] = pfma(f0, (uint64_t)w.x, pmul(pmul(f1, psplat<uint64_t>(-1.f)), (uint64_t)w.y));
+            a[1][k] = pfma(f1, (uint64_t)w.x, pmul(f0, (uint64_t)w.y));
+        }
+    }
+}
+
+// Full: every lane of a group has KU units, and all turn.
+template <typename T, int N, bool Interleaved, int KU, bool Backward, bool Full>
+__global__ void __launch_bounds__(kQkThreads, KU > 1 ? 1 : Backward ? 3 : 2) qk_norm_rotary_kernel(const __grid_constant__ QkNormParams p,
                                                              const __grid_constant__ QkPlan plan) {
-    extern __shared__ float2 cs[];    // as in rotary.cu: [tile][P], where pairs are halves [tile][N][P / N]
+    // two tables [tile][2 P], a tile's and the next one's; behind them the rows on their way, 16 bytes of each vector a lane
+    extern __shared__ __align__(16) float table[];
     using V = Vec<T, N>;
+    using R = Pairs<N>;
+    using P = typename R::P;
     constexpr bool kOne = Interleaved && N > 1;   // whole pairs in one vector
     constexpr int kPairs = kOne ? N / 2 : N, kSides = kOne ? 1 : 2;
-    // rows whose loads are on their way together: up to 64 bytes a lane and array
-    constexpr int kAhead = KU * kSides * (int)sizeof(V) >= 64 ? 1 : 64 / (KU * kSides * (int)sizeof(V)) > 4 ? 4 : 64 / (KU * kSides * (int)sizeof(V));
+    constexpr bool kCopied = copied<T, N, KU, Backward>;
     const int apart = kOne ? 1 : p.P / kPairs, second = Interleaved ? 1 : p.P;
-    const int lane = threadIdx.x % plan.G, group = threadIdx.x / plan.G;
+    const int G = 1 << plan.log_G, lane = threadIdx.x & (G - 1), group = threadIdx.x >> plan.log_G;
     const int hh = group % plan.share, place = group / plan.share, h0 = blockIdx.y * plan.share;
     const bool mine = place < plan.tokens && h0 + hh < plan.heads;
     const int k = mine && h0 + hh >= p.H[0], h = h0 + hh - (k ? p.H[0] : 0);
+    const float over_d = 1.f / (float)p.d;
     int at[KU];                       // a unit's first channel, or -1
     bool turned[KU];
-    float w[KU][kSides][N];
-    float sum[Backward ? KU : 1][kSides][N];
+    P w[KU][kSides][R::n];
+    P sum[Backward ? KU : 1][kSides][R::n];
 #pragma unroll
     for (int u = 0; u < KU; ++u) {
-        const int e = lane + u * plan.G;
-        turned[u] = e < plan.pair_units;
-        at[u] = !mine || e >= plan.units ? -1
+        const int e = lane + u * G;
+        turned[u] = Full || e < plan.pair_units;
+        at[u] = !Full && e >= plan.units ? -1
                 : turned[u]              ? (Interleaved ? 2 : 1) * e * kPairs
                                          : 2 * p.P + (e - plan.pair_units) * N;
 #pragma unroll
-        for (int i = 0; i < kSides; ++i)
+        for (int s = 0; s < kSides; ++s) {
+            Vec<float, N> v;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                const bool on = at[u] >= 0 && (i == 0 || turned[u]);
-                w[u][i][j] = on && p.w[k] ? p.w[k][(p.per_head ? (int64_t)h * p.d : 0) + at[u] + i * second + j] : 1.f;
-                if (Backward) sum[u][i][j] = 0.f;
+                const bool on = mine && (Full || (at[u] >= 0 && (s == 0 || turned[u])));
+                v.v[j] = on && p.w[k] ? p.w[k][(p.per_head ? (int64_t)h * p.d : 0) + at[u] + s * second + j] : 1.f;
             }
+            unpack_pairs<N>(w[u][s], v);
+#pragma unroll
+            for (int j = 0; j < R::n; ++j)
+                if (Backward) sum[u][s][j] = psplat<P>(0.f);
+        }
     }
-    const int64_t first = blockIdx.x * plan.span, end = min64(first + plan.span, p.T);
-    for (int64_t t0 = first; t0 < end; t0 += plan.tile) {
-        const int n = (int)min64(plan.tile, end - t0);
-        for (int b = 0; b < n; b += kAhead * plan.tokens) {
-            V x[kAhead][KU][kSides], dy[Backward ? kAhead : 1][KU][kSides];
-            bool on[kAhead];
+    const T* const x0 = static_cast<const T*>(p.x[k]) + (int64_t)h * p.d;
+    const T* const d0 = static_cast<const T*>(p.dy[k]) + (int64_t)h * p.d;
+    T* const y0 = static_cast<T*>(p.y[k]) + (int64_t)h * p.d;
+    const int64_t row = (int64_t)p.H[k] * p.d, stride = p.stride[k];
+    float* const rstds = p.rstd[k];
+    const int heads_of = p.H[k];
+    uint4* const ring = reinterpret_cast<uint4*>(table + 4 * (int64_t)plan.tile * p.P) + threadIdx.x;
+    constexpr int kVectors = KU * kSides;      // of a row and lane
+    // the block's tiles are gridDim.x apart, so that all blocks together work on neighbouring tokens; a row of this group
+    // is token `place` of each `tokens` of them
+    const int64_t apart_tiles = (int64_t)gridDim.x * plan.tile;
+    struct Row {
+        int64_t t0;                   // of its tile
+        int in;                       // its first place in the tile
+    };
+    auto advance = [&](Row& r) {
+        r.in += plan.tokens;
+        if (r.in >= plan.tile) {
+            r.in = 0;
+            r.t0 += apart_tiles;
+        }
+    };
+    // a lane copies what it will use itself, kRing - 1 rows ahead
+    Row ahead{(int64_t)blockIdx.x * plan.tile, 0};
+    int slot = 0;
+    auto fetch = [&]() {
+        const int64_t t = ahead.t0 + ahead.in + place;
+        if (mine && t < p.T) {
+            uint4* const to = ring + slot * kVectors * blockDim.x;
 #pragma unroll
-            for (int r = 0; r < kAhead; ++r) {
-                const int i = b + r * plan.tokens + place;
-                on[r] = mine && i < n;
-                const int64_t row = (t0 + (on[r] ? i : 0)) * p.H[k] + h;
-                const T* px = static_cast<const T*>(p.x[k]) + (t0 + (on[r] ? i : 0)) * p.stride[k] + (int64_t)h * p.d;
-                const T* pd = static_cast<const T*>(p.dy[k]) + row * p.d;
+            for (int u = 0; u < KU; ++u)
 #pragma unroll
-                for (int u = 0; u < KU; ++u)
-#pragma unroll
-                    for (int s = 0; s < kSides; ++s) {
-                        const bool in = on[r] && at[u] >= 0 && (s == 0 || turned[u]);
-                        x[r][u][s] = in ? *reinterpret_cast<const V*>(px + at[u] + s * second) : V{};
-                        if (Backward) dy[r][u][s] = in ? *reinterpret_cast<const V*>(pd + at[u] + s * second) : V{};
-                    }
-            }
-            if (b == 0) {
-                // the tile's cos and sin, while the first loads are on their way
-                if (t0 != first) __syncthreads();
-                const int groups = max(1, (int)blockDim.x / p.P);
-                for (int i = threadIdx.x; i < groups * p.P; i += blockDim.x) {
-                    const int g = i / p.P, j = i - g * p.P, to = kOne ? j : j % kPairs * apart + j / kPairs;
-                    const Turn turn = turn_of(p, j);
-                    for (int t = g; t < n; t += groups) cs[t * p.P + to] = cos_sin(p, turn, t0 + t);
+                for (int s = 0; s < kSides; ++s) {
+                    if (!Full && (at[u] < 0 || (s > 0 && !turned[u]))) continue;
+                    copy_16(to + (u * kSides + s) * blockDim.x, x0 + t * stride + at[u] + s * second);
                 }
-                __syncthreads();
+        }
+        copies_done();
+        advance(ahead);
+        slot = (slot + 1) & (kRing - 1);
+    };
+    if (kCopied) {
+        for (int q = 0; q < kRing - 1; ++q) fetch();
+    }
+    Row now{(int64_t)blockIdx.x * plan.tile, 0};
+    float next = 0.f;                 // backward: rstd of the next row
+    if (Backward && mine && now.t0 + place < p.T) next = rstds[(now.t0 + place) * heads_of + h];
+    int which = 1;                    // of the tables
+    for (; now.t0 < p.T; advance(now)) {
+        const int64_t t = now.t0 + now.in + place;
+        const bool on = mine && t < p.T;
+        V x[KU][kSides], dy[Backward ? KU : 1][kSides];
+        const float held = next;
+        if (kCopied) {
+            fetch();
+        } else {
+#pragma unroll
+            for (int u = 0; u < KU; ++u)
+#pragma unroll
+                for (int s = 0; s < kSides; ++s) {
+                    const bool in = Full ? on : on && at[u] >= 0 && (s == 0 || turned[u]);
+                    x[u][s] = in ? *reinterpret_cast<const V*>(x0 + t * stride + at[u] + s * second) : V{};
+                    if (Backward) dy[u][s] = in ? *reinterpret_cast<const V*>(d0 + t * row + at[u] + s * second) : V{};
+                }
+        }
+        if (Backward) {
+            Row after = now;
+            advance(after);
+            const int64_t ta = after.t0 + after.in + place;
+            next = mine && ta < p.T ? rstds[ta * heads_of + h] : 0.f;
+        }
+        if (now.in == 0) {
+            // the next tile's cos and sin (whoever still works on the one before has the other table)
+            which ^= 1;
+            const int n = (int)min64(plan.tile, p.T - now.t0), groups = max(1, (int)blockDim.x / p.P);
+            float* const fill = table + which * 2 * plan.tile * p.P;
+            for (int i = threadIdx.x; i < groups * p.P; i += blockDim.x) {
+                const int g = i / p.P, j = i - g * p.P, to = table_place<N, Interleaved>(j, apart);
+                const Turn turn = turn_of(p, j);
+                for (int e = g; e < n; e += groups) {
+                    const float2 cw = cos_sin(p, turn, now.t0 + e);
+                    fill[2 * e * p.P + to] = cw.x;
+                    fill[2 * e * p.P + to + kSinBehind<N, Interleaved>] = cw.y;
+                }
             }
+            __syncthreads();
+        }
+        if (kCopied) {
+            wait_copies<kRing - 1>();
+            const uint4* const from = ring + slot * kVectors * blockDim.x;      // (the slot after the newest is the oldest)
 #pragma unroll
-            for (int r = 0; r < kAhead; ++r) {
-                const int i = b + r * plan.tokens + place;
-                const int64_t row = (t0 + (on[r] ? i : 0)) * p.H[k] + h;
-                T* py = static_cast<T*>(p.y[k]) + row * p.d;
-                float rstd, f[KU][kSides][N], v[Backward ? KU : 1][kSides][N];
-                float square = 0.f;
+            for (int u = 0; u < KU; ++u)
 #pragma unroll
-                for (int u = 0; u < KU; ++u)
+                for (int s = 0; s < kSides; ++s) {
+                    const bool in = Full ? on : on && at[u] >= 0 && (s == 0 || turned[u]);
+                    x[u][s] = in ? *reinterpret_cast<const V*>(from + (u * kSides + s) * blockDim.x) : V{};
+                }
+        }
+        const float* const cs = table + 2 * (which * plan.tile + now.in + place) * p.P;
+        P f[KU][kSides][R::n], v[Backward ? KU : 1][kSides][R::n];
+        float rstd;
+        P part = psplat<P>(0.f);
 #pragma unroll
-                    for (int s = 0; s < kSides; ++s) {
-                        unpack(f[u][s], x[r][u][s]);
-                        if (Backward) unpack(v[u][s], dy[r][u][s]);
-                        if (!Backward) {
+        for (int u = 0; u < KU; ++u)
 #pragma unroll
-                            for (int j = 0; j < N; ++j) square = fmaf(f[u][s][j], f[u][s][j], square);
-                        }
-                    }
+            for (int s = 0; s < kSides; ++s) {
+                unpack_pairs<N>(f[u][s], x[u][s]);
+                if (Backward) unpack_pairs<N>(v[Backward ? u : 0][s], dy[Backward ? u : 0][s]);
                 if (!Backward) {
-                    for (int o = plan.G / 2; o > 0; o /= 2) square += __shfl_xor_sync(0xffffffffu, square, o);
-                    rstd = rsqrtf(square / (float)p.d + p.eps);
-                    if (on[r] && lane == 0 && p.rstd[k]) p.rstd[k][row] = rstd;
-                } else {
-                    rstd = on[r] ? p.rstd[k][row] : 0.f;
+#pragma unroll
+                    for (int j = 0; j < R::n; ++j) part = pfma(f[u][s][j], f[u][s][j], part);
                 }
-                // forward: x becomes u and is turned; backward: dy is turned back
-                float dot = 0.f;
+            }
+        if (!Backward) {
+            float square = psum(part);
+            for (int o = G >> 1; o > 0; o >>= 1) square += __shfl_xor_sync(0xffffffffu, square, o);
+            rstd = rsqrtf(fmaf(square, over_d, p.eps));
+            if (on && lane == 0 && rstds) rstds[t * heads_of + h] = rstd;
+        } else {
+            rstd = held;
+        }
+        const P scale = psplat<P>(rstd);
+        // forward: x becomes u and is turned; backward: dy is turned back
 #pragma unroll
-                for (int u = 0; u < KU; ++u) {
-                    auto& a = Backward ? v[Backward ? u : 0] : f[u];
+        for (int u = 0; u < KU; ++u) {
+            auto& a = Backward ? v[Backward ? u : 0] : f[u];
 #pragma unroll
-                    for (int s = 0; s < kSides; ++s)
+            for (int s = 0; s < kSides; ++s)
 #pragma unroll
-                        for (int j = 0; j < N; ++j) {
-                            f[u][s][j] *= rstd;
-                            if (!Backward) f[u][s][j] *= w[u][s][j];
-                        }
-                    if (turned[u] && on[r] && at[u] >= 0) {
-                        const float2* c = cs + i * p.P + (lane + u * plan.G) * (kOne ? kPairs : 1);
-#pragma unroll
-                        for (int j = 0; j < kPairs; ++j) {
-                            const float2 cw = c[j * apart];
-                            float& x0 = a[0][kOne ? 2 * j : j];
-                            float& x1 = kOne ? a[0][kOne ? 2 * j + 1 : 0] : a[kSides - 1][j];
-                            const float f0 = x0, f1 = x1;
-                            x0 = fmaf(f0, cw.x, -__fmul_rn(f1, cw.y));
-                            x1 = fmaf(f1, cw.x, __fmul_rn(f0, cw.y));
-                        }
-                    }
-                    if (Backward) {
-#pragma unroll
-                        for (int s = 0; s < kSides; ++s)
-#pragma unroll
-                            for (int j = 0; j < N; ++j) {
-                                sum[Backward ? u : 0][s][j] = fmaf(a[s][j], f[u][s][j], sum[Backward ? u : 0][s][j]);
-                                a[s][j] *= w[u][s][j];
-                                dot = fmaf(a[s][j], f[u][s][j], dot);
-                            }
-                    }
+                for (int j = 0; j < R::n; ++j) {
+                    if (!Backward) f[u][s][j] = pmul(f[u][s][j], w[u][s][j]);
+                    f[u][s][j] = pmul(f[u][s][j], scale);
                 }
-                if (Backward) {
-                    for (int o = plan.G / 2; o > 0; o /= 2) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-                    dot /= (float)p.d;
-                }
+            if (Full ? on : turned[u] && on && at[u] >= 0) {
+                const int e = lane + u * G;
+                turn_unit<N, Interleaved>(a, cs + (N > 1 && !Interleaved ? 4 * e : 2 * e * kPairs), apart);
+            }
+            if (Backward) {
 #pragma unroll
-                for (int u = 0; u < KU; ++u)
+                for (int s = 0; s < kSides; ++s)
 #pragma unroll
-                    for (int s = 0; s < kSides; ++s) {
-                        if (!on[r] || at[u] < 0 || (s > 0 && !turned[u])) continue;
-                        if (Backward) {
-#pragma unroll
-                            for (int j = 0; j < N; ++j)
-                                f[u][s][j] = rstd * fmaf(-f[u][s][j], dot, v[Backward ? u : 0][s][j]);
-                        }
-                        V o;
-                        pack(o, f[u][s]);
-                        *reinterpret_cast<V*>(py + at[u] + s * second) = o;
+                    for (int j = 0; j < R::n; ++j) {
+                        sum[Backward ? u : 0][s][j] = pfma(a[s][j], f[u][s][j], sum[Backward ? u : 0][s][j]);
+                        a[s][j] = pmul(a[s][j], w[u][s][j]);
+                        part = pfma(a[s][j], f[u][s][j], part);
                     }
             }
         }
+        P less = psplat<P>(0.f);
+        if (Backward) {
+            float dot = psum(part);
+            for (int o = G >> 1; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+            less = psplat<P>(-dot * over_d);
+        }
+#pragma unroll
+        for (int u = 0; u < KU; ++u)
+#pragma unroll
+            for (int s = 0; s < kSides; ++s) {
+                if (Full ? !on : !on || at[u] < 0 || (s > 0 && !turned[u])) continue;
+                if (Backward) {
+#pragma unroll
+                    for (int j = 0; j < R::n; ++j)
+                        f[u][s][j] = pmul(scale, pfma(f[u][s][j], less, v[Backward ? u : 0][s][j]));
+                }
+                V o;
+                pack_pairs<N>(o, f[u][s]);
+                *reinterpret_cast<V*>(y0 + t * row + at[u] + s * second) = o;
+            }
     }
     if (!Backward || !p.partial) return;
-    // the block's sums for the weights' gradients: over its token places, in order
+    // the block's sums for the weights' gradients: over its token places, and heads that share a weight, in order
     __syncthreads();
-    float* red = reinterpret_cast<float*>(cs);       // [place][head][d]
+    float* const red = table;                        // [place][head][d]
 #pragma unroll
     for (int u = 0; u < KU; ++u)
 #pragma unroll
         for (int s = 0; s < kSides; ++s) {
-            if (at[u] < 0 || (s > 0 && !turned[u])) continue;
+            if (!mine || (!Full && (at[u] < 0 || (s > 0 && !turned[u])))) continue;
+            Vec<float, N> v;
+            pack_pairs<N>(v, sum[Backward ? u : 0][s]);
 #pragma unroll
-            for (int j = 0; j < N; ++j)
-                red[(place * plan.share + hh) * p.d + at[u] + s * second + j] = sum[Backward ? u : 0][s][j];
+            for (int j = 0; j < N; ++j) red[(place * plan.share + hh) * p.d + at[u] + s * second + j] = v.v[j];
         }
     __syncthreads();
     const int heads = min(plan.share, plan.heads - h0);
-    for (int i = threadIdx.x; i < heads * p.d; i += blockDim.x) {
-        float v = 0.f;
-        for (int t = 0; t < plan.tokens; ++t) v += red[t * plan.share * p.d + i];
-        p.partial[((int64_t)blockIdx.x * plan.heads + h0) * p.d + i] = v;
+    if (p.per_head) {
+        for (int i = threadIdx.x; i < heads * p.d; i += blockDim.x) {
+            float v = 0.f;
+            for (int t = 0; t < plan.tokens; ++t) v += red[t * plan.share * p.d + i];
+            p.partial[((int64_t)blockIdx.x * plan.heads + h0) * p.d + i] = v;
+        }
+    } else {
+        const int mid = min(max(p.H[0] - h0, 0), heads);      // heads of q in this block
+        for (int i = threadIdx.x; i < 2 * p.d; i += blockDim.x) {
+            const int key = i >= p.d, c = i - key * p.d;
+            float v = 0.f;
+            for (int t = 0; t < plan.tokens; ++t)
+                for (int e = key ? mid : 0; e < (key ? heads : mid); ++e) v += red[(t * plan.share + e) * p.d + c];
+            p.partial[((int64_t)blockIdx.x * gridDim.y + blockIdx.y) * 2 * p.d + i] = v;
+        }
     }
 }
 
-// dw [rows][d] of q or k from the blocks' sums: of one head (per_head) or of all.
+// dw [rows][d] of q or k from the blocks' sums: of one head (per_head) or of all that share one.
 __global__ void __launch_bounds__(kJoinColumns * kJoinRows) qk_join_kernel(const __grid_constant__ QkNormParams p,
-                                                                           int blocks) {
+                                                                           int sums) {
     __shared__ float part[kJoinRows][kJoinColumns];
-    const int heads = p.H[0] + p.H[1], c = blockIdx.x * kJoinColumns + threadIdx.x;
-    int k, h0, n;                     // heads h0 .. h0 + n - 1 of q and k together
-    if (p.per_head) {
-        h0 = blockIdx.y;
-        n = 1;
-        k = h0 >= p.H[0];
-    } else {
-        k = blockIdx.y;
-        h0 = k ? p.H[0] : 0;
-        n = p.H[k];
-    }
+    const int rows = p.per_head ? p.H[0] + p.H[1] : 2, c = blockIdx.x * kJoinColumns + threadIdx.x, r = blockIdx.y;
+    const int k = p.per_head ? r >= p.H[0] : r;
     float* const out = p.dw[k];
     // compensated: a thread's sum is as good as its terms
     float sum = 0.f, rest = 0.f;
     if (c < p.d) {
-        for (int64_t i = threadIdx.y; i < (int64_t)blocks * n; i += kJoinRows) {
-            const int64_t b = i / n, h = h0 + i % n;
-            const float y = __fsub_rn(p.partial[(b * heads + h) * p.d + c], rest), t = __fadd_rn(sum, y);
+#pragma unroll 8
+        for (int i = threadIdx.y; i < sums; i += kJoinRows) {
+            const float y = __fsub_rn(p.partial[((int64_t)i * rows + r) * p.d + c], rest), t = __fadd_rn(sum, y);
             rest = __fsub_rn(__fsub_rn(t, sum), y);
             sum = t;
         }
@@ -235,10 +348,10 @@ __global__ void __launch_bounds__(kJoinColumns * kJoinRows) qk_join_kernel(const
         __syncthreads();
     }
     if (threadIdx.y == 0 && c < p.d && out)
-        out[(p.per_head ? (int64_t)(h0 - (k ? p.H[0] : 0)) * p.d : 0) + c] = part[0][threadIdx.x];
+        out[(p.per_head ? (int64_t)(r - (k ? p.H[0] : 0)) * p.d : 0) + c] = part[0][threadIdx.x];
 }
 
-constexpr int kTable = 16 * 1024;     // bytes of cos and sin that a block aims at
+constexpr int kTable = 8 * 1024;      // bytes of a tile's cos and sin that a block aims at
 
 // Vectors of 16 bytes: the arrays, the rows of every token and where second halves and tails begin.
 bool whole_vectors(const QkNormParams& p, int N, bool backward) {
@@ -253,72 +366,80 @@ bool whole_vectors(const QkNormParams& p, int N, bool backward) {
     return at % 16 == 0 && strides % N == 0 && p.d % N == 0 && (p.interleaved ? 2 : 1) * p.P % N == 0;
 }
 
-// Blocks along the tokens of the backward pass: what they sum is joined, so no more than run at once.
-int64_t backward_blocks(int64_t T, int sms) { return min64(T, 4 * (int64_t)sms); }
+// Blocks along the tokens: no more than run at once; what those of the backward pass sum is joined.
+constexpr int kForwardBlocks = 2, kBackwardBlocks = 3;      // per SM
+int64_t backward_blocks(int64_t T, int sms) { return min64(T, kBackwardBlocks * (int64_t)sms); }
 
 QkPlan plan_of(const QkNormParams& p, int N, int sms, bool backward) {
     QkPlan plan{};
     plan.heads = p.H[0] + p.H[1];
     plan.pair_units = p.interleaved && N > 1 ? 2 * p.P / N : p.P / N;
     plan.units = plan.pair_units + (p.d - 2 * p.P) / N;
-    plan.G = 1;
-    while (plan.G < plan.units && plan.G < 32) plan.G *= 2;
-    // as few blocks for a token's heads as there can be, with the heads spread evenly over them
-    const int64_t most = kQkThreads / plan.G, parts = ceil_div(plan.heads, most);
-    plan.share = (int)ceil_div(plan.heads, parts);
+    while ((1 << plan.log_G) < plan.units && plan.log_G < 5) ++plan.log_G;
+    // a token's heads over as many blocks as fill them best (each makes the table once), evenly
+    const int64_t most = kQkThreads >> plan.log_G, fewest = ceil_div(plan.heads, most);
+    int64_t best = -1;
+    for (int64_t parts = fewest; parts <= fewest + 3 && parts <= plan.heads; ++parts) {
+        const int64_t share = ceil_div(plan.heads, parts), used = most / share * plan.heads * 100 / (parts * most);
+        if (used > best + 10) {
+            best = used;
+            plan.share = (int)share;
+        }
+    }
     plan.tokens = (int)(most / plan.share);
     const int64_t table = kTable / ((int64_t)sizeof(float2) * p.P);
-    int64_t tile = min64(table, 8 * plan.tokens) / plan.tokens * plan.tokens;
+    int64_t tile = min64(table, (int64_t)8 * plan.tokens) / plan.tokens * plan.tokens;
     if (tile < plan.tokens) tile = plan.tokens;
-    if (backward) {
-        plan.span = ceil_div(p.T, backward_blocks(p.T, sms));
-    } else {
-        // but no fewer blocks than SMs
-        plan.span = min64(tile, ceil_div(p.T * ceil_div(plan.heads, plan.share), 2 * sms));
-        if (plan.span < 1) plan.span = 1;
-    }
-    plan.tile = (int)min64(tile, plan.span);
+    // no more blocks than run at once, and no fewer than that for long tiles
+    const int64_t most_blocks = backward ? backward_blocks(p.T, sms) : kForwardBlocks * (int64_t)sms;
+    tile = min64(tile, ceil_div(ceil_div(p.T, most_blocks), plan.tokens) * plan.tokens);
+    plan.blocks = (int)min64(most_blocks, ceil_div(p.T, tile));
+    plan.tile = (int)tile;
     return plan;
 }
 
-template <typename T, int N, bool Interleaved, int KU, bool Backward>
-cudaError_t launch(const QkNormParams& p, const QkPlan& plan, cudaStream_t s) {
-    size_t smem = sizeof(float2) * (size_t)plan.tile * p.P;
+template <typename T, int N, bool Interleaved, int KU, bool Backward, bool Full>
+cudaError_t launch(const QkNormParams& p, const QkPlan& plan, cudaStream_t s, int64_t* sums) {
+    const int threads = ((plan.share * plan.tokens << plan.log_G) + 31) / 32 * 32;
+    size_t smem = 2 * sizeof(float2) * (size_t)plan.tile * p.P;
+    if (copied<T, N, KU, Backward>) smem += (size_t)kRing * 16 * threads * KU * (Interleaved && N > 1 ? 1 : 2);
     if (Backward) {
         const size_t red = sizeof(float) * (size_t)plan.tokens * plan.share * p.d;
         if (red > smem) smem = red;
     }
-    auto kernel = qk_norm_rotary_kernel<T, N, Interleaved, KU, Backward>;
+    auto kernel = qk_norm_rotary_kernel<T, N, Interleaved, KU, Backward, Full>;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    const dim3 grid((unsigned)ceil_div(p.T, plan.span), (unsigned)ceil_div(plan.heads, plan.share));
-    const int threads = (plan.G * plan.share * plan.tokens + 31) / 32 * 32;
+    const dim3 grid((unsigned)plan.blocks, (unsigned)ceil_div(plan.heads, plan.share));
     kernel<<<grid, threads, smem, s>>>(p, plan);
+    if (sums) *sums = (int64_t)grid.x * (p.per_head ? 1 : grid.y);
     return cudaGetLastError();
 }
 
 template <typename T, int N, bool Interleaved, bool Backward>
-cudaError_t units(const QkNormParams& p, int sms, cudaStream_t s) {
+cudaError_t units(const QkNormParams& p, int sms, cudaStream_t s, int64_t* sums) {
     const QkPlan plan = plan_of(p, N, sms, Backward);
-    const int64_t per = ceil_div(plan.units, plan.G);
+    const int64_t per = ceil_div(plan.units, 1 << plan.log_G);
     // up to 32 / N units a lane: rows of LA_MAX_ROTARY_D that turn few pairs
     static_assert(LA_MAX_ROTARY_D == 32 * 32, "a lane's units");
     constexpr int kSome = N == 1 ? 4 : 2;
-    if (per <= 1) return launch<T, N, Interleaved, 1, Backward>(p, plan, s);
-    if (per <= kSome) return launch<T, N, Interleaved, kSome, Backward>(p, plan, s);
-    return launch<T, N, Interleaved, 32 / N, Backward>(p, plan, s);
+    if (N > 1 && per <= 1 && plan.pair_units == 1 << plan.log_G && plan.units == plan.pair_units)
+        return launch<T, N, Interleaved, 1, Backward, (N > 1)>(p, plan, s, sums);
+    if (per <= 1) return launch<T, N, Interleaved, 1, Backward, false>(p, plan, s, sums);
+    if (per <= kSome) return launch<T, N, Interleaved, kSome, Backward, false>(p, plan, s, sums);
+    return launch<T, N, Interleaved, 32 / N, Backward, false>(p, plan, s, sums);
 }
 
 template <typename T, bool Backward>
-cudaError_t dispatch(const QkNormParams& p, cudaStream_t s) {
+cudaError_t dispatch(const QkNormParams& p, cudaStream_t s, int64_t* sums = nullptr) {   // sums: of the blocks, for each weight
     constexpr int N = 16 / sizeof(T);
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     if (whole_vectors(p, N, Backward))
-        return p.interleaved ? units<T, N, true, Backward>(p, sms, s) : units<T, N, false, Backward>(p, sms, s);
-    return p.interleaved ? units<T, 1, true, Backward>(p, sms, s) : units<T, 1, false, Backward>(p, sms, s);
+        return p.interleaved ? units<T, N, true, Backward>(p, sms, s, sums) : units<T, N, false, Backward>(p, sms, s, sums);
+    return p.interleaved ? units<T, 1, true, Backward>(p, sms, s, sums) : units<T, 1, false, Backward>(p, sms, s, sums);
 }
 
 }  // namespace
@@ -330,21 +451,21 @@ cudaError_t qk_norm_rotary(const QkNormParams& p, int dtype, cudaStream_t s) {
 size_t qk_norm_rotary_backward_workspace_bytes(int64_t T, int H, int d) {
     const int sms = sm_count();
     if (sms <= 0) return 0;
-    return align_up(sizeof(float) * (size_t)(backward_blocks(T < 1 ? 1 : T, sms)) * H * d, kAlign);
+    // (shared weights: two rows for each block, and no more blocks for a token than heads)
+    return align_up(sizeof(float) * (size_t)(backward_blocks(T < 1 ? 1 : T, sms)) * 2 * H * d, kAlign);
 }
 
 cudaError_t qk_norm_rotary_backward(const QkNormParams& p, int dtype, cudaStream_t s) {
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     cudaError_t e = cudaSuccess;
-    int64_t blocks = 0;
+    int64_t sums = 0;
     if (p.T > 0) {
-        e = dtype == LA_F32 ? dispatch<float, true>(p, s) : dispatch<__nv_bfloat16, true>(p, s);
-        blocks = ceil_div(p.T, ceil_div(p.T, backward_blocks(p.T, sms)));
+        e = dtype == LA_F32 ? dispatch<float, true>(p, s, &sums) : dispatch<__nv_bfloat16, true>(p, s, &sums);
     }
     if (e != cudaSuccess || !p.partial) return e;
     const dim3 grid((unsigned)ceil_div(p.d, kJoinColumns), p.per_head ? p.H[0] + p.H[1] : p.H[1] ? 2 : 1);
-    qk_join_kernel<<<grid, dim3(kJoinColumns, kJoinRows), 0, s>>>(p, (int)blocks);
+    qk_join_kernel<<<grid, dim3(kJoinColumns, kJoinRows), 0, s>>>(p, (int)sums);
     return cudaGetLastError();
 }
 

@@ -266,6 +266,24 @@ def test_values_that_are_not_finite_stay_where_they_belong(la, which, dtype, bad
         assert torch.equal(x, y) if r is None else torch.equal(x[~r], y[~r])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_neighbours_full_of_nan(la, d):
+    """Sequences of many chunks that end in the middle of one, between others that hold nothing finite."""
+    H, n = 150, [700, 40, 3, 900, 61]
+    T = sum(n)
+    g = torch.Generator(device="cuda").manual_seed(24)
+    x = {k: torch.randn(T, H, d, generator=g, device="cuda", dtype=torch.bfloat16) for k in ("q", "k", "v", "do")}
+    ld = torch.full((H,), -0.02, device="cuda")
+    cu = torch.tensor(np.cumsum([0] + n), dtype=torch.int32).cuda()
+    alive = torch.cat([torch.full((m,), i % 2 == 0) for i, m in enumerate(n)]).cuda()
+    y = {k: torch.where(alive[:, None, None], v, torch.full_like(v, float("nan"))) for k, v in x.items()}
+    for _ in range(3):
+        a, b = (la.la_decay_attention(z["q"], z["k"], z["v"], ld, cu_seqlens=cu, return_state=True) for z in (x, y))
+        assert torch.equal(a[0][alive], b[0][alive]) and torch.equal(a[1][::2], b[1][::2])
+        a, b = (la.la_decay_attention_backward(z["q"], z["k"], z["v"], z["do"], ld, cu_seqlens=cu) for z in (x, y))
+        assert all(torch.equal(u[alive], w[alive]) for u, w in zip(a, b))
+
+
 def test_large_values_beside_small_ones(la):
     """Tokens whose values differ by many powers of two: the small ones' outputs keep their digits."""
     c = _case([300], 2, 64, 64, "bf16", seed=12)
