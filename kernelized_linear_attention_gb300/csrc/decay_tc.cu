@@ -8,9 +8,10 @@
 //     S = g^n S + (w y)^T z           w_j = g^(n-1-j)
 //
 // Every product is tcgen05.mma kind::f16 on bf16 with fp32 accumulators in tensor memory.  What is computed here enters
-// a product as two bf16, the rounded value and what it leaves (P, S, w y: off by 2^-18 of the value together), in
-// the state sums as three (2^-26): the sums are the states that calls return.  Values keep bf16's range, so nothing is
-// scaled or clamped.  Rows of operands lie in shared memory as in tc_ptx.cuh ([rows][64] blocks with the 128-byte
+// a product rounded: P and w y to bf16 (2^-8; P of a segment of one chunk in two parts), like the outputs that come of
+// them; the state as a bf16 and what that leaves (2^-16); the weighted y of the state sums, which calls return, in
+// three parts (2^-24).  Values keep bf16's range, so nothing is scaled or clamped.  Rows of operands lie in shared
+// memory as in tc_ptx.cuh ([rows][64] blocks with the 128-byte
 // swizzle); D is 64 or 128, the channels of both sides rounded up (missing ones are filled with zeros by TMA).
 //
 // P z with a masked P of 0 would spread a z that is not finite to tokens that do not see it.  Such values are found
@@ -358,7 +359,8 @@ __global__ void __launch_bounds__(kStatesThreads, 1)
 // Warp 0 loads; warps 1, 2 and 3 issue products (scores and P z; the state's update; x S: one warp for all was what the
 // others waited for, a hundred cycles and more for each of its waits and commits); warps 4 .. 11 look z over and turn
 // scores into P; 12 .. 19 weight y (in its place, once the scores have read it) and make an operand of the state;
-// 20 .. 27 write the outputs.
+// 20 .. 27 write the outputs.  Every barrier's waits are consecutive, or behind something that implies the phase before,
+// and no phase can end twice before a waiter has seen it: a wait tells phases by parity alone.
 constexpr int kPassThreads = 896;
 template <int D> struct PassShape {
     static constexpr int blocks = D / 64;
@@ -367,7 +369,7 @@ template <int D> struct PassShape {
     // operands of the state; D = 64: its two parts side by side, one product of twice the width
     static constexpr int states = D == 64 ? 2 : 1, width = 128;
     static constexpr int ring = 4;                        // chunks from the look at z to the outputs, at most
-    // tensor memory: the state, scores (then P: for each 16 tokens eight columns), x S, P z
+    // tensor memory: the state, scores (then P: for each 16 tokens eight columns, and eight of second parts), x S, P z
     static constexpr uint32_t state = 0, score = D, read = score + 128 * scores, out = read + width;
 };
 template <int D> struct __align__(1024) PassSmem {
@@ -405,6 +407,10 @@ __global__ void __launch_bounds__(kPassThreads, 1)
     const int chunks = (g.end - g.start + kC - 1) / kC;
     constexpr bool reverse = Reverse;
     auto token = [&](int it) { return g.start + (reverse ? chunks - 1 - it : it) * kC; };
+    // P in two parts where the segment is one chunk: the outputs are then as exact as in 32 bits, for little.  In every
+    // chunk the second part takes the warps that make P a fifth longer, and all wait for them (65536 x 16 x 64: 218 us
+    // instead of 183), for 0.0021 of the outputs' norm instead of 0.0023, with 0.0017 their own rounding.
+    const bool two = chunks == 1;
     if (threadIdx.x == 0) {
         init_all(s.xy_full, F::stages, 1);
         init_all(s.xy_empty, F::stages, 2);
@@ -488,8 +494,9 @@ __global__ void __launch_bounds__(kPassThreads, 1)
             constexpr uint32_t id = idesc_bf16(128, D, false, true);
             const uint64_t dz = sdesc_sw128(smem_u32(s.z[sz]), kTile, 1024);
 #pragma unroll 4
-            for (int j = 0; j < kC / 16; ++j)
-                mma_ts_w(tm + F::out, tm + F::score + 128 * b + 16 * j, sdesc_add(dz, 2048 * j), id, j > 0 ? 1u : 0u);
+            for (int j = 0; j < (two ? 2 : 1) * kC / 16; ++j)
+                mma_ts_w(tm + F::out, tm + F::score + 128 * b + (two ? 8 : 16) * j, sdesc_add(dz, 2048 * (two ? j >> 1 : j)), id,
+                         j > 0 ? 1u : 0u);
             mma_commit_w(&s.o_full);
             mma_commit_w(&s.z_empty[sz]);
             // (the warps that weight y have seen this buffer's scores done, too)
@@ -573,49 +580,58 @@ __global__ void __launch_bounds__(kPassThreads, 1)
             const uint32_t at = lanes + F::score + 128 * b;
 #pragma unroll 1
             for (int jb = 2 * half; jb < 2 * half + 2; ++jb) {
-                uint32_t o[16];
+                uint32_t v[32];
                 if (reverse ? jb < q : jb > q) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) o[j] = 0;
+                    for (int j = 0; j < 32; ++j) v[j] = 0;
                 } else {
-                    uint32_t v[32];
                     tmem_ld32(at + 32 * jb, v);
                     tmem_ld_wait();
                     arrived(v);
                     if (jb != q) {
                         // decay to the block's nearest token, times that inside the block
                         const uint64_t f = f32x2_splat(c.scale * s.pw[reverse ? 32 * jb - row : row - 32 * jb - 31]);
-                        const float4* const in = reinterpret_cast<const float4*>(s.in_block);
+                        const ulonglong2* const in = reinterpret_cast<const ulonglong2*>(s.in_block);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            const float4 w = in[j];
-                            o[2 * j] = f32x2_to_bf16x2(f32x2_mul(f32x2_mul(f32x2_of(v[4 * j], v[4 * j + 1]), f),
-                                                                 f32x2_of(__float_as_uint(w.x), __float_as_uint(w.y))));
-                            o[2 * j + 1] = f32x2_to_bf16x2(f32x2_mul(f32x2_mul(f32x2_of(v[4 * j + 2], v[4 * j + 3]), f),
-                                                                     f32x2_of(__float_as_uint(w.z), __float_as_uint(w.w))));
+                            const ulonglong2 w = in[j];
+                            const uint64_t e0 = f32x2_mul(f32x2_mul(f32x2_of(v[4 * j], v[4 * j + 1]), f), w.x);
+                            const uint64_t e1 = f32x2_mul(f32x2_mul(f32x2_of(v[4 * j + 2], v[4 * j + 3]), f), w.y);
+                            v[4 * j] = (uint32_t)e0;
+                            v[4 * j + 1] = (uint32_t)(e0 >> 32);
+                            v[4 * j + 2] = (uint32_t)e1;
+                            v[4 * j + 3] = (uint32_t)(e1 >> 32);
                         }
                     } else {
                         const float* const w = s.pw + kC + 4 + (reverse ? -lane : lane);   // (masked ones lie in front)
 #pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            const float e0 = w[reverse ? j : -j] * __uint_as_float(v[j]);
-                            const float e1 = w[reverse ? j + 1 : -j - 1] * __uint_as_float(v[j + 1]);
-                            o[j / 2] = pack_bf16x2((reverse ? j >= lane : j <= lane) ? e0 : 0.f,
-                                                   (reverse ? j + 1 >= lane : j + 1 <= lane) ? e1 : 0.f);
+                        for (int j = 0; j < 32; ++j) {
+                            const float e = w[reverse ? j : -j] * __uint_as_float(v[j]);
+                            v[j] = (reverse ? j >= lane : j <= lane) ? __float_as_uint(e) : 0u;
                         }
                     }
                     if (reverse && 32 * jb + 32 > n) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const int left = n - 32 * jb - 2 * j;       // of this pair and on, tokens that there are
-                            o[j] &= left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
-                        }
+                        for (int j = 0; j < 32; ++j)
+                            if (32 * jb + j >= n) v[j] = 0;
                     }
                 }
-                const uint32_t (&lo)[8] = *reinterpret_cast<const uint32_t (*)[8]>(o);
-                const uint32_t (&hi)[8] = *reinterpret_cast<const uint32_t (*)[8]>(o + 8);
-                tmem_st8(at + 32 * jb, lo);
-                tmem_st8(at + 32 * jb + 16, hi);
+                // for each 16 tokens eight columns, and eight of what these leave
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t o[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        o[j] = f32x2_to_bf16x2(f32x2_of(v[16 * u + 2 * j], v[16 * u + 2 * j + 1]));
+                    tmem_st8(at + 32 * jb + 16 * u, o);
+                    if (two) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            o[j] = f32x2_to_bf16x2(f32x2_fma(pair_of(o[j]), f32x2_splat(-1.f),
+                                                             f32x2_of(v[16 * u + 2 * j], v[16 * u + 2 * j + 1])));
+                        tmem_st8(at + 32 * jb + 16 * u + 8, o);
+                    }
+                }
             }
             tmem_st_wait();
             tc_fence_before();
@@ -646,10 +662,10 @@ __global__ void __launch_bounds__(kPassThreads, 1)
             const int st = it % F::stages, sz = it % F::z_stages, n = min(kC, g.end - token(it));
             const uint32_t zpar = (it / F::z_stages) & 1;
             const bool last = it + 1 == chunks, has = it > 0 || enter;
+            // the scores have read y (in the last chunk too: conv_full must not get a phase ahead of the scores' warp)
+            ok = wait_w(&s.a_full[it % F::scores], (it / F::scores) & 1);
+            if (!ok) break;
             if (!last) {
-                // the scores have read y
-                ok = wait_w(&s.a_full[it % F::scores], (it / F::scores) & 1);
-                if (!ok) break;
                 const uint64_t w = f32x2_splat(row < n ? (reverse ? c.scale * s.pw[row + 1] : s.pw[n - 1 - row]) : 0.f);
 #pragma unroll
                 for (int k = 0; k < F::blocks; ++k) {
