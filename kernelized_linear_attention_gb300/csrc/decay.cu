@@ -14,6 +14,16 @@ namespace la {
 
 namespace {
 
+// State passes and product passes of one call that start together.
+struct StatesList {
+    DecayStates p[2];
+    bool ends[2];                // of the join: something leaves the sequences, and was summed with the segments
+};
+struct PassList {
+    DecayPass p[3];
+    int first[3];                // of its blocks in z
+};
+
 // ---------------------------------------------------------------------------
 // Work table of packed sequences
 // ---------------------------------------------------------------------------
@@ -108,11 +118,13 @@ constexpr int kJoinAhead = 8;      // segments whose loads are on their way toge
 
 template <int N>
 __global__ void __launch_bounds__(kJoinThreads) decay_join_kernel(const __grid_constant__ DecayCall c,
-                                                                  const __grid_constant__ DecayStates p, bool ends) {
+                                                                  const __grid_constant__ StatesList list, int blocks) {
     using V = Vec<float, N>;
     if (decay_malformed(c)) return;
-    const int s = blockIdx.x, h = blockIdx.y, n = c.dk * c.dv;
-    const int e = (blockIdx.z * kJoinThreads + threadIdx.x) * N;
+    const int s = blockIdx.x, h = blockIdx.y, n = c.dk * c.dv, which = blockIdx.z / blocks;
+    const DecayStates& p = list.p[which];
+    const bool ends = list.ends[which];
+    const int e = ((blockIdx.z - which * blocks) * kJoinThreads + threadIdx.x) * N;
     if (e >= n) return;
     const int64_t edge = ((int64_t)s * c.H + h) * n + e;
     V acc;
@@ -166,6 +178,10 @@ constexpr int kSimtThreads = 256;
 constexpr int kRows = 32;          // tokens of a chunk
 constexpr int kCols = 64;          // columns of a block
 
+__device__ __forceinline__ void copy4(float* to, const float* from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_u32(to)), "l"(from) : "memory");
+}
+
 // Eight neighbouring values of a row, nothing from `valid` on; `vec`: the eight start on 16 bytes.
 template <typename T>
 __device__ __forceinline__ void load8(float (&f)[8], const T* p, int valid, bool vec) {
@@ -191,11 +207,13 @@ __device__ __forceinline__ void store8(float* to, const float (&f)[8]) {
 // Sums of one segment (or, final, what leaves each sequence): blocks of 64 x 64 of [dk][dv], 4 x 4 a thread.
 template <typename T>
 __global__ void __launch_bounds__(kSimtThreads) decay_states_kernel(const __grid_constant__ DecayCall c,
-                                                                    const __grid_constant__ DecayStates p, DecayWhich which,
-                                                                    bool vec) {
+                                                                    const __grid_constant__ StatesList list,
+                                                                    DecayWhich of_all, int blocks, bool vec) {
     __shared__ __align__(16) float ys[kRows][kCols], zs[kRows][kCols];
-    const int h = blockIdx.y, nb = (c.dv + kCols - 1) / kCols;
-    const int a0 = blockIdx.z / nb * kCols, b0 = blockIdx.z % nb * kCols;
+    const int h = blockIdx.y, nb = (c.dv + kCols - 1) / kCols, item = blockIdx.z / blocks, block = blockIdx.z - item * blocks;
+    const int a0 = block / nb * kCols, b0 = block % nb * kCols;
+    const DecayStates& p = list.p[item];
+    const DecayWhich which = of_all == kEnds ? kEnds : list.ends[item] ? kAll : kInner;
     DecaySegment g;
     bool any = true;
     if (decay_malformed(c)) return;
@@ -247,20 +265,31 @@ __global__ void __launch_bounds__(kSimtThreads) decay_states_kernel(const __grid
     if (end) to = p.edge_out + ((int64_t)(which == kEnds ? (int)blockIdx.x : g.seq) * c.H + h) * n;
     else to = c.states[p.reverse] + ((int64_t)(decay_slot(g) - (p.reverse ? 1 : 0)) * c.H + h) * n;
     const float keep = any ? decay_power(base, g.end - g.start) : 1.f;
+    const bool whole = c.dv % 4 == 0 && reinterpret_cast<uintptr_t>(to) % 16 == 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) {
+        const int a = a0 + ty * 4 + i, b = b0 + tx * 4;
+        if (a >= c.dk || b >= c.dv) continue;
+        const int64_t at = (int64_t)a * c.dv + b;
+        if (enter) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int a = a0 + ty * 4 + i, b = b0 + tx * 4 + j;
-            if (a >= c.dk || b >= c.dv) continue;
-            const int64_t at = (int64_t)a * c.dv + b;
-            to[at] = enter ? fmaf(keep, enter[at], acc[i][j]) : acc[i][j];
+            for (int j = 0; j < 4; ++j)
+                if (b + j < c.dv) acc[i][j] = fmaf(keep, enter[at + j], acc[i][j]);
         }
+        if (whole) {
+            *reinterpret_cast<float4*>(to + at) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (b + j < c.dv) to[at + j] = acc[i][j];
+        }
+    }
 }
 
+constexpr int kStateRow = kCols + 4;         // a row of the state: eight rows of a column in as many groups of banks
 __host__ __device__ inline int simt_stride(int ds) { return (ds + 31) / 32 * 32 + 4; }   // of rows: no bank twice
 __host__ __device__ inline size_t simt_smem(int ds) {
-    return sizeof(float) * ((size_t)(ds + 3) / 4 * 4 * kCols + 2 * (size_t)kRows * simt_stride(ds) + kRows * kCols +
+    return sizeof(float) * ((size_t)(ds + 3) / 4 * 4 * kStateRow + 2 * (size_t)kRows * simt_stride(ds) + kRows * kCols +
                             kRows * (kRows + 4) + kRows + 1);
 }
 
@@ -268,11 +297,14 @@ __host__ __device__ inline size_t simt_smem(int ds) {
 // state) or two (of the scores).
 template <typename T>
 __global__ void __launch_bounds__(kSimtThreads) decay_pass_kernel(const __grid_constant__ DecayCall c,
-                                                                  const __grid_constant__ DecayPass p, bool vec) {
+                                                                  const __grid_constant__ PassList list, bool vec) {
     extern __shared__ __align__(16) float smem[];
-    const int ds = p.ds, ds4 = (ds + 3) / 4 * 4, ld = simt_stride(ds), h = blockIdx.y, c0 = blockIdx.z * kCols;
-    float* S = smem;                          // [ds4][64]
-    float* xs = S + ds4 * kCols;              // [32][ld]
+    const int item = ((int)blockIdx.z >= list.first[1]) + ((int)blockIdx.z >= list.first[2]);
+    const DecayPass& p = list.p[item];
+    const int ds = p.ds, ds4 = (ds + 3) / 4 * 4, ld = simt_stride(ds), h = blockIdx.y;
+    const int c0 = ((int)blockIdx.z - list.first[item]) * kCols;
+    float* S = smem;                          // [ds4][68]
+    float* xs = S + ds4 * kStateRow;          // [32][ld]
     float* ys = xs + kRows * ld;              // [32][ld]
     float* zs = ys + kRows * ld;              // [32][64]
     float* P = zs + kRows * kCols;            // [32][36]
@@ -282,13 +314,19 @@ __global__ void __launch_bounds__(kSimtThreads) decay_pass_kernel(const __grid_c
     const DecayBase base = decay_base(c.log_decay[h]);
     if (threadIdx.x <= kRows) pw[threadIdx.x] = decay_power(base, threadIdx.x);
     const float* enter = decay_entering(c, g, h, p.reverse, p.edge);
-    for (int i = threadIdx.x; i < ds4 * kCols; i += kSimtThreads) {
-        const int a = p.transposed ? i % ds4 : i / kCols, b = p.transposed ? i / ds4 : i % kCols;
-        float v = 0.f;
-        if (enter && a < ds && c0 + b < p.dz)
-            v = enter[p.transposed ? (int64_t)(c0 + b) * ds + a : (int64_t)a * p.dz + c0 + b];
-        S[a * kCols + b] = v;
+    // The state, on its way while the first scores are made.  A warp of a transposed one has four columns of eight rows:
+    // whole sectors of memory, and a bank for each lane.
+    for (int i = threadIdx.x; i < (ds4 + 7) / 8 * 8 * kCols; i += kSimtThreads) {
+        const int tile = i / 32, lane = i % 32;
+        const int a = p.transposed ? tile / 16 * 8 + lane % 8 : i / kCols;
+        const int b = p.transposed ? tile % 16 * 4 + lane / 8 : i % kCols;
+        if (a >= ds4) continue;
+        const bool in = enter && a < ds && c0 + b < p.dz;
+        const float* from = p.transposed ? enter + (int64_t)(c0 + b) * ds + a : enter + (int64_t)a * p.dz + c0 + b;
+        if (in) copy4(S + a * kStateRow + b, from);
+        else S[a * kStateRow + b] = 0.f;
     }
+    copies_done();
     const int r0 = threadIdx.x / 16, q0 = threadIdx.x % 16, row = threadIdx.x / 8, col = threadIdx.x % 8 * 8;
     const int chunks = (g.end - g.start + kRows - 1) / kRows;
     for (int k = 0; k < chunks; ++k) {
@@ -332,6 +370,7 @@ __global__ void __launch_bounds__(kSimtThreads) decay_pass_kernel(const __grid_c
                     P[ri * (kRows + 4) + rj] = apart >= 0 ? c.scale * pw[apart] * acc[i][j] : 0.f;
                 }
         }
+        wait_copies<0>();
         __syncthreads();
         {
             float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -341,7 +380,7 @@ __global__ void __launch_bounds__(kSimtThreads) decay_pass_kernel(const __grid_c
                 for (int i = 0; i < 2; ++i) x[i] = *reinterpret_cast<const float4*>(xs + (r0 + 16 * i) * ld + a);
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    const float4 s = *reinterpret_cast<const float4*>(S + (a + u) * kCols + q0 * 4);
+                    const float4 s = *reinterpret_cast<const float4*>(S + (a + u) * kStateRow + q0 * 4);
                     const float sv[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -388,7 +427,7 @@ __global__ void __launch_bounds__(kSimtThreads) decay_pass_kernel(const __grid_c
             float acc[4][4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float4 s = *reinterpret_cast<const float4*>(S + (a + i) * kCols + q0 * 4);
+                const float4 s = *reinterpret_cast<const float4*>(S + (a + i) * kStateRow + q0 * 4);
                 acc[i][0] = keep * s.x;
                 acc[i][1] = keep * s.y;
                 acc[i][2] = keep * s.z;
@@ -406,7 +445,7 @@ __global__ void __launch_bounds__(kSimtThreads) decay_pass_kernel(const __grid_c
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<float4*>(S + (a + i) * kCols + q0 * 4) =
+                *reinterpret_cast<float4*>(S + (a + i) * kStateRow + q0 * 4) =
                     make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
         }
         __syncthreads();
@@ -516,13 +555,14 @@ constexpr int64_t kLongest = 1 << 20;      // tokens of a segment: exact in fp32
 
 // Tokens of a segment.  Tensor cores: whole chunks of 128, one block per SM.  Equal sequences are cut so that the waves
 // of blocks times a segment's chunks, and two for a block's beginning and end, are fewest; packed ones, whose lengths
-// are not known here, into three blocks' worth per SM.  CUDA cores: four blocks per SM, of chunks of 32.
+// are not known here, into three blocks' worth per SM.  CUDA cores: four blocks per SM, of chunks of 32 (blocks of a single
+// chunk then for what is short: nothing in them waits for a chunk before).
 int64_t segment_length(const DecayCall& c, bool tensor, int sms) {
     const int64_t n = c.cu_seqlens ? c.T : c.T / c.nseq;
     if (n < 1) return 128;
     if (!tensor) {
-        const int64_t L = ceil_div(ceil_div(c.T * c.H, 4 * sms), 64) * 64;
-        return min64(min64(L < 64 ? 64 : L, ceil_div(n, 64) * 64), kLongest);
+        const int64_t L = ceil_div(ceil_div(c.T * c.H * ceil_div(c.dv, kCols), 4 * sms), kRows) * kRows;
+        return min64(min64(L, ceil_div(n, kRows) * kRows), kLongest);
     }
     const int64_t chunks = ceil_div(n, 128);
     int64_t best = 1, least = INT64_MAX;
@@ -550,48 +590,91 @@ cudaError_t plan(const DecayCall& c, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-cudaError_t join(const DecayCall& c, const DecayStates& p, bool ends, cudaStream_t s) {
-    const int n = c.dk * c.dv;
-    const bool vec = n % 4 == 0 && on_16_bytes({p.edge_in, ends ? p.edge_out : nullptr});
-    const dim3 grid(c.nseq, c.H, (unsigned)ceil_div(n, kJoinThreads * (vec ? 4 : 1)));
-    if (vec) decay_join_kernel<4><<<grid, kJoinThreads, 0, s>>>(c, p, ends);
-    else decay_join_kernel<1><<<grid, kJoinThreads, 0, s>>>(c, p, ends);
+// Whether what leaves the sequences is summed with the segments: unless it takes the place of what enters them.
+bool with_segments(const DecayStates& p) { return p.edge_out && p.edge_out != p.edge_in; }
+
+cudaError_t states(const DecayCall& c, std::initializer_list<DecayStates> passes, int dtype, bool ends_alone,
+                   cudaStream_t s) {
+    StatesList simt{};
+    int n = 0;
+    bool vec = true;
+    for (const DecayStates& p : passes) {
+        if (!ends_alone && c.slots == 0 && !with_segments(p)) continue;
+        if (decay_tc_fits(c, dtype) && on_16_bytes({p.y, p.z})) {
+            const cudaError_t e = decay_tc_states(c, p, ends_alone ? kEnds : with_segments(p) ? kAll : kInner, s);
+            if (e != cudaSuccess) return e;
+            continue;
+        }
+        vec = vec && vector_rows(c, dtype, {p.y, p.z});
+        simt.p[n] = p;
+        simt.ends[n++] = with_segments(p);
+    }
+    if (n == 0) return cudaSuccess;
+    const int blocks = (int)(ceil_div(c.dk, kCols) * ceil_div(c.dv, kCols));
+    const dim3 grid(ends_alone ? c.nseq : c.segments, c.H, (unsigned)(n * blocks));
+    const DecayWhich which = ends_alone ? kEnds : kAll;
+    if (dtype == LA_F32) decay_states_kernel<float><<<grid, kSimtThreads, 0, s>>>(c, simt, which, blocks, vec);
+    else decay_states_kernel<__nv_bfloat16><<<grid, kSimtThreads, 0, s>>>(c, simt, which, blocks, vec);
     return cudaGetLastError();
 }
 
-cudaError_t states(const DecayCall& c, const DecayStates& p, int dtype, DecayWhich which, cudaStream_t s) {
-    if (decay_tc_fits(c, dtype) && on_16_bytes({p.y, p.z})) return decay_tc_states(c, p, which, s);
-    const dim3 grid(which == kEnds ? c.nseq : c.segments, c.H, (unsigned)(ceil_div(c.dk, kCols) * ceil_div(c.dv, kCols)));
-    const bool vec = vector_rows(c, dtype, {p.y, p.z});
-    if (dtype == LA_F32) decay_states_kernel<float><<<grid, kSimtThreads, 0, s>>>(c, p, which, vec);
-    else decay_states_kernel<__nv_bfloat16><<<grid, kSimtThreads, 0, s>>>(c, p, which, vec);
+cudaError_t join(const DecayCall& c, std::initializer_list<DecayStates> passes, cudaStream_t s) {
+    const int n = c.dk * c.dv;
+    StatesList list{};
+    int items = 0;
+    bool vec = n % 4 == 0;
+    for (const DecayStates& p : passes) {
+        list.p[items] = p;
+        list.ends[items++] = with_segments(p);
+        vec = vec && on_16_bytes({p.edge_in, with_segments(p) ? p.edge_out : nullptr});
+    }
+    const int blocks = (int)ceil_div(n, kJoinThreads * (vec ? 4 : 1));
+    const dim3 grid(c.nseq, c.H, (unsigned)(items * blocks));
+    if (vec) decay_join_kernel<4><<<grid, kJoinThreads, 0, s>>>(c, list, blocks);
+    else decay_join_kernel<1><<<grid, kJoinThreads, 0, s>>>(c, list, blocks);
     return cudaGetLastError();
 }
 
 // What enters every segment, and what leaves every sequence unless that overwrites what enters it (nothing to do where
 // every sequence is one segment and nothing is to leave).
-cudaError_t enter(const DecayCall& c, const DecayStates& p, int dtype, cudaStream_t s) {
-    const bool ends = p.edge_out && p.edge_out != p.edge_in;
+cudaError_t enter(const DecayCall& c, std::initializer_list<DecayStates> passes, int dtype, cudaStream_t s) {
+    bool ends = false;
+    for (const DecayStates& p : passes) ends = ends || with_segments(p);
     if (c.slots == 0 && !ends) return cudaSuccess;
     cudaError_t e = cudaSuccess;
-    if (c.T > 0) e = states(c, p, dtype, ends ? kAll : kInner, s);
-    return e != cudaSuccess ? e : join(c, p, ends, s);
+    if (c.T > 0) e = states(c, passes, dtype, false, s);
+    return e != cudaSuccess ? e : join(c, passes, s);
 }
 // What leaves every sequence, where that takes the place of what enters it: once nothing reads it any more.
 cudaError_t leave(const DecayCall& c, const DecayStates& p, int dtype, cudaStream_t s) {
-    return p.edge_out && p.edge_out == p.edge_in ? states(c, p, dtype, kEnds, s) : cudaSuccess;
+    return p.edge_out && p.edge_out == p.edge_in ? states(c, {p}, dtype, true, s) : cudaSuccess;
 }
 
-cudaError_t pass(const DecayCall& c, const DecayPass& p, int dtype, cudaStream_t s) {
+cudaError_t products(const DecayCall& c, std::initializer_list<DecayPass> passes, int dtype, cudaStream_t s) {
     if (c.T == 0) return cudaSuccess;
-    if (decay_tc_fits(c, dtype) && on_16_bytes({p.x, p.y, p.z, p.out})) return decay_tc_pass(c, p, s);
-    const dim3 grid(c.segments, c.H, (unsigned)ceil_div(p.dz, kCols));
-    const size_t smem = simt_smem(p.ds);
-    const bool vec = vector_rows(c, dtype, {p.x, p.y, p.z});
+    PassList simt{};
+    int n = 0, blocks = 0, widest = 0;
+    bool vec = true;
+    for (const DecayPass& p : passes) {
+        if (decay_tc_fits(c, dtype) && on_16_bytes({p.x, p.y, p.z, p.out})) {
+            const cudaError_t e = decay_tc_pass(c, p, s);
+            if (e != cudaSuccess) return e;
+            continue;
+        }
+        vec = vec && vector_rows(c, dtype, {p.x, p.y, p.z});
+        simt.p[n] = p;
+        simt.first[n++] = blocks;
+        blocks += (int)ceil_div(p.dz, kCols);
+        widest = p.ds > widest ? p.ds : widest;
+    }
+    if (n == 0) return cudaSuccess;
+    for (; n < 3; ++n) simt.first[n] = blocks;
+    const dim3 grid(c.segments, c.H, (unsigned)blocks);
+    const size_t smem = simt_smem(widest);
     auto kernel = dtype == LA_F32 ? decay_pass_kernel<float> : decay_pass_kernel<__nv_bfloat16>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kSimtThreads, smem, s>>>(c, p, vec);
+    kernel<<<grid, kSimtThreads, smem, s>>>(c, simt, vec);
     return cudaGetLastError();
 }
 
@@ -629,8 +712,8 @@ cudaError_t decay_forward(const DecayCall& c, const void* q, const void* k, cons
     const DecayStates sums{k, v, 0, state_in, state_out};
     const DecayPass p{q, k, v, out, c.dk, c.dv, 0, 0, state_in};
     cudaError_t e = plan(c, s);
-    if (e == cudaSuccess) e = enter(c, sums, dtype, s);
-    if (e == cudaSuccess) e = pass(c, p, dtype, s);
+    if (e == cudaSuccess) e = enter(c, {sums}, dtype, s);
+    if (e == cudaSuccess) e = products(c, {p}, dtype, s);
     if (e == cudaSuccess) e = leave(c, sums, dtype, s);
     return e;
 }
@@ -642,11 +725,8 @@ cudaError_t decay_backward(const DecayCall& c, const void* q, const void* k, con
     const DecayPass pq{dout, v, k, dq, c.dv, c.dk, 0, 1, state_in}, pk{v, dout, q, dk, c.dv, c.dk, 1, 1, dstate_out},
         pv{k, q, dout, dv, c.dk, c.dv, 1, 0, dstate_out};
     cudaError_t e = plan(c, s);
-    if (e == cudaSuccess) e = enter(c, sums, dtype, s);
-    if (e == cudaSuccess) e = pass(c, pq, dtype, s);
-    if (e == cudaSuccess) e = enter(c, back, dtype, s);
-    if (e == cudaSuccess) e = pass(c, pk, dtype, s);
-    if (e == cudaSuccess) e = pass(c, pv, dtype, s);
+    if (e == cudaSuccess) e = enter(c, {sums, back}, dtype, s);
+    if (e == cudaSuccess) e = products(c, {pq, pk, pv}, dtype, s);
     if (e == cudaSuccess) e = leave(c, back, dtype, s);
     return e;
 }

@@ -34,6 +34,12 @@ __device__ int g_force_wait_timeout = 0;      // test hook: a wait that nothing 
 // ---------------------------------------------------------------------------
 // Pieces
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // Bytes to the next multiple of 1024 (as an offset, so that what lies there is known to be shared memory: through a
 // pointer that went through an integer every access is a generic one).
 __device__ __forceinline__ uint32_t to_1024(const void* p) { return (0u - smem_u32(p)) & 1023u; }
