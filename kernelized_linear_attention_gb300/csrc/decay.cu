@@ -455,30 +455,35 @@ __global__ void __launch_bounds__(kSimtThreads) decay_pass_kernel(const __grid_c
 // ---------------------------------------------------------------------------
 // One token for each of B sequences
 // ---------------------------------------------------------------------------
-constexpr int kStepThreads = 256;
-constexpr int kStepRows = 4;       // rows of the state that a thread has on their way together
+// Threads of a block, and rows of the state that a thread has on their way together (a vector's lanes are LA_MAX_DV / N
+// at most, so that a block always has a whole group of them).
+template <int N>
+constexpr int kStepThreads = N == 4 ? 128 : 256;
+template <int N>
+constexpr int kStepRows = N == 4 ? 8 : 4;
 
 // A block has one (sequence, head); lanes along dv in vectors of N, thread groups along dk.
 template <typename T, int N>
-__global__ void __launch_bounds__(kStepThreads) decay_step_kernel(const T* __restrict__ q, const T* __restrict__ k,
+__global__ void __launch_bounds__(kStepThreads<N>) decay_step_kernel(const T* __restrict__ q, const T* __restrict__ k,
                                                                   const T* __restrict__ v,
                                                                   const float* __restrict__ log_decay, int H, int dk,
                                                                   int dv, int lanes, float scale, const float* state_in,
                                                                   float* state_out, T* __restrict__ out) {
     using V = Vec<float, N>;
+    static_assert(LA_MAX_DV / N <= kStepThreads<N>, "a group of lanes for a row of the state");
     __shared__ float qs[LA_MAX_DK], ks[LA_MAX_DK];
-    __shared__ float part[kStepThreads * N];
+    __shared__ float part[kStepThreads<N> * N];
     const int64_t pair = blockIdx.x;
-    const int h = (int)(pair % H), cols = dv / N, groups = kStepThreads / lanes;
+    const int h = (int)(pair % H), cols = dv / N, groups = kStepThreads<N> / lanes;
     const int lane = threadIdx.x % lanes, group = threadIdx.x / lanes;
     const bool on = lane < cols;
     const int64_t at = pair * dk * dv + lane * N, step = (int64_t)groups * dv;
-    V held[kStepRows];
+    V held[kStepRows<N>];
 #pragma unroll
-    for (int r = 0; r < kStepRows; ++r)
+    for (int r = 0; r < kStepRows<N>; ++r)
         if (on && group + r * groups < dk) held[r] = *reinterpret_cast<const V*>(state_in + at + group * dv + r * step);
     const float g = decay_power(decay_base(log_decay[h]), 1);
-    for (int a = threadIdx.x; a < dk; a += kStepThreads) {
+    for (int a = threadIdx.x; a < dk; a += kStepThreads<N>) {
         qs[a] = (float)q[pair * dk + a];
         ks[a] = (float)k[pair * dk + a];
     }
@@ -489,14 +494,14 @@ __global__ void __launch_bounds__(kStepThreads) decay_step_kernel(const T* __res
         sum[j] = 0.f;
     }
     __syncthreads();
-    for (int a0 = group; a0 < dk; a0 += kStepRows * groups) {
+    for (int a0 = group; a0 < dk; a0 += kStepRows<N> * groups) {
         if (a0 != group) {
 #pragma unroll
-            for (int r = 0; r < kStepRows; ++r)
+            for (int r = 0; r < kStepRows<N>; ++r)
                 if (on && a0 + r * groups < dk) held[r] = *reinterpret_cast<const V*>(state_in + at + (int64_t)a0 * dv + r * step);
         }
 #pragma unroll
-        for (int r = 0; r < kStepRows; ++r) {
+        for (int r = 0; r < kStepRows<N>; ++r) {
             const int a = a0 + r * groups;
             if (!on || a >= dk) continue;
             const float kv = ks[a], qv = qs[a];
@@ -514,7 +519,7 @@ __global__ void __launch_bounds__(kStepThreads) decay_step_kernel(const T* __res
         for (int j = 0; j < N; ++j) part[(group * cols + lane) * N + j] = sum[j];
     }
     __syncthreads();
-    for (int b = threadIdx.x; b < dv; b += kStepThreads) {
+    for (int b = threadIdx.x; b < dv; b += kStepThreads<N>) {
         float o = 0.f;
         for (int i = 0; i < groups; ++i) o += part[i * dv + b];
         store_elem(out, pair * dv + b, scale * o);
@@ -531,11 +536,11 @@ cudaError_t step(const void* q, const void* k, const void* v, const float* log_d
     while (lanes < cols) lanes *= 2;
     const unsigned grid = (unsigned)B * H;
     if (vec)
-        decay_step_kernel<T, 4><<<grid, kStepThreads, 0, s>>>(
+        decay_step_kernel<T, 4><<<grid, kStepThreads<4>, 0, s>>>(
             static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), log_decay, H, dk, dv, lanes,
             scale, state_in, state_out, static_cast<T*>(out));
     else
-        decay_step_kernel<T, 1><<<grid, kStepThreads, 0, s>>>(
+        decay_step_kernel<T, 1><<<grid, kStepThreads<1>, 0, s>>>(
             static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), log_decay, H, dk, dv, lanes,
             scale, state_in, state_out, static_cast<T*>(out));
     return cudaGetLastError();

@@ -47,9 +47,11 @@ __device__ __forceinline__ Turn turn_of(const Turns& p, int j) {
     const float f = p.freq[j];
     return {turn_fraction(f), axis, (bool)isfinite(f)};
 }
-// (cos, sin) at token t; sin negated for the inverse.
-__device__ __forceinline__ float2 cos_sin(const Turns& p, const Turn& turn, int64_t t) {
-    const long long position = p.positions[t * p.naxes + turn.axis];
+// Token t's position on the pair's axis, and (cos, sin) there; sin negated for the inverse.
+__device__ __forceinline__ int position_of(const Turns& p, const Turn& turn, int64_t t) {
+    return p.positions[t * p.naxes + turn.axis];
+}
+__device__ __forceinline__ float2 cos_sin_at(const Turns& p, const Turn& turn, long long position) {
     const unsigned long long angle = turn.fraction * (unsigned long long)position;
     // the nearest quarter of a turn apart, so that fp32 rounds what is left: an eighth at most, in units of 2^-32
     const uint32_t turns = (uint32_t)(angle >> 32), quarter = (turns + (1u << 29)) >> 30;
@@ -59,6 +61,9 @@ __device__ __forceinline__ float2 cos_sin(const Turns& p, const Turn& turn, int6
     float c = __uint_as_float(__float_as_uint(quarter & 1 ? s0 : c0) ^ (quarter + 1 & 2) << 30);
     if (!turn.finite) s = c = __int_as_float(0x7fc00000);
     return make_float2(c, p.inverse ? -s : s);
+}
+__device__ __forceinline__ float2 cos_sin(const Turns& p, const Turn& turn, int64_t t) {
+    return cos_sin_at(p, turn, position_of(p, turn, t));
 }
 
 }  // namespace la

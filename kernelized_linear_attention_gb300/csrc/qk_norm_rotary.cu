@@ -37,6 +37,11 @@ struct QkPlan {
 // more instructions, 106).  The backward pass has twice the rows on their way and more registers to keep, and is faster
 // with three blocks and loads to registers (32768 x 16 x 64: 48 us and 65).
 constexpr int kRing = 4;              // rows on their way, a power of two
+// Positions that a thread of the table's has on their way together: 16384 x 20 x 128 in bf16 take 36 us with four (45 with
+// one, and each token's table made by two blocks); the backward pass has no registers for them (32768 x 16 x 64: 55 us with
+// one, 60 with four).
+template <bool Backward>
+constexpr int kPositionsAhead = Backward ? 1 : 4;
 template <typename T, int N, int KU, bool Backward>
 constexpr bool copied = !Backward && N > 1 && KU == 1 && sizeof(T) * N == 16;
 
@@ -200,10 +205,20 @@ __global__ void __launch_bounds__(kQkThreads, KU > 1 ? 1 : Backward ? 3 : 2) qk_
             for (int i = threadIdx.x; i < groups * p.P; i += blockDim.x) {
                 const int g = i / p.P, j = i - g * p.P, to = table_place<N, Interleaved>(j, apart);
                 const Turn turn = turn_of(p, j);
-                for (int e = g; e < n; e += groups) {
-                    const float2 cw = cos_sin(p, turn, now.t0 + e);
-                    fill[2 * e * p.P + to] = cw.x;
-                    fill[2 * e * p.P + to + kSinBehind<N, Interleaved>] = cw.y;
+                constexpr int kAhead = kPositionsAhead<Backward>;
+                for (int e0 = g; e0 < n; e0 += kAhead * groups) {
+                    int position[kAhead];
+#pragma unroll
+                    for (int q = 0; q < kAhead; ++q)
+                        position[q] = e0 + q * groups < n ? position_of(p, turn, now.t0 + e0 + q * groups) : 0;
+#pragma unroll
+                    for (int q = 0; q < kAhead; ++q) {
+                        const int e = e0 + q * groups;
+                        if (e >= n) break;
+                        const float2 cw = cos_sin_at(p, turn, position[q]);
+                        fill[2 * e * p.P + to] = cw.x;
+                        fill[2 * e * p.P + to + kSinBehind<N, Interleaved>] = cw.y;
+                    }
                 }
             }
             __syncthreads();
@@ -366,8 +381,9 @@ bool whole_vectors(const QkNormParams& p, int N, bool backward) {
     return at % 16 == 0 && strides % N == 0 && p.d % N == 0 && (p.interleaved ? 2 : 1) * p.P % N == 0;
 }
 
-// Blocks along the tokens: no more than run at once; what those of the backward pass sum is joined.
-constexpr int kForwardBlocks = 2, kBackwardBlocks = 3;      // per SM
+// Blocks along the tokens: no more than run at once (more where they are smaller, in the forward pass); what those of the
+// backward pass sum is joined.
+constexpr int kForwardBlocks = 2, kBackwardBlocks = 3;      // of kQkThreads threads, per SM
 int64_t backward_blocks(int64_t T, int sms) { return min64(T, kBackwardBlocks * (int64_t)sms); }
 
 QkPlan plan_of(const QkNormParams& p, int N, int sms, bool backward) {
@@ -378,9 +394,11 @@ QkPlan plan_of(const QkNormParams& p, int N, int sms, bool backward) {
     while ((1 << plan.log_G) < plan.units && plan.log_G < 5) ++plan.log_G;
     // a token's heads over as many blocks as fill them best (each makes the table once), evenly
     const int64_t most = kQkThreads >> plan.log_G, fewest = ceil_div(plan.heads, most);
+    const int64_t of_sm = backward ? most : kForwardBlocks * most;
     int64_t best = -1;
     for (int64_t parts = fewest; parts <= fewest + 3 && parts <= plan.heads; ++parts) {
-        const int64_t share = ceil_div(plan.heads, parts), used = most / share * plan.heads * 100 / (parts * most);
+        const int64_t share = ceil_div(plan.heads, parts), groups = most / share * share;
+        const int64_t used = of_sm / groups * (most / share) * plan.heads * 100 / (parts * of_sm);
         if (used > best + 10) {
             best = used;
             plan.share = (int)share;
@@ -391,7 +409,7 @@ QkPlan plan_of(const QkNormParams& p, int N, int sms, bool backward) {
     int64_t tile = min64(table, (int64_t)8 * plan.tokens) / plan.tokens * plan.tokens;
     if (tile < plan.tokens) tile = plan.tokens;
     // no more blocks than run at once, and no fewer than that for long tiles
-    const int64_t most_blocks = backward ? backward_blocks(p.T, sms) : kForwardBlocks * (int64_t)sms;
+    const int64_t most_blocks = backward ? backward_blocks(p.T, sms) : of_sm / (plan.tokens * plan.share) * (int64_t)sms;
     tile = min64(tile, ceil_div(ceil_div(p.T, most_blocks), plan.tokens) * plan.tokens);
     plan.blocks = (int)min64(most_blocks, ceil_div(p.T, tile));
     plan.tile = (int)tile;
@@ -425,6 +443,7 @@ cudaError_t units(const QkNormParams& p, int sms, cudaStream_t s, int64_t* sums)
     // up to 32 / N units a lane: rows of LA_MAX_ROTARY_D that turn few pairs
     static_assert(LA_MAX_ROTARY_D == 32 * 32, "a lane's units");
     constexpr int kSome = N == 1 ? 4 : 2;
+    if (N == 1 && per == 2) return launch<T, N, Interleaved, N == 1 ? 2 : kSome, Backward, false>(p, plan, s, sums);
     if (N > 1 && per <= 1 && plan.pair_units == 1 << plan.log_G && plan.units == plan.pair_units)
         return launch<T, N, Interleaved, 1, Backward, (N > 1)>(p, plan, s, sums);
     if (per <= 1) return launch<T, N, Interleaved, 1, Backward, false>(p, plan, s, sums);
