@@ -481,6 +481,14 @@ def _addr_or_none(t, name, dtype, shape, index):
     return None if t is None else _addr(t, name, dtype, shape, index)
 
 
+def _out(t, name, dtype, shape, like):
+    """(output, its address): the caller's, or a new one on the device of `like`."""
+    if t is not None:
+        return t, _addr(t, name, dtype, shape, like.get_device())
+    t = like.new_empty(shape, dtype=dtype)
+    return t, t.data_ptr()
+
+
 class _On:
     """Makes an operand's device current for a call and, where a stream is given, that stream: what the
     call allocates belongs to it."""
@@ -813,16 +821,16 @@ def la_qk_norm_rotary(q, k, q_weight, k_weight, freq, positions, pairs, eps=1e-6
     if k is None and (k_out is not None or k_rstd is not None):
         raise ValueError("k_out or k_rstd is given without k")
     dt, f32 = q.dtype, torch.float32
-    q_out = torch.empty((T, Hq, d), dtype=dt, device=q.device) if q_out is None else q_out
-    k_out = torch.empty((T, Hk, d), dtype=dt, device=q.device) if k is not None and k_out is None else k_out
-    if return_rstd:
-        q_rstd = torch.empty((T, Hq), dtype=f32, device=q.device) if q_rstd is None else q_rstd
-        k_rstd = torch.empty((T, Hk), dtype=f32, device=q.device) if k is not None and k_rstd is None else k_rstd
+    q_out, pqo = _out(q_out, "q_out", dt, (T, Hq, d), q)
+    k_out, pko = (None, None) if k is None else _out(k_out, "k_out", dt, (T, Hk, d), q)
+    pqr = pkr = None
+    if return_rstd or q_rstd is not None:
+        q_rstd, pqr = _out(q_rstd, "q_rstd", f32, (T, Hq), q)
+    if k is not None and (return_rstd or k_rstd is not None):
+        k_rstd, pkr = _out(k_rstd, "k_rstd", f32, (T, Hk), q)
     _check("la_qk_norm_rotary", lib.la_qk_norm_rotary(
-        pq, pk, wq, wk, pf, pp, DTYPE_IDS[dt], T, Hq, Hk, d, sq, sk, pa, n, bool(interleaved), per_head, eps,
-        _addr(q_out, "q_out", dt, (T, Hq, d), dev), _addr_or_none(k_out, "k_out", dt, (T, Hk, d), dev),
-        _addr_or_none(q_rstd, "q_rstd", f32, (T, Hq), dev), _addr_or_none(k_rstd, "k_rstd", f32, (T, Hk), dev),
-        _current_stream(dev)))
+        pq, pk, wq, wk, pf, pp, DTYPE_IDS[dt], T, Hq, Hk, d, sq, sk, pa, n, bool(interleaved), per_head, eps, pqo, pko,
+        pqr, pkr, _current_stream(dev)))
     return (q_out, k_out, q_rstd, k_rstd) if return_rstd else (q_out, k_out)
 
 
@@ -854,19 +862,19 @@ def la_qk_norm_rotary_backward(q, k, q_rstd, k_rstd, dq_out, dk_out, q_weight, k
     pkr = pdk = None
     if k is not None:
         pkr, pdk = _addr(k_rstd, "k_rstd", f32, (T, Hk), dev), _addr(dk_out, "dk_out", dt, (T, Hk, d), dev)
-    dq = torch.empty((T, Hq, d), dtype=dt, device=q.device) if dq is None else dq
-    dk = torch.empty((T, Hk, d), dtype=dt, device=q.device) if k is not None and dk is None else dk
-    dq_weight = torch.empty_like(q_weight) if q_weight is not None and dq_weight is None else dq_weight
-    dk_weight = torch.empty_like(k_weight) if k_weight is not None and dk_weight is None else dk_weight
+    dq, po = _out(dq, "dq", dt, (T, Hq, d), q)
+    dk, pko = (None, None) if k is None else _out(dk, "dk", dt, (T, Hk, d), q)
+    pqw = pkw = None
+    if q_weight is not None:
+        dq_weight, pqw = _out(dq_weight, "dq_weight", f32, q_weight.shape, q)
+    if k_weight is not None:
+        dk_weight, pkw = _out(dk_weight, "dk_weight", f32, k_weight.shape, q)
     workspace, pw, nw = _workspace(
         workspace, 0 if workspace is not None else
         lib.la_qk_norm_rotary_backward_workspace_bytes(DTYPE_IDS[dt], T, Hq, Hk, d), dev)
     _check("la_qk_norm_rotary_backward", lib.la_qk_norm_rotary_backward(
         pq, pk, pqr, pkr, pdq, pdk, wq, wk, pf, pp, DTYPE_IDS[dt], T, Hq, Hk, d, sq, sk, pa, n, bool(interleaved),
-        per_head, _addr(dq, "dq", dt, (T, Hq, d), dev), _addr_or_none(dk, "dk", dt, (T, Hk, d), dev),
-        _addr_or_none(dq_weight, "dq_weight", f32, None if q_weight is None else q_weight.shape, dev),
-        _addr_or_none(dk_weight, "dk_weight", f32, None if k_weight is None else k_weight.shape, dev), pw, nw,
-        _current_stream(dev)))
+        per_head, po, pko, pqw, pkw, pw, nw, _current_stream(dev)))
     return dq, dk, dq_weight, dk_weight
 
 

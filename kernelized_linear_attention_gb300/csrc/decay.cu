@@ -32,6 +32,7 @@ constexpr int kPlanThreads = 1024;
 __global__ void __launch_bounds__(kPlanThreads) decay_plan_kernel(const __grid_constant__ DecayCall c) {
     __shared__ int2 sums[32];
     __shared__ int bad;
+    chain_go();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         bad = c.cu_seqlens[0] != 0 || c.cu_seqlens[c.nseq] != c.T;
@@ -120,6 +121,8 @@ template <int N>
 __global__ void __launch_bounds__(kJoinThreads) decay_join_kernel(const __grid_constant__ DecayCall c,
                                                                   const __grid_constant__ StatesList list, int blocks) {
     using V = Vec<float, N>;
+    chain_wait();
+    chain_go();
     if (decay_malformed(c)) return;
     const int s = blockIdx.x, h = blockIdx.y, n = c.dk * c.dv, which = blockIdx.z / blocks;
     const DecayStates& p = list.p[which];
@@ -210,6 +213,8 @@ __global__ void __launch_bounds__(kSimtThreads) decay_states_kernel(const __grid
                                                                     const __grid_constant__ StatesList list,
                                                                     DecayWhich of_all, int blocks, bool vec) {
     __shared__ __align__(16) float ys[kRows][kCols], zs[kRows][kCols];
+    chain_wait();
+    chain_go();
     const int h = blockIdx.y, nb = (c.dv + kCols - 1) / kCols, item = blockIdx.z / blocks, block = blockIdx.z - item * blocks;
     const int a0 = block / nb * kCols, b0 = block % nb * kCols;
     const DecayStates& p = list.p[item];
@@ -299,6 +304,8 @@ template <typename T>
 __global__ void __launch_bounds__(kSimtThreads) decay_pass_kernel(const __grid_constant__ DecayCall c,
                                                                   const __grid_constant__ PassList list, bool vec) {
     extern __shared__ __align__(16) float smem[];
+    chain_wait();
+    chain_go();
     const int item = ((int)blockIdx.z >= list.first[1]) + ((int)blockIdx.z >= list.first[2]);
     const DecayPass& p = list.p[item];
     const int ds = p.ds, ds4 = (ds + 3) / 4 * 4, ld = simt_stride(ds), h = blockIdx.y;
@@ -589,24 +596,23 @@ int64_t segment_length(const DecayCall& c, bool tensor, int sms) {
     return min64(best * 128, kLongest);
 }
 
-cudaError_t plan(const DecayCall& c, cudaStream_t s) {
-    if (!c.cu_seqlens) return cudaMemsetAsync(c.hdr, 0, sizeof(WsHeader), s);
-    decay_plan_kernel<<<1, kPlanThreads, 0, s>>>(c);
-    return cudaGetLastError();
+cudaError_t plan(const DecayCall& c, Chain& chain) {
+    if (!c.cu_seqlens) return cudaMemsetAsync(c.hdr, 0, sizeof(WsHeader), chain.stream);
+    return launch_in(chain, decay_plan_kernel, 1, kPlanThreads, 0, c);
 }
 
 // Whether what leaves the sequences is summed with the segments: unless it takes the place of what enters them.
 bool with_segments(const DecayStates& p) { return p.edge_out && p.edge_out != p.edge_in; }
 
 cudaError_t states(const DecayCall& c, std::initializer_list<DecayStates> passes, int dtype, bool ends_alone,
-                   cudaStream_t s) {
+                   Chain& chain) {
     StatesList simt{};
     int n = 0;
     bool vec = true;
     for (const DecayStates& p : passes) {
         if (!ends_alone && c.slots == 0 && !with_segments(p)) continue;
         if (decay_tc_fits(c, dtype) && on_16_bytes({p.y, p.z})) {
-            const cudaError_t e = decay_tc_states(c, p, ends_alone ? kEnds : with_segments(p) ? kAll : kInner, s);
+            const cudaError_t e = decay_tc_states(c, p, ends_alone ? kEnds : with_segments(p) ? kAll : kInner, chain);
             if (e != cudaSuccess) return e;
             continue;
         }
@@ -618,12 +624,11 @@ cudaError_t states(const DecayCall& c, std::initializer_list<DecayStates> passes
     const int blocks = (int)(ceil_div(c.dk, kCols) * ceil_div(c.dv, kCols));
     const dim3 grid(ends_alone ? c.nseq : c.segments, c.H, (unsigned)(n * blocks));
     const DecayWhich which = ends_alone ? kEnds : kAll;
-    if (dtype == LA_F32) decay_states_kernel<float><<<grid, kSimtThreads, 0, s>>>(c, simt, which, blocks, vec);
-    else decay_states_kernel<__nv_bfloat16><<<grid, kSimtThreads, 0, s>>>(c, simt, which, blocks, vec);
-    return cudaGetLastError();
+    return launch_in(chain, dtype == LA_F32 ? decay_states_kernel<float> : decay_states_kernel<__nv_bfloat16>, grid,
+                     kSimtThreads, 0, c, simt, which, blocks, vec);
 }
 
-cudaError_t join(const DecayCall& c, std::initializer_list<DecayStates> passes, cudaStream_t s) {
+cudaError_t join(const DecayCall& c, std::initializer_list<DecayStates> passes, Chain& chain) {
     const int n = c.dk * c.dv;
     StatesList list{};
     int items = 0;
@@ -635,34 +640,32 @@ cudaError_t join(const DecayCall& c, std::initializer_list<DecayStates> passes, 
     }
     const int blocks = (int)ceil_div(n, kJoinThreads * (vec ? 4 : 1));
     const dim3 grid(c.nseq, c.H, (unsigned)(items * blocks));
-    if (vec) decay_join_kernel<4><<<grid, kJoinThreads, 0, s>>>(c, list, blocks);
-    else decay_join_kernel<1><<<grid, kJoinThreads, 0, s>>>(c, list, blocks);
-    return cudaGetLastError();
+    return launch_in(chain, vec ? decay_join_kernel<4> : decay_join_kernel<1>, grid, kJoinThreads, 0, c, list, blocks);
 }
 
 // What enters every segment, and what leaves every sequence unless that overwrites what enters it (nothing to do where
 // every sequence is one segment and nothing is to leave).
-cudaError_t enter(const DecayCall& c, std::initializer_list<DecayStates> passes, int dtype, cudaStream_t s) {
+cudaError_t enter(const DecayCall& c, std::initializer_list<DecayStates> passes, int dtype, Chain& chain) {
     bool ends = false;
     for (const DecayStates& p : passes) ends = ends || with_segments(p);
     if (c.slots == 0 && !ends) return cudaSuccess;
     cudaError_t e = cudaSuccess;
-    if (c.T > 0) e = states(c, passes, dtype, false, s);
-    return e != cudaSuccess ? e : join(c, passes, s);
+    if (c.T > 0) e = states(c, passes, dtype, false, chain);
+    return e != cudaSuccess ? e : join(c, passes, chain);
 }
 // What leaves every sequence, where that takes the place of what enters it: once nothing reads it any more.
-cudaError_t leave(const DecayCall& c, const DecayStates& p, int dtype, cudaStream_t s) {
-    return p.edge_out && p.edge_out == p.edge_in ? states(c, {p}, dtype, true, s) : cudaSuccess;
+cudaError_t leave(const DecayCall& c, const DecayStates& p, int dtype, Chain& chain) {
+    return p.edge_out && p.edge_out == p.edge_in ? states(c, {p}, dtype, true, chain) : cudaSuccess;
 }
 
-cudaError_t products(const DecayCall& c, std::initializer_list<DecayPass> passes, int dtype, cudaStream_t s) {
+cudaError_t products(const DecayCall& c, std::initializer_list<DecayPass> passes, int dtype, Chain& chain) {
     if (c.T == 0) return cudaSuccess;
     PassList simt{};
     int n = 0, blocks = 0, widest = 0;
     bool vec = true;
     for (const DecayPass& p : passes) {
         if (decay_tc_fits(c, dtype) && on_16_bytes({p.x, p.y, p.z, p.out})) {
-            const cudaError_t e = decay_tc_pass(c, p, s);
+            const cudaError_t e = decay_tc_pass(c, p, chain);
             if (e != cudaSuccess) return e;
             continue;
         }
@@ -679,8 +682,7 @@ cudaError_t products(const DecayCall& c, std::initializer_list<DecayPass> passes
     auto kernel = dtype == LA_F32 ? decay_pass_kernel<float> : decay_pass_kernel<__nv_bfloat16>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kSimtThreads, smem, s>>>(c, simt, vec);
-    return cudaGetLastError();
+    return launch_in(chain, kernel, grid, kSimtThreads, smem, c, simt, vec);
 }
 
 }  // namespace
@@ -716,10 +718,11 @@ cudaError_t decay_forward(const DecayCall& c, const void* q, const void* k, cons
                           const float* state_in, float* state_out, void* out, cudaStream_t s) {
     const DecayStates sums{k, v, 0, state_in, state_out};
     const DecayPass p{q, k, v, out, c.dk, c.dv, 0, 0, state_in};
-    cudaError_t e = plan(c, s);
-    if (e == cudaSuccess) e = enter(c, {sums}, dtype, s);
-    if (e == cudaSuccess) e = products(c, {p}, dtype, s);
-    if (e == cudaSuccess) e = leave(c, sums, dtype, s);
+    Chain chain{s};
+    cudaError_t e = plan(c, chain);
+    if (e == cudaSuccess) e = enter(c, {sums}, dtype, chain);
+    if (e == cudaSuccess) e = products(c, {p}, dtype, chain);
+    if (e == cudaSuccess) e = leave(c, sums, dtype, chain);
     return e;
 }
 
@@ -729,10 +732,11 @@ cudaError_t decay_backward(const DecayCall& c, const void* q, const void* k, con
     const DecayStates sums{k, v, 0, state_in, nullptr}, back{q, dout, 1, dstate_out, dstate_in};
     const DecayPass pq{dout, v, k, dq, c.dv, c.dk, 0, 1, state_in}, pk{v, dout, q, dk, c.dv, c.dk, 1, 1, dstate_out},
         pv{k, q, dout, dv, c.dk, c.dv, 1, 0, dstate_out};
-    cudaError_t e = plan(c, s);
-    if (e == cudaSuccess) e = enter(c, {sums, back}, dtype, s);
-    if (e == cudaSuccess) e = products(c, {pq, pk, pv}, dtype, s);
-    if (e == cudaSuccess) e = leave(c, back, dtype, s);
+    Chain chain{s};
+    cudaError_t e = plan(c, chain);
+    if (e == cudaSuccess) e = enter(c, {sums, back}, dtype, chain);
+    if (e == cudaSuccess) e = products(c, {pq, pk, pv}, dtype, chain);
+    if (e == cudaSuccess) e = leave(c, back, dtype, chain);
     return e;
 }
 

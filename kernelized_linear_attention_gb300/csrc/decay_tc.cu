@@ -163,6 +163,8 @@ __global__ void __launch_bounds__(kStatesThreads, 1)
     StatesSmem<D>& s = *reinterpret_cast<StatesSmem<D>*>(raw + to_1024(raw));
     const int h = blockIdx.x, index = blockIdx.y + 65535 * blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    chain_wait();
+    chain_go();
     DecaySegment g;
     if (index >= (which == kEnds ? c.nseq : c.segments)) return;
     if (decay_malformed(c)) return;
@@ -406,6 +408,8 @@ __global__ void __launch_bounds__(kPassThreads, 1)
     PassSmem<D>& s = *reinterpret_cast<PassSmem<D>*>(raw + to_1024(raw));
     const int h = blockIdx.x, index = blockIdx.y + 65535 * blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, row = 32 * q + lane;
+    chain_wait();
+    chain_go();
     DecaySegment g;
     if (index >= c.segments || !decay_segment(c, index, g)) return;
     const DecayBase base = decay_base(c.log_decay[h]);
@@ -900,7 +904,7 @@ cudaError_t opt_in(K kernel, size_t bytes) {
 }
 
 template <int D>
-cudaError_t states(const DecayCall& c, const DecayStates& p, DecayWhich which, cudaStream_t s) {
+cudaError_t states(const DecayCall& c, const DecayStates& p, DecayWhich which, Chain& chain) {
     CUtensorMap my{}, mz{};
     constexpr int rows = StatesShape<D>::rows;
     if (c.T > 0 && (!rows_map(&my, p.y, c, c.dk, rows) || !rows_map(&mz, p.z, c, c.dv, rows))) return cudaErrorInvalidValue;
@@ -908,12 +912,12 @@ cudaError_t states(const DecayCall& c, const DecayStates& p, DecayWhich which, c
     static_assert(smem <= 227 * 1024, "shared memory");
     const cudaError_t e = opt_in(decay_tc_states_kernel<D>, smem);
     if (e != cudaSuccess) return e;
-    decay_tc_states_kernel<D><<<grid_of(c.H, which == kEnds ? c.nseq : c.segments), kStatesThreads, smem, s>>>(c, p, which, my, mz);
-    return cudaGetLastError();
+    return launch_in(chain, decay_tc_states_kernel<D>, grid_of(c.H, which == kEnds ? c.nseq : c.segments), kStatesThreads,
+                     smem, c, p, which, my, mz);
 }
 
 template <int D>
-cudaError_t pass(const DecayCall& c, const DecayPass& p, cudaStream_t s) {
+cudaError_t pass(const DecayCall& c, const DecayPass& p, Chain& chain) {
     CUtensorMap mx, my, mz;
     if (!rows_map(&mx, p.x, c, p.ds) || !rows_map(&my, p.y, c, p.ds) || !rows_map(&mz, p.z, c, p.dz)) return cudaErrorInvalidValue;
     constexpr size_t smem = sizeof(PassSmem<D>) + 1024;
@@ -923,8 +927,7 @@ cudaError_t pass(const DecayCall& c, const DecayPass& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     // 32-byte stores of 16 channels where every row allows them
     const bool wide = p.dz % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
-    kernel<<<grid_of(c.H, c.segments), kPassThreads, smem, s>>>(c, p, wide, mx, my, mz);
-    return cudaGetLastError();
+    return launch_in(chain, kernel, grid_of(c.H, c.segments), kPassThreads, smem, c, p, wide, mx, my, mz);
 }
 
 }  // namespace
@@ -935,12 +938,12 @@ bool decay_tc_fits(const DecayCall& c, int dtype) {
     return dtype == LA_BF16 && c.dk <= 128 && c.dv <= 128 && c.dk % 8 == 0 && c.dv % 8 == 0;
 }
 
-cudaError_t decay_tc_states(const DecayCall& c, const DecayStates& p, DecayWhich which, cudaStream_t s) {
-    return c.dk <= 64 && c.dv <= 64 ? states<64>(c, p, which, s) : states<128>(c, p, which, s);
+cudaError_t decay_tc_states(const DecayCall& c, const DecayStates& p, DecayWhich which, Chain& chain) {
+    return c.dk <= 64 && c.dv <= 64 ? states<64>(c, p, which, chain) : states<128>(c, p, which, chain);
 }
 
-cudaError_t decay_tc_pass(const DecayCall& c, const DecayPass& p, cudaStream_t s) {
-    return c.dk <= 64 && c.dv <= 64 ? pass<64>(c, p, s) : pass<128>(c, p, s);
+cudaError_t decay_tc_pass(const DecayCall& c, const DecayPass& p, Chain& chain) {
+    return c.dk <= 64 && c.dv <= 64 ? pass<64>(c, p, chain) : pass<128>(c, p, chain);
 }
 
 }  // namespace la

@@ -1,6 +1,7 @@
 // Linear attention with a decay for each head: parameters, work table and launchers.
 #pragma once
 
+#include "chain.cuh"
 #include "ops.h"
 
 namespace la {
@@ -80,8 +81,8 @@ cudaError_t decay_step(const void* q, const void* k, const void* v, const float*
 
 // Tensor cores: bf16 of up to 128 channels, a multiple of 8, in arrays that start on 16 bytes (decay_tc.cu).
 bool decay_tc_fits(const DecayCall& c, int dtype);
-cudaError_t decay_tc_states(const DecayCall& c, const DecayStates& p, DecayWhich which, cudaStream_t s);
-cudaError_t decay_tc_pass(const DecayCall& c, const DecayPass& p, cudaStream_t s);
+cudaError_t decay_tc_states(const DecayCall& c, const DecayStates& p, DecayWhich which, Chain& chain);
+cudaError_t decay_tc_pass(const DecayCall& c, const DecayPass& p, Chain& chain);
 cudaError_t decay_force_wait_timeout(int enable);   // test hook behind la_test_force_wait_timeout
 
 // ---------------------------------------------------------------------------

@@ -12,6 +12,7 @@
 // every row allows it, so that a pair is turned inside a lane.  A group keeps one head and walks tokens: its weights,
 // and in the backward pass its sums for their gradients, stay in registers.  A block has some heads of some tokens, and
 // their cos and sin once for all heads.
+#include "ops/chain.cuh"
 #include "ops/ops.h"
 #include "ops/turn.cuh"
 #include "ops/vec.cuh"
@@ -85,10 +86,11 @@ __device__ __forceinline__ void turn_unit(typename Pairs<N>::P (&a)[Sides][Pairs
 
 // Full: every lane of a group has KU units, and all turn.
 template <typename T, int N, bool Interleaved, int KU, bool Backward, bool Full>
-__global__ void __launch_bounds__(kQkThreads, KU > 1 ? 1 : Backward ? 3 : 2) qk_norm_rotary_kernel(const __grid_constant__ QkNormParams p,
-                                                             const __grid_constant__ QkPlan plan) {
+__global__ void __launch_bounds__(kQkThreads, KU > 1 && KU * N > 4 ? 1 : Backward ? 3 : 2)
+    qk_norm_rotary_kernel(const __grid_constant__ QkNormParams p, const __grid_constant__ QkPlan plan) {
     // two tables [tile][2 P], a tile's and the next one's; behind them the rows on their way, 16 bytes of each vector a lane
     extern __shared__ __align__(16) float table[];
+    if (Backward) chain_go();
     using V = Vec<T, N>;
     using R = Pairs<N>;
     using P = typename R::P;
@@ -343,6 +345,7 @@ __global__ void __launch_bounds__(kQkThreads, KU > 1 ? 1 : Backward ? 3 : 2) qk_
 __global__ void __launch_bounds__(kJoinColumns * kJoinRows) qk_join_kernel(const __grid_constant__ QkNormParams p,
                                                                            int sums) {
     __shared__ float part[kJoinRows][kJoinColumns];
+    chain_wait();
     const int rows = p.per_head ? p.H[0] + p.H[1] : 2, c = blockIdx.x * kJoinColumns + threadIdx.x, r = blockIdx.y;
     const int k = p.per_head ? r >= p.H[0] : r;
     float* const out = p.dw[k];
@@ -417,7 +420,7 @@ QkPlan plan_of(const QkNormParams& p, int N, int sms, bool backward) {
 }
 
 template <typename T, int N, bool Interleaved, int KU, bool Backward, bool Full>
-cudaError_t launch(const QkNormParams& p, const QkPlan& plan, cudaStream_t s, int64_t* sums) {
+cudaError_t launch(const QkNormParams& p, const QkPlan& plan, Chain& chain, int64_t* sums) {
     const int threads = ((plan.share * plan.tokens << plan.log_G) + 31) / 32 * 32;
     size_t smem = 2 * sizeof(float2) * (size_t)plan.tile * p.P;
     if (copied<T, N, KU, Backward>) smem += (size_t)kRing * 16 * threads * KU * (Interleaved && N > 1 ? 1 : 2);
@@ -431,40 +434,40 @@ cudaError_t launch(const QkNormParams& p, const QkPlan& plan, cudaStream_t s, in
         if (e != cudaSuccess) return e;
     }
     const dim3 grid((unsigned)plan.blocks, (unsigned)ceil_div(plan.heads, plan.share));
-    kernel<<<grid, threads, smem, s>>>(p, plan);
     if (sums) *sums = (int64_t)grid.x * (p.per_head ? 1 : grid.y);
-    return cudaGetLastError();
+    return launch_in(chain, kernel, grid, threads, smem, p, plan);
 }
 
 template <typename T, int N, bool Interleaved, bool Backward>
-cudaError_t units(const QkNormParams& p, int sms, cudaStream_t s, int64_t* sums) {
+cudaError_t units(const QkNormParams& p, int sms, Chain& chain, int64_t* sums) {
     const QkPlan plan = plan_of(p, N, sms, Backward);
     const int64_t per = ceil_div(plan.units, 1 << plan.log_G);
     // up to 32 / N units a lane: rows of LA_MAX_ROTARY_D that turn few pairs
     static_assert(LA_MAX_ROTARY_D == 32 * 32, "a lane's units");
     constexpr int kSome = N == 1 ? 4 : 2;
-    if (N == 1 && per == 2) return launch<T, N, Interleaved, N == 1 ? 2 : kSome, Backward, false>(p, plan, s, sums);
+    if (N == 1 && per == 2) return launch<T, N, Interleaved, N == 1 ? 2 : kSome, Backward, false>(p, plan, chain, sums);
     if (N > 1 && per <= 1 && plan.pair_units == 1 << plan.log_G && plan.units == plan.pair_units)
-        return launch<T, N, Interleaved, 1, Backward, (N > 1)>(p, plan, s, sums);
-    if (per <= 1) return launch<T, N, Interleaved, 1, Backward, false>(p, plan, s, sums);
-    if (per <= kSome) return launch<T, N, Interleaved, kSome, Backward, false>(p, plan, s, sums);
-    return launch<T, N, Interleaved, 32 / N, Backward, false>(p, plan, s, sums);
+        return launch<T, N, Interleaved, 1, Backward, (N > 1)>(p, plan, chain, sums);
+    if (per <= 1) return launch<T, N, Interleaved, 1, Backward, false>(p, plan, chain, sums);
+    if (per <= kSome) return launch<T, N, Interleaved, kSome, Backward, false>(p, plan, chain, sums);
+    return launch<T, N, Interleaved, 32 / N, Backward, false>(p, plan, chain, sums);
 }
 
 template <typename T, bool Backward>
-cudaError_t dispatch(const QkNormParams& p, cudaStream_t s, int64_t* sums = nullptr) {   // sums: of the blocks, for each weight
+cudaError_t dispatch(const QkNormParams& p, Chain& chain, int64_t* sums = nullptr) {   // sums: of the blocks, for each weight
     constexpr int N = 16 / sizeof(T);
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     if (whole_vectors(p, N, Backward))
-        return p.interleaved ? units<T, N, true, Backward>(p, sms, s, sums) : units<T, N, false, Backward>(p, sms, s, sums);
-    return p.interleaved ? units<T, 1, true, Backward>(p, sms, s, sums) : units<T, 1, false, Backward>(p, sms, s, sums);
+        return p.interleaved ? units<T, N, true, Backward>(p, sms, chain, sums) : units<T, N, false, Backward>(p, sms, chain, sums);
+    return p.interleaved ? units<T, 1, true, Backward>(p, sms, chain, sums) : units<T, 1, false, Backward>(p, sms, chain, sums);
 }
 
 }  // namespace
 
 cudaError_t qk_norm_rotary(const QkNormParams& p, int dtype, cudaStream_t s) {
-    return dtype == LA_F32 ? dispatch<float, false>(p, s) : dispatch<__nv_bfloat16, false>(p, s);
+    Chain chain{s};
+    return dtype == LA_F32 ? dispatch<float, false>(p, chain) : dispatch<__nv_bfloat16, false>(p, chain);
 }
 
 size_t qk_norm_rotary_backward_workspace_bytes(int64_t T, int H, int d) {
@@ -479,13 +482,11 @@ cudaError_t qk_norm_rotary_backward(const QkNormParams& p, int dtype, cudaStream
     if (sms <= 0) return cudaErrorInvalidDevice;
     cudaError_t e = cudaSuccess;
     int64_t sums = 0;
-    if (p.T > 0) {
-        e = dtype == LA_F32 ? dispatch<float, true>(p, s, &sums) : dispatch<__nv_bfloat16, true>(p, s, &sums);
-    }
+    Chain chain{s};
+    if (p.T > 0) e = dtype == LA_F32 ? dispatch<float, true>(p, chain, &sums) : dispatch<__nv_bfloat16, true>(p, chain, &sums);
     if (e != cudaSuccess || !p.partial) return e;
     const dim3 grid((unsigned)ceil_div(p.d, kJoinColumns), p.per_head ? p.H[0] + p.H[1] : p.H[1] ? 2 : 1);
-    qk_join_kernel<<<grid, dim3(kJoinColumns, kJoinRows), 0, s>>>(p, (int)sums);
-    return cudaGetLastError();
+    return launch_in(chain, qk_join_kernel, grid, dim3(kJoinColumns, kJoinRows), 0, p, (int)sums);
 }
 
 }  // namespace la
