@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kPlanThreads) decay_plan_kernel(const __grid_c
 // Join: what enters each segment, from the segments' own sums
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
-constexpr int kJoinAhead = 8;      // segments whose loads are on their way together
+constexpr int kJoinAhead = 4;      // segments whose loads are on their way together
 
 template <int N>
 __global__ void __launch_bounds__(kJoinThreads) decay_join_kernel(const __grid_constant__ DecayCall c,
@@ -567,7 +567,8 @@ constexpr int64_t kLongest = 1 << 20;      // tokens of a segment: exact in fp32
 
 // Tokens of a segment.  Tensor cores: whole chunks of 128, one block per SM.  Equal sequences are cut so that the waves
 // of blocks times a segment's chunks, and two for a block's beginning and end, are fewest; packed ones, whose lengths
-// are not known here, into three blocks' worth per SM.  CUDA cores: four blocks per SM, of chunks of 32 (blocks of a single
+// are not known here, into one and a half blocks' worth per SM (40009 x 8 x 64 of 64 sequences 135 us, of one 98; three blocks'
+// worth: 145 and 121; one: 129 and 104, but 120000 x 8 x 64 of 64 sequences 271 instead of 241).  CUDA cores: four blocks per SM, of chunks of 32 (blocks of a single
 // chunk then for what is short: nothing in them waits for a chunk before).
 int64_t segment_length(const DecayCall& c, bool tensor, int sms) {
     const int64_t n = c.cu_seqlens ? c.T : c.T / c.nseq;
@@ -579,7 +580,7 @@ int64_t segment_length(const DecayCall& c, bool tensor, int sms) {
     const int64_t chunks = ceil_div(n, 128);
     int64_t best = 1, least = INT64_MAX;
     if (c.cu_seqlens) {
-        best = ceil_div(c.T, 128) * c.H / (3 * sms);
+        best = ceil_div(c.T, 128) * c.H * 2 / (3 * sms);
         best = min64(best < 1 ? 1 : best, chunks);
     } else {
         // (more segments than a few per SM, or than chunks, never pay)
