@@ -610,8 +610,8 @@ LA_API size_t la_qk_norm_rotary_backward_workspace_bytes(int dtype, int64_t T, i
  *   q, k: [T, H, d_k]; v, out: [T, H, d_v], all of dtype.
  *   log_decay: fp32 [H] (device), natural logarithms, at most 0: 0 forgets
  *              nothing, -inf everything but the token itself.  Positive ones
- *              grow, and are computed as given as long as powers over a few
- *              thousand tokens stay in fp32's range.
+ *              grow, and are computed as given as long as their powers over a
+ *              sequence stay in fp32's range.
  *   scale:     finite.
  *   cu_seqlens, nseq: as for la_forward.
  *   state_in:  NULL (every sequence starts from 0) or fp32 [nseq, H, d_k, d_v].
@@ -619,9 +619,15 @@ LA_API size_t la_qk_norm_rotary_backward_workspace_bytes(int dtype, int64_t T, i
  *              sequence's last token; an empty sequence's state_in (or 0) is
  *              copied.  May be the same array as state_in.
  *   States and sums are fp32 and decays are carried beyond fp32, so far tokens
- *   lose nothing; out is rounded once.  Results are deterministic.  A value
- *   that is not finite reaches its own token and later ones of its sequence
- *   only.
+ *   lose nothing.  fp32 rows are computed in fp32, and bf16 rows too where d_k or
+ *   d_v is above 128 or no multiple of 8, an array does not start on 16 bytes, or
+ *   sequences have up to 32 tokens on average: out is rounded once.  Other bf16 rows are products of the tensor
+ *   cores, whose operands are rounded: what a token gives a later one of the same
+ *   128 (scale g^(i-j) q_i . k_j) to bf16, an error of at most 2^-8 of that
+ *   term; the keys that a state takes while a sequence goes on, weighted by
+ *   their decay, likewise; the state that queries read to 2^-16; keys in
+ *   state_out to 2^-24.  Results are deterministic.  A value that is not finite
+ *   reaches its own token and later ones of its sequence only.
  *   workspace: la_decay_attention_workspace_bytes(...) bytes, 256-byte aligned,
  *   contents on entry do not matter; calls that may overlap need workspaces of
  *   their own.  Malformed cu_seqlens are recorded in its error word

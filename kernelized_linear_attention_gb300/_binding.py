@@ -485,7 +485,7 @@ def _out(t, name, dtype, shape, like):
     """(output, its address): the caller's, or a new one on the device of `like`."""
     if t is not None:
         return t, _addr(t, name, dtype, shape, like.get_device())
-    t = like.new_empty(shape, dtype=dtype)
+    t = torch.empty(shape, dtype=dtype, device=like.device)
     return t, t.data_ptr()
 
 

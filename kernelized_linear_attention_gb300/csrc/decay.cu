@@ -115,7 +115,9 @@ __global__ void __launch_bounds__(kPlanThreads) decay_plan_kernel(const __grid_c
 // Join: what enters each segment, from the segments' own sums
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
-constexpr int kJoinAhead = 4;      // segments whose loads are on their way together
+// Segments whose loads are on their way together: fewer registers, for more threads at once, are better than more loads of
+// each (64 sequences of 8 x 64 x 64 in 95 segments: 13 us; with eight 15, with sixteen 31; 7 of 4 in 135: 22, 19 and 16).
+constexpr int kJoinAhead = 4;
 
 template <int N>
 __global__ void __launch_bounds__(kJoinThreads) decay_join_kernel(const __grid_constant__ DecayCall c,
@@ -299,7 +301,9 @@ __host__ __device__ inline size_t simt_smem(int ds) {
 }
 
 // One segment of a product pass.  A thread has two rows, 16 apart, and four columns (of the products with z and the
-// state) or two (of the scores).
+// state) or two (of the scores).  Passes of one call run in one launch: the gradients of 4099 x 4 x 64 in fp32, three
+// passes of 540 blocks, take 58 us (three launches 30 each), of which 33 are instructions at the full rate; the rest are
+// shared memory (three wavefronts for four FMA of a thread) and barriers.
 template <typename T>
 __global__ void __launch_bounds__(kSimtThreads) decay_pass_kernel(const __grid_constant__ DecayCall c,
                                                                   const __grid_constant__ PassList list, bool vec) {
@@ -469,7 +473,9 @@ constexpr int kStepThreads = N == 4 ? 128 : 256;
 template <int N>
 constexpr int kStepRows = N == 4 ? 8 : 4;
 
-// A block has one (sequence, head); lanes along dv in vectors of N, thread groups along dk.
+// A block has one (sequence, head); lanes along dv in vectors of N, thread groups along dk.  Bound by memory, each state
+// read and written once: 256 x 16 x 64 x 64 in 25 us, 20 at the copy rate; 27 from cold caches, where 256 threads with four
+// rows each took 31, 64 with sixteen 29, and streaming loads and stores nothing more or less.
 template <typename T, int N>
 __global__ void __launch_bounds__(kStepThreads<N>) decay_step_kernel(const T* __restrict__ q, const T* __restrict__ k,
                                                                   const T* __restrict__ v,
@@ -566,13 +572,14 @@ bool vector_rows(const DecayCall& c, int dtype, std::initializer_list<const void
 constexpr int64_t kLongest = 1 << 20;      // tokens of a segment: exact in fp32
 
 // Tokens of a segment.  Tensor cores: whole chunks of 128, one block per SM.  Equal sequences are cut so that the waves
-// of blocks times a segment's chunks, and two for a block's beginning and end, are fewest; packed ones, whose lengths
-// are not known here, into one and a half blocks' worth per SM (40009 x 8 x 64 of 64 sequences 135 us, of one 98; three blocks'
-// worth: 145 and 121; one: 129 and 104, but 120000 x 8 x 64 of 64 sequences 271 instead of 241).  CUDA cores: four blocks per SM, of chunks of 32 (blocks of a single
-// chunk then for what is short: nothing in them waits for a chunk before).
+// of blocks times a segment's chunks, and two for a block's beginning and end, are fewest.  Packed ones, whose lengths
+// are not known here, are cut into one and a half blocks' worth per SM (40009 x 8 x 64 of 64 sequences 135 us, of one 98;
+// three blocks' worth 145 and 121; one 129 and 104, but 120000 x 8 x 64 of 64 sequences 271 instead of 241).  CUDA cores:
+// four blocks per SM, of chunks of 32, so that what is short has one chunk to a block and nothing waits for a chunk ahead.
 int64_t segment_length(const DecayCall& c, bool tensor, int sms) {
-    const int64_t n = c.cu_seqlens ? c.T : c.T / c.nseq;
-    if (n < 1) return 128;
+    // (packed: longer than T where one segment would do, so that no boundary inside a sequence has to be reckoned with)
+    const int64_t n = c.cu_seqlens ? c.T + 1 : c.T / c.nseq;
+    if (c.T < 1) return 128;
     if (!tensor) {
         const int64_t L = ceil_div(ceil_div(c.T * c.H * ceil_div(c.dv, kCols), 4 * sms), kRows) * kRows;
         return min64(min64(L, ceil_div(n, kRows) * kRows), kLongest);
@@ -605,6 +612,11 @@ cudaError_t plan(const DecayCall& c, Chain& chain) {
 // Whether what leaves the sequences is summed with the segments: unless it takes the place of what enters them.
 bool with_segments(const DecayStates& p) { return p.edge_out && p.edge_out != p.edge_in; }
 
+// States of sequences of up to 64 tokens on average are summed on CUDA cores, whose many small blocks begin and end beside
+// one another: 256 of 64 x 8 x 64, carried, take 185 us and 240 with the sums on the tensor cores; 256 of 256 tokens 307
+// and 283; 8 of 128 tokens 30 and 25.
+constexpr int64_t kShortSums = 64;
+
 cudaError_t states(const DecayCall& c, std::initializer_list<DecayStates> passes, int dtype, bool ends_alone,
                    Chain& chain) {
     StatesList simt{};
@@ -612,7 +624,7 @@ cudaError_t states(const DecayCall& c, std::initializer_list<DecayStates> passes
     bool vec = true;
     for (const DecayStates& p : passes) {
         if (!ends_alone && c.slots == 0 && !with_segments(p)) continue;
-        if (decay_tc_fits(c, dtype) && on_16_bytes({p.y, p.z})) {
+        if (decay_tc_fits(c, dtype) && on_16_bytes({p.y, p.z}) && c.T > kShortSums * c.nseq) {
             const cudaError_t e = decay_tc_states(c, p, ends_alone ? kEnds : with_segments(p) ? kAll : kInner, chain);
             if (e != cudaSuccess) return e;
             continue;

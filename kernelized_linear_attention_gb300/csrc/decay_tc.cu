@@ -132,6 +132,8 @@ __device__ __forceinline__ void store_32(void* to, const uint32_t (&v)[8]) {
 // Warp 0 loads, warp 1 issues the products, two groups of eight warps weight y, one the even tiles and one the odd ones.
 // The tensor cores truncate when they accumulate: after 64 steps (1024 tokens) the sums go on in fp32 registers, rounded
 // to nearest.  (Two parts of the weighted y instead of three, which outputs alone would not notice: 57 us instead of 60.)
+// 65536 x 16 x 64 take 60 us, 40 for their bytes at the copy rate, and 16384 x 16 x 128 49 with tiles of 64 tokens (128
+// leave no room for a second weighted tile): the weighting warps issue in 40% of the slots, each tile's in a row.
 constexpr int kStatesThreads = 640;
 template <int D> struct StatesShape {
     static constexpr int blocks = D / 64;                 // of 64 channels
@@ -369,6 +371,9 @@ __global__ void __launch_bounds__(kStatesThreads, 1)
 // scores into P; 12 .. 19 weight y (in its place, once the scores have read it) and make an operand of the state;
 // 20 .. 27 write the outputs.  Every barrier's waits are consecutive, or behind something that implies the phase before,
 // and no phase can end twice before a waiter has seen it: a wait tells phases by parity alone.
+// 65536 x 16 x 64 take 107 us, 79 for their bytes at the copy rate: a chunk 2.0 us, of which the products are 0.7; half of
+// the issue slots are used, by the way of the scores through registers above all.  16384 x 16 x 128 take 82 us, one
+// wave of 128 blocks.  A block begins and ends in 4 us.
 constexpr int kPassThreads = 896;
 template <int D> struct PassShape {
     static constexpr int blocks = D / 64;
@@ -934,8 +939,14 @@ cudaError_t pass(const DecayCall& c, const DecayPass& p, Chain& chain) {
 
 cudaError_t decay_force_wait_timeout(int enable) { return cudaMemcpyToSymbol(g_force_wait_timeout, &enable, sizeof(int)); }
 
+// Sequences of up to 32 tokens on average, a quarter of a chunk, go to the CUDA cores, which have many blocks on an SM: 256
+// of 32 x 8 x 64 take 68 us and 86 on the tensor cores, their gradients 176 and 250 (a single one 15 and 11, 14 and 25); 256
+// of 64 tokens 132 and 89, and 362 and 259; one of 65536 x 16 x 64 1500 and 190.
+constexpr int64_t kShortest = 32;
+
 bool decay_tc_fits(const DecayCall& c, int dtype) {
-    return dtype == LA_BF16 && c.dk <= 128 && c.dv <= 128 && c.dk % 8 == 0 && c.dv % 8 == 0;
+    return dtype == LA_BF16 && c.dk <= 128 && c.dv <= 128 && c.dk % 8 == 0 && c.dv % 8 == 0 &&
+           c.T > kShortest * c.nseq;
 }
 
 cudaError_t decay_tc_states(const DecayCall& c, const DecayStates& p, DecayWhich which, Chain& chain) {

@@ -79,7 +79,8 @@ cudaError_t decay_step(const void* q, const void* k, const void* v, const float*
                        int dk, int dv, float scale, const float* state_in, float* state_out, void* out,
                        cudaStream_t s);
 
-// Tensor cores: bf16 of up to 128 channels, a multiple of 8, in arrays that start on 16 bytes (decay_tc.cu).
+// Tensor cores: bf16 of up to 128 channels, a multiple of 8, in arrays that start on 16 bytes, sequences of more than a
+// quarter of a chunk on average (decay_tc.cu).
 bool decay_tc_fits(const DecayCall& c, int dtype);
 cudaError_t decay_tc_states(const DecayCall& c, const DecayStates& p, DecayWhich which, Chain& chain);
 cudaError_t decay_tc_pass(const DecayCall& c, const DecayPass& p, Chain& chain);

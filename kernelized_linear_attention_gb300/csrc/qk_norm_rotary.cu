@@ -34,9 +34,9 @@ struct QkPlan {
 };
 
 // Forward, rows that a lane's vectors of 16 bytes hold are copied to shared memory ahead of their use, by the lane that
-// uses them: two blocks per SM of 114 registers a thread (65536 x 32 x 64 in bf16 97 us; four of 64, which take a quarter
-// more instructions, 106).  The backward pass has twice the rows on their way and more registers to keep, and is faster
-// with three blocks and loads to registers (32768 x 16 x 64: 48 us and 65).
+// uses them: two blocks of 256 threads per SM, with 100 registers a thread (65536 x 32 x 64 in bf16 97 us; four of 64, which
+// take a quarter more instructions, 106).  The backward pass has twice the rows on their way and more registers to keep,
+// and is faster with three blocks and loads to registers (32768 x 16 x 64: 48 us and 65).
 constexpr int kRing = 4;              // rows on their way, a power of two
 // Positions that a thread of the table's has on their way together: 16384 x 20 x 128 in bf16 take 36 us with four (45 with
 // one, and each token's table made by two blocks); the backward pass has no registers for them (32768 x 16 x 64: 55 us with

@@ -429,3 +429,64 @@ def test_gradients_against_differences(la):
         slope = (loss(**{name: x[name] + 1e-4 * way}) - loss(**{name: x[name] - 1e-4 * way})) / 2e-4
         off = ((bound + U * np.abs(_np(grad))) * np.abs(way)).sum() + 2 ** -44 * size / 2e-4
         assert abs((_np(grad) * way).sum() - slope) <= off
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lengths", [[1], [31], [32], [33], [127], [128], [129], [256], [1000], [64, 0, 64]])
+def test_states_that_nobody_asks_for_change_nothing(la, lengths, dtype):
+    c = _case(lengths, 3, 64, 64, dtype, seed=21)
+    for state in (False, True):
+        out, _ = _forward(la, c, state)
+        assert torch.equal(out, _forward(la, c, state, cu_seqlens=c["cu_t"]))
+        if len(lengths) == 1:
+            assert torch.equal(out, _forward(la, c, state, nseq=1))
+        got = _backward(la, c, state)
+        for kw in [dict(cu_seqlens=c["cu_t"])] + [dict(nseq=1)] * (len(lengths) == 1):
+            assert all(torch.equal(x, y) for x, y in zip(got[:3], _backward(la, c, state, **kw)))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_calls_behind_one_another_share_a_workspace(la, dtype):
+    # each call's first kernel has to wait for the last one of the call ahead: nothing but the stream orders them
+    cases = [_case(lengths, 8, 64, 64, dtype, seed=22 + i) for i, lengths in enumerate([[3000, 77], [40] * 60, [129]])]
+    want = [_forward(la, c, True) + _backward(la, c, True) for c in cases]
+    need = max(max(la.la_decay_attention_backward_workspace_bytes(TYPES[dtype], True, len(c["spans"]), c["q"].shape[0], 8,
+                                                                  64, 64) for c in cases), 256)
+    w = torch.empty(need, dtype=torch.uint8, device="cuda")
+    got = [tuple(torch.empty_like(x) for x in r) for r in want]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, (out, state, dq, dk, dv, ds) in zip(cases, got):
+            la.la_decay_attention(c["q"], c["k"], c["v"], c["ld"], scale=c["scale"], cu_seqlens=c["cu_t"],
+                                  state_in=c["s"], state_out=state, out=out, workspace=w)
+            la.la_decay_attention_backward(c["q"], c["k"], c["v"], c["do"], c["ld"], scale=c["scale"],
+                                           cu_seqlens=c["cu_t"], state_in=c["s"], dstate_out=c["ds"], dq=dq, dk=dk,
+                                           dv=dv, dstate_in=ds, workspace=w)
+        kept = [tuple(x.clone() for x in r) for r in got]
+        for r in got:
+            for x in r:
+                x.zero_()
+        assert all(torch.equal(x, y) for r, s in zip(kept, want) for x, y in zip(r, s))
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (37, 53)])
+def test_many_heads_and_short_sequences(la, dk, dv):
+    c = _case([5, 0, 130, 64, 1, 300, 128] * 3, 40, dk, dv, "bf16", seed=25)
+    _check_forward(la, c, True)
+    _check_backward(la, c, True)
+
+
+@pytest.mark.parametrize("dv", [1, 2, 4, 129, 250, 251, 256])
+def test_step_of_any_width(la, dv):
+    g = torch.Generator().manual_seed(dv)
+    q, k = (torch.randn(3, 2, 33, generator=g).cuda() for _ in range(2))
+    v, s = torch.randn(3, 2, dv, generator=g).cuda(), torch.randn(3, 2, 33, dv, generator=g).cuda()
+    ld = torch.tensor([-0.1, -2.0]).cuda()
+    new = torch.empty_like(s)
+    out = la.la_decay_step(q, k, v, ld, s, scale=0.5, state_out=new)
+    want = s.double() * ld.double().exp()[None, :, None, None] + k.double()[..., None] * v.double()[..., None, :]
+    # a product, a sum and a rounding of the decay: 2^-22 of the terms; then 33 terms more
+    size = s.double().abs() + (k.double()[..., None] * v.double()[..., None, :]).abs()
+    assert ((new.double() - want).abs() <= 2.0 ** -21 * size).all()
+    terms = (q.double().abs()[..., None] * size).sum(2)
+    assert ((out.double() - 0.5 * (q.double()[..., None] * want).sum(2)).abs() <= 40 * 2.0 ** -23 * terms).all()
