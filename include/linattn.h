@@ -607,7 +607,7 @@ LA_API size_t la_qk_norm_rotary_backward_workspace_bytes(int dtype, int64_t T, i
 
 /*
  * la_decay_attention - out_t for every token of every packed sequence.
- *   q, k: [T, H, d_k]; v, out: [T, H, d_v], all of dtype.
+ *   q, k: [T, H, d_k]; v, out: [T, H, d_v], all of dtype; T < 2^31 - 1024.
  *   log_decay: fp32 [H] (device), natural logarithms, at most 0: 0 forgets
  *              nothing, -inf everything but the token itself.  Positive ones
  *              grow, and are computed as given as long as their powers over a

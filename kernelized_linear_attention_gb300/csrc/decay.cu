@@ -569,7 +569,9 @@ bool vector_rows(const DecayCall& c, int dtype, std::initializer_list<const void
     return on_16_bytes(arrays) && c.dk % n == 0 && c.dv % n == 0;
 }
 
-constexpr int64_t kLongest = 1 << 20;      // tokens of a segment: exact in fp32
+// Tokens of a segment: exact in fp32; and on the tensor cores, which truncate what they add to the state that the products
+// keep, eight times a chunk: 2^-13 of it after 256 chunks, where a bf16 operand is off by 2^-9.
+constexpr int64_t kLongest = 1 << 20, kMostChunks = 256;
 
 // Tokens of a segment.  Tensor cores: whole chunks of 128, one block per SM.  Equal sequences are cut so that the waves
 // of blocks times a segment's chunks, and two for a block's beginning and end, are fewest.  Packed ones, whose lengths
@@ -588,11 +590,12 @@ int64_t segment_length(const DecayCall& c, bool tensor, int sms) {
     int64_t best = 1, least = INT64_MAX;
     if (c.cu_seqlens) {
         best = ceil_div(c.T, 128) * c.H * 2 / (3 * sms);
-        best = min64(best < 1 ? 1 : best, chunks);
+        best = min64(min64(best < 1 ? 1 : best, chunks), kMostChunks);
     } else {
         // (more segments than a few per SM, or than chunks, never pay)
-        const int64_t pairs = (int64_t)c.nseq * c.H, most = min64(chunks, ceil_div(8 * sms, pairs));
-        for (int64_t per = 1; per <= most; ++per) {
+        const int64_t pairs = (int64_t)c.nseq * c.H, fewest = ceil_div(chunks, kMostChunks);
+        const int64_t most = min64(chunks, ceil_div(8 * sms, pairs));
+        for (int64_t per = fewest; per == fewest || per <= most; ++per) {
             const int64_t k = ceil_div(chunks, per);
             const int64_t cost = ceil_div(ceil_div(chunks, k) * pairs, sms) * (k + 2);
             if (cost < least) {
@@ -601,7 +604,7 @@ int64_t segment_length(const DecayCall& c, bool tensor, int sms) {
             }
         }
     }
-    return min64(best * 128, kLongest);
+    return best * 128;
 }
 
 cudaError_t plan(const DecayCall& c, Chain& chain) {

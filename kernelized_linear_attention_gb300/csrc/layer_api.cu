@@ -56,7 +56,8 @@ la_status decay_dims(int dtype, bool has_cu, int nseq, int64_t T, int H, int dk,
     if (!dtype_ok(dtype) || nseq < 1 || nseq > 65535 || H < 1 || H > 65535 || dk < 1 || dv < 1) return LA_ERR_INVALID_ARG;
     if (T < 0 || T > (int64_t)INT32_MAX) return LA_ERR_INVALID_ARG;
     if (!has_cu && T % nseq != 0) return LA_ERR_INVALID_ARG;
-    if (dk > LA_MAX_DK || dv > LA_MAX_DV) return LA_ERR_UNSUPPORTED;
+    // (tokens of a chunk behind the last one are counted in 32 bits)
+    if (dk > LA_MAX_DK || dv > LA_MAX_DV || T > (int64_t)INT32_MAX - 1024) return LA_ERR_UNSUPPORTED;
     return LA_OK;
 }
 

@@ -490,3 +490,35 @@ def test_step_of_any_width(la, dv):
     assert ((new.double() - want).abs() <= 2.0 ** -21 * size).all()
     terms = (q.double().abs()[..., None] * size).sum(2)
     assert ((out.double() - 0.5 * (q.double()[..., None] * want).sum(2)).abs() <= 40 * 2.0 ** -23 * terms).all()
+
+
+def test_more_chunks_than_a_state_takes(la):
+    """So many heads that each would be one segment, and more tokens than one segment has; nothing is forgotten."""
+    c = _case([33000], 160, 8, 8, "bf16", seed=26, log_decay=torch.tensor([0.0, -1e-6, -1e-4, -1e-2] * 40))
+    _check_forward(la, c, False)
+    out, new = _forward(la, c, False, nseq=1, return_state=True)
+    q, k, v, ld = (_np(c[x]) for x in ("q", "k", "v", "ld"))
+    ref, ref_new = ops.decay_attention(q, k, v, ld, c["scale"], c["cu"])
+    b_out, b_new = forward_bounds(q, k, v, ld, c["scale"], c["spans"], None, "bf16")
+    check(_np(out), ref, b_out, "bf16", "out")
+    check(_np(new), ref_new, b_new, "f32", "state_out")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_an_equal_batch_captured_twice_and_replayed(la, dtype):
+    c = _case([400, 400], 3, 64, 64, dtype, seed=27)
+    want = _forward(la, c, True, nseq=2, return_state=True) + _backward(la, c, True, nseq=2, return_dstate=True)
+    torch.cuda.synchronize()
+    graphs, got = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for graph in graphs:
+        with torch.cuda.graph(graph):
+            got.append(_forward(la, c, True, nseq=2, return_state=True) +
+                       _backward(la, c, True, nseq=2, return_dstate=True))
+    for _ in range(3):
+        for r in got:
+            for x in r:
+                x.zero_()
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for r in got for x, y in zip(r, want))

@@ -283,3 +283,23 @@ def test_binding_refuses_cpu_tensors_and_wrong_ranks():
         la.la_gated_scan(None, None)
     with pytest.raises(ValueError):
         la.la_gated_scan(x, x, cu_seqlens=torch.zeros(3, dtype=torch.int32), nseq=5)
+
+
+def test_decay_attention_of_the_most_tokens(lib):
+    # chunks end behind the last token: their ends are 32-bit numbers too
+    import kernelized_linear_attention_gb300 as la
+    most = (1 << 31) - 1025
+    for T, code, some in ((most, 3, True), (most + 1, 2, False), ((1 << 31) - 1, 2, False)):
+        assert _decay(lib, T=T, H=1, dk=1, dv=1, q=P[0], k=P[0], v=P[0], out=P[0] + (1 << 40), bytes=0) == code
+        for cu in (False, True):
+            assert (la.la_decay_attention_workspace_bytes(torch.float32, cu, 1, T, 1, 1, 1) > 0) == some
+            assert (la.la_decay_attention_backward_workspace_bytes(torch.bfloat16, cu, 1, T, 1, 8, 8) > 0) == some
+
+
+def test_decay_segments_end(lib):
+    """A state on the tensor cores takes 32768 tokens at most before it is begun anew, however many heads there are."""
+    import kernelized_linear_attention_gb300 as la
+    for cu in (False, True):
+        for T, H in ((1 << 20, 400), (1 << 20, 7), (33000, 400)):
+            few = la.la_decay_attention_workspace_bytes(torch.bfloat16, cu, 1, T, H, 64, 64)
+            assert few >= (-(-T // 32768) - 1) * H * 64 * 64 * 4
