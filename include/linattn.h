@@ -554,8 +554,9 @@ LA_API la_status la_rotary(const void* q, const void* k, const float* freq, cons
  *   is 1.  q_rstd, k_rstd: NULL or fp32 [T, Hq] and [T, Hk], what
  *   la_qk_norm_rotary_backward reads.
  *   freq, positions, pairs, naxes, interleaved: as for la_rotary.  eps >= 0.
- *   Arithmetic is fp32, outputs are rounded once.  A row whose squares
- *   overflow in sum has rstd 0; a row of zeros with eps = 0 gives NaN.
+ *   Arithmetic is fp32, outputs are rounded once.  A row of finite values whose
+ *   squares overflow in sum has rstd 0 and gives zeros; a row of zeros with eps = 0
+ *   gives NaN.
  *   d <= LA_MAX_ROTARY_D, (Hq + Hk) d <= LA_MAX_CHANNELS.  T = 0 enqueues nothing.
  */
 LA_API la_status la_qk_norm_rotary(const void* q, const void* k, const float* q_weight, const float* k_weight,

@@ -268,8 +268,9 @@ __global__ void __launch_bounds__(kQkThreads, KU > 1 && KU * N > 4 ? 1 : Backwar
             for (int s = 0; s < kSides; ++s)
 #pragma unroll
                 for (int j = 0; j < R::n; ++j) {
-                    if (!Backward) f[u][s][j] = pmul(f[u][s][j], w[u][s][j]);
+                    // (the weight last: x w may leave fp32 where x rstd w does not, as in a row whose rstd is 0)
                     f[u][s][j] = pmul(f[u][s][j], scale);
+                    if (!Backward) f[u][s][j] = pmul(f[u][s][j], w[u][s][j]);
                 }
             if (Full ? on : turned[u] && on && at[u] >= 0) {
                 const int e = lane + u * G;
