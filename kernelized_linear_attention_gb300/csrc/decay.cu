@@ -569,9 +569,13 @@ bool vector_rows(const DecayCall& c, int dtype, std::initializer_list<const void
     return on_16_bytes(arrays) && c.dk % n == 0 && c.dv % n == 0;
 }
 
-// Tokens of a segment: exact in fp32; and on the tensor cores, which truncate what they add to the state that the products
-// keep, eight times a chunk: 2^-13 of it after 256 chunks, where a bf16 operand is off by 2^-9.
-constexpr int64_t kLongest = 1 << 20, kMostChunks = 256;
+// Tokens of a segment: exact in fp32.  The tensor cores cut off what they add to the state that the products keep: of 16
+// tokens' terms all below 2^-25, of their sum with the state all below 2^-23 of the largest one's power of two (seen with
+// terms of one bit each).  That is 5 2^-23 of the state at most, eight times a chunk: 2^-11 of it after 64 chunks, mostly
+// toward zero, and half as much where terms are spread evenly, beside outputs rounded by 2^-8.  (256 chunks lose four times
+// that; 65536 x 152 x 64 take 1180 us so and 1418 with 64, which sum seven eighths of the tokens a second time instead of
+// half, 262144 x 16 x 64 635 and 668, 65536 x 40 x 128 960 both.)
+constexpr int64_t kLongest = 1 << 20, kMostChunks = 64;
 
 // Tokens of a segment.  Tensor cores: whole chunks of 128, one block per SM.  Equal sequences are cut so that the waves
 // of blocks times a segment's chunks, and two for a block's beginning and end, are fewest.  Packed ones, whose lengths
