@@ -559,20 +559,15 @@ cudaError_t bwd_transpose_omega(const FwdParams& p, cudaStream_t s) {
 
 size_t bwd_smem_bytes(int dk, int dv, int r) { return plan_bwd_smem(dk, dv, r, true).total; }
 
-template <typename Kern>
-static cudaError_t bwd_set_smem(Kern k, size_t bytes) {
-    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 cudaError_t bwd_q(const FwdParams& p, int dtype, int prefix_is_zero, cudaStream_t s) {
     const size_t bytes = plan_bwd_smem(p.dk, p.dv, p.r, true).total;
     const dim3 grid((unsigned)p.U, (unsigned)p.H);
     cudaError_t e;
     if (dtype == LA_F32) {
-        if ((e = bwd_set_smem(bwd_q_kernel<float>, bytes)) != cudaSuccess) return e;
+        if ((e = allow_all_shared(bwd_q_kernel<float>)) != cudaSuccess) return e;
         bwd_q_kernel<float><<<grid, kBwdThreads, bytes, s>>>(p, prefix_is_zero);
     } else {
-        if ((e = bwd_set_smem(bwd_q_kernel<__nv_bfloat16>, bytes)) != cudaSuccess) return e;
+        if ((e = allow_all_shared(bwd_q_kernel<__nv_bfloat16>)) != cudaSuccess) return e;
         bwd_q_kernel<__nv_bfloat16><<<grid, kBwdThreads, bytes, s>>>(p, prefix_is_zero);
     }
     return cudaGetLastError();
@@ -583,10 +578,10 @@ cudaError_t bwd_kv(const FwdParams& p, int dtype, cudaStream_t s) {
     const dim3 grid((unsigned)p.U, (unsigned)p.H);
     cudaError_t e;
     if (dtype == LA_F32) {
-        if ((e = bwd_set_smem(bwd_kv_kernel<float>, bytes)) != cudaSuccess) return e;
+        if ((e = allow_all_shared(bwd_kv_kernel<float>)) != cudaSuccess) return e;
         bwd_kv_kernel<float><<<grid, kBwdThreads, bytes, s>>>(p);
     } else {
-        if ((e = bwd_set_smem(bwd_kv_kernel<__nv_bfloat16>, bytes)) != cudaSuccess) return e;
+        if ((e = allow_all_shared(bwd_kv_kernel<__nv_bfloat16>)) != cudaSuccess) return e;
         bwd_kv_kernel<__nv_bfloat16><<<grid, kBwdThreads, bytes, s>>>(p);
     }
     return cudaGetLastError();

@@ -58,6 +58,15 @@ struct Layout {
 
 constexpr int kAlign = 256;
 
+// Shared memory of a block, at most.  More than 48 KB of it takes a permission, which belongs to the kernel and not to a
+// launch: every call asks for the same, all that the kernel's own arrays (`fixed`) leave, so that calls of other threads,
+// whose sizes need less, take nothing away from a launch that needs more.
+constexpr size_t kSmemLimitBytes = 227 * 1024;
+template <typename K>
+cudaError_t allow_all_shared(K kernel, size_t fixed = 0) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kSmemLimitBytes - fixed));
+}
+
 __host__ __device__ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 __host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 __host__ __device__ inline int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }

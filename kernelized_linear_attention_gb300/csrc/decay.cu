@@ -700,7 +700,7 @@ cudaError_t products(const DecayCall& c, std::initializer_list<DecayPass> passes
     const dim3 grid(c.segments, c.H, (unsigned)blocks);
     const size_t smem = simt_smem(widest);
     auto kernel = dtype == LA_F32 ? decay_pass_kernel<float> : decay_pass_kernel<__nv_bfloat16>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_all_shared(kernel);
     if (e != cudaSuccess) return e;
     return launch_in(chain, kernel, grid, kSimtThreads, smem, c, simt, vec);
 }

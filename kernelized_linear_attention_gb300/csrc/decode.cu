@@ -309,8 +309,7 @@ template <typename TIn, int NJ>
 cudaError_t launch_one(dim3 grid, cudaStream_t s, const DecodeParams& p) {
     const size_t bytes = plan_dec_smem(p.dk, p.dv, p.r).total;
     if (bytes > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(decode_kernel<TIn, NJ>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        const cudaError_t e = allow_all_shared(decode_kernel<TIn, NJ>);
         if (e != cudaSuccess) return e;
     }
     decode_kernel<TIn, NJ><<<grid, kDecThreads, bytes, s>>>(p);

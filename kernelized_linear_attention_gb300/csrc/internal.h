@@ -16,7 +16,6 @@ cudaError_t launch_scan(const FwdParams& p, cudaStream_t s);
 // fp32 CUDA-core path (simt.cu).
 size_t simt_smem_bytes(int map, int dk, int dv, int r);
 size_t simt_fmap_smem_bytes(int map, int d, int r);
-constexpr size_t kSmemLimitBytes = 227 * 1024;
 int simt_chunk();
 cudaError_t simt_feature_map(const void* x, const float* omega, int map, int dtype,
                              int64_t T, int H, int d, int r, float* phi, cudaStream_t s);

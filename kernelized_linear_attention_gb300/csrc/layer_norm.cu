@@ -954,7 +954,7 @@ int64_t slots(int64_t rows, int groups, int d, int sms) {
 template <typename K>
 cudaError_t allow_shared(K kernel, size_t bytes) {
     if (bytes <= 40 * 1024) return cudaSuccess;      // 48 KB with the static part need no permission
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    return allow_all_shared(kernel, 2 * 1024);
 }
 
 struct Forward {

@@ -80,7 +80,7 @@ cudaError_t orf_build(const double* blocks, const double* lengths, int r, int d,
                       cudaStream_t s) {
     const int nb = (int)ceil_div(r, d);
     const size_t bytes = ((size_t)d * d + d) * sizeof(double);
-    cudaError_t e = cudaFuncSetAttribute(orf_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    cudaError_t e = allow_all_shared(orf_kernel, kOrfThreads / 32 * sizeof(double));
     if (e != cudaSuccess) return e;
     orf_kernel<<<nb, kOrfThreads, bytes, s>>>(blocks, lengths, r, d, omega);
     return cudaGetLastError();

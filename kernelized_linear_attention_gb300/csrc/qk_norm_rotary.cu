@@ -431,7 +431,7 @@ cudaError_t launch(const QkNormParams& p, const QkPlan& plan, Chain& chain, int6
     }
     auto kernel = qk_norm_rotary_kernel<T, N, Interleaved, KU, Backward, Full>;
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = allow_all_shared(kernel);
         if (e != cudaSuccess) return e;
     }
     const dim3 grid((unsigned)plan.blocks, (unsigned)ceil_div(plan.heads, plan.share));

@@ -39,8 +39,6 @@ __host__ __device__ inline SmemPlan plan_smem(int map, int dk, int dv, int r, bo
     return s;
 }
 
-constexpr size_t kSmemLimit = 227 * 1024;
-
 // Feature-map kernel: Omega (optional) + x rows + phi rows + |x|^2/2.
 __host__ __device__ inline SmemPlan plan_fmap_smem(int map, int d, int r, bool om_in_smem) {
     SmemPlan s{};
@@ -54,11 +52,11 @@ __host__ __device__ inline SmemPlan plan_fmap_smem(int map, int d, int r, bool o
 }
 
 inline bool fmap_omega_fits(int map, int d, int r) {
-    return map == LA_MAP_FAVOR && plan_fmap_smem(map, d, r, true).total <= kSmemLimit;
+    return map == LA_MAP_FAVOR && plan_fmap_smem(map, d, r, true).total <= kSmemLimitBytes;
 }
 
 inline bool omega_fits(int map, int dk, int dv, int r) {
-    return map == LA_MAP_FAVOR && plan_smem(map, dk, dv, r, true).total <= kSmemLimit;
+    return map == LA_MAP_FAVOR && plan_smem(map, dk, dv, r, true).total <= kSmemLimitBytes;
 }
 
 // ---------------------------------------------------------------------------
@@ -254,23 +252,18 @@ size_t simt_fmap_smem_bytes(int map, int d, int r) {
     return plan_fmap_smem(map, d, r, fmap_omega_fits(map, d, r)).total;
 }
 
-template <typename Kern>
-static cudaError_t set_smem(Kern k, size_t bytes) {
-    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 cudaError_t simt_feature_map(const void* x, const float* omega, int map, int dtype,
                              int64_t T, int H, int d, int r, float* phi, cudaStream_t s) {
     const int om_smem = fmap_omega_fits(map, d, r) ? 1 : 0;
     const size_t bytes = plan_fmap_smem(map, d, r, om_smem).total;
-    if (bytes > kSmemLimit) return cudaErrorInvalidValue;
+    if (bytes > kSmemLimitBytes) return cudaErrorInvalidValue;
     dim3 grid((unsigned)ceil_div(T, CS), (unsigned)H);
     cudaError_t e;
     if (dtype == LA_F32) {
-        if ((e = set_smem(fmap_kernel<float>, bytes)) != cudaSuccess) return e;
+        if ((e = allow_all_shared(fmap_kernel<float>)) != cudaSuccess) return e;
         fmap_kernel<float><<<grid, NT, bytes, s>>>(static_cast<const float*>(x), omega, map, T, H, d, r, phi, om_smem);
     } else {
-        if ((e = set_smem(fmap_kernel<__nv_bfloat16>, bytes)) != cudaSuccess) return e;
+        if ((e = allow_all_shared(fmap_kernel<__nv_bfloat16>)) != cudaSuccess) return e;
         fmap_kernel<__nv_bfloat16><<<grid, NT, bytes, s>>>(static_cast<const __nv_bfloat16*>(x), omega, map, T,
                                                           H, d, r, phi, om_smem);
     }
@@ -283,10 +276,10 @@ cudaError_t simt_state(const FwdParams& p, int dtype, cudaStream_t s) {
     dim3 grid((unsigned)p.U, (unsigned)p.H);
     cudaError_t e;
     if (dtype == LA_F32) {
-        if ((e = set_smem(state_kernel<float>, bytes)) != cudaSuccess) return e;
+        if ((e = allow_all_shared(state_kernel<float>)) != cudaSuccess) return e;
         state_kernel<float><<<grid, NT, bytes, s>>>(p, om_smem);
     } else {
-        if ((e = set_smem(state_kernel<__nv_bfloat16>, bytes)) != cudaSuccess) return e;
+        if ((e = allow_all_shared(state_kernel<__nv_bfloat16>)) != cudaSuccess) return e;
         state_kernel<__nv_bfloat16><<<grid, NT, bytes, s>>>(p, om_smem);
     }
     return cudaGetLastError();
@@ -298,10 +291,10 @@ cudaError_t simt_out(const FwdParams& p, int dtype, int prefix_is_zero, cudaStre
     dim3 grid((unsigned)p.U, (unsigned)p.H);
     cudaError_t e;
     if (dtype == LA_F32) {
-        if ((e = set_smem(out_kernel<float>, bytes)) != cudaSuccess) return e;
+        if ((e = allow_all_shared(out_kernel<float>)) != cudaSuccess) return e;
         out_kernel<float><<<grid, NT, bytes, s>>>(p, om_smem, prefix_is_zero);
     } else {
-        if ((e = set_smem(out_kernel<__nv_bfloat16>, bytes)) != cudaSuccess) return e;
+        if ((e = allow_all_shared(out_kernel<__nv_bfloat16>)) != cudaSuccess) return e;
         out_kernel<__nv_bfloat16><<<grid, NT, bytes, s>>>(p, om_smem, prefix_is_zero);
     }
     return cudaGetLastError();
