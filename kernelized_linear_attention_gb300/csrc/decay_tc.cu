@@ -391,7 +391,9 @@ template <int D> struct __align__(1024) PassSmem {
     unsigned char state[F::states][2][F::blocks][D * 128];   // [D][64] in blocks, in two parts
     float pw[kC + 4 + 32];                                // powers of the decay, then 0 .. 31 of them with the scale
     __align__(16) float in_block[32];                     // decay inside a block of 32 tokens
-    // by chunk: the first token whose channel is not finite (or 128); reverse: one behind the last one (or 0)
+    // by chunk: the first token whose channel is not finite (or 128); reverse: one behind the last one (or 0).  What is left
+    // of the chunk that had the place before need not go: that channel is not finite in the state any more, and so in no
+    // output of a later chunk.
     unsigned short edge[F::ring][D];
     int strange[F::ring];                                 // by chunk: whether there is one
     uint64_t xy_full[F::stages], xy_empty[F::stages], z_full[F::z_stages], z_empty[F::z_stages];
@@ -823,12 +825,6 @@ __global__ void __launch_bounds__(kPassThreads, 1)
                 }
                 if (k + 1 == F::blocks) {
                     tc_fence_before();
-                    if (strange) {
-                        named_sync(1, 256);
-                        for (int i = threadIdx.x - 640; i < D; i += 256) s.edge[it % F::ring][i] = reverse ? 0 : kC;
-                        if (threadIdx.x == 640) s.strange[it % F::ring] = 0;
-                        named_sync(1, 256);
-                    }
                     if (D != 64) arrive_w(&s.r_empty);
                     arrive_w(&s.o_empty);
                 }
