@@ -130,6 +130,13 @@ def _need(t: torch.Tensor, name: str, dtype=None, cuda=True):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
 
 
+def _holds(n: int, **tensors):
+    """Every tensor that is given has the n elements that the call reads or writes."""
+    for name, t in tensors.items():
+        if t is not None and t.numel() < n:
+            raise ValueError(f"{name} must have {n} elements, got {tuple(t.shape)}")
+
+
 def _map_id(m) -> int:
     """Map id from a name ("identity", "elu1", "favor", "dpfp<nu>") or an id."""
     if isinstance(m, str):
@@ -186,6 +193,8 @@ def la_feature_map(x: torch.Tensor, map, omega: Optional[torch.Tensor] = None,
     if phi is None:
         phi = torch.empty((T, H, r), dtype=torch.float32, device=x.device)
     _need(phi, "phi", torch.float32)
+    _holds(T * H * r, phi=phi)
+    _holds(r * d, omega=omega if m == MAP_IDS["favor"] else None)
     _check("la_feature_map", lib.la_feature_map(_ptr(x), _ptr(omega), m, DTYPE_IDS[x.dtype], T, H, d, r,
                                                 _ptr(phi), _stream(stream)))
     return phi
@@ -245,6 +254,9 @@ def la_forward_causal_noalloc(q, k, v, map, omega=None, cu_seqlens=None, nseq=No
     if out is None:
         out = torch.empty((T, H, d_v), dtype=q.dtype, device=q.device)
     _need(out, "out", q.dtype)
+    _holds(T * H * d_k, k=k)
+    _holds(T * H * d_v, v=v, out=out)
+    _holds(r * d_k, omega=omega if m == MAP_IDS["favor"] else None)
     _check("la_forward_causal_noalloc", load_library().la_forward_causal_noalloc(
         _ptr(q), _ptr(k), _ptr(v), _ptr(omega), m, DTYPE_IDS[q.dtype], _ptr(cu_seqlens), nseq, T, H, d_k, d_v, r,
         eps, _ptr(out), _stream(stream)))
@@ -303,6 +315,9 @@ def _forward(causal, q, k, v, map, omega, cu_seqlens, nseq, eps, out, workspace,
     if out is None:
         out = torch.empty((T, H, d_v), dtype=q.dtype, device=q.device)
     _need(out, "out", q.dtype)
+    _holds(T * H * d_k, k=k)
+    _holds(T * H * d_v, v=v, out=out)
+    _holds(r * d_k, omega=omega if m == MAP_IDS["favor"] else None)
     need = la_workspace_bytes(causal, m, q.dtype, cu_seqlens is not None, nseq, T, H, d_k, d_v, r)
     if workspace is None:
         # a size of 0 means the call will be rejected: let the library say why
@@ -364,6 +379,9 @@ def la_decode_step(q, k, v, state, map, omega=None, norm="attention", eps=1e-6, 
     if out is None:
         out = torch.empty((B, H, d_v), dtype=q.dtype, device=q.device)
     _need(out, "out", q.dtype)
+    _holds(B * H * d_k, k=k)
+    _holds(B * H * d_v, v=v, out=out)
+    _holds(r * d_k, omega=omega if _map_id(map) == MAP_IDS["favor"] else None)
     _check("la_decode_step", load_library().la_decode_step(
         _ptr(q), _ptr(k), _ptr(v), _ptr(omega), _map_id(map), DTYPE_IDS[q.dtype], _norm_id(norm), B, H, d_k, d_v,
         r, eps, _ptr(state), _ptr(out), _stream(stream)))
@@ -400,6 +418,9 @@ def la_backward(q, k, v, dout, map, omega=None, causal=True, norm="attention", c
     dv = torch.empty_like(v) if dv is None else dv
     for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
         _need(t, name, q.dtype)
+    _holds(T * H * d_k, k=k, dq=dq, dk=dk)
+    _holds(T * H * d_v, v=v, dout=dout, dv=dv)
+    _holds(r * d_k, omega=omega if m == MAP_IDS["favor"] else None)
     need = la_backward_workspace_bytes(causal, m, q.dtype, cu_seqlens is not None, nseq, T, H, d_k, d_v, r)
     if workspace is None:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
@@ -444,6 +465,8 @@ def la_orthogonal_features(gauss_blocks: torch.Tensor, gauss_lengths: torch.Tens
     if omega is None:
         omega = torch.empty((r, d), dtype=torch.float32, device=gauss_blocks.device)
     _need(omega, "omega", torch.float32)
+    _holds(-(-r // max(d, 1)) * d * d, gauss_blocks=gauss_blocks)
+    _holds(r * d, gauss_lengths=gauss_lengths, omega=omega)
     _check("la_orthogonal_features", load_library().la_orthogonal_features(
         _ptr(gauss_blocks), _ptr(gauss_lengths), r, d, _ptr(omega), _stream(stream)))
     return omega
