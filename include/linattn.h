@@ -621,13 +621,13 @@ LA_API size_t la_qk_norm_rotary_backward_workspace_bytes(int dtype, int64_t T, i
  *              copied.  May be the same array as state_in.
  *   States and sums are fp32 and decays are carried beyond fp32.  fp32 rows are
  *   computed in fp32, and bf16 rows too where d_k or d_v is above 128 or no
- *   multiple of 8, an array does not start on 16 bytes, or sequences have up to 32
- *   tokens on average: out is rounded once.  Other bf16 rows are products of the
- *   tensor cores, whose operands are rounded: what a token gives a later one of
- *   the same 128 (scale g^(i-j) q_i . k_j) to bf16, an error of at most 2^-8 of
- *   that term; the keys that a state takes while a sequence goes on, weighted by
- *   their decay, likewise; the state that queries read to 2^-16; keys in
- *   state_out to 2^-24.  Their sums are cut off instead of rounded: with 16
+ *   multiple of 8, an array does not start on 16 bytes, or sequences (empty ones
+ *   among them) have up to 32 tokens on average: out is rounded once.  Other bf16
+ *   rows are products of the tensor cores, whose operands are rounded: what a
+ *   token gives a later one of the same 128 (scale g^(i-j) q_i . k_j) to bf16, an
+ *   error of at most 2^-8 of that term; the keys that a state takes while a
+ *   sequence goes on, weighted by their decay, likewise; the state that queries
+ *   read to 2^-16; keys in state_out to 2^-24.  Their sums are cut off instead of rounded: with 16
  *   tokens a state loses 5 2^-23 of itself at most, mostly toward zero.  This
  *   adds up over 8192 tokens, to 2^-11, in the state that queries read inside a
  *   call, and over 1024, to 2^-14, in what state_out and later parts of a

@@ -579,8 +579,8 @@ constexpr int64_t kLongest = 1 << 20, kMostChunks = 64;
 
 // Tokens of a segment.  Tensor cores: whole chunks of 128, one block per SM.  Equal sequences are cut so that the waves
 // of blocks times a segment's chunks, and two for a block's beginning and end, are fewest.  Packed ones, whose lengths
-// are not known here, are cut into one and a half blocks' worth per SM (40009 x 8 x 64 of 64 sequences 135 us, of one 98;
-// three blocks' worth 145 and 121; one 129 and 104, but 120000 x 8 x 64 of 64 sequences 271 instead of 241).  CUDA cores:
+// are not known here, are cut into one and a half blocks' worth per SM (40009 x 8 x 64 of 64 sequences 129 us, of one 96,
+// 120000 of 64 245; three blocks' worth 135, 120 and 235; one 139, 102 and 247).  CUDA cores:
 // four blocks per SM, of chunks of 32, so that what is short has one chunk to a block and nothing waits for a chunk ahead.
 int64_t segment_length(const DecayCall& c, bool tensor, int sms) {
     // (packed: longer than T where one segment would do, so that no boundary inside a sequence has to be reckoned with)

@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(kPassThreads, 1)
             arrive_w(&s.p_full[b]);
         }
     } else if (warp >= 12 && warp < 20) {
-        // ---- weighted y, the state as an operand, a look at z
+        // ---- weighted y, the state as an operand, nothing in rows behind a chunk's end
         const int part = (warp - 12) >> 2;                         // this thread's 32 channels of every 64
         const uint32_t place = sw128_chunk(row, 4 * part);         // of their first 16 bytes; the j-th: place ^ 16 j
         const bool rows = D == 128 || q < 2;                       // tensor memory lanes that are rows of the state
@@ -937,7 +937,11 @@ cudaError_t decay_force_wait_timeout(int enable) { return cudaMemcpyToSymbol(g_f
 
 // Sequences of up to 32 tokens on average, a quarter of a chunk, go to the CUDA cores, which have many blocks on an SM: 256
 // of 32 x 8 x 64 take 68 us and 86 on the tensor cores, their gradients 176 and 250 (a single one 15 and 11, 14 and 25); 256
-// of 64 tokens 132 and 89, and 362 and 259; one of 65536 x 16 x 64 1500 and 190.
+// of 64 tokens 132 and 89, and 362 and 259; one of 65536 x 16 x 64 1500 and 190.  Packed batches are judged by their
+// average, since the host does not know their lengths.  Where these are mixed, a segment bound's blocks that find
+// nothing to do count as much as the products: a prompt of 4096 with 256 single tokens 129 us and 130, gradients 286 and 316;
+// 65536 with 4096 of them 1705 and 1701, 4249 and 4418; 2048 with 512 of four tokens 157 and 201, 369 and 531.  Empty sequences
+// count as well: 4096 tokens with 256 of them 83 and 68, 165 and 125; 65536 with 4096 941 and 687, 2243 and 1342.
 constexpr int64_t kShortest = 32;
 
 bool decay_tc_fits(const DecayCall& c, int dtype) {

@@ -1,9 +1,9 @@
 // Kernels of one call that are launched before the one ahead of them has ended (programmatic dependent launch), so that
-// nothing waits for a launch: 40009 x 8 x 64 packed 147 us, 153 without; 1025 x 3 x 37 x 53 28 and 32.  The first one is
+// nothing waits for a launch: 40009 x 8 x 64 packed 129 us, 136 without; 1025 x 3 x 37 x 53 22 and 27.  The first one is
 // launched like any other; every later one has chain_wait() as its first step, in all of its threads, before anything is
 // read, written or allocated (tensor memory that a waiting block held could be what a block of the kernel ahead still
 // needs), so that the end of the last kernel is the end of all.  (Product passes of the gradients that wait for one
-// another at their ends only, side by side, were slower: 8 x 4096 x 8 x 64 180 us and 173.)
+// another at their ends only, side by side, were slower by a twenty-fifth for 8 x 4096 x 8 x 64.)
 #pragma once
 
 #include <cuda_runtime.h>

@@ -78,7 +78,8 @@ struct QkNormParams : Turns {
     const float* w[2];         // [d], or [H][d] per head, or NULL
     float* rstd[2];            // [T][H]: written if not NULL (forward), read (backward)
     float* dw[2];              // backward: as w, or NULL
-    float* partial;            // backward: [blocks][H of both][d], or NULL: no gradients of weights
+    float* partial;            // backward: [blocks along tokens][H of both][d], or, where heads share a weight,
+                               // [blocks][2][d] (of q, of k); NULL: no gradients of weights
     int64_t stride[2];         // of x's tokens, in elements
     int64_t T;
     int H[2];

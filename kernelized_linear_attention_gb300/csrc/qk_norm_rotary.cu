@@ -34,7 +34,7 @@ struct QkPlan {
 };
 
 // Forward, rows that a lane's vectors of 16 bytes hold are copied to shared memory ahead of their use, by the lane that
-// uses them: two blocks of 256 threads per SM, with 100 registers a thread (65536 x 32 x 64 in bf16 97 us; four of 64, which
+// uses them: two blocks of 256 threads per SM, with 100 registers a thread (65536 x 32 x 64 in bf16 98 us; four of 64, which
 // take a quarter more instructions, 106).  The backward pass has twice the rows on their way and more registers to keep,
 // and is faster with three blocks and loads to registers (32768 x 16 x 64: 48 us and 65).
 constexpr int kRing = 4;              // rows on their way, a power of two
