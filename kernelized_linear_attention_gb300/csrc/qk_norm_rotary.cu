@@ -347,7 +347,9 @@ __global__ void __launch_bounds__(kJoinColumns * kJoinRows) qk_join_kernel(const
                                                                            int sums) {
     __shared__ float part[kJoinRows][kJoinColumns];
     chain_wait();
-    const int rows = p.per_head ? p.H[0] + p.H[1] : 2, c = blockIdx.x * kJoinColumns + threadIdx.x, r = blockIdx.y;
+    // (the blocks in one dimension: there may be more weight rows than a grid has in y)
+    const int rows = p.per_head ? p.H[0] + p.H[1] : 2, across = (p.d + kJoinColumns - 1) / kJoinColumns;
+    const int r = blockIdx.x / across, c = (blockIdx.x - r * across) * kJoinColumns + threadIdx.x;
     const int k = p.per_head ? r >= p.H[0] : r;
     float* const out = p.dw[k];
     // compensated: a thread's sum is as good as its terms
@@ -486,8 +488,9 @@ cudaError_t qk_norm_rotary_backward(const QkNormParams& p, int dtype, cudaStream
     Chain chain{s};
     if (p.T > 0) e = dtype == LA_F32 ? dispatch<float, true>(p, chain, &sums) : dispatch<__nv_bfloat16, true>(p, chain, &sums);
     if (e != cudaSuccess || !p.partial) return e;
-    const dim3 grid((unsigned)ceil_div(p.d, kJoinColumns), p.per_head ? p.H[0] + p.H[1] : p.H[1] ? 2 : 1);
-    return launch_in(chain, qk_join_kernel, grid, dim3(kJoinColumns, kJoinRows), 0, p, (int)sums);
+    const int rows = p.per_head ? p.H[0] + p.H[1] : p.H[1] ? 2 : 1;
+    return launch_in(chain, qk_join_kernel, (unsigned)(ceil_div(p.d, kJoinColumns) * rows), dim3(kJoinColumns, kJoinRows), 0, p,
+                     (int)sums);
 }
 
 }  // namespace la
